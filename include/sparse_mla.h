@@ -236,6 +236,130 @@ sparse_mla_status_t sparse_mla_decode_fp8(const void* q, const void* kv_cache, c
                                           size_t workspace_bytes, void* stream);
 
 /*
+ * sparse_mla_decode over a 4-bit paged KV cache, read in place.  One cache
+ * slot (one token's latent row) is 416 bytes:
+ *
+ *   bytes [0, 256)    512 e2m1 codes of the latent's first 512 values, code 2i
+ *                     in the low and 2i + 1 in the high half of byte i (bit 3
+ *                     the sign; magnitudes 0, 0.5, 1, 1.5, 2, 3, 4, 6);
+ *   bytes [256, 288)  32 scales, float8 e4m3 (OCP E4M3); scale k applies to
+ *                     codes 16k .. 16k+15;
+ *   bytes [288, 416)  the latent's last 64 values (rope), bf16.
+ *
+ * The row the attention uses is code * scale * kv_scale (d < 512) and the rope
+ * values.  code * scale is exact in the kernel; a NaN scale (0x7F, 0xFF) gives
+ * NaN.  mla_norm_rope writes such slots.
+ *
+ *   kv_cache      uint8 [num_blocks, page_size, 416], 16-byte aligned
+ *   kv_scale      one finite, positive factor for the whole cache (1 for none)
+ *   workspace     at least sparse_mla_decode_fp4_workspace_size(...) bytes,
+ *                 16-byte aligned; used as sparse_mla_decode uses its own: two
+ *                 calls that may run concurrently need separate workspaces
+ *   everything else as sparse_mla_decode.
+ */
+sparse_mla_status_t sparse_mla_decode_fp4(const void* q, const void* kv_cache, const int32_t* block_table,
+                                          const int32_t* cache_seqlens, const int32_t* indices, float sm_scale,
+                                          float kv_scale, void* out, float* lse, int batch, int s_next, int h_q,
+                                          int d_qk, int d_v, int topk, int page_size, int max_blocks, int num_blocks,
+                                          void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace sparse_mla_decode_fp4 needs for this shape on the current device (0: none). */
+size_t sparse_mla_decode_fp4_workspace_size(int batch, int s_next, int h_q, int d_v, int topk);
+
+/* Formats of a paged KV cache's slots: bf16 rows of 576 values (1152 bytes,
+ * sparse_mla_decode), the 656-byte FP8 slots of sparse_mla_decode_fp8 and the
+ * 416-byte slots of sparse_mla_decode_fp4. */
+typedef enum {
+  SPARSE_MLA_CACHE_BF16 = 0,
+  SPARSE_MLA_CACHE_FP8 = 1,
+  SPARSE_MLA_CACHE_FP4 = 2
+} sparse_mla_cache_format_t;
+
+/*
+ * The step before the attention: RMS norm of every query head's row and of
+ * the token's latent row, the position rotation, and the latent row's write
+ * into its cache slot, in one pass.  A row x has 512 latent values a and 64
+ * rotated values r:
+ *
+ *   a' = a * rsqrt(mean(a^2) + eps) * weight      (no weight: a' = a)
+ *   r' = r turned by its position's angles: plane i has cos_sin[pos][i] and
+ *        cos_sin[pos][32 + i], and is values (2i, 2i + 1) of r when
+ *        `interleaved`, else values (i, i + 32):
+ *        (x, y) -> (x cos - y sin, y cos + x sin)
+ *
+ *   q          bf16, row (t, h) at q + t q_tok_stride + h q_head_stride
+ *   kv         bf16, row t at kv + t kv_tok_stride
+ *              (strides in elements, multiples of 8; the 576 values of a row
+ *              are contiguous; q and kv 16-byte aligned)
+ *   positions  int32 [n_tok]
+ *   cos_sin    fp32 [n_pos, 64], 16-byte aligned
+ *   q_weight   bf16 [512], 16-byte aligned, or NULL: queries are not normed
+ *   kv_weight  bf16 [512], 16-byte aligned, or NULL: the latent row is not normed
+ *   q_out      bf16 [n_tok, h_q, 576]   written; may be q itself where q is dense
+ *   kv_out     bf16 [n_tok, 576] or NULL: written with what the slot stands
+ *              for (codes times scales, rounded to bf16), so that attention
+ *              over kv_out and over the cache sees the same rows; may be kv
+ *              itself where kv is dense
+ *   kv_cache   the cache's slots, 16-byte aligned, or NULL (nothing is stored;
+ *              kv_out is still rounded as cache_format would hold it)
+ *   cache_format  sparse_mla_cache_format_t
+ *   kv_scale   the 4-bit cache's factor (1 for the other formats)
+ *   slots      int32 [n_tok]: the token's slot (page * page_size + offset); a
+ *              slot outside [0, n_slots) stores nothing.  The slots of a call
+ *              are distinct (a slot given twice holds parts of either row).
+ *
+ * A token whose position is outside [0, n_pos) is padding: its rows of q_out
+ * and kv_out and its slot are left as they were.
+ *
+ * The latent row's norm is carried to about 46 bits and rounded once to bf16
+ * (nearest even); codes are the nearest to those bf16 values, ties to even:
+ *   FP8    tile scale 2^k, the smallest with largest / 2^k <= 448, k kept in
+ *          [-64, 31] (1 for a tile of zeros): code * scale is exact in bf16
+ *   4 bits group scale e4m3(largest / (6 kv_scale)), at least 2^-9 and at most
+ *          448; code = e2m1(a' / (scale kv_scale)), at most 6
+ * A tile or group with a value that is not finite gets a NaN scale and reads
+ * as NaN.
+ */
+sparse_mla_status_t mla_norm_rope(const void* q, long long q_tok_stride, long long q_head_stride, const void* kv,
+                                  long long kv_tok_stride, const int32_t* positions, const float* cos_sin, int n_pos,
+                                  const void* q_weight, const void* kv_weight, float eps, int interleaved,
+                                  void* q_out, void* kv_out, void* kv_cache, int cache_format, float kv_scale,
+                                  const int32_t* slots, int n_slots, int n_tok, int h_q, int d_qk, void* stream);
+
+/*
+ * Gradients of mla_norm_rope with respect to q, kv and the weights, from the
+ * gradients of q_out and kv_out as sparse_mla_bwd writes them (the rounding to
+ * bf16 and to the cache's codes passes gradients unchanged).  With r =
+ * rsqrt(mean(a^2) + eps), xhat = a r and g = weight * da':
+ *
+ *   da = r (g - xhat mean(g xhat)),   dweight = sum over rows of da' xhat,
+ *   dr = dr' turned back.
+ *
+ *   q .. interleaved  as for mla_norm_rope (its inputs)
+ *   dq         fp32 [n_tok, h_q, 576], 16-byte aligned
+ *   dkv        fp32 [n_tok, 576], 16-byte aligned
+ *   dq_in      bf16 [n_tok, h_q, 576]   written (the inputs' type, rounded once)
+ *   dkv_in     bf16 [n_tok, 576]        written
+ *   dq_weight  fp32 [512], NULL exactly where q_weight is   written
+ *   dkv_weight fp32 [512], NULL exactly where kv_weight is  written
+ *   workspace  at least mla_norm_rope_bwd_workspace_size(n_tok, h_q) bytes,
+ *              16-byte aligned, where a weight is given; contents ignored.  Two
+ *              calls that may run concurrently need separate workspaces
+ *
+ * Padding tokens take no part: their rows of dq_in and dkv_in are zero.  Sums
+ * are taken in a fixed order: the same call gives the same bits.
+ */
+sparse_mla_status_t mla_norm_rope_bwd(const void* q, long long q_tok_stride, long long q_head_stride, const void* kv,
+                                      long long kv_tok_stride, const int32_t* positions, const float* cos_sin,
+                                      int n_pos, const void* q_weight, const void* kv_weight, float eps,
+                                      int interleaved, const float* dq, const float* dkv, void* dq_in, void* dkv_in,
+                                      float* dq_weight, float* dkv_weight, int n_tok, int h_q, int d_qk,
+                                      void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace mla_norm_rope_bwd needs on the current device. */
+size_t mla_norm_rope_bwd_workspace_size(int n_tok, int h_q);
+
+/*
  * sparse_mla_decode without a caller workspace, for callers that cannot
  * allocate device memory at the point of the call: code running inside a
  * serving engine whose allocator owns every byte of the device (a KV-cache

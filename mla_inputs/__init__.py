@@ -368,6 +368,64 @@ def decode_case_fp8(seed: int, batch: int, s_next: int, h_q: int, lo: int, hi: i
     return c, quantize_fp8_slots(c.kv_cache, pow2_scales=pow2_scales)
 
 
+# --------------------------------------------------------------------------
+# 4-bit KV cache and the rows that the norms and the rotation take
+# --------------------------------------------------------------------------
+
+FP4_SLOT_BYTES = 416   # 256 bytes of e2m1 codes, 32 e4m3 scales, 64 bf16 rope values
+FP4_VALUES = (0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0)
+
+
+def quantize_fp4_slots(latent: torch.Tensor, kv_scale: float = 1.0) -> torch.Tensor:
+    """Latent rows [..., 576] -> 4-bit cache slots uint8 [..., 416]: groups of
+    16 of the first 512 values with an e4m3 scale amax / (6 kv_scale) (at
+    least 2^-9) and the nearest e2m1 codes, then the last 64 values as bf16.
+    A group holding NaN (a poisoned slot) gets a NaN scale."""
+    lead = latent.shape[:-1]
+    x = latent.float().reshape(-1, D_QK)
+    v = x[:, :512].reshape(-1, 32, 16)
+    amax = v.abs().amax(dim=-1)
+    bad = torch.isnan(amax)
+    scale = (torch.nan_to_num(amax) / (6 * kv_scale)).clamp(2.0 ** -9, 448.0).to(torch.float8_e4m3fn)
+    step = (scale.float() * kv_scale)[..., None]
+    grid = torch.tensor(FP4_VALUES)
+    mag = torch.nan_to_num(v.abs() / step)
+    code = torch.bucketize(mag, (grid[1:] + grid[:-1]) / 2)
+    code = code | (torch.signbit(v).long() << 3)
+    sc = torch.where(bad, torch.tensor(0x7F, dtype=torch.uint8), scale.view(torch.uint8))
+    code = code.reshape(-1, 256, 2).to(torch.uint8)
+    rope = x[:, 512:].to(torch.bfloat16).contiguous().view(torch.uint8).reshape(-1, 128)
+    return torch.cat([code[..., 0] | (code[..., 1] << 4), sc, rope], dim=1).reshape(*lead, FP4_SLOT_BYTES).contiguous()
+
+
+def decode_case_fp4(seed: int, batch: int, s_next: int, h_q: int, lo: int, hi: int, topk: int = TOPK,
+                    page: int = PAGE, spare_pages: int = 64, kv_scale: float = 1.0, name: str = ""):
+    """A paged decode case whose cache is in 4 bits (decode_case's contexts,
+    pool, lists and poisoned slots).  Returns (case, cache_u8 [num_blocks,
+    page, 416])."""
+    c = decode_case(seed, batch, s_next, h_q, lo, hi, topk=topk, page=page, spare_pages=spare_pages,
+                    name=name or f"decode_fp4_b{batch}_s{s_next}_h{h_q}")
+    return c, quantize_fp4_slots(c.kv_cache, kv_scale)
+
+
+def rope_table(n_pos: int, base: float = 10000.0) -> torch.Tensor:
+    """cos_sin [n_pos, 64] fp32: 32 cosines, then 32 sines, of position times
+    base^(-i/32), taken in float64."""
+    a = torch.arange(n_pos, dtype=torch.float64)[:, None] * base ** (-torch.arange(32, dtype=torch.float64) / 32)
+    return torch.cat([a.cos(), a.sin()], dim=1).float()
+
+
+def norm_rows(seed: int, n_tok: int, h_q: int):
+    """q [n_tok, h_q, 576], kv [n_tok, 576] (N(0,1) times factors per column
+    and per row, bf16) and two norm weights [512] around 1 (bf16)."""
+    g = _gen(seed * 6101 + 13)
+    rn = lambda *shape: torch.randn(shape, generator=g)  # noqa: E731
+    size = torch.exp(0.5 * rn(D_QK))
+    q = (rn(n_tok, h_q, D_QK) * size * torch.exp(rn(n_tok, h_q, 1))).bfloat16()
+    kv = (rn(n_tok, D_QK) * size * torch.exp(rn(n_tok, 1))).bfloat16()
+    return q, kv, (1 + 0.2 * rn(512)).bfloat16(), (1 + 0.2 * rn(512)).bfloat16()
+
+
 def nominal_flops(s_q: int, h_q: int, topk: int = TOPK, d_qk: int = D_QK, d_v: int = D_V) -> float:
     """2*s_q*h_q*topk*(d_qk+d_v): the workload's nominal FLOP count."""
     return 2.0 * s_q * h_q * topk * (d_qk + d_v)

@@ -25,6 +25,7 @@ from . import build as _build
 _LIB: Optional[ctypes.CDLL] = None
 
 c_int, c_float, c_void_p, c_size_t = ctypes.c_int, ctypes.c_float, ctypes.c_void_p, ctypes.c_size_t
+c_longlong = ctypes.c_longlong
 
 STATUS = {0: "SPARSE_MLA_OK", 1: "SPARSE_MLA_ERR_INVALID_ARG", 2: "SPARSE_MLA_ERR_UNSUPPORTED_SHAPE",
           3: "SPARSE_MLA_ERR_UNSUPPORTED_ARCH", 4: "SPARSE_MLA_ERR_CUDA", 5: "SPARSE_MLA_ERR_DEVICE_TIMEOUT",
@@ -54,6 +55,17 @@ SIGNATURES = {
                                           c_void_p, c_int, c_int, c_int, c_int, c_int, c_int, c_int, c_int, c_int,
                                           c_void_p]),
     "sparse_mla_decode_noalloc_max_scratch_bytes": (c_size_t, []),
+    "sparse_mla_decode_fp4": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_float, c_float, c_void_p,
+                                      c_void_p, c_int, c_int, c_int, c_int, c_int, c_int, c_int, c_int, c_int,
+                                      c_void_p, c_size_t, c_void_p]),
+    "sparse_mla_decode_fp4_workspace_size": (c_size_t, [c_int, c_int, c_int, c_int, c_int]),
+    "mla_norm_rope": (c_int, [c_void_p, c_longlong, c_longlong, c_void_p, c_longlong, c_void_p, c_void_p, c_int,
+                              c_void_p, c_void_p, c_float, c_int, c_void_p, c_void_p, c_void_p, c_int, c_float,
+                              c_void_p, c_int, c_int, c_int, c_int, c_void_p]),
+    "mla_norm_rope_bwd": (c_int, [c_void_p, c_longlong, c_longlong, c_void_p, c_longlong, c_void_p, c_void_p, c_int,
+                                  c_void_p, c_void_p, c_float, c_int, c_void_p, c_void_p, c_void_p, c_void_p,
+                                  c_void_p, c_void_p, c_int, c_int, c_int, c_void_p, c_size_t, c_void_p]),
+    "mla_norm_rope_bwd_workspace_size": (c_size_t, [c_int, c_int]),
     "sparse_mla_debug_valid_count": (c_int, [c_void_p, c_int, c_int, c_int, c_void_p, c_void_p]),
     "sparse_mla_debug_valid_count_varlen": (c_int, [c_void_p, c_void_p, c_void_p, c_int, c_int, c_int, c_int,
                                                     c_void_p, c_void_p]),
@@ -397,6 +409,221 @@ def sparse_mla_decode_fp8(q, kv_cache, block_table, cache_seqlens, indices, sm_s
                                    max_blocks, num_blocks, _ptr(workspace), ws_bytes, _stream(stream))
     _check(st, "sparse_mla_decode_fp8")
     return out, lse
+
+
+# ---------------------------------------------------------------- 4-bit cache decode
+
+FP4_SLOT_BYTES = 416
+
+
+class _launch_on:
+    """The stream a call launches on, with the tensors' device current
+    meanwhile (the library launches on the current device): `stream`, or the
+    current stream of that device."""
+
+    def __init__(self, device, stream):
+        on = getattr(stream, "device", None)
+        if on is not None and _device_key(on) != _device_key(device):
+            raise ValueError(f"stream is on {on}; the call's tensors are on {device}")
+        self.device, self.stream, self.guard = device, stream, None
+
+    def __enter__(self):
+        if self.device.type == "cuda" and self.device.index != torch.cuda.current_device():
+            self.guard = torch.cuda.device(self.device)
+            self.guard.__enter__()
+        return _stream(self.stream)
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def decode_fp4_workspace_size(batch: int, s_next: int, h_q: int, topk: int, d_v: int = 512) -> int:
+    """Bytes sparse_mla_decode_fp4 needs on the current device."""
+    return int(load().sparse_mla_decode_fp4_workspace_size(batch, s_next, h_q, d_v, topk))
+
+
+def sparse_mla_decode_fp4(q, kv_cache, block_table, cache_seqlens, indices, sm_scale, page_size=None,
+                          kv_scale: float = 1.0, workspace: Optional[torch.Tensor] = None, out=None, lse=None,
+                          stream=None):
+    """Paged decode over a 4-bit cache: kv_cache uint8 [num_blocks, page, 416]
+    (512 e2m1 codes, 32 e4m3 scales, 64 bf16 rope values per slot, as
+    mla_norm_rope writes them), a row's latent values code * scale *
+    kv_scale; everything else as sparse_mla_decode."""
+    lib = load()
+    batch, s_next, h_q, d_qk = q.shape
+    num_blocks = kv_cache.shape[0]
+    page = kv_cache.shape[1] if page_size is None else page_size
+    max_blocks = block_table.shape[1]
+    topk = indices.shape[-1]
+    for t, dt, n in ((q, torch.bfloat16, "q"), (kv_cache, torch.uint8, "kv_cache"),
+                     (block_table, torch.int32, "block_table"), (cache_seqlens, torch.int32, "cache_seqlens"),
+                     (indices, torch.int32, "indices")):
+        _need(t, dt, n)
+    if kv_cache.shape[-1] != FP4_SLOT_BYTES:
+        raise ValueError(f"kv_cache slots must be {FP4_SLOT_BYTES} bytes, got {kv_cache.shape[-1]}")
+    dev = q.device
+    _fits(kv_cache, num_blocks * page * FP4_SLOT_BYTES, "kv_cache", dev)
+    _fits(block_table, batch * max_blocks, "block_table", dev)
+    _fits(cache_seqlens, batch, "cache_seqlens", dev)
+    _fits(indices, batch * s_next * topk, "indices", dev)
+    _given(out, torch.bfloat16, "out", batch * s_next * h_q * 512, dev)
+    _given(lse, torch.float32, "lse", batch * s_next * h_q, dev)
+    _workspace(workspace, dev)
+    with _launch_on(dev, stream) as cs:
+        if out is None:
+            out = torch.empty((batch, s_next, h_q, 512), dtype=torch.bfloat16, device=dev)
+        if lse is None:
+            lse = torch.empty((batch, s_next, h_q), dtype=torch.float32, device=dev)
+        need = lib.sparse_mla_decode_fp4_workspace_size(batch, s_next, h_q, 512, topk)
+        if workspace is None and need > 0:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        st = lib.sparse_mla_decode_fp4(_ptr(q), _ptr(kv_cache), _ptr(block_table), _ptr(cache_seqlens),
+                                       _ptr(indices), float(sm_scale), float(kv_scale), _ptr(out), _ptr(lse), batch,
+                                       s_next, h_q, d_qk, 512, topk, page, max_blocks, num_blocks, _ptr(workspace),
+                                       ws_bytes, cs)
+    _check(st, "sparse_mla_decode_fp4")
+    return out, lse
+
+
+# ---------------------------------------------------------------- norms, rotation, cache write
+
+_CACHE_FORMATS = {(torch.bfloat16, 576): 0, (torch.uint8, FP8_SLOT_BYTES): 1, (torch.uint8, FP4_SLOT_BYTES): 2}
+
+
+def _rows(t: torch.Tensor, name: str, heads: bool):
+    """(token stride, head stride) in elements of bf16 rows of 576 values:
+    [n, h, 576] with `heads`, else [n, 576] or [n, 1, 576].  The values of a
+    row are contiguous; rows start on 16 bytes."""
+    _on_cuda(t, name)
+    if t.dtype != torch.bfloat16:
+        raise ValueError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if not heads and t.dim() == 3 and t.shape[1] == 1:
+        t = t[:, 0]
+    if t.dim() != (3 if heads else 2) or t.shape[-1] != 576:
+        raise ValueError(f"{name} must be {'[n, h, 576]' if heads else '[n, 576]'}, got {tuple(t.shape)}")
+    if t.stride(-1) != 1:
+        raise ValueError(f"the 576 values of a row of {name} must be contiguous")
+    steps = [t.stride(i) if t.shape[i] > 1 else 0 for i in range(t.dim() - 1)]
+    if any(s % 8 for s in steps) or t.data_ptr() % 16:
+        raise ValueError(f"rows of {name} must start on 16 bytes (strides {t.stride()})")
+    return steps
+
+
+def _norm_args(q, kv, positions, cos_sin, q_weight, kv_weight):
+    q_steps = _rows(q, "q", True)
+    kv_steps = _rows(kv, "kv", False)
+    n, h = q.shape[0], q.shape[1]
+    dev = q.device
+    if kv.shape[0] != n:
+        raise ValueError(f"kv has {kv.shape[0]} rows; q has {n} tokens")
+    if _device_key(kv.device) != _device_key(dev):
+        raise ValueError(f"kv is on {kv.device}; the call's tensors are on {dev}")
+    _need(positions, torch.int32, "positions")
+    _fits(positions, n, "positions", dev)
+    _need(cos_sin, torch.float32, "cos_sin")
+    if cos_sin.dim() != 2 or cos_sin.shape[1] != 64:
+        raise ValueError(f"cos_sin must be [n_pos, 64], got {tuple(cos_sin.shape)}")
+    _fits(cos_sin, 0, "cos_sin", dev)
+    for w, name in ((q_weight, "q_weight"), (kv_weight, "kv_weight")):
+        if w is not None:
+            _given(w, torch.bfloat16, name, 512, dev)
+            if w.numel() != 512:
+                raise ValueError(f"{name} must hold 512 values, got {w.numel()}")
+    return n, h, dev, q_steps, kv_steps
+
+
+def mla_norm_rope(q, kv, positions, cos_sin, q_weight=None, kv_weight=None, eps: float = 1e-6,
+                  interleaved: bool = True, kv_cache: Optional[torch.Tensor] = None,
+                  slots: Optional[torch.Tensor] = None, kv_scale: float = 1.0, q_out=None, kv_out=None, stream=None):
+    """RMS norm of every query head's row and of the latent row (their first
+    512 values; a weight that is None leaves its rows unnormed), the position
+    rotation of their last 64, and the latent row's write into its cache slot.
+
+    q [n, h, 576] and kv [n, 576] (or [n, 1, 576]) bf16, rows strided as they
+    are; positions [n] int32 (outside [0, n_pos): a padding token, left as it
+    was); cos_sin [n_pos, 64] fp32, 32 cosines then 32 sines; kv_cache
+    [num_blocks, page, w]: bf16 with w = 576, or uint8 with w = 656 (FP8) or
+    416 (4 bits, with its factor kv_scale); slots [n] int32, distinct (outside
+    the cache: not stored).  -> (q_out [n, h, 576], kv_out [n, 576]), bf16;
+    kv_out holds what the slots stand for.  q_out / kv_out may be q / kv."""
+    lib = load()
+    n, h, dev, q_steps, kv_steps = _norm_args(q, kv, positions, cos_sin, q_weight, kv_weight)
+    form, n_slots = 0, 0
+    if kv_cache is not None:
+        _need(kv_cache, kv_cache.dtype, "kv_cache")
+        form = _CACHE_FORMATS.get((kv_cache.dtype, kv_cache.shape[-1]), -1)
+        if form < 0:
+            raise ValueError("kv_cache must be bf16 [.., 576] or uint8 [.., 656] or [.., 416], got "
+                             f"{kv_cache.dtype} {tuple(kv_cache.shape)}")
+        if slots is None:
+            raise ValueError("kv_cache is given without slots")
+        _fits(kv_cache, 0, "kv_cache", dev)
+        _need(slots, torch.int32, "slots")
+        _fits(slots, n, "slots", dev)
+        n_slots = kv_cache.numel() // kv_cache.shape[-1]
+        if n_slots > 2 ** 31 - 1:
+            raise ValueError("a cache of more than 2^31 - 1 slots")
+    elif slots is not None:
+        raise ValueError("slots are given without kv_cache")
+    _given(q_out, torch.bfloat16, "q_out", n * h * 576, dev)
+    _given(kv_out, torch.bfloat16, "kv_out", n * 576, dev)
+    with _launch_on(dev, stream) as cs:
+        if q_out is None:
+            q_out = torch.empty((n, h, 576), dtype=torch.bfloat16, device=dev)
+        if kv_out is None:
+            kv_out = torch.empty((n, 576), dtype=torch.bfloat16, device=dev)
+        st = lib.mla_norm_rope(_ptr(q), q_steps[0], q_steps[1], _ptr(kv), kv_steps[0], _ptr(positions),
+                               _ptr(cos_sin), cos_sin.shape[0], _ptr(q_weight), _ptr(kv_weight), float(eps),
+                               int(bool(interleaved)), _ptr(q_out), _ptr(kv_out), _ptr(kv_cache), form,
+                               float(kv_scale), _ptr(slots), n_slots, n, h, 576, cs)
+    _check(st, "mla_norm_rope")
+    return q_out, kv_out
+
+
+def norm_rope_bwd_workspace_size(n_tok: int, h_q: int) -> int:
+    """Bytes mla_norm_rope_bwd needs on the current device."""
+    return int(load().mla_norm_rope_bwd_workspace_size(n_tok, h_q))
+
+
+def mla_norm_rope_bwd(q, kv, positions, cos_sin, dq, dkv, q_weight=None, kv_weight=None, eps: float = 1e-6,
+                      interleaved: bool = True, workspace: Optional[torch.Tensor] = None, dq_in=None, dkv_in=None,
+                      dq_weight=None, dkv_weight=None, stream=None):
+    """Gradients of mla_norm_rope from dq [n, h, 576] and dkv [n, 576] fp32 (as
+    sparse_mla_bwd returns them) -> (dq_in [n, h, 576] bf16, dkv_in [n, 576]
+    bf16, dq_weight [512] fp32 or None, dkv_weight [512] fp32 or None).
+    Padding tokens get zero rows."""
+    lib = load()
+    n, h, dev, q_steps, kv_steps = _norm_args(q, kv, positions, cos_sin, q_weight, kv_weight)
+    for t, need, name in ((dq, n * h * 576, "dq"), (dkv, n * 576, "dkv")):
+        _need(t, torch.float32, name)
+        _fits(t, need, name, dev)
+    _given(dq_in, torch.bfloat16, "dq_in", n * h * 576, dev)
+    _given(dkv_in, torch.bfloat16, "dkv_in", n * 576, dev)
+    for w, dw, name in ((q_weight, dq_weight, "dq_weight"), (kv_weight, dkv_weight, "dkv_weight")):
+        if w is None and dw is not None:
+            raise ValueError(f"{name} is given without its weight")
+        _given(dw, torch.float32, name, 512, dev)
+    _workspace(workspace, dev)
+    with _launch_on(dev, stream) as cs:
+        if dq_in is None:
+            dq_in = torch.empty((n, h, 576), dtype=torch.bfloat16, device=dev)
+        if dkv_in is None:
+            dkv_in = torch.empty((n, 576), dtype=torch.bfloat16, device=dev)
+        if q_weight is not None and dq_weight is None:
+            dq_weight = torch.empty(512, dtype=torch.float32, device=dev)
+        if kv_weight is not None and dkv_weight is None:
+            dkv_weight = torch.empty(512, dtype=torch.float32, device=dev)
+        if workspace is None and (q_weight is not None or kv_weight is not None):
+            workspace = torch.empty(max(16, lib.mla_norm_rope_bwd_workspace_size(n, h)), dtype=torch.uint8, device=dev)
+        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        st = lib.mla_norm_rope_bwd(_ptr(q), q_steps[0], q_steps[1], _ptr(kv), kv_steps[0], _ptr(positions),
+                                   _ptr(cos_sin), cos_sin.shape[0], _ptr(q_weight), _ptr(kv_weight), float(eps),
+                                   int(bool(interleaved)), _ptr(dq), _ptr(dkv), _ptr(dq_in), _ptr(dkv_in),
+                                   _ptr(dq_weight), _ptr(dkv_weight), n, h, 576, _ptr(workspace), ws_bytes, cs)
+    _check(st, "mla_norm_rope_bwd")
+    return dq_in, dkv_in, dq_weight, dkv_weight
 
 
 # ---------------------------------------------------------------- debug: valid entries per token

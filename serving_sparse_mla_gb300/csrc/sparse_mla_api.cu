@@ -6,13 +6,16 @@
 
 #include <atomic>
 #include <climits>
+#include <cmath>
 #include <cstdint>
 #include <cstring>
 #include <mutex>
 
 #include "bwd_kernel.cuh"
+#include "fp4_decode_kernel.cuh"
 #include "fwd_kernel.cuh"
 #include "indexer_kernel.cuh"
+#include "norm_rope_kernel.cuh"
 #include "sparse_mla.h"
 
 namespace {
@@ -77,6 +80,10 @@ sparse_mla_status_t device_setup(int* sm_count) {
                              smla::idx_smem_bytes()) != cudaSuccess ||
         cudaFuncSetAttribute(smla::dsa_scores_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              smla::idx_smem_bytes()) != cudaSuccess ||
+        cudaFuncSetAttribute(smla::fp4_decode_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             smla::Fp4Layout<1>::kBytes) != cudaSuccess ||
+        cudaFuncSetAttribute(smla::fp4_decode_kernel<2>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             smla::Fp4Layout<2>::kBytes) != cudaSuccess ||
         cudaFuncSetAttribute(smla::dsa_topk_kernel<256>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              kTopkMaxSmem) != cudaSuccess ||
         cudaFuncSetAttribute(smla::dsa_topk_kernel<1024>, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -476,6 +483,262 @@ sparse_mla_status_t sparse_mla_decode_fp8(const void* q, const void* kv_cache, c
   return run_decode(smla::kPagedFp8, q, kv_cache, block_table, cache_seqlens, indices, sm_scale, out, lse, batch,
                     s_next, h_q, d_qk, d_v, topk, page_size, max_blocks, num_blocks, workspace, workspace_bytes,
                     stream);
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------------------ 4-bit cache decode
+
+namespace {
+
+// Heads of a unit: 8 or 16 (more heads are several units of 16).
+int f4_heads(int h_q) { return h_q <= 8 ? 8 : 16; }
+
+// The grid: two CTAs per SM, or fewer where the lists are short (a unit is
+// cut into at most 32 pieces, as decode_ctas).
+int f4_ctas(long long n_tok, int h_q, int topk, int sms) {
+  const int nb = blocks_per_list(topk);
+  const int groups = (h_q + f4_heads(h_q) - 1) / f4_heads(h_q);
+  const long long min_blocks = (nb + 30) / 31;
+  const long long g = n_tok * groups * nb / min_blocks;
+  return static_cast<int>(g > 2 * sms ? 2 * sms : (g < 1 ? 1 : g));
+}
+
+struct F4Plan {
+  int ctas, groups, rows;
+  size_t lse_at, count_at, bytes;   // bytes from the workspace's start; bytes 0: no workspace
+};
+
+F4Plan f4_plan(long long n_tok, int h_q, int topk, int sms) {
+  F4Plan f;
+  const int H = f4_heads(h_q);
+  f.groups = (h_q + H - 1) / H;
+  f.rows = h_q < H ? h_q : H;
+  f.ctas = f4_ctas(n_tok, h_q, topk, sms);
+  const size_t slots = 2 * static_cast<size_t>(f.ctas) * static_cast<size_t>(f.rows);
+  f.lse_at = slots * smla::kDv * sizeof(float);
+  f.count_at = (f.lse_at + slots * sizeof(float) + 15) & ~size_t(15);
+  f.bytes = f.ctas > 1 ? f.count_at + static_cast<size_t>(n_tok) * f.groups * sizeof(int32_t) : 0;
+  return f;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t sparse_mla_decode_fp4_workspace_size(int batch, int s_next, int h_q, int d_v, int topk) {
+  if (batch < 1 || s_next < 1 || h_q < 1 || topk < 1 || d_v != smla::kDv) return 0;
+  int sms = 0;
+  if (device_setup(&sms) != SPARSE_MLA_OK) return 0;
+  return f4_plan(static_cast<long long>(batch) * s_next, h_q, topk, sms).bytes;
+}
+
+sparse_mla_status_t sparse_mla_decode_fp4(const void* q, const void* kv_cache, const int32_t* block_table,
+                                          const int32_t* cache_seqlens, const int32_t* indices, float sm_scale,
+                                          float kv_scale, void* out, float* lse, int batch, int s_next, int h_q,
+                                          int d_qk, int d_v, int topk, int page_size, int max_blocks, int num_blocks,
+                                          void* workspace, size_t workspace_bytes, void* stream) {
+  int sms = 0;
+  sparse_mla_status_t st = check_decode(q, kv_cache, block_table, cache_seqlens, indices, out, lse, batch, s_next,
+                                        h_q, d_qk, d_v, topk, page_size, max_blocks, num_blocks, &sms);
+  if (st != SPARSE_MLA_OK) return st;
+  if (!std::isfinite(kv_scale) || kv_scale <= 0.f) return SPARSE_MLA_ERR_INVALID_ARG;
+  const long long n_tok = static_cast<long long>(batch) * s_next;
+  if (n_tok == 0) return SPARSE_MLA_OK;
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  if (num_blocks == 0 || max_blocks == 0) return launch_fill(out, lse, n_tok * h_q, cs);
+  const F4Plan f = f4_plan(n_tok, h_q, topk, sms);
+  if (n_tok * f.groups > INT_MAX) return SPARSE_MLA_ERR_INVALID_ARG;   // units are counted in 32 bits
+  if (f.bytes > 0 && (workspace_bytes < f.bytes || !workspace)) return SPARSE_MLA_ERR_WORKSPACE_TOO_SMALL;
+  if (f.bytes > 0 && !aligned(workspace, 16)) return SPARSE_MLA_ERR_INVALID_ARG;
+  smla::Fp4Params p;
+  std::memset(&p, 0, sizeof(p));
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.cache = static_cast<const uint8_t*>(kv_cache);
+  p.indices = indices;
+  p.block_table = block_table;
+  p.seqlens = cache_seqlens;
+  p.out = static_cast<__nv_bfloat16*>(out);
+  p.lse = lse;
+  p.n_tok = static_cast<int>(n_tok);
+  p.h_q = h_q;
+  p.topk = topk;
+  p.s_next = s_next;
+  p.page_size = page_size;
+  p.max_blocks = max_blocks;
+  p.num_blocks = num_blocks;
+  p.groups = f.groups;
+  p.nb = blocks_per_list(topk);
+  p.ctas = f.ctas;
+  p.part_rows = f.rows;
+  p.scale_log2 = sm_scale * 1.4426950408889634f;
+  p.kv_scale = kv_scale;
+  if (f.bytes > 0) {
+    unsigned char* ws = static_cast<unsigned char*>(workspace);
+    p.part_o = reinterpret_cast<float*>(ws);
+    p.part_lse = reinterpret_cast<float*>(ws + f.lse_at);
+    p.merge_count = reinterpret_cast<int32_t*>(ws + f.count_at);
+    if (cudaMemsetAsync(p.merge_count, 0, static_cast<size_t>(n_tok) * f.groups * sizeof(int32_t), cs) != cudaSuccess)
+      return SPARSE_MLA_ERR_CUDA;
+  }
+  if (f4_heads(h_q) == 8)
+    smla::fp4_decode_kernel<1><<<p.ctas, smla::kF4Threads, smla::Fp4Layout<1>::kBytes, cs>>>(p);
+  else
+    smla::fp4_decode_kernel<2><<<p.ctas, smla::kF4Threads, smla::Fp4Layout<2>::kBytes, cs>>>(p);
+  return cudaGetLastError() == cudaSuccess ? SPARSE_MLA_OK : SPARSE_MLA_ERR_CUDA;
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------------------ norms, rotation, cache write
+
+namespace {
+
+// Row strides: whole 16-byte steps, so that every row starts on one.
+bool row_strides_ok(long long a, long long b) { return a % 8 == 0 && b % 8 == 0; }
+
+sparse_mla_status_t check_norm(const void* q, long long q_tok_stride, long long q_head_stride, const void* kv,
+                               long long kv_tok_stride, const int32_t* positions, const float* cos_sin, int n_pos,
+                               const void* q_weight, const void* kv_weight, float eps, int n_tok, int h_q, int d_qk) {
+  if (n_tok < 0 || h_q < 1 || n_pos < 0 || !(eps >= 0.f) || !std::isfinite(eps)) return SPARSE_MLA_ERR_INVALID_ARG;
+  if (d_qk != smla::kRowW) return SPARSE_MLA_ERR_UNSUPPORTED_SHAPE;
+  if (!row_strides_ok(q_tok_stride, q_head_stride) || !row_strides_ok(kv_tok_stride, 0))
+    return SPARSE_MLA_ERR_INVALID_ARG;
+  if (!aligned(q_weight, 16) || !aligned(kv_weight, 16)) return SPARSE_MLA_ERR_INVALID_ARG;
+  if (n_tok == 0) return SPARSE_MLA_OK;
+  if (!q || !kv || !positions || (n_pos > 0 && !cos_sin)) return SPARSE_MLA_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(kv, 16) || !aligned(positions, 4) || !aligned(cos_sin, 16))
+    return SPARSE_MLA_ERR_INVALID_ARG;
+  return SPARSE_MLA_OK;
+}
+
+smla::NormParams norm_params(const void* q, long long q_tok_stride, long long q_head_stride, const void* kv,
+                             long long kv_tok_stride, const int32_t* positions, const float* cos_sin, int n_pos,
+                             const void* q_weight, const void* kv_weight, float eps, int interleaved, int n_tok,
+                             int h_q) {
+  smla::NormParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.kv = static_cast<const __nv_bfloat16*>(kv);
+  p.q_tok = q_tok_stride;
+  p.q_head = q_head_stride;
+  p.kv_tok = kv_tok_stride;
+  p.positions = positions;
+  p.cos_sin = cos_sin;
+  p.n_pos = n_pos;
+  p.q_weight = static_cast<const __nv_bfloat16*>(q_weight);
+  p.kv_weight = static_cast<const __nv_bfloat16*>(kv_weight);
+  p.eps = eps;
+  p.interleaved = interleaved;
+  p.n_tok = n_tok;
+  p.h_q = h_q;
+  return p;
+}
+
+// Rows per warp grow with the batch once the card is full (CTAs of 8 warps,
+// one row per warp at a time).
+int norm_ctas(long long rows, int sms, int per_sm) {
+  const long long need = (rows + smla::kNormWarps - 1) / smla::kNormWarps;
+  const long long most = static_cast<long long>(sms) * per_sm;
+  return static_cast<int>(need < most ? (need < 1 ? 1 : need) : most);
+}
+constexpr int kNormFwdPerSm = 32;
+constexpr int kNormBwdPerSm = 4;
+
+}  // namespace
+
+extern "C" {
+
+sparse_mla_status_t mla_norm_rope(const void* q, long long q_tok_stride, long long q_head_stride, const void* kv,
+                                  long long kv_tok_stride, const int32_t* positions, const float* cos_sin, int n_pos,
+                                  const void* q_weight, const void* kv_weight, float eps, int interleaved,
+                                  void* q_out, void* kv_out, void* kv_cache, int cache_format, float kv_scale,
+                                  const int32_t* slots, int n_slots, int n_tok, int h_q, int d_qk, void* stream) {
+  sparse_mla_status_t st = check_norm(q, q_tok_stride, q_head_stride, kv, kv_tok_stride, positions, cos_sin, n_pos,
+                                      q_weight, kv_weight, eps, n_tok, h_q, d_qk);
+  if (st != SPARSE_MLA_OK) return st;
+  if (n_slots < 0 || cache_format < 0 || cache_format > 2) return SPARSE_MLA_ERR_INVALID_ARG;
+  if (!std::isfinite(kv_scale) || kv_scale <= 0.f || (cache_format != SPARSE_MLA_CACHE_FP4 && kv_scale != 1.f))
+    return SPARSE_MLA_ERR_INVALID_ARG;
+  const bool cached = kv_cache != nullptr && n_slots > 0;
+  if (cached && n_tok > 0 && (!slots || !aligned(slots, 4) || !aligned(kv_cache, 16))) return SPARSE_MLA_ERR_INVALID_ARG;
+  if (n_tok > 0 && (!q_out || !aligned(q_out, 16) || !aligned(kv_out, 16))) return SPARSE_MLA_ERR_INVALID_ARG;
+  int sms = 0;
+  if ((st = device_setup(&sms)) != SPARSE_MLA_OK) return st;
+  if (n_tok == 0) return SPARSE_MLA_OK;
+  smla::NormParams p = norm_params(q, q_tok_stride, q_head_stride, kv, kv_tok_stride, positions, cos_sin, n_pos,
+                                   q_weight, kv_weight, eps, interleaved, n_tok, h_q);
+  p.q_out = static_cast<__nv_bfloat16*>(q_out);
+  p.kv_out = static_cast<__nv_bfloat16*>(kv_out);
+  p.cache = static_cast<uint8_t*>(kv_cache);
+  p.slots = slots;
+  // Without a cache the row is still rounded as that format would hold it.
+  p.format = cache_format;
+  p.n_slots = cached ? n_slots : 0;
+  p.kv_scale = kv_scale;
+  p.kv_scale6 = static_cast<float>(6.0 * kv_scale);
+  const long long rows = static_cast<long long>(n_tok) * (h_q + 1);
+  smla::norm_rope_kernel<<<norm_ctas(rows, sms, kNormFwdPerSm), smla::kNormWarps * 32, 0,
+                           static_cast<cudaStream_t>(stream)>>>(p);
+  return cudaGetLastError() == cudaSuccess ? SPARSE_MLA_OK : SPARSE_MLA_ERR_CUDA;
+}
+
+size_t mla_norm_rope_bwd_workspace_size(int n_tok, int h_q) {
+  if (n_tok < 1 || h_q < 1) return 0;
+  int sms = 0;
+  if (device_setup(&sms) != SPARSE_MLA_OK) return 0;
+  // one share of 512 sums per CTA for either weight
+  return 2 * static_cast<size_t>(norm_ctas(static_cast<long long>(n_tok) * h_q, sms, kNormBwdPerSm)) * smla::kLatW *
+         sizeof(float);
+}
+
+sparse_mla_status_t mla_norm_rope_bwd(const void* q, long long q_tok_stride, long long q_head_stride, const void* kv,
+                                      long long kv_tok_stride, const int32_t* positions, const float* cos_sin,
+                                      int n_pos, const void* q_weight, const void* kv_weight, float eps,
+                                      int interleaved, const float* dq, const float* dkv, void* dq_in, void* dkv_in,
+                                      float* dq_weight, float* dkv_weight, int n_tok, int h_q, int d_qk,
+                                      void* workspace, size_t workspace_bytes, void* stream) {
+  sparse_mla_status_t st = check_norm(q, q_tok_stride, q_head_stride, kv, kv_tok_stride, positions, cos_sin, n_pos,
+                                      q_weight, kv_weight, eps, n_tok, h_q, d_qk);
+  if (st != SPARSE_MLA_OK) return st;
+  if ((q_weight != nullptr) != (dq_weight != nullptr) || (kv_weight != nullptr) != (dkv_weight != nullptr) ||
+      !aligned(dq_weight, 4) || !aligned(dkv_weight, 4))
+    return SPARSE_MLA_ERR_INVALID_ARG;
+  if (n_tok > 0 && (!dq || !dkv || !dq_in || !dkv_in || !aligned(dq, 16) || !aligned(dkv, 16) || !aligned(dq_in, 16) ||
+                    !aligned(dkv_in, 16)))
+    return SPARSE_MLA_ERR_INVALID_ARG;
+  int sms = 0;
+  if ((st = device_setup(&sms)) != SPARSE_MLA_OK) return st;
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  if (n_tok == 0) {
+    if (dq_weight && cudaMemsetAsync(dq_weight, 0, smla::kLatW * sizeof(float), cs) != cudaSuccess)
+      return SPARSE_MLA_ERR_CUDA;
+    if (dkv_weight && cudaMemsetAsync(dkv_weight, 0, smla::kLatW * sizeof(float), cs) != cudaSuccess)
+      return SPARSE_MLA_ERR_CUDA;
+    return SPARSE_MLA_OK;
+  }
+  const bool sums = dq_weight || dkv_weight;
+  const size_t need = sums ? mla_norm_rope_bwd_workspace_size(n_tok, h_q) : 0;
+  if (sums && (!workspace || workspace_bytes < need)) return SPARSE_MLA_ERR_WORKSPACE_TOO_SMALL;
+  if (sums && !aligned(workspace, 16)) return SPARSE_MLA_ERR_INVALID_ARG;
+  smla::NormParams p = norm_params(q, q_tok_stride, q_head_stride, kv, kv_tok_stride, positions, cos_sin, n_pos,
+                                   q_weight, kv_weight, eps, interleaved, n_tok, h_q);
+  p.dq = dq;
+  p.dkv = dkv;
+  p.dq_in = static_cast<__nv_bfloat16*>(dq_in);
+  p.dkv_in = static_cast<__nv_bfloat16*>(dkv_in);
+  const int ctas = norm_ctas(static_cast<long long>(n_tok) * h_q, sms, kNormBwdPerSm);
+  p.part_q = static_cast<float*>(workspace);
+  p.part_kv = p.part_q + static_cast<size_t>(ctas) * smla::kLatW;
+  const dim3 threads(smla::kNormWarps * 32);
+  if (q_weight && kv_weight) smla::norm_rope_bwd_kernel<true, true><<<ctas, threads, 0, cs>>>(p);
+  else if (q_weight) smla::norm_rope_bwd_kernel<true, false><<<ctas, threads, 0, cs>>>(p);
+  else if (kv_weight) smla::norm_rope_bwd_kernel<false, true><<<ctas, threads, 0, cs>>>(p);
+  else smla::norm_rope_bwd_kernel<false, false><<<ctas, threads, 0, cs>>>(p);
+  if (sums)
+    smla::norm_weight_grad_kernel<<<dim3(smla::kLatW / 32, 2), 256, 0, cs>>>(p.part_q, p.part_kv, dq_weight,
+                                                                             dkv_weight, ctas);
+  return cudaGetLastError() == cudaSuccess ? SPARSE_MLA_OK : SPARSE_MLA_ERR_CUDA;
 }
 
 }  // extern "C"
