@@ -161,7 +161,7 @@ def _fits(t: Optional[torch.Tensor], need: int, name: str, device) -> None:
     to the library imply, is refused before anything is launched."""
     if t is None:
         return
-    if _device_key(t.device) != _device_key(device):
+    if t.device != device and _device_key(t.device) != _device_key(device):
         raise ValueError(f"{name} is on {t.device}; the call's tensors are on {device}")
     if t.numel() < need:
         raise ValueError(f"{name} holds {t.numel()} elements; the call addresses {need}")
@@ -416,22 +416,33 @@ def sparse_mla_decode_fp8(q, kv_cache, block_table, cache_seqlens, indices, sm_s
 FP4_SLOT_BYTES = 416
 
 
+def _at(t: Optional[torch.Tensor]):
+    """The address as the number that ctypes takes for a pointer argument."""
+    return None if t is None else t.data_ptr()
+
+
 class _launch_on:
     """The stream a call launches on, with the tensors' device current
     meanwhile (the library launches on the current device): `stream`, or the
     current stream of that device."""
 
+    __slots__ = ("device", "stream", "guard")
+
     def __init__(self, device, stream):
-        on = getattr(stream, "device", None)
-        if on is not None and _device_key(on) != _device_key(device):
-            raise ValueError(f"stream is on {on}; the call's tensors are on {device}")
+        if stream is not None:
+            on = getattr(stream, "device", None)
+            if on is not None and on != device and _device_key(on) != _device_key(device):
+                raise ValueError(f"stream is on {on}; the call's tensors are on {device}")
         self.device, self.stream, self.guard = device, stream, None
 
     def __enter__(self):
-        if self.device.type == "cuda" and self.device.index != torch.cuda.current_device():
-            self.guard = torch.cuda.device(self.device)
+        dev = self.device
+        if dev.type == "cuda" and dev.index != torch.cuda.current_device():
+            self.guard = torch.cuda.device(dev)
             self.guard.__enter__()
-        return _stream(self.stream)
+        if self.stream is not None:
+            return self.stream.cuda_stream
+        return torch._C._cuda_getCurrentRawStream(dev.index)   # current_stream(dev).cuda_stream without its objects
 
     def __exit__(self, *exc):
         if self.guard is not None:
@@ -479,9 +490,9 @@ def sparse_mla_decode_fp4(q, kv_cache, block_table, cache_seqlens, indices, sm_s
         if workspace is None and need > 0:
             workspace = torch.empty(need, dtype=torch.uint8, device=dev)
         ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-        st = lib.sparse_mla_decode_fp4(_ptr(q), _ptr(kv_cache), _ptr(block_table), _ptr(cache_seqlens),
-                                       _ptr(indices), float(sm_scale), float(kv_scale), _ptr(out), _ptr(lse), batch,
-                                       s_next, h_q, d_qk, 512, topk, page, max_blocks, num_blocks, _ptr(workspace),
+        st = lib.sparse_mla_decode_fp4(_at(q), _at(kv_cache), _at(block_table), _at(cache_seqlens),
+                                       _at(indices), float(sm_scale), float(kv_scale), _at(out), _at(lse), batch,
+                                       s_next, h_q, d_qk, 512, topk, page, max_blocks, num_blocks, _at(workspace),
                                        ws_bytes, cs)
     _check(st, "sparse_mla_decode_fp4")
     return out, lse
@@ -499,27 +510,28 @@ def _rows(t: torch.Tensor, name: str, heads: bool):
     _on_cuda(t, name)
     if t.dtype != torch.bfloat16:
         raise ValueError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-    if not heads and t.dim() == 3 and t.shape[1] == 1:
-        t = t[:, 0]
-    if t.dim() != (3 if heads else 2) or t.shape[-1] != 576:
+    shape, steps = t.shape, t.stride()
+    if not heads and len(shape) == 3 and shape[1] == 1:
+        shape, steps = (shape[0], shape[2]), (steps[0], steps[2])
+    if len(shape) != (3 if heads else 2) or shape[-1] != 576:
         raise ValueError(f"{name} must be {'[n, h, 576]' if heads else '[n, 576]'}, got {tuple(t.shape)}")
-    if t.stride(-1) != 1:
+    if steps[-1] != 1:
         raise ValueError(f"the 576 values of a row of {name} must be contiguous")
-    steps = [t.stride(i) if t.shape[i] > 1 else 0 for i in range(t.dim() - 1)]
-    if any(s % 8 for s in steps) or t.data_ptr() % 16:
+    tok = steps[0] if shape[0] > 1 else 0
+    head = steps[1] if heads and shape[1] > 1 else 0
+    if tok % 8 or head % 8 or t.data_ptr() % 16:
         raise ValueError(f"rows of {name} must start on 16 bytes (strides {t.stride()})")
-    return steps
+    return tok, head
 
 
 def _norm_args(q, kv, positions, cos_sin, q_weight, kv_weight):
     q_steps = _rows(q, "q", True)
     kv_steps = _rows(kv, "kv", False)
-    n, h = q.shape[0], q.shape[1]
+    n, h, _ = q.shape
     dev = q.device
     if kv.shape[0] != n:
         raise ValueError(f"kv has {kv.shape[0]} rows; q has {n} tokens")
-    if _device_key(kv.device) != _device_key(dev):
-        raise ValueError(f"kv is on {kv.device}; the call's tensors are on {dev}")
+    _fits(kv, 0, "kv", dev)
     _need(positions, torch.int32, "positions")
     _fits(positions, n, "positions", dev)
     _need(cos_sin, torch.float32, "cos_sin")
@@ -574,10 +586,10 @@ def mla_norm_rope(q, kv, positions, cos_sin, q_weight=None, kv_weight=None, eps:
             q_out = torch.empty((n, h, 576), dtype=torch.bfloat16, device=dev)
         if kv_out is None:
             kv_out = torch.empty((n, 576), dtype=torch.bfloat16, device=dev)
-        st = lib.mla_norm_rope(_ptr(q), q_steps[0], q_steps[1], _ptr(kv), kv_steps[0], _ptr(positions),
-                               _ptr(cos_sin), cos_sin.shape[0], _ptr(q_weight), _ptr(kv_weight), float(eps),
-                               int(bool(interleaved)), _ptr(q_out), _ptr(kv_out), _ptr(kv_cache), form,
-                               float(kv_scale), _ptr(slots), n_slots, n, h, 576, cs)
+        st = lib.mla_norm_rope(_at(q), q_steps[0], q_steps[1], _at(kv), kv_steps[0], _at(positions),
+                               _at(cos_sin), cos_sin.shape[0], _at(q_weight), _at(kv_weight), float(eps),
+                               int(bool(interleaved)), _at(q_out), _at(kv_out), _at(kv_cache), form,
+                               float(kv_scale), _at(slots), n_slots, n, h, 576, cs)
     _check(st, "mla_norm_rope")
     return q_out, kv_out
 
@@ -618,10 +630,10 @@ def mla_norm_rope_bwd(q, kv, positions, cos_sin, dq, dkv, q_weight=None, kv_weig
         if workspace is None and (q_weight is not None or kv_weight is not None):
             workspace = torch.empty(max(16, lib.mla_norm_rope_bwd_workspace_size(n, h)), dtype=torch.uint8, device=dev)
         ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-        st = lib.mla_norm_rope_bwd(_ptr(q), q_steps[0], q_steps[1], _ptr(kv), kv_steps[0], _ptr(positions),
-                                   _ptr(cos_sin), cos_sin.shape[0], _ptr(q_weight), _ptr(kv_weight), float(eps),
-                                   int(bool(interleaved)), _ptr(dq), _ptr(dkv), _ptr(dq_in), _ptr(dkv_in),
-                                   _ptr(dq_weight), _ptr(dkv_weight), n, h, 576, _ptr(workspace), ws_bytes, cs)
+        st = lib.mla_norm_rope_bwd(_at(q), q_steps[0], q_steps[1], _at(kv), kv_steps[0], _at(positions),
+                                   _at(cos_sin), cos_sin.shape[0], _at(q_weight), _at(kv_weight), float(eps),
+                                   int(bool(interleaved)), _at(dq), _at(dkv), _at(dq_in), _at(dkv_in),
+                                   _at(dq_weight), _at(dkv_weight), n, h, 576, _at(workspace), ws_bytes, cs)
     _check(st, "mla_norm_rope_bwd")
     return dq_in, dkv_in, dq_weight, dkv_weight
 

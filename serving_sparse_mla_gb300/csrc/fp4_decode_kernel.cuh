@@ -30,12 +30,12 @@
 // f16 (11 bits).  The rotated part stays bf16 (its own MMAs).  All sums are
 // fp32.
 //
-// 256 threads, 64-row blocks in a ring of three (2 x 26 KB in flight per CTA,
-// two CTAs per SM): warp w takes rows 16 (w % 4) .. of S^T over half of the
-// columns (w / 4), then heads w, w + 8 of the softmax, then columns 64 w .. of
-// O^T.  Work is dealt as in the paged forward (block ranges, fwd_kernel.cuh):
-// the units' lists laid end to end and cut into one equal range per CTA; the
-// CTA that writes a cut unit's last piece merges its pieces.
+// A warp takes 16 rows of a block: it copies their slots (cp.async, its own
+// part of the ring), scores them, writes P to shared memory, and after one
+// barrier a block takes 512 / W columns of O^T over all of the block's rows.
+// Work is dealt as in the paged forward (block ranges, fwd_kernel.cuh): the
+// units' lists laid end to end and cut into one equal range per CTA; a second
+// kernel merges the pieces of cut units.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -46,11 +46,7 @@
 
 namespace smla {
 
-constexpr int kF4Threads = 256;
-constexpr int kF4Stages = 3;
-constexpr int kF4StageBytes = kBlk * kFp4Slot;
-constexpr int kF4SRow = kBlk + 4;    // floats of one head's partial scores (the 4 spread the banks)
-constexpr int kF4PRow = kBlk + 16;   // f16 values of one head's P
+constexpr int kF4TileBytes = 16 * kFp4Slot;   // one warp's 16 rows
 
 struct Fp4Params {
   const __nv_bfloat16* q;      // [n_tok, h_q, 576]
@@ -62,31 +58,40 @@ struct Fp4Params {
   float* lse;                  // [n_tok, h_q]
   float* part_o;               // [2 ctas, part_rows, 512]
   float* part_lse;             // [2 ctas, part_rows]
-  int32_t* merge_count;        // [units], zeroed before the launch
   int n_tok, h_q, topk, s_next, page_size, max_blocks, num_blocks;
   int groups;                  // head groups of a token
-  int nb;                      // 64-entry blocks of a list
+  int nb;                      // blocks of a list (Fp4Layout::kRows entries each)
   int ctas, part_rows;
   float scale_log2;            // sm_scale * log2(e)
   float kv_scale;
 };
 
-template <int NT>   // heads / 8 of a group
+// NT: heads / 8 of a unit; W: warps of a CTA (a block is 16 rows per warp);
+// S: blocks in the ring.
+template <int NT, int W, int S>
 struct Fp4Layout {
   static constexpr int kHeads = 8 * NT;
-  static constexpr int kQOff = kF4Stages * kF4StageBytes;
-  static constexpr int kQBytes = 18 * NT * 512;   // 16 latent + 2 rope fragments of 32 lanes x 16 bytes
-  static constexpr int kSOff = kQOff + kQBytes;
-  static constexpr int kPOff = kSOff + 2 * kHeads * kF4SRow * 4;
-  static constexpr int kMiscOff = kPOff + kHeads * kF4PRow * 2;
-  static constexpr int kBytes = kMiscOff + 4 * kHeads * 4 + kF4Stages * kBlk * 4 + 64 * 4;
+  static constexpr int kThreads = 32 * W;
+  static constexpr int kRows = 16 * W;
+  static constexpr int kStage = W * kF4TileBytes;
+  static constexpr int kPRow = kRows + 16;            // f16 values of one head's P (the 16 spread the banks)
+  static constexpr int kQOff = S * kStage;
+  static constexpr int kPOff = kQOff + 18 * NT * 512; // Q: 16 latent + 2 rope fragments of 32 lanes x 16 bytes
+  static constexpr int kRedOff = kPOff + 2 * kHeads * kPRow * 2;
+  static constexpr int kMiscOff = kRedOff + W * kHeads * 4;
+  static constexpr int kBytes = kMiscOff + kHeads * 4 + 2 * W * 4;
 };
 
-// A row of the list, prepared ahead of its copy: the list entry, then its
-// page-table entry, then the slot.
-struct Fp4Cursor {
-  int unit, j;   // unit and block of the list
+template <int NT_, int W_, int S_, int kPerSm_>
+struct Fp4Shape {
+  static constexpr int NT = NT_, W = W_, S = S_, kPerSm = kPerSm_;
+  using Layout = Fp4Layout<NT, W, S>;
+  static_assert((Layout::kBytes + 1024) * kPerSm <= 233472, "shared memory of an SM");
 };
+using Fp4Shape8 = Fp4Shape<1, 4, 2, 3>;
+using Fp4Shape16 = Fp4Shape<2, 4, 3, 2>;
+using Fp4Shape32 = Fp4Shape<4, 4, 2, 2>;
+using Fp4Shape64 = Fp4Shape<8, 8, 2, 1>;
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -111,29 +116,28 @@ __device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t v) {
   return h;
 }
 
-// S^T: this warp's 16 rows over its half of the columns.  The MMA's row g is
-// row rho(g) = g with bits 0 and 1 swapped, so that the two rows a quarter of
-// a warp reads together lie 832 bytes apart: their 16-byte reads fall into
+// S^T of this warp's 16 rows, times 2^-e (f4_load_q).  The MMA's row g is row
+// rho(g) = g with bits 0 and 1 swapped, so that the two rows a quarter of a
+// warp reads together lie 832 bytes apart: their 16-byte reads fall into
 // different banks (416-byte rows step by 8 of 32 banks).  Lane (g, c) owns
-// codes 128 c .. 128 c + 127 of its rows, the four 32-code chunks taken in
-// an order rotated by c for the same reason; Q's fragments are laid out to
-// match (f4_load_q).
+// codes 128 c .. 128 c + 127 of rows rho(g) and rho(g) + 8, the four 32-code
+// chunks taken in an order rotated by c for the same reason; Q's fragments are
+// laid out to match (f4_load_q).  Two chains of sums per head tile keep
+// dependent MMAs apart.
 template <int NT>
-__device__ __forceinline__ void f4_scores(const uint8_t* stage, const uint4* qf, float* s_out, int warp, int lane,
+__device__ __forceinline__ void f4_scores(const uint8_t* tile, const uint4* qf, float (&acc)[NT][4], int lane,
                                           float kv_scale) {
   const int g = lane >> 2, c = lane & 3;
-  const int mt = warp & 3, kh = warp >> 2;
   const int rho = (g & 4) | ((g & 1) << 1) | ((g >> 1) & 1);
-  const uint8_t* row0 = stage + (16 * mt + rho) * kFp4Slot;
+  const uint8_t* row0 = tile + rho * kFp4Slot;
   const uint8_t* row1 = row0 + 8 * kFp4Slot;
-  float acc[NT][4];
+  float alt[NT][4];
 #pragma unroll
   for (int n = 0; n < NT; ++n)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
+    for (int i = 0; i < 4; ++i) acc[n][i] = alt[n][i] = 0.f;
 #pragma unroll
-  for (int it = 0; it < 2; ++it) {
-    const int i0 = 2 * kh + it;
+  for (int i0 = 0; i0 < 4; ++i0) {
     const int chunk = 4 * c + ((i0 + c) & 3);   // 32 codes: 16 bytes, two scales
     const uint4 w0 = *reinterpret_cast<const uint4*>(row0 + 16 * chunk);
     const uint4 w1 = *reinterpret_cast<const uint4*>(row1 + 16 * chunk);
@@ -159,86 +163,101 @@ __device__ __forceinline__ void f4_scores(const uint8_t* stage, const uint4* qf,
       for (int n = 0; n < NT; ++n) {
         const uint4 b = qf[((i0 * 4 + j) * NT + n) * 32 + lane];
         mma_f16(acc[n], fa, b.x, b.y);
-        mma_f16(acc[n], fb, b.z, b.w);
+        mma_f16(alt[n], fb, b.z, b.w);
       }
     }
   }
   // the rotated part (bf16), after the latent part took kv_scale
-  const int piece = 2 * c + ((kh + (c >> 1)) & 1);
-  const uint4 r0 = *reinterpret_cast<const uint4*>(row0 + kFp4RopeAt + 16 * piece);
-  const uint4 r1 = *reinterpret_cast<const uint4*>(row1 + kFp4RopeAt + 16 * piece);
-  const uint32_t fa[4] = {r0.x, r1.x, r0.y, r1.y};
-  const uint32_t fb[4] = {r0.z, r1.z, r0.w, r1.w};
 #pragma unroll
-  for (int n = 0; n < NT; ++n) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) acc[n][i] *= kv_scale;
-    const uint4 b = qf[((16 + kh) * NT + n) * 32 + lane];
-    mma_bf16(acc[n], fa, b.x, b.y);
-    mma_bf16(acc[n], fb, b.z, b.w);
-  }
-  float* dst = s_out + kh * (8 * NT * kF4SRow) + 16 * mt + rho;
-#pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    float* d = dst + (8 * n + 2 * c) * kF4SRow;
-    d[0] = acc[n][0];
-    d[kF4SRow] = acc[n][1];
-    d[8] = acc[n][2];
-    d[kF4SRow + 8] = acc[n][3];
-  }
-}
-
-// O^T: columns 64 warp .. 64 warp + 63 over the block's 64 rows.  The MMA's
-// K slots 2c, 2c + 1, 2c + 8, 2c + 9 are rows c, c + 4, c + 8, c + 12 of a
-// 16-row tile: the four lanes' reads of one row each then fall into different
-// banks.  Lane (g, c) widens columns 8 g .. 8 g + 7 of the warp's 64 (half a
-// scale group): MMA tile t takes columns 8 g + 2 t (its row g) and 8 g + 2 t + 1
-// (its row g + 8).  P of a head is stored in the order of the slots.
-template <int NT>
-__device__ __forceinline__ void f4_values(const uint8_t* stage, const __half* pf, float (&o)[4][NT][4], int warp,
-                                          int lane) {
-  const int g = lane >> 2, c = lane & 3;
-  const uint8_t* base = stage + c * kFp4Slot;
-  const int code_at = 32 * warp + 4 * g, scale_at = kFp4ScaleAt + 4 * warp + (g >> 1);
-#pragma unroll
-  for (int kt = 0; kt < 4; ++kt) {
-    const uint8_t* r = base + 16 * kt * kFp4Slot;
-    uint32_t w[4], s[4];
+  for (int n = 0; n < NT; ++n)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      w[i] = *reinterpret_cast<const uint32_t*>(r + 4 * i * kFp4Slot + code_at);
+      acc[n][i] = (acc[n][i] + alt[n][i]) * kv_scale;
+      alt[n][i] = 0.f;
+    }
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int piece = 2 * c + ((k + (c >> 1)) & 1);
+    const uint4 r0 = *reinterpret_cast<const uint4*>(row0 + kFp4RopeAt + 16 * piece);
+    const uint4 r1 = *reinterpret_cast<const uint4*>(row1 + kFp4RopeAt + 16 * piece);
+    const uint32_t fa[4] = {r0.x, r1.x, r0.y, r1.y};
+    const uint32_t fb[4] = {r0.z, r1.z, r0.w, r1.w};
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const uint4 b = qf[((16 + k) * NT + n) * 32 + lane];
+      mma_bf16(acc[n], fa, b.x, b.y);
+      mma_bf16(alt[n], fb, b.z, b.w);
+    }
+  }
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[n][i] += alt[n][i];
+}
+
+// O^T: this warp's 512 / W columns over the block's rows.  The MMA's K slots
+// 2c, 2c + 1, 2c + 8, 2c + 9 are rows c, c + 4, c + 8, c + 12 of a 16-row tile:
+// the four lanes' reads of one row each then fall into different banks.  Lane
+// (g, c) widens 64 / W neighbouring columns (all in one scale group): MMA tile
+// 4 j + t takes columns 8 j + 2 t (its row g) and 8 j + 2 t + 1 (its row g + 8) of
+// the lane's.  P of a head is stored in the order of the slots.
+template <int NT, int W>
+__device__ __forceinline__ void f4_values(const uint8_t* stage, const __half* pf, const uint32_t* livew,
+                                          float (&o)[32 / W][NT][4], int warp, int lane) {
+  constexpr int kWords = 8 / W;             // 8 codes each, per row
+  constexpr int kPRow = 16 * W + 16;
+  const int g = lane >> 2, c = lane & 3;
+  const uint8_t* base = stage + c * kFp4Slot;
+  const int code_at = (256 / W) * warp + (32 / W) * g;
+  const int scale_at = kFp4ScaleAt + (code_at >> 3);
+#pragma unroll
+  for (int kt = 0; kt < W; ++kt) {
+    if (livew[kt] == 0u) continue;          // no valid row in the tile
+    const uint8_t* r = base + kt * kF4TileBytes;
+    uint32_t w[4][kWords], s[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (kWords == 2) {
+        const uint2 v = *reinterpret_cast<const uint2*>(r + 4 * i * kFp4Slot + code_at);
+        w[i][0] = v.x;
+        w[i][1] = v.y;
+      } else {
+        w[i][0] = *reinterpret_cast<const uint32_t*>(r + 4 * i * kFp4Slot + code_at);
+      }
       s[i] = r[4 * i * kFp4Slot + scale_at];
     }
     uint2 b[NT];
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
-      b[n] = *reinterpret_cast<const uint2*>(pf + (8 * n + g) * kF4PRow + 16 * kt + 4 * c);
+    for (int n = 0; n < NT; ++n) b[n] = *reinterpret_cast<const uint2*>(pf + (8 * n + g) * kPRow + 16 * kt + 4 * c);
     const uint32_t f0 = e4m3x2_f16x2(s[0] | (s[1] << 8)), f1 = e4m3x2_f16x2(s[2] | (s[3] << 8));
-    // byte t: the codes of column 2t (even) or 2t + 1 (odd) of two rows
-    uint32_t e0[4], o0[4], e1[4], o1[4];
-    e2m1x8_value((w[0] & 0x0f0f0f0fu) | ((w[1] << 4) & 0xf0f0f0f0u), e0);
-    e2m1x8_value(((w[0] >> 4) & 0x0f0f0f0fu) | (w[1] & 0xf0f0f0f0u), o0);
-    e2m1x8_value((w[2] & 0x0f0f0f0fu) | ((w[3] << 4) & 0xf0f0f0f0u), e1);
-    e2m1x8_value(((w[2] >> 4) & 0x0f0f0f0fu) | (w[3] & 0xf0f0f0f0u), o1);
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      const uint32_t a[4] = {mul_f16x2(e0[t], f0), mul_f16x2(o0[t], f0), mul_f16x2(e1[t], f1), mul_f16x2(o1[t], f1)};
+    for (int j = 0; j < kWords; ++j) {
+      // byte t: the codes of column 2t (even) or 2t + 1 (odd) of two rows
+      uint32_t e0[4], o0[4], e1[4], o1[4];
+      e2m1x8_value((w[0][j] & 0x0f0f0f0fu) | ((w[1][j] << 4) & 0xf0f0f0f0u), e0);
+      e2m1x8_value(((w[0][j] >> 4) & 0x0f0f0f0fu) | (w[1][j] & 0xf0f0f0f0u), o0);
+      e2m1x8_value((w[2][j] & 0x0f0f0f0fu) | ((w[3][j] << 4) & 0xf0f0f0f0u), e1);
+      e2m1x8_value(((w[2][j] >> 4) & 0x0f0f0f0fu) | (w[3][j] & 0xf0f0f0f0u), o1);
 #pragma unroll
-      for (int n = 0; n < NT; ++n) mma_f16(o[t][n], a, b[n].x, b[n].y);
+      for (int t = 0; t < 4; ++t) {
+        const uint32_t a[4] = {mul_f16x2(e0[t], f0), mul_f16x2(o0[t], f0), mul_f16x2(e1[t], f1), mul_f16x2(o1[t], f1)};
+#pragma unroll
+        for (int n = 0; n < NT; ++n) mma_f16(o[4 * j + t][n], a, b[n].x, b[n].y);
+      }
     }
   }
 }
 
-// Q of a unit: warp w brings heads w, w + 8 .. to f16 / bf16 by 2^-e (the
+// Q of a unit: warp w brings heads w, w + W .. to f16 / bf16 by 2^-e (the
 // exponent of the head's largest value) and stores them as MMA fragments;
 // qscale[h] = sm_scale log2(e) 2^e.  Heads past h_q are zero.
-template <int NT>
+template <int NT, int W>
 __device__ __forceinline__ void f4_load_q(const Fp4Params& p, int unit, uint8_t* qbytes, float* qscale, int warp,
                                           int lane) {
   const int tok = unit / p.groups, h0 = (unit % p.groups) * (8 * NT);
-#pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    const int h = h0 + 8 * n + warp;
+#pragma unroll 2
+  for (int hl = warp; hl < 8 * NT; hl += W) {
+    const int h = h0 + hl, n = hl >> 3, g = hl & 7;
     const bool live = h < p.h_q;
     const uint4* src = reinterpret_cast<const uint4*>(p.q + (static_cast<size_t>(tok) * p.h_q + (live ? h : 0)) * kRowW);
     uint4 v[3];
@@ -261,7 +280,7 @@ __device__ __forceinline__ void f4_load_q(const Fp4Params& p, int unit, uint8_t*
     int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;
     e = top > 0.f && top <= 3.402823466e38f ? min(max(e, -126), 126) : 0;
     const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-    if (lane == 0) qscale[8 * n + warp] = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+    if (lane == 0) qscale[hl] = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
     // values 8 x .. 8 x + 7 (x = lane or 32 + lane) are word j of chunk i of
     // owner c; the owner's iteration i0 has (i0 + c) % 4 = i
 #pragma unroll
@@ -274,7 +293,7 @@ __device__ __forceinline__ void f4_load_q(const Fp4Params& p, int unit, uint8_t*
         const __half2 t = __floats2half2_rn(x[k][2 * y] * down, x[k][2 * y + 1] * down);
         h2[y] = *reinterpret_cast<const uint32_t*>(&t);
       }
-      *reinterpret_cast<uint4*>(qbytes + (((i0 * 4 + j) * NT + n) * 32 + 4 * warp + c) * 16) =
+      *reinterpret_cast<uint4*>(qbytes + (((i0 * 4 + j) * NT + n) * 32 + 4 * g + c) * 16) =
           make_uint4(h2[0], h2[1], h2[2], h2[3]);
     }
     if (lane < 8) {   // rotated part: piece `lane` belongs to owner c = lane / 2, half kh with (kh + c / 2) % 2 = lane % 2
@@ -282,221 +301,298 @@ __device__ __forceinline__ void f4_load_q(const Fp4Params& p, int unit, uint8_t*
       float y[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) y[i] = x[2][i] * down;
-      *reinterpret_cast<uint4*>(qbytes + (((16 + kh) * NT + n) * 32 + 4 * warp + c) * 16) = pack8(y);
+      *reinterpret_cast<uint4*>(qbytes + (((16 + kh) * NT + n) * 32 + 4 * g + c) * 16) = pack8(y);
     }
   }
 }
 
-// The pieces of a cut unit merged, as merge_unit in fwd_kernel.cuh:
-// LSE = ln sum exp(LSE_s), out = sum exp(LSE_s - LSE) O_s, in piece order.
-// 16 threads per head row.
-__device__ __forceinline__ void f4_merge(const Fp4Params& p, int unit, int h0, int heads, int c_first, int pieces) {
+// The pieces of the cut units merged: LSE = ln sum exp(LSE_s), out = sum
+// exp(LSE_s - LSE) O_s, in piece order (at most 64 pieces).  A warp takes half of a
+// head row: lanes form the pieces' weights, then every lane adds 8 of the 256
+// columns, the pieces' reads independent of one another.  Launched as a
+// dependent of the decode, so that it is set up while that runs; it reads only
+// after the decode has completed.
+__global__ void __launch_bounds__(256) fp4_merge_kernel(const __grid_constant__ Fp4Params p, int heads_per_unit) {
+  const int lane = static_cast<int>(lane_id());
+  const long long item = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  const long long row = item >> 1;   // (token, head)
+  const int half = static_cast<int>(item & 1);
   const long long total = static_cast<long long>(p.n_tok) * p.groups * p.nb;
-  const long long ub = static_cast<long long>(unit) * p.nb;
-  const int tok = unit / p.groups;
-  const int c16 = static_cast<int>(threadIdx.x) & 15;
-  for (int h = static_cast<int>(threadIdx.x) >> 4; h < heads; h += kF4Threads / 16) {
-    float m = -INFINITY, l = 0.f;
-    float4 acc[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
-    for (int i = 0; i < pieces; ++i) {
-      const int cta = c_first + i;
-      const size_t slot = 2 * static_cast<size_t>(cta) + (range_start(cta, total, p.ctas) < ub ? 1 : 0);
-      const float ls = __ldcg(p.part_lse + slot * p.part_rows + h);
-      const float4* src = reinterpret_cast<const float4*>(p.part_o + (slot * p.part_rows + h) * kDv) + c16;
-      float4 v[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] = __ldcg(src + 16 * k);
-      if (ls == -INFINITY) continue;
-      const float mn = fmaxf(m, ls);
-      const float a = expf(m - mn), w = expf(ls - mn);
-      l = l * a + w;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        acc[k].x = acc[k].x * a + w * v[k].x;
-        acc[k].y = acc[k].y * a + w * v[k].y;
-        acc[k].z = acc[k].z * a + w * v[k].z;
-        acc[k].w = acc[k].w * a + w * v[k].w;
-      }
-      m = mn;
-    }
-    const size_t row = static_cast<size_t>(tok) * p.h_q + h0 + h;
-    const float inv = m == -INFINITY ? 0.f : 1.f / l;
-    if (c16 == 0) p.lse[row] = m == -INFINITY ? -INFINITY : m + logf(l);
-    uint2* o = reinterpret_cast<uint2*>(p.out + row * kDv) + c16;
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-      o[16 * k] = make_uint2(pack_bf16x2(acc[k].x * inv, acc[k].y * inv), pack_bf16x2(acc[k].z * inv, acc[k].w * inv));
+  int pieces = 1, c_first = 0, h = 0;
+  long long ub = 0;
+  if (row < static_cast<long long>(p.n_tok) * p.h_q) {
+    const int tok = static_cast<int>(row / p.h_q), hq = static_cast<int>(row - static_cast<long long>(tok) * p.h_q);
+    const long long unit = static_cast<long long>(tok) * p.groups + hq / heads_per_unit;
+    h = hq % heads_per_unit;
+    ub = unit * p.nb;
+    c_first = range_cta(ub, total, p.ctas);
+    pieces = range_cta(ub + p.nb - 1, total, p.ctas) - c_first + 1;
   }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (pieces == 1) return;   // one CTA ran the whole unit
+  int slot[2];
+  float w[2];
+  float m = -INFINITY;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    slot[k] = 0;
+    w[k] = -INFINITY;
+    const int i = lane + 32 * k;
+    if (i < pieces) {
+      const int cta = c_first + i;
+      slot[k] = 2 * cta + (range_start(cta, total, p.ctas) < ub ? 1 : 0);
+      w[k] = __ldcg(p.part_lse + static_cast<size_t>(slot[k]) * p.part_rows + h);
+    }
+    m = fmaxf(m, w[k]);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+#pragma unroll
+  for (int k = 0; k < 2; ++k) w[k] = w[k] == -INFINITY ? 0.f : expf(w[k] - m);
+  const float l = warp_sum(w[0] + w[1]);
+  if (half == 0 && lane == 0) p.lse[row] = l == 0.f ? -INFINITY : m + logf(l);
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  float4 a0 = make_float4(0.f, 0.f, 0.f, 0.f), a1 = a0;
+#pragma unroll 8
+  for (int i = 0; i < pieces; ++i) {
+    const int sl = __shfl_sync(0xffffffffu, i < 32 ? slot[0] : slot[1], i & 31);
+    const float wi = __shfl_sync(0xffffffffu, i < 32 ? w[0] : w[1], i & 31) * inv;
+    const float4* src = reinterpret_cast<const float4*>(p.part_o + (static_cast<size_t>(sl) * p.part_rows + h) * kDv + 256 * half) + lane;
+    const float4 v0 = __ldcg(src), v1 = __ldcg(src + 32);
+    a0.x += wi * v0.x;
+    a0.y += wi * v0.y;
+    a0.z += wi * v0.z;
+    a0.w += wi * v0.w;
+    a1.x += wi * v1.x;
+    a1.y += wi * v1.y;
+    a1.z += wi * v1.z;
+    a1.w += wi * v1.w;
+  }
+  uint2* o = reinterpret_cast<uint2*>(p.out + row * kDv + 256 * half) + lane;
+  o[0] = make_uint2(pack_bf16x2(a0.x, a0.y), pack_bf16x2(a0.z, a0.w));
+  o[32] = make_uint2(pack_bf16x2(a1.x, a1.y), pack_bf16x2(a1.z, a1.w));
 }
 
-template <int NT>
-__global__ void __launch_bounds__(kF4Threads, 2) fp4_decode_kernel(const __grid_constant__ Fp4Params p) {
-  using L = Fp4Layout<NT>;
+template <int NT, int W, int S, int kCtas>
+__global__ void __launch_bounds__(32 * W, kCtas) fp4_decode_kernel(const __grid_constant__ Fp4Params p) {
+  using L = Fp4Layout<NT, W, S>;
   extern __shared__ __align__(128) uint8_t f4_smem[];
   uint8_t* qbytes = f4_smem + L::kQOff;
-  float* s_part = reinterpret_cast<float*>(f4_smem + L::kSOff);
-  __half* pf = reinterpret_cast<__half*>(f4_smem + L::kPOff);
-  float* alpha = reinterpret_cast<float*>(f4_smem + L::kMiscOff);   // [heads] rescale of O
-  float* qscale = alpha + L::kHeads;
-  float* fin = qscale + L::kHeads;                                  // [heads] 1 / l
-  float* lse_s = fin + L::kHeads;
-  int* valid = reinterpret_cast<int*>(lse_s + L::kHeads);           // [stages][64]
-  int* flag = valid + kF4Stages * kBlk;
+  __half* pf = reinterpret_cast<__half*>(f4_smem + L::kPOff);         // [2][heads][kPRow]
+  float* red = reinterpret_cast<float*>(f4_smem + L::kRedOff);        // [W][heads]
+  float* qscale = reinterpret_cast<float*>(f4_smem + L::kMiscOff);    // [heads]
+  uint32_t* livew = reinterpret_cast<uint32_t*>(qscale + L::kHeads);  // [2][W] validity of a warp's rows
   const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5, lane = tid & 31;
+  const int g = lane >> 2, c = lane & 3;
+  asm volatile("griddepcontrol.launch_dependents;");   // the merge may be set up (it waits for this grid's end)
 
   const long long total = static_cast<long long>(p.n_tok) * p.groups * p.nb;
   const long long x0 = range_start(static_cast<int>(blockIdx.x), total, p.ctas);
   const int n_blocks = static_cast<int>(range_start(static_cast<int>(blockIdx.x) + 1, total, p.ctas) - x0);
   const int unit0 = static_cast<int>(x0 / p.nb), j0 = static_cast<int>(x0 % p.nb);
 
-  // Gather: four threads per row.  The list entry of block b + 4, the
-  // page-table entry of block b + 3 and the copy of block b + 2 go out
-  // together, so none waits for the one before it.
-  const int grow = tid >> 2, part = tid & 3;
-  Fp4Cursor ci = {unit0, j0};   // next list entry to read
-  int n_read = 0;
-  int tok_t = 0, idx_t = -1;    // token and entry whose page is looked up next
-  int tok_n = 0, idx_n = -1;
+  // The gather of this warp's rows goes by pairs of blocks: lane 16 k + r
+  // follows row r of block 2 i + k from its list entry (read two pairs ahead)
+  // over its page-table entry (one pair ahead) to its slot, so that no step
+  // waits for the one before it.
+  int eu = unit0, ej = j0 + (lane >> 4), eb = lane >> 4;   // unit, block of the list and block of the CTA
+  if (ej >= p.nb) {
+    ej -= p.nb;
+    ++eu;
+  }
+  int req_n = 0, len_n = 0, idx_n = -1, idx_p = -1, page_p = -1, slot_n = -1;
   auto read_entry = [&]() {
     idx_n = -1;
-    if (n_read < n_blocks) {
-      tok_n = ci.unit / p.groups;
-      const int e = ci.j * kBlk + grow;
-      if (e < p.topk) idx_n = __ldg(p.indices + static_cast<size_t>(tok_n) * p.topk + e);
-      if (++ci.j == p.nb) {
-        ci.j = 0;
-        ++ci.unit;
+    if (eb < n_blocks) {
+      const int tok = eu / p.groups;
+      req_n = tok / p.s_next;
+      len_n = __ldg(p.seqlens + req_n);
+      const int e = ej * L::kRows + 16 * warp + (lane & 15);
+      if (e < p.topk) idx_n = __ldg(p.indices + static_cast<size_t>(tok) * p.topk + e);
+    }
+    eb += 2;
+    ej += 2;
+    while (ej >= p.nb) {   // lists of one block: two units on
+      ej -= p.nb;
+      ++eu;
+    }
+  };
+  auto look_up = [&]() {
+    idx_p = idx_n;
+    page_p = -1;
+    if (idx_n >= 0 && idx_n < len_n) {
+      const int pg = idx_n / p.page_size;
+      if (pg < p.max_blocks) page_p = __ldg(p.block_table + static_cast<size_t>(req_n) * p.max_blocks + pg);
+    }
+  };
+  auto resolve = [&]() {
+    slot_n = page_p >= 0 && page_p < p.num_blocks ? page_p * p.page_size + idx_p % p.page_size : -1;
+  };
+  // Copies of this warp's 16 rows of a block (row r's slot is held by lane
+  // 16 half + r), eight lanes a row; masked rows are zeros and are not read.
+  // Returns the rows' validity.
+  auto copy = [&](int slots, int half, int st) -> uint32_t {
+    const uint32_t rows = (__ballot_sync(0xffffffffu, slots >= 0) >> (16 * half)) & 0xffffu;
+    if (rows != 0u) {
+      const uint32_t dst = smem_u32(f4_smem + st * L::kStage + warp * kF4TileBytes);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int r = 4 * q + (lane >> 3), ch = lane & 7;
+        const int sl = __shfl_sync(0xffffffffu, slots, 16 * half + r);
+        const uint8_t* src = p.cache + static_cast<size_t>(sl < 0 ? 0 : sl) * kFp4Slot + 16 * ch;
+        const uint32_t bytes = sl < 0 ? 0u : 16u, d = dst + r * kFp4Slot + 16 * ch;
+        cp_async_16(d, src, bytes);
+        cp_async_16(d + 128, src + 128, bytes);
+        cp_async_16(d + 256, src + 256, bytes);
+        if (ch < 2) cp_async_16(d + 384, src + 384, bytes);
       }
     }
-    ++n_read;
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    return rows;
   };
-  int page = -1, idx_p = -1;    // page-table entry read, and its list entry
-  auto look_up = [&]() {        // list entry (idx_t) -> its page
-    page = -1;
-    idx_p = idx_t;
-    if (idx_t >= 0) {
-      const int b = tok_t / p.s_next;
-      const int pg = idx_t / p.page_size;
-      if (idx_t < __ldg(p.seqlens + b) && pg < p.max_blocks)
-        page = __ldg(p.block_table + static_cast<size_t>(b) * p.max_blocks + pg);
-    }
-  };
-  auto copy = [&](int b) {      // block b of this CTA into its ring slot
-    const int st = b % kF4Stages;
-    const bool ok = page >= 0 && page < p.num_blocks;
-    const int row = ok ? page * p.page_size + idx_p % p.page_size : 0;
-    const uint8_t* src = p.cache + static_cast<size_t>(row) * kFp4Slot;
-    const uint32_t dst = smem_u32(f4_smem + st * kF4StageBytes + grow * kFp4Slot);
-    const uint32_t bytes = ok ? 16u : 0u;   // masked rows are zeros and are not read
-#pragma unroll
-    for (int k = 0; k < 7; ++k)
-      if (k < 6 || part < 2) cp_async_16(dst + 16 * (part + 4 * k), src + 16 * (part + 4 * k), bytes);
-    if (part == 0) valid[st * kBlk + grow] = ok ? 1 : 0;
-    return ok;
-  };
-  auto advance = [&]() {
-    tok_t = tok_n;
-    idx_t = idx_n;
-  };
-  bool ok0, ok1;   // validity of this thread's row in blocks b and b + 1
+  int slots_a, slots_b;       // the current pair's slots, the next pair's
+  uint32_t live0, live1 = 0;  // validity of this warp's rows in block b and (S = 3) b + 1
   read_entry();
-  advance();
-  read_entry();
+  f4_load_q<NT, W>(p, unit0, qbytes, qscale, warp, lane);   // while the first entries are on their way
   look_up();
-  ok0 = copy(0);
-  asm volatile("cp.async.commit_group;" ::: "memory");
-  advance();
   read_entry();
+  resolve();
+  slots_a = slot_n;
   look_up();
-  ok1 = copy(1);
-  asm volatile("cp.async.commit_group;" ::: "memory");
-  advance();
   read_entry();
+  live0 = copy(slots_a, 0, 0);
+  if constexpr (S == 3) live1 = copy(slots_a, 1, 1);
+  resolve();
+  slots_b = slot_n;
   look_up();
+  read_entry();
 
-  float o[4][NT][4];
-  float m_run[NT], l_run[NT];   // this warp's heads (warp, warp + 8, ..)
-  bool any = false;             // a valid row was met in this unit
+  float o[32 / W][NT][4];
+  float m[NT][2], l[NT][2], f[NT][2];   // heads 8 n + 2 c + k: maximum (of the CTA), this lane's share of the sum
   int unit = unit0, j = j0;
+  int st = 0;   // ring slot of block b
+#pragma unroll 1
   for (int b = 0; b < n_blocks; ++b) {
-    if (b == 0 || j == 0) {     // a new unit
-      if (b > 0) __syncthreads();   // qscale and the fragments of the last unit have been read
-      f4_load_q<NT>(p, unit, qbytes, qscale, warp, lane);
+    if (b == 0 || j == 0) {   // a new unit
+      if (b > 0) {
+        __syncthreads();   // the last unit's Q has been read
+        f4_load_q<NT, W>(p, unit, qbytes, qscale, warp, lane);
+      }
+      __syncthreads();
 #pragma unroll
-      for (int t = 0; t < 4; ++t)
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          m[n][k] = -INFINITY;
+          l[n][k] = 0.f;
+          f[n][k] = qscale[8 * n + 2 * c + k];
+        }
+#pragma unroll
+      for (int t = 0; t < 32 / W; ++t)
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int i = 0; i < 4; ++i) o[t][n][i] = 0.f;
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        m_run[n] = -INFINITY;
-        l_run[n] = 0.f;
-      }
-      any = false;
     }
-    asm volatile("cp.async.wait_group 1;" ::: "memory");
-    // block b has landed for every thread, and block b - 1 has been read
-    const bool live = __syncthreads_or(ok0) != 0;
-    ok0 = ok1;
-    ok1 = copy(b + 2);
-    asm volatile("cp.async.commit_group;" ::: "memory");
-    advance();
-    read_entry();
-    look_up();
-    const uint8_t* stage = f4_smem + (b % kF4Stages) * kF4StageBytes;
-    if (live) {
-      any = true;
-      f4_scores<NT>(stage, reinterpret_cast<const uint4*>(qbytes), s_part, warp, lane, p.kv_scale);
-      __syncthreads();
-      // Softmax of heads warp, warp + 8, ..: lane l has rows l and l + 32.
-      const int* vrow = valid + (b % kF4Stages) * kBlk;
-      const bool v0 = vrow[lane] != 0, v1 = vrow[lane + 32] != 0;
+    asm volatile("cp.async.wait_group %0;" ::"n"(S - 2) : "memory");
+    __syncwarp();   // this warp's rows of block b have landed
+    const uint8_t* stage = f4_smem + st * L::kStage;
+    __half* pb = pf + (b & 1) * L::kHeads * L::kPRow;
+    uint32_t* lw = livew + (b & 1) * W;
+    float s[NT][4];
+    const uint32_t mask = live0;
+    const int rho = (g & 4) | ((g & 1) << 1) | ((g >> 1) & 1);
+    const bool v0 = (mask >> rho) & 1u, v1 = (mask >> (rho + 8)) & 1u;
+    if (mask != 0u) f4_scores<NT>(stage + warp * kF4TileBytes, reinterpret_cast<const uint4*>(qbytes), s, lane, p.kv_scale);
+    // Scores in log2 units; a maximum moves only when a score passes it by
+    // 2^8 (P stays far inside f16's range), always with a unit's first rows.
+    bool need = false;
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const int h = 8 * n + warp;
-        const float* sa = s_part + h * kF4SRow;
-        const float* sb = sa + L::kHeads * kF4SRow;
-        const float f = qscale[h];
-        const float s0 = v0 ? (sa[lane] + sb[lane]) * f : -INFINITY;
-        const float s1 = v1 ? (sa[lane + 32] + sb[lane + 32]) * f : -INFINITY;
-        float top = fmaxf(s0, s1);
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int k = 16; k > 0; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
-        const float mn = fmaxf(m_run[n], top);
-        const float ms = mn == -INFINITY ? 0.f : mn;
-        const float a = fast_exp2(m_run[n] - ms);
-        const float e0 = fast_exp2(s0 - ms), e1 = fast_exp2(s1 - ms);
-        m_run[n] = mn;
-        l_run[n] = l_run[n] * a + (e0 + e1);
-        // row r of a 16-row tile sits at 4 (r % 4) + r / 4
-        const int at = (lane & 16) + 4 * (lane & 3) + ((lane >> 2) & 3);
-        pf[h * kF4PRow + at] = __float2half_rn(e0);
-        pf[h * kF4PRow + 32 + at] = __float2half_rn(e1);
-        if (lane == 0) alpha[h] = a;
+      for (int i = 0; i < 4; ++i) {
+        s[n][i] = (i < 2 ? v0 : v1) ? s[n][i] * f[n][i & 1] : -INFINITY;
+        need |= s[n][i] > m[n][i & 1] + 8.0f;
       }
-      __syncthreads();
-      const int c = lane & 3;
+    // P of row r of this warp's tile sits at 16 warp + 4 (r % 4) + r / 4
+    const int at = 16 * warp + 4 * (rho & 3) + (rho >> 2);
+    float e[NT][4];
+    auto weights = [&]() {
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const float a0 = alpha[8 * n + 2 * c], a1 = alpha[8 * n + 2 * c + 1];
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          o[t][n][0] *= a0;
-          o[t][n][1] *= a1;
-          o[t][n][2] *= a0;
-          o[t][n][3] *= a1;
+        for (int k = 0; k < 2; ++k) {
+          const float ms = m[n][k] == -INFINITY ? 0.f : m[n][k];
+          e[n][k] = fast_exp2(s[n][k] - ms);
+          e[n][2 + k] = fast_exp2(s[n][2 + k] - ms);
+          __half* d = pb + (8 * n + 2 * c + k) * L::kPRow + at;
+          d[0] = __float2half_rn(e[n][k]);
+          d[2] = __float2half_rn(e[n][2 + k]);
         }
-      }
-      f4_values<NT>(stage, pf, o, warp, lane);
+    };
+    weights();
+    if (lane == 0) lw[warp] = mask;
+    // Every warp's P and rows are there, and block b - 1 has been read.
+    if (__syncthreads_or(need)) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          float top = fmaxf(s[n][k], s[n][2 + k]);
+#pragma unroll
+          for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+          if (g == 0) red[warp * L::kHeads + 8 * n + 2 * c + k] = top;
+        }
+      __syncthreads();
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          float mn = m[n][k];
+#pragma unroll
+          for (int w = 0; w < W; ++w) mn = fmaxf(mn, red[w * L::kHeads + 8 * n + 2 * c + k]);
+          const float a = m[n][k] == mn ? 1.f : fast_exp2(m[n][k] - mn);
+          m[n][k] = mn;
+          l[n][k] *= a;
+#pragma unroll
+          for (int t = 0; t < 32 / W; ++t) {
+            o[t][n][k] *= a;
+            o[t][n][2 + k] *= a;
+          }
+        }
+      weights();
+      __syncthreads();
     }
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) l[n][k] += e[n][k] + e[n][2 + k];
+    // Block b + S - 1 goes where block b - 1 was.
+    const int back = st == 0 ? S - 1 : st - 1;
+    if constexpr (S == 3) {
+      live0 = live1;
+      live1 = copy(slots_b, b & 1, back);
+    } else {
+      live0 = (b & 1) == 0 ? copy(slots_a, 1, back) : copy(slots_b, 0, back);
+    }
+    if ((b & 1) == 1) {
+      slots_a = slots_b;
+      resolve();
+      slots_b = slot_n;
+      look_up();
+      read_entry();
+    }
+    st = st == S - 1 ? 0 : st + 1;
+    if (b + 1 < n_blocks && j == p.nb - 1) {   // the next unit's Q on its way into L2
+      const int tok = (unit + 1) / p.groups, h0 = ((unit + 1) % p.groups) * L::kHeads;
+      const char* q0 = reinterpret_cast<const char*>(p.q + (static_cast<size_t>(tok) * p.h_q + h0) * kRowW);
+      const int bytes = min(L::kHeads, p.h_q - h0) * 2 * kRowW;
+      for (int x = 128 * tid; x < bytes; x += 128 * 32 * W) prefetch_line_l2(q0 + x);
+    }
+    f4_values<NT, W>(stage, pb, lw, o, warp, lane);
     ++j;
     if (j == p.nb || b == n_blocks - 1) {
       // End of the unit, or of this CTA's piece of it.
-      const int je = j;
       const int tok = unit / p.groups, h0 = (unit % p.groups) * L::kHeads;
       const int heads = min(L::kHeads, p.h_q - h0);
       const long long ub = static_cast<long long>(unit) * p.nb;
@@ -504,59 +600,52 @@ __global__ void __launch_bounds__(kF4Threads, 2) fp4_decode_kernel(const __grid_
       const int pieces = range_cta(ub + p.nb - 1, total, p.ctas) - c_first + 1;
       const bool whole = pieces == 1;
       const size_t slot = 2 * static_cast<size_t>(blockIdx.x) + (x0 < ub ? 1 : 0);
+      // sums over this warp's rows, then over the warps
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const int h = 8 * n + warp;
-        const float l = warp_sum(l_run[n]);
-        if (lane == 0) {
-          const bool some = any && l != 0.f;
-          const float v = some ? (m_run[n] + log2f(l)) * 0.69314718055994530942f : -INFINITY;
-          fin[h] = some ? p.kv_scale / l : 0.f;
-          if (h < heads) {
-            if (whole) p.lse[static_cast<size_t>(tok) * p.h_q + h0 + h] = v;
-            else p.part_lse[slot * p.part_rows + h] = v;
-          }
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          float v = l[n][k];
+#pragma unroll
+          for (int x = 4; x < 32; x <<= 1) v += __shfl_xor_sync(0xffffffffu, v, x);
+          if (g == 0) red[warp * L::kHeads + 8 * n + 2 * c + k] = v;
         }
-      }
       __syncthreads();
-      const int g = lane >> 2, c = lane & 3;
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           const int h = 8 * n + 2 * c + k;
-          if (h < heads) {
-            const float f = fin[h];
-            float y[8];
+          float sum = 0.f;
 #pragma unroll
-            for (int t = 0; t < 4; ++t) {
-              y[2 * t] = f == 0.f ? 0.f : o[t][n][k] * f;
-              y[2 * t + 1] = f == 0.f ? 0.f : o[t][n][k + 2] * f;
+          for (int w = 0; w < W; ++w) sum += red[w * L::kHeads + h];
+          const float inv = sum == 0.f ? 0.f : p.kv_scale / sum;
+          if (h < heads) {
+            if (warp == 0 && g == 0) {
+              const float v = sum == 0.f ? -INFINITY : (m[n][k] + log2f(sum)) * 0.69314718055994530942f;
+              if (whole) p.lse[static_cast<size_t>(tok) * p.h_q + h0 + h] = v;
+              else p.part_lse[slot * p.part_rows + h] = v;
             }
-            const int col = 64 * warp + 8 * g;
-            if (whole) {
-              *reinterpret_cast<uint4*>(p.out + (static_cast<size_t>(tok) * p.h_q + h0 + h) * kDv + col) = pack8(y);
-            } else {
-              float4* d = reinterpret_cast<float4*>(p.part_o + (slot * p.part_rows + h) * kDv + col);
-              d[0] = make_float4(y[0], y[1], y[2], y[3]);
-              d[1] = make_float4(y[4], y[5], y[6], y[7]);
+#pragma unroll
+            for (int q = 0; q < 8 / W; ++q) {
+              float y[8];
+#pragma unroll
+              for (int t = 0; t < 4; ++t) {
+                y[2 * t] = sum == 0.f ? 0.f : o[4 * q + t][n][k] * inv;
+                y[2 * t + 1] = sum == 0.f ? 0.f : o[4 * q + t][n][2 + k] * inv;
+              }
+              const int col = (512 / W) * warp + (64 / W) * g + 8 * q;
+              if (whole) {
+                *reinterpret_cast<uint4*>(p.out + (static_cast<size_t>(tok) * p.h_q + h0 + h) * kDv + col) = pack8(y);
+              } else {
+                float4* d = reinterpret_cast<float4*>(p.part_o + (slot * p.part_rows + h) * kDv + col);
+                d[0] = make_float4(y[0], y[1], y[2], y[3]);
+                d[1] = make_float4(y[4], y[5], y[6], y[7]);
+              }
             }
           }
         }
-      if (!whole) {
-        // One thread counts the piece with a release add after the barrier
-        // that orders every thread's writes before it; the CTA that completes
-        // the unit acquires the others' and merges.
-        __syncthreads();
-        if (tid == 0) {
-          const int last = atomic_add_release_gpu(p.merge_count + unit, 1) + 1 == pieces;
-          if (last) fence_acquire_gpu();
-          *flag = last;
-        }
-        __syncthreads();
-        if (*flag) f4_merge(p, unit, h0, heads, c_first, pieces);
-      }
-      if (je == p.nb) {
+      if (j == p.nb) {
         j = 0;
         ++unit;
       }

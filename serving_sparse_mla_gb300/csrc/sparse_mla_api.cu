@@ -41,6 +41,12 @@ DeviceState g_dev[kMaxDevices];
 constexpr int kTopkStageCap = 49152;
 constexpr int kTopkMaxSmem = smla::kTopkBins * 4 + kTopkStageCap * 4;
 
+template <class C>
+cudaError_t f4_attributes() {
+  return cudaFuncSetAttribute(smla::fp4_decode_kernel<C::NT, C::W, C::S, C::kPerSm>,
+                              cudaFuncAttributeMaxDynamicSharedMemorySize, C::Layout::kBytes);
+}
+
 sparse_mla_status_t device_setup(int* sm_count) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return SPARSE_MLA_ERR_CUDA;
@@ -80,10 +86,8 @@ sparse_mla_status_t device_setup(int* sm_count) {
                              smla::idx_smem_bytes()) != cudaSuccess ||
         cudaFuncSetAttribute(smla::dsa_scores_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              smla::idx_smem_bytes()) != cudaSuccess ||
-        cudaFuncSetAttribute(smla::fp4_decode_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             smla::Fp4Layout<1>::kBytes) != cudaSuccess ||
-        cudaFuncSetAttribute(smla::fp4_decode_kernel<2>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             smla::Fp4Layout<2>::kBytes) != cudaSuccess ||
+        f4_attributes<smla::Fp4Shape8>() != cudaSuccess || f4_attributes<smla::Fp4Shape16>() != cudaSuccess ||
+        f4_attributes<smla::Fp4Shape32>() != cudaSuccess || f4_attributes<smla::Fp4Shape64>() != cudaSuccess ||
         cudaFuncSetAttribute(smla::dsa_topk_kernel<256>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              kTopkMaxSmem) != cudaSuccess ||
         cudaFuncSetAttribute(smla::dsa_topk_kernel<1024>, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -491,35 +495,62 @@ sparse_mla_status_t sparse_mla_decode_fp8(const void* q, const void* kv_cache, c
 
 namespace {
 
-// Heads of a unit: 8 or 16 (more heads are several units of 16).
-int f4_heads(int h_q) { return h_q <= 8 ? 8 : 16; }
-
-// The grid: two CTAs per SM, or fewer where the lists are short (a unit is
-// cut into at most 32 pieces, as decode_ctas).
-int f4_ctas(long long n_tok, int h_q, int topk, int sms) {
-  const int nb = blocks_per_list(topk);
-  const int groups = (h_q + f4_heads(h_q) - 1) / f4_heads(h_q);
-  const long long min_blocks = (nb + 30) / 31;
-  const long long g = n_tok * groups * nb / min_blocks;
-  return static_cast<int>(g > 2 * sms ? 2 * sms : (g < 1 ? 1 : g));
+// The kernel's shape for a number of heads: the smallest of 8, 16, 32 and 64
+// that holds them (more heads are several units of 64).
+template <class F>
+auto f4_pick(int h_q, F&& f) {
+  if (h_q <= 8) return f(smla::Fp4Shape8());
+  if (h_q <= 16) return f(smla::Fp4Shape16());
+  if (h_q <= 32) return f(smla::Fp4Shape32());
+  return f(smla::Fp4Shape64());
 }
 
 struct F4Plan {
-  int ctas, groups, rows;
-  size_t lse_at, count_at, bytes;   // bytes from the workspace's start; bytes 0: no workspace
+  int ctas, groups, rows, nb;
+  size_t lse_at, bytes;   // bytes from the workspace's start; bytes 0: no unit is cut
 };
 
-F4Plan f4_plan(long long n_tok, int h_q, int topk, int sms) {
+// The grid: as many CTAs as the card holds at once, or fewer where the lists
+// are short (a range has at least nb / 62 blocks, so a unit at most 64 pieces).
+template <class C>
+F4Plan f4_plan_of(long long n_tok, int h_q, int topk, int sms) {
   F4Plan f;
-  const int H = f4_heads(h_q);
+  constexpr int H = C::Layout::kHeads;
   f.groups = (h_q + H - 1) / H;
   f.rows = h_q < H ? h_q : H;
-  f.ctas = f4_ctas(n_tok, h_q, topk, sms);
+  f.nb = (topk + C::Layout::kRows - 1) / C::Layout::kRows;
+  const long long most = static_cast<long long>(sms) * C::kPerSm;
+  const long long g = n_tok * f.groups * f.nb / ((f.nb + 61) / 62);
+  f.ctas = static_cast<int>(g > most ? most : (g < 1 ? 1 : g));
   const size_t slots = 2 * static_cast<size_t>(f.ctas) * static_cast<size_t>(f.rows);
   f.lse_at = slots * smla::kDv * sizeof(float);
-  f.count_at = (f.lse_at + slots * sizeof(float) + 15) & ~size_t(15);
-  f.bytes = f.ctas > 1 ? f.count_at + static_cast<size_t>(n_tok) * f.groups * sizeof(int32_t) : 0;
+  const long long total = n_tok * f.groups * f.nb;
+  const bool whole = total % f.ctas == 0 && total / f.ctas % f.nb == 0;   // every range is whole units
+  f.bytes = whole ? 0 : f.lse_at + slots * sizeof(float);
   return f;
+}
+
+F4Plan f4_plan(long long n_tok, int h_q, int topk, int sms) {
+  return f4_pick(h_q, [&](auto shape) { return f4_plan_of<decltype(shape)>(n_tok, h_q, topk, sms); });
+}
+
+template <class C>
+cudaError_t f4_launch(const smla::Fp4Params& p, cudaStream_t cs) {
+  smla::fp4_decode_kernel<C::NT, C::W, C::S, C::kPerSm>
+      <<<p.ctas, C::Layout::kThreads, C::Layout::kBytes, cs>>>(p);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || p.part_o == nullptr) return e;
+  // two warps a row, eight a CTA; set up while the decode runs
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((static_cast<long long>(p.n_tok) * p.h_q + 3) / 4));
+  cfg.blockDim = dim3(256);
+  cfg.stream = cs;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, smla::fp4_merge_kernel, p, C::Layout::kHeads);
 }
 
 }  // namespace
@@ -548,7 +579,8 @@ sparse_mla_status_t sparse_mla_decode_fp4(const void* q, const void* kv_cache, c
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   if (num_blocks == 0 || max_blocks == 0) return launch_fill(out, lse, n_tok * h_q, cs);
   const F4Plan f = f4_plan(n_tok, h_q, topk, sms);
-  if (n_tok * f.groups > INT_MAX) return SPARSE_MLA_ERR_INVALID_ARG;   // units are counted in 32 bits
+  // units and rows are counted in 32 bits
+  if (n_tok * f.groups > INT_MAX || n_tok * h_q > INT_MAX) return SPARSE_MLA_ERR_INVALID_ARG;
   if (f.bytes > 0 && (workspace_bytes < f.bytes || !workspace)) return SPARSE_MLA_ERR_WORKSPACE_TOO_SMALL;
   if (f.bytes > 0 && !aligned(workspace, 16)) return SPARSE_MLA_ERR_INVALID_ARG;
   smla::Fp4Params p;
@@ -568,7 +600,7 @@ sparse_mla_status_t sparse_mla_decode_fp4(const void* q, const void* kv_cache, c
   p.max_blocks = max_blocks;
   p.num_blocks = num_blocks;
   p.groups = f.groups;
-  p.nb = blocks_per_list(topk);
+  p.nb = f.nb;
   p.ctas = f.ctas;
   p.part_rows = f.rows;
   p.scale_log2 = sm_scale * 1.4426950408889634f;
@@ -577,15 +609,9 @@ sparse_mla_status_t sparse_mla_decode_fp4(const void* q, const void* kv_cache, c
     unsigned char* ws = static_cast<unsigned char*>(workspace);
     p.part_o = reinterpret_cast<float*>(ws);
     p.part_lse = reinterpret_cast<float*>(ws + f.lse_at);
-    p.merge_count = reinterpret_cast<int32_t*>(ws + f.count_at);
-    if (cudaMemsetAsync(p.merge_count, 0, static_cast<size_t>(n_tok) * f.groups * sizeof(int32_t), cs) != cudaSuccess)
-      return SPARSE_MLA_ERR_CUDA;
   }
-  if (f4_heads(h_q) == 8)
-    smla::fp4_decode_kernel<1><<<p.ctas, smla::kF4Threads, smla::Fp4Layout<1>::kBytes, cs>>>(p);
-  else
-    smla::fp4_decode_kernel<2><<<p.ctas, smla::kF4Threads, smla::Fp4Layout<2>::kBytes, cs>>>(p);
-  return cudaGetLastError() == cudaSuccess ? SPARSE_MLA_OK : SPARSE_MLA_ERR_CUDA;
+  const cudaError_t e = f4_pick(h_q, [&](auto shape) { return f4_launch<decltype(shape)>(p, cs); });
+  return e == cudaSuccess ? SPARSE_MLA_OK : SPARSE_MLA_ERR_CUDA;
 }
 
 }  // extern "C"
