@@ -66,32 +66,31 @@ struct Fp4Params {
   float kv_scale;
 };
 
-// NT: heads / 8 of a unit; W: warps of a CTA (a block is 16 rows per warp);
-// S: blocks in the ring.
-template <int NT, int W, int S>
-struct Fp4Layout {
+// A CTA's shape: 8 NT heads; blocks are 16 rows for each of W
+// warps, two blocks in the ring.  kPad spreads P's rows over the banks.
+template <int NT_, int W_, int kPerSm_, int kPad_>
+struct Fp4Shape {
+  static constexpr int NT = NT_, W = W_, kPerSm = kPerSm_;
   static constexpr int kHeads = 8 * NT;
   static constexpr int kThreads = 32 * W;
   static constexpr int kRows = 16 * W;
   static constexpr int kStage = W * kF4TileBytes;
-  static constexpr int kPRow = kRows + 16;            // f16 values of one head's P (the 16 spread the banks)
-  static constexpr int kQOff = S * kStage;
-  static constexpr int kPOff = kQOff + 18 * NT * 512; // Q: 16 latent + 2 rope fragments of 32 lanes x 16 bytes
+  static constexpr int kPRow = kRows + kPad_;            // f16 values of one head's P
+  static constexpr int kQOff = 2 * kStage;
+  static constexpr int kPOff = kQOff + 18 * NT * 512;    // Q: 16 latent + 2 rope fragments of 32 lanes x 16 bytes
   static constexpr int kRedOff = kPOff + 2 * kHeads * kPRow * 2;
   static constexpr int kMiscOff = kRedOff + W * kHeads * 4;
   static constexpr int kBytes = kMiscOff + kHeads * 4 + 2 * W * 4;
+  static_assert(W == 4 || W == 8, "64 / W columns of O^T per lane, in one scale group");
+  static_assert((kBytes + 1024) * kPerSm <= 233472, "shared memory of an SM");
 };
-
-template <int NT_, int W_, int S_, int kPerSm_>
-struct Fp4Shape {
-  static constexpr int NT = NT_, W = W_, S = S_, kPerSm = kPerSm_;
-  using Layout = Fp4Layout<NT, W, S>;
-  static_assert((Layout::kBytes + 1024) * kPerSm <= 233472, "shared memory of an SM");
-};
-using Fp4Shape8 = Fp4Shape<1, 4, 2, 3>;
-using Fp4Shape16 = Fp4Shape<2, 4, 3, 2>;
-using Fp4Shape32 = Fp4Shape<4, 4, 2, 2>;
-using Fp4Shape64 = Fp4Shape<8, 8, 2, 1>;
+// 8 and 16 heads: three CTAs of four warps per SM; at 16 P's rows keep an 8-value
+// pad (two-way bank conflicts on its few reads), which is what makes three fit.
+// 32 heads: one CTA of eight warps, half of the sums per thread (84.7 us at 128
+// lists of 2048 against 92.8 us for two CTAs of four warps, which spill).
+using Fp4Shape8 = Fp4Shape<1, 4, 3, 16>;
+using Fp4Shape16 = Fp4Shape<2, 4, 3, 8>;
+using Fp4Shape32 = Fp4Shape<4, 8, 1, 16>;
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -201,11 +200,10 @@ __device__ __forceinline__ void f4_scores(const uint8_t* tile, const uint4* qf, 
 // (g, c) widens 64 / W neighbouring columns (all in one scale group): MMA tile
 // 4 j + t takes columns 8 j + 2 t (its row g) and 8 j + 2 t + 1 (its row g + 8) of
 // the lane's.  P of a head is stored in the order of the slots.
-template <int NT, int W>
+template <int NT, int W, int kPRow>
 __device__ __forceinline__ void f4_values(const uint8_t* stage, const __half* pf, const uint32_t* livew,
                                           float (&o)[32 / W][NT][4], int warp, int lane) {
   constexpr int kWords = 8 / W;             // 8 codes each, per row
-  constexpr int kPRow = 16 * W + 16;
   const int g = lane >> 2, c = lane & 3;
   const uint8_t* base = stage + c * kFp4Slot;
   const int code_at = (256 / W) * warp + (32 / W) * g;
@@ -248,7 +246,7 @@ __device__ __forceinline__ void f4_values(const uint8_t* stage, const __half* pf
   }
 }
 
-// Q of a unit: warp w brings heads w, w + W .. to f16 / bf16 by 2^-e (the
+// Q of a unit: a warp brings every W-th head to f16 / bf16 by 2^-e (the
 // exponent of the head's largest value) and stores them as MMA fragments;
 // qscale[h] = sm_scale log2(e) 2^e.  Heads past h_q are zero.
 template <int NT, int W>
@@ -373,9 +371,9 @@ __global__ void __launch_bounds__(256) fp4_merge_kernel(const __grid_constant__ 
   o[32] = make_uint2(pack_bf16x2(a1.x, a1.y), pack_bf16x2(a1.z, a1.w));
 }
 
-template <int NT, int W, int S, int kCtas>
-__global__ void __launch_bounds__(32 * W, kCtas) fp4_decode_kernel(const __grid_constant__ Fp4Params p) {
-  using L = Fp4Layout<NT, W, S>;
+template <class L>
+__global__ void __launch_bounds__(L::kThreads, L::kPerSm) fp4_decode_kernel(const __grid_constant__ Fp4Params p) {
+  constexpr int NT = L::NT, W = L::W;
   extern __shared__ __align__(128) uint8_t f4_smem[];
   uint8_t* qbytes = f4_smem + L::kQOff;
   __half* pf = reinterpret_cast<__half*>(f4_smem + L::kPOff);         // [2][heads][kPRow]
@@ -432,8 +430,8 @@ __global__ void __launch_bounds__(32 * W, kCtas) fp4_decode_kernel(const __grid_
   // 16 half + r), eight lanes a row; masked rows are zeros and are not read.
   // Returns the rows' validity.
   auto copy = [&](int slots, int half, int st) -> uint32_t {
-    const uint32_t rows = (__ballot_sync(0xffffffffu, slots >= 0) >> (16 * half)) & 0xffffu;
-    if (rows != 0u) {
+    const uint32_t valid = (__ballot_sync(0xffffffffu, slots >= 0) >> (16 * half)) & 0xffffu;
+    if (valid != 0u) {
       const uint32_t dst = smem_u32(f4_smem + st * L::kStage + warp * kF4TileBytes);
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
@@ -448,10 +446,9 @@ __global__ void __launch_bounds__(32 * W, kCtas) fp4_decode_kernel(const __grid_
       }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
-    return rows;
+    return valid;
   };
-  int slots_a, slots_b;       // the current pair's slots, the next pair's
-  uint32_t live0, live1 = 0;  // validity of this warp's rows in block b and (S = 3) b + 1
+  int slots_a, slots_b;   // the current pair's slots, the next pair's
   read_entry();
   f4_load_q<NT, W>(p, unit0, qbytes, qscale, warp, lane);   // while the first entries are on their way
   look_up();
@@ -460,8 +457,7 @@ __global__ void __launch_bounds__(32 * W, kCtas) fp4_decode_kernel(const __grid_
   slots_a = slot_n;
   look_up();
   read_entry();
-  live0 = copy(slots_a, 0, 0);
-  if constexpr (S == 3) live1 = copy(slots_a, 1, 1);
+  uint32_t rows = copy(slots_a, 0, 0);   // validity of this warp's rows in block b
   resolve();
   slots_b = slot_n;
   look_up();
@@ -470,7 +466,6 @@ __global__ void __launch_bounds__(32 * W, kCtas) fp4_decode_kernel(const __grid_
   float o[32 / W][NT][4];
   float m[NT][2], l[NT][2], f[NT][2];   // heads 8 n + 2 c + k: maximum (of the CTA), this lane's share of the sum
   int unit = unit0, j = j0;
-  int st = 0;   // ring slot of block b
 #pragma unroll 1
   for (int b = 0; b < n_blocks; ++b) {
     if (b == 0 || j == 0) {   // a new unit
@@ -494,13 +489,14 @@ __global__ void __launch_bounds__(32 * W, kCtas) fp4_decode_kernel(const __grid_
 #pragma unroll
           for (int i = 0; i < 4; ++i) o[t][n][i] = 0.f;
     }
-    asm volatile("cp.async.wait_group %0;" ::"n"(S - 2) : "memory");
-    __syncwarp();   // this warp's rows of block b have landed
-    const uint8_t* stage = f4_smem + st * L::kStage;
-    __half* pb = pf + (b & 1) * L::kHeads * L::kPRow;
     uint32_t* lw = livew + (b & 1) * W;
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    if (lane == 0) lw[warp] = rows;
+    __syncwarp();   // this warp's rows of block b have landed
+    const uint8_t* stage = f4_smem + (b & 1) * L::kStage;
+    __half* pb = pf + (b & 1) * L::kHeads * L::kPRow;
     float s[NT][4];
-    const uint32_t mask = live0;
+    const uint32_t mask = rows;
     const int rho = (g & 4) | ((g & 1) << 1) | ((g >> 1) & 1);
     const bool v0 = (mask >> rho) & 1u, v1 = (mask >> (rho + 8)) & 1u;
     if (mask != 0u) f4_scores<NT>(stage + warp * kF4TileBytes, reinterpret_cast<const uint4*>(qbytes), s, lane, p.kv_scale);
@@ -531,7 +527,6 @@ __global__ void __launch_bounds__(32 * W, kCtas) fp4_decode_kernel(const __grid_
         }
     };
     weights();
-    if (lane == 0) lw[warp] = mask;
     // Every warp's P and rows are there, and block b - 1 has been read.
     if (__syncthreads_or(need)) {
 #pragma unroll
@@ -567,29 +562,24 @@ __global__ void __launch_bounds__(32 * W, kCtas) fp4_decode_kernel(const __grid_
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int k = 0; k < 2; ++k) l[n][k] += e[n][k] + e[n][2 + k];
-    // Block b + S - 1 goes where block b - 1 was.
-    const int back = st == 0 ? S - 1 : st - 1;
-    if constexpr (S == 3) {
-      live0 = live1;
-      live1 = copy(slots_b, b & 1, back);
+    // Block b + 1 goes where block b - 1 was.
+    if ((b & 1) == 0) {
+      rows = copy(slots_a, 1, 1);
     } else {
-      live0 = (b & 1) == 0 ? copy(slots_a, 1, back) : copy(slots_b, 0, back);
-    }
-    if ((b & 1) == 1) {
+      rows = copy(slots_b, 0, 0);
       slots_a = slots_b;
       resolve();
       slots_b = slot_n;
       look_up();
       read_entry();
     }
-    st = st == S - 1 ? 0 : st + 1;
     if (b + 1 < n_blocks && j == p.nb - 1) {   // the next unit's Q on its way into L2
       const int tok = (unit + 1) / p.groups, h0 = ((unit + 1) % p.groups) * L::kHeads;
       const char* q0 = reinterpret_cast<const char*>(p.q + (static_cast<size_t>(tok) * p.h_q + h0) * kRowW);
       const int bytes = min(L::kHeads, p.h_q - h0) * 2 * kRowW;
-      for (int x = 128 * tid; x < bytes; x += 128 * 32 * W) prefetch_line_l2(q0 + x);
+      for (int x = 128 * tid; x < bytes; x += 128 * L::kThreads) prefetch_line_l2(q0 + x);
     }
-    f4_values<NT, W>(stage, pb, lw, o, warp, lane);
+    f4_values<NT, W, L::kPRow>(stage, pb, lw, o, warp, lane);
     ++j;
     if (j == p.nb || b == n_blocks - 1) {
       // End of the unit, or of this CTA's piece of it.

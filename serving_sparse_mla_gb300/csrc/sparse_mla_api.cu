@@ -43,8 +43,7 @@ constexpr int kTopkMaxSmem = smla::kTopkBins * 4 + kTopkStageCap * 4;
 
 template <class C>
 cudaError_t f4_attributes() {
-  return cudaFuncSetAttribute(smla::fp4_decode_kernel<C::NT, C::W, C::S, C::kPerSm>,
-                              cudaFuncAttributeMaxDynamicSharedMemorySize, C::Layout::kBytes);
+  return cudaFuncSetAttribute(smla::fp4_decode_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kBytes);
 }
 
 sparse_mla_status_t device_setup(int* sm_count) {
@@ -87,7 +86,7 @@ sparse_mla_status_t device_setup(int* sm_count) {
         cudaFuncSetAttribute(smla::dsa_scores_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              smla::idx_smem_bytes()) != cudaSuccess ||
         f4_attributes<smla::Fp4Shape8>() != cudaSuccess || f4_attributes<smla::Fp4Shape16>() != cudaSuccess ||
-        f4_attributes<smla::Fp4Shape32>() != cudaSuccess || f4_attributes<smla::Fp4Shape64>() != cudaSuccess ||
+        f4_attributes<smla::Fp4Shape32>() != cudaSuccess ||
         cudaFuncSetAttribute(smla::dsa_topk_kernel<256>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              kTopkMaxSmem) != cudaSuccess ||
         cudaFuncSetAttribute(smla::dsa_topk_kernel<1024>, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -495,14 +494,13 @@ sparse_mla_status_t sparse_mla_decode_fp8(const void* q, const void* kv_cache, c
 
 namespace {
 
-// The kernel's shape for a number of heads: the smallest of 8, 16, 32 and 64
-// that holds them (more heads are several units of 64).
+// The kernel's shape for a number of heads: the smallest of 8, 16 and 32 that
+// holds them (more heads are several units of 32).
 template <class F>
 auto f4_pick(int h_q, F&& f) {
   if (h_q <= 8) return f(smla::Fp4Shape8());
   if (h_q <= 16) return f(smla::Fp4Shape16());
-  if (h_q <= 32) return f(smla::Fp4Shape32());
-  return f(smla::Fp4Shape64());
+  return f(smla::Fp4Shape32());
 }
 
 struct F4Plan {
@@ -515,10 +513,10 @@ struct F4Plan {
 template <class C>
 F4Plan f4_plan_of(long long n_tok, int h_q, int topk, int sms) {
   F4Plan f;
-  constexpr int H = C::Layout::kHeads;
+  constexpr int H = C::kHeads;
   f.groups = (h_q + H - 1) / H;
   f.rows = h_q < H ? h_q : H;
-  f.nb = (topk + C::Layout::kRows - 1) / C::Layout::kRows;
+  f.nb = (topk + C::kRows - 1) / C::kRows;
   const long long most = static_cast<long long>(sms) * C::kPerSm;
   const long long g = n_tok * f.groups * f.nb / ((f.nb + 61) / 62);
   f.ctas = static_cast<int>(g > most ? most : (g < 1 ? 1 : g));
@@ -536,8 +534,7 @@ F4Plan f4_plan(long long n_tok, int h_q, int topk, int sms) {
 
 template <class C>
 cudaError_t f4_launch(const smla::Fp4Params& p, cudaStream_t cs) {
-  smla::fp4_decode_kernel<C::NT, C::W, C::S, C::kPerSm>
-      <<<p.ctas, C::Layout::kThreads, C::Layout::kBytes, cs>>>(p);
+  smla::fp4_decode_kernel<C><<<p.ctas, C::kThreads, C::kBytes, cs>>>(p);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || p.part_o == nullptr) return e;
   // two warps a row, eight a CTA; set up while the decode runs
@@ -550,7 +547,7 @@ cudaError_t f4_launch(const smla::Fp4Params& p, cudaStream_t cs) {
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, smla::fp4_merge_kernel, p, C::Layout::kHeads);
+  return cudaLaunchKernelEx(&cfg, smla::fp4_merge_kernel, p, C::kHeads);
 }
 
 }  // namespace
