@@ -255,13 +255,33 @@ __device__ __forceinline__ void store_fp4(uint8_t* slot, bool keep, int half, in
 
 // ------------------------------------------------------------------ forward
 
+// A row as this lane holds it: 8 values of either latent half, one pair of the
+// rotated part, and where the row belongs.
+struct NormRow {
+  uint4 v0, v1;
+  uint32_t vr;
+  int t, h, pos;
+};
+
+__device__ __forceinline__ NormRow load_row(const NormParams& p, long long r, int lane) {
+  NormRow x;
+  x.t = static_cast<int>(r / (p.h_q + 1));
+  x.h = static_cast<int>(r - static_cast<long long>(x.t) * (p.h_q + 1));
+  const __nv_bfloat16* row = x.h == p.h_q ? p.kv + static_cast<long long>(x.t) * p.kv_tok
+                                          : p.q + static_cast<long long>(x.t) * p.q_tok + static_cast<long long>(x.h) * p.q_head;
+  x.v0 = *reinterpret_cast<const uint4*>(row + 8 * lane);
+  x.v1 = *reinterpret_cast<const uint4*>(row + 256 + 8 * lane);
+  x.vr = *reinterpret_cast<const uint32_t*>(row + kLatW + 2 * lane);
+  x.pos = __ldg(p.positions + x.t);
+  return x;
+}
+
 // The latent row of token t: norm carried in two floats, rotation, kv_out and
 // the slot.
-__device__ __forceinline__ void norm_kv_row(const NormParams& p, int t, int pos, int lane) {
-  const __nv_bfloat16* row = p.kv + static_cast<long long>(t) * p.kv_tok;
-  const uint4 v0 = *reinterpret_cast<const uint4*>(row + 8 * lane);
-  const uint4 v1 = *reinterpret_cast<const uint4*>(row + 256 + 8 * lane);
-  const uint32_t vr = *reinterpret_cast<const uint32_t*>(row + kLatW + 2 * lane);
+__device__ __forceinline__ void norm_kv_row(const NormParams& p, const NormRow& x, int lane) {
+  const int t = x.t, pos = x.pos;
+  const uint4 v0 = x.v0, v1 = x.v1;
+  const uint32_t vr = x.vr;
   float y[16];
   unpack8(v0, y);
   unpack8(v1, y + 8);
@@ -312,11 +332,10 @@ __device__ __forceinline__ void norm_kv_row(const NormParams& p, int t, int pos,
   }
 }
 
-__device__ __forceinline__ void norm_q_row(const NormParams& p, int t, int h, int pos, int lane) {
-  const __nv_bfloat16* row = p.q + static_cast<long long>(t) * p.q_tok + static_cast<long long>(h) * p.q_head;
-  uint4 v0 = *reinterpret_cast<const uint4*>(row + 8 * lane);
-  uint4 v1 = *reinterpret_cast<const uint4*>(row + 256 + 8 * lane);
-  const uint32_t vr = *reinterpret_cast<const uint32_t*>(row + kLatW + 2 * lane);
+__device__ __forceinline__ void norm_q_row(const NormParams& p, const NormRow& x, int lane) {
+  const int t = x.t, h = x.h, pos = x.pos;
+  uint4 v0 = x.v0, v1 = x.v1;
+  const uint32_t vr = x.vr;
   if (p.q_weight != nullptr) {
     float y[16], w[16];
     unpack8(v0, y);
@@ -340,32 +359,59 @@ __device__ __forceinline__ void norm_q_row(const NormParams& p, int t, int h, in
   *reinterpret_cast<uint32_t*>(o + kLatW + 2 * lane) = pack_bf16x2(rr.x, rr.y);
 }
 
-// Rows t (h_q + 1) + h; h = h_q is the latent row.
+// Rows t (h_q + 1) + h; h = h_q is the latent row.  A warp reads its next row
+// before it works on the one it has.
 __global__ void __launch_bounds__(kNormWarps * 32) norm_rope_kernel(const __grid_constant__ NormParams p) {
   const int lane = static_cast<int>(lane_id());
   const long long rows = static_cast<long long>(p.n_tok) * (p.h_q + 1);
   const long long step = static_cast<long long>(gridDim.x) * kNormWarps;
-  for (long long r = static_cast<long long>(blockIdx.x) * kNormWarps + (threadIdx.x >> 5); r < rows; r += step) {
-    const int t = static_cast<int>(r / (p.h_q + 1));
-    const int h = static_cast<int>(r - static_cast<long long>(t) * (p.h_q + 1));
-    const int pos = __ldg(p.positions + t);
-    if (pos < 0 || pos >= p.n_pos) continue;   // a padding row: nothing of it is written
-    if (h == p.h_q) norm_kv_row(p, t, pos, lane);
-    else norm_q_row(p, t, h, pos, lane);
+  long long r = static_cast<long long>(blockIdx.x) * kNormWarps + (threadIdx.x >> 5);
+  if (r >= rows) return;
+  NormRow next = load_row(p, r, lane);
+  for (; r < rows; r += step) {
+    const NormRow x = next;
+    if (r + step < rows) next = load_row(p, r + step, lane);
+    if (x.pos < 0 || x.pos >= p.n_pos) continue;   // a padding row: nothing of it is written
+    if (x.h == p.h_q) norm_kv_row(p, x, lane);
+    else norm_q_row(p, x, lane);
   }
 }
 
 // ------------------------------------------------------------------ backward
+
+// A row of the backward as this lane holds it: 16 latent gradients, the pair of
+// the rotated part and (normed rows) the 16 latent values.
+struct GradRow {
+  float4 g[4];
+  float2 gr;
+  uint4 x0, x1;
+  int pos;
+};
+
+template <bool kNorm>
+__device__ __forceinline__ GradRow load_grad_row(const __nv_bfloat16* x, const float* dy, const int32_t* pos,
+                                                 int lane) {
+  GradRow v;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    v.g[i] = __ldg(reinterpret_cast<const float4*>(dy + 256 * (i >> 1) + 8 * lane + 4 * (i & 1)));
+  v.gr = __ldg(reinterpret_cast<const float2*>(dy + kLatW + 2 * lane));
+  if constexpr (kNorm) {
+    v.x0 = __ldg(reinterpret_cast<const uint4*>(x + 8 * lane));
+    v.x1 = __ldg(reinterpret_cast<const uint4*>(x + 256 + 8 * lane));
+  }
+  v.pos = __ldg(pos);
+  return v;
+}
 
 // With g = w dy and xhat = a r, r = rsqrt(mean a^2 + eps):
 //   da = r (g - xhat mean(g xhat)),  dw = sum over rows of dy xhat,
 // and the rotated part turns back.  One row per warp; acc keeps this warp's
 // rows' shares of dw.
 template <bool kNorm>
-__device__ __forceinline__ void grad_row(const NormParams& p, const __nv_bfloat16* x, const float* dy,
-                                         __nv_bfloat16* dx, const __nv_bfloat16* weight, int pos, int lane,
-                                         float (&acc)[16]) {
-  if (pos < 0 || pos >= p.n_pos) {   // a padding row takes no part in the output
+__device__ __forceinline__ void grad_row(const NormParams& p, const GradRow& v, __nv_bfloat16* dx,
+                                         const __nv_bfloat16* weight, int lane, float (&acc)[16]) {
+  if (v.pos < 0 || v.pos >= p.n_pos) {   // a padding row takes no part in the output
     const uint4 z = make_uint4(0, 0, 0, 0);
     *reinterpret_cast<uint4*>(dx + 8 * lane) = z;
     *reinterpret_cast<uint4*>(dx + 256 + 8 * lane) = z;
@@ -375,17 +421,15 @@ __device__ __forceinline__ void grad_row(const NormParams& p, const __nv_bfloat1
   float g[16];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float4 v = __ldg(reinterpret_cast<const float4*>(dy + 256 * (i >> 1) + 8 * lane + 4 * (i & 1)));
-    g[4 * i] = v.x;
-    g[4 * i + 1] = v.y;
-    g[4 * i + 2] = v.z;
-    g[4 * i + 3] = v.w;
+    g[4 * i] = v.g[i].x;
+    g[4 * i + 1] = v.g[i].y;
+    g[4 * i + 2] = v.g[i].z;
+    g[4 * i + 3] = v.g[i].w;
   }
-  const float2 gr = __ldg(reinterpret_cast<const float2*>(dy + kLatW + 2 * lane));
   if constexpr (kNorm) {
     float a[16], w[16];
-    unpack8(__ldg(reinterpret_cast<const uint4*>(x + 8 * lane)), a);
-    unpack8(__ldg(reinterpret_cast<const uint4*>(x + 256 + 8 * lane)), a + 8);
+    unpack8(v.x0, a);
+    unpack8(v.x1, a + 8);
     unpack8(__ldg(reinterpret_cast<const uint4*>(weight + 8 * lane)), w);
     unpack8(__ldg(reinterpret_cast<const uint4*>(weight + 256 + 8 * lane)), w + 8);
     float ss = 0.f, dot = 0.f;
@@ -409,7 +453,7 @@ __device__ __forceinline__ void grad_row(const NormParams& p, const __nv_bfloat1
   }
   *reinterpret_cast<uint4*>(dx + 8 * lane) = pack8(g);
   *reinterpret_cast<uint4*>(dx + 256 + 8 * lane) = pack8(g + 8);
-  const float2 rr = rotate_pair(gr, p.cos_sin + static_cast<size_t>(pos) * 64, lane, p.interleaved != 0, -1.f);
+  const float2 rr = rotate_pair(v.gr, p.cos_sin + static_cast<size_t>(v.pos) * 64, lane, p.interleaved != 0, -1.f);
   *reinterpret_cast<uint32_t*>(dx + kLatW + 2 * lane) = pack_bf16x2(rr.x, rr.y);
 }
 
@@ -430,21 +474,36 @@ __device__ __forceinline__ void store_part(float (&sums)[kNormWarps][kLatW], flo
   }
 }
 
+// Query rows first, then the latent rows; a warp reads its next row before it
+// works on the one it has.
 template <bool kQNorm, bool kKvNorm>
-__global__ void __launch_bounds__(kNormWarps * 32) norm_rope_bwd_kernel(const __grid_constant__ NormParams p) {
+__global__ void __launch_bounds__(kNormWarps * 32, 2) norm_rope_bwd_kernel(const __grid_constant__ NormParams p) {
   __shared__ float sums[kNormWarps][kLatW];
   const int lane = static_cast<int>(lane_id()), warp = static_cast<int>(threadIdx.x >> 5);
+  if constexpr (kQNorm || kKvNorm)
+    asm volatile("griddepcontrol.launch_dependents;");   // the weights' sums may be set up (they wait for this grid's end)
   const long long step = static_cast<long long>(gridDim.x) * kNormWarps;
   const long long first = static_cast<long long>(blockIdx.x) * kNormWarps + warp;
   float acc[16];
 #pragma unroll
   for (int i = 0; i < 16; ++i) acc[i] = 0.f;
   const long long rows = static_cast<long long>(p.n_tok) * p.h_q;
-  for (long long r = first; r < rows; r += step) {
+  auto load_q = [&](long long r) {
     const int t = static_cast<int>(r / p.h_q);
     const int h = static_cast<int>(r - static_cast<long long>(t) * p.h_q);
-    grad_row<kQNorm>(p, p.q + static_cast<long long>(t) * p.q_tok + static_cast<long long>(h) * p.q_head,
-                     p.dq + r * kRowW, p.dq_in + r * kRowW, p.q_weight, __ldg(p.positions + t), lane, acc);
+    return load_grad_row<kQNorm>(p.q + static_cast<long long>(t) * p.q_tok + static_cast<long long>(h) * p.q_head,
+                                 p.dq + r * kRowW, p.positions + t, lane);
+  };
+  auto load_kv = [&](long long r) {
+    return load_grad_row<kKvNorm>(p.kv + r * p.kv_tok, p.dkv + r * kRowW, p.positions + r, lane);
+  };
+  if (first < rows) {
+    GradRow next = load_q(first);
+    for (long long r = first; r < rows; r += step) {
+      const GradRow v = next;
+      if (r + step < rows) next = load_q(r + step);
+      grad_row<kQNorm>(p, v, p.dq_in + r * kRowW, p.q_weight, lane, acc);
+    }
   }
   if constexpr (kQNorm) {
     store_part(sums, acc, p.part_q, warp, lane);
@@ -452,30 +511,29 @@ __global__ void __launch_bounds__(kNormWarps * 32) norm_rope_bwd_kernel(const __
     for (int i = 0; i < 16; ++i) acc[i] = 0.f;
   }
   for (long long r = first; r < p.n_tok; r += step)
-    grad_row<kKvNorm>(p, p.kv + r * p.kv_tok, p.dkv + r * kRowW, p.dkv_in + r * kRowW, p.kv_weight,
-                      __ldg(p.positions + r), lane, acc);
+    grad_row<kKvNorm>(p, load_kv(r), p.dkv_in + r * kRowW, p.kv_weight, lane, acc);
   if constexpr (kKvNorm) store_part(sums, acc, p.part_kv, warp, lane);
 }
 
-// dw = the CTAs' shares added in a fixed order: 8 warps take every eighth
-// share of 32 columns, then add their sums.
-__global__ void __launch_bounds__(256) norm_weight_grad_kernel(const float* part_q, const float* part_kv, float* dw_q,
-                                                               float* dw_kv, int ctas) {
-  __shared__ float sums[8][32];
+// dw = the CTAs' shares added in a fixed order: 32 warps take every 32nd share
+// of 32 columns, then add their sums.  Launched as a dependent of the kernel
+// above; it reads only after that has completed.
+__global__ void __launch_bounds__(1024) norm_weight_grad_kernel(const float* part_q, const float* part_kv, float* dw_q,
+                                                                float* dw_kv, int ctas) {
+  __shared__ float sums[32][33];
   const float* part = blockIdx.y == 0 ? part_q : part_kv;
   float* dw = blockIdx.y == 0 ? dw_q : dw_kv;
-  if (dw == nullptr) return;
   const int lane = static_cast<int>(lane_id()), warp = static_cast<int>(threadIdx.x >> 5);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (dw == nullptr) return;
   const int c = static_cast<int>(blockIdx.x) * 32 + lane;
   float s = 0.f;
-  for (int i = warp; i < ctas; i += 8) s += part[static_cast<size_t>(i) * kLatW + c];
+#pragma unroll 8
+  for (int i = warp; i < ctas; i += 32) s += __ldcg(part + static_cast<size_t>(i) * kLatW + c);
   sums[warp][lane] = s;
   __syncthreads();
-  if (warp == 0) {
-#pragma unroll
-    for (int w = 1; w < 8; ++w) s += sums[w][lane];
-    dw[c] = s;
-  }
+  s = warp_sum(sums[lane][warp]);   // column `warp`, one share per lane
+  if (lane == 0) dw[static_cast<int>(blockIdx.x) * 32 + warp] = s;
 }
 
 }  // namespace smla
