@@ -483,12 +483,12 @@ def sparse_mla_decode_fp4(q, kv_cache, block_table, cache_seqlens, indices, sm_s
     _workspace(workspace, dev)
     with _launch_on(dev, stream) as cs:
         if out is None:
-            out = q.new_empty((batch, s_next, h_q, 512))
+            out = torch.empty((batch, s_next, h_q, 512), dtype=torch.bfloat16, device=dev)
         if lse is None:
-            lse = q.new_empty((batch, s_next, h_q), dtype=torch.float32)
+            lse = torch.empty((batch, s_next, h_q), dtype=torch.float32, device=dev)
         need = lib.sparse_mla_decode_fp4_workspace_size(batch, s_next, h_q, 512, topk)
         if workspace is None and need > 0:
-            workspace = kv_cache.new_empty(need)
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
         ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
         st = lib.sparse_mla_decode_fp4(_at(q), _at(kv_cache), _at(block_table), _at(cache_seqlens),
                                        _at(indices), float(sm_scale), float(kv_scale), _at(out), _at(lse), batch,
@@ -583,9 +583,9 @@ def mla_norm_rope(q, kv, positions, cos_sin, q_weight=None, kv_weight=None, eps:
     _given(kv_out, torch.bfloat16, "kv_out", n * 576, dev)
     with _launch_on(dev, stream) as cs:
         if q_out is None:
-            q_out = q.new_empty((n, h, 576))
+            q_out = torch.empty((n, h, 576), dtype=torch.bfloat16, device=dev)
         if kv_out is None:
-            kv_out = kv.new_empty((n, 576))
+            kv_out = torch.empty((n, 576), dtype=torch.bfloat16, device=dev)
         st = lib.mla_norm_rope(_at(q), q_steps[0], q_steps[1], _at(kv), kv_steps[0], _at(positions),
                                _at(cos_sin), cos_sin.shape[0], _at(q_weight), _at(kv_weight), float(eps),
                                int(bool(interleaved)), _at(q_out), _at(kv_out), _at(kv_cache), form,
@@ -620,15 +620,15 @@ def mla_norm_rope_bwd(q, kv, positions, cos_sin, dq, dkv, q_weight=None, kv_weig
     _workspace(workspace, dev)
     with _launch_on(dev, stream) as cs:
         if dq_in is None:
-            dq_in = q.new_empty((n, h, 576))
+            dq_in = torch.empty((n, h, 576), dtype=torch.bfloat16, device=dev)
         if dkv_in is None:
-            dkv_in = kv.new_empty((n, 576))
+            dkv_in = torch.empty((n, 576), dtype=torch.bfloat16, device=dev)
         if q_weight is not None and dq_weight is None:
-            dq_weight = dq.new_empty(512)
+            dq_weight = torch.empty(512, dtype=torch.float32, device=dev)
         if kv_weight is not None and dkv_weight is None:
-            dkv_weight = dq.new_empty(512)
+            dkv_weight = torch.empty(512, dtype=torch.float32, device=dev)
         if workspace is None and (q_weight is not None or kv_weight is not None):
-            workspace = dq.new_empty(max(4, lib.mla_norm_rope_bwd_workspace_size(n, h) // 4))
+            workspace = torch.empty(max(16, lib.mla_norm_rope_bwd_workspace_size(n, h)), dtype=torch.uint8, device=dev)
         ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
         st = lib.mla_norm_rope_bwd(_at(q), q_steps[0], q_steps[1], _at(kv), kv_steps[0], _at(positions),
                                    _at(cos_sin), cos_sin.shape[0], _at(q_weight), _at(kv_weight), float(eps),

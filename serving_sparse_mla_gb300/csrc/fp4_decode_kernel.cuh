@@ -33,9 +33,11 @@
 // A warp takes 16 rows of a block: it copies their slots (cp.async, its own
 // part of the ring), scores them, writes P to shared memory, and after one
 // barrier a block takes 512 / W columns of O^T over all of the block's rows.
-// Work is dealt as in the paged forward (block ranges, fwd_kernel.cuh): the
-// units' lists laid end to end and cut into one equal range per CTA; a second
-// kernel merges the pieces of cut units.
+// Work is dealt in one of two ways.  Few units: a cluster of CTAs takes a unit,
+// each an equal part of its list, and merges through distributed shared memory.
+// Many: as in the paged forward (block ranges, fwd_kernel.cuh), the units' lists
+// laid end to end and cut into one equal range per CTA; a second kernel merges
+// the pieces of cut units.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -47,6 +49,8 @@
 namespace smla {
 
 constexpr int kF4TileBytes = 16 * kFp4Slot;   // one warp's 16 rows
+constexpr int kF4MaxCluster = 16;
+constexpr int kF4PartRow = kDv + 8;           // floats of one head's piece in shared memory (the 8 spread the banks)
 
 struct Fp4Params {
   const __nv_bfloat16* q;      // [n_tok, h_q, 576]
@@ -62,6 +66,7 @@ struct Fp4Params {
   int groups;                  // head groups of a token
   int nb;                      // blocks of a list (Fp4Layout::kRows entries each)
   int ctas, part_rows;
+  int cluster;                 // CTAs of a unit's cluster (0: the units' blocks cut into ranges)
   float scale_log2;            // sm_scale * log2(e)
   float kv_scale;
 };
@@ -81,6 +86,8 @@ struct Fp4Shape {
   static constexpr int kRedOff = kPOff + 2 * kHeads * kPRow * 2;
   static constexpr int kMiscOff = kRedOff + W * kHeads * 4;
   static constexpr int kBytes = kMiscOff + kHeads * 4 + 2 * W * 4;
+  // A cluster's pieces: O in the ring's place, its LSEs and the weights in Q's.
+  static_assert(kHeads * kF4PartRow * 4 <= 2 * kStage && (1 + kF4MaxCluster) * kHeads * 4 <= 18 * NT * 512, "pieces");
   static_assert(W == 4 || W == 8, "64 / W columns of O^T per lane, in one scale group");
   static_assert((kBytes + 1024) * kPerSm <= 233472, "shared memory of an SM");
 };
@@ -371,6 +378,72 @@ __global__ void __launch_bounds__(256) fp4_merge_kernel(const __grid_constant__ 
   o[32] = make_uint2(pack_bf16x2(a1.x, a1.y), pack_bf16x2(a1.z, a1.w));
 }
 
+// CTA `rank` of this cluster: its shared address of what is at `local` here.
+__device__ __forceinline__ uint32_t cluster_addr(uint32_t local, int rank) {
+  uint32_t a;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(local), "r"(rank));
+  return a;
+}
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ float ld_cluster_f(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// The merge of a unit whose pieces are in the shared memory of its cluster's CTAs:
+// every CTA forms all pieces' weights, then adds its share of the columns.
+// part: [heads][kF4PartRow] here and at the same place in every CTA, lse: [heads].
+template <class L>
+__device__ __forceinline__ void f4_cluster_merge(const Fp4Params& p, int unit, int rank, const float* part, const float* lse,
+                                                 float* weight) {
+  const int tid = static_cast<int>(threadIdx.x);
+  const int tok = unit / p.groups, h0 = (unit % p.groups) * L::kHeads;
+  const int heads = min(L::kHeads, p.h_q - h0);
+  for (int i = tid; i < p.cluster * L::kHeads; i += L::kThreads)
+    weight[i] = ld_cluster_f(cluster_addr(smem_u32(lse + i % L::kHeads), i / L::kHeads));
+  __syncthreads();
+  if (tid < heads) {
+    float m = -INFINITY, sum = 0.f;
+    for (int s = 0; s < p.cluster; ++s) m = fmaxf(m, weight[s * L::kHeads + tid]);
+    for (int s = 0; s < p.cluster; ++s) {
+      const float v = weight[s * L::kHeads + tid];
+      sum += v == -INFINITY ? 0.f : expf(v - m);
+    }
+    for (int s = 0; s < p.cluster; ++s) {
+      const float v = weight[s * L::kHeads + tid];
+      weight[s * L::kHeads + tid] = v == -INFINITY ? 0.f : expf(v - m) / sum;
+    }
+    if (rank == 0) p.lse[static_cast<size_t>(tok) * p.h_q + h0 + tid] = sum == 0.f ? -INFINITY : m + logf(sum);
+  }
+  __syncthreads();
+  const int n = heads * (kDv / 4);   // float4 of the unit's output
+  const int hi = (rank + 1) * n / p.cluster;
+  for (int i = rank * n / p.cluster + tid; i < hi; i += L::kThreads) {
+    const int h = i / (kDv / 4), c4 = i % (kDv / 4);
+    const uint32_t at = smem_u32(part + h * kF4PartRow + 4 * c4);
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+    for (int s = 0; s < p.cluster; ++s) {
+      const float w = weight[s * L::kHeads + h];
+      const float4 v = ld_cluster_f4(cluster_addr(at, s));
+      a.x += w * v.x;
+      a.y += w * v.y;
+      a.z += w * v.z;
+      a.w += w * v.w;
+    }
+    *reinterpret_cast<uint2*>(p.out + (static_cast<size_t>(tok) * p.h_q + h0 + h) * kDv + 4 * c4) =
+        make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
+  }
+}
+
 template <class L>
 __global__ void __launch_bounds__(L::kThreads, L::kPerSm) fp4_decode_kernel(const __grid_constant__ Fp4Params p) {
   constexpr int NT = L::NT, W = L::W;
@@ -385,9 +458,20 @@ __global__ void __launch_bounds__(L::kThreads, L::kPerSm) fp4_decode_kernel(cons
   asm volatile("griddepcontrol.launch_dependents;");   // the merge may be set up (it waits for this grid's end)
 
   const long long total = static_cast<long long>(p.n_tok) * p.groups * p.nb;
-  const long long x0 = range_start(static_cast<int>(blockIdx.x), total, p.ctas);
-  const int n_blocks = static_cast<int>(range_start(static_cast<int>(blockIdx.x) + 1, total, p.ctas) - x0);
-  const int unit0 = static_cast<int>(x0 / p.nb), j0 = static_cast<int>(x0 % p.nb);
+  long long x0;     // this CTA's first block, over all units' lists laid end to end
+  int n_blocks, unit0, j0, rank = 0;
+  if (p.cluster == 0) {
+    x0 = range_start(static_cast<int>(blockIdx.x), total, p.ctas);
+    n_blocks = static_cast<int>(range_start(static_cast<int>(blockIdx.x) + 1, total, p.ctas) - x0);
+    unit0 = static_cast<int>(x0 / p.nb);
+    j0 = static_cast<int>(x0 % p.nb);
+  } else {
+    unit0 = static_cast<int>(blockIdx.x) / p.cluster;
+    rank = static_cast<int>(blockIdx.x) % p.cluster;
+    j0 = rank * p.nb / p.cluster;
+    n_blocks = (rank + 1) * p.nb / p.cluster - j0;
+    x0 = static_cast<long long>(unit0) * p.nb + j0;
+  }
 
   // The gather of this warp's rows goes by pairs of blocks: lane 16 k + r
   // follows row r of block 2 i + k from its list entry (read two pairs ahead)
@@ -448,10 +532,17 @@ __global__ void __launch_bounds__(L::kThreads, L::kPerSm) fp4_decode_kernel(cons
     asm volatile("cp.async.commit_group;" ::: "memory");
     return valid;
   };
+  auto prefetch_q = [&](int u) {   // a unit's Q on its way into L2
+    const int tok = u / p.groups, h0 = (u % p.groups) * L::kHeads;
+    const char* q0 = reinterpret_cast<const char*>(p.q + (static_cast<size_t>(tok) * p.h_q + h0) * kRowW);
+    const int bytes = min(L::kHeads, p.h_q - h0) * 2 * kRowW;
+    for (int x = 128 * tid; x < bytes; x += 128 * L::kThreads) prefetch_line_l2(q0 + x);
+  };
   int slots_a, slots_b;   // the current pair's slots, the next pair's
+  prefetch_q(unit0);
   read_entry();
-  f4_load_q<NT, W>(p, unit0, qbytes, qscale, warp, lane);   // while the first entries are on their way
   look_up();
+  f4_load_q<NT, W>(p, unit0, qbytes, qscale, warp, lane);   // while the first page-table entries are on their way
   read_entry();
   resolve();
   slots_a = slot_n;
@@ -573,12 +664,7 @@ __global__ void __launch_bounds__(L::kThreads, L::kPerSm) fp4_decode_kernel(cons
       look_up();
       read_entry();
     }
-    if (b + 1 < n_blocks && j == p.nb - 1) {   // the next unit's Q on its way into L2
-      const int tok = (unit + 1) / p.groups, h0 = ((unit + 1) % p.groups) * L::kHeads;
-      const char* q0 = reinterpret_cast<const char*>(p.q + (static_cast<size_t>(tok) * p.h_q + h0) * kRowW);
-      const int bytes = min(L::kHeads, p.h_q - h0) * 2 * kRowW;
-      for (int x = 128 * tid; x < bytes; x += 128 * L::kThreads) prefetch_line_l2(q0 + x);
-    }
+    if (b + 1 < n_blocks && j == p.nb - 1) prefetch_q(unit + 1);
     f4_values<NT, W, L::kPRow>(stage, pb, lw, o, warp, lane);
     ++j;
     if (j == p.nb || b == n_blocks - 1) {
@@ -586,10 +672,12 @@ __global__ void __launch_bounds__(L::kThreads, L::kPerSm) fp4_decode_kernel(cons
       const int tok = unit / p.groups, h0 = (unit % p.groups) * L::kHeads;
       const int heads = min(L::kHeads, p.h_q - h0);
       const long long ub = static_cast<long long>(unit) * p.nb;
-      const int c_first = range_cta(ub, total, p.ctas);
-      const int pieces = range_cta(ub + p.nb - 1, total, p.ctas) - c_first + 1;
-      const bool whole = pieces == 1;
+      const bool whole = p.cluster == 0 && range_cta(ub, total, p.ctas) == range_cta(ub + p.nb - 1, total, p.ctas);
       const size_t slot = 2 * static_cast<size_t>(blockIdx.x) + (x0 < ub ? 1 : 0);
+      // (a cluster's piece: the ring and Q are free, every warp past the barrier below is done with them)
+      float* part = p.cluster > 0 ? reinterpret_cast<float*>(f4_smem) : p.part_o + slot * p.part_rows * kDv;
+      float* part_lse = p.cluster > 0 ? reinterpret_cast<float*>(qbytes) : p.part_lse + slot * p.part_rows;
+      const int part_row = p.cluster > 0 ? kF4PartRow : kDv;
       // sums over this warp's rows, then over the warps
 #pragma unroll
       for (int n = 0; n < NT; ++n)
@@ -614,7 +702,7 @@ __global__ void __launch_bounds__(L::kThreads, L::kPerSm) fp4_decode_kernel(cons
             if (warp == 0 && g == 0) {
               const float v = sum == 0.f ? -INFINITY : (m[n][k] + log2f(sum)) * 0.69314718055994530942f;
               if (whole) p.lse[static_cast<size_t>(tok) * p.h_q + h0 + h] = v;
-              else p.part_lse[slot * p.part_rows + h] = v;
+              else part_lse[h] = v;
             }
 #pragma unroll
             for (int q = 0; q < 8 / W; ++q) {
@@ -628,7 +716,7 @@ __global__ void __launch_bounds__(L::kThreads, L::kPerSm) fp4_decode_kernel(cons
               if (whole) {
                 *reinterpret_cast<uint4*>(p.out + (static_cast<size_t>(tok) * p.h_q + h0 + h) * kDv + col) = pack8(y);
               } else {
-                float4* d = reinterpret_cast<float4*>(p.part_o + (slot * p.part_rows + h) * kDv + col);
+                float4* d = reinterpret_cast<float4*>(part + h * part_row + col);
                 d[0] = make_float4(y[0], y[1], y[2], y[3]);
                 d[1] = make_float4(y[4], y[5], y[6], y[7]);
               }
@@ -642,6 +730,12 @@ __global__ void __launch_bounds__(L::kThreads, L::kPerSm) fp4_decode_kernel(cons
     }
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
+  if (p.cluster > 0) {
+    cluster_sync();   // every piece is in its CTA's shared memory
+    float* lse = reinterpret_cast<float*>(qbytes);
+    f4_cluster_merge<L>(p, unit0, rank, reinterpret_cast<const float*>(f4_smem), lse, lse + L::kHeads);
+    cluster_sync();   // and stays there until all have read it
+  }
 }
 
 }  // namespace smla

@@ -26,11 +26,15 @@ constexpr int kMaxDevices = 64;
 constexpr unsigned long long kDefaultTimeoutNs = 1000000000ull;
 std::atomic<unsigned long long> g_timeout_ns{kDefaultTimeoutNs};
 
+constexpr int kF4ClusterSizes = 4;   // 16, 8, 4 and 2 CTAs
+constexpr int kF4ClusterSlack = 192;   // list entries
+
 struct DeviceState {
   bool probed = false;
   bool supported = false;
   int sm_count = 0;
   bool attrs_set = false;
+  int f4_clusters[3][kF4ClusterSizes] = {};   // 4-bit decode, per shape: clusters held at once
 };
 
 std::mutex g_mu;
@@ -42,8 +46,31 @@ constexpr int kTopkStageCap = 49152;
 constexpr int kTopkMaxSmem = smla::kTopkBins * 4 + kTopkStageCap * 4;
 
 template <class C>
-cudaError_t f4_attributes() {
-  return cudaFuncSetAttribute(smla::fp4_decode_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kBytes);
+void f4_cluster_config(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attr, int ctas, int cluster) {
+  cfg->gridDim = dim3(static_cast<unsigned>(ctas));
+  cfg->blockDim = dim3(C::kThreads);
+  cfg->dynamicSmemBytes = C::kBytes;
+  attr->id = cudaLaunchAttributeClusterDimension;
+  attr->val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr->val.clusterDim.y = attr->val.clusterDim.z = 1;
+  cfg->attrs = attr;
+  cfg->numAttrs = 1;
+}
+
+// Kernel attributes of a shape, and how many of its clusters of 16, 8, 4 and 2 CTAs
+// the device holds at once.
+template <class C>
+cudaError_t f4_setup(int* clusters) {
+  cudaError_t e = cudaFuncSetAttribute(smla::fp4_decode_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kBytes);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(smla::fp4_decode_kernel<C>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  for (int i = 0; i < kF4ClusterSizes && e == cudaSuccess; ++i) {
+    const int c = smla::kF4MaxCluster >> i;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr = {};
+    f4_cluster_config<C>(&cfg, &attr, c, c);
+    e = cudaOccupancyMaxActiveClusters(&clusters[i], smla::fp4_decode_kernel<C>, &cfg);
+  }
+  return e;
 }
 
 sparse_mla_status_t device_setup(int* sm_count) {
@@ -85,8 +112,9 @@ sparse_mla_status_t device_setup(int* sm_count) {
                              smla::idx_smem_bytes()) != cudaSuccess ||
         cudaFuncSetAttribute(smla::dsa_scores_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              smla::idx_smem_bytes()) != cudaSuccess ||
-        f4_attributes<smla::Fp4Shape8>() != cudaSuccess || f4_attributes<smla::Fp4Shape16>() != cudaSuccess ||
-        f4_attributes<smla::Fp4Shape32>() != cudaSuccess ||
+        f4_setup<smla::Fp4Shape8>(st.f4_clusters[0]) != cudaSuccess ||
+        f4_setup<smla::Fp4Shape16>(st.f4_clusters[1]) != cudaSuccess ||
+        f4_setup<smla::Fp4Shape32>(st.f4_clusters[2]) != cudaSuccess ||
         cudaFuncSetAttribute(smla::dsa_topk_kernel<256>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              kTopkMaxSmem) != cudaSuccess ||
         cudaFuncSetAttribute(smla::dsa_topk_kernel<1024>, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -523,15 +551,18 @@ auto f4_pick(int h_q, F&& f) {
   return f(smla::Fp4Shape32());
 }
 
+int f4_index(int h_q) { return h_q <= 8 ? 0 : (h_q <= 16 ? 1 : 2); }
+
 struct F4Plan {
   int ctas, groups, rows, nb;
+  int cluster;                      // CTAs per unit, merging among themselves (0: ranges)
   size_t lse_at, bytes;   // bytes from the workspace's start; bytes 0: no unit is cut
 };
 
 // The grid: as many CTAs as the card holds at once, or fewer where the lists
 // are short (a range has at least nb / 62 blocks, so a unit at most 64 pieces).
 template <class C>
-F4Plan f4_plan_of(long long n_tok, int h_q, int topk, int sms) {
+F4Plan f4_plan_of(long long n_tok, int h_q, int topk, int sms, const int* clusters) {
   F4Plan f;
   constexpr int H = C::kHeads;
   f.groups = (h_q + H - 1) / H;
@@ -542,6 +573,22 @@ F4Plan f4_plan_of(long long n_tok, int h_q, int topk, int sms) {
   f.ctas = static_cast<int>(g > most ? most : (g < 1 ? 1 : g));
   const size_t slots = 2 * static_cast<size_t>(f.ctas) * static_cast<size_t>(f.rows);
   f.lse_at = slots * smla::kDv * sizeof(float);
+  // Few units: the largest cluster of which all fit at once, where that leaves a
+  // CTA at most kF4ClusterSlack list entries more than an equal cut of all the work
+  // (8 heads, lists of 2048, clusters against ranges: 1 token 12.8 and 14.1 us, 16
+  // tokens 15.5 and 19.4, 96 tokens 35.2 and 37.1; at 128 tokens clusters would
+  // take 46.7 us and ranges take 42.5).
+  const long long units = n_tok * f.groups;
+  f.cluster = 0;
+  for (int i = 0; i < kF4ClusterSizes && f.cluster == 0; ++i) {
+    const int c = smla::kF4MaxCluster >> i;
+    if (c <= f.nb && units <= clusters[i] && (f.nb + c - 1) / c <= units * f.nb / most + kF4ClusterSlack / C::kRows) f.cluster = c;
+  }
+  if (f.cluster > 0) {
+    f.ctas = static_cast<int>(units) * f.cluster;
+    f.lse_at = f.bytes = 0;
+    return f;
+  }
   const long long total = n_tok * f.groups * f.nb;
   const bool whole = total % f.ctas == 0 && total / f.ctas % f.nb == 0;   // every range is whole units
   f.bytes = whole ? 0 : f.lse_at + slots * sizeof(float);
@@ -549,11 +596,21 @@ F4Plan f4_plan_of(long long n_tok, int h_q, int topk, int sms) {
 }
 
 F4Plan f4_plan(long long n_tok, int h_q, int topk, int sms) {
-  return f4_pick(h_q, [&](auto shape) { return f4_plan_of<decltype(shape)>(n_tok, h_q, topk, sms); });
+  int dev = 0;
+  const int* clusters = cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < kMaxDevices ? g_dev[dev].f4_clusters[f4_index(h_q)]
+                                                                                           : g_dev[0].f4_clusters[0];
+  return f4_pick(h_q, [&](auto shape) { return f4_plan_of<decltype(shape)>(n_tok, h_q, topk, sms, clusters); });
 }
 
 template <class C>
 cudaError_t f4_launch(const smla::Fp4Params& p, cudaStream_t cs) {
+  if (p.cluster > 0) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr = {};
+    f4_cluster_config<C>(&cfg, &attr, p.ctas, p.cluster);
+    cfg.stream = cs;
+    return cudaLaunchKernelEx(&cfg, smla::fp4_decode_kernel<C>, p);
+  }
   smla::fp4_decode_kernel<C><<<p.ctas, C::kThreads, C::kBytes, cs>>>(p);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || p.part_o == nullptr) return e;
@@ -613,6 +670,7 @@ sparse_mla_status_t sparse_mla_decode_fp4(const void* q, const void* kv_cache, c
   p.nb = f.nb;
   p.ctas = f.ctas;
   p.part_rows = f.rows;
+  p.cluster = f.cluster;
   p.scale_log2 = sm_scale * 1.4426950408889634f;
   p.kv_scale = kv_scale;
   if (f.bytes > 0) {

@@ -77,6 +77,16 @@ def test_long_lists_cut_over_ctas(smla, h_q):
     _check(smla, c, u, f"fp4 decode short lists h={h_q}")
 
 
+@pytest.mark.parametrize("h_q", [8, 16, 40])
+@pytest.mark.parametrize("tokens,topk", [(1, 70), (2, 2048), (9, 640), (20, 1100), (60, 2048), (120, 500)])
+def test_every_split_of_the_lists(smla, h_q, tokens, topk):
+    """From one token to more units than clusters fit: clusters of 16 to 2 CTAs,
+    ranges with a merge, and whole units."""
+    c, u = mi.decode_case_fp4(1000 + tokens, batch=1, s_next=tokens, h_q=h_q, lo=2500, hi=2500, topk=topk, page=64,
+                              spare_pages=2)
+    _check(smla, c, u, f"fp4 decode {tokens} tokens, {topk} entries h={h_q}")
+
+
 @pytest.mark.parametrize("h_q", [8, 16, 64])
 def test_many_tokens_of_one_request(smla, h_q):
     """More units than CTAs, so that a CTA works through several."""
@@ -156,19 +166,21 @@ def test_queries_of_any_size(smla, h_q):
         assert torch.equal(o, o2) and torch.equal(l, l2)
 
 
-@pytest.mark.parametrize("h_q", [8, 64])
-def test_workspace_streams_and_graphs(smla, h_q):
-    """A dirty workspace of exactly the size asked for; two decodes on two
-    streams with their own workspaces; two captured graphs replayed."""
-    cases = [mi.decode_case_fp4(995 + k, batch=2, s_next=2, h_q=h_q, lo=2100, hi=3000, topk=2048, spare_pages=2)
+@pytest.mark.parametrize("h_q,s_next", [(8, 2), (64, 2), (8, 60), (64, 60)])
+def test_workspace_streams_and_graphs(smla, h_q, s_next):
+    """A dirty workspace of exactly the size asked for (few tokens ask for none:
+    their pieces meet in a cluster); two decodes on two streams with their own
+    workspaces; two captured graphs replayed."""
+    cases = [mi.decode_case_fp4(995 + k, batch=2, s_next=s_next, h_q=h_q, lo=2100, hi=3000, topk=2048, spare_pages=2)
              for k in range(2)]
     want = [_run(smla, c, u) for c, u in cases]
-    need = smla.decode_fp4_workspace_size(2, 2, h_q, 2048)
-    assert need > 0
-    ws = [torch.full((need,), 0xFF, dtype=torch.uint8, device=DEV) for _ in cases]
+    need = smla.decode_fp4_workspace_size(2, s_next, h_q, 2048)
+    assert need > 0 if s_next == 60 else (need == 0 or h_q > 8)
+    ws = [torch.full((max(need, 16),), 0xFF, dtype=torch.uint8, device=DEV) for _ in cases]
     args = [([t.to(DEV) for t in (c.q, u, c.block_table, c.cache_seqlens, c.indices)], c.sm_scale) for c, u in cases]
-    with pytest.raises(smla.SparseMLAError):
-        smla.sparse_mla_decode_fp4(*args[0][0], args[0][1], workspace=ws[0][:need - 16])
+    if need:
+        with pytest.raises(smla.SparseMLAError):
+            smla.sparse_mla_decode_fp4(*args[0][0], args[0][1], workspace=ws[0][:need - 16])
     streams = [torch.cuda.Stream() for _ in cases]
     torch.cuda.synchronize()
     got = []
