@@ -170,7 +170,8 @@ def _fits(t: Optional[torch.Tensor], need: int, name: str, device) -> None:
 def _given(t: Optional[torch.Tensor], dtype, name: str, need: int, device) -> None:
     """A caller-supplied output or workspace: CUDA, dtype, contiguous, large
     enough and on the call's device."""
-    if t is None:
+    if t is None or (t.is_cuda and t.dtype is dtype and t.device == device and t.is_contiguous()
+                     and t.numel() >= need):
         return
     _need(t, dtype, name)
     _fits(t, need, name, device)
@@ -414,11 +415,21 @@ def sparse_mla_decode_fp8(q, kv_cache, block_table, cache_seqlens, indices, sm_s
 # ---------------------------------------------------------------- 4-bit cache decode
 
 FP4_SLOT_BYTES = 416
+_BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
 
 
 def _at(t: Optional[torch.Tensor]):
     """The address as the number that ctypes takes for a pointer argument."""
     return None if t is None else t.data_ptr()
+
+
+# A decode step's calls take a few microseconds on the GPU, and a tensor's every
+# attribute costs the host about a tenth of one: the entry points below first ask
+# in one expression whether all is as it should be, and only where it is not go
+# through the checks that say what is wrong.
+
+def _dense(t: torch.Tensor, dtype, need: int, dev) -> bool:
+    return t.dtype is dtype and t.device == dev and t.is_contiguous() and t.numel() >= need
 
 
 class _launch_on:
@@ -442,11 +453,22 @@ class _launch_on:
             self.guard.__enter__()
         if self.stream is not None:
             return self.stream.cuda_stream
-        return torch._C._cuda_getCurrentRawStream(dev.index)   # current_stream(dev).cuda_stream without its objects
+        return torch.cuda.current_stream(dev).cuda_stream
 
     def __exit__(self, *exc):
         if self.guard is not None:
             self.guard.__exit__(*exc)
+
+
+def _launch(go, dev, stream, where: str):
+    """go(stream handle) with `dev` current."""
+    if stream is None and dev.index == torch._C._cuda_getDevice():
+        st = go(torch._C._cuda_getCurrentRawStream(dev.index))
+    else:
+        with _launch_on(dev, stream) as cs:
+            st = go(cs)
+    if st != 0:
+        raise SparseMLAError(st, where)
 
 
 def decode_fp4_workspace_size(batch: int, s_next: int, h_q: int, topk: int, d_v: int = 512) -> int:
@@ -463,38 +485,46 @@ def sparse_mla_decode_fp4(q, kv_cache, block_table, cache_seqlens, indices, sm_s
     kv_scale; everything else as sparse_mla_decode."""
     lib = load()
     batch, s_next, h_q, d_qk = q.shape
-    num_blocks = kv_cache.shape[0]
-    page = kv_cache.shape[1] if page_size is None else page_size
+    cache_shape = kv_cache.shape
+    num_blocks = cache_shape[0]
+    page = cache_shape[1] if page_size is None else page_size
     max_blocks = block_table.shape[1]
     topk = indices.shape[-1]
-    for t, dt, n in ((q, torch.bfloat16, "q"), (kv_cache, torch.uint8, "kv_cache"),
-                     (block_table, torch.int32, "block_table"), (cache_seqlens, torch.int32, "cache_seqlens"),
-                     (indices, torch.int32, "indices")):
-        _need(t, dt, n)
-    if kv_cache.shape[-1] != FP4_SLOT_BYTES:
-        raise ValueError(f"kv_cache slots must be {FP4_SLOT_BYTES} bytes, got {kv_cache.shape[-1]}")
     dev = q.device
-    _fits(kv_cache, num_blocks * page * FP4_SLOT_BYTES, "kv_cache", dev)
-    _fits(block_table, batch * max_blocks, "block_table", dev)
-    _fits(cache_seqlens, batch, "cache_seqlens", dev)
-    _fits(indices, batch * s_next * topk, "indices", dev)
-    _given(out, torch.bfloat16, "out", batch * s_next * h_q * 512, dev)
-    _given(lse, torch.float32, "lse", batch * s_next * h_q, dev)
+    if not (q.is_cuda and q.dtype is _BF16 and q.is_contiguous() and cache_shape[-1] == FP4_SLOT_BYTES
+            and _dense(kv_cache, _U8, num_blocks * page * FP4_SLOT_BYTES, dev)
+            and _dense(block_table, _I32, batch * max_blocks, dev) and _dense(cache_seqlens, _I32, batch, dev)
+            and _dense(indices, _I32, batch * s_next * topk, dev)):
+        for t, dt, n in ((q, _BF16, "q"), (kv_cache, _U8, "kv_cache"), (block_table, _I32, "block_table"),
+                         (cache_seqlens, _I32, "cache_seqlens"), (indices, _I32, "indices")):
+            _need(t, dt, n)
+        if cache_shape[-1] != FP4_SLOT_BYTES:
+            raise ValueError(f"kv_cache slots must be {FP4_SLOT_BYTES} bytes, got {cache_shape[-1]}")
+        _fits(kv_cache, num_blocks * page * FP4_SLOT_BYTES, "kv_cache", dev)
+        _fits(block_table, batch * max_blocks, "block_table", dev)
+        _fits(cache_seqlens, batch, "cache_seqlens", dev)
+        _fits(indices, batch * s_next * topk, "indices", dev)
+    _given(out, _BF16, "out", batch * s_next * h_q * 512, dev)
+    _given(lse, _F32, "lse", batch * s_next * h_q, dev)
     _workspace(workspace, dev)
-    with _launch_on(dev, stream) as cs:
-        if out is None:
-            out = torch.empty((batch, s_next, h_q, 512), dtype=torch.bfloat16, device=dev)
-        if lse is None:
-            lse = torch.empty((batch, s_next, h_q), dtype=torch.float32, device=dev)
-        need = lib.sparse_mla_decode_fp4_workspace_size(batch, s_next, h_q, 512, topk)
-        if workspace is None and need > 0:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-        st = lib.sparse_mla_decode_fp4(_at(q), _at(kv_cache), _at(block_table), _at(cache_seqlens),
-                                       _at(indices), float(sm_scale), float(kv_scale), _at(out), _at(lse), batch,
-                                       s_next, h_q, d_qk, 512, topk, page, max_blocks, num_blocks, _at(workspace),
-                                       ws_bytes, cs)
-    _check(st, "sparse_mla_decode_fp4")
+    if out is None:
+        out = torch.empty((batch, s_next, h_q, 512), dtype=_BF16, device=dev)
+    if lse is None:
+        lse = torch.empty((batch, s_next, h_q), dtype=_F32, device=dev)
+
+    def go(cs):
+        ws = workspace
+        if ws is None:
+            need = lib.sparse_mla_decode_fp4_workspace_size(batch, s_next, h_q, 512, topk)
+            if need > 0:
+                ws = torch.empty(need, dtype=_U8, device=dev)
+        ws_bytes = 0 if ws is None else ws.numel() * ws.element_size()
+        return lib.sparse_mla_decode_fp4(q.data_ptr(), kv_cache.data_ptr(), block_table.data_ptr(),
+                                         cache_seqlens.data_ptr(), indices.data_ptr(), sm_scale, kv_scale,
+                                         out.data_ptr(), lse.data_ptr(), batch, s_next, h_q, d_qk, 512, topk, page,
+                                         max_blocks, num_blocks, _at(ws), ws_bytes, cs)
+
+    _launch(go, dev, stream, "sparse_mla_decode_fp4")
     return out, lse
 
 
@@ -524,13 +554,24 @@ def _rows(t: torch.Tensor, name: str, heads: bool):
     return tok, head
 
 
+def _is_weight(w, dev) -> bool:
+    return w is None or (w.dtype is _BF16 and w.device == dev and w.is_contiguous() and w.numel() == 512)
+
+
 def _norm_args(q, kv, positions, cos_sin, q_weight, kv_weight):
-    q_steps = _rows(q, "q", True)
-    kv_steps = _rows(kv, "kv", False)
-    n, h, _ = q.shape
-    dev = q.device
-    if kv.shape[0] != n:
-        raise ValueError(f"kv has {kv.shape[0]} rows; q has {n} tokens")
+    """(tokens, heads, device, strides of q, token stride of kv) of checked arguments."""
+    qs, qt, ks, kt, dev = q.shape, q.stride(), kv.shape, kv.stride(), q.device
+    if (q.is_cuda and q.dtype is _BF16 and kv.dtype is _BF16 and len(qs) == 3 and len(ks) == 2 and qs[2] == 576
+            and ks[1] == 576 and qs[0] == ks[0] and qt[2] == 1 and kt[1] == 1 and not (qt[0] | qt[1] | kt[0]) & 7
+            and not (q.data_ptr() | kv.data_ptr()) & 15 and kv.device == dev
+            and _dense(positions, _I32, qs[0], dev) and _dense(cos_sin, _F32, 0, dev) and cos_sin.dim() == 2
+            and cos_sin.shape[1] == 64 and _is_weight(q_weight, dev) and _is_weight(kv_weight, dev)):
+        return qs[0], qs[1], dev, qt[0], qt[1], kt[0]
+    q_tok, q_head = _rows(q, "q", True)
+    kv_tok, _ = _rows(kv, "kv", False)
+    n = qs[0]
+    if ks[0] != n:
+        raise ValueError(f"kv has {ks[0]} rows; q has {n} tokens")
     _fits(kv, 0, "kv", dev)
     _need(positions, torch.int32, "positions")
     _fits(positions, n, "positions", dev)
@@ -543,7 +584,7 @@ def _norm_args(q, kv, positions, cos_sin, q_weight, kv_weight):
             _given(w, torch.bfloat16, name, 512, dev)
             if w.numel() != 512:
                 raise ValueError(f"{name} must hold 512 values, got {w.numel()}")
-    return n, h, dev, q_steps, kv_steps
+    return n, qs[1], dev, q_tok, q_head, kv_tok
 
 
 def mla_norm_rope(q, kv, positions, cos_sin, q_weight=None, kv_weight=None, eps: float = 1e-6,
@@ -561,36 +602,37 @@ def mla_norm_rope(q, kv, positions, cos_sin, q_weight=None, kv_weight=None, eps:
     the cache: not stored).  -> (q_out [n, h, 576], kv_out [n, 576]), bf16;
     kv_out holds what the slots stand for.  q_out / kv_out may be q / kv."""
     lib = load()
-    n, h, dev, q_steps, kv_steps = _norm_args(q, kv, positions, cos_sin, q_weight, kv_weight)
+    n, h, dev, q_tok, q_head, kv_tok = _norm_args(q, kv, positions, cos_sin, q_weight, kv_weight)
     form, n_slots = 0, 0
     if kv_cache is not None:
-        _need(kv_cache, kv_cache.dtype, "kv_cache")
-        form = _CACHE_FORMATS.get((kv_cache.dtype, kv_cache.shape[-1]), -1)
+        width = kv_cache.shape[-1]
+        form = _CACHE_FORMATS.get((kv_cache.dtype, width), -1)
         if form < 0:
             raise ValueError("kv_cache must be bf16 [.., 576] or uint8 [.., 656] or [.., 416], got "
                              f"{kv_cache.dtype} {tuple(kv_cache.shape)}")
         if slots is None:
             raise ValueError("kv_cache is given without slots")
-        _fits(kv_cache, 0, "kv_cache", dev)
-        _need(slots, torch.int32, "slots")
-        _fits(slots, n, "slots", dev)
-        n_slots = kv_cache.numel() // kv_cache.shape[-1]
+        _given(kv_cache, kv_cache.dtype, "kv_cache", 0, dev)
+        _given(slots, _I32, "slots", n, dev)
+        n_slots = kv_cache.numel() // width
         if n_slots > 2 ** 31 - 1:
             raise ValueError("a cache of more than 2^31 - 1 slots")
     elif slots is not None:
         raise ValueError("slots are given without kv_cache")
-    _given(q_out, torch.bfloat16, "q_out", n * h * 576, dev)
-    _given(kv_out, torch.bfloat16, "kv_out", n * 576, dev)
-    with _launch_on(dev, stream) as cs:
-        if q_out is None:
-            q_out = torch.empty((n, h, 576), dtype=torch.bfloat16, device=dev)
-        if kv_out is None:
-            kv_out = torch.empty((n, 576), dtype=torch.bfloat16, device=dev)
-        st = lib.mla_norm_rope(_at(q), q_steps[0], q_steps[1], _at(kv), kv_steps[0], _at(positions),
-                               _at(cos_sin), cos_sin.shape[0], _at(q_weight), _at(kv_weight), float(eps),
-                               int(bool(interleaved)), _at(q_out), _at(kv_out), _at(kv_cache), form,
-                               float(kv_scale), _at(slots), n_slots, n, h, 576, cs)
-    _check(st, "mla_norm_rope")
+    _given(q_out, _BF16, "q_out", n * h * 576, dev)
+    _given(kv_out, _BF16, "kv_out", n * 576, dev)
+    if q_out is None:
+        q_out = torch.empty((n, h, 576), dtype=_BF16, device=dev)
+    if kv_out is None:
+        kv_out = torch.empty((n, 576), dtype=_BF16, device=dev)
+
+    def go(cs):
+        return lib.mla_norm_rope(q.data_ptr(), q_tok, q_head, kv.data_ptr(), kv_tok, positions.data_ptr(),
+                                 cos_sin.data_ptr(), cos_sin.shape[0], _at(q_weight), _at(kv_weight), eps,
+                                 1 if interleaved else 0, q_out.data_ptr(), kv_out.data_ptr(), _at(kv_cache), form,
+                                 kv_scale, _at(slots), n_slots, n, h, 576, cs)
+
+    _launch(go, dev, stream, "mla_norm_rope")
     return q_out, kv_out
 
 
@@ -607,34 +649,38 @@ def mla_norm_rope_bwd(q, kv, positions, cos_sin, dq, dkv, q_weight=None, kv_weig
     bf16, dq_weight [512] fp32 or None, dkv_weight [512] fp32 or None).
     Padding tokens get zero rows."""
     lib = load()
-    n, h, dev, q_steps, kv_steps = _norm_args(q, kv, positions, cos_sin, q_weight, kv_weight)
-    for t, need, name in ((dq, n * h * 576, "dq"), (dkv, n * 576, "dkv")):
-        _need(t, torch.float32, name)
-        _fits(t, need, name, dev)
-    _given(dq_in, torch.bfloat16, "dq_in", n * h * 576, dev)
-    _given(dkv_in, torch.bfloat16, "dkv_in", n * 576, dev)
-    for w, dw, name in ((q_weight, dq_weight, "dq_weight"), (kv_weight, dkv_weight, "dkv_weight")):
-        if w is None and dw is not None:
-            raise ValueError(f"{name} is given without its weight")
-        _given(dw, torch.float32, name, 512, dev)
+    n, h, dev, q_tok, q_head, kv_tok = _norm_args(q, kv, positions, cos_sin, q_weight, kv_weight)
+    _given(dq, _F32, "dq", n * h * 576, dev)
+    _given(dkv, _F32, "dkv", n * 576, dev)
+    _given(dq_in, _BF16, "dq_in", n * h * 576, dev)
+    _given(dkv_in, _BF16, "dkv_in", n * 576, dev)
+    if (q_weight is None and dq_weight is not None) or (kv_weight is None and dkv_weight is not None):
+        raise ValueError(f"{'dq_weight' if q_weight is None and dq_weight is not None else 'dkv_weight'} is given "
+                         "without its weight")
+    _given(dq_weight, _F32, "dq_weight", 512, dev)
+    _given(dkv_weight, _F32, "dkv_weight", 512, dev)
     _workspace(workspace, dev)
-    with _launch_on(dev, stream) as cs:
-        if dq_in is None:
-            dq_in = torch.empty((n, h, 576), dtype=torch.bfloat16, device=dev)
-        if dkv_in is None:
-            dkv_in = torch.empty((n, 576), dtype=torch.bfloat16, device=dev)
-        if q_weight is not None and dq_weight is None:
-            dq_weight = torch.empty(512, dtype=torch.float32, device=dev)
-        if kv_weight is not None and dkv_weight is None:
-            dkv_weight = torch.empty(512, dtype=torch.float32, device=dev)
-        if workspace is None and (q_weight is not None or kv_weight is not None):
-            workspace = torch.empty(max(16, lib.mla_norm_rope_bwd_workspace_size(n, h)), dtype=torch.uint8, device=dev)
-        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-        st = lib.mla_norm_rope_bwd(_at(q), q_steps[0], q_steps[1], _at(kv), kv_steps[0], _at(positions),
-                                   _at(cos_sin), cos_sin.shape[0], _at(q_weight), _at(kv_weight), float(eps),
-                                   int(bool(interleaved)), _at(dq), _at(dkv), _at(dq_in), _at(dkv_in),
-                                   _at(dq_weight), _at(dkv_weight), n, h, 576, _at(workspace), ws_bytes, cs)
-    _check(st, "mla_norm_rope_bwd")
+    if dq_in is None:
+        dq_in = torch.empty((n, h, 576), dtype=_BF16, device=dev)
+    if dkv_in is None:
+        dkv_in = torch.empty((n, 576), dtype=_BF16, device=dev)
+    if q_weight is not None and dq_weight is None:
+        dq_weight = torch.empty(512, dtype=_F32, device=dev)
+    if kv_weight is not None and dkv_weight is None:
+        dkv_weight = torch.empty(512, dtype=_F32, device=dev)
+
+    def go(cs):
+        ws = workspace
+        if ws is None and (q_weight is not None or kv_weight is not None):
+            ws = torch.empty(max(16, lib.mla_norm_rope_bwd_workspace_size(n, h)), dtype=_U8, device=dev)
+        ws_bytes = 0 if ws is None else ws.numel() * ws.element_size()
+        return lib.mla_norm_rope_bwd(q.data_ptr(), q_tok, q_head, kv.data_ptr(), kv_tok, positions.data_ptr(),
+                                     cos_sin.data_ptr(), cos_sin.shape[0], _at(q_weight), _at(kv_weight), eps,
+                                     1 if interleaved else 0, dq.data_ptr(), dkv.data_ptr(), dq_in.data_ptr(),
+                                     dkv_in.data_ptr(), _at(dq_weight), _at(dkv_weight), n, h, 576, _at(ws),
+                                     ws_bytes, cs)
+
+    _launch(go, dev, stream, "mla_norm_rope_bwd")
     return dq_in, dkv_in, dq_weight, dkv_weight
 
 
