@@ -251,7 +251,7 @@ sparse_mla_status_t sparse_mla_decode_fp8(const void* q, const void* kv_cache, c
  * NaN.  mla_norm_rope writes such slots.
  *
  *   kv_cache      uint8 [num_blocks, page_size, 416], 16-byte aligned
- *   kv_scale      one finite, positive factor for the whole cache (1 for none)
+ *   kv_scale      one factor for the whole cache (1 for none), in [2^-64, 2^64]
  *   workspace     at least sparse_mla_decode_fp4_workspace_size(...) bytes,
  *                 16-byte aligned; used as sparse_mla_decode uses its own: two
  *                 calls that may run concurrently need separate workspaces
@@ -303,7 +303,7 @@ typedef enum {
  *   kv_cache   the cache's slots, 16-byte aligned, or NULL (nothing is stored;
  *              kv_out is still rounded as cache_format would hold it)
  *   cache_format  sparse_mla_cache_format_t
- *   kv_scale   the 4-bit cache's factor (1 for the other formats)
+ *   kv_scale   the 4-bit cache's factor, in [2^-64, 2^64] (1 for the other formats)
  *   slots      int32 [n_tok]: the token's slot (page * page_size + offset); a
  *              slot outside [0, n_slots) stores nothing.  The slots of a call
  *              are distinct (a slot given twice holds parts of either row).

@@ -217,7 +217,8 @@ __device__ __forceinline__ void store_fp8(uint8_t* slot, bool keep, int half, in
 // e4m3(largest / (6 kv_scale)), at least 2^-9; code = e2m1(y / (scale kv_scale)).
 // The quotient is one multiplication by the reciprocal and its correction
 // by the remainder, exact where y / step is (halfway values are common: few
-// bits on both sides).
+// bits on both sides); values past 8 steps, all of code 6, are cut there, so
+// that the quotient stays finite where the scale is at its largest.
 __device__ __forceinline__ void store_fp4(uint8_t* slot, bool keep, int half, int lane, float kv_scale, float kv_scale6,
                                           float* y) {
   float top = 0.f;
@@ -235,8 +236,9 @@ __device__ __forceinline__ void store_fp4(uint8_t* slot, bool keep, int half, in
   float x[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float t = __fmul_rn(y[i], inv);
-    x[i] = __fmaf_rn(__fmaf_rn(-t, step, y[i]), inv, t);
+    const float v = fminf(fmaxf(y[i], -8.f * step), 8.f * step);
+    const float t = __fmul_rn(v, inv);
+    x[i] = __fmaf_rn(__fmaf_rn(-t, step, v), inv, t);
   }
   const uint32_t c = bad ? 0u : e2m1x8_of(x);
   uint32_t h[4];

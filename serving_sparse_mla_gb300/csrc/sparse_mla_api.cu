@@ -542,6 +542,10 @@ cudaError_t launch_dependent(void (*kernel)(Args...), dim3 grid, dim3 block, cud
 
 namespace {
 
+// A 4-bit cache's factor: far enough from fp32's ends that a group's step
+// (a scale of 2^-9 .. 448 times the factor) and its reciprocal are normal.
+bool kv_scale_ok(float f) { return f >= 0x1p-64f && f <= 0x1p64f; }
+
 // The kernel's shape for a number of heads: the smallest of 8, 16 and 32 that
 // holds them (more heads are several units of 32).
 template <class F>
@@ -637,10 +641,10 @@ sparse_mla_status_t sparse_mla_decode_fp4(const void* q, const void* kv_cache, c
                                           int d_qk, int d_v, int topk, int page_size, int max_blocks, int num_blocks,
                                           void* workspace, size_t workspace_bytes, void* stream) {
   int sms = 0;
+  if (!kv_scale_ok(kv_scale)) return SPARSE_MLA_ERR_INVALID_ARG;
   sparse_mla_status_t st = check_decode(q, kv_cache, block_table, cache_seqlens, indices, out, lse, batch, s_next,
                                         h_q, d_qk, d_v, topk, page_size, max_blocks, num_blocks, &sms);
   if (st != SPARSE_MLA_OK) return st;
-  if (!std::isfinite(kv_scale) || kv_scale <= 0.f) return SPARSE_MLA_ERR_INVALID_ARG;
   const long long n_tok = static_cast<long long>(batch) * s_next;
   if (n_tok == 0) return SPARSE_MLA_OK;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
@@ -754,7 +758,7 @@ sparse_mla_status_t mla_norm_rope(const void* q, long long q_tok_stride, long lo
                                       q_weight, kv_weight, eps, n_tok, h_q, d_qk);
   if (st != SPARSE_MLA_OK) return st;
   if (n_slots < 0 || cache_format < 0 || cache_format > 2) return SPARSE_MLA_ERR_INVALID_ARG;
-  if (!std::isfinite(kv_scale) || kv_scale <= 0.f || (cache_format != SPARSE_MLA_CACHE_FP4 && kv_scale != 1.f))
+  if (!kv_scale_ok(kv_scale) || (cache_format != SPARSE_MLA_CACHE_FP4 && kv_scale != 1.f))
     return SPARSE_MLA_ERR_INVALID_ARG;
   const bool cached = kv_cache != nullptr && n_slots > 0;
   if (cached && n_tok > 0 && (!slots || !aligned(slots, 4) || !aligned(kv_cache, 16))) return SPARSE_MLA_ERR_INVALID_ARG;

@@ -192,6 +192,25 @@ def test_rows_of_zeros_extremes_and_non_finite_values(smla, form):
     assert bool(torch.isfinite(ko[[1, 2, 5, 6]]).all())
 
 
+@pytest.mark.parametrize("ks", [2.0 ** -64, 2.0 ** -20, 2.0 ** 20, 2.0 ** 64])
+def test_values_far_past_the_largest_scale(smla, ks):
+    """Groups whose values pass 448 * 6 factors many times over keep code 6 and
+    their signs; factors at the ends of their range."""
+    n = 6
+    _, kv, _, _ = mi.norm_rows(18, n, 1)
+    size = torch.tensor([2.0 ** 120, 2.0 ** 60, 1.0, 2.0 ** -60, ks, ks * 2.0 ** 12], dtype=torch.float64)
+    kv[:, :512] = (kv[:, :512].double() * size[:, None]).bfloat16()
+    kv[0, :16] = 2.0 ** -70
+    kv[0, 3] = -2.0 ** 127
+    pos, cs = torch.arange(n, dtype=torch.int32, device=DEV), mi.rope_table(n).to(DEV)
+    cache = _cache("fp4", 1, 16, 0)
+    q = kv.view(n, 1, 576).to(DEV)
+    _, ko = smla.mla_norm_rope(q, kv.to(DEV), pos, cs, kv_cache=cache, slots=pos, kv_scale=ks)
+    val, lat = _want_latent(_f64(kv)[:, :512], "fp4", ks)
+    assert np.array_equal(_slot_bytes(cache)[:n, :288], lat)
+    assert np.array_equal(_f64(ko)[:, :512], torch.from_numpy(val).to(torch.float32).bfloat16().double().numpy())
+
+
 def _bwd_reference(q, kv, qw, kw, ang, live, dq, dkv, il):
     rq, rwq = nro.norm_rope_bwd(q, dq * live[:, None, None], ang[:, None], qw, EPS, il)
     rk, rwk = nro.norm_rope_bwd(kv, dkv * live[:, None], ang, kw, EPS, il)

@@ -87,6 +87,12 @@ def test_fp4_argument_codes(lib):
     assert lib.mla_norm_rope_bwd_workspace_size(0, 8) == 0
 
 
+def test_a_cache_factor_near_the_ends_of_fp32_is_refused(lib):
+    """A group's step is 2^-9 .. 448 factors; it and its reciprocal have to be normal."""
+    for ks in (2.0 ** -65, 1e-38, 1e-45, 2.0 ** 65, 3e38):
+        assert _norm(lib, ks=ks) == 1 and _fp4(lib, ks=ks) == 1, ks
+
+
 # ------------------------------------------------------------------ binding
 
 def _args(n=5, h=3, n_pos=20):
