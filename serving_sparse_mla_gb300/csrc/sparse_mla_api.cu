@@ -555,6 +555,14 @@ auto f4_pick(int h_q, F&& f) {
   return f(smla::Fp4Shape32());
 }
 
+// Units, rows and list entries are counted in 32 bits (a list's last block may
+// be a block past its end), CTAs times blocks in 64 (3 CTAs per SM are far below 4096).
+bool f4_sizes_ok(long long n_tok, int h_q, int topk) {
+  if (n_tok > INT_MAX / 2 || static_cast<long long>(h_q) * n_tok > INT_MAX || topk > INT_MAX - 1024) return false;
+  const long long blocks = n_tok * ((h_q - 1) / 8 + 1) * ((topk - 1) / 64 + 1);   // at least as many as any shape's
+  return blocks <= (1LL << 62) / 4096;
+}
+
 int f4_index(int h_q) { return h_q <= 8 ? 0 : (h_q <= 16 ? 1 : 2); }
 
 struct F4Plan {
@@ -569,7 +577,7 @@ template <class C>
 F4Plan f4_plan_of(long long n_tok, int h_q, int topk, int sms, const int* clusters) {
   F4Plan f;
   constexpr int H = C::kHeads;
-  f.groups = (h_q + H - 1) / H;
+  f.groups = (h_q - 1) / H + 1;
   f.rows = h_q < H ? h_q : H;
   f.nb = (topk + C::kRows - 1) / C::kRows;
   const long long most = static_cast<long long>(sms) * C::kPerSm;
@@ -631,8 +639,9 @@ extern "C" {
 size_t sparse_mla_decode_fp4_workspace_size(int batch, int s_next, int h_q, int d_v, int topk) {
   if (batch < 1 || s_next < 1 || h_q < 1 || topk < 1 || d_v != smla::kDv) return 0;
   int sms = 0;
-  if (device_setup(&sms) != SPARSE_MLA_OK) return 0;
-  return f4_plan(static_cast<long long>(batch) * s_next, h_q, topk, sms).bytes;
+  const long long n_tok = static_cast<long long>(batch) * s_next;
+  if (device_setup(&sms) != SPARSE_MLA_OK || !f4_sizes_ok(n_tok, h_q, topk)) return 0;
+  return f4_plan(n_tok, h_q, topk, sms).bytes;
 }
 
 sparse_mla_status_t sparse_mla_decode_fp4(const void* q, const void* kv_cache, const int32_t* block_table,
@@ -642,6 +651,9 @@ sparse_mla_status_t sparse_mla_decode_fp4(const void* q, const void* kv_cache, c
                                           void* workspace, size_t workspace_bytes, void* stream) {
   int sms = 0;
   if (!kv_scale_ok(kv_scale)) return SPARSE_MLA_ERR_INVALID_ARG;
+  if (batch > 0 && s_next > 0 && h_q > 0 && topk > 0 &&
+      !f4_sizes_ok(static_cast<long long>(batch) * s_next, h_q, topk))
+    return SPARSE_MLA_ERR_INVALID_ARG;
   sparse_mla_status_t st = check_decode(q, kv_cache, block_table, cache_seqlens, indices, out, lse, batch, s_next,
                                         h_q, d_qk, d_v, topk, page_size, max_blocks, num_blocks, &sms);
   if (st != SPARSE_MLA_OK) return st;
@@ -650,8 +662,6 @@ sparse_mla_status_t sparse_mla_decode_fp4(const void* q, const void* kv_cache, c
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   if (num_blocks == 0 || max_blocks == 0) return launch_fill(out, lse, n_tok * h_q, cs);
   const F4Plan f = f4_plan(n_tok, h_q, topk, sms);
-  // units and rows are counted in 32 bits
-  if (n_tok * f.groups > INT_MAX || n_tok * h_q > INT_MAX) return SPARSE_MLA_ERR_INVALID_ARG;
   if (f.bytes > 0 && (workspace_bytes < f.bytes || !workspace)) return SPARSE_MLA_ERR_WORKSPACE_TOO_SMALL;
   if (f.bytes > 0 && !aligned(workspace, 16)) return SPARSE_MLA_ERR_INVALID_ARG;
   smla::Fp4Params p;
@@ -699,6 +709,7 @@ sparse_mla_status_t check_norm(const void* q, long long q_tok_stride, long long 
                                long long kv_tok_stride, const int32_t* positions, const float* cos_sin, int n_pos,
                                const void* q_weight, const void* kv_weight, float eps, int n_tok, int h_q, int d_qk) {
   if (n_tok < 0 || h_q < 1 || n_pos < 0 || !(eps >= 0.f) || !std::isfinite(eps)) return SPARSE_MLA_ERR_INVALID_ARG;
+  if (n_tok > INT_MAX / 2 || static_cast<long long>(h_q) * 64 > INT_MAX) return SPARSE_MLA_ERR_INVALID_ARG;
   if (d_qk != smla::kRowW) return SPARSE_MLA_ERR_UNSUPPORTED_SHAPE;
   if (!row_strides_ok(q_tok_stride, q_head_stride) || !row_strides_ok(kv_tok_stride, 0))
     return SPARSE_MLA_ERR_INVALID_ARG;

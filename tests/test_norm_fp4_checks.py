@@ -93,6 +93,18 @@ def test_a_cache_factor_near_the_ends_of_fp32_is_refused(lib):
         assert _norm(lib, ks=ks) == 1 and _fp4(lib, ks=ks) == 1, ks
 
 
+def test_sizes_past_the_counters_are_refused(lib):
+    """Lists, rows and blocks whose counts would leave their integers."""
+    big = 2 ** 31 - 1
+    for bad in (dict(topk=big), dict(topk=big - 1000), dict(h=big), dict(b=big), dict(b=big, s=big),
+                dict(b=1 << 27, s=1, h=16), dict(b=1 << 27, s=1, h=8, topk=1 << 30)):
+        assert _fp4(lib, **bad) == 1, bad
+        a = dict(dict(b=2, s=3, h=8, topk=64), **bad)
+        assert lib.sparse_mla_decode_fp4_workspace_size(a["b"], a["s"], a["h"], 512, a["topk"]) == 0, bad
+    for call in (_norm, _grad):
+        assert call(lib, h=big) == 1 and call(lib, n=big) == 1
+
+
 # ------------------------------------------------------------------ binding
 
 def _args(n=5, h=3, n_pos=20):
