@@ -433,9 +433,10 @@ def _dense(t: torch.Tensor, dtype, need: int, dev) -> bool:
 
 
 class _launch_on:
-    """The stream a call launches on, with the tensors' device current
-    meanwhile (the library launches on the current device): `stream`, or the
-    current stream of that device."""
+    """The stream a call launches on, current meanwhile with its device (the
+    library launches on the current device, and what the call allocates then
+    belongs to the stream that uses it): `stream`, or the current stream of
+    the tensors' device."""
 
     __slots__ = ("device", "stream", "guard")
 
@@ -448,8 +449,11 @@ class _launch_on:
 
     def __enter__(self):
         dev = self.device
-        if dev.type == "cuda" and dev.index != torch.cuda.current_device():
+        if isinstance(self.stream, torch.cuda.Stream):
+            self.guard = torch.cuda.stream(self.stream)
+        elif dev.type == "cuda" and dev.index != torch.cuda.current_device():
             self.guard = torch.cuda.device(dev)
+        if self.guard is not None:
             self.guard.__enter__()
         if self.stream is not None:
             return self.stream.cuda_stream
@@ -461,14 +465,16 @@ class _launch_on:
 
 
 def _launch(go, dev, stream, where: str):
-    """go(stream handle) with `dev` current."""
+    """go(stream handle) -> (status, results) with `dev` and the stream current;
+    outputs and workspaces that the call allocates are made in go."""
     if stream is None and dev.index == torch._C._cuda_getDevice():
-        st = go(torch._C._cuda_getCurrentRawStream(dev.index))
+        st, results = go(torch._C._cuda_getCurrentRawStream(dev.index))
     else:
         with _launch_on(dev, stream) as cs:
-            st = go(cs)
+            st, results = go(cs)
     if st != 0:
         raise SparseMLAError(st, where)
+    return results
 
 
 def decode_fp4_workspace_size(batch: int, s_next: int, h_q: int, topk: int, d_v: int = 512) -> int:
@@ -507,12 +513,10 @@ def sparse_mla_decode_fp4(q, kv_cache, block_table, cache_seqlens, indices, sm_s
     _given(out, _BF16, "out", batch * s_next * h_q * 512, dev)
     _given(lse, _F32, "lse", batch * s_next * h_q, dev)
     _workspace(workspace, dev)
-    if out is None:
-        out = torch.empty((batch, s_next, h_q, 512), dtype=_BF16, device=dev)
-    if lse is None:
-        lse = torch.empty((batch, s_next, h_q), dtype=_F32, device=dev)
 
     def go(cs):
+        o = torch.empty((batch, s_next, h_q, 512), dtype=_BF16, device=dev) if out is None else out
+        ls = torch.empty((batch, s_next, h_q), dtype=_F32, device=dev) if lse is None else lse
         ws = workspace
         if ws is None:
             need = lib.sparse_mla_decode_fp4_workspace_size(batch, s_next, h_q, 512, topk)
@@ -521,11 +525,10 @@ def sparse_mla_decode_fp4(q, kv_cache, block_table, cache_seqlens, indices, sm_s
         ws_bytes = 0 if ws is None else ws.numel() * ws.element_size()
         return lib.sparse_mla_decode_fp4(q.data_ptr(), kv_cache.data_ptr(), block_table.data_ptr(),
                                          cache_seqlens.data_ptr(), indices.data_ptr(), sm_scale, kv_scale,
-                                         out.data_ptr(), lse.data_ptr(), batch, s_next, h_q, d_qk, 512, topk, page,
-                                         max_blocks, num_blocks, _at(ws), ws_bytes, cs)
+                                         o.data_ptr(), ls.data_ptr(), batch, s_next, h_q, d_qk, 512, topk, page,
+                                         max_blocks, num_blocks, _at(ws), ws_bytes, cs), (o, ls)
 
-    _launch(go, dev, stream, "sparse_mla_decode_fp4")
-    return out, lse
+    return _launch(go, dev, stream, "sparse_mla_decode_fp4")
 
 
 # ---------------------------------------------------------------- norms, rotation, cache write
@@ -621,19 +624,16 @@ def mla_norm_rope(q, kv, positions, cos_sin, q_weight=None, kv_weight=None, eps:
         raise ValueError("slots are given without kv_cache")
     _given(q_out, _BF16, "q_out", n * h * 576, dev)
     _given(kv_out, _BF16, "kv_out", n * 576, dev)
-    if q_out is None:
-        q_out = torch.empty((n, h, 576), dtype=_BF16, device=dev)
-    if kv_out is None:
-        kv_out = torch.empty((n, 576), dtype=_BF16, device=dev)
 
     def go(cs):
+        qo = torch.empty((n, h, 576), dtype=_BF16, device=dev) if q_out is None else q_out
+        ko = torch.empty((n, 576), dtype=_BF16, device=dev) if kv_out is None else kv_out
         return lib.mla_norm_rope(q.data_ptr(), q_tok, q_head, kv.data_ptr(), kv_tok, positions.data_ptr(),
                                  cos_sin.data_ptr(), cos_sin.shape[0], _at(q_weight), _at(kv_weight), eps,
-                                 1 if interleaved else 0, q_out.data_ptr(), kv_out.data_ptr(), _at(kv_cache), form,
-                                 kv_scale, _at(slots), n_slots, n, h, 576, cs)
+                                 1 if interleaved else 0, qo.data_ptr(), ko.data_ptr(), _at(kv_cache), form,
+                                 kv_scale, _at(slots), n_slots, n, h, 576, cs), (qo, ko)
 
-    _launch(go, dev, stream, "mla_norm_rope")
-    return q_out, kv_out
+    return _launch(go, dev, stream, "mla_norm_rope")
 
 
 def norm_rope_bwd_workspace_size(n_tok: int, h_q: int) -> int:
@@ -660,28 +660,26 @@ def mla_norm_rope_bwd(q, kv, positions, cos_sin, dq, dkv, q_weight=None, kv_weig
     _given(dq_weight, _F32, "dq_weight", 512, dev)
     _given(dkv_weight, _F32, "dkv_weight", 512, dev)
     _workspace(workspace, dev)
-    if dq_in is None:
-        dq_in = torch.empty((n, h, 576), dtype=_BF16, device=dev)
-    if dkv_in is None:
-        dkv_in = torch.empty((n, 576), dtype=_BF16, device=dev)
-    if q_weight is not None and dq_weight is None:
-        dq_weight = torch.empty(512, dtype=_F32, device=dev)
-    if kv_weight is not None and dkv_weight is None:
-        dkv_weight = torch.empty(512, dtype=_F32, device=dev)
 
     def go(cs):
+        dqi = torch.empty((n, h, 576), dtype=_BF16, device=dev) if dq_in is None else dq_in
+        dki = torch.empty((n, 576), dtype=_BF16, device=dev) if dkv_in is None else dkv_in
+        dqw, dkw = dq_weight, dkv_weight
+        if q_weight is not None and dqw is None:
+            dqw = torch.empty(512, dtype=_F32, device=dev)
+        if kv_weight is not None and dkw is None:
+            dkw = torch.empty(512, dtype=_F32, device=dev)
         ws = workspace
         if ws is None and (q_weight is not None or kv_weight is not None):
             ws = torch.empty(max(16, lib.mla_norm_rope_bwd_workspace_size(n, h)), dtype=_U8, device=dev)
         ws_bytes = 0 if ws is None else ws.numel() * ws.element_size()
         return lib.mla_norm_rope_bwd(q.data_ptr(), q_tok, q_head, kv.data_ptr(), kv_tok, positions.data_ptr(),
                                      cos_sin.data_ptr(), cos_sin.shape[0], _at(q_weight), _at(kv_weight), eps,
-                                     1 if interleaved else 0, dq.data_ptr(), dkv.data_ptr(), dq_in.data_ptr(),
-                                     dkv_in.data_ptr(), _at(dq_weight), _at(dkv_weight), n, h, 576, _at(ws),
-                                     ws_bytes, cs)
+                                     1 if interleaved else 0, dq.data_ptr(), dkv.data_ptr(), dqi.data_ptr(),
+                                     dki.data_ptr(), _at(dqw), _at(dkw), n, h, 576, _at(ws),
+                                     ws_bytes, cs), (dqi, dki, dqw, dkw)
 
-    _launch(go, dev, stream, "mla_norm_rope_bwd")
-    return dq_in, dkv_in, dq_weight, dkv_weight
+    return _launch(go, dev, stream, "mla_norm_rope_bwd")
 
 
 # ---------------------------------------------------------------- debug: valid entries per token

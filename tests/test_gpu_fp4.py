@@ -205,3 +205,34 @@ def test_workspace_streams_and_graphs(smla, h_q, s_next):
         torch.cuda.synchronize()
         for (g, r), x in zip(graphs, want):
             assert torch.equal(r[0], x[0]) and torch.equal(r[1], x[1])
+
+
+def test_a_given_stream_owns_what_the_call_allocates(smla):
+    """stream=s with the call's own outputs and workspace.  s held up: memory
+    that the current stream takes next is not the call's workspace.  The current
+    stream held up: the outputs are not memory that it has yet to write."""
+    c, u = mi.decode_case_fp4(51, batch=2, s_next=60, h_q=8, lo=2100, hi=3000, topk=2048, spare_pages=2)
+    want = _run(smla, c, u)
+    need = smla.decode_fp4_workspace_size(2, 60, 8, 2048)
+    assert need > 0
+    a = [t.to(DEV) for t in (c.q, u, c.block_table, c.cache_seqlens, c.indices)]
+    s = torch.cuda.Stream()
+
+    def nan():
+        return [torch.full((need // 4,), float("nan"), device=DEV), torch.full_like(want[0], float("nan")),
+                torch.full_like(want[1], float("nan"))]
+
+    for late in (s, torch.cuda.current_stream()):
+        smla.sparse_mla_decode_fp4(*a, c.sm_scale, stream=s)   # every block of memory is there before the streams wait
+        nan()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(late):
+            torch.cuda._sleep(100_000_000)   # some 50 ms
+        if late is not s:
+            nan()                            # written late, free at once
+        got = smla.sparse_mla_decode_fp4(*a, c.sm_scale, stream=s)
+        took = nan() if late is s else []
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        assert all(bool(torch.isnan(t).all()) for t in took)
+        del got, took
