@@ -64,7 +64,7 @@ struct Fp4Params {
   float* part_lse;             // [2 ctas, part_rows]
   int n_tok, h_q, topk, s_next, page_size, max_blocks, num_blocks;
   int groups;                  // head groups of a token
-  int nb;                      // blocks of a list (Fp4Layout::kRows entries each)
+  int nb;                      // blocks of a list (Fp4Shape::kRows entries each)
   int ctas, part_rows;
   int cluster;                 // CTAs of a unit's cluster (0: the units' blocks cut into ranges)
   float scale_log2;            // sm_scale * log2(e)
@@ -206,10 +206,13 @@ __device__ __forceinline__ void f4_scores(const uint8_t* tile, const uint4* qf, 
 // the four lanes' reads of one row each then fall into different banks.  Lane
 // (g, c) widens 64 / W neighbouring columns (all in one scale group): MMA tile
 // 4 j + t takes columns 8 j + 2 t (its row g) and 8 j + 2 t + 1 (its row g + 8) of
-// the lane's.  P of a head is stored in the order of the slots.
+// the lane's.  P of a head is stored in the order of the slots.  Masked rows are
+// zeros and take part: without a branch a tile, the next one's reads and
+// conversions start under this one's MMAs (a chunk of 512 tokens: 165 us, 172
+// with the branch).
 template <int NT, int W, int kPRow>
-__device__ __forceinline__ void f4_values(const uint8_t* stage, const __half* pf, const uint32_t* livew,
-                                          float (&o)[32 / W][NT][4], int warp, int lane) {
+__device__ __forceinline__ void f4_values(const uint8_t* stage, const __half* pf, float (&o)[32 / W][NT][4], int warp,
+                                          int lane) {
   constexpr int kWords = 8 / W;             // 8 codes each, per row
   const int g = lane >> 2, c = lane & 3;
   const uint8_t* base = stage + c * kFp4Slot;
@@ -217,7 +220,6 @@ __device__ __forceinline__ void f4_values(const uint8_t* stage, const __half* pf
   const int scale_at = kFp4ScaleAt + (code_at >> 3);
 #pragma unroll
   for (int kt = 0; kt < W; ++kt) {
-    if (livew[kt] == 0u) continue;          // no valid row in the tile
     const uint8_t* r = base + kt * kF4TileBytes;
     uint32_t w[4][kWords], s[4];
 #pragma unroll
@@ -512,10 +514,11 @@ __global__ void __launch_bounds__(L::kThreads, L::kPerSm) fp4_decode_kernel(cons
   };
   // Copies of this warp's 16 rows of a block (row r's slot is held by lane
   // 16 half + r), eight lanes a row; masked rows are zeros and are not read.
-  // Returns the rows' validity.
-  auto copy = [&](int slots, int half, int st) -> uint32_t {
+  // Returns the rows' validity.  Past the CTA's last block (live false) nothing
+  // is written: a cluster's piece may be there.
+  auto copy = [&](int slots, int half, int st, bool live) -> uint32_t {
     const uint32_t valid = (__ballot_sync(0xffffffffu, slots >= 0) >> (16 * half)) & 0xffffu;
-    if (valid != 0u) {
+    if (live) {
       const uint32_t dst = smem_u32(f4_smem + st * L::kStage + warp * kF4TileBytes);
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
@@ -548,7 +551,7 @@ __global__ void __launch_bounds__(L::kThreads, L::kPerSm) fp4_decode_kernel(cons
   slots_a = slot_n;
   look_up();
   read_entry();
-  uint32_t rows = copy(slots_a, 0, 0);   // validity of this warp's rows in block b
+  uint32_t rows = copy(slots_a, 0, 0, true);   // validity of this warp's rows in block b
   resolve();
   slots_b = slot_n;
   look_up();
@@ -655,9 +658,9 @@ __global__ void __launch_bounds__(L::kThreads, L::kPerSm) fp4_decode_kernel(cons
       for (int k = 0; k < 2; ++k) l[n][k] += e[n][k] + e[n][2 + k];
     // Block b + 1 goes where block b - 1 was.
     if ((b & 1) == 0) {
-      rows = copy(slots_a, 1, 1);
+      rows = copy(slots_a, 1, 1, b + 1 < n_blocks);
     } else {
-      rows = copy(slots_b, 0, 0);
+      rows = copy(slots_b, 0, 0, b + 1 < n_blocks);
       slots_a = slots_b;
       resolve();
       slots_b = slot_n;
@@ -665,7 +668,10 @@ __global__ void __launch_bounds__(L::kThreads, L::kPerSm) fp4_decode_kernel(cons
       read_entry();
     }
     if (b + 1 < n_blocks && j == p.nb - 1) prefetch_q(unit + 1);
-    f4_values<NT, W, L::kPRow>(stage, pb, lw, o, warp, lane);
+    uint32_t any = 0u;   // a block without a valid row adds nothing
+#pragma unroll
+    for (int w = 0; w < W; ++w) any |= lw[w];
+    if (any != 0u) f4_values<NT, W, L::kPRow>(stage, pb, o, warp, lane);
     ++j;
     if (j == p.nb || b == n_blocks - 1) {
       // End of the unit, or of this CTA's piece of it.
