@@ -98,6 +98,9 @@ struct Fp4Shape {
 using Fp4Shape8 = Fp4Shape<1, 4, 3, 16>;
 using Fp4Shape16 = Fp4Shape<2, 4, 3, 8>;
 using Fp4Shape32 = Fp4Shape<4, 8, 1, 16>;
+// 8 and 16 heads of few units: eight warps work at a unit's few blocks at once.
+using Fp4Shape8Few = Fp4Shape<1, 8, 1, 16>;
+using Fp4Shape16Few = Fp4Shape<2, 8, 1, 16>;
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -401,48 +404,75 @@ __device__ __forceinline__ void cluster_sync() {
 }
 
 // The merge of a unit whose pieces are in the shared memory of its cluster's CTAs:
-// every CTA forms all pieces' weights, then adds its share of the columns.
-// part: [heads][kF4PartRow] here and at the same place in every CTA, lse: [heads].
+// every CTA forms all pieces' weights, a lane a piece, then adds its share of the
+// columns, whose first reads are under way meanwhile (a remote read takes about
+// a microsecond).  part: [heads][kF4PartRow] here and at the same place in every
+// CTA, lse: [heads], weight: [cluster][heads].
 template <class L>
 __device__ __forceinline__ void f4_cluster_merge(const Fp4Params& p, int unit, int rank, const float* part, const float* lse,
                                                  float* weight) {
-  const int tid = static_cast<int>(threadIdx.x);
+  const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5, lane = tid & 31;
   const int tok = unit / p.groups, h0 = (unit % p.groups) * L::kHeads;
   const int heads = min(L::kHeads, p.h_q - h0);
-  for (int i = tid; i < p.cluster * L::kHeads; i += L::kThreads)
-    weight[i] = ld_cluster_f(cluster_addr(smem_u32(lse + i % L::kHeads), i / L::kHeads));
-  __syncthreads();
-  if (tid < heads) {
-    float m = -INFINITY, sum = 0.f;
-    for (int s = 0; s < p.cluster; ++s) m = fmaxf(m, weight[s * L::kHeads + tid]);
-    for (int s = 0; s < p.cluster; ++s) {
-      const float v = weight[s * L::kHeads + tid];
-      sum += v == -INFINITY ? 0.f : expf(v - m);
-    }
-    for (int s = 0; s < p.cluster; ++s) {
-      const float v = weight[s * L::kHeads + tid];
-      weight[s * L::kHeads + tid] = v == -INFINITY ? 0.f : expf(v - m) / sum;
-    }
-    if (rank == 0) p.lse[static_cast<size_t>(tok) * p.h_q + h0 + tid] = sum == 0.f ? -INFINITY : m + logf(sum);
-  }
-  __syncthreads();
   const int n = heads * (kDv / 4);   // float4 of the unit's output
   const int hi = (rank + 1) * n / p.cluster;
-  for (int i = rank * n / p.cluster + tid; i < hi; i += L::kThreads) {
+  int i = rank * n / p.cluster + tid;
+  // 8 heads: all pieces' reads of a float4 at once.  More heads: two at a time (a
+  // larger batch cost the decode loop registers: 512 tokens x 16 heads 171 us
+  // against 167), each CTA from its own piece on, so that they do not all read the
+  // same CTA's (one token, 32 heads: 17.1 and 18.3 us; 8 heads: 10.9 and 10.5).
+  constexpr int kBatch = L::NT == 1 ? kF4MaxCluster : 2;
+  auto piece = [&](int s) { return L::NT == 1 ? s : (rank + s) & (p.cluster - 1); };
+  float4 v[kBatch];
+  auto read = [&](int s0) {
+    const uint32_t at = smem_u32(part + (i / (kDv / 4)) * kF4PartRow + 4 * (i % (kDv / 4)));
+#pragma unroll
+    for (int s = 0; s < kBatch; ++s)
+      if (s0 + s < p.cluster) v[s] = ld_cluster_f4(cluster_addr(at, piece(s0 + s)));
+  };
+  if (i < hi) read(0);
+  constexpr int kMine = L::kHeads / L::W;
+  float x[kMine];
+#pragma unroll
+  for (int k = 0; k < kMine; ++k)
+    x[k] = lane < p.cluster ? ld_cluster_f(cluster_addr(smem_u32(lse + warp + k * L::W), lane)) : -INFINITY;
+#pragma unroll
+  for (int k = 0; k < kMine; ++k) {
+    const int h = warp + k * L::W;
+    float m = x[k];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const float e = x[k] == -INFINITY ? 0.f : expf(x[k] - m);
+    const float sum = warp_sum(e);
+    if (lane < p.cluster) weight[lane * L::kHeads + h] = sum == 0.f ? 0.f : e / sum;
+    if (rank == 0 && lane == 0 && h < heads)
+      p.lse[static_cast<size_t>(tok) * p.h_q + h0 + h] = sum == 0.f ? -INFINITY : m + logf(sum);
+  }
+  __syncthreads();
+  while (i < hi) {
     const int h = i / (kDv / 4), c4 = i % (kDv / 4);
-    const uint32_t at = smem_u32(part + h * kF4PartRow + 4 * c4);
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-    for (int s = 0; s < p.cluster; ++s) {
-      const float w = weight[s * L::kHeads + h];
-      const float4 v = ld_cluster_f4(cluster_addr(at, s));
-      a.x += w * v.x;
-      a.y += w * v.y;
-      a.z += w * v.z;
-      a.w += w * v.w;
+#pragma unroll
+    for (int s0 = 0; s0 < kF4MaxCluster; s0 += kBatch) {
+      if (s0 > 0) {
+        if (s0 >= p.cluster) break;
+        read(s0);
+      }
+#pragma unroll
+      for (int s = 0; s < kBatch; ++s) {
+        if (s0 + s < p.cluster) {
+          const float w = weight[piece(s0 + s) * L::kHeads + h];
+          a.x += w * v[s].x;
+          a.y += w * v[s].y;
+          a.z += w * v[s].z;
+          a.w += w * v[s].w;
+        }
+      }
     }
     *reinterpret_cast<uint2*>(p.out + (static_cast<size_t>(tok) * p.h_q + h0 + h) * kDv + 4 * c4) =
         make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
+    i += L::kThreads;
+    if (i < hi) read(0);
   }
 }
 
@@ -459,11 +489,11 @@ __global__ void __launch_bounds__(L::kThreads, L::kPerSm) fp4_decode_kernel(cons
   const int g = lane >> 2, c = lane & 3;
   asm volatile("griddepcontrol.launch_dependents;");   // the merge may be set up (it waits for this grid's end)
 
-  const long long total = static_cast<long long>(p.n_tok) * p.groups * p.nb;
-  long long x0;     // this CTA's first block, over all units' lists laid end to end
   int n_blocks, unit0, j0, rank = 0;
   if (p.cluster == 0) {
-    x0 = range_start(static_cast<int>(blockIdx.x), total, p.ctas);
+    const long long total = static_cast<long long>(p.n_tok) * p.groups * p.nb;
+    // this CTA's first block, over all units' lists laid end to end
+    const long long x0 = range_start(static_cast<int>(blockIdx.x), total, p.ctas);
     n_blocks = static_cast<int>(range_start(static_cast<int>(blockIdx.x) + 1, total, p.ctas) - x0);
     unit0 = static_cast<int>(x0 / p.nb);
     j0 = static_cast<int>(x0 % p.nb);
@@ -472,7 +502,6 @@ __global__ void __launch_bounds__(L::kThreads, L::kPerSm) fp4_decode_kernel(cons
     rank = static_cast<int>(blockIdx.x) % p.cluster;
     j0 = rank * p.nb / p.cluster;
     n_blocks = (rank + 1) * p.nb / p.cluster - j0;
-    x0 = static_cast<long long>(unit0) * p.nb + j0;
   }
 
   // The gather of this warp's rows goes by pairs of blocks: lane 16 k + r
@@ -677,9 +706,8 @@ __global__ void __launch_bounds__(L::kThreads, L::kPerSm) fp4_decode_kernel(cons
       // End of the unit, or of this CTA's piece of it.
       const int tok = unit / p.groups, h0 = (unit % p.groups) * L::kHeads;
       const int heads = min(L::kHeads, p.h_q - h0);
-      const long long ub = static_cast<long long>(unit) * p.nb;
-      const bool whole = p.cluster == 0 && range_cta(ub, total, p.ctas) == range_cta(ub + p.nb - 1, total, p.ctas);
-      const size_t slot = 2 * static_cast<size_t>(blockIdx.x) + (x0 < ub ? 1 : 0);
+      const bool whole = p.cluster == 0 && j == p.nb && (unit > unit0 || j0 == 0);
+      const size_t slot = 2 * static_cast<size_t>(blockIdx.x) + (unit > unit0 ? 1 : 0);
       // (a cluster's piece: the ring and Q are free, every warp past the barrier below is done with them)
       float* part = p.cluster > 0 ? reinterpret_cast<float*>(f4_smem) : p.part_o + slot * p.part_rows * kDv;
       float* part_lse = p.cluster > 0 ? reinterpret_cast<float*>(qbytes) : p.part_lse + slot * p.part_rows;

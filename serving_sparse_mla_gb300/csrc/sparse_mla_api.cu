@@ -28,13 +28,14 @@ std::atomic<unsigned long long> g_timeout_ns{kDefaultTimeoutNs};
 
 constexpr int kF4ClusterSizes = 4;   // 16, 8, 4 and 2 CTAs
 constexpr int kF4ClusterSlack = 192;   // list entries
+enum F4ShapeId { kF4Heads8, kF4Heads16, kF4Heads32, kF4Heads8Few, kF4Heads16Few, kF4Shapes };
 
 struct DeviceState {
   bool probed = false;
   bool supported = false;
   int sm_count = 0;
   bool attrs_set = false;
-  int f4_clusters[3][kF4ClusterSizes] = {};   // 4-bit decode, per shape: clusters held at once
+  int f4_clusters[kF4Shapes][kF4ClusterSizes] = {};   // 4-bit decode, per shape: clusters held at once
 };
 
 std::mutex g_mu;
@@ -112,9 +113,11 @@ sparse_mla_status_t device_setup(int* sm_count) {
                              smla::idx_smem_bytes()) != cudaSuccess ||
         cudaFuncSetAttribute(smla::dsa_scores_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              smla::idx_smem_bytes()) != cudaSuccess ||
-        f4_setup<smla::Fp4Shape8>(st.f4_clusters[0]) != cudaSuccess ||
-        f4_setup<smla::Fp4Shape16>(st.f4_clusters[1]) != cudaSuccess ||
-        f4_setup<smla::Fp4Shape32>(st.f4_clusters[2]) != cudaSuccess ||
+        f4_setup<smla::Fp4Shape8>(st.f4_clusters[kF4Heads8]) != cudaSuccess ||
+        f4_setup<smla::Fp4Shape16>(st.f4_clusters[kF4Heads16]) != cudaSuccess ||
+        f4_setup<smla::Fp4Shape32>(st.f4_clusters[kF4Heads32]) != cudaSuccess ||
+        f4_setup<smla::Fp4Shape8Few>(st.f4_clusters[kF4Heads8Few]) != cudaSuccess ||
+        f4_setup<smla::Fp4Shape16Few>(st.f4_clusters[kF4Heads16Few]) != cudaSuccess ||
         cudaFuncSetAttribute(smla::dsa_topk_kernel<256>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              kTopkMaxSmem) != cudaSuccess ||
         cudaFuncSetAttribute(smla::dsa_topk_kernel<1024>, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -546,13 +549,15 @@ namespace {
 // (a scale of 2^-9 .. 448 times the factor) and its reciprocal are normal.
 bool kv_scale_ok(float f) { return f >= 0x1p-64f && f <= 0x1p64f; }
 
-// The kernel's shape for a number of heads: the smallest of 8, 16 and 32 that
-// holds them (more heads are several units of 32).
 template <class F>
-auto f4_pick(int h_q, F&& f) {
-  if (h_q <= 8) return f(smla::Fp4Shape8());
-  if (h_q <= 16) return f(smla::Fp4Shape16());
-  return f(smla::Fp4Shape32());
+auto f4_with(int shape, F&& f) {
+  switch (shape) {
+    case kF4Heads8: return f(smla::Fp4Shape8());
+    case kF4Heads16: return f(smla::Fp4Shape16());
+    case kF4Heads8Few: return f(smla::Fp4Shape8Few());
+    case kF4Heads16Few: return f(smla::Fp4Shape16Few());
+    default: return f(smla::Fp4Shape32());
+  }
 }
 
 // Units, rows and list entries are counted in 32 bits (a list's last block may
@@ -563,9 +568,8 @@ bool f4_sizes_ok(long long n_tok, int h_q, int topk) {
   return blocks <= (1LL << 62) / 4096;
 }
 
-int f4_index(int h_q) { return h_q <= 8 ? 0 : (h_q <= 16 ? 1 : 2); }
-
 struct F4Plan {
+  int shape;
   int ctas, groups, rows, nb;
   int cluster;                      // CTAs per unit, merging among themselves (0: ranges)
   size_t lse_at, bytes;   // bytes from the workspace's start; bytes 0: no unit is cut
@@ -587,9 +591,8 @@ F4Plan f4_plan_of(long long n_tok, int h_q, int topk, int sms, const int* cluste
   f.lse_at = slots * smla::kDv * sizeof(float);
   // Few units: the largest cluster of which all fit at once, where that leaves a
   // CTA at most kF4ClusterSlack list entries more than an equal cut of all the work
-  // (8 heads, lists of 2048, clusters against ranges: 1 token 12.8 and 14.1 us, 16
-  // tokens 15.5 and 19.4, 96 tokens 35.2 and 37.1; at 128 tokens clusters would
-  // take 46.7 us and ranges take 42.5).
+  // (8 heads, lists of 2048, clusters against ranges: 28 tokens 17.1 and 19.9 us, 96
+  // tokens 33.5 and 37.1; at 170 tokens clusters would take 58 us and ranges take 50).
   const long long units = n_tok * f.groups;
   f.cluster = 0;
   for (int i = 0; i < kF4ClusterSizes && f.cluster == 0; ++i) {
@@ -607,11 +610,25 @@ F4Plan f4_plan_of(long long n_tok, int h_q, int topk, int sms, const int* cluste
   return f;
 }
 
+// The smallest of 8, 16 and 32 heads that holds h_q (more are several units of
+// 32).  At 8 and 16 heads the eight-warp shape where it leaves a CTA at most 256
+// list entries (512 at 16 heads), else three CTAs of four warps per
+// SM (lists of 2048, eight warps against four; 8 heads: 1 token 9.0 and 10.5 us, 12
+// tokens 11.1 and 13.0, 28 tokens 17.7 and 17.1; 16 heads: 1 token 11.9 and 14.3,
+// 16 tokens 15.8 and 20.6, 32 tokens 21.3 and 23.3, 48 tokens 29.8 and 29.6).
 F4Plan f4_plan(long long n_tok, int h_q, int topk, int sms) {
   int dev = 0;
-  const int* clusters = cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < kMaxDevices ? g_dev[dev].f4_clusters[f4_index(h_q)]
-                                                                                           : g_dev[0].f4_clusters[0];
-  return f4_pick(h_q, [&](auto shape) { return f4_plan_of<decltype(shape)>(n_tok, h_q, topk, sms, clusters); });
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) dev = 0;
+  auto plan = [&](int shape) {
+    F4Plan f = f4_with(shape, [&](auto c) { return f4_plan_of<decltype(c)>(n_tok, h_q, topk, sms, g_dev[dev].f4_clusters[shape]); });
+    f.shape = shape;
+    return f;
+  };
+  if (h_q > 16) return plan(kF4Heads32);
+  const F4Plan few = plan(h_q <= 8 ? kF4Heads8Few : kF4Heads16Few);
+  const long long entries = few.cluster > 0 ? topk : n_tok * topk;   // of a cluster, of the grid
+  if (entries <= (h_q <= 8 ? 256LL : 512LL) * (few.cluster > 0 ? few.cluster : few.ctas)) return few;
+  return plan(h_q <= 8 ? kF4Heads8 : kF4Heads16);
 }
 
 template <class C>
@@ -692,7 +709,7 @@ sparse_mla_status_t sparse_mla_decode_fp4(const void* q, const void* kv_cache, c
     p.part_o = reinterpret_cast<float*>(ws);
     p.part_lse = reinterpret_cast<float*>(ws + f.lse_at);
   }
-  const cudaError_t e = f4_pick(h_q, [&](auto shape) { return f4_launch<decltype(shape)>(p, cs); });
+  const cudaError_t e = f4_with(f.shape, [&](auto c) { return f4_launch<decltype(c)>(p, cs); });
   return e == cudaSuccess ? SPARSE_MLA_OK : SPARSE_MLA_ERR_CUDA;
 }
 

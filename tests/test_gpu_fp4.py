@@ -166,7 +166,7 @@ def test_queries_of_any_size(smla, h_q):
         assert torch.equal(o, o2) and torch.equal(l, l2)
 
 
-@pytest.mark.parametrize("h_q,s_next", [(8, 2), (64, 2), (8, 60), (64, 60)])
+@pytest.mark.parametrize("h_q,s_next", [(8, 2), (64, 2), (8, 90), (64, 90)])
 def test_workspace_streams_and_graphs(smla, h_q, s_next):
     """A dirty workspace of exactly the size asked for (few tokens ask for none:
     their pieces meet in a cluster); two decodes on two streams with their own
@@ -175,7 +175,7 @@ def test_workspace_streams_and_graphs(smla, h_q, s_next):
              for k in range(2)]
     want = [_run(smla, c, u) for c, u in cases]
     need = smla.decode_fp4_workspace_size(2, s_next, h_q, 2048)
-    assert need > 0 if s_next == 60 else (need == 0 or h_q > 8)
+    assert need > 0 if s_next == 90 else (need == 0 or h_q > 8)
     ws = [torch.full((max(need, 16),), 0xFF, dtype=torch.uint8, device=DEV) for _ in cases]
     args = [([t.to(DEV) for t in (c.q, u, c.block_table, c.cache_seqlens, c.indices)], c.sm_scale) for c, u in cases]
     if need:
@@ -211,9 +211,9 @@ def test_a_given_stream_owns_what_the_call_allocates(smla):
     """stream=s with the call's own outputs and workspace.  s held up: memory
     that the current stream takes next is not the call's workspace.  The current
     stream held up: the outputs are not memory that it has yet to write."""
-    c, u = mi.decode_case_fp4(51, batch=2, s_next=60, h_q=8, lo=2100, hi=3000, topk=2048, spare_pages=2)
+    c, u = mi.decode_case_fp4(51, batch=2, s_next=90, h_q=8, lo=2100, hi=3000, topk=2048, spare_pages=2)
     want = _run(smla, c, u)
-    need = smla.decode_fp4_workspace_size(2, 60, 8, 2048)
+    need = smla.decode_fp4_workspace_size(2, 90, 8, 2048)
     assert need > 0
     a = [t.to(DEV) for t in (c.q, u, c.block_table, c.cache_seqlens, c.indices)]
     s = torch.cuda.Stream()
