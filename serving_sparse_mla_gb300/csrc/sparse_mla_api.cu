@@ -599,8 +599,11 @@ F4Plan f4_plan_of(long long n_tok, int h_q, int topk, int sms, const int* cluste
     const int c = smla::kF4MaxCluster >> i;
     if (c <= f.nb && units <= clusters[i] && (f.nb + c - 1) / c <= units * f.nb / most + kF4ClusterSlack / C::kRows) f.cluster = c;
   }
-  if (f.cluster > 0) {
-    f.ctas = static_cast<int>(units) * f.cluster;
+  // Short lists: by the same rule a CTA takes a whole list (300 lists of 256, 8
+  // heads: 16.2 us, cut into ranges 24.2).
+  const bool own = units <= most && f.nb <= units * f.nb / most + kF4ClusterSlack / C::kRows;
+  if (f.cluster > 0 || own) {
+    f.ctas = static_cast<int>(units) * (f.cluster > 0 ? f.cluster : 1);
     f.lse_at = f.bytes = 0;
     return f;
   }
@@ -611,11 +614,13 @@ F4Plan f4_plan_of(long long n_tok, int h_q, int topk, int sms, const int* cluste
 }
 
 // The smallest of 8, 16 and 32 heads that holds h_q (more are several units of
-// 32).  At 8 and 16 heads the eight-warp shape where it leaves a CTA at most 256
-// list entries (512 at 16 heads), else three CTAs of four warps per
-// SM (lists of 2048, eight warps against four; 8 heads: 1 token 9.0 and 10.5 us, 12
-// tokens 11.1 and 13.0, 28 tokens 17.7 and 17.1; 16 heads: 1 token 11.9 and 14.3,
-// 16 tokens 15.8 and 20.6, 32 tokens 21.3 and 23.3, 48 tokens 29.8 and 29.6).
+// 32), three CTAs of four warps per SM at 8 and 16 heads.  Few tokens: CTAs of
+// eight warps and units of at most 16 heads, where that leaves a CTA at most 256
+// list entries (512 at 9 to 16 heads).  Lists of 2048, few against the other; 8
+// heads: 1 token 8.9 and 10.5 us, 12 tokens 11.2 and 13.0, 28 tokens 17.7 and 17.1;
+// 16 heads: 1 token 11.9 and 14.3, 16 tokens 15.5 and 20.6, 48 tokens 29.8 and
+// 29.6; 32 heads: 1 token 12.0 and 17.2, 8 tokens 15.6 and 17.3, 24 tokens 28.1
+// and 26.8.
 F4Plan f4_plan(long long n_tok, int h_q, int topk, int sms) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) dev = 0;
@@ -624,11 +629,11 @@ F4Plan f4_plan(long long n_tok, int h_q, int topk, int sms) {
     f.shape = shape;
     return f;
   };
-  if (h_q > 16) return plan(kF4Heads32);
   const F4Plan few = plan(h_q <= 8 ? kF4Heads8Few : kF4Heads16Few);
-  const long long entries = few.cluster > 0 ? topk : n_tok * topk;   // of a cluster, of the grid
-  if (entries <= (h_q <= 8 ? 256LL : 512LL) * (few.cluster > 0 ? few.cluster : few.ctas)) return few;
-  return plan(h_q <= 8 ? kF4Heads8 : kF4Heads16);
+  const long long entries = few.cluster > 0 ? topk : n_tok * few.groups * topk;   // of a cluster, of the grid
+  const long long limit = h_q > 8 && h_q <= 16 ? 512 : 256;
+  if (n_tok * few.groups <= few.ctas && entries <= limit * (few.cluster > 0 ? few.cluster : few.ctas)) return few;
+  return plan(h_q <= 8 ? kF4Heads8 : (h_q <= 16 ? kF4Heads16 : kF4Heads32));
 }
 
 template <class C>
