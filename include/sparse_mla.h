@@ -281,7 +281,8 @@ typedef enum {
  * into its cache slot, in one pass.  A row x has 512 latent values a and 64
  * rotated values r:
  *
- *   a' = a * rsqrt(mean(a^2) + eps) * weight      (no weight: a' = a)
+ *   a' = a * rsqrt(mean(a^2) + eps) * weight      (no weight: a' = a; a normed
+ *        row's mean(a^2) + eps has to be a normal fp32 number)
  *   r' = r turned by its position's angles: plane i has cos_sin[pos][i] and
  *        cos_sin[pos][32 + i], and is values (2i, 2i + 1) of r when
  *        `interleaved`, else values (i, i + 32):

@@ -12,7 +12,14 @@
 // One warp takes one row: 8 values of either half of the latent part per lane
 // (two 16-byte loads, each 512 contiguous bytes per warp) and one 4-byte pair
 // of the rotated part, so that a row is read once and written once and every
-// statistic is a warp reduction.
+// statistic is a warp reduction.  Both directions are bound by memory: 8192
+// tokens x 64 heads take 185 us forward (1.23 GB, 6640 GB/s, 0.98 of the rate
+// measured for a copy) and 363 us backward (2.46 GB, 6760 GB/s, 0.995); 2119 x 8
+// takes 11.9 and 20.6 us (3840 and 4290 GB/s: a launch's start and end are 4 us of
+// it); one token 3.4 us, a launch.
+//
+// Squares are summed as fp32 numbers: a row whose mean square leaves fp32's
+// range is outside of what the norm is made for.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
