@@ -87,6 +87,43 @@ def test_every_split_of_the_lists(smla, h_q, tokens, topk):
     _check(smla, c, u, f"fp4 decode {tokens} tokens, {topk} entries h={h_q}")
 
 
+@pytest.mark.parametrize("h_q", [8, 16, 40])
+@pytest.mark.parametrize("tokens,topk", [(1, 9000), (3, 5000), (150, 256), (300, 100)])
+def test_lists_longer_and_shorter_than_usual(smla, h_q, tokens, topk):
+    """Few long lists (ranges of at most 64 pieces a list) and many short ones
+    (a list a CTA)."""
+    c, u = mi.decode_case_fp4(1200 + tokens, batch=1, s_next=tokens, h_q=h_q, lo=9500, hi=9500, topk=topk, page=64,
+                              spare_pages=2)
+    _check(smla, c, u, f"fp4 decode {tokens} tokens, {topk} entries h={h_q}")
+
+
+@pytest.mark.parametrize("h_q", [8, 16, 40])
+@pytest.mark.parametrize("tokens,topk", [(4, 700), (40, 700), (300, 300), (300, 700)])
+def test_masked_tiles_blocks_and_tokens(smla, h_q, tokens, topk):
+    """-1 in single entries, in 16-entry tiles, in whole blocks and in whole
+    lists, wherever the lists are cut; unnamed slots hold NaN scales."""
+    c, u = mi.decode_case_fp4(1300 + tokens, batch=1, s_next=tokens, h_q=h_q, lo=1500, hi=1500, topk=topk, page=64,
+                              spare_pages=2)
+    g = torch.Generator().manual_seed(tokens + topk)
+    i = c.indices[0]
+    i[torch.rand(tokens, topk, generator=g) < 0.2] = -1
+    tile = torch.rand(tokens, (topk + 15) // 16, generator=g) < 0.3
+    i[tile.repeat_interleave(16, 1)[:, :topk]] = -1
+    block = torch.rand(tokens, (topk + 127) // 128, generator=g) < 0.4
+    i[block.repeat_interleave(128, 1)[:, :topk]] = -1
+    i[torch.rand(tokens, generator=g) < 0.2] = -1
+    i[0] = -1
+    named = i[i >= 0].long()
+    slot = c.block_table[0, named // 64].long() * 64 + named % 64
+    keep = torch.zeros(u.shape[0] * 64, dtype=torch.bool)
+    keep[slot] = True
+    u.view(-1, 416)[~keep, 256:288] = 0x7F
+    _check(smla, c, u, f"fp4 decode masked {tokens} tokens, {topk} entries h={h_q}")
+    out, lse = _run(smla, c, u)
+    empty = (i < 0).all(1)
+    assert bool((out[0, empty] == 0).all()) and bool(torch.isneginf(lse[0, empty]).all())
+
+
 @pytest.mark.parametrize("h_q", [8, 16, 64])
 def test_many_tokens_of_one_request(smla, h_q):
     """More units than CTAs, so that a CTA works through several."""
