@@ -49,7 +49,7 @@
 // each an equal part of its list, and merges through distributed shared memory.
 // Many: as in the paged forward (block ranges, fwd_kernel.cuh), the units' lists
 // laid end to end and cut into one equal range per CTA; a second kernel merges
-// the pieces of cut units.
+// the pieces of cut units.  With as many CTAs as units the ranges are whole lists.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -105,8 +105,8 @@ struct Fp4Shape {
 };
 // 8 and 16 heads: three CTAs of four warps per SM; at 16 P's rows keep an 8-value
 // pad (two-way bank conflicts on its few reads), which is what makes three fit.
-// 32 heads: one CTA of eight warps, half of the sums per thread (84.7 us at 128
-// lists of 2048 against 92.8 us for two CTAs of four warps, which spill).
+// 32 heads: one CTA of eight warps, half of the sums per thread (82 us at 128
+// lists of 2048 against 93 us for two CTAs of four warps, which spill).
 using Fp4Shape8 = Fp4Shape<1, 4, 3, 16>;
 using Fp4Shape16 = Fp4Shape<2, 4, 3, 8>;
 using Fp4Shape32 = Fp4Shape<4, 8, 1, 16>;
