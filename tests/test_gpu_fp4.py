@@ -124,6 +124,21 @@ def test_masked_tiles_blocks_and_tokens(smla, h_q, tokens, topk):
     assert bool((out[0, empty] == 0).all()) and bool(torch.isneginf(lse[0, empty]).all())
 
 
+@pytest.mark.parametrize("h_q", [8, 24])
+@pytest.mark.parametrize("page", [1, 7, 48])
+def test_repeated_entries_and_odd_pages(smla, h_q, page):
+    """An entry counts once for every time it is listed (a list of one entry
+    only among them); pages of 1, 7 and 48 slots, requests that share pages."""
+    c, u = mi.decode_case_fp4(1400 + page, batch=3, s_next=2, h_q=h_q, lo=100, hi=400, topk=90, page=page, spare_pages=3)
+    c.indices[0, 0, 45:] = c.indices[0, 0, :45]
+    c.indices[0, 1, :] = c.indices[0, 1, 0]
+    c.indices[1, 0, 3:30] = c.indices[1, 0, 2]
+    c.indices[2] = c.indices[1]
+    c.cache_seqlens[2] = c.cache_seqlens[1]
+    c.block_table[2] = c.block_table[1]
+    _check(smla, c, u, f"fp4 decode repeated entries h={h_q} page={page}")
+
+
 @pytest.mark.parametrize("h_q", [8, 16, 64])
 def test_many_tokens_of_one_request(smla, h_q):
     """More units than CTAs, so that a CTA works through several."""
