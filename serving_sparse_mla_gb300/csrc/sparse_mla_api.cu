@@ -35,7 +35,8 @@ struct DeviceState {
   bool supported = false;
   int sm_count = 0;
   bool attrs_set = false;
-  int f4_clusters[kF4Shapes][kF4ClusterSizes] = {};   // 4-bit decode, per shape: clusters held at once
+  bool f4_set = false;                                // the 4-bit decode's kernels, set up with its first call
+  int f4_clusters[kF4Shapes][kF4ClusterSizes] = {};   // per shape: clusters held at once
 };
 
 std::mutex g_mu;
@@ -59,19 +60,29 @@ void f4_cluster_config(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attr, int c
 }
 
 // Kernel attributes of a shape, and how many of its clusters of 16, 8, 4 and 2 CTAs
-// the device holds at once.
+// the device holds at once: none of a size that it refuses (16 is past what every
+// device takes, and a part of a device may take less).
 template <class C>
-cudaError_t f4_setup(int* clusters) {
-  cudaError_t e = cudaFuncSetAttribute(smla::fp4_decode_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kBytes);
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(smla::fp4_decode_kernel<C>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-  for (int i = 0; i < kF4ClusterSizes && e == cudaSuccess; ++i) {
-    const int c = smla::kF4MaxCluster >> i;
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr = {};
-    f4_cluster_config<C>(&cfg, &attr, c, c);
-    e = cudaOccupancyMaxActiveClusters(&clusters[i], smla::fp4_decode_kernel<C>, &cfg);
+bool f4_setup(int* clusters) {
+  bool refused = false;
+  const bool ok = cudaFuncSetAttribute(smla::fp4_decode_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       C::kBytes) == cudaSuccess;
+  if (ok) {
+    refused = cudaFuncSetAttribute(smla::fp4_decode_kernel<C>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) !=
+              cudaSuccess;
+    for (int i = 0; i < kF4ClusterSizes; ++i) {
+      const int c = smla::kF4MaxCluster >> i;
+      cudaLaunchConfig_t cfg = {};
+      cudaLaunchAttribute attr = {};
+      f4_cluster_config<C>(&cfg, &attr, c, c);
+      if (cudaOccupancyMaxActiveClusters(&clusters[i], smla::fp4_decode_kernel<C>, &cfg) != cudaSuccess) {
+        clusters[i] = 0;
+        refused = true;
+      }
+    }
   }
-  return e;
+  if (!ok || refused) cudaGetLastError();   // not the next launch's error
+  return ok;
 }
 
 sparse_mla_status_t device_setup(int* sm_count) {
@@ -113,11 +124,6 @@ sparse_mla_status_t device_setup(int* sm_count) {
                              smla::idx_smem_bytes()) != cudaSuccess ||
         cudaFuncSetAttribute(smla::dsa_scores_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              smla::idx_smem_bytes()) != cudaSuccess ||
-        f4_setup<smla::Fp4Shape8>(st.f4_clusters[kF4Heads8]) != cudaSuccess ||
-        f4_setup<smla::Fp4Shape16>(st.f4_clusters[kF4Heads16]) != cudaSuccess ||
-        f4_setup<smla::Fp4Shape32>(st.f4_clusters[kF4Heads32]) != cudaSuccess ||
-        f4_setup<smla::Fp4Shape8Few>(st.f4_clusters[kF4Heads8Few]) != cudaSuccess ||
-        f4_setup<smla::Fp4Shape16Few>(st.f4_clusters[kF4Heads16Few]) != cudaSuccess ||
         cudaFuncSetAttribute(smla::dsa_topk_kernel<256>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              kTopkMaxSmem) != cudaSuccess ||
         cudaFuncSetAttribute(smla::dsa_topk_kernel<1024>, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -127,6 +133,22 @@ sparse_mla_status_t device_setup(int* sm_count) {
   }
   *sm_count = st.sm_count;
   return SPARSE_MLA_OK;
+}
+
+// The 4-bit decode's kernels, apart from device_setup (which comes first): what a
+// device refuses of them stops no other call.
+sparse_mla_status_t f4_device_setup() {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return SPARSE_MLA_ERR_CUDA;
+  std::lock_guard<std::mutex> lock(g_mu);
+  DeviceState& st = g_dev[dev];
+  if (!st.f4_set)
+    st.f4_set = f4_setup<smla::Fp4Shape8>(st.f4_clusters[kF4Heads8]) &&
+                f4_setup<smla::Fp4Shape16>(st.f4_clusters[kF4Heads16]) &&
+                f4_setup<smla::Fp4Shape32>(st.f4_clusters[kF4Heads32]) &&
+                f4_setup<smla::Fp4Shape8Few>(st.f4_clusters[kF4Heads8Few]) &&
+                f4_setup<smla::Fp4Shape16Few>(st.f4_clusters[kF4Heads16Few]);
+  return st.f4_set ? SPARSE_MLA_OK : SPARSE_MLA_ERR_CUDA;
 }
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
@@ -662,7 +684,7 @@ size_t sparse_mla_decode_fp4_workspace_size(int batch, int s_next, int h_q, int 
   if (batch < 1 || s_next < 1 || h_q < 1 || topk < 1 || d_v != smla::kDv) return 0;
   int sms = 0;
   const long long n_tok = static_cast<long long>(batch) * s_next;
-  if (device_setup(&sms) != SPARSE_MLA_OK || !f4_sizes_ok(n_tok, h_q, topk)) return 0;
+  if (!f4_sizes_ok(n_tok, h_q, topk) || device_setup(&sms) != SPARSE_MLA_OK || f4_device_setup() != SPARSE_MLA_OK) return 0;
   return f4_plan(n_tok, h_q, topk, sms).bytes;
 }
 
@@ -683,6 +705,7 @@ sparse_mla_status_t sparse_mla_decode_fp4(const void* q, const void* kv_cache, c
   if (n_tok == 0) return SPARSE_MLA_OK;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   if (num_blocks == 0 || max_blocks == 0) return launch_fill(out, lse, n_tok * h_q, cs);
+  if ((st = f4_device_setup()) != SPARSE_MLA_OK) return st;
   const F4Plan f = f4_plan(n_tok, h_q, topk, sms);
   if (f.bytes > 0 && (workspace_bytes < f.bytes || !workspace)) return SPARSE_MLA_ERR_WORKSPACE_TOO_SMALL;
   if (f.bytes > 0 && !aligned(workspace, 16)) return SPARSE_MLA_ERR_INVALID_ARG;
