@@ -27,11 +27,11 @@
 // code * scale is exact in f16.  Q is brought to f16 by a power of two per
 // head (bf16 has 8 significant bits; values below 2^-14 of the head's largest
 // lose bits below 2^-25 of it, the size of an fp32 sum's own rounding).  P is
-// f16: 11 bits down to 2^-14 of the running maximum's weight, steps of 2^-24
-// below, so that a list of n rows loses at most n 2^-25 of a value's size (2048
-// rows: 6e-5, where bf16's rounding of the output is 2e-3); its sum is taken from
-// the unrounded weights.  The rotated part stays bf16 (its own MMAs).  All sums
-// are fp32.
+// f16 with the running maximum's weight at 2^kF4PBits: 11 bits down to 2^-21 of that
+// weight, steps of 2^-31 below, so that a list of n rows loses at most n 2^-32 of a
+// value's size (2^18 rows: 6e-5, where bf16's rounding of the output is 2e-3); its
+// sum is taken from the unrounded weights.  The rotated part stays bf16 (its own
+// MMAs).  All sums are fp32.
 //
 // What bounds it: the instructions that widen codes.  Per 16 rows a warp issues
 // about 1100 (8 heads), of which 256 are conversions, 256 multiplications by the
@@ -62,6 +62,9 @@ namespace smla {
 
 constexpr int kF4TileBytes = 16 * kFp4Slot;   // one warp's 16 rows
 constexpr int kF4MaxCluster = 16;
+// P = 2^kF4PBits exp(s - maximum), and a score may pass the maximum by 2^8 before that
+// moves: below 2^15, inside f16's range.
+constexpr int kF4PBits = 7;
 constexpr int kF4PartRow = kDv + 8;           // floats of one head's piece in shared memory (the 8 spread the banks)
 
 struct Fp4Params {
@@ -599,7 +602,7 @@ __global__ void __launch_bounds__(L::kThreads, L::kPerSm) fp4_decode_kernel(cons
   read_entry();
 
   float o[32 / W][NT][4];
-  float m[NT][2], l[NT][2], f[NT][2];   // heads 8 n + 2 c + k: maximum (of the CTA), this lane's share of the sum
+  float m[NT][2], l[NT][2], f[NT][2];   // heads 8 n + 2 c + k: maximum (of the CTA) less kF4PBits, this lane's share of the sum
   int unit = unit0, j = j0;
 #pragma unroll 1
   for (int b = 0; b < n_blocks; ++b) {
@@ -636,14 +639,15 @@ __global__ void __launch_bounds__(L::kThreads, L::kPerSm) fp4_decode_kernel(cons
     const bool v0 = (mask >> rho) & 1u, v1 = (mask >> (rho + 8)) & 1u;
     if (mask != 0u) f4_scores<NT>(stage + warp * kF4TileBytes, reinterpret_cast<const uint4*>(qbytes), s, lane, p.kv_scale);
     // Scores in log2 units; a maximum moves only when a score passes it by
-    // 2^8 (P stays far inside f16's range), always with a unit's first rows.
+    // 2^8, always with a unit's first rows.  (The difference is exact where it matters;
+    // a sum m + 15 would be rounded to the step of large scores, and P pass f16's range.)
     bool need = false;
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         s[n][i] = (i < 2 ? v0 : v1) ? s[n][i] * f[n][i & 1] : -INFINITY;
-        need |= s[n][i] > m[n][i & 1] + 8.0f;
+        need |= s[n][i] - m[n][i & 1] > 8.0f + kF4PBits;
       }
     // P of row r of this warp's tile sits at 16 warp + 4 (r % 4) + r / 4
     const int at = 16 * warp + 4 * (rho & 3) + (rho >> 2);
@@ -680,7 +684,7 @@ __global__ void __launch_bounds__(L::kThreads, L::kPerSm) fp4_decode_kernel(cons
         for (int k = 0; k < 2; ++k) {
           float mn = m[n][k];
 #pragma unroll
-          for (int w = 0; w < W; ++w) mn = fmaxf(mn, red[w * L::kHeads + 8 * n + 2 * c + k]);
+          for (int w = 0; w < W; ++w) mn = fmaxf(mn, red[w * L::kHeads + 8 * n + 2 * c + k] - kF4PBits);
           const float a = m[n][k] == mn ? 1.f : fast_exp2(m[n][k] - mn);
           m[n][k] = mn;
           l[n][k] *= a;
