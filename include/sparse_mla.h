@@ -248,7 +248,9 @@ sparse_mla_status_t sparse_mla_decode_fp8(const void* q, const void* kv_cache, c
  *
  * The row the attention uses is code * scale * kv_scale (d < 512) and the rope
  * values.  code * scale is exact in the kernel; a NaN scale (0x7F, 0xFF) gives
- * NaN.  mla_norm_rope writes such slots.
+ * NaN.  mla_norm_rope writes such slots.  Of a head's 512 latent query values,
+ * those below 2^-17 of the largest one lose bits below 2^-25 of that; the 64
+ * rotated ones are taken as they are.
  *
  *   kv_cache      uint8 [num_blocks, page_size, 416], 16-byte aligned
  *   kv_scale      one factor for the whole cache (1 for none), in [2^-64, 2^64]

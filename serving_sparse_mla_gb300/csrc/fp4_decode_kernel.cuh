@@ -24,9 +24,11 @@
 //                                                    instructions per 8 codes
 //
 // e2m1 * e4m3 has at most 6 significant bits and lies in [2^-10, 2688], so
-// code * scale is exact in f16.  Q is brought to f16 by a power of two per
-// head (bf16 has 8 significant bits; values below 2^-14 of the head's largest
-// lose bits below 2^-25 of it, the size of an fp32 sum's own rounding).  P is
+// code * scale is exact in f16.  Q's latent part is brought to f16 by a power of two
+// per head, from its own largest value (bf16 has 8 significant bits: values down to
+// 2^-17 of that are exact, smaller ones lose bits below 2^-25 of it; the score is off
+// by at most 2^-25 max |q| sum |x|).  The latent score takes that power and kv_scale,
+// then the rotated part is added, whose Q is as it came.  P is
 // f16 with the running maximum's weight at 2^kF4PBits: 11 bits down to 2^-21 of that
 // weight, steps of 2^-31 below, so that a list of n rows loses at most n 2^-32 of a
 // value's size (2^18 rows: 6e-5, where bf16's rounding of the output is 2e-3); its
@@ -140,7 +142,7 @@ __device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t v) {
   return h;
 }
 
-// S^T of this warp's 16 rows, times 2^-e (f4_load_q).  The MMA's row g is row
+// S^T of this warp's 16 rows; f: the heads' 2^e (f4_load_q).  The MMA's row g is row
 // rho(g) = g with bits 0 and 1 swapped, so that the two rows a quarter of a
 // warp reads together lie 832 bytes apart: their 16-byte reads fall into
 // different banks (416-byte rows step by 8 of 32 banks).  Lane (g, c) owns
@@ -150,7 +152,7 @@ __device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t v) {
 // dependent MMAs apart.
 template <int NT>
 __device__ __forceinline__ void f4_scores(const uint8_t* tile, const uint4* qf, float (&acc)[NT][4], int lane,
-                                          float kv_scale) {
+                                          float kv_scale, const float (&f)[NT][2]) {
   const int g = lane >> 2, c = lane & 3;
   const int rho = (g & 4) | ((g & 1) << 1) | ((g >> 1) & 1);
   const uint8_t* row0 = tile + rho * kFp4Slot;
@@ -191,12 +193,13 @@ __device__ __forceinline__ void f4_scores(const uint8_t* tile, const uint4* qf, 
       }
     }
   }
-  // the rotated part (bf16), after the latent part took kv_scale
+  // the rotated part (bf16), after the latent part took kv_scale and 2^e (one after the
+  // other: their product may leave fp32's range where the score does not)
 #pragma unroll
   for (int n = 0; n < NT; ++n)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      acc[n][i] = (acc[n][i] + alt[n][i]) * kv_scale;
+      acc[n][i] = (acc[n][i] + alt[n][i]) * kv_scale * f[n][i & 1];
       alt[n][i] = 0.f;
     }
 #pragma unroll
@@ -273,9 +276,9 @@ __device__ __forceinline__ void f4_values(const uint8_t* stage, const __half* pf
   }
 }
 
-// Q of a unit: a warp brings every W-th head to f16 / bf16 by 2^-e (the
-// exponent of the head's largest value) and stores them as MMA fragments;
-// qscale[h] = sm_scale log2(e) 2^e.  Heads past h_q are zero.
+// Q of a unit: a warp brings every W-th head's latent part to f16 by 2^-e (the exponent
+// of its largest value), leaves the rotated part in bf16 and stores both as MMA
+// fragments; qscale[h] = 2^e.  Heads past h_q are zero.
 template <int NT, int W>
 __device__ __forceinline__ void f4_load_q(const Fp4Params& p, int unit, uint8_t* qbytes, float* qscale, int warp,
                                           int lane) {
@@ -297,7 +300,7 @@ __device__ __forceinline__ void f4_load_q(const Fp4Params& p, int unit, uint8_t*
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         if (!live) x[k][i] = 0.f;
-        top = fmaxf(top, fabsf(x[k][i]));
+        if (k < 2) top = fmaxf(top, fabsf(x[k][i]));
       }
     }
 #pragma unroll
@@ -305,7 +308,7 @@ __device__ __forceinline__ void f4_load_q(const Fp4Params& p, int unit, uint8_t*
     int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;
     e = top > 0.f && top <= 3.402823466e38f ? min(max(e, -126), 126) : 0;
     const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-    if (lane == 0) qscale[hl] = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+    if (lane == 0) qscale[hl] = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
     // values 8 x .. 8 x + 7 (x = lane or 32 + lane) are word j of chunk i of
     // owner c; the owner's iteration i0 has (i0 + c) % 4 = i
 #pragma unroll
@@ -323,10 +326,7 @@ __device__ __forceinline__ void f4_load_q(const Fp4Params& p, int unit, uint8_t*
     }
     if (lane < 8) {   // rotated part: piece `lane` belongs to owner c = lane / 2, half kh with (kh + c / 2) % 2 = lane % 2
       const int c = lane >> 1, kh = (lane + (c >> 1)) & 1;
-      float y[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] = x[2][i] * down;
-      *reinterpret_cast<uint4*>(qbytes + (((16 + kh) * NT + n) * 32 + 4 * g + c) * 16) = pack8(y);
+      *reinterpret_cast<uint4*>(qbytes + (((16 + kh) * NT + n) * 32 + 4 * g + c) * 16) = pack8(x[2]);
     }
   }
 }
@@ -602,7 +602,7 @@ __global__ void __launch_bounds__(L::kThreads, L::kPerSm) fp4_decode_kernel(cons
   read_entry();
 
   float o[32 / W][NT][4];
-  float m[NT][2], l[NT][2], f[NT][2];   // heads 8 n + 2 c + k: maximum (of the CTA) less kF4PBits, this lane's share of the sum
+  float m[NT][2], l[NT][2], f[NT][2];   // heads 8 n + 2 c + k: maximum (of the CTA) less kF4PBits, this lane's share of the sum, 2^e
   int unit = unit0, j = j0;
 #pragma unroll 1
   for (int b = 0; b < n_blocks; ++b) {
@@ -637,7 +637,7 @@ __global__ void __launch_bounds__(L::kThreads, L::kPerSm) fp4_decode_kernel(cons
     const uint32_t mask = rows;
     const int rho = (g & 4) | ((g & 1) << 1) | ((g >> 1) & 1);
     const bool v0 = (mask >> rho) & 1u, v1 = (mask >> (rho + 8)) & 1u;
-    if (mask != 0u) f4_scores<NT>(stage + warp * kF4TileBytes, reinterpret_cast<const uint4*>(qbytes), s, lane, p.kv_scale);
+    if (mask != 0u) f4_scores<NT>(stage + warp * kF4TileBytes, reinterpret_cast<const uint4*>(qbytes), s, lane, p.kv_scale, f);
     // Scores in log2 units; a maximum moves only when a score passes it by
     // 2^8, always with a unit's first rows.  (The difference is exact where it matters;
     // a sum m + 15 would be rounded to the step of large scores, and P pass f16's range.)
@@ -646,7 +646,7 @@ __global__ void __launch_bounds__(L::kThreads, L::kPerSm) fp4_decode_kernel(cons
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        s[n][i] = (i < 2 ? v0 : v1) ? s[n][i] * f[n][i & 1] : -INFINITY;
+        s[n][i] = (i < 2 ? v0 : v1) ? s[n][i] * p.scale_log2 : -INFINITY;
         need |= s[n][i] - m[n][i & 1] > 8.0f + kF4PBits;
       }
     // P of row r of this warp's tile sits at 16 warp + 4 (r % 4) + r / 4

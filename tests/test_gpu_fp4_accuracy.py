@@ -67,6 +67,29 @@ def _check(smla, c, u, ks):
         assert not bad.any(), f"{int(bad.sum())} outputs off, worst {(np.abs(o[t] - ref) / tol).max():.2f} of the bound"
 
 
+@pytest.mark.parametrize("h_q", [8, 12, 24, 64])
+@pytest.mark.parametrize("ks", [2.0 ** 16, 2.0 ** 20, 2.0 ** 24, 2.0 ** -24, 2.0 ** 60, 2.0 ** -60])
+def test_latent_queries_that_make_up_for_the_factor(smla, h_q, ks):
+    """Latent rows of size ks, latent queries of size 1 / ks, rotated parts of
+    size 1: scores as ever.  The latent part's exponent is its own."""
+    c, u = mi.decode_case_fp4(1500 + h_q, batch=3, s_next=2, h_q=h_q, lo=100, hi=400, topk=200, page=64, spare_pages=2)
+    q = c.q.float()
+    q[..., :512] /= ks
+    c.q = q.bfloat16()
+    _check(smla, c, u, ks)
+
+
+@pytest.mark.parametrize("h_q", [8, 24])
+@pytest.mark.parametrize("latent,rotated", [(0.0, 1.0), (1.0, 0.0), (2.0 ** -30, 1.0), (1.0, 2.0 ** -30), (1.0, 2.0 ** 6)])
+def test_parts_of_unequal_size(smla, h_q, latent, rotated):
+    c, u = mi.decode_case_fp4(1520 + h_q, batch=2, s_next=2, h_q=h_q, lo=100, hi=400, topk=200, page=64, spare_pages=2)
+    q = c.q.float()
+    q[..., :512] *= latent
+    q[..., 512:] *= rotated
+    c.q = q.bfloat16()
+    _check(smla, c, u, 1.0)
+
+
 @pytest.mark.parametrize("h_q", [8, 16, 24, 64])
 @pytest.mark.parametrize("ks", [0.3, 2.0 ** 8, 2.0 ** 12])
 def test_large_scores(smla, h_q, ks):
