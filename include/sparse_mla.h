@@ -319,7 +319,10 @@ typedef enum {
  *   FP8    tile scale 2^k, the smallest with largest / 2^k <= 448, k kept in
  *          [-64, 31] (1 for a tile of zeros): code * scale is exact in bf16
  *   4 bits group scale e4m3(largest / (6 kv_scale)), at least 2^-9 and at most
- *          448; code = e2m1(a' / (scale kv_scale)), at most 6
+ *          448; step = scale kv_scale; code = e2m1(a' / step), at most 6.  The
+ *          product 6 kv_scale, both quotients and the step are fp32, each
+ *          rounded to nearest even (where kv_scale is a power of two that
+ *          changes no scale and no code)
  * A tile or group with a value that is not finite gets a NaN scale and reads
  * as NaN.
  */

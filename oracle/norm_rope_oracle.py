@@ -8,7 +8,9 @@ with the CUDA path.  A row x has 512 latent values a and 64 rotated values r:
 
 The latent row's a' is rounded to bf16 (8 significant bits, ties to even) and
 then to the cache's codes, the nearest of the format's values (ties to the
-even code), found here by comparing with every value.
+even code), found here by comparing with every value.  The 4-bit cache's factor
+is an fp32 number, and what is formed with it before a code is chosen (6 factors,
+a group's step, the quotients) is rounded to fp32 as its definition says.
 
 Pins (tests/test_norm_rope_oracle_pins.py): the rounding against torch's; the
 codes against brute force on the borders; the gradients against differences.
@@ -81,13 +83,17 @@ def quantize_fp8(y):
 
 def quantize_fp4(y, kv_scale=1.0):
     """y [n, 512] bf16 values -> (code bytes [n, 256], scale bytes [n, 32], values)."""
+    f = np.float32(kv_scale)
+    f6 = np.float32(6.0 * np.float64(f))
     t = y.reshape(-1, 32, 16)
     bad = ~np.isfinite(t).all(axis=-1)
     t = np.where(bad[..., None], 0.0, t)
     top = np.abs(t).max(axis=-1)
-    sc = nearest_code(np.clip(top / (6.0 * kv_scale), 2.0 ** -9, 448.0), E4M3_POS).astype(np.uint8)
-    step = E4M3_POS[sc] * kv_scale
-    code = nearest_code(np.abs(t) / step[..., None], E2M1_POS).astype(np.uint8)
+    with np.errstate(over="ignore", under="ignore"):
+        sc = nearest_code(np.clip(top.astype(np.float32) / f6, 2.0 ** -9, 448.0), E4M3_POS).astype(np.uint8)
+        step = E4M3_POS[sc].astype(np.float32) * f
+        code = nearest_code(np.abs(t).astype(np.float32) / step[..., None], E2M1_POS).astype(np.uint8)
+    step = step.astype(np.float64)
     val = np.copysign(E2M1_POS[code], t) * step[..., None]
     code = (code | (np.signbit(t).astype(np.uint8) << 3))
     code[bad] = 0

@@ -221,11 +221,14 @@ __device__ __forceinline__ void store_fp8(uint8_t* slot, bool keep, int half, in
 }
 
 // 4 bits: two lanes share a group of 16 and its scale
-// e4m3(largest / (6 kv_scale)), at least 2^-9; code = e2m1(y / (scale kv_scale)).
-// The quotient is one multiplication by the reciprocal and its correction
-// by the remainder, exact where y / step is (halfway values are common: few
-// bits on both sides); values past 8 steps, all of code 6, are cut there, so
-// that the quotient stays finite where the scale is at its largest.
+// e4m3(largest / (6 kv_scale)), at least 2^-9; code = e2m1(y / step), step = scale
+// kv_scale.  6 kv_scale, the step and both quotients are fp32, rounded to nearest:
+// with a factor that is not a power of two quotients near a code's border are
+// common, and that rounding is part of the cache's definition.  y / step is one
+// multiplication by the rounded reciprocal and its correction by the remainder
+// (Markstein, Computation of elementary functions on the IBM RISC System/6000
+// processor, 1990), the correctly rounded quotient; values past 8 steps, all of code
+// 6, are cut there, so that it stays finite where the scale is at its largest.
 __device__ __forceinline__ void store_fp4(uint8_t* slot, bool keep, int half, int lane, float kv_scale, float kv_scale6,
                                           float* y) {
   float top = 0.f;
