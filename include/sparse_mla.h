@@ -300,9 +300,12 @@ typedef enum {
  *   kv_weight  bf16 [512], 16-byte aligned, or NULL: the latent row is not normed
  *   q_out      bf16 [n_tok, h_q, 576]   written; may be q itself where q is dense
  *   kv_out     bf16 [n_tok, 576] or NULL: written with what the slot stands
- *              for (codes times scales, rounded to bf16), so that attention
- *              over kv_out and over the cache sees the same rows; may be kv
- *              itself where kv is dense
+ *              for, rounded to bf16 (FP8: code * scale, 4 bits: code * step,
+ *              below).  Attention over kv_out and over the cache sees the same
+ *              rows, but for a 4-bit cache whose factor is not a power of two:
+ *              there code * step has more bits than bf16 and kv_out's values
+ *              are up to half a bf16 step away; may be kv itself where kv is
+ *              dense
  *   kv_cache   the cache's slots, 16-byte aligned, or NULL (nothing is stored;
  *              kv_out is still rounded as cache_format would hold it)
  *   cache_format  sparse_mla_cache_format_t

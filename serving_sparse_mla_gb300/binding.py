@@ -603,7 +603,8 @@ def mla_norm_rope(q, kv, positions, cos_sin, q_weight=None, kv_weight=None, eps:
     [num_blocks, page, w]: bf16 with w = 576, or uint8 with w = 656 (FP8) or
     416 (4 bits, with its factor kv_scale); slots [n] int32, distinct (outside
     the cache: not stored).  -> (q_out [n, h, 576], kv_out [n, 576]), bf16;
-    kv_out holds what the slots stand for.  q_out / kv_out may be q / kv."""
+    kv_out holds what the slots stand for, rounded to bf16 (4-bit slots with a
+    factor that is not a power of two have more bits).  q_out / kv_out may be q / kv."""
     lib = load()
     n, h, dev, q_tok, q_head, kv_tok = _norm_args(q, kv, positions, cos_sin, q_weight, kv_weight)
     form, n_slots = 0, 0

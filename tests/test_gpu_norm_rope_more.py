@@ -29,3 +29,40 @@ def test_cache_bytes_with_any_factor(smla, ks, normed):
     """Scales and codes where the factor rounds: unnormed rows have few bits, so
     that many quotients lie at a border."""
     base._run_and_check(smla, 91, 700, 1, "fp4", True, q_norm=False, kv_norm=normed, kv_scale=ks, page=64)
+
+
+@pytest.mark.parametrize("ks", [1.0, 0.25, 0.3, 0.7])
+def test_kv_out_and_the_slots(smla, ks):
+    """kv_out is the slot's row rounded to bf16: the same where the factor is a
+    power of two, else within half a step of it (and not always the same)."""
+    n = 200
+    q, kv, _, kw = (t.to(DEV) for t in mi.norm_rows(92, n, 1))
+    pos = torch.arange(n, dtype=torch.int32, device=DEV)
+    cache = torch.zeros(4, 64, 416, dtype=torch.uint8, device=DEV)
+    _, ko = smla.mla_norm_rope(q, kv, pos, mi.rope_table(n).to(DEV), kv_weight=kw, kv_cache=cache, slots=pos, kv_scale=ks)
+    row = f4.dequantize_slots(cache.view(-1, 416)[:n], ks)
+    d = np.abs(ko.double().cpu().numpy() - row)
+    # half a step, and one fp32 rounding before it (scale * factor; the product)
+    assert np.all(d <= (2.0 ** -8 + 2.0 ** -22) * np.abs(row))
+    assert (d.max() == 0) == (ks in (1.0, 0.25))
+
+
+@pytest.mark.parametrize("ks", [0.3, 0.7, 2.0 ** -3])
+def test_serving_chain_with_a_factor(smla, ks):
+    """Rows written with a factor, then the decode with it, against the oracle
+    over the slots themselves: an engine's two calls of a step."""
+    n, h, page, topk, sn = 150, 8, 16, 96, 3
+    q, kv, qw, kw = (t.to(DEV) for t in mi.norm_rows(33, n, h))
+    table = torch.randperm(14, generator=torch.Generator().manual_seed(1))[:10].int().view(1, 10)
+    pos = torch.arange(n, dtype=torch.int32)
+    slots = table[0][(pos // page).long()] * page + pos % page
+    cache = torch.full((14, page, 416), 0x7F, dtype=torch.uint8, device=DEV)   # NaN scales wherever nothing is written
+    qo, _ = smla.mla_norm_rope(q, kv, pos.to(DEV), mi.rope_table(n).to(DEV), qw, kw, kv_cache=cache,
+                               slots=slots.to(DEV), kv_scale=ks)
+    idx = mi.prefill_indices(4, n, n, topk)[n - sn:].view(1, sn, topk)
+    qd, lens = qo[n - sn:].view(1, sn, h, 576), torch.tensor([n], dtype=torch.int32)
+    o, l = smla.sparse_mla_decode_fp4(qd, cache, table.to(DEV), lens.to(DEV), idx.to(DEV), 576 ** -0.5, kv_scale=ks)
+    ro, rl = f4.sparse_mla_decode_fp4(qd.cpu(), cache.cpu(), table, lens, idx, 576 ** -0.5, page, ks)
+    got = o.double().cpu().numpy().reshape(ro.shape)
+    assert np.all(np.abs(got - ro) <= 2.0 ** -8 * np.abs(ro) + 2e-3)
+    assert np.all(np.abs(l.double().cpu().numpy().reshape(rl.shape) - rl) <= 1e-4)
