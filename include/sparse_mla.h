@@ -277,6 +277,11 @@ typedef enum {
   SPARSE_MLA_CACHE_FP4 = 2
 } sparse_mla_cache_format_t;
 
+/* Added to mla_norm_rope's cache_format: padding tokens' rows of q_out / kv_out
+ * are written with zeros (for outputs whose memory holds nothing yet). */
+#define SPARSE_MLA_ZERO_Q_PADDING 0x100
+#define SPARSE_MLA_ZERO_KV_PADDING 0x200
+
 /*
  * The step before the attention: RMS norm of every query head's row and of
  * the token's latent row, the position rotation, and the latent row's write
@@ -308,14 +313,15 @@ typedef enum {
  *              dense
  *   kv_cache   the cache's slots, 16-byte aligned, or NULL (nothing is stored;
  *              kv_out is still rounded as cache_format would hold it)
- *   cache_format  sparse_mla_cache_format_t
+ *   cache_format  sparse_mla_cache_format_t, and the flags above
  *   kv_scale   the 4-bit cache's factor, in [2^-64, 2^64] (1 for the other formats)
  *   slots      int32 [n_tok]: the token's slot (page * page_size + offset); a
  *              slot outside [0, n_slots) stores nothing.  The slots of a call
  *              are distinct (a slot given twice holds parts of either row).
  *
  * A token whose position is outside [0, n_pos) is padding: its rows of q_out
- * and kv_out and its slot are left as they were.
+ * and kv_out and its slot are left as they were (its rows are zeros with the
+ * flags of cache_format).
  *
  * The latent row's norm is carried to about 46 bits and rounded once to bf16
  * (nearest even); codes are the nearest to those bf16 values, ties to even:

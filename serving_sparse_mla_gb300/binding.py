@@ -534,6 +534,7 @@ def sparse_mla_decode_fp4(q, kv_cache, block_table, cache_seqlens, indices, sm_s
 # ---------------------------------------------------------------- norms, rotation, cache write
 
 _CACHE_FORMATS = {(torch.bfloat16, 576): 0, (torch.uint8, FP8_SLOT_BYTES): 1, (torch.uint8, FP4_SLOT_BYTES): 2}
+_ZERO_Q_PADDING, _ZERO_KV_PADDING = 0x100, 0x200
 
 
 def _rows(t: torch.Tensor, name: str, heads: bool):
@@ -599,7 +600,7 @@ def mla_norm_rope(q, kv, positions, cos_sin, q_weight=None, kv_weight=None, eps:
 
     q [n, h, 576] and kv [n, 576] (or [n, 1, 576]) bf16, rows strided as they
     are; positions [n] int32 (outside [0, n_pos): a padding token, left as it
-    was); cos_sin [n_pos, 64] fp32, 32 cosines then 32 sines; kv_cache
+    was in outputs that are given, zeros in those made here); cos_sin [n_pos, 64] fp32, 32 cosines then 32 sines; kv_cache
     [num_blocks, page, w]: bf16 with w = 576, or uint8 with w = 656 (FP8) or
     416 (4 bits, with its factor kv_scale); slots [n] int32, distinct (outside
     the cache: not stored).  -> (q_out [n, h, 576], kv_out [n, 576]), bf16;
@@ -623,6 +624,8 @@ def mla_norm_rope(q, kv, positions, cos_sin, q_weight=None, kv_weight=None, eps:
             raise ValueError("a cache of more than 2^31 - 1 slots")
     elif slots is not None:
         raise ValueError("slots are given without kv_cache")
+    # padding tokens' rows of outputs made here are zeros
+    form |= (_ZERO_Q_PADDING if q_out is None else 0) | (_ZERO_KV_PADDING if kv_out is None else 0)
     _given(q_out, _BF16, "q_out", n * h * 576, dev)
     _given(kv_out, _BF16, "kv_out", n * 576, dev)
 

@@ -57,6 +57,7 @@ struct NormParams {
   uint8_t* cache;
   const int32_t* slots;      // [n_tok]
   int format, n_slots;
+  int zero_q, zero_kv;       // padding rows of q_out / kv_out are written with zeros
   float kv_scale, kv_scale6;
   // backward
   const float* dq;           // [n_tok, h_q, 576]
@@ -77,6 +78,13 @@ __device__ __forceinline__ void unpack8(const uint4& v, float* x) {
 __device__ __forceinline__ uint4 pack8(const float* x) {
   return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
                     pack_bf16x2(x[6], x[7]));
+}
+
+__device__ __forceinline__ void zero_row(__nv_bfloat16* row, int lane) {
+  const uint4 z = make_uint4(0, 0, 0, 0);
+  *reinterpret_cast<uint4*>(row + 8 * lane) = z;
+  *reinterpret_cast<uint4*>(row + 256 + 8 * lane) = z;
+  *reinterpret_cast<uint32_t*>(row + kLatW + 2 * lane) = 0u;
 }
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -383,7 +391,12 @@ __global__ void __launch_bounds__(kNormWarps * 32) norm_rope_kernel(const __grid
   for (; r < rows; r += step) {
     const NormRow x = next;
     if (r + step < rows) next = load_row(p, r + step, lane);
-    if (x.pos < 0 || x.pos >= p.n_pos) continue;   // a padding row: nothing of it is written
+    if (x.pos < 0 || x.pos >= p.n_pos) {   // a padding row: left as it was, or zeros
+      if (x.h == p.h_q ? p.zero_kv : p.zero_q)
+        zero_row(x.h == p.h_q ? p.kv_out + static_cast<size_t>(x.t) * kRowW
+                              : p.q_out + (static_cast<size_t>(x.t) * p.h_q + x.h) * kRowW, lane);
+      continue;
+    }
     if (x.h == p.h_q) norm_kv_row(p, x, lane);
     else norm_q_row(p, x, lane);
   }
@@ -424,10 +437,7 @@ template <bool kNorm>
 __device__ __forceinline__ void grad_row(const NormParams& p, const GradRow& v, __nv_bfloat16* dx,
                                          const __nv_bfloat16* weight, int lane, float (&acc)[16]) {
   if (v.pos < 0 || v.pos >= p.n_pos) {   // a padding row takes no part in the output
-    const uint4 z = make_uint4(0, 0, 0, 0);
-    *reinterpret_cast<uint4*>(dx + 8 * lane) = z;
-    *reinterpret_cast<uint4*>(dx + 256 + 8 * lane) = z;
-    *reinterpret_cast<uint32_t*>(dx + kLatW + 2 * lane) = 0u;
+    zero_row(dx, lane);
     return;
   }
   float g[16];

@@ -813,8 +813,9 @@ sparse_mla_status_t mla_norm_rope(const void* q, long long q_tok_stride, long lo
   sparse_mla_status_t st = check_norm(q, q_tok_stride, q_head_stride, kv, kv_tok_stride, positions, cos_sin, n_pos,
                                       q_weight, kv_weight, eps, n_tok, h_q, d_qk);
   if (st != SPARSE_MLA_OK) return st;
-  if (n_slots < 0 || cache_format < 0 || cache_format > 2) return SPARSE_MLA_ERR_INVALID_ARG;
-  if (!kv_scale_ok(kv_scale) || (cache_format != SPARSE_MLA_CACHE_FP4 && kv_scale != 1.f))
+  const int format = cache_format & ~(SPARSE_MLA_ZERO_Q_PADDING | SPARSE_MLA_ZERO_KV_PADDING);
+  if (n_slots < 0 || format < 0 || format > 2) return SPARSE_MLA_ERR_INVALID_ARG;
+  if (!kv_scale_ok(kv_scale) || (format != SPARSE_MLA_CACHE_FP4 && kv_scale != 1.f))
     return SPARSE_MLA_ERR_INVALID_ARG;
   const bool cached = kv_cache != nullptr && n_slots > 0;
   if (cached && n_tok > 0 && (!slots || !aligned(slots, 4) || !aligned(kv_cache, 16))) return SPARSE_MLA_ERR_INVALID_ARG;
@@ -829,7 +830,9 @@ sparse_mla_status_t mla_norm_rope(const void* q, long long q_tok_stride, long lo
   p.cache = static_cast<uint8_t*>(kv_cache);
   p.slots = slots;
   // Without a cache the row is still rounded as that format would hold it.
-  p.format = cache_format;
+  p.format = format;
+  p.zero_q = (cache_format & SPARSE_MLA_ZERO_Q_PADDING) != 0;
+  p.zero_kv = (cache_format & SPARSE_MLA_ZERO_KV_PADDING) != 0 && kv_out != nullptr;
   p.n_slots = cached ? n_slots : 0;
   p.kv_scale = kv_scale;
   p.kv_scale6 = static_cast<float>(6.0 * kv_scale);

@@ -66,3 +66,26 @@ def test_serving_chain_with_a_factor(smla, ks):
     got = o.double().cpu().numpy().reshape(ro.shape)
     assert np.all(np.abs(got - ro) <= 2.0 ** -8 * np.abs(ro) + 2e-3)
     assert np.all(np.abs(l.double().cpu().numpy().reshape(rl.shape) - rl) <= 1e-4)
+
+
+@pytest.mark.parametrize("given", ["", "q", "kv", "both"])
+def test_padding_rows_of_fresh_outputs(smla, given):
+    """Outputs that the call allocates are zeros in padding tokens' rows; those
+    it is given keep what they hold."""
+    n, h = 40, 4
+    q, kv, qw, kw = (t.to(DEV) for t in mi.norm_rows(93, n, h))
+    pos = torch.arange(n, dtype=torch.int32)
+    pos[5], pos[30:] = n, -1
+    live = (pos >= 0) & (pos < n)
+    cs = mi.rope_table(n).to(DEV)
+    out = dict(q_out=torch.full((n, h, 576), 3.0, dtype=torch.bfloat16, device=DEV) if given in ("q", "both") else None,
+               kv_out=torch.full((n, 576), 3.0, dtype=torch.bfloat16, device=DEV) if given in ("kv", "both") else None)
+    for _ in range(3):
+        # blocks of the outputs' sizes, freed full of NaN, are what the call gets
+        dirty = [torch.full_like(q, float("nan")) for _ in range(4)] + [torch.full_like(kv, float("nan")) for _ in range(4)]
+        del dirty
+        qo, ko = smla.mla_norm_rope(q, kv, pos.to(DEV), cs, qw, kw, **out)
+        assert bool((qo[~live] == (3 if given in ("q", "both") else 0)).all())
+        assert bool((ko[~live] == (3 if given in ("kv", "both") else 0)).all())
+        want = smla.mla_norm_rope(q[live], kv[live], pos[live].to(DEV), cs, qw, kw)
+        assert torch.equal(qo[live], want[0]) and torch.equal(ko[live], want[1])
