@@ -658,6 +658,9 @@ F4Plan f4_plan(long long n_tok, int h_q, int topk, int sms) {
   return plan(h_q <= 8 ? kF4Heads8 : (h_q <= 16 ? kF4Heads16 : kF4Heads32));
 }
 
+// A CTA counts its blocks, and a few past them, in an int.
+bool f4_blocks_ok(const F4Plan& f, long long n_tok) { return n_tok * f.groups * f.nb / f.ctas < INT_MAX - 8; }
+
 template <class C>
 cudaError_t f4_launch(const smla::Fp4Params& p, cudaStream_t cs) {
   if (p.cluster > 0) {
@@ -685,7 +688,8 @@ size_t sparse_mla_decode_fp4_workspace_size(int batch, int s_next, int h_q, int 
   int sms = 0;
   const long long n_tok = static_cast<long long>(batch) * s_next;
   if (!f4_sizes_ok(n_tok, h_q, topk) || device_setup(&sms) != SPARSE_MLA_OK || f4_device_setup() != SPARSE_MLA_OK) return 0;
-  return f4_plan(n_tok, h_q, topk, sms).bytes;
+  const F4Plan f = f4_plan(n_tok, h_q, topk, sms);
+  return f4_blocks_ok(f, n_tok) ? f.bytes : 0;
 }
 
 sparse_mla_status_t sparse_mla_decode_fp4(const void* q, const void* kv_cache, const int32_t* block_table,
@@ -707,6 +711,7 @@ sparse_mla_status_t sparse_mla_decode_fp4(const void* q, const void* kv_cache, c
   if (num_blocks == 0 || max_blocks == 0) return launch_fill(out, lse, n_tok * h_q, cs);
   if ((st = f4_device_setup()) != SPARSE_MLA_OK) return st;
   const F4Plan f = f4_plan(n_tok, h_q, topk, sms);
+  if (!f4_blocks_ok(f, n_tok)) return SPARSE_MLA_ERR_INVALID_ARG;
   if (f.bytes > 0 && (workspace_bytes < f.bytes || !workspace)) return SPARSE_MLA_ERR_WORKSPACE_TOO_SMALL;
   if (f.bytes > 0 && !aligned(workspace, 16)) return SPARSE_MLA_ERR_INVALID_ARG;
   smla::Fp4Params p;

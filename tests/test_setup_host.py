@@ -117,6 +117,18 @@ assert lib.fake_pending() == 0
 """)
 
 
+def test_ctas_with_more_blocks_than_an_int_counts_are_refused(lib_path):
+    """60 million heads over a list of 2^31 entries is 10^11 blocks for a CTA."""
+    _run(lib_path, "0, 0", """
+big = 2 ** 31 - 1025
+for n, h, topk in ((1, 60_000_000, big), (10, 6_000_000, big), (16_000_000, 8, big)):
+    assert need(n, h, topk) == 0, (n, h, topk)
+    assert fp4(n, h, topk) == 1, (n, h, topk)
+for n, h, topk in ((2000, 64, 100_000), (1, 128, big), (500_000, 128, 2048)):
+    assert need(n, h, topk) > 0, (n, h, topk)
+""")
+
+
 def test_the_stand_in_has_every_entry_point(lib_path):
     from serving_sparse_mla_gb300.binding import SIGNATURES
     lib = ctypes.CDLL(lib_path)
