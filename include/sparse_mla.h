@@ -289,7 +289,8 @@ typedef enum {
  * rotated values r:
  *
  *   a' = a * rsqrt(mean(a^2) + eps) * weight      (no weight: a' = a; a normed
- *        row's mean(a^2) + eps has to be a normal fp32 number)
+ *        row's mean(a^2) + eps has to be a normal fp32 number, and its mean(a^2)
+ *        below 2^119: the 512 squares are added up before they are divided)
  *   r' = r turned by its position's angles: plane i has cos_sin[pos][i] and
  *        cos_sin[pos][32 + i], and is values (2i, 2i + 1) of r when
  *        `interleaved`, else values (i, i + 32):
@@ -323,8 +324,8 @@ typedef enum {
  * and kv_out and its slot are left as they were (its rows are zeros with the
  * flags of cache_format).
  *
- * The latent row's norm is carried to about 46 bits and rounded once to bf16
- * (nearest even); codes are the nearest to those bf16 values, ties to even:
+ * The latent row's norm is carried to about 46 bits (where mean(a^2) + eps is
+ * within [2^-100, 2^100]) and rounded once to bf16 (nearest even); codes are the nearest to those bf16 values, ties to even:
  *   FP8    tile scale 2^k, the smallest with largest / 2^k <= 448, k kept in
  *          [-64, 31] (1 for a tile of zeros): code * scale is exact in bf16
  *   4 bits group scale e4m3(largest / (6 kv_scale)), at least 2^-9 and at most

@@ -18,8 +18,8 @@
 // takes 11.9 and 20.6 us (3840 and 4290 GB/s: a launch's start and end are 4 us of
 // it); one token 3.4 us, a launch.
 //
-// Squares are summed as fp32 numbers: a row whose mean square leaves fp32's
-// range is outside of what the norm is made for.
+// 512 squares are summed as fp32 numbers before they are divided: a row whose mean
+// square is 2^119 or more is outside of what the norm is made for.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -117,6 +117,10 @@ __device__ __forceinline__ float2 rotate_pair(float2 x, const float* table, int 
 // of that row is carried to about 46 bits (pairs hi + lo of floats, with the
 // error-free sum and product) and rounded once: the codes then follow from
 // the formula alone, not from the order of a sum.  This is 1 row in h_q + 1.
+// (Sums: Knuth's, The Art of Computer Programming 2, 4.2.2; products: Dekker's, A
+// floating-point technique for extending the available precision, 1971, with a fused
+// multiply-add.  46 bits where the low parts are normal numbers: mean squares within
+// [2^-100, 2^100]; outside of that fewer.)
 struct Two {
   float hi, lo;
 };

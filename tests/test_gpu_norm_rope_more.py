@@ -89,3 +89,36 @@ def test_padding_rows_of_fresh_outputs(smla, given):
         assert bool((ko[~live] == (3 if given in ("kv", "both") else 0)).all())
         want = smla.mla_norm_rope(q[live], kv[live], pos[live].to(DEV), cs, qw, kw)
         assert torch.equal(qo[live], want[0]) and torch.equal(ko[live], want[1])
+
+
+@pytest.mark.parametrize("size,eps", [(2.0 ** 59, 1e-6), (2.0 ** -50, 0.0), (2.0 ** 40, 0.0), (2.0 ** -40, 1e-30)])
+def test_rows_at_the_ends_of_the_range(smla, size, eps):
+    """Mean squares up to 2^118 and down to 2^-100."""
+    n, h = 6, 3
+    g = torch.Generator().manual_seed(7)
+    q, kv = torch.randn(n, h, 576, generator=g), torch.randn(n, 576, generator=g)
+    q[..., :512] *= size
+    kv[..., :512] *= size
+    q, kv = q.bfloat16(), kv.bfloat16()
+    qw, kw = (1 + 0.2 * torch.randn(2, 512, generator=g)).bfloat16()
+    pos, cs = torch.arange(n, dtype=torch.int32), mi.rope_table(n)
+    d = lambda t: t.to(DEV)  # noqa: E731
+    qo, ko = smla.mla_norm_rope(d(q), d(kv), d(pos), d(cs), d(qw), d(kw), eps=eps)
+    f64 = lambda t: t.double().cpu().numpy()  # noqa: E731
+    ref = nro.rms_norm(f64(q)[..., :512], f64(qw), eps)
+    assert np.all(np.abs(f64(qo)[..., :512] - ref) <= (2.0 ** -8 + 2.0 ** -20) * np.abs(ref))
+    assert np.array_equal(f64(ko)[:, :512], nro.round_bf16(nro.rms_norm(f64(kv)[:, :512], f64(kw), eps)))
+    dq, dkv = torch.randn(n, h, 576, generator=g), torch.randn(n, 576, generator=g)
+    got = smla.mla_norm_rope_bwd(d(q), d(kv), d(pos), d(cs), d(dq), d(dkv), d(qw), d(kw), eps=eps)
+    ang = f64(cs)
+    for k, x, dy, w, a in ((0, q, dq, qw, ang[:, None]), (1, kv, dkv, kw, ang)):
+        dx, dw = nro.norm_rope_bwd(f64(x), f64(dy), a, f64(w), eps, True)
+        x64 = f64(x)[..., :512]
+        r = 1 / np.sqrt((x64 * x64).mean(-1, keepdims=True) + eps)
+        gw, xh = np.abs(f64(dy)[..., :512] * f64(w)), np.abs(x64) * r
+        terms = r * (gw + xh * (gw * xh).mean(-1, keepdims=True))
+        # 2^-133: half of bf16's smallest step, which gradients of rows of 2^59 come near to
+        tol = 2.0 ** -8 * np.abs(dx[..., :512]) + 2.0 ** -18 * terms + 2.0 ** -133
+        assert np.all(np.abs(f64(got[k])[..., :512] - dx[..., :512]) <= tol)
+        tw = (np.abs(f64(dy)[..., :512]) * xh).reshape(-1, 512).sum(0)
+        assert np.all(np.abs(f64(got[2 + k]) - dw) <= 2.0 ** -18 * tw)
