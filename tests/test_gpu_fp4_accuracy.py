@@ -13,6 +13,9 @@ f16's steps end at 2^-24: P, 2^7 for a weight as large as the running maximum,
 is off by up to 2^-25 however small it is, that is by 2^-32 of the largest
 weight p <= 1, and the output by 2^-32 sum |x|."""
 import math
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -25,6 +28,7 @@ from oracle import sparse_mla_oracle as orc
 pytestmark = pytest.mark.gpu
 
 DEV = "cuda:0"
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 @pytest.fixture(scope="module")
@@ -154,3 +158,28 @@ def test_scores_past_the_steps_of_one(smla, h_q, step):
     assert np.all(np.abs(o[:, 0] - 8) <= 2.0 ** -8 * 8) and np.all((o[:, 16] >= 1 - 2.0 ** -8) & (o[:, 16] <= 6 + 6 * 2.0 ** -8))
     want = math.log(2) * 2.0 ** 24 * (8 + float(rope[1]))
     assert np.all(np.abs(lse.double().cpu().numpy() - want) <= 2.0 ** -21 * want)
+
+
+def test_the_first_call_of_a_process_may_be_captured():
+    """A process whose first call of the library is a captured 4-bit decode: the
+    kernels' set-up takes place during the capture."""
+    code = """
+import torch
+import mla_inputs as mi
+import serving_sparse_mla_gb300 as smla
+d = lambda t: t.to("cuda:0")
+cases = [mi.decode_case_fp4(60 + k, batch=2, s_next=2, h_q=h, lo=300, hi=400, topk=256, spare_pages=2) for k, h in enumerate((8, 24))]
+args = [([d(t) for t in (c.q, u, c.block_table, c.cache_seqlens, c.indices)], c.sm_scale) for c, u in cases]
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    got = [smla.sparse_mla_decode_fp4(*a, s) for a, s in args]
+g.replay()
+torch.cuda.synchronize()
+for (a, s), r in zip(args, got):
+    want = smla.sparse_mla_decode_fp4(*a, s)
+    torch.cuda.synchronize()
+    assert torch.equal(r[0], want[0]) and torch.equal(r[1], want[1]) and bool((r[0] != 0).any())
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, cwd=ROOT)
+    assert r.returncode == 0, r.stdout + r.stderr

@@ -122,3 +122,9 @@ def test_rows_at_the_ends_of_the_range(smla, size, eps):
         assert np.all(np.abs(f64(got[k])[..., :512] - dx[..., :512]) <= tol)
         tw = (np.abs(f64(dy)[..., :512]) * xh).reshape(-1, 512).sum(0)
         assert np.all(np.abs(f64(got[2 + k]) - dw) <= 2.0 ** -18 * tw)
+
+
+@pytest.mark.parametrize("n,h,norms", [(5200, 1, "qk"), (6001, 2, "k"), (5200, 1, "q")])
+def test_backward_of_more_rows_than_warps(smla, n, h, norms):
+    """Over 2 x 2432 tokens: every warp takes several latent rows."""
+    base.test_backward(smla, True, n, h, norms, 7)
