@@ -35,14 +35,16 @@
 // sum is taken from the unrounded weights.  The rotated part stays bf16 (its own
 // MMAs).  All sums are fp32.
 //
-// What bounds it: the instructions that widen codes.  Per 16 rows a warp issues
-// about 1100 (8 heads), of which 256 are conversions, 256 multiplications by the
-// scale and 68 MMAs per 8 heads; the schedulers issue in half of the cycles (16
-// heads: MMA 37 %, ALU 37 %, shared memory 49 % of their peaks), and leaving out
-// the multiplications alone takes 12 % off, the conversions alone 1 %.  Gathering
-// the slots (416 bytes a row) is 8 % of the time.  Lists of 2048, GPU time: 96
-// tokens x 8 heads 33.5 us (the bf16 cache's decode 60), 512 x 16 168 (212), 128 x
-// 64 145 (101: there the bf16 decode's tensor-core blocks win), one token x 8 8.9.
+// What bounds it: the order of its phases.  Scores, barrier and values of a block
+// follow one another with 8 or 12 warps on an SM, and the schedulers issue in 37 to
+// 48 % of the cycles while no pipe is full (16 heads: MMA 37 %, ALU 37 %, shared memory
+// 49 % of their peaks).  Per 16 rows a warp issues about 1100 instructions (8 heads), of
+// which 256 are conversions, 256 multiplications by the scale and 68 MMAs per 8 heads;
+// leaving out the multiplications alone takes 12 % off, the gather of the slots 8 %,
+// the conversions 1 %.  Above 32 heads each unit of 32 gathers and widens its token's list
+// again.  Lists of 2048, GPU time: 96 tokens x 8 heads 33.5 us (the bf16 cache's decode
+// 60), 512 x 16 169 (212), 128 x 64 146 (101: there the bf16 decode wins), one token x 8
+// 8.8.
 //
 // A warp takes 16 rows of a block: it copies their slots (cp.async, its own
 // part of the ring), scores them, writes P to shared memory, and after one
