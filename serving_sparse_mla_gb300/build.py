@@ -14,9 +14,9 @@ CSRC = os.path.join(PKG_DIR, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_NAME = "libsparse_mla_gb300.so"
 LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
-SOURCES = ["sparse_mla_api.cu"]
-DEPS = ["sparse_mla_api.cu", "fwd_kernel.cuh", "bwd_kernel.cuh", "indexer_kernel.cuh", "fp4_decode_kernel.cuh",
-        "norm_rope_kernel.cuh", "ptx.cuh"]
+SOURCES = ["library.cu"]
+DEPS = ["library.cu", "sparse_mla_api.cu", "latent_api.cuh", "fwd_kernel.cuh", "bwd_kernel.cuh", "indexer_kernel.cuh",
+        "fp4_decode_kernel.cuh", "norm_rope_kernel.cuh", "ptx.cuh"]
 
 
 def nvcc_path() -> str:

@@ -44,7 +44,7 @@ inline cudaError_t last() { const cudaError_t e = pending; pending = cudaSuccess
 #define cudaFuncSetAttribute fake::function
 #define cudaOccupancyMaxActiveClusters fake::clusters
 #define cudaGetLastError fake::last
-#include "sparse_mla_api.cu"
+#include "library.cu"
 extern "C" {
 void fake_refuse(int clusters, int fp4) { fake::refuse_clusters = clusters; fake::refuse_fp4 = fp4; }
 int fake_pending() { return fake::pending; }
