@@ -375,6 +375,150 @@ sparse_mla_status_t mla_norm_rope_bwd(const void* q, long long q_tok_stride, lon
 /* Bytes of workspace mla_norm_rope_bwd needs on the current device. */
 size_t mla_norm_rope_bwd_workspace_size(int n_tok, int h_q);
 
+/* Forms of mla_add_norm's output: bf16 rows, or e4m3 codes with one scale for
+ * each 128 values of a row, or one for each row. */
+typedef enum {
+  MLA_ADD_NORM_BF16 = 0,
+  MLA_ADD_NORM_E4M3_GROUPS = 1,
+  MLA_ADD_NORM_E4M3_ROW = 2
+} mla_add_norm_format_t;
+
+/*
+ * The residual's addition and the RMS norm of the sum, over whole rows of a
+ * model's hidden width, before the projections whose rows mla_norm_rope and
+ * dense_mha_fwd take:
+ *
+ *   z = x + residual, rounded to bf16             (no residual: z = x)
+ *   y = z * rsqrt(mean(z^2) + eps) * weight, rounded to bf16
+ *
+ * The norm's factor is carried to about 46 bits and y rounded once (nearest
+ * even; the sum of a row's squares has to stay below 2^127, and mean(z^2) + eps
+ * within [2^-100, 2^100]).  8-bit forms hold y as float8 e4m3 codes (OCP E4M3)
+ * and fp32 scales: code * scale, the scale 2^k the smallest with
+ * largest / 2^k <= 448, k kept in [-64, 31] (1 for zeros), code = e4m3(y / 2^k),
+ * ties to even.  A group or row with a value that is not finite gets a NaN
+ * scale and codes 0.
+ *
+ *   x             bf16 [n, d], row r at x + r x_stride
+ *   residual      bf16, row r at residual + r residual_stride, or NULL
+ *                 (strides in elements, multiples of 8; rows are contiguous)
+ *   weight        bf16 [d]
+ *   out           bf16 [n, d] or e4m3 [n, d], written
+ *   scales        fp32 [n, ceil(d / 128)] or [n] with an 8-bit form (else
+ *                 ignored), written; the last group of a row may be short
+ *   out_format    mla_add_norm_format_t
+ *   residual_out  bf16 [n, d]: z, written where a residual is given; may be x or
+ *                 residual itself where that is dense
+ *
+ * Pointers but `scales` are 16-byte aligned.  d is a multiple of 8, at most
+ * 16384 (SPARSE_MLA_ERR_UNSUPPORTED_SHAPE otherwise).
+ */
+sparse_mla_status_t mla_add_norm(const void* x, long long x_stride, const void* residual, long long residual_stride,
+                                 const void* weight, float eps, void* out, float* scales, int out_format,
+                                 void* residual_out, int n, int d, void* stream);
+
+/*
+ * Gradients of mla_add_norm with respect to its sum (hence to x and to the
+ * residual alike) and the weight; rounding passes gradients unchanged.  With
+ * r = rsqrt(mean(z^2) + eps), zhat = z r and g = weight * dout:
+ *
+ *   dx = r (g - zhat mean(g zhat)) + dresidual,   dweight = sum over rows of dout zhat.
+ *
+ *   z          bf16, the forward's sum (x where it had no residual), strided as there
+ *   dout       bf16, the gradient of out, strided likewise
+ *   dresidual  bf16, the gradient that reaches residual_out from later layers,
+ *              strided likewise, or NULL
+ *   dx         bf16 [n, d], written (rounded once); may be dout or dresidual
+ *              itself where that is dense
+ *   dweight    fp32 [d], written
+ *   workspace  at least mla_add_norm_bwd_workspace_size(n, d) bytes, 16-byte
+ *              aligned; contents ignored.  Two calls that may run concurrently
+ *              need separate workspaces
+ *
+ * Sums are taken in a fixed order: the same call gives the same bits.
+ */
+sparse_mla_status_t mla_add_norm_bwd(const void* z, long long z_stride, const void* weight, float eps,
+                                     const void* dout, long long dout_stride, const void* dresidual,
+                                     long long dresidual_stride, void* dx, float* dweight, int n, int d,
+                                     void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace mla_add_norm_bwd needs on the current device. */
+size_t mla_add_norm_bwd_workspace_size(int n, int d);
+
+/* dense_mha_fwd's `fill`: rows of no sequence get out = 0, lse = -inf (for
+ * outputs whose memory holds nothing yet); without, they are left as they were. */
+#define DENSE_MHA_FILL_OUT 1
+#define DENSE_MHA_FILL_LSE 2
+
+/*
+ * Causal attention over whole prompts in the heads' own space: the dense
+ * counterpart of sparse_mla_fwd_causal before the latent projection is absorbed
+ * (192-value query and key heads, 128-value value heads: 320 products a pair
+ * of positions where the absorbed form has 1088), and of models with grouped
+ * heads.  Query head j reads key and value head j / (h_q / h_kv).
+ *
+ *   s_ij = sm_scale * q_i . k_j over the keys j that query i sees
+ *   lse_i = ln sum_j exp(s_ij)                        (natural log, fp32)
+ *   out_i = sum_j exp(s_ij - lse_i) * v_j             (bf16)
+ *
+ * The lq queries of a sequence are the last lq of its lk positions: its query i
+ * sees keys 0 .. i + lk - lq; one that sees none gets out = 0 and lse = -inf.
+ *
+ *   q    bf16 [total_q, h_q, d_qk], row (t, h) at q + t q_tok_stride + h q_head_stride
+ *   k    bf16 [total_kv, h_kv, d_qk], v bf16 [total_kv, h_kv, d_v], strided likewise
+ *        (strides in elements, positive multiples of 8; the values of a row are
+ *        contiguous; pointers 16-byte aligned)
+ *   cu_seqlens_q, cu_seqlens_kv  int32 [batch + 1] packed-sequence offsets,
+ *        non-decreasing from 0, or both NULL for one dense sequence (batch is
+ *        then ignored).  Offsets outside of the tensors are cut to them.  Rows
+ *        behind the last sequence belong to none: see `fill`
+ *   sm_scale  finite, not negative
+ *   out  bf16 [total_q, h_q, d_v], 16-byte aligned   written
+ *   lse  fp32 [total_q, h_q]                         written
+ *   fill DENSE_MHA_FILL_OUT | DENSE_MHA_FILL_LSE
+ *
+ * d_qk is 192 or 128 and d_v 128 (SPARSE_MLA_ERR_UNSUPPORTED_SHAPE otherwise);
+ * h_kv divides h_q.  Sums are taken in a fixed order: the same call gives the
+ * same bits.
+ */
+sparse_mla_status_t dense_mha_fwd(const void* q, long long q_tok_stride, long long q_head_stride, const void* k,
+                                  long long k_tok_stride, long long k_head_stride, const void* v,
+                                  long long v_tok_stride, long long v_head_stride, const int32_t* cu_seqlens_q,
+                                  const int32_t* cu_seqlens_kv, int batch, float sm_scale, void* out, float* lse,
+                                  int fill, int total_q, int total_kv, int h_q, int h_kv, int d_qk, int d_v,
+                                  void* stream);
+
+/*
+ * Gradients of dense_mha_fwd with respect to q, k and v for an upstream
+ * gradient dout of out (the LSE output carries no gradient).  With P_ij =
+ * exp(s_ij - lse_i):
+ *   dS = P * (dout V^T - rowsum(dout * out)),  dq = sm_scale dS K,
+ *   dk = sm_scale dS^T q,  dv = P^T dout       (sums over the heads of a group)
+ *
+ *   q .. sm_scale  as for dense_mha_fwd
+ *   out, lse       the forward's outputs
+ *   dout           bf16 [total_q, h_q, d_v], strided like q
+ *   dq             bf16 [total_q, h_q, d_qk]    written (rounded once)
+ *   dk, dv         bf16 [total_kv, h_kv, d_qk], [total_kv, h_kv, d_v]   written
+ *   workspace      at least dense_mha_bwd_workspace_size(...) bytes, 16-byte
+ *                  aligned; contents ignored.  Two calls that may run
+ *                  concurrently need separate workspaces
+ *
+ * Rows of no sequence take no part: their gradients are zero.  Sums are taken
+ * in a fixed order: the same call gives the same bits.
+ */
+sparse_mla_status_t dense_mha_bwd(const void* q, long long q_tok_stride, long long q_head_stride, const void* k,
+                                  long long k_tok_stride, long long k_head_stride, const void* v,
+                                  long long v_tok_stride, long long v_head_stride, const int32_t* cu_seqlens_q,
+                                  const int32_t* cu_seqlens_kv, int batch, float sm_scale, const void* out,
+                                  const float* lse, const void* dout, long long dout_tok_stride,
+                                  long long dout_head_stride, void* dq, void* dk, void* dv, int total_q, int total_kv,
+                                  int h_q, int h_kv, int d_qk, int d_v, void* workspace, size_t workspace_bytes,
+                                  void* stream);
+
+/* Bytes of workspace dense_mha_bwd needs. */
+size_t dense_mha_bwd_workspace_size(int total_q, int total_kv, int batch, int h_q, int h_kv, int d_qk, int d_v);
+
 /*
  * sparse_mla_decode without a caller workspace, for callers that cannot
  * allocate device memory at the point of the call: code running inside a

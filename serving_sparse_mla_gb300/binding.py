@@ -66,6 +66,19 @@ SIGNATURES = {
                                   c_void_p, c_void_p, c_float, c_int, c_void_p, c_void_p, c_void_p, c_void_p,
                                   c_void_p, c_void_p, c_int, c_int, c_int, c_void_p, c_size_t, c_void_p]),
     "mla_norm_rope_bwd_workspace_size": (c_size_t, [c_int, c_int]),
+    "mla_add_norm": (c_int, [c_void_p, c_longlong, c_void_p, c_longlong, c_void_p, c_float, c_void_p, c_void_p, c_int,
+                             c_void_p, c_int, c_int, c_void_p]),
+    "mla_add_norm_bwd": (c_int, [c_void_p, c_longlong, c_void_p, c_float, c_void_p, c_longlong, c_void_p, c_longlong,
+                                 c_void_p, c_void_p, c_int, c_int, c_void_p, c_size_t, c_void_p]),
+    "mla_add_norm_bwd_workspace_size": (c_size_t, [c_int, c_int]),
+    "dense_mha_fwd": (c_int, [c_void_p, c_longlong, c_longlong, c_void_p, c_longlong, c_longlong, c_void_p, c_longlong,
+                              c_longlong, c_void_p, c_void_p, c_int, c_float, c_void_p, c_void_p, c_int, c_int, c_int,
+                              c_int, c_int, c_int, c_int, c_void_p]),
+    "dense_mha_bwd": (c_int, [c_void_p, c_longlong, c_longlong, c_void_p, c_longlong, c_longlong, c_void_p, c_longlong,
+                              c_longlong, c_void_p, c_void_p, c_int, c_float, c_void_p, c_void_p, c_void_p, c_longlong,
+                              c_longlong, c_void_p, c_void_p, c_void_p, c_int, c_int, c_int, c_int, c_int, c_int,
+                              c_void_p, c_size_t, c_void_p]),
+    "dense_mha_bwd_workspace_size": (c_size_t, [c_int, c_int, c_int, c_int, c_int, c_int, c_int]),
     "sparse_mla_debug_valid_count": (c_int, [c_void_p, c_int, c_int, c_int, c_void_p, c_void_p]),
     "sparse_mla_debug_valid_count_varlen": (c_int, [c_void_p, c_void_p, c_void_p, c_int, c_int, c_int, c_int,
                                                     c_void_p, c_void_p]),
@@ -684,6 +697,255 @@ def mla_norm_rope_bwd(q, kv, positions, cos_sin, dq, dkv, q_weight=None, kv_weig
                                      ws_bytes, cs), (dqi, dki, dqw, dkw)
 
     return _launch(go, dev, stream, "mla_norm_rope_bwd")
+
+
+# ---------------------------------------------------------------- residual norm
+
+def _wide_rows(t: torch.Tensor, n: int, d: int, name: str, dev) -> int:
+    """Row stride in elements of bf16 rows [n, d], contiguous in themselves, each on 16 bytes."""
+    if (t.is_cuda and t.dtype is _BF16 and t.device == dev and t.shape == (n, d) and t.stride(1) == 1
+            and not t.stride(0) & 7 and not t.data_ptr() & 15):
+        return t.stride(0)
+    _on_cuda(t, name)
+    if t.dtype != _BF16:
+        raise ValueError(f"{name} must be {_BF16}, got {t.dtype}")
+    _fits(t, 0, name, dev)
+    if tuple(t.shape) != (n, d):
+        raise ValueError(f"{name} must be [{n}, {d}], got {tuple(t.shape)}")
+    step = t.stride(0) if n > 1 else 0
+    if n > 0 and ((d > 1 and t.stride(1) != 1) or step % 8 or t.data_ptr() % 16):
+        raise ValueError(f"rows of {name} must be contiguous and start on 16 bytes (strides {t.stride()})")
+    return step
+
+
+def _overlap(a: torch.Tensor, b: torch.Tensor) -> bool:
+    """Whether the memory between a's first and last element meets that of b's."""
+    if a.numel() == 0 or b.numel() == 0:
+        return False
+    ends = [x.data_ptr() + (sum((n - 1) * abs(s) for n, s in zip(x.shape, x.stride())) + 1) * x.element_size()
+            for x in (a, b)]
+    return a.data_ptr() < ends[1] and b.data_ptr() < ends[0]
+
+
+def _row_by_row(out: Optional[torch.Tensor], name: str, *inputs) -> None:
+    """An output [n, d] of whole rows may be one of the inputs, dense and at the same
+    address (each row is read before it is written), and may not share memory with
+    one in any other way."""
+    if out is None:
+        return
+    for t, what in inputs:
+        if t is not None and _overlap(out, t) and not (out.data_ptr() == t.data_ptr() and t.is_contiguous()):
+            raise ValueError(f"{name} shares memory with {what} other than as the same dense tensor")
+
+
+def mla_add_norm(x, weight, residual=None, eps: float = 1e-6, group: Optional[int] = None, out=None, scales=None,
+                 residual_out=None, stream=None):
+    """z = x + residual (bf16), y = z * rsqrt(mean(z^2) + eps) * weight over rows [n, d].
+
+    x and residual bf16, rows strided as they are; weight [d] bf16.  group None: out
+    is y in bf16; 128 or 0: out is float8_e4m3fn, y's codes under a power-of-two
+    scale for each 128 values of a row (the last group may be shorter), or for each
+    row.  -> (out [n, d], scales [n, ceil(d / 128)] or [n, 1] fp32 or None,
+    residual_out [n, d] bf16: z, or x itself where no residual is given).
+    residual_out may be x or residual."""
+    lib = load()
+    if x.dim() != 2:
+        raise ValueError(f"x must be [n, d], got {tuple(x.shape)}")
+    n, d = x.shape
+    dev = x.device
+    x_step = _wide_rows(x, n, d, "x", dev)
+    _given(weight, _BF16, "weight", d, dev)
+    if weight.numel() != d:
+        raise ValueError(f"weight must hold {d} values, got {weight.numel()}")
+    res_step = _wide_rows(residual, n, d, "residual", dev) if residual is not None else 0
+    if group not in (None, 0, 128):
+        raise ValueError(f"group must be None, 128 or 0, got {group}")
+    form = 0 if group is None else (1 if group else 2)
+    n_scales = (d + 127) // 128 if form == 1 else 1
+    kind = torch.float8_e4m3fn if form else _BF16
+    _given(out, kind, "out", n * d, dev)
+    if scales is not None and not form:
+        raise ValueError("scales are given without a group")
+    _given(scales, _F32, "scales", n * n_scales, dev)
+    if residual is None and residual_out is not None:
+        raise ValueError("residual_out is given without residual")
+    _given(residual_out, _BF16, "residual_out", n * d, dev)
+    _row_by_row(residual_out, "residual_out", (x, "x"), (residual, "residual"))
+    for t, name in ((out, "out"), (scales, "scales")):
+        for u, what in ((x, "x"), (residual, "residual"), (weight, "weight"), (residual_out, "residual_out")):
+            if t is not None and u is not None and _overlap(t, u):
+                raise ValueError(f"{name} shares memory with {what}")
+
+    def go(cs):
+        o = torch.empty((n, d), dtype=kind, device=dev) if out is None else out
+        sc = torch.empty((n, n_scales), dtype=_F32, device=dev) if form and scales is None else scales
+        z = residual_out
+        if residual is not None and z is None:
+            z = torch.empty((n, d), dtype=_BF16, device=dev)
+        return lib.mla_add_norm(x.data_ptr(), x_step, _at(residual), res_step, weight.data_ptr(), eps, o.data_ptr(),
+                                _at(sc), form, _at(z), n, d, cs), (o, sc, x if residual is None else z)
+
+    return _launch(go, dev, stream, "mla_add_norm")
+
+
+def add_norm_bwd_workspace_size(n: int, d: int) -> int:
+    """Bytes mla_add_norm_bwd needs on the current device."""
+    return int(load().mla_add_norm_bwd_workspace_size(n, d))
+
+
+def mla_add_norm_bwd(z, weight, dout, dresidual=None, eps: float = 1e-6, workspace: Optional[torch.Tensor] = None,
+                     dx=None, dweight=None, stream=None):
+    """Gradients of mla_add_norm: z [n, d] is its sum (what it returned last),
+    dout the gradient of its rows, dresidual the one that reaches z from later
+    layers (or None), all bf16, rows strided as they are -> (dx [n, d] bf16, the
+    gradient of x and of the residual alike, dweight [d] fp32).  dx may be dout or
+    dresidual."""
+    lib = load()
+    if z.dim() != 2:
+        raise ValueError(f"z must be [n, d], got {tuple(z.shape)}")
+    n, d = z.shape
+    dev = z.device
+    z_step = _wide_rows(z, n, d, "z", dev)
+    _given(weight, _BF16, "weight", d, dev)
+    if weight.numel() != d:
+        raise ValueError(f"weight must hold {d} values, got {weight.numel()}")
+    g_step = _wide_rows(dout, n, d, "dout", dev)
+    r_step = _wide_rows(dresidual, n, d, "dresidual", dev) if dresidual is not None else 0
+    _given(dx, _BF16, "dx", n * d, dev)
+    _given(dweight, _F32, "dweight", d, dev)
+    _row_by_row(dx, "dx", (dout, "dout"), (dresidual, "dresidual"))
+    for t, name in ((dx, "dx"), (dweight, "dweight"), (workspace, "workspace")):
+        for u, what in ((z, "z"), (weight, "weight")) + (() if name == "dx" else ((dout, "dout"),
+                                                                                 (dresidual, "dresidual"))):
+            if t is not None and u is not None and _overlap(t, u):
+                raise ValueError(f"{name} shares memory with {what}")
+    _workspace(workspace, dev)
+
+    def go(cs):
+        gx = torch.empty((n, d), dtype=_BF16, device=dev) if dx is None else dx
+        gw = torch.empty(d, dtype=_F32, device=dev) if dweight is None else dweight
+        ws = workspace
+        if ws is None:
+            ws = torch.empty(max(16, lib.mla_add_norm_bwd_workspace_size(n, d)), dtype=_U8, device=dev)
+        return lib.mla_add_norm_bwd(z.data_ptr(), z_step, weight.data_ptr(), eps, dout.data_ptr(), g_step,
+                                    _at(dresidual), r_step, gx.data_ptr(), gw.data_ptr(), n, d, ws.data_ptr(),
+                                    ws.numel() * ws.element_size(), cs), (gx, gw)
+
+    return _launch(go, dev, stream, "mla_add_norm_bwd")
+
+
+# ---------------------------------------------------------------- dense causal attention
+
+def _heads(t: torch.Tensor, name: str, dev):
+    """(token stride, head stride) in elements of bf16 rows [tokens, heads, width]."""
+    shape, (tok, head, one) = t.shape, t.stride() if t.dim() == 3 else (0, 0, 0)
+    if (t.is_cuda and t.dtype is _BF16 and one == 1 and not (tok | head) & 7 and tok > 0 and head > 0
+            and not t.data_ptr() & 15 and t.device == dev):
+        return tok, head
+    _on_cuda(t, name)
+    if t.dtype != _BF16:
+        raise ValueError(f"{name} must be {_BF16}, got {t.dtype}")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [tokens, heads, width], got {tuple(shape)}")
+    _fits(t, 0, name, dev)
+    if t.numel() == 0:
+        return 0, 0
+    if one != 1:
+        raise ValueError(f"the values of a row of {name} must be contiguous")
+    tok, head = tok if shape[0] > 1 else 0, head if shape[1] > 1 else 0
+    if tok % 8 or head % 8 or t.data_ptr() % 16:
+        raise ValueError(f"rows of {name} must start on 16 bytes (strides {t.stride()})")
+    if (shape[0] > 1 and tok <= 0) or (shape[1] > 1 and head <= 0):
+        raise ValueError(f"{name} repeats rows (strides {t.stride()}); shared heads are given once")
+    return tok, head
+
+
+def _mha_args(q, k, v, cu_seqlens_q, cu_seqlens_kv):
+    """(total_q, total_kv, heads, kv heads, d_qk, d_v, batch, device, strides) of checked arguments."""
+    dev = q.device
+    steps = _heads(q, "q", dev) + _heads(k, "k", dev) + _heads(v, "v", dev)
+    total_q, h_q, d_qk = q.shape
+    total_kv, h_kv, d_k = k.shape
+    if d_k != d_qk:
+        raise ValueError(f"k has rows of {d_k} values; q of {d_qk}")
+    if tuple(v.shape[:2]) != (total_kv, h_kv):
+        raise ValueError(f"v must be [{total_kv}, {h_kv}, width], got {tuple(v.shape)}")
+    if h_kv == 0 or h_q % h_kv:
+        raise ValueError(f"{h_q} query heads do not share {h_kv} key heads evenly")
+    batch = _seq_args(cu_seqlens_q, cu_seqlens_kv, dev)
+    if cu_seqlens_q is not None and cu_seqlens_kv.numel() != batch + 1:
+        raise ValueError(f"cu_seqlens_kv holds {cu_seqlens_kv.numel()} offsets; cu_seqlens_q {batch + 1}")
+    return total_q, total_kv, h_q, h_kv, d_qk, v.shape[2], batch, dev, steps
+
+
+_MHA_FILL_OUT, _MHA_FILL_LSE = 1, 2
+
+
+def dense_mha_fwd(q, k, v, sm_scale, cu_seqlens_q=None, cu_seqlens_kv=None, out: Optional[torch.Tensor] = None,
+                  lse: Optional[torch.Tensor] = None, stream=None):
+    """Causal attention over whole prompts in the heads' own space: q [total_q, h_q,
+    192 or 128], k [total_kv, h_kv, the same], v [total_kv, h_kv, 128] bf16, rows
+    strided as they are; h_q / h_kv query heads share a key and value head.
+    cu_seqlens_q / cu_seqlens_kv int32 [batch + 1] for packed sequences (neither: one
+    sequence); a sequence's queries are its last positions.  -> (out [total_q, h_q,
+    128] bf16, lse [total_q, h_q] fp32).  Rows behind the last sequence are left as
+    they were in outputs that are given, zeros and -inf in those made here."""
+    lib = load()
+    total_q, total_kv, h_q, h_kv, d_qk, d_v, batch, dev, steps = _mha_args(q, k, v, cu_seqlens_q, cu_seqlens_kv)
+    _given(out, _BF16, "out", total_q * h_q * d_v, dev)
+    _given(lse, _F32, "lse", total_q * h_q, dev)
+    fill = (_MHA_FILL_OUT if out is None else 0) | (_MHA_FILL_LSE if lse is None else 0)
+
+    def go(cs):
+        o = torch.empty((total_q, h_q, d_v), dtype=_BF16, device=dev) if out is None else out
+        ls = torch.empty((total_q, h_q), dtype=_F32, device=dev) if lse is None else lse
+        return lib.dense_mha_fwd(q.data_ptr(), steps[0], steps[1], k.data_ptr(), steps[2], steps[3], v.data_ptr(),
+                                 steps[4], steps[5], _at(cu_seqlens_q), _at(cu_seqlens_kv), batch, sm_scale,
+                                 o.data_ptr(), ls.data_ptr(), fill, total_q, total_kv, h_q, h_kv, d_qk, d_v,
+                                 cs), (o, ls)
+
+    return _launch(go, dev, stream, "dense_mha_fwd")
+
+
+def dense_mha_bwd_workspace_size(total_q: int, total_kv: int, batch: int, h_q: int, h_kv: int, d_qk: int,
+                                 d_v: int = 128) -> int:
+    """Bytes dense_mha_bwd needs."""
+    return int(load().dense_mha_bwd_workspace_size(total_q, total_kv, batch, h_q, h_kv, d_qk, d_v))
+
+
+def dense_mha_bwd(q, k, v, sm_scale, out, lse, dout, cu_seqlens_q=None, cu_seqlens_kv=None,
+                  dq: Optional[torch.Tensor] = None, dk: Optional[torch.Tensor] = None,
+                  dv: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None, stream=None):
+    """Gradients of dense_mha_fwd from its out and lse and the gradient dout [total_q,
+    h_q, 128] bf16 of out -> (dq, dk, dv), bf16, dense, of the shapes of q, k and v.
+    Rows behind the last sequence get zeros."""
+    lib = load()
+    total_q, total_kv, h_q, h_kv, d_qk, d_v, batch, dev, steps = _mha_args(q, k, v, cu_seqlens_q, cu_seqlens_kv)
+    _given(out, _BF16, "out", total_q * h_q * d_v, dev)
+    _given(lse, _F32, "lse", total_q * h_q, dev)
+    steps += _heads(dout, "dout", dev)
+    if tuple(dout.shape) != (total_q, h_q, d_v):
+        raise ValueError(f"dout must be [{total_q}, {h_q}, {d_v}], got {tuple(dout.shape)}")
+    _given(dq, _BF16, "dq", total_q * h_q * d_qk, dev)
+    _given(dk, _BF16, "dk", total_kv * h_kv * d_qk, dev)
+    _given(dv, _BF16, "dv", total_kv * h_kv * d_v, dev)
+    _workspace(workspace, dev)
+
+    def go(cs):
+        gq = torch.empty((total_q, h_q, d_qk), dtype=_BF16, device=dev) if dq is None else dq
+        gk = torch.empty((total_kv, h_kv, d_qk), dtype=_BF16, device=dev) if dk is None else dk
+        gv = torch.empty((total_kv, h_kv, d_v), dtype=_BF16, device=dev) if dv is None else dv
+        ws = workspace
+        if ws is None:
+            need = lib.dense_mha_bwd_workspace_size(total_q, total_kv, batch, h_q, h_kv, d_qk, d_v)
+            ws = torch.empty(max(16, need), dtype=_U8, device=dev)
+        return lib.dense_mha_bwd(q.data_ptr(), steps[0], steps[1], k.data_ptr(), steps[2], steps[3], v.data_ptr(),
+                                 steps[4], steps[5], _at(cu_seqlens_q), _at(cu_seqlens_kv), batch, sm_scale,
+                                 out.data_ptr(), lse.data_ptr(), dout.data_ptr(), steps[6], steps[7], gq.data_ptr(),
+                                 gk.data_ptr(), gv.data_ptr(), total_q, total_kv, h_q, h_kv, d_qk, d_v,
+                                 ws.data_ptr(), ws.numel() * ws.element_size(), cs), (gq, gk, gv)
+
+    return _launch(go, dev, stream, "dense_mha_bwd")
 
 
 # ---------------------------------------------------------------- debug: valid entries per token

@@ -1,0 +1,277 @@
+// Entry points of the operators around a layer's dense attention: the residual norm,
+// causal attention over whole prompts in the heads' own space, and the gradients of
+// both.  It comes behind latent_api.cuh in the library's one translation unit
+// (library.cu) and uses that file's launches and sparse_mla_api.cu's checks and set-up.
+#pragma once
+#include <cmath>
+
+#include "add_norm_kernel.cuh"
+#include "dense_mha_kernel.cuh"
+
+// ------------------------------------------------------------------ residual norm
+
+namespace {
+
+bool step_ok(long long step) { return step % 8 == 0; }
+
+sparse_mla_status_t check_add_norm(const void* x, long long x_stride, const void* weight, float eps, int n, int d) {
+  if (n < 0 || d < 1 || !(eps >= 0.f) || !std::isfinite(eps) || !step_ok(x_stride)) return SPARSE_MLA_ERR_INVALID_ARG;
+  if (d % 8 != 0 || d > smla::kAddNormMaxWidth) return SPARSE_MLA_ERR_UNSUPPORTED_SHAPE;
+  if (!aligned(x, 16) || !aligned(weight, 16)) return SPARSE_MLA_ERR_INVALID_ARG;
+  if (n > 0 && (!x || !weight)) return SPARSE_MLA_ERR_INVALID_ARG;
+  return SPARSE_MLA_OK;
+}
+
+smla::AddNormParams add_norm_params(const void* x, long long x_stride, const void* weight, float eps, int n, int d) {
+  smla::AddNormParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.x = static_cast<const __nv_bfloat16*>(x);
+  p.x_step = x_stride;
+  p.weight = static_cast<const __nv_bfloat16*>(weight);
+  p.eps = eps;
+  p.n = n;
+  p.d = d;
+  auto two = [](double v) {
+    const float hi = static_cast<float>(v);
+    return smla::Two{hi, static_cast<float>(v - hi)};
+  };
+  p.sqrt_d = two(std::sqrt(static_cast<double>(d)));
+  p.d_eps = two(static_cast<double>(d) * eps);
+  return p;
+}
+
+// Vectors of 8 values per thread, and threads: whole warps that hold a row.
+int add_norm_vectors(int d) { return d <= 2048 ? 1 : (d <= 4096 ? 2 : 4); }
+int add_norm_threads(int d, int v) { return ((d / 8 + v - 1) / v + 31) / 32 * 32; }
+
+// CTAs: as many as are resident at once.
+int add_norm_ctas(int n, int threads, int sms, int warps_per_sm) {
+  const long long most = static_cast<long long>(sms) * (warps_per_sm * 32 / threads > 0 ? warps_per_sm * 32 / threads : 1);
+  return static_cast<int>(n < most ? n : most);
+}
+constexpr int kAddNormFwdWarps = 32;
+constexpr int kAddNormBwdWarps = 16;
+
+}  // namespace
+
+extern "C" {
+
+sparse_mla_status_t mla_add_norm(const void* x, long long x_stride, const void* residual, long long residual_stride,
+                                 const void* weight, float eps, void* out, float* scales, int out_format,
+                                 void* residual_out, int n, int d, void* stream) {
+  sparse_mla_status_t st = check_add_norm(x, x_stride, weight, eps, n, d);
+  if (st != SPARSE_MLA_OK) return st;
+  if (out_format < MLA_ADD_NORM_BF16 || out_format > MLA_ADD_NORM_E4M3_ROW) return SPARSE_MLA_ERR_INVALID_ARG;
+  if (!step_ok(residual_stride) || !aligned(residual, 16) || !aligned(residual_out, 16) || !aligned(out, 16) ||
+      !aligned(scales, 4))
+    return SPARSE_MLA_ERR_INVALID_ARG;
+  if (n > 0 && (!out || (residual && !residual_out) || (out_format != MLA_ADD_NORM_BF16 && !scales)))
+    return SPARSE_MLA_ERR_INVALID_ARG;
+  int sms = 0;
+  if ((st = device_setup(&sms)) != SPARSE_MLA_OK) return st;
+  if (n == 0) return SPARSE_MLA_OK;
+  smla::AddNormParams p = add_norm_params(x, x_stride, weight, eps, n, d);
+  p.residual = static_cast<const __nv_bfloat16*>(residual);
+  p.residual_step = residual_stride;
+  p.z = static_cast<__nv_bfloat16*>(residual_out);
+  p.out = out;
+  p.scales = scales;
+  p.form = out_format;
+  const int v = add_norm_vectors(d), threads = add_norm_threads(d, v);
+  const int ctas = add_norm_ctas(n, threads, sms, kAddNormFwdWarps);
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  if (v == 1) smla::add_norm_kernel<1><<<ctas, threads, 0, cs>>>(p);
+  else if (v == 2) smla::add_norm_kernel<2><<<ctas, threads, 0, cs>>>(p);
+  else smla::add_norm_kernel<4><<<ctas, threads, 0, cs>>>(p);
+  return cudaGetLastError() == cudaSuccess ? SPARSE_MLA_OK : SPARSE_MLA_ERR_CUDA;
+}
+
+size_t mla_add_norm_bwd_workspace_size(int n, int d) {
+  if (n < 1 || d < 8 || d % 8 != 0 || d > smla::kAddNormMaxWidth) return 0;
+  int sms = 0;
+  if (device_setup(&sms) != SPARSE_MLA_OK) return 0;
+  const int ctas = add_norm_ctas(n, add_norm_threads(d, add_norm_vectors(d)), sms, kAddNormBwdWarps);
+  return static_cast<size_t>(ctas) * static_cast<size_t>(d) * sizeof(float);   // one share of the sums per CTA
+}
+
+sparse_mla_status_t mla_add_norm_bwd(const void* z, long long z_stride, const void* weight, float eps,
+                                     const void* dout, long long dout_stride, const void* dresidual,
+                                     long long dresidual_stride, void* dx, float* dweight, int n, int d,
+                                     void* workspace, size_t workspace_bytes, void* stream) {
+  sparse_mla_status_t st = check_add_norm(z, z_stride, weight, eps, n, d);
+  if (st != SPARSE_MLA_OK) return st;
+  if (!step_ok(dout_stride) || !step_ok(dresidual_stride) || !aligned(dout, 16) || !aligned(dresidual, 16) ||
+      !aligned(dx, 16) || !aligned(dweight, 4) || !dweight)
+    return SPARSE_MLA_ERR_INVALID_ARG;
+  if (n > 0 && (!dout || !dx)) return SPARSE_MLA_ERR_INVALID_ARG;
+  int sms = 0;
+  if ((st = device_setup(&sms)) != SPARSE_MLA_OK) return st;
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  if (n == 0)
+    return cudaMemsetAsync(dweight, 0, static_cast<size_t>(d) * sizeof(float), cs) == cudaSuccess
+               ? SPARSE_MLA_OK : SPARSE_MLA_ERR_CUDA;
+  if (!workspace || workspace_bytes < mla_add_norm_bwd_workspace_size(n, d)) return SPARSE_MLA_ERR_WORKSPACE_TOO_SMALL;
+  if (!aligned(workspace, 16)) return SPARSE_MLA_ERR_INVALID_ARG;
+  smla::AddNormParams p = add_norm_params(z, z_stride, weight, eps, n, d);
+  p.dout = static_cast<const __nv_bfloat16*>(dout);
+  p.dout_step = dout_stride;
+  p.dresidual = static_cast<const __nv_bfloat16*>(dresidual);
+  p.dresidual_step = dresidual_stride;
+  p.dx = static_cast<__nv_bfloat16*>(dx);
+  p.part = static_cast<float*>(workspace);
+  const int v = add_norm_vectors(d), threads = add_norm_threads(d, v);
+  const int ctas = add_norm_ctas(n, threads, sms, kAddNormBwdWarps);
+  if (v == 1) smla::add_norm_bwd_kernel<1><<<ctas, threads, 0, cs>>>(p);
+  else if (v == 2) smla::add_norm_bwd_kernel<2><<<ctas, threads, 0, cs>>>(p);
+  else smla::add_norm_bwd_kernel<4><<<ctas, threads, 0, cs>>>(p);
+  if (cudaGetLastError() != cudaSuccess) return SPARSE_MLA_ERR_CUDA;
+  const cudaError_t e = launch_dependent(smla::add_norm_weight_grad_kernel, dim3(static_cast<unsigned>((d + 31) / 32)),
+                                         dim3(1024), cs, static_cast<const float*>(p.part), dweight, ctas, d);
+  return e == cudaSuccess ? SPARSE_MLA_OK : SPARSE_MLA_ERR_CUDA;
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------------------ dense causal attention
+
+namespace {
+
+struct MhaRows {   // an operand as the caller gives it: row (t, h) at p + t tok + h head
+  const void* p;
+  long long tok, head;
+};
+
+bool mha_rows_ok(const MhaRows& r, int total, int heads) {
+  return aligned(r.p, 16) && step_ok(r.tok) && step_ok(r.head) && (total < 2 || r.tok > 0) && (heads < 2 || r.head > 0);
+}
+
+sparse_mla_status_t check_mha(const MhaRows& q, const MhaRows& k, const MhaRows& v, const int32_t* cu_q,
+                              const int32_t* cu_kv, int batch, float sm_scale, int total_q, int total_kv, int h_q,
+                              int h_kv, int d_qk, int d_v) {
+  if (total_q < 0 || total_kv < 0 || h_q < 1 || h_kv < 1 || h_q % h_kv != 0 || !(sm_scale >= 0.f) ||
+      !std::isfinite(sm_scale))
+    return SPARSE_MLA_ERR_INVALID_ARG;
+  if ((d_qk != 192 && d_qk != 128) || d_v != 128) return SPARSE_MLA_ERR_UNSUPPORTED_SHAPE;
+  if (total_q > INT_MAX / 2 || total_kv > INT_MAX / 2 || h_q > 65535) return SPARSE_MLA_ERR_INVALID_ARG;
+  if ((cu_q == nullptr) != (cu_kv == nullptr)) return SPARSE_MLA_ERR_INVALID_ARG;
+  if (cu_q && (batch < 1 || batch > INT_MAX / 2 || !aligned(cu_q, 4) || !aligned(cu_kv, 4)))
+    return SPARSE_MLA_ERR_INVALID_ARG;
+  if (!mha_rows_ok(q, total_q, h_q) || !mha_rows_ok(k, total_kv, h_kv) || !mha_rows_ok(v, total_kv, h_kv))
+    return SPARSE_MLA_ERR_INVALID_ARG;
+  if ((total_q > 0 && !q.p) || (total_kv > 0 && (!k.p || !v.p))) return SPARSE_MLA_ERR_INVALID_ARG;
+  return SPARSE_MLA_OK;
+}
+
+smla::MhaParams mha_params(const MhaRows& q, const MhaRows& k, const MhaRows& v, const int32_t* cu_q,
+                           const int32_t* cu_kv, int batch, float sm_scale, int total_q, int total_kv, int h_q,
+                           int h_kv) {
+  smla::MhaParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.q = static_cast<const __nv_bfloat16*>(q.p);
+  p.q_tok = q.tok;
+  p.q_head = q.head;
+  p.k = static_cast<const __nv_bfloat16*>(k.p);
+  p.k_tok = k.tok;
+  p.k_head = k.head;
+  p.v = static_cast<const __nv_bfloat16*>(v.p);
+  p.v_tok = v.tok;
+  p.v_head = v.head;
+  p.cu_q = cu_q;
+  p.cu_kv = cu_kv;
+  p.batch = cu_q ? batch : 1;
+  p.total_q = total_q;
+  p.total_kv = total_kv;
+  p.h_q = h_q;
+  p.h_kv = h_kv;
+  p.scale = sm_scale;
+  return p;
+}
+
+int mha_ctas(long long rows) { return static_cast<int>(rows < 8 * 65536LL ? (rows + 7) / 8 : 65536); }
+
+}  // namespace
+
+extern "C" {
+
+sparse_mla_status_t dense_mha_fwd(const void* q, long long q_tok_stride, long long q_head_stride, const void* k,
+                                  long long k_tok_stride, long long k_head_stride, const void* v,
+                                  long long v_tok_stride, long long v_head_stride, const int32_t* cu_seqlens_q,
+                                  const int32_t* cu_seqlens_kv, int batch, float sm_scale, void* out, float* lse,
+                                  int fill, int total_q, int total_kv, int h_q, int h_kv, int d_qk, int d_v,
+                                  void* stream) {
+  const MhaRows rq = {q, q_tok_stride, q_head_stride}, rk = {k, k_tok_stride, k_head_stride},
+                rv = {v, v_tok_stride, v_head_stride};
+  sparse_mla_status_t st = check_mha(rq, rk, rv, cu_seqlens_q, cu_seqlens_kv, batch, sm_scale, total_q, total_kv, h_q,
+                                     h_kv, d_qk, d_v);
+  if (st != SPARSE_MLA_OK) return st;
+  if (fill < 0 || fill > 3 || !aligned(out, 16) || !aligned(lse, 4) || (total_q > 0 && (!out || !lse)))
+    return SPARSE_MLA_ERR_INVALID_ARG;
+  int sms = 0;
+  if ((st = device_setup(&sms)) != SPARSE_MLA_OK) return st;
+  if (total_q == 0) return SPARSE_MLA_OK;
+  smla::MhaParams p = mha_params(rq, rk, rv, cu_seqlens_q, cu_seqlens_kv, batch, sm_scale, total_q, total_kv, h_q, h_kv);
+  p.out = static_cast<__nv_bfloat16*>(out);
+  p.lse = lse;
+  p.fill = fill;
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  const int ctas = mha_ctas(static_cast<long long>(total_q) * h_q);
+  if (d_qk == 192) smla::dense_mha_fwd_kernel<3><<<ctas, 256, 0, cs>>>(p);
+  else smla::dense_mha_fwd_kernel<2><<<ctas, 256, 0, cs>>>(p);
+  return cudaGetLastError() == cudaSuccess ? SPARSE_MLA_OK : SPARSE_MLA_ERR_CUDA;
+}
+
+size_t dense_mha_bwd_workspace_size(int total_q, int total_kv, int batch, int h_q, int h_kv, int d_qk, int d_v) {
+  (void)batch, (void)d_qk, (void)d_v;
+  if (total_q < 1 || total_kv < 0 || h_q < 1 || h_kv < 1) return 0;
+  return static_cast<size_t>(total_q) * static_cast<size_t>(h_q) * sizeof(float);
+}
+
+sparse_mla_status_t dense_mha_bwd(const void* q, long long q_tok_stride, long long q_head_stride, const void* k,
+                                  long long k_tok_stride, long long k_head_stride, const void* v,
+                                  long long v_tok_stride, long long v_head_stride, const int32_t* cu_seqlens_q,
+                                  const int32_t* cu_seqlens_kv, int batch, float sm_scale, const void* out,
+                                  const float* lse, const void* dout, long long dout_tok_stride,
+                                  long long dout_head_stride, void* dq, void* dk, void* dv, int total_q, int total_kv,
+                                  int h_q, int h_kv, int d_qk, int d_v, void* workspace, size_t workspace_bytes,
+                                  void* stream) {
+  const MhaRows rq = {q, q_tok_stride, q_head_stride}, rk = {k, k_tok_stride, k_head_stride},
+                rv = {v, v_tok_stride, v_head_stride}, rg = {dout, dout_tok_stride, dout_head_stride};
+  sparse_mla_status_t st = check_mha(rq, rk, rv, cu_seqlens_q, cu_seqlens_kv, batch, sm_scale, total_q, total_kv, h_q,
+                                     h_kv, d_qk, d_v);
+  if (st != SPARSE_MLA_OK) return st;
+  if (!mha_rows_ok(rg, total_q, h_q) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(dq, 16) || !aligned(dk, 16) ||
+      !aligned(dv, 16))
+    return SPARSE_MLA_ERR_INVALID_ARG;
+  if ((total_q > 0 && (!out || !lse || !dout || !dq)) || (total_kv > 0 && (!dk || !dv))) return SPARSE_MLA_ERR_INVALID_ARG;
+  int sms = 0;
+  if ((st = device_setup(&sms)) != SPARSE_MLA_OK) return st;
+  const size_t need = dense_mha_bwd_workspace_size(total_q, total_kv, batch, h_q, h_kv, d_qk, d_v);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return SPARSE_MLA_ERR_WORKSPACE_TOO_SMALL;
+  if (!aligned(workspace, 16)) return SPARSE_MLA_ERR_INVALID_ARG;
+  smla::MhaParams p = mha_params(rq, rk, rv, cu_seqlens_q, cu_seqlens_kv, batch, sm_scale, total_q, total_kv, h_q, h_kv);
+  p.out = static_cast<__nv_bfloat16*>(const_cast<void*>(out));
+  p.lse = const_cast<float*>(lse);
+  p.dout = static_cast<const __nv_bfloat16*>(dout);
+  p.do_tok = dout_tok_stride;
+  p.do_head = dout_head_stride;
+  p.dq = static_cast<__nv_bfloat16*>(dq);
+  p.dk = static_cast<__nv_bfloat16*>(dk);
+  p.dv = static_cast<__nv_bfloat16*>(dv);
+  p.delta = static_cast<float*>(workspace);
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  if (total_q > 0) {
+    const int ctas = mha_ctas(static_cast<long long>(total_q) * h_q);
+    if (d_qk == 192) smla::dense_mha_dq_kernel<3><<<ctas, 256, 0, cs>>>(p);
+    else smla::dense_mha_dq_kernel<2><<<ctas, 256, 0, cs>>>(p);
+    if (cudaGetLastError() != cudaSuccess) return SPARSE_MLA_ERR_CUDA;
+  }
+  if (total_kv > 0) {
+    const int ctas = mha_ctas(static_cast<long long>(total_kv) * h_kv);
+    if (d_qk == 192) smla::dense_mha_dkv_kernel<3><<<ctas, 256, 0, cs>>>(p);
+    else smla::dense_mha_dkv_kernel<2><<<ctas, 256, 0, cs>>>(p);
+    if (cudaGetLastError() != cudaSuccess) return SPARSE_MLA_ERR_CUDA;
+  }
+  return SPARSE_MLA_OK;
+}
+
+}  // extern "C"
