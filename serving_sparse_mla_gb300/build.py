@@ -17,7 +17,7 @@ LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
 SOURCES = ["library.cu"]
 DEPS = ["library.cu", "sparse_mla_api.cu", "latent_api.cuh", "fwd_kernel.cuh", "bwd_kernel.cuh", "indexer_kernel.cuh",
         "fp4_decode_kernel.cuh", "norm_rope_kernel.cuh", "layer_api.cuh", "add_norm_kernel.cuh", "dense_mha_kernel.cuh",
-        "ptx.cuh"]
+        "dense_mha_bwd_kernel.cuh", "ptx.cuh"]
 
 
 def nvcc_path() -> str:

@@ -1,199 +1,613 @@
-// Causal attention over whole prompts in the heads' own space, and its gradients.
+// Causal attention over whole prompts in the heads' own space (tcgen05 + TMA).
 //
 //   s_ij = scale q_i . k_j  over the keys j that query i sees,
 //   lse_i = ln sum_j exp(s_ij),   out_i = sum_j exp(s_ij - lse_i) v_j
 //
 // A sequence's lq queries are the last lq of its lk positions: local query i sees keys
 // 0 .. i + lk - lq.  h_q / h_kv query heads share a key and value head.
+//
+// A CTA takes NT tiles of 128 query rows against all keys that they see, 128 at a time.
+// A tile's rows are (token, head) pairs: `pack` heads of one group side by side, so that
+// a group of query heads reads its keys once and few tokens still fill a tile.
+//
+//   warps 0 .. 4 NT - 1  softmax, a thread per row: S from TMEM, running maximum and
+//                        sum, P (bf16) back into the same TMEM columns; the epilogue
+//   warp 4 NT            one thread issues the MMAs:
+//                          S_t = Q_t K_j^T   (both operands in shared memory)
+//                          O_t += P_t V_j    (P_t in TMEM)
+//   warp 4 NT + 1        one thread issues the TMA loads: Q once, then K and V through
+//                        a ring of 16 KB units (K: 128 keys x 64 columns, V: 64 keys x
+//                        128 columns)
+//
+// With two tiles the tensor core works on one while the softmax works on the other.  O
+// is rescaled only when a row's maximum has grown by more than 2^8: until then the
+// weights are relative to the older maximum, which the sum and the LSE take into
+// account exactly.  P is rounded to bf16 for the product (2^-8 of each weight at most);
+// scores, sums and O are fp32.
+//
+// All waits are bounded; a CTA that times out records an error, waits (bounded) for its
+// copies and MMAs in flight, frees TMEM and returns.
 #pragma once
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cstdint>
 
+#include "fwd_kernel.cuh"
 #include "norm_rope_kernel.cuh"
 #include "ptx.cuh"
 
 namespace smla {
 
-struct MhaParams {
-  const __nv_bfloat16 *q, *k, *v;          // row (t, h) at q + t q_tok + h q_head
-  long long q_tok, q_head, k_tok, k_head, v_tok, v_head;
-  const int32_t *cu_q, *cu_kv;             // [batch + 1], null for one dense sequence
-  int batch, total_q, total_kv, h_q, h_kv;
-  float scale;
-  __nv_bfloat16* out;                      // [total_q, h_q, d_v]
-  float* lse;                              // [total_q, h_q]
-  int fill;                                // rows of no sequence: 1 out is zero, 2 lse is -inf
-  // backward
-  const __nv_bfloat16* dout;
-  long long do_tok, do_head;
-  __nv_bfloat16 *dq, *dk, *dv;             // [total, h, d]
-  float* delta;                            // [total_q, h_q]: rowsum(dout out)
+constexpr int kMhaTile = 128;              // query rows of a tile, keys of a block
+constexpr int kMhaDv = 128;
+constexpr uint32_t kMhaUnit = 16384;       // bytes of a ring unit, and of 64 columns of a Q tile
+constexpr float kMhaLazy = 8.f;            // log2 of the growth of a maximum that O is rescaled for
+
+enum MhaErrCode : int {
+  kErrMhaLoadWait = 0x701,
+  kErrMhaMmaWait = 0x702,
+  kErrMhaSoftmaxWait = 0x703,
 };
 
-// Offsets of sequence b within [0, total], whatever the array holds.
+struct MhaFwdParams {
+  CUtensorMap map_q, map_k, map_v;         // [token, head, d]: boxes 64 x pack x tok_tile, 64 x 1 x 128, 64 x 1 x 64
+  const int32_t *cu_q, *cu_kv;             // [batch + 1], null for one dense sequence
+  int batch, total_q, total_kv, h_q, group; // query heads per key head
+  int pack, tok_tile;                      // a tile is tok_tile tokens x pack heads
+  int slots;                               // tiles (of NT) per head pack that the grid has room for
+  float scale_log2;
+  const __nv_bfloat16* v;                  // row (t, h) at v + t v_tok + h v_head
+  long long v_tok, v_head;
+  __nv_bfloat16* out;                      // [total_q, h_q, 128]
+  float* lse;                              // [total_q, h_q]
+  int fill;                                // rows of no sequence: 1 out is zero, 2 lse is -inf
+  unsigned long long timeout_ns;
+};
+
+// ------------------------------------------------------------------ sequences
+
+// Offset b of `cu` within [0, total], whatever the array holds.
 __device__ __forceinline__ int mha_offset(const int32_t* cu, int b, int total) {
   const int c = __ldg(cu + b);
   return c < 0 ? 0 : (c > total ? total : c);
 }
 
-struct MhaSeq {
-  int q0, q1, k0, k1;
+// The rows of a sequence, and of one CTA's tile among those of one side.
+struct MhaWork {
+  int q0, q1, k0, k1;   // q1 <= q0: nothing to do
+  int tile;             // from the sequence's first row
+  int rest;             // rows behind the last sequence (k0 = k1 = 0)
 };
 
-__device__ __forceinline__ MhaSeq mha_seq(const MhaParams& p, int b) {
-  if (p.cu_q == nullptr) return {0, p.total_q, 0, p.total_kv};
-  MhaSeq s;
-  s.q0 = mha_offset(p.cu_q, b, p.total_q);
-  s.q1 = max(s.q0, mha_offset(p.cu_q, b + 1, p.total_q));
-  s.k0 = mha_offset(p.cu_kv, b, p.total_kv);
-  s.k1 = max(s.k0, mha_offset(p.cu_kv, b + 1, p.total_kv));
-  return s;
-}
-
-// The sequence that holds row r of the offsets `cu` (the last b with cu[b] <= r), or -1.
-__device__ __forceinline__ int mha_seq_of(const int32_t* cu, int batch, int r) {
-  if (cu == nullptr) return 0;
-  int lo = 0, hi = batch - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (__ldg(cu + mid) <= r) lo = mid;
-    else hi = mid - 1;
+// Tile `slot` of all sequences' tiles of `per` rows (of the queries, or of the keys with
+// `keys`), laid end to end, a sequence's last tile first: that is its longest under the
+// causal mask for queries (and its shortest for keys, so there the first comes first).
+// Behind them come the rows of no sequence where `rest` is set.  One warp, all lanes.
+__device__ __forceinline__ MhaWork mha_find(const int32_t* cu_q, const int32_t* cu_kv, int batch, int total_q,
+                                            int total_kv, int slot, int per, bool keys, bool rest) {
+  MhaWork w = {0, 0, 0, 0, 0, 0};
+  if (cu_q == nullptr) {
+    w.q1 = total_q;
+    w.k1 = total_kv;
+    const int tiles = ((keys ? total_kv : total_q) + per - 1) / per;
+    w.tile = keys ? slot : tiles - 1 - slot;
+    if (slot >= tiles) w.q1 = w.k1 = 0;
+    return w;
   }
-  return __ldg(cu + lo) <= r && r < __ldg(cu + lo + 1) ? lo : -1;
-}
-
-// A row of N * 64 values, two per lane and 64.
-template <int N>
-__device__ __forceinline__ void mha_row(const __nv_bfloat16* row, int lane, float (&x)[2 * N]) {
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const uint32_t v = *reinterpret_cast<const uint32_t*>(row + 64 * i + 2 * lane);
-    x[2 * i] = bf16_lo(v);
-    x[2 * i + 1] = bf16_hi(v);
-  }
-}
-
-template <int N>
-__device__ __forceinline__ void mha_store(__nv_bfloat16* row, int lane, const float (&x)[2 * N], float f) {
-#pragma unroll
-  for (int i = 0; i < N; ++i)
-    *reinterpret_cast<uint32_t*>(row + 64 * i + 2 * lane) = pack_bf16x2(x[2 * i] * f, x[2 * i + 1] * f);
-}
-
-template <int N>
-__device__ __forceinline__ float mha_dot(const float (&a)[2 * N], const float (&b)[2 * N]) {
-  float s = 0.f;
-#pragma unroll
-  for (int i = 0; i < 2 * N; ++i) s += a[i] * b[i];
-  return warp_sum(s);
-}
-
-// One warp per (query row, head).
-template <int NQK>
-__global__ void __launch_bounds__(256) dense_mha_fwd_kernel(const __grid_constant__ MhaParams p) {
   const int lane = static_cast<int>(lane_id());
-  const long long rows = static_cast<long long>(p.total_q) * p.h_q, step = static_cast<long long>(gridDim.x) * 8;
-  for (long long r = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5); r < rows; r += step) {
-    const int t = static_cast<int>(r / p.h_q), h = static_cast<int>(r % p.h_q);
-    float acc[4] = {0.f, 0.f, 0.f, 0.f};
-    const int b = mha_seq_of(p.cu_q, p.batch, t);
-    if (b < 0) {
-      if (p.fill & 1) mha_store<2>(p.out + r * 128, lane, acc, 0.f);
-      if ((p.fill & 2) && lane == 0) p.lse[r] = -INFINITY;
-      continue;
+  int before = 0, end = 0;   // tiles of the sequences so far, the largest end of their rows
+  for (int base = 0; base < batch; base += 32) {
+    const int b = base + lane;
+    int q0 = 0, q1 = 0, k0 = 0, k1 = 0;
+    if (b < batch) {
+      q0 = mha_offset(cu_q, b, total_q);
+      q1 = max(q0, mha_offset(cu_q, b + 1, total_q));
+      k0 = mha_offset(cu_kv, b, total_kv);
+      k1 = max(k0, mha_offset(cu_kv, b + 1, total_kv));
     }
-    const MhaSeq s = mha_seq(p, b);
-    const int lk = s.k1 - s.k0;
-    const int sees = min(lk, t - s.q0 + lk - (s.q1 - s.q0) + 1);
-    float q[2 * NQK], k[2 * NQK], v[4], top = -INFINITY, sum = 0.f;
-    mha_row<NQK>(p.q + t * p.q_tok + h * p.q_head, lane, q);
-    const int hk = h / (p.h_q / p.h_kv);
-    for (int j = 0; j < sees; ++j) {
-      mha_row<NQK>(p.k + (s.k0 + j) * p.k_tok + hk * p.k_head, lane, k);
-      mha_row<2>(p.v + (s.k0 + j) * p.v_tok + hk * p.v_head, lane, v);
-      const float z = mha_dot<NQK>(q, k) * p.scale;
-      const float up = fmaxf(top, z);
-      const float old = top == -INFINITY ? 0.f : __expf(top - up), e = up == -INFINITY ? 0.f : __expf(z - up);
-      top = up;
-      sum = sum * old + e;
+    const int tiles = ((keys ? k1 - k0 : q1 - q0) + per - 1) / per;
+    int incl = tiles;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) acc[i] = acc[i] * old + e * v[i];
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
     }
-    mha_store<2>(p.out + r * 128, lane, acc, sum == 0.f ? 0.f : 1.f / sum);
-    if (lane == 0) p.lse[r] = sum == 0.f ? -INFINITY : top + logf(sum);
+    const uint32_t past = __ballot_sync(0xffffffffu, before + incl > slot);
+    if (past != 0u) {
+      const int at = __ffs(past) - 1;
+      w.q0 = __shfl_sync(0xffffffffu, q0, at);
+      w.q1 = __shfl_sync(0xffffffffu, q1, at);
+      w.k0 = __shfl_sync(0xffffffffu, k0, at);
+      w.k1 = __shfl_sync(0xffffffffu, k1, at);
+      const int first = before + __shfl_sync(0xffffffffu, incl - tiles, at);
+      w.tile = keys ? slot - first : first + __shfl_sync(0xffffffffu, tiles, at) - 1 - slot;
+      return w;
+    }
+    before += __shfl_sync(0xffffffffu, incl, 31);
+    end = max(end, __reduce_max_sync(0xffffffffu, keys ? k1 : q1));
   }
+  const int total = keys ? total_kv : total_q;
+  const int tile = slot - before;
+  if (rest && tile < (total - end + per - 1) / per) {
+    if (keys) {
+      w.k0 = end;
+      w.k1 = total;
+    } else {
+      w.q0 = end;
+      w.q1 = total;
+    }
+    w.tile = tile;
+    w.rest = 1;
+  }
+  return w;
 }
 
-// One warp per (query row, head): D = rowsum(dout out) and dq.
-template <int NQK>
-__global__ void __launch_bounds__(256) dense_mha_dq_kernel(const __grid_constant__ MhaParams p) {
-  const int lane = static_cast<int>(lane_id());
-  const long long rows = static_cast<long long>(p.total_q) * p.h_q, step = static_cast<long long>(gridDim.x) * 8;
-  for (long long r = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5); r < rows; r += step) {
-    const int t = static_cast<int>(r / p.h_q), h = static_cast<int>(r % p.h_q);
-    float acc[2 * NQK];
+// ------------------------------------------------------------------ PTX
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, int x, int y, int z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+      ::"r"(dst), "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+
+// D[tmem] (+)= A[tmem] * B[smem]: A's row i in lane i, two bf16 values per column.
+__device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                            uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+      ::"r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// (a0, a1) * b + c, packed.
+__device__ __forceinline__ void scale_shift2(float& a0, float& a1, float b, float c) {
+  asm("{\n\t.reg .b64 pa, pb, pc;\n\t"
+      "mov.b64 pa, {%0, %1};\n\t"
+      "mov.b64 pb, {%2, %2};\n\t"
+      "mov.b64 pc, {%3, %3};\n\t"
+      "fma.rn.f32x2 pa, pa, pb, pc;\n\t"
+      "mov.b64 {%0, %1}, pa;\n\t}"
+      : "+f"(a0), "+f"(a1)
+      : "f"(b), "f"(c));
+}
+
+__device__ __forceinline__ void add2(float& a0, float& a1, float b0, float b1) {
+  asm("{\n\t.reg .b64 pa, pb;\n\t"
+      "mov.b64 pa, {%0, %1};\n\t"
+      "mov.b64 pb, {%2, %3};\n\t"
+      "add.rn.f32x2 pa, pa, pb;\n\t"
+      "mov.b64 {%0, %1}, pa;\n\t}"
+      : "+f"(a0), "+f"(a1)
+      : "f"(b0), "f"(b1));
+}
+
+// ------------------------------------------------------------------ forward
+
+constexpr int kMhaMaxUnits = 12;
+
+struct __align__(16) MhaMisc {
+  uint64_t q_full[2], full[kMhaMaxUnits], empty[kMhaMaxUnits], s_full[2], p_full[2], o_full[2], drain;
+  uint32_t tmem_base;
+  int abort_flag;
+  int prior_error;
+  int cleared;   // values of V that are not finite were taken out of a block that some rows do not see all of
+  MhaWork work;
+};
+
+// Shared memory: Q (NT tiles), then the ring.
+template <int DQK, int NT>
+struct MhaFwdShape {
+  static constexpr int kSub = DQK / 64;                        // 64-column units of a K block or Q tile
+  static constexpr uint32_t kQBytes = NT * kSub * kMhaUnit;
+  static constexpr int kFree = kMaxSmem - 1024 - static_cast<int>(sizeof(MhaMisc)) - static_cast<int>(kQBytes);
+  static constexpr int kUnits = kFree / static_cast<int>(kMhaUnit) < kMhaMaxUnits ? kFree / static_cast<int>(kMhaUnit)
+                                                                                   : kMhaMaxUnits;
+  static constexpr uint32_t kMiscOff = kQBytes + kUnits * kMhaUnit;
+  static constexpr int kBytes = static_cast<int>(kMiscOff) + static_cast<int>(sizeof(MhaMisc)) + 1024;
+  static constexpr int kThreads = NT * 128 + 64;               // two tiles: 200 registers each, no more than their rows take
+  static constexpr int kTmemCols = NT * 256;
+  static_assert(kUnits >= kSub + 4, "a K block and two V blocks");
+  static_assert(kBytes <= kMaxSmem, "shared memory");
+};
+
+// What one CTA does: keys' blocks of each of its tiles.
+template <int NT>
+struct MhaSpan {
+  int t0[NT];      // first token of the tile, in the sequence
+  int blocks[NT];  // blocks of 128 keys that its rows see
+  int most;
+  __device__ __forceinline__ MhaSpan(const MhaFwdParams& p, const MhaWork& w) {
+    const int lq = w.q1 - w.q0, lk = w.k1 - w.k0;
+    most = 0;
 #pragma unroll
-    for (int i = 0; i < 2 * NQK; ++i) acc[i] = 0.f;
-    const int b = mha_seq_of(p.cu_q, p.batch, t);
-    if (b >= 0) {
-      const MhaSeq s = mha_seq(p, b);
-      const int lk = s.k1 - s.k0;
-      const int sees = min(lk, t - s.q0 + lk - (s.q1 - s.q0) + 1);
-      float q[2 * NQK], k[2 * NQK], v[4], g[4], o[4];
-      mha_row<NQK>(p.q + t * p.q_tok + h * p.q_head, lane, q);
-      mha_row<2>(p.dout + t * p.do_tok + h * p.do_head, lane, g);
-      mha_row<2>(p.out + r * 128, lane, o);
-      const float delta = mha_dot<2>(g, o), lse = p.lse[r];
-      if (lane == 0) p.delta[r] = delta;
-      const int hk = h / (p.h_q / p.h_kv);
-      for (int j = 0; j < sees; ++j) {
-        mha_row<NQK>(p.k + (s.k0 + j) * p.k_tok + hk * p.k_head, lane, k);
-        mha_row<2>(p.v + (s.k0 + j) * p.v_tok + hk * p.v_head, lane, v);
-        const float e = __expf(mha_dot<NQK>(q, k) * p.scale - lse);
-        const float ds = e * (mha_dot<2>(g, v) - delta);
+    for (int t = 0; t < NT; ++t) {
+      t0[t] = (w.tile * NT + t) * p.tok_tile;
+      const int last = min(t0[t] + p.tok_tile, lq) - 1;
+      const int sees = t0[t] < lq ? last + lk - lq + 1 : 0;   // of its last row
+      blocks[t] = sees > 0 ? (sees + kMhaTile - 1) / kMhaTile : 0;
+      most = max(most, blocks[t]);
+    }
+  }
+};
+
+__device__ __forceinline__ void mha_raise(MhaMisc& m, int code) {
+  *reinterpret_cast<volatile int*>(&m.abort_flag) = 1;
+  atomicCAS(&g_device_error, 0, code);
+}
+
+// A position in the ring: its unit and the parity of that unit's fill.
+template <int UNITS>
+struct MhaRing {
+  uint32_t at = 0, turn = 0;
+  __device__ __forceinline__ void next() {
+    if (++at == UNITS) {
+      at = 0;
+      turn ^= 1u;
+    }
+  }
+};
+
+template <int DQK, int NT>
+__device__ __forceinline__ bool mha_load(const MhaFwdParams& p, MhaMisc& m, uint32_t sb, const MhaWork& w,
+                                         const MhaSpan<NT>& s, int pack0, int kvh, uint32_t& fills) {
+  using C = MhaFwdShape<DQK, NT>;
+  const volatile int* ab = &m.abort_flag;
+  const uint64_t deadline = global_timer_ns() + p.timeout_ns;
+  MhaRing<C::kUnits> r;
+  auto take = [&]() -> bool {
+    return mbar_wait(smem_u32(&m.empty[r.at]), r.turn ^ 1u, deadline, ab);
+  };
+  auto load_k = [&](int j) -> bool {
+    for (int c = 0; c < C::kSub; ++c) {
+      if (!take()) return false;
+      const uint32_t bar = smem_u32(&m.full[r.at]);
+      mbar_arrive_expect_tx(bar, kMhaUnit);
+      tma_load_3d(sb + C::kQBytes + r.at * kMhaUnit, &p.map_k, 64 * c, kvh, w.k0 + j * kMhaTile, bar);
+      ++fills;
+      r.next();
+    }
+    return true;
+  };
+  auto load_q = [&](int t) {
+    const uint32_t bar = smem_u32(&m.q_full[t]);
+    const uint32_t bytes = static_cast<uint32_t>(p.pack * p.tok_tile) * 128u;
+    mbar_arrive_expect_tx(bar, C::kSub * bytes);
+    for (int c = 0; c < C::kSub; ++c)
+      tma_load_3d(sb + (t * C::kSub + c) * kMhaUnit, &p.map_q, 64 * c, pack0, w.q0 + s.t0[t], bar);
+  };
+  if (s.blocks[0] > 0) load_q(0);
+  if (!load_k(0)) return false;
+  if (NT > 1 && s.blocks[NT - 1] > 0) load_q(NT - 1);
+  for (int j = 0; j < s.most; ++j) {
+    for (int c = 0; c < 2; ++c) {
+      if (!take()) return false;
+      const uint32_t bar = smem_u32(&m.full[r.at]), dst = sb + C::kQBytes + r.at * kMhaUnit;
+      mbar_arrive_expect_tx(bar, kMhaUnit);
+      tma_load_3d(dst, &p.map_v, 0, kvh, w.k0 + j * kMhaTile + 64 * c, bar);
+      tma_load_3d(dst + kMhaUnit / 2, &p.map_v, 64, kvh, w.k0 + j * kMhaTile + 64 * c, bar);
+      ++fills;
+      r.next();
+    }
+    if (j + 1 < s.most && !load_k(j + 1)) return false;
+  }
+  return true;
+}
+
+template <int DQK, int NT>
+__device__ __forceinline__ bool mha_mma(const MhaFwdParams& p, MhaMisc& m, uint32_t sb, uint32_t tmem,
+                                        const MhaSpan<NT>& s) {
+  using C = MhaFwdShape<DQK, NT>;
+  constexpr uint32_t kIdescS = idesc_bf16_f32(kMhaTile, kMhaTile, false, false);
+  constexpr uint32_t kIdescO = idesc_bf16_f32(kMhaTile, kMhaDv, false, true);
+  const volatile int* ab = &m.abort_flag;
+  const uint64_t deadline = global_timer_ns() + p.timeout_ns;
+  MhaRing<C::kUnits> rk, rv;   // where the K block in use, and the V block, start
+  auto wait_unit = [&](const MhaRing<C::kUnits>& r) -> bool {
+    return mbar_wait(smem_u32(&m.full[r.at]), r.turn, deadline, ab);
+  };
+  // S_t = Q_t K^T of the block at `r`; `first`: its units have not been waited for, `last`: they are free behind it
+  auto scores = [&](int t, MhaRing<C::kUnits> r, bool first, bool last) -> bool {
 #pragma unroll
-        for (int i = 0; i < 2 * NQK; ++i) acc[i] += ds * k[i];
+    for (int c = 0; c < C::kSub; ++c) {
+      if (first && !wait_unit(r)) return false;
+      const uint32_t a = sb + (t * C::kSub + c) * kMhaUnit, b = sb + C::kQBytes + r.at * kMhaUnit;
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk)
+        mma_bf16_ss(tmem + t * kMhaTile, smem_desc(a + kk * 32, 16, 1024, SWZ_128B),
+                    smem_desc(b + kk * 32, 16, 1024, SWZ_128B), kIdescS, c + kk > 0 ? 1u : 0u);
+      if (last) mma_commit(smem_u32(&m.empty[r.at]));
+      r.next();
+    }
+    mma_commit(smem_u32(&m.s_full[t]));
+    return true;
+  };
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    if (s.blocks[t] == 0) continue;
+    if (!mbar_wait(smem_u32(&m.q_full[t]), 0, deadline, ab)) return false;
+    const bool alone = NT == 1 || s.blocks[1 - t] == 0;
+    if (!scores(t, rk, t == 0 || alone, t == NT - 1 || alone)) return false;
+  }
+  for (int c = 0; c < C::kSub; ++c) rk.next();
+  for (int j = 0; j < s.most; ++j) {
+    rv = rk;                                   // block j's V, then block j + 1's K
+    rk.next();
+    rk.next();
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      if (j >= s.blocks[t]) continue;
+      const bool alone = NT == 1 || j >= s.blocks[1 - t];
+      const bool first = t == 0 || alone, last = t == NT - 1 || alone;
+      if (!mbar_wait(smem_u32(&m.p_full[t]), static_cast<uint32_t>(j) & 1u, deadline, ab)) return false;
+      tc_fence_after();
+      MhaRing<C::kUnits> r = rv;
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        if (first && !wait_unit(r)) return false;
+        const uint32_t b = sb + C::kQBytes + r.at * kMhaUnit;
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          mma_bf16_ts(tmem + (NT + t) * kMhaTile, tmem + t * kMhaTile + 8 * (4 * c + kk),
+                      smem_desc(b + kk * 2048, kMhaUnit / 2, 1024, SWZ_128B), kIdescO, j + c + kk > 0 ? 1u : 0u);
+        if (last) mma_commit(smem_u32(&m.empty[r.at]));
+        r.next();
+      }
+      if (j + 1 < s.blocks[t]) {
+        const bool alone_k = NT == 1 || j + 1 >= s.blocks[1 - t];
+        if (!scores(t, rk, t == 0 || alone_k, t == NT - 1 || alone_k)) return false;
+      } else {
+        mma_commit(smem_u32(&m.o_full[t]));
       }
     }
-    mha_store<NQK>(p.dq + r * (64 * NQK), lane, acc, p.scale);
+    if (j + 1 < s.most)
+      for (int c = 0; c < C::kSub; ++c) rk.next();
   }
+  return true;
 }
 
-// One warp per (key row, key head): dk and dv over the rows that see the key, of every head of the group.
-template <int NQK>
-__global__ void __launch_bounds__(256) dense_mha_dkv_kernel(const __grid_constant__ MhaParams p) {
-  const int lane = static_cast<int>(lane_id());
-  const int share = p.h_q / p.h_kv;
-  const long long rows = static_cast<long long>(p.total_kv) * p.h_kv, step = static_cast<long long>(gridDim.x) * 8;
-  for (long long r = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5); r < rows; r += step) {
-    const int t = static_cast<int>(r / p.h_kv), hk = static_cast<int>(r % p.h_kv);
-    float dk[2 * NQK], dv[4] = {0.f, 0.f, 0.f, 0.f};
+// A hidden key's weight is 0, but 0 times an infinity or a NaN is a NaN: before a product
+// with a block that some rows do not see all of, values that are not finite are taken
+// out of it.  Each of 128 threads looks over an eighth of a KB of `bytes`, a multiple of
+// 2 KB; true where it found some.
+__device__ __forceinline__ bool mha_clear(uint32_t tile, uint32_t bytes) {
+  uint32_t seen = 0;
+  for (uint32_t at = (threadIdx.x & 127u) * 16; at < bytes; at += 2048) {
+    uint32_t x[4];
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]) : "r"(tile + at));
+    // the sign bit's place is carried into where the exponent is all ones
 #pragma unroll
-    for (int i = 0; i < 2 * NQK; ++i) dk[i] = 0.f;
-    const int b = mha_seq_of(p.cu_kv, p.batch, t);
-    if (b >= 0) {
-      const MhaSeq s = mha_seq(p, b);
-      float q[2 * NQK], k[2 * NQK], v[4], g[4];
-      mha_row<NQK>(p.k + t * p.k_tok + hk * p.k_head, lane, k);
-      mha_row<2>(p.v + t * p.v_tok + hk * p.v_head, lane, v);
-      const int first = max(0, t - s.k0 - (s.k1 - s.k0) + (s.q1 - s.q0));
-      for (int h = hk * share; h < (hk + 1) * share; ++h) {
-        for (int i = s.q0 + first; i < s.q1; ++i) {
-          const long long qr = static_cast<long long>(i) * p.h_q + h;
-          mha_row<NQK>(p.q + i * p.q_tok + h * p.q_head, lane, q);
-          mha_row<2>(p.dout + i * p.do_tok + h * p.do_head, lane, g);
-          const float e = __expf(mha_dot<NQK>(q, k) * p.scale - p.lse[qr]);
-          const float ds = e * (mha_dot<2>(g, v) - p.delta[qr]);
+    for (int i = 0; i < 4; ++i) seen |= (x[i] & 0x7fff7fffu) + 0x00800080u;
+  }
+  if ((seen & 0x80008000u) == 0u) return false;
+  for (uint32_t at = (threadIdx.x & 127u) * 16; at < bytes; at += 2048) {
+    uint32_t x[4];
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]) : "r"(tile + at));
 #pragma unroll
-          for (int j = 0; j < 2 * NQK; ++j) dk[j] += ds * q[j];
+    for (int i = 0; i < 4; ++i) {
+      if ((x[i] & 0x7f80u) == 0x7f80u) x[i] &= 0xffff0000u;
+      if ((x[i] & 0x7f800000u) == 0x7f800000u) x[i] &= 0xffffu;
+    }
+    st_shared_v4(tile + at, x[0], x[1], x[2], x[3]);
+  }
+  fence_proxy_async_smem();
+  return true;
+}
+
+// One thread per row of tile t.
+template <int DQK, int NT>
+__device__ __forceinline__ bool mha_softmax(const MhaFwdParams& p, MhaMisc& m, uint32_t sb, uint32_t tmem,
+                                            const MhaWork& w, const MhaSpan<NT>& s, int pack0, int t) {
+  using C = MhaFwdShape<DQK, NT>;
+  const volatile int* ab = &m.abort_flag;
+  const uint64_t deadline = global_timer_ns() + p.timeout_ns;
+  const int row = static_cast<int>(threadIdx.x) & 127;
+  const int lq = w.q1 - w.q0, lk = w.k1 - w.k0;
+  const int tok = s.t0[t] + row / p.pack;
+  const bool live = row < p.pack * p.tok_tile && tok < lq;
+  const int blocks = s.blocks[t];
+  const int whole = max(0, s.t0[t] + lk - lq + 1) / kMhaTile;   // blocks that every row sees all of
+  const uint32_t quarter = static_cast<uint32_t>((row >> 5) * 32) << 16;
+  const uint32_t ts = tmem + quarter + t * kMhaTile, to = tmem + quarter + (NT + t) * kMhaTile;
+  const float c = p.scale_log2;
+  float top = -INFINITY, sum = 0.f;   // the maximum that the weights are relative to, their sum
+  for (int j = 0; j < blocks; ++j) {
+    if (j >= whole) {
+      for (int i = 0; i < 2; ++i) {   // the block's V: units (j + 1) kSub + 2 j and the next
+        const uint32_t n = static_cast<uint32_t>((j + 1) * C::kSub + 2 * j + i);
+        if (!mbar_wait(smem_u32(&m.full[n % C::kUnits]), n / C::kUnits & 1u, deadline, ab)) return false;
+        if (mha_clear(sb + C::kQBytes + n % C::kUnits * kMhaUnit, kMhaUnit)) m.cleared = 1;
+      }
+    }
+    if (!mbar_wait(smem_u32(&m.s_full[t]), static_cast<uint32_t>(j) & 1u, deadline, ab)) return false;
+    tc_fence_after();
+    float v[kMhaTile];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) dv[j] += e * g[j];
+    for (int i = 0; i < 4; ++i) tmem_ld32(ts + 32 * i, v + 32 * i);
+    tmem_wait_ld();
+    if (j >= whole) {
+      const int sees = tok + lk - lq + 1 - j * kMhaTile;
+#pragma unroll
+      for (int i = 0; i < kMhaTile; ++i) v[i] = i < sees ? v[i] : -INFINITY;
+    }
+    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+    for (int i = 0; i < kMhaTile; i += 8) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) mx[k] = max3(mx[k], v[i + 2 * k], v[i + 2 * k + 1]);
+    }
+    const float now = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
+    const bool grown = (now - top) * c > kMhaLazy;
+    if (__any_sync(0xffffffffu, grown)) {
+      // the block's scores are there, so the product before them has ended: O is this warp's to change
+      const float f = grown ? fast_exp2((top - now) * c) : 1.f;
+      if (grown) top = now;
+      sum *= f;
+      if (j > 0) {
+#pragma unroll
+        for (int i = 0; i < kMhaDv / 32; ++i) {
+          float o[32];
+          tmem_ld32(to + 32 * i, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int k = 0; k < 32; ++k) o[k] *= f;
+          tmem_st16(to + 32 * i, o);
+          tmem_st16(to + 32 * i + 16, o + 16);
         }
       }
     }
-    mha_store<NQK>(p.dk + r * (64 * NQK), lane, dk, p.scale);
-    mha_store<2>(p.dv + r * 128, lane, dv, 1.f);
+    const float shift = top == -INFINITY ? 0.f : -top * c;
+    float add[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < kMhaTile; i += 32) {
+      float pk[16];
+#pragma unroll
+      for (int k = 0; k < 32; k += 2) {
+        float &a = v[i + k], &b = v[i + k + 1];
+        scale_shift2(a, b, c, shift);
+        a = fast_exp2(a);
+        b = fast_exp2(b);
+        add2(add[k & 6], add[(k & 6) + 1], a, b);
+        pk[k >> 1] = __uint_as_float(pack_bf16x2(a, b));
+      }
+      tmem_st16(ts + (i >> 1), pk);
+    }
+    tmem_wait_st();
+    tc_fence_before();
+    __syncwarp();
+    if (lane_id() == 0) mbar_arrive(smem_u32(&m.p_full[t]));
+    add2(add[0], add[1], add[2], add[3]);
+    add2(add[4], add[5], add[6], add[7]);
+    add2(add[0], add[1], add[4], add[5]);
+    sum += add[0] + add[1];
   }
+  const size_t at = live ? static_cast<size_t>(w.q0 + tok) * p.h_q + pack0 + row % p.pack : 0;
+  __nv_bfloat16* o = p.out + at * kMhaDv;
+  if (blocks > 0) {
+    if (!mbar_wait(smem_u32(&m.o_full[t]), 0, deadline, ab)) return false;
+    tc_fence_after();
+  }
+  const bool store_o = live && (!w.rest || (p.fill & 1)), store_l = live && (!w.rest || (p.fill & 2));
+  if (store_l) p.lse[at] = sum == 0.f ? -INFINITY : (top * c + log2f(sum)) * 0.6931471805599453f;
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+  for (int i = 0; i < kMhaDv / 32; ++i) {
+    float x[32];
+    if (blocks > 0) {
+      tmem_ld32(to + 32 * i, x);
+      tmem_wait_ld();
+    }
+#pragma unroll
+    for (int k = 0; k < 32; ++k) x[k] = sum == 0.f ? 0.f : x[k] * inv;
+    if (store_o) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) *reinterpret_cast<uint4*>(o + 32 * i + 8 * k) = pack8(x + 8 * k);
+    }
+  }
+  if (blocks > 0 && store_o && *reinterpret_cast<volatile int*>(&m.cleared)) {
+    // columns where a key that the row sees is not finite, among the blocks that were looked over
+    const int first = max(0, s.t0[0] + lk - lq + 1) / kMhaTile * kMhaTile, end = tok + lk - lq + 1;
+    const __nv_bfloat16* values = p.v + w.k0 * p.v_tok + pack0 / p.group * p.v_head;
+#pragma unroll 1
+    for (int d = 0; d < kMhaDv; ++d) {
+      float acc = 0.f;
+#pragma unroll 1
+      for (int key = first; key < end; ++key) {
+        const float y = __bfloat162float(values[key * p.v_tok + d]);
+        if (!(fabsf(y) <= 3.402823466e38f)) acc += y;
+      }
+      if (acc != 0.f) o[d] = __float2bfloat16_rn(acc);
+    }
+  }
+  return true;
+}
+
+template <int DQK, int NT>
+__global__ void __launch_bounds__(MhaFwdShape<DQK, NT>::kThreads, 1) dense_mha_fwd_kernel(
+    const __grid_constant__ MhaFwdParams p) {
+  using C = MhaFwdShape<DQK, NT>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sbase = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  MhaMisc& m = *reinterpret_cast<MhaMisc*>(sbase + C::kMiscOff);
+  const int warp = static_cast<int>(threadIdx.x >> 5);
+  const uint32_t sb = smem_u32(sbase);
+  const int slot = static_cast<int>(blockIdx.x % static_cast<unsigned>(p.slots));
+  const int pack0 = static_cast<int>(blockIdx.x / static_cast<unsigned>(p.slots)) * p.pack;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::kUnits; ++i) {
+      mbar_init(smem_u32(&m.full[i]), 1);
+      mbar_init(smem_u32(&m.empty[i]), 1);
+    }
+    for (int i = 0; i < NT; ++i) {
+      mbar_init(smem_u32(&m.q_full[i]), 1);
+      mbar_init(smem_u32(&m.s_full[i]), 1);
+      mbar_init(smem_u32(&m.p_full[i]), 4);   // one arrival per softmax warp
+      mbar_init(smem_u32(&m.o_full[i]), 1);
+    }
+    mbar_init(smem_u32(&m.drain), 1);
+    m.abort_flag = 0;
+    m.cleared = 0;
+    m.prior_error = *reinterpret_cast<volatile int*>(&g_device_error);
+    fence_mbar_init();
+    prefetch_tmap(&p.map_q);
+    prefetch_tmap(&p.map_k);
+    prefetch_tmap(&p.map_v);
+  }
+  if (warp == 4 * NT) {
+    tmem_alloc(smem_u32(&m.tmem_base), C::kTmemCols);
+    tmem_relinquish();
+  }
+  if (warp == 4 * NT + 1) {
+    const MhaWork w = mha_find(p.cu_q, p.cu_kv, p.batch, p.total_q, p.total_kv, slot, NT * p.tok_tile, false, p.fill != 0);
+    if (lane_id() == 0) m.work = w;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = m.tmem_base;
+  const MhaWork w = m.work;
+
+  if (m.prior_error == 0 && w.q1 > w.q0) {
+    const MhaSpan<NT> s(p, w);
+    if (warp < 4 * NT) {
+      if (!mha_softmax<DQK, NT>(p, m, sb, tmem, w, s, pack0, warp >> 2)) mha_raise(m, kErrMhaSoftmaxWait);
+    } else {
+      if (s.most > 0 && lane_id() == 0) {
+        const int never = 0;
+        if (warp == 4 * NT) {
+          if (!mha_mma<DQK, NT>(p, m, sb, tmem, s)) mha_raise(m, kErrMhaMmaWait);
+          // every MMA issued completes before TMEM is freed
+          mma_commit(smem_u32(&m.drain));
+          mbar_wait(smem_u32(&m.drain), 0, global_timer_ns() + 100000000ull, &never);
+        } else if (warp == 4 * NT + 1) {
+          uint32_t fills = 0;
+          if (!mha_load<DQK, NT>(p, m, sb, w, s, pack0, pack0 / p.group, fills)) mha_raise(m, kErrMhaLoadWait);
+          // every copy issued has landed before the CTA exits (only a unit's last fill can be in flight)
+          const uint64_t dl = global_timer_ns() + 100000000ull;
+          for (int t = 0; t < NT; ++t)
+            if (s.blocks[t] > 0) mbar_wait(smem_u32(&m.q_full[t]), 0, dl, &never);
+          for (uint32_t i = fills > C::kUnits ? fills - C::kUnits : 0; i < fills; ++i)
+            mbar_wait(smem_u32(&m.full[i % C::kUnits]), (i / C::kUnits) & 1u, dl, &never);
+        }
+      }
+      __syncwarp();
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 4 * NT) tmem_dealloc(tmem, C::kTmemCols);
 }
 
 }  // namespace smla

@@ -6,6 +6,7 @@
 #include <cmath>
 
 #include "add_norm_kernel.cuh"
+#include "dense_mha_bwd_kernel.cuh"
 #include "dense_mha_kernel.cuh"
 
 // ------------------------------------------------------------------ residual norm
@@ -187,6 +188,77 @@ smla::MhaParams mha_params(const MhaRows& q, const MhaRows& k, const MhaRows& v,
   return p;
 }
 
+// Query heads of one group that a tile takes side by side: the most that leave at most
+// 8 of its 128 rows unused.
+int mha_pack(int group) {
+  for (int n = group < smla::kMhaTile ? group : smla::kMhaTile; n > 1; --n)
+    if (group % n == 0 && smla::kMhaTile % n <= 8) return n;
+  return 1;
+}
+
+// Tiles of `per` rows that any `batch` sequences of `total` rows in all have at most
+// (0: one dense sequence), and the rows behind them.
+long long mha_slots(int total, int per, int batch, bool rest) {
+  if (batch == 0) return (total + per - 1LL) / per;
+  return total / per + static_cast<long long>(batch < total ? batch : total) + (rest ? 1 : 0);
+}
+
+// exp's scale in powers of two; kept off zero so that a hidden key's -inf stays one.
+float mha_scale_log2(float sm_scale) {
+  const float c = sm_scale * 1.4426950408889634f;
+  return c > 1e-30f ? c : 1e-30f;
+}
+
+// bf16 rows [total, heads, d] in boxes of 64 columns x `box_heads` x `box_rows`,
+// 128B-swizzled; boxes past the last row read zeros.
+sparse_mla_status_t mha_map(CUtensorMap* map, const MhaRows& r, int total, int heads, int d, int box_heads, int box_rows) {
+  EncodeTiledFn enc = nullptr;
+  const sparse_mla_status_t st = get_encode(&enc);
+  if (st != SPARSE_MLA_OK) return st;
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(total)};
+  // the stride of a dimension of one row is never used
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(heads > 1 ? r.head : d) * 2,
+                           static_cast<cuuint64_t>(total > 1 ? r.tok : d) * 2};
+  if (strides[0] >= (1ull << 40) || strides[1] >= (1ull << 40)) return SPARSE_MLA_ERR_INVALID_ARG;
+  cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_heads), static_cast<cuuint32_t>(box_rows)};
+  cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult e = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(r.p), dims, strides, box, estr,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return e == CUDA_SUCCESS ? SPARSE_MLA_OK : SPARSE_MLA_ERR_INVALID_ARG;
+}
+
+template <int DQK, int NT>
+void mha_fwd_launch(const smla::MhaFwdParams& p, unsigned ctas, cudaStream_t cs) {
+  using C = smla::MhaFwdShape<DQK, NT>;
+  smla::dense_mha_fwd_kernel<DQK, NT><<<ctas, C::kThreads, C::kBytes, cs>>>(p);
+}
+
+struct MhaState {
+  bool set = false;
+};
+MhaState g_mha[kMaxDevices];   // under g_mu
+
+template <int DQK, int NT>
+bool mha_setup_fwd() {
+  return cudaFuncSetAttribute(smla::dense_mha_fwd_kernel<DQK, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              smla::MhaFwdShape<DQK, NT>::kBytes) == cudaSuccess;
+}
+
+// The dense attention's kernels, apart from device_setup (which comes first): what a
+// device refuses of them stops no other call.
+sparse_mla_status_t mha_device_setup() {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return SPARSE_MLA_ERR_CUDA;
+  std::lock_guard<std::mutex> lock(g_mu);
+  MhaState& st = g_mha[dev];
+  if (!st.set) {
+    st.set = mha_setup_fwd<192, 2>() && mha_setup_fwd<192, 1>() && mha_setup_fwd<128, 2>() && mha_setup_fwd<128, 1>();
+    if (!st.set) cudaGetLastError();   // not the next launch's error
+  }
+  return st.set ? SPARSE_MLA_OK : SPARSE_MLA_ERR_CUDA;
+}
+
 int mha_ctas(long long rows) { return static_cast<int>(rows < 8 * 65536LL ? (rows + 7) / 8 : 65536); }
 
 }  // namespace
@@ -209,14 +281,45 @@ sparse_mla_status_t dense_mha_fwd(const void* q, long long q_tok_stride, long lo
   int sms = 0;
   if ((st = device_setup(&sms)) != SPARSE_MLA_OK) return st;
   if (total_q == 0) return SPARSE_MLA_OK;
-  smla::MhaParams p = mha_params(rq, rk, rv, cu_seqlens_q, cu_seqlens_kv, batch, sm_scale, total_q, total_kv, h_q, h_kv);
+  if ((st = mha_device_setup()) != SPARSE_MLA_OK) return st;
+  smla::MhaFwdParams p;
+  std::memset(&p, 0, sizeof(p));
+  const int group = h_q / h_kv;
+  p.pack = mha_pack(group);
+  p.tok_tile = smla::kMhaTile / p.pack;
+  if ((st = mha_map(&p.map_q, rq, total_q, h_q, d_qk, p.pack, p.tok_tile)) != SPARSE_MLA_OK) return st;
+  // without keys nothing is loaded: any map does
+  const bool keys = total_kv > 0;
+  if ((st = mha_map(&p.map_k, keys ? rk : rq, keys ? total_kv : total_q, keys ? h_kv : h_q, d_qk, 1, smla::kMhaTile)) !=
+          SPARSE_MLA_OK ||
+      (st = mha_map(&p.map_v, keys ? rv : rq, keys ? total_kv : total_q, keys ? h_kv : h_q, smla::kMhaDv, 1,
+                    smla::kMhaTile / 2)) != SPARSE_MLA_OK)
+    return st;
+  p.cu_q = cu_seqlens_q;
+  p.cu_kv = cu_seqlens_kv;
+  p.batch = cu_seqlens_q ? batch : 1;
+  p.total_q = total_q;
+  p.total_kv = total_kv;
+  p.h_q = h_q;
+  p.group = group;
+  p.scale_log2 = mha_scale_log2(sm_scale);
+  p.v = static_cast<const __nv_bfloat16*>(v);
+  p.v_tok = v_tok_stride;
+  p.v_head = v_head_stride;
   p.out = static_cast<__nv_bfloat16*>(out);
   p.lse = lse;
-  p.fill = fill;
+  p.fill = cu_seqlens_q ? fill : 0;
+  const unsigned long long t = g_timeout_ns.load();
+  p.timeout_ns = t ? t : kDefaultTimeoutNs;
+  // two tiles a CTA where a sequence's rows fill more than one
+  const bool two = static_cast<long long>(total_q) * p.pack > static_cast<long long>(smla::kMhaTile) * p.batch;
+  const long long slots = mha_slots(total_q, p.tok_tile * (two ? 2 : 1), cu_seqlens_q ? batch : 0, p.fill != 0);
+  if (slots * (h_q / p.pack) > INT_MAX) return SPARSE_MLA_ERR_INVALID_ARG;
+  p.slots = static_cast<int>(slots);
+  const unsigned ctas = static_cast<unsigned>(slots * (h_q / p.pack));
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
-  const int ctas = mha_ctas(static_cast<long long>(total_q) * h_q);
-  if (d_qk == 192) smla::dense_mha_fwd_kernel<3><<<ctas, 256, 0, cs>>>(p);
-  else smla::dense_mha_fwd_kernel<2><<<ctas, 256, 0, cs>>>(p);
+  if (d_qk == 192) two ? mha_fwd_launch<192, 2>(p, ctas, cs) : mha_fwd_launch<192, 1>(p, ctas, cs);
+  else two ? mha_fwd_launch<128, 2>(p, ctas, cs) : mha_fwd_launch<128, 1>(p, ctas, cs);
   return cudaGetLastError() == cudaSuccess ? SPARSE_MLA_OK : SPARSE_MLA_ERR_CUDA;
 }
 
