@@ -1,156 +1,793 @@
-// Gradients of causal attention over whole prompts in the heads' own space.
+// Gradients of causal attention over whole prompts in the heads' own space (tcgen05 + TMA).
 //
-//   s_ij = scale q_i . k_j  over the keys j that query i sees,
-//   lse_i = ln sum_j exp(s_ij),   out_i = sum_j exp(s_ij - lse_i) v_j
+//   P = exp(scale q k^T - lse),  D = rowsum(dout out),  dS = P (dout V^T - D),
+//   dq = scale dS K,   dk = scale dS^T q,   dv = P^T dout
 //
-// A sequence's lq queries are the last lq of its lk positions: local query i sees keys
-// 0 .. i + lk - lq.  h_q / h_kv query heads share a key and value head.
+// dk and dv are sums over the queries, dq over the keys: two kernels, each with its own
+// accumulators in TMEM and in a fixed order, at the price of forming S and dout V^T
+// twice (512 + 640 products a pair at 192 columns where one pass would have 832, but
+// that pass would need 640 columns of TMEM where there are 512, and would add dq up
+// across CTAs in an order that changes).
+//
+// dense_mha_dq_kernel: a tile of 128 query rows ((token, head) pairs, as in the forward)
+// against the keys that they see, 128 at a time.
+//   warps 0 .. 7   a thread per row and half of the columns.  First dout's row into TMEM
+//                  (A of the second product) and D; then per block P from S, dS from
+//                  dout V^T into the latter's columns; dq's rows at the end
+//   warp 8         one thread issues   S = Q K^T,  T = dout V^T,  dQ += dS K
+//                  in the order T(j + 1), S(j + 2), dQ(j + 1): S is ahead of its use by a
+//                  block, so that P is formed while T is, and dS while the next S is
+//   warp 9         one thread issues the TMA loads (K three blocks deep)
+//
+// dense_mha_dkv_kernel: a tile of 128 keys against the query rows that see them, N at a
+// time (128; at 192 columns 64, with V in TMEM: 128 + 192 columns of accumulators leave
+// 192), of every head of the group.
+//   warps 0 .. 7   a thread per key and half of the columns: P^T and dS^T in TMEM, in the
+//                  columns of the products that they come from
+//   warp 8         S^T = K Q^T,  T^T = V dout^T,  dV += P^T dout,  dK += dS^T Q
+//   warp 9         the TMA loads
+//   warp 10        the rows' lse and D into shared memory
+//
+// All waits are bounded, as in the forward.
 #pragma once
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cstdint>
 
 #include "dense_mha_kernel.cuh"
-#include "norm_rope_kernel.cuh"
-#include "ptx.cuh"
 
 namespace smla {
 
-struct MhaParams {
-  const __nv_bfloat16 *q, *k, *v;          // row (t, h) at q + t q_tok + h q_head
-  long long q_tok, q_head, k_tok, k_head, v_tok, v_head;
+enum MhaBwdErrCode : int {
+  kErrMhaDqLoadWait = 0x711,
+  kErrMhaDqMmaWait = 0x712,
+  kErrMhaDqRowsWait = 0x713,
+  kErrMhaDkvLoadWait = 0x721,
+  kErrMhaDkvMmaWait = 0x722,
+  kErrMhaDkvRowsWait = 0x723,
+  kErrMhaDkvStatWait = 0x724,
+};
+
+struct MhaBwdParams {
+  CUtensorMap map_q, map_do;               // [token, head, d]: boxes 64 x pack x tok_tile
+  CUtensorMap map_k, map_v;                // boxes 64 x 1 x 128
   const int32_t *cu_q, *cu_kv;             // [batch + 1], null for one dense sequence
-  int batch, total_q, total_kv, h_q, h_kv;
-  float scale;
-  __nv_bfloat16* out;                      // [total_q, h_q, d_v]
-  float* lse;                              // [total_q, h_q]
-  const __nv_bfloat16* dout;
-  long long do_tok, do_head;
+  int batch, total_q, total_kv, h_q, h_kv, group;
+  int pack, tok_tile;                      // rows of a query tile: tok_tile tokens x pack heads
+  int slots;                               // tiles per head (pack) that the grid has room for
+  float scale, scale_log2;
+  const __nv_bfloat16 *v, *dout;           // row (t, h) at v + t v_tok + h v_head
+  long long v_tok, v_head, do_tok, do_head;
+  const __nv_bfloat16* out;                // [total_q, h_q, 128]
+  const float* lse;                        // [total_q, h_q]
+  float* delta;                            // [total_q, h_q]: D
   __nv_bfloat16 *dq, *dk, *dv;             // [total, h, d]
-  float* delta;                            // [total_q, h_q]: rowsum(dout out)
+  unsigned long long timeout_ns;
 };
 
-struct MhaSeq {
-  int q0, q1, k0, k1;
-};
-
-__device__ __forceinline__ MhaSeq mha_seq(const MhaParams& p, int b) {
-  if (p.cu_q == nullptr) return {0, p.total_q, 0, p.total_kv};
-  MhaSeq s;
-  s.q0 = mha_offset(p.cu_q, b, p.total_q);
-  s.q1 = max(s.q0, mha_offset(p.cu_q, b + 1, p.total_q));
-  s.k0 = mha_offset(p.cu_kv, b, p.total_kv);
-  s.k1 = max(s.k0, mha_offset(p.cu_kv, b + 1, p.total_kv));
-  return s;
+// Half a row of 128 values as A of a product: 32 columns of TMEM.
+__device__ __forceinline__ void mha_row_to_tmem(uint32_t taddr, const uint4 (&x)[8]) {
+  const float* f = reinterpret_cast<const float*>(&x[0]);
+  tmem_st16(taddr, f);
+  tmem_st16(taddr + 16, f + 16);
 }
 
-// The sequence that holds row r of the offsets `cu` (the last b with cu[b] <= r), or -1.
-__device__ __forceinline__ int mha_seq_of(const int32_t* cu, int batch, int r) {
-  if (cu == nullptr) return 0;
-  int lo = 0, hi = batch - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (__ldg(cu + mid) <= r) lo = mid;
-    else hi = mid - 1;
-  }
-  return __ldg(cu + lo) <= r && r < __ldg(cu + lo + 1) ? lo : -1;
-}
-
-// A row of N * 64 values, two per lane and 64.
+// Columns 0 .. 32 n - 1 of this thread's TMEM lane times `f` into a bf16 row (zeros where
+// there are no sums).
 template <int N>
-__device__ __forceinline__ void mha_row(const __nv_bfloat16* row, int lane, float (&x)[2 * N]) {
+__device__ __forceinline__ void mha_store_sums(__nv_bfloat16* row, uint32_t taddr, float f, bool sums, bool live) {
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    const uint32_t v = *reinterpret_cast<const uint32_t*>(row + 64 * i + 2 * lane);
-    x[2 * i] = bf16_lo(v);
-    x[2 * i + 1] = bf16_hi(v);
-  }
-}
-
-template <int N>
-__device__ __forceinline__ void mha_store(__nv_bfloat16* row, int lane, const float (&x)[2 * N], float f) {
+    float x[32];
+    if (sums) tmem_load32(taddr + 32 * i, x);
 #pragma unroll
-  for (int i = 0; i < N; ++i)
-    *reinterpret_cast<uint32_t*>(row + 64 * i + 2 * lane) = pack_bf16x2(x[2 * i] * f, x[2 * i + 1] * f);
-}
-
-template <int N>
-__device__ __forceinline__ float mha_dot(const float (&a)[2 * N], const float (&b)[2 * N]) {
-  float s = 0.f;
+    for (int k = 0; k < 32; ++k) x[k] = sums ? x[k] * f : 0.f;
+    if (live) {
 #pragma unroll
-  for (int i = 0; i < 2 * N; ++i) s += a[i] * b[i];
-  return warp_sum(s);
-}
-
-// One warp per (query row, head): D = rowsum(dout out) and dq.
-template <int NQK>
-__global__ void __launch_bounds__(256) dense_mha_dq_kernel(const __grid_constant__ MhaParams p) {
-  const int lane = static_cast<int>(lane_id());
-  const long long rows = static_cast<long long>(p.total_q) * p.h_q, step = static_cast<long long>(gridDim.x) * 8;
-  for (long long r = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5); r < rows; r += step) {
-    const int t = static_cast<int>(r / p.h_q), h = static_cast<int>(r % p.h_q);
-    float acc[2 * NQK];
-#pragma unroll
-    for (int i = 0; i < 2 * NQK; ++i) acc[i] = 0.f;
-    const int b = mha_seq_of(p.cu_q, p.batch, t);
-    if (b >= 0) {
-      const MhaSeq s = mha_seq(p, b);
-      const int lk = s.k1 - s.k0;
-      const int sees = min(lk, t - s.q0 + lk - (s.q1 - s.q0) + 1);
-      float q[2 * NQK], k[2 * NQK], v[4], g[4], o[4];
-      mha_row<NQK>(p.q + t * p.q_tok + h * p.q_head, lane, q);
-      mha_row<2>(p.dout + t * p.do_tok + h * p.do_head, lane, g);
-      mha_row<2>(p.out + r * 128, lane, o);
-      const float delta = mha_dot<2>(g, o), lse = p.lse[r];
-      if (lane == 0) p.delta[r] = delta;
-      const int hk = h / (p.h_q / p.h_kv);
-      for (int j = 0; j < sees; ++j) {
-        mha_row<NQK>(p.k + (s.k0 + j) * p.k_tok + hk * p.k_head, lane, k);
-        mha_row<2>(p.v + (s.k0 + j) * p.v_tok + hk * p.v_head, lane, v);
-        const float e = __expf(mha_dot<NQK>(q, k) * p.scale - lse);
-        const float ds = e * (mha_dot<2>(g, v) - delta);
-#pragma unroll
-        for (int i = 0; i < 2 * NQK; ++i) acc[i] += ds * k[i];
-      }
+      for (int k = 0; k < 4; ++k) *reinterpret_cast<uint4*>(row + 32 * i + 8 * k) = pack8(x + 8 * k);
     }
-    mha_store<NQK>(p.dq + r * (64 * NQK), lane, acc, p.scale);
   }
 }
 
-// One warp per (key row, key head): dk and dv over the rows that see the key, of every head of the group.
-template <int NQK>
-__global__ void __launch_bounds__(256) dense_mha_dkv_kernel(const __grid_constant__ MhaParams p) {
-  const int lane = static_cast<int>(lane_id());
-  const int share = p.h_q / p.h_kv;
-  const long long rows = static_cast<long long>(p.total_kv) * p.h_kv, step = static_cast<long long>(gridDim.x) * 8;
-  for (long long r = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5); r < rows; r += step) {
-    const int t = static_cast<int>(r / p.h_kv), hk = static_cast<int>(r % p.h_kv);
-    float dk[2 * NQK], dv[4] = {0.f, 0.f, 0.f, 0.f};
+// ------------------------------------------------------------------ dq
+
+struct __align__(16) MhaDqMisc {
+  uint64_t q_full, k_full[3], k_empty[3], v_full[3], v_empty[3], do_ready, s_full, s_free, t_full, ds_full, dq_full, drain;
+  uint32_t tmem_base;
+  int abort_flag;
+  int prior_error;
+  MhaWork work;
+  float part[2][kMhaTile];
+};
+
+template <int DQK>
+struct MhaDqShape {
+  static constexpr int kSub = DQK / 64;
+  static constexpr int kKStages = 3, kVStages = DQK == 192 ? 1 : 3;
+  static constexpr uint32_t kKBytes = kSub * kMhaUnit, kVBytes = 2 * kMhaUnit;
+  static constexpr uint32_t kKOff = kSub * kMhaUnit, kVOff = kKOff + kKStages * kKBytes;
+  static constexpr uint32_t kMiscOff = kVOff + kVStages * kVBytes;
+  static constexpr int kBytes = static_cast<int>(kMiscOff) + static_cast<int>(sizeof(MhaDqMisc)) + 1024;
+  static constexpr int kThreads = 10 * 32;
+  // columns of TMEM
+  static constexpr uint32_t kS = 0, kT = 128, kDq = 256, kDo = 448;
+  static_assert(kBytes <= kMaxSmem, "shared memory");
+};
+
+template <class Misc>
+__device__ __forceinline__ void mha_bwd_raise(Misc& m, int code) {
+  *reinterpret_cast<volatile int*>(&m.abort_flag) = 1;
+  atomicCAS(&g_device_error, 0, code);
+}
+
+template <int DQK>
+__device__ __forceinline__ bool mha_dq_load(const MhaBwdParams& p, MhaDqMisc& m, uint32_t sb, const MhaWork& w, int t0,
+                                            int blocks, int pack0, int& k_fills, int& v_fills) {
+  using C = MhaDqShape<DQK>;
+  const volatile int* ab = &m.abort_flag;
+  const uint64_t deadline = global_timer_ns() + p.timeout_ns;
+  const int kvh = pack0 / p.group;
+  uint32_t bar = smem_u32(&m.q_full);
+  mbar_arrive_expect_tx(bar, C::kSub * static_cast<uint32_t>(p.pack * p.tok_tile) * 128u);
+  for (int c = 0; c < C::kSub; ++c) tma_load_3d(sb + c * kMhaUnit, &p.map_q, 64 * c, pack0, w.q0 + t0, bar);
+  for (int j = 0; j < blocks; ++j) {
+    const int ks = j % C::kKStages, vs = j % C::kVStages, row = w.k0 + j * kMhaTile;
+    if (!mbar_wait(smem_u32(&m.k_empty[ks]), (j / C::kKStages & 1) ^ 1, deadline, ab)) return false;
+    bar = smem_u32(&m.k_full[ks]);
+    mbar_arrive_expect_tx(bar, C::kKBytes);
+    ++k_fills;
+    for (int c = 0; c < C::kSub; ++c)
+      tma_load_3d(sb + C::kKOff + ks * C::kKBytes + c * kMhaUnit, &p.map_k, 64 * c, kvh, row, bar);
+    if (!mbar_wait(smem_u32(&m.v_empty[vs]), (j / C::kVStages & 1) ^ 1, deadline, ab)) return false;
+    bar = smem_u32(&m.v_full[vs]);
+    mbar_arrive_expect_tx(bar, C::kVBytes);
+    ++v_fills;
+    for (int c = 0; c < 2; ++c)
+      tma_load_3d(sb + C::kVOff + vs * C::kVBytes + c * kMhaUnit, &p.map_v, 64 * c, kvh, row, bar);
+  }
+  return true;
+}
+
+template <int DQK>
+__device__ __forceinline__ bool mha_dq_mma(const MhaBwdParams& p, MhaDqMisc& m, uint32_t sb, uint32_t tmem, int blocks) {
+  using C = MhaDqShape<DQK>;
+  constexpr uint32_t kIdescS = idesc_bf16_f32(kMhaTile, kMhaTile, false, false);
+  constexpr uint32_t kIdescQ = idesc_bf16_f32(kMhaTile, DQK, false, true);
+  const volatile int* ab = &m.abort_flag;
+  const uint64_t deadline = global_timer_ns() + p.timeout_ns;
+  auto scores = [&](int j) -> bool {
+    const int st = j % C::kKStages;
+    if (!mbar_wait(smem_u32(&m.k_full[st]), j / C::kKStages & 1, deadline, ab)) return false;
+    const uint32_t k = sb + C::kKOff + st * C::kKBytes;
 #pragma unroll
-    for (int i = 0; i < 2 * NQK; ++i) dk[i] = 0.f;
-    const int b = mha_seq_of(p.cu_kv, p.batch, t);
-    if (b >= 0) {
-      const MhaSeq s = mha_seq(p, b);
-      float q[2 * NQK], k[2 * NQK], v[4], g[4];
-      mha_row<NQK>(p.k + t * p.k_tok + hk * p.k_head, lane, k);
-      mha_row<2>(p.v + t * p.v_tok + hk * p.v_head, lane, v);
-      const int first = max(0, t - s.k0 - (s.k1 - s.k0) + (s.q1 - s.q0));
-      for (int h = hk * share; h < (hk + 1) * share; ++h) {
-        for (int i = s.q0 + first; i < s.q1; ++i) {
-          const long long qr = static_cast<long long>(i) * p.h_q + h;
-          mha_row<NQK>(p.q + i * p.q_tok + h * p.q_head, lane, q);
-          mha_row<2>(p.dout + i * p.do_tok + h * p.do_head, lane, g);
-          const float e = __expf(mha_dot<NQK>(q, k) * p.scale - p.lse[qr]);
-          const float ds = e * (mha_dot<2>(g, v) - p.delta[qr]);
+    for (int kk = 0; kk < DQK / 16; ++kk) {
+      const uint32_t off = (kk >> 2) * kMhaUnit + (kk & 3) * 32;
+      mma_bf16_ss(tmem + C::kS, smem_desc(sb + off, 16, 1024, SWZ_128B), smem_desc(k + off, 16, 1024, SWZ_128B), kIdescS,
+                  kk > 0 ? 1u : 0u);
+    }
+    mma_commit(smem_u32(&m.s_full));
+    return true;
+  };
+  auto values = [&](int j) -> bool {
+    const int st = j % C::kVStages;
+    if (!mbar_wait(smem_u32(&m.v_full[st]), j / C::kVStages & 1, deadline, ab)) return false;
+    const uint32_t v = sb + C::kVOff + st * C::kVBytes;
 #pragma unroll
-          for (int j = 0; j < 2 * NQK; ++j) dk[j] += ds * q[j];
+    for (int kk = 0; kk < kMhaDv / 16; ++kk)
+      mma_bf16_ts(tmem + C::kT, tmem + C::kDo + 8 * kk,
+                  smem_desc(v + (kk >> 2) * kMhaUnit + (kk & 3) * 32, 16, 1024, SWZ_128B), kIdescS, kk > 0 ? 1u : 0u);
+    mma_commit(smem_u32(&m.v_empty[st]));
+    mma_commit(smem_u32(&m.t_full));
+    return true;
+  };
+  if (!mbar_wait(smem_u32(&m.q_full), 0, deadline, ab)) return false;
+  if (!scores(0)) return false;
+  if (!mbar_wait(smem_u32(&m.do_ready), 0, deadline, ab)) return false;
+  tc_fence_after();
+  if (!values(0)) return false;
+  if (blocks > 1) {
+    if (!mbar_wait(smem_u32(&m.s_free), 0, deadline, ab)) return false;
+    tc_fence_after();
+    if (!scores(1)) return false;
+  }
+  for (int j = 0; j < blocks; ++j) {
+    if (!mbar_wait(smem_u32(&m.ds_full), j & 1, deadline, ab)) return false;
+    tc_fence_after();
+    const int st = j % C::kKStages;
+    const uint32_t k = sb + C::kKOff + st * C::kKBytes;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) dv[j] += e * g[j];
+    for (int kk = 0; kk < kMhaTile / 16; ++kk)   // either half's dS is in its own columns
+      mma_bf16_ts(tmem + C::kDq, tmem + C::kT + 64 * (kk >> 2) + 8 * (kk & 3),
+                  smem_desc(k + kk * 2048, kMhaUnit, 1024, SWZ_128B), kIdescQ, j + kk > 0 ? 1u : 0u);
+    mma_commit(smem_u32(&m.k_empty[st]));
+    if (j + 1 < blocks && !values(j + 1)) return false;
+    if (j + 2 < blocks) {
+      if (!mbar_wait(smem_u32(&m.s_free), (j + 1) & 1, deadline, ab)) return false;
+      tc_fence_after();
+      if (!scores(j + 2)) return false;
+    }
+  }
+  mma_commit(smem_u32(&m.dq_full));
+  return true;
+}
+
+template <int DQK>
+__device__ __forceinline__ bool mha_dq_rows(const MhaBwdParams& p, MhaDqMisc& m, uint32_t sb, uint32_t tmem,
+                                            const MhaWork& w, int t0, int blocks, int pack0) {
+  using C = MhaDqShape<DQK>;
+  const volatile int* ab = &m.abort_flag;
+  const uint64_t deadline = global_timer_ns() + p.timeout_ns;
+  const int row = static_cast<int>(threadIdx.x) & 127, half = static_cast<int>(threadIdx.x) >> 7;
+  const int lq = w.q1 - w.q0, lk = w.k1 - w.k0;
+  const int tok = t0 + row / p.pack, head = pack0 + row % p.pack;
+  const bool live = row < p.pack * p.tok_tile && tok < lq;
+  const uint32_t lane0 = tmem + (static_cast<uint32_t>((row >> 5) * 32) << 16);
+  const size_t at = live ? static_cast<size_t>(w.q0 + tok) * p.h_q + head : 0;
+  float lse2 = 0.f, delta = 0.f;
+  if (blocks > 0) {
+    uint4 g[8];
+    float dot = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) g[i] = make_uint4(0, 0, 0, 0);
+    if (live) {
+      const uint4* gp = reinterpret_cast<const uint4*>(p.dout + (w.q0 + tok) * p.do_tok + head * p.do_head + 64 * half);
+      const uint4* op = reinterpret_cast<const uint4*>(p.out + at * kMhaDv + 64 * half);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        g[i] = __ldg(gp + i);
+        float a[8], b[8];
+        unpack8(g[i], a);
+        unpack8(__ldg(op + i), b);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) dot += a[k] * b[k];
+      }
+      lse2 = p.lse[at] * 1.4426950408889634f;
+    }
+    mha_row_to_tmem(lane0 + C::kDo + 32 * half, g);
+    tmem_wait_st();
+    tc_fence_before();
+    __syncwarp();
+    if (lane_id() == 0) mbar_arrive(smem_u32(&m.do_ready));
+    m.part[half][row] = dot;
+    named_bar_sync(1, 256);
+    delta = m.part[0][row] + m.part[1][row];
+    if (live && half == 0) p.delta[at] = delta;
+  }
+  const int whole = max(0, t0 + lk - lq + 1) / kMhaTile;
+  const uint32_t ts = lane0 + C::kS + 64 * half, tt = lane0 + C::kT + 64 * half;
+  for (int j = 0; j < blocks; ++j) {
+    if (!mbar_wait(smem_u32(&m.s_full), j & 1, deadline, ab)) return false;
+    tc_fence_after();
+    float s[64];
+    tmem_load64(ts, s);
+    tc_fence_before();
+    __syncwarp();
+    if (lane_id() == 0) mbar_arrive(smem_u32(&m.s_free));
+    const bool edge = j >= whole;
+    if (edge) {   // the product with dS must not meet what is not finite in a hidden key
+      const int st = j % C::kKStages;
+      if (!mbar_wait(smem_u32(&m.k_full[st]), j / C::kKStages & 1, deadline, ab)) return false;
+      mha_clear(sb + C::kKOff + st * C::kKBytes, C::kKBytes);
+    }
+    const int sees = edge ? tok + lk - lq + 1 - j * kMhaTile - 64 * half : 64;
+#pragma unroll
+    for (int i = 0; i < 64; i += 2) {
+      scale_shift2(s[i], s[i + 1], p.scale_log2, -lse2);
+      s[i] = fast_exp2(s[i]);
+      s[i + 1] = fast_exp2(s[i + 1]);
+    }
+    if (!mbar_wait(smem_u32(&m.t_full), j & 1, deadline, ab)) return false;
+    tc_fence_after();
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      float x[32];
+      tmem_load32(tt + 32 * c, x);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        x[i] = s[32 * c + i] * (x[i] - delta);
+        if (edge) x[i] = 32 * c + i < sees ? x[i] : 0.f;
+      }
+      float pk[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) pk[i] = __uint_as_float(pack_bf16x2(x[2 * i], x[2 * i + 1]));
+      tmem_st16(tt + 16 * c, pk);   // columns that have been read
+    }
+    tmem_wait_st();
+    tc_fence_before();
+    __syncwarp();
+    if (lane_id() == 0) mbar_arrive(smem_u32(&m.ds_full));
+  }
+  if (blocks > 0) {
+    if (!mbar_wait(smem_u32(&m.dq_full), 0, deadline, ab)) return false;
+    tc_fence_after();
+  }
+  mha_store_sums<DQK / 64>(p.dq + at * DQK + half * (DQK / 2), lane0 + C::kDq + half * (DQK / 2), p.scale, blocks > 0, live);
+  return true;
+}
+
+template <int DQK>
+__global__ void __launch_bounds__(MhaDqShape<DQK>::kThreads, 1) dense_mha_dq_kernel(const __grid_constant__ MhaBwdParams p) {
+  using C = MhaDqShape<DQK>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sbase = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  MhaDqMisc& m = *reinterpret_cast<MhaDqMisc*>(sbase + C::kMiscOff);
+  const int warp = static_cast<int>(threadIdx.x >> 5);
+  const uint32_t sb = smem_u32(sbase);
+  const int slot = static_cast<int>(blockIdx.x % static_cast<unsigned>(p.slots));
+  const int pack0 = static_cast<int>(blockIdx.x / static_cast<unsigned>(p.slots)) * p.pack;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 3; ++i) {
+      mbar_init(smem_u32(&m.k_full[i]), 1);
+      mbar_init(smem_u32(&m.k_empty[i]), 1);
+      mbar_init(smem_u32(&m.v_full[i]), 1);
+      mbar_init(smem_u32(&m.v_empty[i]), 1);
+    }
+    mbar_init(smem_u32(&m.q_full), 1);
+    mbar_init(smem_u32(&m.do_ready), 8);   // one arrival per row warp
+    mbar_init(smem_u32(&m.s_full), 1);
+    mbar_init(smem_u32(&m.s_free), 8);
+    mbar_init(smem_u32(&m.t_full), 1);
+    mbar_init(smem_u32(&m.ds_full), 8);
+    mbar_init(smem_u32(&m.dq_full), 1);
+    mbar_init(smem_u32(&m.drain), 1);
+    m.abort_flag = 0;
+    m.prior_error = *reinterpret_cast<volatile int*>(&g_device_error);
+    fence_mbar_init();
+    prefetch_tmap(&p.map_q);
+    prefetch_tmap(&p.map_k);
+    prefetch_tmap(&p.map_v);
+  }
+  if (warp == 8) {
+    tmem_alloc(smem_u32(&m.tmem_base), 512);
+    tmem_relinquish();
+  }
+  if (warp == 9) {
+    const MhaWork w = mha_find(p.cu_q, p.cu_kv, p.batch, p.total_q, p.total_kv, slot, p.tok_tile, false, true);
+    if (lane_id() == 0) m.work = w;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = m.tmem_base;
+  const MhaWork w = m.work;
+
+  if (m.prior_error == 0 && w.q1 > w.q0) {
+    const int lq = w.q1 - w.q0, t0 = w.tile * p.tok_tile;
+    const int sees = min(t0 + p.tok_tile, lq) + (w.k1 - w.k0) - lq;   // of the tile's last row
+    const int blocks = sees > 0 ? (sees + kMhaTile - 1) / kMhaTile : 0;
+    const int never = 0;
+    if (warp < 8) {
+      if (!mha_dq_rows<DQK>(p, m, sb, tmem, w, t0, blocks, pack0)) mha_bwd_raise(m, kErrMhaDqRowsWait);
+    } else if (blocks > 0) {
+      if (lane_id() == 0) {
+        if (warp == 8) {
+          if (!mha_dq_mma<DQK>(p, m, sb, tmem, blocks)) mha_bwd_raise(m, kErrMhaDqMmaWait);
+          mma_commit(smem_u32(&m.drain));   // every MMA issued completes before TMEM is freed
+          mbar_wait(smem_u32(&m.drain), 0, global_timer_ns() + 100000000ull, &never);
+        } else {
+          int kf = 0, vf = 0;
+          if (!mha_dq_load<DQK>(p, m, sb, w, t0, blocks, pack0, kf, vf)) mha_bwd_raise(m, kErrMhaDqLoadWait);
+          // every copy issued has landed before the CTA exits
+          const uint64_t dl = global_timer_ns() + 100000000ull;
+          mbar_wait(smem_u32(&m.q_full), 0, dl, &never);
+          for (int i = max(0, kf - C::kKStages); i < kf; ++i)
+            mbar_wait(smem_u32(&m.k_full[i % C::kKStages]), i / C::kKStages & 1, dl, &never);
+          for (int i = max(0, vf - C::kVStages); i < vf; ++i)
+            mbar_wait(smem_u32(&m.v_full[i % C::kVStages]), i / C::kVStages & 1, dl, &never);
         }
       }
+      __syncwarp();
     }
-    mha_store<NQK>(p.dk + r * (64 * NQK), lane, dk, p.scale);
-    mha_store<2>(p.dv + r * 128, lane, dv, 1.f);
   }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 8) tmem_dealloc(tmem, 512);
+}
+
+// ------------------------------------------------------------------ dk, dv
+
+constexpr int kMhaStats = 4;   // query blocks whose lse and D are held
+
+struct __align__(16) MhaDkvMisc {
+  uint64_t k_full, v_ready, q_full[4], q_empty[4], do_full[4], do_empty[4], stat_full[kMhaStats], stat_empty[kMhaStats];
+  uint64_t s_full, p_full, t_full, ds_full, out_full, drain;
+  uint32_t tmem_base;
+  int abort_flag;
+  int prior_error;
+  MhaWork work;
+  alignas(16) float lse2[kMhaStats][kMhaTile];    // read four at a time
+  alignas(16) float delta[kMhaStats][kMhaTile];
+};
+
+template <int DQK>
+struct MhaDkvShape {
+  static constexpr int kN = DQK == 192 ? 64 : 128;             // query rows of a block
+  static constexpr bool kVTmem = DQK == 192;
+  static constexpr int kSub = DQK / 64;
+  static constexpr int kStages = DQK == 192 ? 4 : 2;
+  static constexpr uint32_t kQUnit = kN * 128;                 // 64 columns of a block
+  static constexpr uint32_t kQBytes = kSub * kQUnit, kDoBytes = 2 * kQUnit;
+  static constexpr uint32_t kVOff = kSub * kMhaUnit;
+  static constexpr uint32_t kQOff = kVOff + (kVTmem ? 0 : 2 * kMhaUnit), kDoOff = kQOff + kStages * kQBytes;
+  static constexpr uint32_t kMiscOff = kDoOff + kStages * kDoBytes;
+  static constexpr int kBytes = static_cast<int>(kMiscOff) + static_cast<int>(sizeof(MhaDkvMisc)) + 1024;
+  static constexpr int kThreads = 11 * 32;
+  // columns of TMEM
+  static constexpr uint32_t kDv = 0, kDk = 128, kS = 128 + DQK, kT = kS + kN, kV = kT + kN;
+  static_assert(kBytes <= kMaxSmem, "shared memory");
+  static_assert(kT + kN + (kVTmem ? 64 : 0) <= 512, "TMEM");
+};
+
+// The query blocks of one key tile: blocks of tok_tile tokens from the first that sees
+// its first key, for each pack of heads of the group.
+struct MhaQueries {
+  int first, blocks, total;
+  __device__ __forceinline__ MhaQueries(const MhaBwdParams& p, const MhaWork& w) {
+    const int lq = w.q1 - w.q0, lk = w.k1 - w.k0;
+    first = max(0, w.tile * kMhaTile - (lk - lq));
+    blocks = first < lq ? (lq - first + p.tok_tile - 1) / p.tok_tile : 0;
+    total = blocks * (p.group / p.pack);
+  }
+};
+
+template <int DQK>
+__device__ __forceinline__ bool mha_dkv_load(const MhaBwdParams& p, MhaDkvMisc& m, uint32_t sb, const MhaWork& w,
+                                             const MhaQueries& s, int kvh, int& q_fills, int& do_fills) {
+  using C = MhaDkvShape<DQK>;
+  const volatile int* ab = &m.abort_flag;
+  const uint64_t deadline = global_timer_ns() + p.timeout_ns;
+  const int row = w.k0 + w.tile * kMhaTile;
+  const uint32_t kb = smem_u32(&m.k_full);
+  mbar_arrive_expect_tx(kb, (C::kSub + (C::kVTmem ? 0 : 2)) * kMhaUnit);
+  for (int c = 0; c < C::kSub; ++c) tma_load_3d(sb + c * kMhaUnit, &p.map_k, 64 * c, kvh, row, kb);
+  if (!C::kVTmem)
+    for (int c = 0; c < 2; ++c) tma_load_3d(sb + C::kVOff + c * kMhaUnit, &p.map_v, 64 * c, kvh, row, kb);
+  const uint32_t bytes = static_cast<uint32_t>(p.pack * p.tok_tile) * 128u;
+  int head = kvh * p.group, b = 0;
+  for (int j = 0; j < s.total; ++j) {
+    const int st = j % C::kStages, par = j / C::kStages & 1, tok = w.q0 + s.first + b * p.tok_tile;
+    if (!mbar_wait(smem_u32(&m.q_empty[st]), par ^ 1, deadline, ab)) return false;
+    uint32_t bar = smem_u32(&m.q_full[st]);
+    mbar_arrive_expect_tx(bar, C::kSub * bytes);
+    ++q_fills;
+    for (int c = 0; c < C::kSub; ++c)
+      tma_load_3d(sb + C::kQOff + st * C::kQBytes + c * C::kQUnit, &p.map_q, 64 * c, head, tok, bar);
+    if (!mbar_wait(smem_u32(&m.do_empty[st]), par ^ 1, deadline, ab)) return false;
+    bar = smem_u32(&m.do_full[st]);
+    mbar_arrive_expect_tx(bar, 2 * bytes);
+    ++do_fills;
+    for (int c = 0; c < 2; ++c)
+      tma_load_3d(sb + C::kDoOff + st * C::kDoBytes + c * C::kQUnit, &p.map_do, 64 * c, head, tok, bar);
+    if (++b == s.blocks) {
+      b = 0;
+      head += p.pack;
+    }
+  }
+  return true;
+}
+
+template <int DQK>
+__device__ __forceinline__ bool mha_dkv_mma(const MhaBwdParams& p, MhaDkvMisc& m, uint32_t sb, uint32_t tmem, int total) {
+  using C = MhaDkvShape<DQK>;
+  constexpr uint32_t kIdescS = idesc_bf16_f32(kMhaTile, C::kN, false, false);
+  constexpr uint32_t kIdescV = idesc_bf16_f32(kMhaTile, kMhaDv, false, true);
+  constexpr uint32_t kIdescK = idesc_bf16_f32(kMhaTile, DQK, false, true);
+  const volatile int* ab = &m.abort_flag;
+  const uint64_t deadline = global_timer_ns() + p.timeout_ns;
+  auto scores = [&](int j) -> bool {
+    const int st = j % C::kStages;
+    if (!mbar_wait(smem_u32(&m.q_full[st]), j / C::kStages & 1, deadline, ab)) return false;
+    const uint32_t q = sb + C::kQOff + st * C::kQBytes;
+#pragma unroll
+    for (int kk = 0; kk < DQK / 16; ++kk)
+      mma_bf16_ss(tmem + C::kS, smem_desc(sb + (kk >> 2) * kMhaUnit + (kk & 3) * 32, 16, 1024, SWZ_128B),
+                  smem_desc(q + (kk >> 2) * C::kQUnit + (kk & 3) * 32, 16, 1024, SWZ_128B), kIdescS, kk > 0 ? 1u : 0u);
+    mma_commit(smem_u32(&m.s_full));
+    return true;
+  };
+  auto values = [&](int j) -> bool {
+    const int st = j % C::kStages;
+    if (!mbar_wait(smem_u32(&m.do_full[st]), j / C::kStages & 1, deadline, ab)) return false;
+    const uint32_t g = sb + C::kDoOff + st * C::kDoBytes;
+#pragma unroll
+    for (int kk = 0; kk < kMhaDv / 16; ++kk) {
+      const uint64_t b = smem_desc(g + (kk >> 2) * C::kQUnit + (kk & 3) * 32, 16, 1024, SWZ_128B);
+      if (C::kVTmem)
+        mma_bf16_ts(tmem + C::kT, tmem + C::kV + 8 * kk, b, kIdescS, kk > 0 ? 1u : 0u);
+      else
+        mma_bf16_ss(tmem + C::kT, smem_desc(sb + C::kVOff + (kk >> 2) * kMhaUnit + (kk & 3) * 32, 16, 1024, SWZ_128B), b,
+                    kIdescS, kk > 0 ? 1u : 0u);
+    }
+    mma_commit(smem_u32(&m.t_full));
+    return true;
+  };
+  // either half's P^T and dS^T are at the start of its own columns
+  auto step_at = [](int kk) -> uint32_t {
+    constexpr int kHalf = C::kN / 32;
+    return static_cast<uint32_t>(kk < kHalf ? 8 * kk : C::kN / 2 + 8 * (kk - kHalf));
+  };
+  if (!mbar_wait(smem_u32(&m.k_full), 0, deadline, ab)) return false;
+  if (!scores(0)) return false;
+  if (C::kVTmem) {
+    if (!mbar_wait(smem_u32(&m.v_ready), 0, deadline, ab)) return false;
+    tc_fence_after();
+  }
+  if (!values(0)) return false;
+  for (int j = 0; j < total; ++j) {
+    const int st = j % C::kStages;
+    if (!mbar_wait(smem_u32(&m.p_full), j & 1, deadline, ab)) return false;
+    tc_fence_after();
+    const uint32_t g = sb + C::kDoOff + st * C::kDoBytes, q = sb + C::kQOff + st * C::kQBytes;
+#pragma unroll
+    for (int kk = 0; kk < C::kN / 16; ++kk)
+      mma_bf16_ts(tmem + C::kDv, tmem + C::kS + step_at(kk), smem_desc(g + kk * 2048, C::kQUnit, 1024, SWZ_128B), kIdescV,
+                  j + kk > 0 ? 1u : 0u);
+    mma_commit(smem_u32(&m.do_empty[st]));
+    if (j + 1 < total && !scores(j + 1)) return false;
+    if (!mbar_wait(smem_u32(&m.ds_full), j & 1, deadline, ab)) return false;
+    tc_fence_after();
+#pragma unroll
+    for (int kk = 0; kk < C::kN / 16; ++kk)
+      mma_bf16_ts(tmem + C::kDk, tmem + C::kT + step_at(kk), smem_desc(q + kk * 2048, C::kQUnit, 1024, SWZ_128B), kIdescK,
+                  j + kk > 0 ? 1u : 0u);
+    mma_commit(smem_u32(&m.q_empty[st]));
+    if (j + 1 < total && !values(j + 1)) return false;
+  }
+  mma_commit(smem_u32(&m.out_full));
+  return true;
+}
+
+// The rows' lse (in powers of two) and D; where D is not finite the row's gradient was
+// not, and its weights become NaN.  Rows of no token weigh nothing.
+template <int DQK>
+__device__ __forceinline__ bool mha_dkv_stats(const MhaBwdParams& p, MhaDkvMisc& m, const MhaWork& w, const MhaQueries& s,
+                                              int kvh) {
+  using C = MhaDkvShape<DQK>;
+  const volatile int* ab = &m.abort_flag;
+  const uint64_t deadline = global_timer_ns() + p.timeout_ns;
+  const int lane = static_cast<int>(lane_id()), lq = w.q1 - w.q0;
+  int head = kvh * p.group, b = 0;
+  for (int j = 0; j < s.total; ++j) {
+    const int st = j % kMhaStats;
+    float l[C::kN / 32], d[C::kN / 32];
+#pragma unroll
+    for (int i = 0; i < C::kN / 32; ++i) {
+      const int r = 32 * i + lane, tok = s.first + b * p.tok_tile + r / p.pack;
+      l[i] = INFINITY;
+      d[i] = 0.f;
+      if (r < p.pack * p.tok_tile && tok < lq) {
+        const size_t at = static_cast<size_t>(w.q0 + tok) * p.h_q + head + r % p.pack;
+        l[i] = __ldg(p.lse + at) * 1.4426950408889634f;
+        d[i] = __ldg(p.delta + at);
+        if (!(fabsf(d[i]) <= 3.402823466e38f)) l[i] = __uint_as_float(0x7fc00000u);
+      }
+    }
+    if (!mbar_wait(smem_u32(&m.stat_empty[st]), (j / kMhaStats & 1) ^ 1, deadline, ab)) return false;
+#pragma unroll
+    for (int i = 0; i < C::kN / 32; ++i) {
+      m.lse2[st][32 * i + lane] = l[i];
+      m.delta[st][32 * i + lane] = d[i];
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&m.stat_full[st]));
+    if (++b == s.blocks) {
+      b = 0;
+      head += p.pack;
+    }
+  }
+  return true;
+}
+
+template <int DQK>
+__device__ __forceinline__ bool mha_dkv_rows(const MhaBwdParams& p, MhaDkvMisc& m, uint32_t sb, uint32_t tmem,
+                                             const MhaWork& w, const MhaQueries& s, int kvh) {
+  using C = MhaDkvShape<DQK>;
+  constexpr int kHalf = C::kN / 2;
+  const volatile int* ab = &m.abort_flag;
+  const uint64_t deadline = global_timer_ns() + p.timeout_ns;
+  const int row = static_cast<int>(threadIdx.x) & 127, half = static_cast<int>(threadIdx.x) >> 7;
+  const int lq = w.q1 - w.q0, lk = w.k1 - w.k0;
+  const int key = w.tile * kMhaTile + row;
+  const bool live = key < lk;
+  const uint32_t lane0 = tmem + (static_cast<uint32_t>((row >> 5) * 32) << 16);
+  if (C::kVTmem && s.total > 0) {
+    uint4 v[8];
+    const uint4* vp = reinterpret_cast<const uint4*>(p.v + (w.k0 + key) * p.v_tok + kvh * p.v_head + 64 * half);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = live ? __ldg(vp + i) : make_uint4(0, 0, 0, 0);
+    mha_row_to_tmem(lane0 + C::kV + 32 * half, v);
+    tmem_wait_st();
+    tc_fence_before();
+    __syncwarp();
+    if (lane_id() == 0) mbar_arrive(smem_u32(&m.v_ready));
+  }
+  const int last_key = min((w.tile + 1) * kMhaTile, lk) - 1;
+  const uint32_t ts = lane0 + C::kS + kHalf * half, tt = lane0 + C::kT + kHalf * half;
+  int b = 0;
+  for (int j = 0; j < s.total; ++j) {
+    const int t0 = s.first + b * p.tok_tile;
+    if (++b == s.blocks) b = 0;
+    const bool edge = t0 + lk - lq < last_key || t0 + p.tok_tile > lq;   // some rows do not see all of the keys
+    // the columns that see this thread's key
+    const int lo = edge ? p.pack * (key - (lk - lq) - t0) - kHalf * half : 0;
+    const int hi = edge ? p.pack * (lq - t0) - kHalf * half : kHalf;
+    const int st = j % kMhaStats;
+    if (!mbar_wait(smem_u32(&m.s_full), j & 1, deadline, ab)) return false;
+    tc_fence_after();
+    float x[kHalf];
+    if constexpr (kHalf == 64) tmem_load64(ts, x);
+    else tmem_load32(ts, x);
+    if (!mbar_wait(smem_u32(&m.stat_full[st]), j / kMhaStats & 1, deadline, ab)) return false;
+    if (edge) {
+      // the products with P and dS must not meet what is not finite in a row that does not
+      // see a key; the product that gives T has read dout by then
+      if (!mbar_wait(smem_u32(&m.t_full), j & 1, deadline, ab)) return false;
+      const int qs = j % C::kStages;
+      if (!mbar_wait(smem_u32(&m.q_full[qs]), j / C::kStages & 1, deadline, ab) ||
+          !mbar_wait(smem_u32(&m.do_full[qs]), j / C::kStages & 1, deadline, ab))
+        return false;
+      mha_clear(sb + C::kQOff + qs * C::kQBytes, C::kQBytes);
+      mha_clear(sb + C::kDoOff + qs * C::kDoBytes, C::kDoBytes);
+    }
+    const float4* l4 = reinterpret_cast<const float4*>(&m.lse2[st][kHalf * half]);
+#pragma unroll
+    for (int i = 0; i < kHalf; i += 4) {
+      const float4 l = l4[i >> 2];
+      x[i] = fast_exp2(fmaf(x[i], p.scale_log2, -l.x));
+      x[i + 1] = fast_exp2(fmaf(x[i + 1], p.scale_log2, -l.y));
+      x[i + 2] = fast_exp2(fmaf(x[i + 2], p.scale_log2, -l.z));
+      x[i + 3] = fast_exp2(fmaf(x[i + 3], p.scale_log2, -l.w));
+    }
+    if (edge) {
+#pragma unroll
+      for (int i = 0; i < kHalf; ++i) x[i] = i >= lo && i < hi ? x[i] : 0.f;
+    }
+#pragma unroll
+    for (int c = 0; c < kHalf; c += 32) {
+      float pk[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) pk[i] = __uint_as_float(pack_bf16x2(x[c + 2 * i], x[c + 2 * i + 1]));
+      tmem_st16(ts + c / 2, pk);
+    }
+    tmem_wait_st();
+    tc_fence_before();
+    __syncwarp();
+    if (lane_id() == 0) mbar_arrive(smem_u32(&m.p_full));
+    if (!mbar_wait(smem_u32(&m.t_full), j & 1, deadline, ab)) return false;
+    tc_fence_after();
+    const float4* d4 = reinterpret_cast<const float4*>(&m.delta[st][kHalf * half]);
+#pragma unroll
+    for (int c = 0; c < kHalf; c += 32) {
+      float y[32];
+      tmem_load32(tt + c, y);
+#pragma unroll
+      for (int i = 0; i < 32; i += 4) {
+        const float4 d = d4[(c + i) >> 2];
+        y[i] = x[c + i] * (y[i] - d.x);
+        y[i + 1] = x[c + i + 1] * (y[i + 1] - d.y);
+        y[i + 2] = x[c + i + 2] * (y[i + 2] - d.z);
+        y[i + 3] = x[c + i + 3] * (y[i + 3] - d.w);
+      }
+      if (edge) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) y[i] = c + i >= lo && c + i < hi ? y[i] : 0.f;
+      }
+      float pk[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) pk[i] = __uint_as_float(pack_bf16x2(y[2 * i], y[2 * i + 1]));
+      tmem_st16(tt + c / 2, pk);   // columns that have been read
+    }
+    tmem_wait_st();
+    tc_fence_before();
+    __syncwarp();
+    if (lane_id() == 0) {
+      mbar_arrive(smem_u32(&m.ds_full));
+      mbar_arrive(smem_u32(&m.stat_empty[st]));
+    }
+  }
+  if (s.total > 0) {
+    if (!mbar_wait(smem_u32(&m.out_full), 0, deadline, ab)) return false;
+    tc_fence_after();
+  }
+  const size_t at = live ? static_cast<size_t>(w.k0 + key) * p.h_kv + kvh : 0;
+  mha_store_sums<2>(p.dv + at * kMhaDv + 64 * half, lane0 + C::kDv + 64 * half, 1.f, s.total > 0, live);
+  mha_store_sums<DQK / 64>(p.dk + at * DQK + half * (DQK / 2), lane0 + C::kDk + half * (DQK / 2), p.scale, s.total > 0, live);
+  return true;
+}
+
+template <int DQK>
+__global__ void __launch_bounds__(MhaDkvShape<DQK>::kThreads, 1) dense_mha_dkv_kernel(
+    const __grid_constant__ MhaBwdParams p) {
+  using C = MhaDkvShape<DQK>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sbase = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  MhaDkvMisc& m = *reinterpret_cast<MhaDkvMisc*>(sbase + C::kMiscOff);
+  const int warp = static_cast<int>(threadIdx.x >> 5);
+  const uint32_t sb = smem_u32(sbase);
+  const int slot = static_cast<int>(blockIdx.x % static_cast<unsigned>(p.slots));
+  const int kvh = static_cast<int>(blockIdx.x / static_cast<unsigned>(p.slots));
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(smem_u32(&m.q_full[i]), 1);
+      mbar_init(smem_u32(&m.q_empty[i]), 1);
+      mbar_init(smem_u32(&m.do_full[i]), 1);
+      mbar_init(smem_u32(&m.do_empty[i]), 1);
+    }
+    for (int i = 0; i < kMhaStats; ++i) {
+      mbar_init(smem_u32(&m.stat_full[i]), 1);
+      mbar_init(smem_u32(&m.stat_empty[i]), 8);   // one arrival per row warp
+    }
+    mbar_init(smem_u32(&m.k_full), 1);
+    mbar_init(smem_u32(&m.v_ready), 8);
+    mbar_init(smem_u32(&m.s_full), 1);
+    mbar_init(smem_u32(&m.p_full), 8);
+    mbar_init(smem_u32(&m.t_full), 1);
+    mbar_init(smem_u32(&m.ds_full), 8);
+    mbar_init(smem_u32(&m.out_full), 1);
+    mbar_init(smem_u32(&m.drain), 1);
+    m.abort_flag = 0;
+    m.prior_error = *reinterpret_cast<volatile int*>(&g_device_error);
+    fence_mbar_init();
+    prefetch_tmap(&p.map_q);
+    prefetch_tmap(&p.map_do);
+    prefetch_tmap(&p.map_k);
+    prefetch_tmap(&p.map_v);
+  }
+  if (warp == 8) {
+    tmem_alloc(smem_u32(&m.tmem_base), 512);
+    tmem_relinquish();
+  }
+  if (warp == 9) {
+    const MhaWork w = mha_find(p.cu_q, p.cu_kv, p.batch, p.total_q, p.total_kv, slot, kMhaTile, true, true);
+    if (lane_id() == 0) m.work = w;
+  }
+  if (p.pack * p.tok_tile < C::kN) {
+    // rows that no copy writes: a block's last ones, which weigh nothing, have to be numbers
+    for (uint32_t i = threadIdx.x * 16; i < C::kStages * (C::kQBytes + C::kDoBytes); i += C::kThreads * 16)
+      *reinterpret_cast<uint4*>(sbase + C::kQOff + i) = make_uint4(0, 0, 0, 0);
+    fence_proxy_async_smem();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = m.tmem_base;
+  const MhaWork w = m.work;
+
+  if (m.prior_error == 0 && w.k1 > w.k0) {
+    const MhaQueries s(p, w);
+    const int never = 0;
+    if (warp < 8) {
+      if (!mha_dkv_rows<DQK>(p, m, sb, tmem, w, s, kvh)) mha_bwd_raise(m, kErrMhaDkvRowsWait);
+    } else if (s.total > 0) {
+      if (warp == 10) {
+        if (!mha_dkv_stats<DQK>(p, m, w, s, kvh)) mha_bwd_raise(m, kErrMhaDkvStatWait);
+      } else if (lane_id() == 0) {
+        if (warp == 8) {
+          if (!mha_dkv_mma<DQK>(p, m, sb, tmem, s.total)) mha_bwd_raise(m, kErrMhaDkvMmaWait);
+          mma_commit(smem_u32(&m.drain));   // every MMA issued completes before TMEM is freed
+          mbar_wait(smem_u32(&m.drain), 0, global_timer_ns() + 100000000ull, &never);
+        } else {
+          int qf = 0, df = 0;
+          if (!mha_dkv_load<DQK>(p, m, sb, w, s, kvh, qf, df)) mha_bwd_raise(m, kErrMhaDkvLoadWait);
+          // every copy issued has landed before the CTA exits
+          const uint64_t dl = global_timer_ns() + 100000000ull;
+          mbar_wait(smem_u32(&m.k_full), 0, dl, &never);
+          for (int i = max(0, qf - C::kStages); i < qf; ++i)
+            mbar_wait(smem_u32(&m.q_full[i % C::kStages]), i / C::kStages & 1, dl, &never);
+          for (int i = max(0, df - C::kStages); i < df; ++i)
+            mbar_wait(smem_u32(&m.do_full[i % C::kStages]), i / C::kStages & 1, dl, &never);
+        }
+      }
+      __syncwarp();
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 8) tmem_dealloc(tmem, 512);
 }
 
 }  // namespace smla

@@ -163,36 +163,11 @@ sparse_mla_status_t check_mha(const MhaRows& q, const MhaRows& k, const MhaRows&
   return SPARSE_MLA_OK;
 }
 
-smla::MhaParams mha_params(const MhaRows& q, const MhaRows& k, const MhaRows& v, const int32_t* cu_q,
-                           const int32_t* cu_kv, int batch, float sm_scale, int total_q, int total_kv, int h_q,
-                           int h_kv) {
-  smla::MhaParams p;
-  std::memset(&p, 0, sizeof(p));
-  p.q = static_cast<const __nv_bfloat16*>(q.p);
-  p.q_tok = q.tok;
-  p.q_head = q.head;
-  p.k = static_cast<const __nv_bfloat16*>(k.p);
-  p.k_tok = k.tok;
-  p.k_head = k.head;
-  p.v = static_cast<const __nv_bfloat16*>(v.p);
-  p.v_tok = v.tok;
-  p.v_head = v.head;
-  p.cu_q = cu_q;
-  p.cu_kv = cu_kv;
-  p.batch = cu_q ? batch : 1;
-  p.total_q = total_q;
-  p.total_kv = total_kv;
-  p.h_q = h_q;
-  p.h_kv = h_kv;
-  p.scale = sm_scale;
-  return p;
-}
-
-// Query heads of one group that a tile takes side by side: the most that leave at most
-// 8 of its 128 rows unused.
-int mha_pack(int group) {
-  for (int n = group < smla::kMhaTile ? group : smla::kMhaTile; n > 1; --n)
-    if (group % n == 0 && smla::kMhaTile % n <= 8) return n;
+// Query heads of one group that a tile of `rows` takes side by side: the most that leave
+// at most one row in 16 unused.
+int mha_pack(int group, int rows) {
+  for (int n = group < rows ? group : rows; n > 1; --n)
+    if (group % n == 0 && rows % n <= rows / 16) return n;
   return 1;
 }
 
@@ -239,6 +214,14 @@ struct MhaState {
 };
 MhaState g_mha[kMaxDevices];   // under g_mu
 
+template <int DQK>
+bool mha_setup_bwd() {
+  return cudaFuncSetAttribute(smla::dense_mha_dq_kernel<DQK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              smla::MhaDqShape<DQK>::kBytes) == cudaSuccess &&
+         cudaFuncSetAttribute(smla::dense_mha_dkv_kernel<DQK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              smla::MhaDkvShape<DQK>::kBytes) == cudaSuccess;
+}
+
 template <int DQK, int NT>
 bool mha_setup_fwd() {
   return cudaFuncSetAttribute(smla::dense_mha_fwd_kernel<DQK, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -253,13 +236,82 @@ sparse_mla_status_t mha_device_setup() {
   std::lock_guard<std::mutex> lock(g_mu);
   MhaState& st = g_mha[dev];
   if (!st.set) {
-    st.set = mha_setup_fwd<192, 2>() && mha_setup_fwd<192, 1>() && mha_setup_fwd<128, 2>() && mha_setup_fwd<128, 1>();
+    st.set = mha_setup_fwd<192, 2>() && mha_setup_fwd<192, 1>() && mha_setup_fwd<128, 2>() && mha_setup_fwd<128, 1>() &&
+             mha_setup_bwd<192>() && mha_setup_bwd<128>();
     if (!st.set) cudaGetLastError();   // not the next launch's error
   }
   return st.set ? SPARSE_MLA_OK : SPARSE_MLA_ERR_CUDA;
 }
 
-int mha_ctas(long long rows) { return static_cast<int>(rows < 8 * 65536LL ? (rows + 7) / 8 : 65536); }
+// dq (and D into the workspace), then dk and dv.
+template <int DQK>
+sparse_mla_status_t mha_bwd_launch(const MhaRows& q, const MhaRows& k, const MhaRows& v, const MhaRows& g,
+                                   const int32_t* cu_q, const int32_t* cu_kv, int batch, float sm_scale, const void* out,
+                                   const float* lse, void* dq, void* dk, void* dv, int total_q, int total_kv, int h_q,
+                                   int h_kv, void* workspace, cudaStream_t cs) {
+  smla::MhaBwdParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.cu_q = cu_q;
+  p.cu_kv = cu_kv;
+  p.batch = cu_q ? batch : 1;
+  p.total_q = total_q;
+  p.total_kv = total_kv;
+  p.h_q = h_q;
+  p.h_kv = h_kv;
+  p.group = h_q / h_kv;
+  p.scale = sm_scale;
+  p.scale_log2 = mha_scale_log2(sm_scale);
+  p.v = static_cast<const __nv_bfloat16*>(v.p);
+  p.v_tok = v.tok;
+  p.v_head = v.head;
+  p.dout = static_cast<const __nv_bfloat16*>(g.p);
+  p.do_tok = g.tok;
+  p.do_head = g.head;
+  p.out = static_cast<const __nv_bfloat16*>(out);
+  p.lse = lse;
+  p.delta = static_cast<float*>(workspace);
+  p.dq = static_cast<__nv_bfloat16*>(dq);
+  p.dk = static_cast<__nv_bfloat16*>(dk);
+  p.dv = static_cast<__nv_bfloat16*>(dv);
+  const unsigned long long t = g_timeout_ns.load();
+  p.timeout_ns = t ? t : kDefaultTimeoutNs;
+  const int seqs = cu_q ? batch : 0;
+  sparse_mla_status_t st = SPARSE_MLA_OK;
+  // without rows on one side nothing of it is loaded: any map does
+  const bool both = total_q > 0 && total_kv > 0;
+  const MhaRows &mk = both ? k : (total_q > 0 ? q : k), &mv = both ? v : mk, &mq = both ? q : mk, &mg = both ? g : mk;
+  const int tk = both ? total_kv : (total_q > 0 ? total_q : total_kv), hk = both || total_q == 0 ? h_kv : h_q;
+  const int tq = both ? total_q : tk, hq = both ? h_q : hk, dv_cols = both ? smla::kMhaDv : DQK;
+  if ((st = mha_map(&p.map_k, mk, tk, hk, DQK, 1, smla::kMhaTile)) != SPARSE_MLA_OK ||
+      (st = mha_map(&p.map_v, mv, tk, hk, dv_cols, 1, smla::kMhaTile)) != SPARSE_MLA_OK)
+    return st;
+  auto queries = [&](int rows) {
+    p.pack = mha_pack(p.group, rows);
+    p.tok_tile = rows / p.pack;
+    if ((st = mha_map(&p.map_q, mq, tq, hq, DQK, p.pack, p.tok_tile)) == SPARSE_MLA_OK)
+      st = mha_map(&p.map_do, mg, tq, hq, dv_cols, p.pack, p.tok_tile);
+    return st == SPARSE_MLA_OK;
+  };
+  if (total_q > 0) {
+    using C = smla::MhaDqShape<DQK>;
+    if (!queries(smla::kMhaTile)) return st;
+    const long long slots = mha_slots(total_q, p.tok_tile, seqs, seqs > 0), ctas = slots * (h_q / p.pack);
+    if (ctas > INT_MAX) return SPARSE_MLA_ERR_INVALID_ARG;
+    p.slots = static_cast<int>(slots);
+    smla::dense_mha_dq_kernel<DQK><<<static_cast<unsigned>(ctas), C::kThreads, C::kBytes, cs>>>(p);
+    if (cudaGetLastError() != cudaSuccess) return SPARSE_MLA_ERR_CUDA;
+  }
+  if (total_kv > 0) {
+    using C = smla::MhaDkvShape<DQK>;
+    if (!queries(C::kN)) return st;
+    const long long slots = mha_slots(total_kv, smla::kMhaTile, seqs, seqs > 0), ctas = slots * h_kv;
+    if (ctas > INT_MAX) return SPARSE_MLA_ERR_INVALID_ARG;
+    p.slots = static_cast<int>(slots);
+    smla::dense_mha_dkv_kernel<DQK><<<static_cast<unsigned>(ctas), C::kThreads, C::kBytes, cs>>>(p);
+    if (cudaGetLastError() != cudaSuccess) return SPARSE_MLA_ERR_CUDA;
+  }
+  return SPARSE_MLA_OK;
+}
 
 }  // namespace
 
@@ -285,7 +337,7 @@ sparse_mla_status_t dense_mha_fwd(const void* q, long long q_tok_stride, long lo
   smla::MhaFwdParams p;
   std::memset(&p, 0, sizeof(p));
   const int group = h_q / h_kv;
-  p.pack = mha_pack(group);
+  p.pack = mha_pack(group, smla::kMhaTile);
   p.tok_tile = smla::kMhaTile / p.pack;
   if ((st = mha_map(&p.map_q, rq, total_q, h_q, d_qk, p.pack, p.tok_tile)) != SPARSE_MLA_OK) return st;
   // without keys nothing is loaded: any map does
@@ -351,30 +403,12 @@ sparse_mla_status_t dense_mha_bwd(const void* q, long long q_tok_stride, long lo
   const size_t need = dense_mha_bwd_workspace_size(total_q, total_kv, batch, h_q, h_kv, d_qk, d_v);
   if (need > 0 && (!workspace || workspace_bytes < need)) return SPARSE_MLA_ERR_WORKSPACE_TOO_SMALL;
   if (!aligned(workspace, 16)) return SPARSE_MLA_ERR_INVALID_ARG;
-  smla::MhaParams p = mha_params(rq, rk, rv, cu_seqlens_q, cu_seqlens_kv, batch, sm_scale, total_q, total_kv, h_q, h_kv);
-  p.out = static_cast<__nv_bfloat16*>(const_cast<void*>(out));
-  p.lse = const_cast<float*>(lse);
-  p.dout = static_cast<const __nv_bfloat16*>(dout);
-  p.do_tok = dout_tok_stride;
-  p.do_head = dout_head_stride;
-  p.dq = static_cast<__nv_bfloat16*>(dq);
-  p.dk = static_cast<__nv_bfloat16*>(dk);
-  p.dv = static_cast<__nv_bfloat16*>(dv);
-  p.delta = static_cast<float*>(workspace);
-  cudaStream_t cs = static_cast<cudaStream_t>(stream);
-  if (total_q > 0) {
-    const int ctas = mha_ctas(static_cast<long long>(total_q) * h_q);
-    if (d_qk == 192) smla::dense_mha_dq_kernel<3><<<ctas, 256, 0, cs>>>(p);
-    else smla::dense_mha_dq_kernel<2><<<ctas, 256, 0, cs>>>(p);
-    if (cudaGetLastError() != cudaSuccess) return SPARSE_MLA_ERR_CUDA;
-  }
-  if (total_kv > 0) {
-    const int ctas = mha_ctas(static_cast<long long>(total_kv) * h_kv);
-    if (d_qk == 192) smla::dense_mha_dkv_kernel<3><<<ctas, 256, 0, cs>>>(p);
-    else smla::dense_mha_dkv_kernel<2><<<ctas, 256, 0, cs>>>(p);
-    if (cudaGetLastError() != cudaSuccess) return SPARSE_MLA_ERR_CUDA;
-  }
-  return SPARSE_MLA_OK;
+  if (total_q == 0 && total_kv == 0) return SPARSE_MLA_OK;
+  if ((st = mha_device_setup()) != SPARSE_MLA_OK) return st;
+  return d_qk == 192 ? mha_bwd_launch<192>(rq, rk, rv, rg, cu_seqlens_q, cu_seqlens_kv, batch, sm_scale, out, lse, dq, dk,
+                                           dv, total_q, total_kv, h_q, h_kv, workspace, static_cast<cudaStream_t>(stream))
+                     : mha_bwd_launch<128>(rq, rk, rv, rg, cu_seqlens_q, cu_seqlens_kv, batch, sm_scale, out, lse, dq, dk,
+                                           dv, total_q, total_kv, h_q, h_kv, workspace, static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"
