@@ -47,6 +47,55 @@ struct AddNormParams {
   float eps;
 };
 
+// Two floats side by side, each operation rounded as on its own.
+struct Pair {
+  unsigned long long v;
+};
+__device__ __forceinline__ Pair pair_of(float a, float b) {
+  Pair p;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(p.v) : "f"(a), "f"(b));
+  return p;
+}
+__device__ __forceinline__ float2 halves(Pair p) {
+  float2 f;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(p.v));
+  return f;
+}
+__device__ __forceinline__ Pair operator+(Pair a, Pair b) {
+  Pair p;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(p.v) : "l"(a.v), "l"(b.v));
+  return p;
+}
+__device__ __forceinline__ Pair operator-(Pair a, Pair b) {
+  Pair p;
+  asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(p.v) : "l"(a.v), "l"(b.v));
+  return p;
+}
+__device__ __forceinline__ Pair operator*(Pair a, Pair b) {
+  Pair p;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(p.v) : "l"(a.v), "l"(b.v));
+  return p;
+}
+__device__ __forceinline__ Pair fma(Pair a, Pair b, Pair c) {
+  Pair p;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(p.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return p;
+}
+
+// Two bf16 values as a pair of floats.
+__device__ __forceinline__ Pair unpack2(uint32_t v) { return pair_of(bf16_lo(v), bf16_hi(v)); }
+__device__ __forceinline__ uint32_t pack2(Pair p) {
+  const float2 f = halves(p);
+  return pack_bf16x2(f.x, f.y);
+}
+
+// hi + lo += b, two sums side by side (two_add's steps).
+__device__ __forceinline__ void pair_two_add(Pair& hi, Pair& lo, Pair b) {
+  const Pair s = hi + b, t = s - hi;
+  lo = lo + ((hi - (s - t)) + (b - t));
+  hi = s;
+}
+
 __device__ __forceinline__ Two two_sum(Two a, Two b) { return two_add({a.hi, __fadd_rn(a.lo, b.lo)}, b.hi); }
 
 __device__ __forceinline__ Two two_mul(Two a, Two b) {
@@ -73,10 +122,55 @@ __device__ __forceinline__ int scale_exponent(float top) {
   return top > 0.f ? min(max(k, -64), 31) : 0;
 }
 
+// Eight products u (exact floats) times the factor hi + lo, rounded once to bf16 (nearest
+// even).  |lo| of a renormalised product is at most half an ulp of its high part, so it
+// matters only where that lies halfway between two bf16 numbers, which is seldom: one
+// test for all eight.
+__device__ __forceinline__ uint4 times_factor(const Pair (&u)[4], Two f) {
+  const Pair fh = pair_of(f.hi, f.hi), fl = pair_of(f.lo, f.lo), minus = pair_of(-1.f, -1.f);
+  uint32_t out[4];
+  bool tie = false;
+  Pair h[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const Pair p = u[i] * fh;
+    h[i] = p + fma(u[i], fl, fma(u[i], fh, p * minus));
+    const float2 x = halves(h[i]);
+    out[i] = pack_bf16x2(x.x, x.y);
+    tie |= (__float_as_uint(x.x) & 0xffffu) == 0x8000u || (__float_as_uint(x.y) & 0xffffu) == 0x8000u;
+  }
+  if (tie) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 x = halves(u[i]);
+      out[i] = pack_bf16x2(two_mul_bf16(x.x, f), two_mul_bf16(x.y, f));
+    }
+  }
+  return make_uint4(out[0], out[1], out[2], out[3]);
+}
+
+// The largest magnitude of eight bf16 values as a bf16 bit pattern: a NaN's is above an
+// infinity's, and that above every number's.
+__device__ __forceinline__ uint32_t largest8(const uint4& v) {
+  const uint32_t m = 0x7fff7fffu;
+  const uint32_t a = __vmaxu2(__vmaxu2(v.x & m, v.y & m), __vmaxu2(v.z & m, v.w & m));
+  return max(a & 0xffffu, a >> 16);
+}
+
+// Codes of eight bf16 values times 2^-k.
+__device__ __forceinline__ uint2 codes8(const uint4& v, float down) {
+  float a[8];
+  unpack8(v, a);
+  uint32_t c[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) c[j] = e4m3x2_of(a[2 * j] * down, a[2 * j + 1] * down);
+  return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+}
+
 template <int V>
-__global__ void __launch_bounds__(V == 4 ? 512 : 1024) add_norm_kernel(const __grid_constant__ AddNormParams p) {
+__global__ void __launch_bounds__(1024) add_norm_kernel(const __grid_constant__ AddNormParams p) {
   __shared__ Two sums[2][32];
-  __shared__ float tops[2][32];
+  __shared__ uint32_t tops[2][32];
   const int lane = static_cast<int>(lane_id()), warp = static_cast<int>(threadIdx.x >> 5);
   const int warps = static_cast<int>(blockDim.x >> 5), nvec = p.d >> 3;
   const int groups = (p.d + kAddNormGroup - 1) / kAddNormGroup;
@@ -94,25 +188,22 @@ __global__ void __launch_bounds__(V == 4 ? 512 : 1024) add_norm_kernel(const __g
   fetch(r);
   for (; r < p.n; r += gridDim.x, buf ^= 1) {
     uint4 z[V];
-    Two ss = {0.f, 0.f};
+    Pair hi = pair_of(0.f, 0.f), lo = hi;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int vec = static_cast<int>(threadIdx.x + i * blockDim.x);
-      float a[8];
-      unpack8(nx[i], a);
       z[i] = nx[i];
       if (p.residual != nullptr) {
-        float b[8];
-        unpack8(nr[i], b);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) a[j] += b[j];
-        z[i] = pack8(a);
-        unpack8(z[i], a);
+        z[i] = make_uint4(pack2(unpack2(nx[i].x) + unpack2(nr[i].x)), pack2(unpack2(nx[i].y) + unpack2(nr[i].y)),
+                          pack2(unpack2(nx[i].z) + unpack2(nr[i].z)), pack2(unpack2(nx[i].w) + unpack2(nr[i].w)));
         if (vec < nvec) *reinterpret_cast<uint4*>(p.z + r * p.d + 8 * static_cast<size_t>(vec)) = z[i];
       }
+      const Pair a[4] = {unpack2(z[i].x), unpack2(z[i].y), unpack2(z[i].z), unpack2(z[i].w)};
 #pragma unroll
-      for (int j = 0; j < 8; ++j) ss = two_add(ss, __fmul_rn(a[j], a[j]));   // squares of 8-bit numbers: exact
+      for (int j = 0; j < 4; ++j) pair_two_add(hi, lo, a[j] * a[j]);   // squares of 8-bit numbers: exact
     }
+    const float2 sh = halves(hi), sl = halves(lo);
+    Two ss = two_sum({sh.x, sl.x}, {sh.y, sl.y});
     if (r + gridDim.x < p.n) fetch(r + gridDim.x);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
@@ -124,65 +215,47 @@ __global__ void __launch_bounds__(V == 4 ? 512 : 1024) add_norm_kernel(const __g
     for (int o = 16; o > 0; o >>= 1)
       ss = two_sum(ss, {__shfl_xor_sync(0xffffffffu, ss.hi, o), __shfl_xor_sync(0xffffffffu, ss.lo, o)});
     const Two f = norm_factor(ss, p);
-    float row_top = 0.f;   // NaN where a value of the row is not finite
-    uint4 y[V];
+    uint32_t row_top = 0;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int vec = static_cast<int>(threadIdx.x + i * blockDim.x);
-      float a[8], w[8];
-      unpack8(z[i], a);
-      unpack8(vec < nvec ? __ldg(reinterpret_cast<const uint4*>(p.weight) + vec) : make_uint4(0, 0, 0, 0), w);
-      bool bad = false;
-      float top = 0.f;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        a[j] = vec < nvec ? two_mul_bf16(__fmul_rn(a[j], w[j]), f) : 0.f;   // 8 x 8 bits: exact
-        top = fmaxf(top, fabsf(a[j]));
-        bad |= !(fabsf(a[j]) <= 3.402823466e38f);
-      }
+      const uint4 w = vec < nvec ? __ldg(reinterpret_cast<const uint4*>(p.weight) + vec) : make_uint4(0, 0, 0, 0);
+      // 8 x 8 bits: exact
+      const Pair u[4] = {unpack2(z[i].x) * unpack2(w.x), unpack2(z[i].y) * unpack2(w.y),
+                         unpack2(z[i].z) * unpack2(w.z), unpack2(z[i].w) * unpack2(w.w)};
+      z[i] = times_factor(u, f);
       if (p.form == kAddNormBf16) {
-        if (vec < nvec) reinterpret_cast<uint4*>(p.out)[r * nvec + vec] = pack8(a);
+        if (vec < nvec) reinterpret_cast<uint4*>(p.out)[r * nvec + vec] = z[i];
         continue;
       }
+      uint32_t top = vec < nvec ? largest8(z[i]) : 0u;
       if (p.form == kAddNormRow) {
-        y[i] = pack8(a);
-        row_top = bad || row_top != row_top ? __uint_as_float(0x7fc00000u) : fmaxf(row_top, top);
+        row_top = max(row_top, top);
         continue;
       }
 #pragma unroll
-      for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      bad = (__ballot_sync(0xffffffffu, bad) & (lane < 16 ? 0xffffu : 0xffff0000u)) != 0u;
-      const int k = scale_exponent(top);
+      for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const bool bad = top >= 0x7f80u;
+      const int k = scale_exponent(__uint_as_float(top << 16));
       const float down = __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
-      uint32_t c[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) c[j] = bad ? 0u : e4m3x2_of(a[2 * j] * down, a[2 * j + 1] * down);
       if (vec < nvec) {
-        reinterpret_cast<uint2*>(p.out)[r * nvec + vec] = make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+        reinterpret_cast<uint2*>(p.out)[r * nvec + vec] = bad ? make_uint2(0, 0) : codes8(z[i], down);
         if ((lane & 15) == 0)
-          p.scales[r * groups + (vec >> 4)] =
-              __uint_as_float(bad ? 0x7fc00000u : static_cast<uint32_t>(127 + k) << 23);
+          p.scales[r * groups + (vec >> 4)] = __uint_as_float(bad ? 0x7fc00000u : static_cast<uint32_t>(127 + k) << 23);
       }
     }
     if (p.form == kAddNormRow) {
-      // a NaN's image is the largest of the bit patterns of numbers without a sign
-      uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(row_top));
-      if (lane == 0) tops[buf][warp] = __uint_as_float(top);
+      row_top = __reduce_max_sync(0xffffffffu, row_top);
+      if (lane == 0) tops[buf][warp] = row_top;
       __syncthreads();
-      top = __reduce_max_sync(0xffffffffu, lane < warps ? __float_as_uint(tops[buf][lane]) : 0u);
-      const bool bad = top > 0x7f800000u;
-      const int k = scale_exponent(__uint_as_float(top));
+      row_top = __reduce_max_sync(0xffffffffu, lane < warps ? tops[buf][lane] : 0u);
+      const bool bad = row_top >= 0x7f80u;
+      const int k = scale_exponent(__uint_as_float(row_top << 16));
       const float down = __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         const int vec = static_cast<int>(threadIdx.x + i * blockDim.x);
-        float a[8];
-        unpack8(y[i], a);
-        uint32_t c[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) c[j] = bad ? 0u : e4m3x2_of(a[2 * j] * down, a[2 * j + 1] * down);
-        if (vec < nvec)
-          reinterpret_cast<uint2*>(p.out)[r * nvec + vec] = make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+        if (vec < nvec) reinterpret_cast<uint2*>(p.out)[r * nvec + vec] = bad ? make_uint2(0, 0) : codes8(z[i], down);
       }
       if (threadIdx.x == 0) p.scales[r] = __uint_as_float(bad ? 0x7fc00000u : static_cast<uint32_t>(127 + k) << 23);
     }
@@ -193,21 +266,18 @@ __global__ void __launch_bounds__(V == 4 ? 512 : 1024) add_norm_kernel(const __g
 //   dx = r (g - zhat mean(g zhat)) + dresidual,   dw = sum over rows of dout zhat.
 // A thread's columns are the same in every row, so its share of dw stays in registers.
 template <int V>
-__global__ void __launch_bounds__(V == 4 ? 512 : 1024) add_norm_bwd_kernel(const __grid_constant__ AddNormParams p) {
+__global__ void __launch_bounds__(1024) add_norm_bwd_kernel(const __grid_constant__ AddNormParams p) {
   __shared__ float2 sums[2][32];
   asm volatile("griddepcontrol.launch_dependents;");   // the weight's sums may be set up (they wait for this grid's end)
   const int lane = static_cast<int>(lane_id()), warp = static_cast<int>(threadIdx.x >> 5);
   const int warps = static_cast<int>(blockDim.x >> 5), nvec = p.d >> 3;
   const float inv_d = 1.f / static_cast<float>(p.d);
-  float acc[V][8];
-  uint4 nz[V], ng[V], nr[V], w[V];
+  Pair acc[V][4];
+  uint4 nz[V], ng[V], nr[V];
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int vec = static_cast<int>(threadIdx.x + i * blockDim.x);
-    w[i] = vec < nvec ? __ldg(reinterpret_cast<const uint4*>(p.weight) + vec) : make_uint4(0, 0, 0, 0);
+  for (int i = 0; i < V; ++i)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) acc[i][j] = 0.f;
-  }
+    for (int j = 0; j < 4; ++j) acc[i][j] = pair_of(0.f, 0.f);
   auto fetch = [&](long long r) {
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -217,28 +287,33 @@ __global__ void __launch_bounds__(V == 4 ? 512 : 1024) add_norm_bwd_kernel(const
       if (p.dresidual != nullptr) nr[i] = load_vec(p.dresidual + r * p.dresidual_step, vec, nvec);
     }
   };
+  auto weight = [&](int vec) {
+    return vec < nvec ? __ldg(reinterpret_cast<const uint4*>(p.weight) + vec) : make_uint4(0, 0, 0, 0);
+  };
   int buf = 0;
   long long r = blockIdx.x;
   fetch(r);
   for (; r < p.n; r += gridDim.x, buf ^= 1) {
     uint4 zv[V], gv[V], rv[V];
-    float ss = 0.f, dot = 0.f;
+    Pair sq = pair_of(0.f, 0.f), pr = sq;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       zv[i] = nz[i];
       gv[i] = ng[i];
       rv[i] = nr[i];
-      float a[8], g[8], u[8];
-      unpack8(zv[i], a);
-      unpack8(gv[i], g);
-      unpack8(w[i], u);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        ss += a[j] * a[j];
-        dot += g[j] * u[j] * a[j];
-      }
+      const uint4 w = weight(static_cast<int>(threadIdx.x + i * blockDim.x));
+      auto step = [&](uint32_t z, uint32_t g, uint32_t u) {
+        const Pair a = unpack2(z);
+        sq = fma(a, a, sq);
+        pr = fma(unpack2(g) * unpack2(u), a, pr);
+      };
+      step(zv[i].x, gv[i].x, w.x);
+      step(zv[i].y, gv[i].y, w.y);
+      step(zv[i].z, gv[i].z, w.z);
+      step(zv[i].w, gv[i].w, w.w);
     }
     if (r + gridDim.x < p.n) fetch(r + gridDim.x);
+    float ss = halves(sq).x + halves(sq).y, dot = halves(pr).x + halves(pr).y;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
       ss += __shfl_xor_sync(0xffffffffu, ss, o);
@@ -250,26 +325,25 @@ __global__ void __launch_bounds__(V == 4 ? 512 : 1024) add_norm_bwd_kernel(const
     ss = warp_sum(t.x);
     dot = warp_sum(t.y);
     const float f = rsqrtf(ss * inv_d + p.eps);
-    const float c = dot * inv_d * f * f;
+    const Pair f2 = pair_of(f, f), c2 = pair_of(-dot * inv_d * f * f, -dot * inv_d * f * f);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int vec = static_cast<int>(threadIdx.x + i * blockDim.x);
       if (vec >= nvec) continue;
-      float a[8], g[8], u[8];
-      unpack8(zv[i], a);
-      unpack8(gv[i], g);
-      unpack8(w[i], u);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        acc[i][j] += g[j] * (a[j] * f);
-        g[j] = f * (g[j] * u[j] - a[j] * c);
-      }
-      if (p.dresidual != nullptr) {
-        unpack8(rv[i], a);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) g[j] += a[j];
-      }
-      *reinterpret_cast<uint4*>(p.dx + r * p.d + 8 * static_cast<size_t>(vec)) = pack8(g);
+      const uint4 w = weight(vec);
+      auto step = [&](uint32_t z, uint32_t g, uint32_t u, uint32_t later, Pair& sum) -> uint32_t {
+        const Pair a = unpack2(z), y = unpack2(g);
+        sum = fma(y, a * f2, sum);
+        Pair d = f2 * fma(a, c2, y * unpack2(u));
+        if (p.dresidual != nullptr) d = d + unpack2(later);
+        return pack2(d);
+      };
+      uint4 o;
+      o.x = step(zv[i].x, gv[i].x, w.x, rv[i].x, acc[i][0]);
+      o.y = step(zv[i].y, gv[i].y, w.y, rv[i].y, acc[i][1]);
+      o.z = step(zv[i].z, gv[i].z, w.z, rv[i].z, acc[i][2]);
+      o.w = step(zv[i].w, gv[i].w, w.w, rv[i].w, acc[i][3]);
+      *reinterpret_cast<uint4*>(p.dx + r * p.d + 8 * static_cast<size_t>(vec)) = o;
     }
   }
 #pragma unroll
@@ -277,8 +351,8 @@ __global__ void __launch_bounds__(V == 4 ? 512 : 1024) add_norm_bwd_kernel(const
     const int vec = static_cast<int>(threadIdx.x + i * blockDim.x);
     if (vec >= nvec) continue;
     float4* o = reinterpret_cast<float4*>(p.part + static_cast<size_t>(blockIdx.x) * p.d + 8 * static_cast<size_t>(vec));
-    o[0] = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
-    o[1] = make_float4(acc[i][4], acc[i][5], acc[i][6], acc[i][7]);
+    o[0] = make_float4(halves(acc[i][0]).x, halves(acc[i][0]).y, halves(acc[i][1]).x, halves(acc[i][1]).y);
+    o[1] = make_float4(halves(acc[i][2]).x, halves(acc[i][2]).y, halves(acc[i][3]).x, halves(acc[i][3]).y);
   }
 }
 

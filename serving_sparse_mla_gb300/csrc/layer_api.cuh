@@ -42,16 +42,14 @@ smla::AddNormParams add_norm_params(const void* x, long long x_stride, const voi
 }
 
 // Vectors of 8 values per thread, and threads: whole warps that hold a row.
-int add_norm_vectors(int d) { return d <= 2048 ? 1 : (d <= 4096 ? 2 : 4); }
+int add_norm_vectors(int d, bool backward) { return d <= (backward ? 8192 : 2048) ? 1 : 2; }
 int add_norm_threads(int d, int v) { return ((d / 8 + v - 1) / v + 31) / 32 * 32; }
 
-// CTAs: as many as are resident at once.
-int add_norm_ctas(int n, int threads, int sms, int warps_per_sm) {
-  const long long most = static_cast<long long>(sms) * (warps_per_sm * 32 / threads > 0 ? warps_per_sm * 32 / threads : 1);
+// CTAs: as many as are resident at once (64 registers a thread).
+int add_norm_ctas(int n, int threads, int sms) {
+  const long long most = static_cast<long long>(sms) * (1024 / threads);
   return static_cast<int>(n < most ? n : most);
 }
-constexpr int kAddNormFwdWarps = 32;
-constexpr int kAddNormBwdWarps = 16;
 
 }  // namespace
 
@@ -78,12 +76,11 @@ sparse_mla_status_t mla_add_norm(const void* x, long long x_stride, const void* 
   p.out = out;
   p.scales = scales;
   p.form = out_format;
-  const int v = add_norm_vectors(d), threads = add_norm_threads(d, v);
-  const int ctas = add_norm_ctas(n, threads, sms, kAddNormFwdWarps);
+  const int v = add_norm_vectors(d, false), threads = add_norm_threads(d, v);
+  const int ctas = add_norm_ctas(n, threads, sms);
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   if (v == 1) smla::add_norm_kernel<1><<<ctas, threads, 0, cs>>>(p);
-  else if (v == 2) smla::add_norm_kernel<2><<<ctas, threads, 0, cs>>>(p);
-  else smla::add_norm_kernel<4><<<ctas, threads, 0, cs>>>(p);
+  else smla::add_norm_kernel<2><<<ctas, threads, 0, cs>>>(p);
   return cudaGetLastError() == cudaSuccess ? SPARSE_MLA_OK : SPARSE_MLA_ERR_CUDA;
 }
 
@@ -91,7 +88,7 @@ size_t mla_add_norm_bwd_workspace_size(int n, int d) {
   if (n < 1 || d < 8 || d % 8 != 0 || d > smla::kAddNormMaxWidth) return 0;
   int sms = 0;
   if (device_setup(&sms) != SPARSE_MLA_OK) return 0;
-  const int ctas = add_norm_ctas(n, add_norm_threads(d, add_norm_vectors(d)), sms, kAddNormBwdWarps);
+  const int ctas = add_norm_ctas(n, add_norm_threads(d, add_norm_vectors(d, true)), sms);
   return static_cast<size_t>(ctas) * static_cast<size_t>(d) * sizeof(float);   // one share of the sums per CTA
 }
 
@@ -120,11 +117,10 @@ sparse_mla_status_t mla_add_norm_bwd(const void* z, long long z_stride, const vo
   p.dresidual_step = dresidual_stride;
   p.dx = static_cast<__nv_bfloat16*>(dx);
   p.part = static_cast<float*>(workspace);
-  const int v = add_norm_vectors(d), threads = add_norm_threads(d, v);
-  const int ctas = add_norm_ctas(n, threads, sms, kAddNormBwdWarps);
+  const int v = add_norm_vectors(d, true), threads = add_norm_threads(d, v);
+  const int ctas = add_norm_ctas(n, threads, sms);
   if (v == 1) smla::add_norm_bwd_kernel<1><<<ctas, threads, 0, cs>>>(p);
-  else if (v == 2) smla::add_norm_bwd_kernel<2><<<ctas, threads, 0, cs>>>(p);
-  else smla::add_norm_bwd_kernel<4><<<ctas, threads, 0, cs>>>(p);
+  else smla::add_norm_bwd_kernel<2><<<ctas, threads, 0, cs>>>(p);
   if (cudaGetLastError() != cudaSuccess) return SPARSE_MLA_ERR_CUDA;
   const cudaError_t e = launch_dependent(smla::add_norm_weight_grad_kernel, dim3(static_cast<unsigned>((d + 31) / 32)),
                                          dim3(1024), cs, static_cast<const float*>(p.part), dweight, ctas, d);
