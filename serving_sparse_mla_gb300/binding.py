@@ -428,7 +428,7 @@ def sparse_mla_decode_fp8(q, kv_cache, block_table, cache_seqlens, indices, sm_s
 # ---------------------------------------------------------------- 4-bit cache decode
 
 FP4_SLOT_BYTES = 416
-_BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
+_BF16, _F32, _I32, _U8, _E4M3 = torch.bfloat16, torch.float32, torch.int32, torch.uint8, torch.float8_e4m3fn
 
 
 def _at(t: Optional[torch.Tensor]):
@@ -703,9 +703,10 @@ def mla_norm_rope_bwd(q, kv, positions, cos_sin, dq, dkv, q_weight=None, kv_weig
 
 def _wide_rows(t: torch.Tensor, n: int, d: int, name: str, dev) -> int:
     """Row stride in elements of bf16 rows [n, d], contiguous in themselves, each on 16 bytes."""
-    if (t.is_cuda and t.dtype is _BF16 and t.device == dev and t.shape == (n, d) and t.stride(1) == 1
-            and not t.stride(0) & 7 and not t.data_ptr() & 15):
-        return t.stride(0)
+    if t.is_cuda and t.dtype is _BF16 and t.device == dev and t.shape == (n, d):
+        step, one = t.stride()
+        if one == 1 and not step & 7 and not t.data_ptr() & 15:
+            return step
     _on_cuda(t, name)
     if t.dtype != _BF16:
         raise ValueError(f"{name} must be {_BF16}, got {t.dtype}")
@@ -718,24 +719,34 @@ def _wide_rows(t: torch.Tensor, n: int, d: int, name: str, dev) -> int:
     return step
 
 
-def _overlap(a: torch.Tensor, b: torch.Tensor) -> bool:
-    """Whether the memory between a's first and last element meets that of b's."""
-    if a.numel() == 0 or b.numel() == 0:
-        return False
-    ends = [x.data_ptr() + (sum((n - 1) * abs(s) for n, s in zip(x.shape, x.stride())) + 1) * x.element_size()
-            for x in (a, b)]
-    return a.data_ptr() < ends[1] and b.data_ptr() < ends[0]
+def _norm_weight(weight: torch.Tensor, d: int, dev) -> None:
+    if weight.dtype is _BF16 and weight.device == dev and weight.is_contiguous() and weight.numel() == d and weight.is_cuda:
+        return
+    _given(weight, _BF16, "weight", d, dev)
+    if weight.numel() != d:
+        raise ValueError(f"weight must hold {d} values, got {weight.numel()}")
 
 
-def _row_by_row(out: Optional[torch.Tensor], name: str, *inputs) -> None:
-    """An output [n, d] of whole rows may be one of the inputs, dense and at the same
-    address (each row is read before it is written), and may not share memory with
-    one in any other way."""
+def _apart(out: Optional[torch.Tensor], name: str, size: int, inputs, same=()) -> None:
+    """A given output's first `size` bytes may not meet memory that the call still
+    reads: `inputs` are (tensor, its row stride in elements or 0, name).  An output of
+    whole rows may be one of `same`, dense and at the same address (each row is read
+    before it is written)."""
     if out is None:
         return
-    for t, what in inputs:
-        if t is not None and _overlap(out, t) and not (out.data_ptr() == t.data_ptr() and t.is_contiguous()):
-            raise ValueError(f"{name} shares memory with {what} other than as the same dense tensor")
+    at = out.data_ptr()
+    for t, step, what in inputs:
+        if t is None:
+            continue
+        lo = t.data_ptr()
+        if step and t.shape[0] > 0:
+            first, last = min(0, (t.shape[0] - 1) * step), max(0, (t.shape[0] - 1) * step) + t.shape[1]
+        else:
+            first, last = 0, t.numel()
+        if at < lo + last * t.element_size() and lo + first * t.element_size() < at + size:
+            if not (what in same and lo == at and t.is_contiguous()):
+                raise ValueError(f"{name} shares memory with {what}"
+                                 + (" other than as the same dense tensor" if what in same else ""))
 
 
 def mla_add_norm(x, weight, residual=None, eps: float = 1e-6, group: Optional[int] = None, out=None, scales=None,
@@ -754,36 +765,38 @@ def mla_add_norm(x, weight, residual=None, eps: float = 1e-6, group: Optional[in
     n, d = x.shape
     dev = x.device
     x_step = _wide_rows(x, n, d, "x", dev)
-    _given(weight, _BF16, "weight", d, dev)
-    if weight.numel() != d:
-        raise ValueError(f"weight must hold {d} values, got {weight.numel()}")
-    res_step = _wide_rows(residual, n, d, "residual", dev) if residual is not None else 0
-    if group not in (None, 0, 128):
+    _norm_weight(weight, d, dev)
+    res_step = 0 if residual is None else _wide_rows(residual, n, d, "residual", dev)
+    if group is None:
+        form, n_scales, kind, width = 0, 0, _BF16, 2
+    elif group == 128 or group == 0:
+        form, n_scales, kind, width = (1, (d + 127) // 128, _E4M3, 1) if group else (2, 1, _E4M3, 1)
+    else:
         raise ValueError(f"group must be None, 128 or 0, got {group}")
-    form = 0 if group is None else (1 if group else 2)
-    n_scales = (d + 127) // 128 if form == 1 else 1
-    kind = torch.float8_e4m3fn if form else _BF16
-    _given(out, kind, "out", n * d, dev)
-    if scales is not None and not form:
-        raise ValueError("scales are given without a group")
-    _given(scales, _F32, "scales", n * n_scales, dev)
-    if residual is None and residual_out is not None:
-        raise ValueError("residual_out is given without residual")
-    _given(residual_out, _BF16, "residual_out", n * d, dev)
-    _row_by_row(residual_out, "residual_out", (x, "x"), (residual, "residual"))
-    for t, name in ((out, "out"), (scales, "scales")):
-        for u, what in ((x, "x"), (residual, "residual"), (weight, "weight"), (residual_out, "residual_out")):
-            if t is not None and u is not None and _overlap(t, u):
-                raise ValueError(f"{name} shares memory with {what}")
+    if out is not None or scales is not None or residual_out is not None:
+        _given(out, kind, "out", n * d, dev)
+        if scales is not None and not form:
+            raise ValueError("scales are given without a group")
+        _given(scales, _F32, "scales", n * n_scales, dev)
+        if residual is None and residual_out is not None:
+            raise ValueError("residual_out is given without residual")
+        _given(residual_out, _BF16, "residual_out", n * d, dev)
+        reads = (x, x_step, "x"), (residual, res_step, "residual"), (weight, 0, "weight")
+        _apart(residual_out, "residual_out", 2 * n * d, reads, ("x", "residual"))
+        reads += ((residual_out, 0, "residual_out"),)
+        _apart(out, "out", width * n * d, reads)
+        _apart(scales, "scales", 4 * n * n_scales, reads + ((out, 0, "out"),))
 
     def go(cs):
         o = torch.empty((n, d), dtype=kind, device=dev) if out is None else out
         sc = torch.empty((n, n_scales), dtype=_F32, device=dev) if form and scales is None else scales
-        z = residual_out
-        if residual is not None and z is None:
-            z = torch.empty((n, d), dtype=_BF16, device=dev)
-        return lib.mla_add_norm(x.data_ptr(), x_step, _at(residual), res_step, weight.data_ptr(), eps, o.data_ptr(),
-                                _at(sc), form, _at(z), n, d, cs), (o, sc, x if residual is None else z)
+        if residual is None:
+            z, res_at, z_at = x, None, None
+        else:
+            z = torch.empty((n, d), dtype=_BF16, device=dev) if residual_out is None else residual_out
+            res_at, z_at = residual.data_ptr(), z.data_ptr()
+        return lib.mla_add_norm(x.data_ptr(), x_step, res_at, res_step, weight.data_ptr(), eps, o.data_ptr(),
+                                sc.data_ptr() if form else None, form, z_at, n, d, cs), (o, sc, z)
 
     return _launch(go, dev, stream, "mla_add_norm")
 
@@ -806,20 +819,19 @@ def mla_add_norm_bwd(z, weight, dout, dresidual=None, eps: float = 1e-6, workspa
     n, d = z.shape
     dev = z.device
     z_step = _wide_rows(z, n, d, "z", dev)
-    _given(weight, _BF16, "weight", d, dev)
-    if weight.numel() != d:
-        raise ValueError(f"weight must hold {d} values, got {weight.numel()}")
+    _norm_weight(weight, d, dev)
     g_step = _wide_rows(dout, n, d, "dout", dev)
-    r_step = _wide_rows(dresidual, n, d, "dresidual", dev) if dresidual is not None else 0
-    _given(dx, _BF16, "dx", n * d, dev)
-    _given(dweight, _F32, "dweight", d, dev)
-    _row_by_row(dx, "dx", (dout, "dout"), (dresidual, "dresidual"))
-    for t, name in ((dx, "dx"), (dweight, "dweight"), (workspace, "workspace")):
-        for u, what in ((z, "z"), (weight, "weight")) + (() if name == "dx" else ((dout, "dout"),
-                                                                                 (dresidual, "dresidual"))):
-            if t is not None and u is not None and _overlap(t, u):
-                raise ValueError(f"{name} shares memory with {what}")
-    _workspace(workspace, dev)
+    r_step = 0 if dresidual is None else _wide_rows(dresidual, n, d, "dresidual", dev)
+    if dx is not None or dweight is not None or workspace is not None:
+        _given(dx, _BF16, "dx", n * d, dev)
+        _given(dweight, _F32, "dweight", d, dev)
+        _workspace(workspace, dev)
+        reads = (z, z_step, "z"), (weight, 0, "weight"), (dout, g_step, "dout"), (dresidual, r_step, "dresidual")
+        _apart(dx, "dx", 2 * n * d, reads, ("dout", "dresidual"))
+        reads += ((dx, 0, "dx"),)
+        _apart(dweight, "dweight", 4 * d, reads)
+        if workspace is not None:
+            _apart(workspace, "workspace", workspace.numel() * workspace.element_size(), reads + ((dweight, 0, "dweight"),))
 
     def go(cs):
         gx = torch.empty((n, d), dtype=_BF16, device=dev) if dx is None else dx
@@ -863,6 +875,21 @@ def _heads(t: torch.Tensor, name: str, dev):
 def _mha_args(q, k, v, cu_seqlens_q, cu_seqlens_kv):
     """(total_q, total_kv, heads, kv heads, d_qk, d_v, batch, device, strides) of checked arguments."""
     dev = q.device
+    if q.dim() == 3 and k.dim() == 3 and v.dim() == 3:
+        (nq, hq, dq), (nk, hk, dk), (nv, hv, dv) = q.shape, k.shape, v.shape
+        (qt, qh, q1), (kt, kh, k1), (vt, vh, v1) = q.stride(), k.stride(), v.stride()
+        if (q.is_cuda and q.dtype is _BF16 and k.dtype is _BF16 and v.dtype is _BF16 and k.device == dev
+                and v.device == dev and dq == dk and nk == nv and hk == hv and hk > 0 and hq % hk == 0
+                and q1 == 1 and k1 == 1 and v1 == 1 and not (qt | qh | kt | kh | vt | vh) & 7
+                and qt > 0 and qh > 0 and kt > 0 and kh > 0 and vt > 0 and vh > 0
+                and not (q.data_ptr() | k.data_ptr() | v.data_ptr()) & 15):
+            if cu_seqlens_q is None and cu_seqlens_kv is None:
+                return nq, nk, hq, hk, dq, dv, 1, dev, (qt, qh, kt, kh, vt, vh)
+            if cu_seqlens_q is not None and cu_seqlens_kv is not None:
+                n = cu_seqlens_q.numel()
+                if (n > 0 and cu_seqlens_kv.numel() == n and _dense(cu_seqlens_q, _I32, n, dev)
+                        and _dense(cu_seqlens_kv, _I32, n, dev)):
+                    return nq, nk, hq, hk, dq, dv, n - 1, dev, (qt, qh, kt, kh, vt, vh)
     steps = _heads(q, "q", dev) + _heads(k, "k", dev) + _heads(v, "v", dev)
     total_q, h_q, d_qk = q.shape
     total_kv, h_kv, d_k = k.shape

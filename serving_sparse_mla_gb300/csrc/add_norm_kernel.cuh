@@ -26,6 +26,8 @@ namespace smla {
 constexpr int kAddNormMaxWidth = 16384;
 constexpr int kAddNormGroup = 128;   // values under one scale
 
+constexpr int kAddNormRegs = 56;     // of a thread of the forward
+
 enum AddNormForm : int { kAddNormBf16 = 0, kAddNormGroups = 1, kAddNormRow = 2 };
 
 struct AddNormParams {
@@ -36,7 +38,7 @@ struct AddNormParams {
   __nv_bfloat16* z;               // [n, d], or null without a residual
   void* out;                      // [n, d] bf16 or e4m3
   float* scales;                  // [n, ceil(d / 128)] or [n]
-  int n, d, form;
+  int n, d;
   Two sqrt_d, d_eps;              // sqrt(d), d eps
   // backward
   const __nv_bfloat16* dout;
@@ -159,16 +161,14 @@ __device__ __forceinline__ uint32_t largest8(const uint4& v) {
 
 // Codes of eight bf16 values times 2^-k.
 __device__ __forceinline__ uint2 codes8(const uint4& v, float down) {
-  float a[8];
-  unpack8(v, a);
-  uint32_t c[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) c[j] = e4m3x2_of(a[2 * j] * down, a[2 * j + 1] * down);
-  return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+  const Pair d = pair_of(down, down);
+  const float2 a = halves(unpack2(v.x) * d), b = halves(unpack2(v.y) * d), c = halves(unpack2(v.z) * d),
+               e = halves(unpack2(v.w) * d);
+  return make_uint2(e4m3x2_of(a.x, a.y) | (e4m3x2_of(b.x, b.y) << 16), e4m3x2_of(c.x, c.y) | (e4m3x2_of(e.x, e.y) << 16));
 }
 
-template <int V>
-__global__ void __launch_bounds__(1024) add_norm_kernel(const __grid_constant__ AddNormParams p) {
+template <int V, int FORM>
+__global__ void __maxnreg__(kAddNormRegs) add_norm_kernel(const __grid_constant__ AddNormParams p) {
   __shared__ Two sums[2][32];
   __shared__ uint32_t tops[2][32];
   const int lane = static_cast<int>(lane_id()), warp = static_cast<int>(threadIdx.x >> 5);
@@ -215,7 +215,6 @@ __global__ void __launch_bounds__(1024) add_norm_kernel(const __grid_constant__ 
     for (int o = 16; o > 0; o >>= 1)
       ss = two_sum(ss, {__shfl_xor_sync(0xffffffffu, ss.hi, o), __shfl_xor_sync(0xffffffffu, ss.lo, o)});
     const Two f = norm_factor(ss, p);
-    uint32_t row_top = 0;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int vec = static_cast<int>(threadIdx.x + i * blockDim.x);
@@ -224,27 +223,35 @@ __global__ void __launch_bounds__(1024) add_norm_kernel(const __grid_constant__ 
       const Pair u[4] = {unpack2(z[i].x) * unpack2(w.x), unpack2(z[i].y) * unpack2(w.y),
                          unpack2(z[i].z) * unpack2(w.z), unpack2(z[i].w) * unpack2(w.w)};
       z[i] = times_factor(u, f);
-      if (p.form == kAddNormBf16) {
-        if (vec < nvec) reinterpret_cast<uint4*>(p.out)[r * nvec + vec] = z[i];
-        continue;
-      }
-      uint32_t top = vec < nvec ? largest8(z[i]) : 0u;
-      if (p.form == kAddNormRow) {
-        row_top = max(row_top, top);
-        continue;
-      }
+      if (FORM == kAddNormBf16 && vec < nvec) reinterpret_cast<uint4*>(p.out)[r * nvec + vec] = z[i];
+    }
+    if (FORM == kAddNormGroups) {
+      uint32_t top = 0;   // of either vector, side by side
 #pragma unroll
-      for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-      const bool bad = top >= 0x7f80u;
-      const int k = scale_exponent(__uint_as_float(top << 16));
-      const float down = __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
-      if (vec < nvec) {
-        reinterpret_cast<uint2*>(p.out)[r * nvec + vec] = bad ? make_uint2(0, 0) : codes8(z[i], down);
-        if ((lane & 15) == 0)
-          p.scales[r * groups + (vec >> 4)] = __uint_as_float(bad ? 0x7fc00000u : static_cast<uint32_t>(127 + k) << 23);
+      for (int i = 0; i < V; ++i)
+        if (static_cast<int>(threadIdx.x + i * blockDim.x) < nvec) top |= largest8(z[i]) << (16 * i);
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, o));
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int vec = static_cast<int>(threadIdx.x + i * blockDim.x);
+        const uint32_t t = i == 0 ? top << 16 : top & 0xffff0000u;
+        const bool bad = t >= 0x7f800000u;
+        const int k = scale_exponent(__uint_as_float(t));
+        const float down = __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
+        if (vec < nvec) {
+          reinterpret_cast<uint2*>(p.out)[r * nvec + vec] = bad ? make_uint2(0, 0) : codes8(z[i], down);
+          if ((lane & 15) == 0)
+            p.scales[r * groups + (vec >> 4)] =
+                __uint_as_float(bad ? 0x7fc00000u : static_cast<uint32_t>(127 + k) << 23);
+        }
       }
     }
-    if (p.form == kAddNormRow) {
+    if (FORM == kAddNormRow) {
+      uint32_t row_top = 0;
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (static_cast<int>(threadIdx.x + i * blockDim.x) < nvec) row_top = max(row_top, largest8(z[i]));
       row_top = __reduce_max_sync(0xffffffffu, row_top);
       if (lane == 0) tops[buf][warp] = row_top;
       __syncthreads();

@@ -45,10 +45,18 @@ smla::AddNormParams add_norm_params(const void* x, long long x_stride, const voi
 int add_norm_vectors(int d, bool backward) { return d <= (backward ? 8192 : 2048) ? 1 : 2; }
 int add_norm_threads(int d, int v) { return ((d / 8 + v - 1) / v + 31) / 32 * 32; }
 
-// CTAs: as many as are resident at once (64 registers a thread).
-int add_norm_ctas(int n, int threads, int sms) {
-  const long long most = static_cast<long long>(sms) * (1024 / threads);
-  return static_cast<int>(n < most ? n : most);
+// CTAs: as many as are resident at once.
+int add_norm_ctas(int n, int threads, int sms, int regs) {
+  const int most = sms * (65536 / regs / threads);
+  return n < most ? n : most;
+}
+constexpr int kAddNormBwdRegs = 64;
+
+template <int V>
+void add_norm_launch(const smla::AddNormParams& p, int form, int ctas, int threads, cudaStream_t cs) {
+  if (form == smla::kAddNormBf16) smla::add_norm_kernel<V, smla::kAddNormBf16><<<ctas, threads, 0, cs>>>(p);
+  else if (form == smla::kAddNormGroups) smla::add_norm_kernel<V, smla::kAddNormGroups><<<ctas, threads, 0, cs>>>(p);
+  else smla::add_norm_kernel<V, smla::kAddNormRow><<<ctas, threads, 0, cs>>>(p);
 }
 
 }  // namespace
@@ -75,12 +83,11 @@ sparse_mla_status_t mla_add_norm(const void* x, long long x_stride, const void* 
   p.z = static_cast<__nv_bfloat16*>(residual_out);
   p.out = out;
   p.scales = scales;
-  p.form = out_format;
   const int v = add_norm_vectors(d, false), threads = add_norm_threads(d, v);
-  const int ctas = add_norm_ctas(n, threads, sms);
+  const int ctas = add_norm_ctas(n, threads, sms, smla::kAddNormRegs);
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
-  if (v == 1) smla::add_norm_kernel<1><<<ctas, threads, 0, cs>>>(p);
-  else smla::add_norm_kernel<2><<<ctas, threads, 0, cs>>>(p);
+  if (v == 1) add_norm_launch<1>(p, out_format, ctas, threads, cs);
+  else add_norm_launch<2>(p, out_format, ctas, threads, cs);
   return cudaGetLastError() == cudaSuccess ? SPARSE_MLA_OK : SPARSE_MLA_ERR_CUDA;
 }
 
@@ -88,7 +95,7 @@ size_t mla_add_norm_bwd_workspace_size(int n, int d) {
   if (n < 1 || d < 8 || d % 8 != 0 || d > smla::kAddNormMaxWidth) return 0;
   int sms = 0;
   if (device_setup(&sms) != SPARSE_MLA_OK) return 0;
-  const int ctas = add_norm_ctas(n, add_norm_threads(d, add_norm_vectors(d, true)), sms);
+  const int ctas = add_norm_ctas(n, add_norm_threads(d, add_norm_vectors(d, true)), sms, kAddNormBwdRegs);
   return static_cast<size_t>(ctas) * static_cast<size_t>(d) * sizeof(float);   // one share of the sums per CTA
 }
 
@@ -118,7 +125,7 @@ sparse_mla_status_t mla_add_norm_bwd(const void* z, long long z_stride, const vo
   p.dx = static_cast<__nv_bfloat16*>(dx);
   p.part = static_cast<float*>(workspace);
   const int v = add_norm_vectors(d, true), threads = add_norm_threads(d, v);
-  const int ctas = add_norm_ctas(n, threads, sms);
+  const int ctas = add_norm_ctas(n, threads, sms, kAddNormBwdRegs);
   if (v == 1) smla::add_norm_bwd_kernel<1><<<ctas, threads, 0, cs>>>(p);
   else smla::add_norm_bwd_kernel<2><<<ctas, threads, 0, cs>>>(p);
   if (cudaGetLastError() != cudaSuccess) return SPARSE_MLA_ERR_CUDA;
