@@ -19,7 +19,10 @@
 //                        a ring of 16 KB units (K: 128 keys x 64 columns, V: 64 keys x
 //                        128 columns)
 //
-// With two tiles the tensor core works on one while the softmax works on the other.  O
+// With two tiles the tensor core works on one while the softmax works on the other.  Where
+// there are few tiles a CTA takes one, and a cluster of CTAs shares its keys out: each
+// leaves its O, maximum and sum in its shared memory, and every CTA of the cluster joins a
+// share of the rows from there.  O
 // is rescaled only when a row's maximum has grown by more than 2^8: until then the
 // weights are relative to the older maximum, which the sum and the LSE take into
 // account exactly.  P is rounded to bf16 for the product (2^-8 of each weight at most);
@@ -32,6 +35,7 @@
 #include <cuda_bf16.h>
 #include <cstdint>
 
+#include "fp4_decode_kernel.cuh"
 #include "fwd_kernel.cuh"
 #include "norm_rope_kernel.cuh"
 #include "ptx.cuh"
@@ -55,6 +59,7 @@ struct MhaFwdParams {
   int batch, total_q, total_kv, h_q, group; // query heads per key head
   int pack, tok_tile;                      // a tile is tok_tile tokens x pack heads
   int slots;                               // tiles (of NT) per head pack that the grid has room for
+  int cluster;                             // CTAs that share a tile's keys out (one tile a CTA; else 1)
   float scale_log2;
   const __nv_bfloat16* v;                  // row (t, h) at v + t v_tok + h v_head
   long long v_tok, v_head;
@@ -267,7 +272,9 @@ struct __align__(16) MhaMisc {
   int prior_error;
   int cleared;   // values of V that are not finite were taken out of a block that some rows do not see all of
   MhaWork work;
+  float2 part[kMhaTile];   // a row's maximum (in powers of two) and sum over this CTA's keys
 };
+constexpr int kMhaPartRow = kMhaDv + 4;   // floats of a row that is joined; neighbours in other banks
 
 // Shared memory: Q (NT tiles), then the ring.
 template <int DQK, int NT>
@@ -283,15 +290,17 @@ struct MhaFwdShape {
   static constexpr int kTmemCols = NT * 256;
   static_assert(kUnits >= kSub + 4, "a K block and two V blocks");
   static_assert(kBytes <= kMaxSmem, "shared memory");
+  static_assert(kUnits * kMhaUnit >= kMhaTile * kMhaPartRow * 4, "rows that are joined");
 };
 
 // What one CTA does: keys' blocks of each of its tiles.
 template <int NT>
 struct MhaSpan {
   int t0[NT];      // first token of the tile, in the sequence
-  int blocks[NT];  // blocks of 128 keys that its rows see
+  int blocks[NT];  // blocks of 128 keys that its rows see (of which this CTA takes them)
+  int from;        // the first of them
   int most;
-  __device__ __forceinline__ MhaSpan(const MhaFwdParams& p, const MhaWork& w) {
+  __device__ __forceinline__ MhaSpan(const MhaFwdParams& p, const MhaWork& w, int rank) {
     const int lq = w.q1 - w.q0, lk = w.k1 - w.k0;
     most = 0;
 #pragma unroll
@@ -301,6 +310,11 @@ struct MhaSpan {
       const int sees = t0[t] < lq ? last + lk - lq + 1 : 0;   // of its last row
       blocks[t] = sees > 0 ? (sees + kMhaTile - 1) / kMhaTile : 0;
       most = max(most, blocks[t]);
+    }
+    from = 0;
+    if (NT == 1 && p.cluster > 1) {
+      from = static_cast<int>(static_cast<long long>(most) * rank / p.cluster);
+      most = blocks[0] = static_cast<int>(static_cast<long long>(most) * (rank + 1) / p.cluster) - from;
     }
   }
 };
@@ -337,7 +351,7 @@ __device__ __forceinline__ bool mha_load(const MhaFwdParams& p, MhaMisc& m, uint
       if (!take()) return false;
       const uint32_t bar = smem_u32(&m.full[r.at]);
       mbar_arrive_expect_tx(bar, kMhaUnit);
-      tma_load_3d(sb + C::kQBytes + r.at * kMhaUnit, &p.map_k, 64 * c, kvh, w.k0 + j * kMhaTile, bar);
+      tma_load_3d(sb + C::kQBytes + r.at * kMhaUnit, &p.map_k, 64 * c, kvh, w.k0 + (s.from + j) * kMhaTile, bar);
       ++fills;
       r.next();
     }
@@ -358,8 +372,8 @@ __device__ __forceinline__ bool mha_load(const MhaFwdParams& p, MhaMisc& m, uint
       if (!take()) return false;
       const uint32_t bar = smem_u32(&m.full[r.at]), dst = sb + C::kQBytes + r.at * kMhaUnit;
       mbar_arrive_expect_tx(bar, kMhaUnit);
-      tma_load_3d(dst, &p.map_v, 0, kvh, w.k0 + j * kMhaTile + 64 * c, bar);
-      tma_load_3d(dst + kMhaUnit / 2, &p.map_v, 64, kvh, w.k0 + j * kMhaTile + 64 * c, bar);
+      tma_load_3d(dst, &p.map_v, 0, kvh, w.k0 + (s.from + j) * kMhaTile + 64 * c, bar);
+      tma_load_3d(dst + kMhaUnit / 2, &p.map_v, 64, kvh, w.k0 + (s.from + j) * kMhaTile + 64 * c, bar);
       ++fills;
       r.next();
     }
@@ -472,7 +486,7 @@ __device__ __forceinline__ bool mha_clear(uint32_t tile, uint32_t bytes) {
 
 // One thread per row of tile t.
 template <int DQK, int NT>
-__device__ __forceinline__ bool mha_softmax(const MhaFwdParams& p, MhaMisc& m, uint32_t sb, uint32_t tmem,
+__device__ __forceinline__ bool mha_softmax(const MhaFwdParams& p, MhaMisc& m, uint8_t* sbase, uint32_t sb, uint32_t tmem,
                                             const MhaWork& w, const MhaSpan<NT>& s, int pack0, int t) {
   using C = MhaFwdShape<DQK, NT>;
   const volatile int* ab = &m.abort_flag;
@@ -482,7 +496,7 @@ __device__ __forceinline__ bool mha_softmax(const MhaFwdParams& p, MhaMisc& m, u
   const int tok = s.t0[t] + row / p.pack;
   const bool live = row < p.pack * p.tok_tile && tok < lq;
   const int blocks = s.blocks[t];
-  const int whole = max(0, s.t0[t] + lk - lq + 1) / kMhaTile;   // blocks that every row sees all of
+  const int whole = max(0, s.t0[t] + lk - lq + 1) / kMhaTile - s.from;   // blocks that every row sees all of
   const uint32_t quarter = static_cast<uint32_t>((row >> 5) * 32) << 16;
   const uint32_t ts = tmem + quarter + t * kMhaTile, to = tmem + quarter + (NT + t) * kMhaTile;
   const float c = p.scale_log2;
@@ -500,7 +514,7 @@ __device__ __forceinline__ bool mha_softmax(const MhaFwdParams& p, MhaMisc& m, u
     float v[kMhaTile];
     tmem_load128(ts, v);
     if (j >= whole) {
-      const int sees = tok + lk - lq + 1 - j * kMhaTile;
+      const int sees = tok + lk - lq + 1 - (s.from + j) * kMhaTile;
 #pragma unroll
       for (int i = 0; i < kMhaTile; ++i) v[i] = i < sees ? v[i] : -INFINITY;
     }
@@ -560,23 +574,32 @@ __device__ __forceinline__ bool mha_softmax(const MhaFwdParams& p, MhaMisc& m, u
     if (!mbar_wait(smem_u32(&m.o_full[t]), 0, deadline, ab)) return false;
     tc_fence_after();
   }
-  const bool store_o = live && (!w.rest || (p.fill & 1)), store_l = live && (!w.rest || (p.fill & 2));
+  const bool join = NT == 1 && p.cluster > 1;
+  const bool store_o = live && (!w.rest || (p.fill & 1)), store_l = live && (!w.rest || (p.fill & 2)) && !join;
   if (store_l) p.lse[at] = sum == 0.f ? -INFINITY : (top * c + log2f(sum)) * 0.6931471805599453f;
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  // the products and loads are done: the ring's memory holds the rows that are joined
+  float* part = reinterpret_cast<float*>(sbase + C::kQBytes) + row * kMhaPartRow;
+  if (join) m.part[row] = make_float2(sum == 0.f ? -INFINITY : top * c, sum);
+  const float inv = sum == 0.f ? 0.f : (join ? 1.f : 1.f / sum);
 #pragma unroll
   for (int i = 0; i < kMhaDv / 32; ++i) {
     float x[32];
     if (blocks > 0) tmem_load32(to + 32 * i, x);
 #pragma unroll
     for (int k = 0; k < 32; ++k) x[k] = sum == 0.f ? 0.f : x[k] * inv;
-    if (store_o) {
+    if (join) {
+#pragma unroll
+      for (int k = 0; k < 32; k += 4)
+        *reinterpret_cast<float4*>(part + 32 * i + k) = make_float4(x[k], x[k + 1], x[k + 2], x[k + 3]);
+    } else if (store_o) {
 #pragma unroll
       for (int k = 0; k < 4; ++k) *reinterpret_cast<uint4*>(o + 32 * i + 8 * k) = pack8(x + 8 * k);
     }
   }
   if (blocks > 0 && store_o && *reinterpret_cast<volatile int*>(&m.cleared)) {
     // columns where a key that the row sees is not finite, among the blocks that were looked over
-    const int first = max(0, s.t0[0] + lk - lq + 1) / kMhaTile * kMhaTile, end = tok + lk - lq + 1;
+    const int first = max(max(0, s.t0[0] + lk - lq + 1) / kMhaTile, s.from) * kMhaTile;
+    const int end = min(tok + lk - lq + 1, (s.from + blocks) * kMhaTile);
     const __nv_bfloat16* values = p.v + w.k0 * p.v_tok + pack0 / p.group * p.v_head;
 #pragma unroll 1
     for (int d = 0; d < kMhaDv; ++d) {
@@ -586,10 +609,55 @@ __device__ __forceinline__ bool mha_softmax(const MhaFwdParams& p, MhaMisc& m, u
         const float y = __bfloat162float(values[key * p.v_tok + d]);
         if (!(fabsf(y) <= 3.402823466e38f)) acc += y;
       }
-      if (acc != 0.f) o[d] = __float2bfloat16_rn(acc);
+      if (acc != 0.f) {
+        if (join) part[d] = acc;
+        else o[d] = __float2bfloat16_rn(acc);
+      }
     }
   }
   return true;
+}
+
+// The parts that a cluster's CTAs have left of a tile, joined: a warp takes a row, four
+// columns a lane, parts in the order of their keys.
+template <int DQK>
+__device__ __forceinline__ void mha_join(const MhaFwdParams& p, MhaMisc& m, uint32_t sb, const MhaWork& w,
+                                         const MhaSpan<1>& s, int pack0, int rank) {
+  using C = MhaFwdShape<DQK, 1>;
+  const int lane = static_cast<int>(lane_id()), warp = static_cast<int>(threadIdx.x >> 5);
+  const int rows = min(p.tok_tile, w.q1 - w.q0 - s.t0[0]) * p.pack;
+  for (int row = rank * 4 + warp; row < rows; row += 4 * p.cluster) {
+    float2 mine = make_float2(-INFINITY, 0.f);
+    if (lane < p.cluster) {
+      const uint32_t at = cluster_addr(smem_u32(&m.part[row]), lane);
+      mine = make_float2(ld_cluster_f(at), ld_cluster_f(at + 4));
+    }
+    float top = mine.x;
+#pragma unroll
+    for (int i = 16; i > 0; i >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, i));
+    const float weight = mine.y == 0.f ? 0.f : fast_exp2(mine.x - top);   // a sum that is NaN passes it on
+    const float sum = warp_sum(weight * mine.y);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    const uint32_t at = sb + C::kQBytes + static_cast<uint32_t>(row * kMhaPartRow + 4 * lane) * 4u;
+#pragma unroll 4
+    for (int i = 0; i < p.cluster; ++i) {
+      const float f = __shfl_sync(0xffffffffu, weight, i);
+      const float4 x = ld_cluster_f4(cluster_addr(at, i));
+      if (f != 0.f) {
+        acc.x += f * x.x;
+        acc.y += f * x.y;
+        acc.z += f * x.z;
+        acc.w += f * x.w;
+      }
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const size_t out = static_cast<size_t>(w.q0 + s.t0[0] + row / p.pack) * p.h_q + pack0 + row % p.pack;
+    if (!w.rest || (p.fill & 1))
+      *reinterpret_cast<uint2*>(p.out + out * kMhaDv + 4 * lane) =
+          make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+    if (lane == 0 && (!w.rest || (p.fill & 2)))
+      p.lse[out] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+  }
 }
 
 template <int DQK, int NT>
@@ -601,8 +669,10 @@ __global__ void __launch_bounds__(MhaFwdShape<DQK, NT>::kThreads, 1) dense_mha_f
   MhaMisc& m = *reinterpret_cast<MhaMisc*>(sbase + C::kMiscOff);
   const int warp = static_cast<int>(threadIdx.x >> 5);
   const uint32_t sb = smem_u32(sbase);
-  const int slot = static_cast<int>(blockIdx.x % static_cast<unsigned>(p.slots));
-  const int pack0 = static_cast<int>(blockIdx.x / static_cast<unsigned>(p.slots)) * p.pack;
+  const unsigned unit = NT == 1 ? blockIdx.x / static_cast<unsigned>(p.cluster) : blockIdx.x;
+  const int rank = NT == 1 ? static_cast<int>(blockIdx.x % static_cast<unsigned>(p.cluster)) : 0;
+  const int slot = static_cast<int>(unit % static_cast<unsigned>(p.slots));
+  const int pack0 = static_cast<int>(unit / static_cast<unsigned>(p.slots)) * p.pack;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kUnits; ++i) {
@@ -639,9 +709,9 @@ __global__ void __launch_bounds__(MhaFwdShape<DQK, NT>::kThreads, 1) dense_mha_f
   const MhaWork w = m.work;
 
   if (m.prior_error == 0 && w.q1 > w.q0) {
-    const MhaSpan<NT> s(p, w);
+    const MhaSpan<NT> s(p, w, rank);
     if (warp < 4 * NT) {
-      if (!mha_softmax<DQK, NT>(p, m, sb, tmem, w, s, pack0, warp >> 2)) mha_raise(m, kErrMhaSoftmaxWait);
+      if (!mha_softmax<DQK, NT>(p, m, sbase, sb, tmem, w, s, pack0, warp >> 2)) mha_raise(m, kErrMhaSoftmaxWait);
     } else {
       if (s.most > 0 && lane_id() == 0) {
         const int never = 0;
@@ -668,6 +738,14 @@ __global__ void __launch_bounds__(MhaFwdShape<DQK, NT>::kThreads, 1) dense_mha_f
   __syncthreads();
   tc_fence_after();
   if (warp == 4 * NT) tmem_dealloc(tmem, C::kTmemCols);
+  if constexpr (NT == 1) {
+    if (p.cluster > 1) {
+      cluster_sync();   // every CTA's part is there
+      if (warp < 4 && m.prior_error == 0 && m.abort_flag == 0 && w.q1 > w.q0)
+        mha_join<DQK>(p, m, sb, w, MhaSpan<1>(p, w, rank), pack0, rank);
+      cluster_sync();   // no CTA leaves while another reads its part
+    }
+  }
 }
 
 }  // namespace smla

@@ -3,6 +3,7 @@
 // both.  It comes behind latent_api.cuh in the library's one translation unit
 // (library.cu) and uses that file's launches and sparse_mla_api.cu's checks and set-up.
 #pragma once
+#include <algorithm>
 #include <cmath>
 
 #include "add_norm_kernel.cuh"
@@ -206,44 +207,115 @@ sparse_mla_status_t mha_map(CUtensorMap* map, const MhaRows& r, int total, int h
   return e == CUDA_SUCCESS ? SPARSE_MLA_OK : SPARSE_MLA_ERR_INVALID_ARG;
 }
 
-template <int DQK, int NT>
-void mha_fwd_launch(const smla::MhaFwdParams& p, unsigned ctas, cudaStream_t cs) {
-  using C = smla::MhaFwdShape<DQK, NT>;
-  smla::dense_mha_fwd_kernel<DQK, NT><<<ctas, C::kThreads, C::kBytes, cs>>>(p);
-}
+constexpr int kMhaClusterSizes = 4;   // 16, 8, 4 and 2 CTAs
+constexpr int kMhaMaxCluster = 16;
 
 struct MhaState {
   bool set = false;
+  int clusters[2][kMhaClusterSizes] = {};   // at 192 and 128 columns: clusters of one-tile CTAs held at once
 };
 MhaState g_mha[kMaxDevices];   // under g_mu
 
 template <int DQK>
-bool mha_setup_bwd() {
-  return cudaFuncSetAttribute(smla::dense_mha_dq_kernel<DQK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              smla::MhaDqShape<DQK>::kBytes) == cudaSuccess &&
-         cudaFuncSetAttribute(smla::dense_mha_dkv_kernel<DQK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              smla::MhaDkvShape<DQK>::kBytes) == cudaSuccess;
+void mha_cluster_config(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attr, unsigned ctas, int cluster) {
+  using C = smla::MhaFwdShape<DQK, 1>;
+  cfg->gridDim = dim3(ctas);
+  cfg->blockDim = dim3(C::kThreads);
+  cfg->dynamicSmemBytes = C::kBytes;
+  attr->id = cudaLaunchAttributeClusterDimension;
+  attr->val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr->val.clusterDim.y = attr->val.clusterDim.z = 1;
+  cfg->attrs = attr;
+  cfg->numAttrs = 1;
 }
 
-template <int DQK, int NT>
-bool mha_setup_fwd() {
-  return cudaFuncSetAttribute(smla::dense_mha_fwd_kernel<DQK, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              smla::MhaFwdShape<DQK, NT>::kBytes) == cudaSuccess;
+// Kernel attributes, and how many clusters of each size the device holds at once (none
+// of a size that it refuses).
+template <int DQK>
+bool mha_setup(int* clusters) {
+  auto memory = [](const void* kernel, int bytes) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess;
+  };
+  const void* one = reinterpret_cast<const void*>(smla::dense_mha_fwd_kernel<DQK, 1>);
+  const bool ok = memory(one, smla::MhaFwdShape<DQK, 1>::kBytes) &&
+                  memory(reinterpret_cast<const void*>(smla::dense_mha_fwd_kernel<DQK, 2>), smla::MhaFwdShape<DQK, 2>::kBytes) &&
+                  memory(reinterpret_cast<const void*>(smla::dense_mha_dq_kernel<DQK>), smla::MhaDqShape<DQK>::kBytes) &&
+                  memory(reinterpret_cast<const void*>(smla::dense_mha_dkv_kernel<DQK>), smla::MhaDkvShape<DQK>::kBytes);
+  bool refused = false;
+  if (ok) {
+    refused = cudaFuncSetAttribute(one, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess;
+    for (int i = 0; i < kMhaClusterSizes; ++i) {
+      const int c = kMhaMaxCluster >> i;
+      cudaLaunchConfig_t cfg = {};
+      cudaLaunchAttribute attr = {};
+      mha_cluster_config<DQK>(&cfg, &attr, static_cast<unsigned>(c), c);
+      if (cudaOccupancyMaxActiveClusters(&clusters[i], smla::dense_mha_fwd_kernel<DQK, 1>, &cfg) != cudaSuccess) {
+        clusters[i] = 0;
+        refused = true;
+      }
+    }
+  }
+  if (!ok || refused) cudaGetLastError();   // not the next launch's error
+  return ok;
 }
 
 // The dense attention's kernels, apart from device_setup (which comes first): what a
 // device refuses of them stops no other call.
-sparse_mla_status_t mha_device_setup() {
+sparse_mla_status_t mha_device_setup(const MhaState** state) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return SPARSE_MLA_ERR_CUDA;
   std::lock_guard<std::mutex> lock(g_mu);
   MhaState& st = g_mha[dev];
-  if (!st.set) {
-    st.set = mha_setup_fwd<192, 2>() && mha_setup_fwd<192, 1>() && mha_setup_fwd<128, 2>() && mha_setup_fwd<128, 1>() &&
-             mha_setup_bwd<192>() && mha_setup_bwd<128>();
-    if (!st.set) cudaGetLastError();   // not the next launch's error
-  }
+  if (!st.set) st.set = mha_setup<192>(st.clusters[0]) && mha_setup<128>(st.clusters[1]);
+  *state = &st;
   return st.set ? SPARSE_MLA_OK : SPARSE_MLA_ERR_CUDA;
+}
+
+// How the forward's work is laid out: tiles per CTA and CTAs that share a tile's keys.
+struct MhaPlan {
+  int tiles, cluster;
+  long long slots;
+};
+
+// The layout whose slowest CTA has the least to do, by the sequences' mean lengths: key
+// blocks one after the other, of a longest tile and of the card's mean.  A CTA of two
+// tiles takes about as long for a block of both as one of a single tile for its own.
+MhaPlan mha_plan(int total_q, int total_kv, int batch, bool packed, bool rest, int packs, int tok_tile, int sms,
+                 const int* clusters) {
+  const double lq = static_cast<double>(total_q) / batch, lk = static_cast<double>(total_kv) / batch;
+  const double longest = std::ceil(lk / smla::kMhaTile), mean = (lk - std::min(lq, lk) / 2) / smla::kMhaTile + 0.5;
+  auto units = [&](int tiles) { return std::ceil(lq / (tok_tile * tiles)) * batch * packs; };
+  MhaPlan best = {2, 1, 0};
+  double least = std::max(longest, units(2) * mean / sms);
+  for (int c = 1; c <= kMhaMaxCluster; c *= 2) {
+    if (c > 1) {
+      int held = 0;
+      for (int i = 0; i < kMhaClusterSizes; ++i)
+        if (kMhaMaxCluster >> i == c) held = clusters[i];
+      if (units(1) > held || longest < 2 * c) continue;
+    }
+    const double t = std::max(std::ceil(longest / c), units(1) * mean / sms) + (c > 1 ? 1.0 : 0.0);
+    if (t < least) {
+      least = t;
+      best = {1, c, 0};
+    }
+  }
+  best.slots = mha_slots(total_q, tok_tile * best.tiles, packed ? batch : 0, rest);
+  return best;
+}
+
+template <int DQK>
+cudaError_t mha_fwd_launch(const smla::MhaFwdParams& p, const MhaPlan& plan, unsigned ctas, cudaStream_t cs) {
+  if (plan.tiles == 2) {
+    using C = smla::MhaFwdShape<DQK, 2>;
+    smla::dense_mha_fwd_kernel<DQK, 2><<<ctas, C::kThreads, C::kBytes, cs>>>(p);
+    return cudaGetLastError();
+  }
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr = {};
+  mha_cluster_config<DQK>(&cfg, &attr, ctas, plan.cluster);
+  cfg.stream = cs;
+  return cudaLaunchKernelEx(&cfg, smla::dense_mha_fwd_kernel<DQK, 1>, p);
 }
 
 // dq (and D into the workspace), then dk and dv.
@@ -336,7 +408,8 @@ sparse_mla_status_t dense_mha_fwd(const void* q, long long q_tok_stride, long lo
   int sms = 0;
   if ((st = device_setup(&sms)) != SPARSE_MLA_OK) return st;
   if (total_q == 0) return SPARSE_MLA_OK;
-  if ((st = mha_device_setup()) != SPARSE_MLA_OK) return st;
+  const MhaState* state = nullptr;
+  if ((st = mha_device_setup(&state)) != SPARSE_MLA_OK) return st;
   smla::MhaFwdParams p;
   std::memset(&p, 0, sizeof(p));
   const int group = h_q / h_kv;
@@ -366,16 +439,16 @@ sparse_mla_status_t dense_mha_fwd(const void* q, long long q_tok_stride, long lo
   p.fill = cu_seqlens_q ? fill : 0;
   const unsigned long long t = g_timeout_ns.load();
   p.timeout_ns = t ? t : kDefaultTimeoutNs;
-  // two tiles a CTA where a sequence's rows fill more than one
-  const bool two = static_cast<long long>(total_q) * p.pack > static_cast<long long>(smla::kMhaTile) * p.batch;
-  const long long slots = mha_slots(total_q, p.tok_tile * (two ? 2 : 1), cu_seqlens_q ? batch : 0, p.fill != 0);
-  if (slots * (h_q / p.pack) > INT_MAX) return SPARSE_MLA_ERR_INVALID_ARG;
-  p.slots = static_cast<int>(slots);
-  const unsigned ctas = static_cast<unsigned>(slots * (h_q / p.pack));
+  const MhaPlan plan = mha_plan(total_q, total_kv, p.batch, cu_seqlens_q != nullptr, p.fill != 0, h_q / p.pack, p.tok_tile,
+                                sms, state->clusters[d_qk == 192 ? 0 : 1]);
+  p.cluster = plan.cluster;
+  const long long ctas = plan.slots * (h_q / p.pack) * plan.cluster;
+  if (ctas > INT_MAX) return SPARSE_MLA_ERR_INVALID_ARG;
+  p.slots = static_cast<int>(plan.slots);
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
-  if (d_qk == 192) two ? mha_fwd_launch<192, 2>(p, ctas, cs) : mha_fwd_launch<192, 1>(p, ctas, cs);
-  else two ? mha_fwd_launch<128, 2>(p, ctas, cs) : mha_fwd_launch<128, 1>(p, ctas, cs);
-  return cudaGetLastError() == cudaSuccess ? SPARSE_MLA_OK : SPARSE_MLA_ERR_CUDA;
+  const cudaError_t e = d_qk == 192 ? mha_fwd_launch<192>(p, plan, static_cast<unsigned>(ctas), cs)
+                                    : mha_fwd_launch<128>(p, plan, static_cast<unsigned>(ctas), cs);
+  return e == cudaSuccess ? SPARSE_MLA_OK : SPARSE_MLA_ERR_CUDA;
 }
 
 size_t dense_mha_bwd_workspace_size(int total_q, int total_kv, int batch, int h_q, int h_kv, int d_qk, int d_v) {
@@ -407,7 +480,8 @@ sparse_mla_status_t dense_mha_bwd(const void* q, long long q_tok_stride, long lo
   if (need > 0 && (!workspace || workspace_bytes < need)) return SPARSE_MLA_ERR_WORKSPACE_TOO_SMALL;
   if (!aligned(workspace, 16)) return SPARSE_MLA_ERR_INVALID_ARG;
   if (total_q == 0 && total_kv == 0) return SPARSE_MLA_OK;
-  if ((st = mha_device_setup()) != SPARSE_MLA_OK) return st;
+  const MhaState* state = nullptr;
+  if ((st = mha_device_setup(&state)) != SPARSE_MLA_OK) return st;
   return d_qk == 192 ? mha_bwd_launch<192>(rq, rk, rv, rg, cu_seqlens_q, cu_seqlens_kv, batch, sm_scale, out, lse, dq, dk,
                                            dv, total_q, total_kv, h_q, h_kv, workspace, static_cast<cudaStream_t>(stream))
                      : mha_bwd_launch<128>(rq, rk, rv, rg, cu_seqlens_q, cu_seqlens_kv, batch, sm_scale, out, lse, dq, dk,

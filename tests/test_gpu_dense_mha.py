@@ -347,3 +347,25 @@ def test_a_layer(smla):
     assert (y.double() - nrm(zz2, t[3])).norm() < 0.04 * y.double().norm()
     for got, want in ((dx, t[0].grad), (dx, t[1].grad), (dw1, t[2].grad), (dw2, t[3].grad)):
         assert (got.double() - want).norm() < 0.08 * want.norm()
+
+
+@pytest.mark.parametrize("d", [192, 128])
+@pytest.mark.parametrize("lq,lk,h,hk", [([1], [5000], 8, 8), ([3], [4097], 2, 2), ([130], [4500], 2, 1), ([1], [9000], 1, 1),
+                                        ([1, 2, 1, 1], [3000, 1, 130, 4000], 8, 2), ([257], [2200], 1, 1)])
+def test_few_rows_of_long_sequences(smla, lq, lk, h, hk, d):
+    """A tile's keys shared out over the CTAs of a cluster, down to CTAs with none."""
+    _run(smla, sum(lk), lq, lk, h, hk, d, tail=2)
+
+
+@pytest.mark.parametrize("what", [NAN, INF])
+def test_few_rows_and_values_that_are_not_finite(smla, what):
+    q, k, v, _, cq, ck = _inputs(15, [100], [3100], 2, 2, 128)
+    want = smla.dense_mha_fwd(q, k, v, 0.1, cq, ck)
+    v[3060, :, 7] = what      # seen by the rows from 60 on
+    v[5, 1, 9] = what         # by all
+    out, lse = smla.dense_mha_fwd(q, k, v, 0.1, cq, ck)
+    assert torch.equal(lse, want[1])
+    bad = torch.zeros_like(out, dtype=torch.bool)
+    bad[60:, :, 7] = True
+    bad[:, 1, 9] = True
+    assert not out[bad].isfinite().any() and torch.equal(out[~bad], want[0][~bad])
