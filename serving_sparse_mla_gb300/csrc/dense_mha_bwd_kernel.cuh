@@ -153,17 +153,19 @@ __device__ __forceinline__ bool mha_dq_mma(const MhaBwdParams& p, MhaDqMisc& m, 
   using C = MhaDqShape<DQK>;
   constexpr uint32_t kIdescS = idesc_bf16_f32(kMhaTile, kMhaTile, false, false);
   constexpr uint32_t kIdescQ = idesc_bf16_f32(kMhaTile, DQK, false, true);
+  const uint64_t q_desc = smem_desc(sb, 16, 1024, SWZ_128B), k_desc = smem_desc(sb + C::kKOff, 16, 1024, SWZ_128B),
+                 kt_desc = smem_desc(sb + C::kKOff, kMhaUnit, 1024, SWZ_128B),   // its rows as columns
+                 v_desc = smem_desc(sb + C::kVOff, 16, 1024, SWZ_128B);
   const volatile int* ab = &m.abort_flag;
   const uint64_t deadline = global_timer_ns() + p.timeout_ns;
   auto scores = [&](int j) -> bool {
     const int st = j % C::kKStages;
     if (!mbar_wait(smem_u32(&m.k_full[st]), j / C::kKStages & 1, deadline, ab)) return false;
-    const uint32_t k = sb + C::kKOff + st * C::kKBytes;
+    const uint64_t k = desc_plus(k_desc, st * C::kKBytes);
 #pragma unroll
     for (int kk = 0; kk < DQK / 16; ++kk) {
       const uint32_t off = (kk >> 2) * kMhaUnit + (kk & 3) * 32;
-      mma_bf16_ss(tmem + C::kS, smem_desc(sb + off, 16, 1024, SWZ_128B), smem_desc(k + off, 16, 1024, SWZ_128B), kIdescS,
-                  kk > 0 ? 1u : 0u);
+      mma_bf16_ss(tmem + C::kS, desc_plus(q_desc, off), desc_plus(k, off), kIdescS, kk > 0 ? 1u : 0u);
     }
     mma_commit(smem_u32(&m.s_full));
     return true;
@@ -171,11 +173,11 @@ __device__ __forceinline__ bool mha_dq_mma(const MhaBwdParams& p, MhaDqMisc& m, 
   auto values = [&](int j) -> bool {
     const int st = j % C::kVStages;
     if (!mbar_wait(smem_u32(&m.v_full[st]), j / C::kVStages & 1, deadline, ab)) return false;
-    const uint32_t v = sb + C::kVOff + st * C::kVBytes;
+    const uint64_t v = desc_plus(v_desc, st * C::kVBytes);
 #pragma unroll
     for (int kk = 0; kk < kMhaDv / 16; ++kk)
-      mma_bf16_ts(tmem + C::kT, tmem + C::kDo + 8 * kk,
-                  smem_desc(v + (kk >> 2) * kMhaUnit + (kk & 3) * 32, 16, 1024, SWZ_128B), kIdescS, kk > 0 ? 1u : 0u);
+      mma_bf16_ts(tmem + C::kT, tmem + C::kDo + 8 * kk, desc_plus(v, (kk >> 2) * kMhaUnit + (kk & 3) * 32), kIdescS,
+                  kk > 0 ? 1u : 0u);
     mma_commit(smem_u32(&m.v_empty[st]));
     mma_commit(smem_u32(&m.t_full));
     return true;
@@ -194,11 +196,11 @@ __device__ __forceinline__ bool mha_dq_mma(const MhaBwdParams& p, MhaDqMisc& m, 
     if (!mbar_wait(smem_u32(&m.ds_full), j & 1, deadline, ab)) return false;
     tc_fence_after();
     const int st = j % C::kKStages;
-    const uint32_t k = sb + C::kKOff + st * C::kKBytes;
+    const uint64_t k = desc_plus(kt_desc, st * C::kKBytes);
 #pragma unroll
     for (int kk = 0; kk < kMhaTile / 16; ++kk)   // either half's dS is in its own columns
-      mma_bf16_ts(tmem + C::kDq, tmem + C::kT + 64 * (kk >> 2) + 8 * (kk & 3),
-                  smem_desc(k + kk * 2048, kMhaUnit, 1024, SWZ_128B), kIdescQ, j + kk > 0 ? 1u : 0u);
+      mma_bf16_ts(tmem + C::kDq, tmem + C::kT + 64 * (kk >> 2) + 8 * (kk & 3), desc_plus(k, kk * 2048), kIdescQ,
+                  j + kk > 0 ? 1u : 0u);
     mma_commit(smem_u32(&m.k_empty[st]));
     if (j + 1 < blocks && !values(j + 1)) return false;
     if (j + 2 < blocks) {
@@ -474,31 +476,34 @@ __device__ __forceinline__ bool mha_dkv_mma(const MhaBwdParams& p, MhaDkvMisc& m
   constexpr uint32_t kIdescS = idesc_bf16_f32(kMhaTile, C::kN, false, false);
   constexpr uint32_t kIdescV = idesc_bf16_f32(kMhaTile, kMhaDv, false, true);
   constexpr uint32_t kIdescK = idesc_bf16_f32(kMhaTile, DQK, false, true);
+  const uint64_t k_desc = smem_desc(sb, 16, 1024, SWZ_128B), v_desc = smem_desc(sb + C::kVOff, 16, 1024, SWZ_128B),
+                 q_desc = smem_desc(sb + C::kQOff, 16, 1024, SWZ_128B), g_desc = smem_desc(sb + C::kDoOff, 16, 1024, SWZ_128B),
+                 qt_desc = smem_desc(sb + C::kQOff, C::kQUnit, 1024, SWZ_128B),    // their rows as columns
+                 gt_desc = smem_desc(sb + C::kDoOff, C::kQUnit, 1024, SWZ_128B);
   const volatile int* ab = &m.abort_flag;
   const uint64_t deadline = global_timer_ns() + p.timeout_ns;
   auto scores = [&](int j) -> bool {
     const int st = j % C::kStages;
     if (!mbar_wait(smem_u32(&m.q_full[st]), j / C::kStages & 1, deadline, ab)) return false;
-    const uint32_t q = sb + C::kQOff + st * C::kQBytes;
+    const uint64_t q = desc_plus(q_desc, st * C::kQBytes);
 #pragma unroll
     for (int kk = 0; kk < DQK / 16; ++kk)
-      mma_bf16_ss(tmem + C::kS, smem_desc(sb + (kk >> 2) * kMhaUnit + (kk & 3) * 32, 16, 1024, SWZ_128B),
-                  smem_desc(q + (kk >> 2) * C::kQUnit + (kk & 3) * 32, 16, 1024, SWZ_128B), kIdescS, kk > 0 ? 1u : 0u);
+      mma_bf16_ss(tmem + C::kS, desc_plus(k_desc, (kk >> 2) * kMhaUnit + (kk & 3) * 32),
+                  desc_plus(q, (kk >> 2) * C::kQUnit + (kk & 3) * 32), kIdescS, kk > 0 ? 1u : 0u);
     mma_commit(smem_u32(&m.s_full));
     return true;
   };
   auto values = [&](int j) -> bool {
     const int st = j % C::kStages;
     if (!mbar_wait(smem_u32(&m.do_full[st]), j / C::kStages & 1, deadline, ab)) return false;
-    const uint32_t g = sb + C::kDoOff + st * C::kDoBytes;
+    const uint64_t g = desc_plus(g_desc, st * C::kDoBytes);
 #pragma unroll
     for (int kk = 0; kk < kMhaDv / 16; ++kk) {
-      const uint64_t b = smem_desc(g + (kk >> 2) * C::kQUnit + (kk & 3) * 32, 16, 1024, SWZ_128B);
+      const uint64_t b = desc_plus(g, (kk >> 2) * C::kQUnit + (kk & 3) * 32);
       if (C::kVTmem)
         mma_bf16_ts(tmem + C::kT, tmem + C::kV + 8 * kk, b, kIdescS, kk > 0 ? 1u : 0u);
       else
-        mma_bf16_ss(tmem + C::kT, smem_desc(sb + C::kVOff + (kk >> 2) * kMhaUnit + (kk & 3) * 32, 16, 1024, SWZ_128B), b,
-                    kIdescS, kk > 0 ? 1u : 0u);
+        mma_bf16_ss(tmem + C::kT, desc_plus(v_desc, (kk >> 2) * kMhaUnit + (kk & 3) * 32), b, kIdescS, kk > 0 ? 1u : 0u);
     }
     mma_commit(smem_u32(&m.t_full));
     return true;
@@ -519,10 +524,10 @@ __device__ __forceinline__ bool mha_dkv_mma(const MhaBwdParams& p, MhaDkvMisc& m
     const int st = j % C::kStages;
     if (!mbar_wait(smem_u32(&m.p_full), j & 1, deadline, ab)) return false;
     tc_fence_after();
-    const uint32_t g = sb + C::kDoOff + st * C::kDoBytes, q = sb + C::kQOff + st * C::kQBytes;
+    const uint64_t g = desc_plus(gt_desc, st * C::kDoBytes), q = desc_plus(qt_desc, st * C::kQBytes);
 #pragma unroll
     for (int kk = 0; kk < C::kN / 16; ++kk)
-      mma_bf16_ts(tmem + C::kDv, tmem + C::kS + step_at(kk), smem_desc(g + kk * 2048, C::kQUnit, 1024, SWZ_128B), kIdescV,
+      mma_bf16_ts(tmem + C::kDv, tmem + C::kS + step_at(kk), desc_plus(g, kk * 2048), kIdescV,
                   j + kk > 0 ? 1u : 0u);
     mma_commit(smem_u32(&m.do_empty[st]));
     if (j + 1 < total && !scores(j + 1)) return false;
@@ -530,7 +535,7 @@ __device__ __forceinline__ bool mha_dkv_mma(const MhaBwdParams& p, MhaDkvMisc& m
     tc_fence_after();
 #pragma unroll
     for (int kk = 0; kk < C::kN / 16; ++kk)
-      mma_bf16_ts(tmem + C::kDk, tmem + C::kT + step_at(kk), smem_desc(q + kk * 2048, C::kQUnit, 1024, SWZ_128B), kIdescK,
+      mma_bf16_ts(tmem + C::kDk, tmem + C::kT + step_at(kk), desc_plus(q, kk * 2048), kIdescK,
                   j + kk > 0 ? 1u : 0u);
     mma_commit(smem_u32(&m.q_empty[st]));
     if (j + 1 < total && !values(j + 1)) return false;

@@ -167,6 +167,17 @@ __device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, ui
       : "memory");
 }
 
+// The descriptor of an operand `bytes` further on in shared memory (below 256 KB, so the
+// address' field does not overflow): one addition, where forming it anew takes several
+// and a block's products are issued by one thread.
+__device__ __forceinline__ uint64_t desc_plus(uint64_t desc, uint32_t bytes) {
+  uint32_t lo, hi;
+  asm("mov.b64 {%0, %1}, %2;" : "=r"(lo), "=r"(hi) : "l"(desc));
+  lo += bytes >> 4;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(desc) : "r"(lo), "r"(hi));
+  return desc;
+}
+
 // This thread's TMEM lane, columns taddr .. taddr + N - 1, and the wait for them in one
 // statement: nothing can be done with the registers before they hold the values.
 __device__ __forceinline__ void tmem_load32(uint32_t taddr, float* v) {
@@ -266,7 +277,7 @@ __device__ __forceinline__ void add2(float& a0, float& a1, float b0, float b1) {
 constexpr int kMhaMaxUnits = 12;
 
 struct __align__(16) MhaMisc {
-  uint64_t q_full[2], full[kMhaMaxUnits], empty[kMhaMaxUnits], s_full[2], p_full[2], o_full[2], drain;
+  uint64_t q_full[2], full[kMhaMaxUnits], empty[kMhaMaxUnits], s_full[2], p_full[2], o_full[2], o_step, drain;
   uint32_t tmem_base;
   int abort_flag;
   int prior_error;
@@ -286,8 +297,10 @@ struct MhaFwdShape {
                                                                                    : kMhaMaxUnits;
   static constexpr uint32_t kMiscOff = kQBytes + kUnits * kMhaUnit;
   static constexpr int kBytes = static_cast<int>(kMiscOff) + static_cast<int>(sizeof(MhaMisc)) + 1024;
+  static constexpr int kAhead = NT == 1 ? 2 : 1;               // key blocks whose scores are ahead of the weights
   static constexpr int kThreads = NT * 128 + 64;               // two tiles: 200 registers each, no more than their rows take
-  static constexpr int kTmemCols = NT * 256;
+  static constexpr int kTmemCols = 512;
+  static constexpr uint32_t kO = 256;                          // columns of TMEM: two S of 128 each, then O
   static_assert(kUnits >= kSub + 4, "a K block and two V blocks");
   static_assert(kBytes <= kMaxSmem, "shared memory");
   static_assert(kUnits * kMhaUnit >= kMhaTile * kMhaPartRow * 4, "rows that are joined");
@@ -328,9 +341,11 @@ __device__ __forceinline__ void mha_raise(MhaMisc& m, int code) {
 template <int UNITS>
 struct MhaRing {
   uint32_t at = 0, turn = 0;
-  __device__ __forceinline__ void next() {
-    if (++at == UNITS) {
-      at = 0;
+  __device__ __forceinline__ void next() { skip(1); }
+  __device__ __forceinline__ void skip(uint32_t n) {
+    at += n;
+    if (at >= UNITS) {
+      at -= UNITS;
       turn ^= 1u;
     }
   }
@@ -367,6 +382,7 @@ __device__ __forceinline__ bool mha_load(const MhaFwdParams& p, MhaMisc& m, uint
   if (s.blocks[0] > 0) load_q(0);
   if (!load_k(0)) return false;
   if (NT > 1 && s.blocks[NT - 1] > 0) load_q(NT - 1);
+  if (C::kAhead > 1 && s.most > 1 && !load_k(1)) return false;
   for (int j = 0; j < s.most; ++j) {
     for (int c = 0; c < 2; ++c) {
       if (!take()) return false;
@@ -377,7 +393,7 @@ __device__ __forceinline__ bool mha_load(const MhaFwdParams& p, MhaMisc& m, uint
       ++fills;
       r.next();
     }
-    if (j + 1 < s.most && !load_k(j + 1)) return false;
+    if (j + C::kAhead < s.most && !load_k(j + C::kAhead)) return false;
   }
   return true;
 }
@@ -390,66 +406,88 @@ __device__ __forceinline__ bool mha_mma(const MhaFwdParams& p, MhaMisc& m, uint3
   constexpr uint32_t kIdescO = idesc_bf16_f32(kMhaTile, kMhaDv, false, true);
   const volatile int* ab = &m.abort_flag;
   const uint64_t deadline = global_timer_ns() + p.timeout_ns;
-  MhaRing<C::kUnits> rk, rv;   // where the K block in use, and the V block, start
-  auto wait_unit = [&](const MhaRing<C::kUnits>& r) -> bool {
-    return mbar_wait(smem_u32(&m.full[r.at]), r.turn, deadline, ab);
+  const uint64_t q_desc = smem_desc(sb, 16, 1024, SWZ_128B), k_desc = smem_desc(sb + C::kQBytes, 16, 1024, SWZ_128B),
+                 v_desc = smem_desc(sb + C::kQBytes, kMhaUnit / 2, 1024, SWZ_128B);
+  MhaRing<C::kUnits> r;   // the units in the order of their use
+  auto wait_unit = [&](const MhaRing<C::kUnits>& u) -> bool {
+    return mbar_wait(smem_u32(&m.full[u.at]), u.turn, deadline, ab);
   };
-  // S_t = Q_t K^T of the block at `r`; `first`: its units have not been waited for, `last`: they are free behind it
-  auto scores = [&](int t, MhaRing<C::kUnits> r, bool first, bool last) -> bool {
+  // S (columns `to`, barrier `bar`) = Q_t K^T of the block at `u`; `first`: its units have not been waited for, `last`:
+  // they are free behind it
+  auto scores = [&](int t, uint32_t to, uint64_t* bar, MhaRing<C::kUnits> u, bool first, bool last) -> bool {
 #pragma unroll
     for (int c = 0; c < C::kSub; ++c) {
-      if (first && !wait_unit(r)) return false;
-      const uint32_t a = sb + (t * C::kSub + c) * kMhaUnit, b = sb + C::kQBytes + r.at * kMhaUnit;
+      if (first && !wait_unit(u)) return false;
+      const uint64_t a = desc_plus(q_desc, (t * C::kSub + c) * kMhaUnit), b = desc_plus(k_desc, u.at * kMhaUnit);
 #pragma unroll
       for (int kk = 0; kk < 4; ++kk)
-        mma_bf16_ss(tmem + t * kMhaTile, smem_desc(a + kk * 32, 16, 1024, SWZ_128B),
-                    smem_desc(b + kk * 32, 16, 1024, SWZ_128B), kIdescS, c + kk > 0 ? 1u : 0u);
-      if (last) mma_commit(smem_u32(&m.empty[r.at]));
-      r.next();
+        mma_bf16_ss(tmem + to, desc_plus(a, kk * 32), desc_plus(b, kk * 32), kIdescS, c + kk > 0 ? 1u : 0u);
+      if (last) mma_commit(smem_u32(&m.empty[u.at]));
+      u.next();
     }
-    mma_commit(smem_u32(&m.s_full[t]));
+    mma_commit(smem_u32(bar));
     return true;
   };
+  // O_t += P (columns `from`) V of block j at `u`
+  auto weighted = [&](int t, uint32_t from, int j, MhaRing<C::kUnits> u, bool first, bool last) -> bool {
 #pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    if (s.blocks[t] == 0) continue;
-    if (!mbar_wait(smem_u32(&m.q_full[t]), 0, deadline, ab)) return false;
-    const bool alone = NT == 1 || s.blocks[1 - t] == 0;
-    if (!scores(t, rk, t == 0 || alone, t == NT - 1 || alone)) return false;
-  }
-  for (int c = 0; c < C::kSub; ++c) rk.next();
-  for (int j = 0; j < s.most; ++j) {
-    rv = rk;                                   // block j's V, then block j + 1's K
-    rk.next();
-    rk.next();
+    for (int c = 0; c < 2; ++c) {
+      if (first && !wait_unit(u)) return false;
+      const uint64_t b = desc_plus(v_desc, u.at * kMhaUnit);
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      if (j >= s.blocks[t]) continue;
-      const bool alone = NT == 1 || j >= s.blocks[1 - t];
-      const bool first = t == 0 || alone, last = t == NT - 1 || alone;
-      if (!mbar_wait(smem_u32(&m.p_full[t]), static_cast<uint32_t>(j) & 1u, deadline, ab)) return false;
+      for (int kk = 0; kk < 4; ++kk)
+        mma_bf16_ts(tmem + C::kO + t * kMhaDv, tmem + from + 8 * (4 * c + kk), desc_plus(b, kk * 2048), kIdescO,
+                    j + c + kk > 0 ? 1u : 0u);
+      if (last) mma_commit(smem_u32(&m.empty[u.at]));
+      u.next();
+    }
+    return true;
+  };
+  if constexpr (NT == 1) {
+    // two S in turn: block j + 2's scores follow block j's weights, so that a block's are there when the softmax has done
+    // the one before
+    if (!mbar_wait(smem_u32(&m.q_full[0]), 0, deadline, ab)) return false;
+    for (int j = 0; j < 2 && j < s.most; ++j) {
+      if (!scores(0, kMhaTile * j, &m.s_full[j], r, true, true)) return false;
+      r.skip(C::kSub);
+    }
+    for (int j = 0; j < s.most; ++j) {
+      const int buf = j & 1;
+      if (!mbar_wait(smem_u32(&m.p_full[buf]), j >> 1 & 1, deadline, ab)) return false;
       tc_fence_after();
-      MhaRing<C::kUnits> r = rv;
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        if (first && !wait_unit(r)) return false;
-        const uint32_t b = sb + C::kQBytes + r.at * kMhaUnit;
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          mma_bf16_ts(tmem + (NT + t) * kMhaTile, tmem + t * kMhaTile + 8 * (4 * c + kk),
-                      smem_desc(b + kk * 2048, kMhaUnit / 2, 1024, SWZ_128B), kIdescO, j + c + kk > 0 ? 1u : 0u);
-        if (last) mma_commit(smem_u32(&m.empty[r.at]));
-        r.next();
-      }
-      if (j + 1 < s.blocks[t]) {
-        const bool alone_k = NT == 1 || j + 1 >= s.blocks[1 - t];
-        if (!scores(t, rk, t == 0 || alone_k, t == NT - 1 || alone_k)) return false;
-      } else {
-        mma_commit(smem_u32(&m.o_full[t]));
+      if (!weighted(0, kMhaTile * buf, j, r, true, true)) return false;
+      mma_commit(smem_u32(j + 1 < s.most ? &m.o_step : &m.o_full[0]));
+      r.skip(2);
+      if (j + 2 < s.most) {
+        if (!scores(0, kMhaTile * buf, &m.s_full[buf], r, true, true)) return false;
+        r.skip(C::kSub);
       }
     }
-    if (j + 1 < s.most)
-      for (int c = 0; c < C::kSub; ++c) rk.next();
+  } else {
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      if (s.blocks[t] == 0) continue;
+      if (!mbar_wait(smem_u32(&m.q_full[t]), 0, deadline, ab)) return false;
+      const bool alone = s.blocks[1 - t] == 0;
+      if (!scores(t, kMhaTile * t, &m.s_full[t], r, t == 0 || alone, t == 1 || alone)) return false;
+    }
+    r.skip(C::kSub);
+    for (int j = 0; j < s.most; ++j) {
+      MhaRing<C::kUnits> rk = r;                 // block j's V, then block j + 1's K
+      rk.skip(2);
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        if (j >= s.blocks[t]) continue;
+        const bool alone = j >= s.blocks[1 - t], alone_k = j + 1 >= s.blocks[1 - t];
+        if (!mbar_wait(smem_u32(&m.p_full[t]), j & 1, deadline, ab)) return false;
+        tc_fence_after();
+        if (!weighted(t, kMhaTile * t, j, r, t == 0 || alone, t == 1 || alone)) return false;
+        if (j + 1 == s.blocks[t]) mma_commit(smem_u32(&m.o_full[t]));
+        else if (!scores(t, kMhaTile * t, &m.s_full[t], rk, t == 0 || alone_k, t == 1 || alone_k)) return false;
+      }
+      r = rk;
+      if (j + 1 < s.most) r.skip(C::kSub);
+    }
   }
   return true;
 }
@@ -498,18 +536,20 @@ __device__ __forceinline__ bool mha_softmax(const MhaFwdParams& p, MhaMisc& m, u
   const int blocks = s.blocks[t];
   const int whole = max(0, s.t0[t] + lk - lq + 1) / kMhaTile - s.from;   // blocks that every row sees all of
   const uint32_t quarter = static_cast<uint32_t>((row >> 5) * 32) << 16;
-  const uint32_t ts = tmem + quarter + t * kMhaTile, to = tmem + quarter + (NT + t) * kMhaTile;
+  const uint32_t to = tmem + quarter + C::kO + t * kMhaDv;
   const float c = p.scale_log2;
   float top = -INFINITY, sum = 0.f;   // the maximum that the weights are relative to, their sum
   for (int j = 0; j < blocks; ++j) {
+    const int buf = NT == 1 ? j & 1 : t, par = NT == 1 ? j >> 1 & 1 : j & 1;   // the S that the block's scores are in
+    const uint32_t ts = tmem + quarter + buf * kMhaTile;
     if (j >= whole) {
-      for (int i = 0; i < 2; ++i) {   // the block's V: units (j + 1) kSub + 2 j and the next
-        const uint32_t n = static_cast<uint32_t>((j + 1) * C::kSub + 2 * j + i);
+      for (int i = 0; i < 2; ++i) {   // the block's V: units behind those of the K before it and of the V before it
+        const uint32_t n = static_cast<uint32_t>(min(j + C::kAhead, s.most) * C::kSub + 2 * j + i);
         if (!mbar_wait(smem_u32(&m.full[n % C::kUnits]), n / C::kUnits & 1u, deadline, ab)) return false;
         if (mha_clear(sb + C::kQBytes + n % C::kUnits * kMhaUnit, kMhaUnit)) m.cleared = 1;
       }
     }
-    if (!mbar_wait(smem_u32(&m.s_full[t]), static_cast<uint32_t>(j) & 1u, deadline, ab)) return false;
+    if (!mbar_wait(smem_u32(&m.s_full[buf]), par, deadline, ab)) return false;
     tc_fence_after();
     float v[kMhaTile];
     tmem_load128(ts, v);
@@ -527,7 +567,11 @@ __device__ __forceinline__ bool mha_softmax(const MhaFwdParams& p, MhaMisc& m, u
     const float now = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
     const bool grown = (now - top) * c > kMhaLazy;
     if (__any_sync(0xffffffffu, grown)) {
-      // the block's scores are there, so the product before them has ended: O is this warp's to change
+      // O is this warp's to change once the product before has ended: with two tiles the block's scores came after it
+      if (NT == 1 && j > 0) {
+        if (!mbar_wait(smem_u32(&m.o_step), (j - 1) & 1, deadline, ab)) return false;
+        tc_fence_after();
+      }
       const float f = grown ? fast_exp2((top - now) * c) : 1.f;
       if (grown) top = now;
       sum *= f;
@@ -562,7 +606,7 @@ __device__ __forceinline__ bool mha_softmax(const MhaFwdParams& p, MhaMisc& m, u
     tmem_wait_st();
     tc_fence_before();
     __syncwarp();
-    if (lane_id() == 0) mbar_arrive(smem_u32(&m.p_full[t]));
+    if (lane_id() == 0) mbar_arrive(smem_u32(&m.p_full[buf]));
     add2(add[0], add[1], add[2], add[3]);
     add2(add[4], add[5], add[6], add[7]);
     add2(add[0], add[1], add[4], add[5]);
@@ -679,12 +723,13 @@ __global__ void __launch_bounds__(MhaFwdShape<DQK, NT>::kThreads, 1) dense_mha_f
       mbar_init(smem_u32(&m.full[i]), 1);
       mbar_init(smem_u32(&m.empty[i]), 1);
     }
-    for (int i = 0; i < NT; ++i) {
+    for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&m.q_full[i]), 1);
       mbar_init(smem_u32(&m.s_full[i]), 1);
       mbar_init(smem_u32(&m.p_full[i]), 4);   // one arrival per softmax warp
       mbar_init(smem_u32(&m.o_full[i]), 1);
     }
+    mbar_init(smem_u32(&m.o_step), 1);
     mbar_init(smem_u32(&m.drain), 1);
     m.abort_flag = 0;
     m.cleared = 0;
