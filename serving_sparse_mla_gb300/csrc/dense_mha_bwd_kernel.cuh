@@ -55,6 +55,7 @@ struct MhaBwdParams {
   int batch, total_q, total_kv, h_q, h_kv, group;
   int pack, tok_tile;                      // rows of a query tile: tok_tile tokens x pack heads
   int slots;                               // tiles per head (pack) that the grid has room for
+  int heads, heads_near;                   // head packs (of keys: heads); of so many at a time the longest tiles come first
   float scale, scale_log2;
   const __nv_bfloat16 *v, *dout;           // row (t, h) at v + t v_tok + h v_head
   long long v_tok, v_head, do_tok, do_head;
@@ -315,8 +316,9 @@ __global__ void __launch_bounds__(MhaDqShape<DQK>::kThreads, 1) dense_mha_dq_ker
   MhaDqMisc& m = *reinterpret_cast<MhaDqMisc*>(sbase + C::kMiscOff);
   const int warp = static_cast<int>(threadIdx.x >> 5);
   const uint32_t sb = smem_u32(sbase);
-  const int slot = static_cast<int>(blockIdx.x % static_cast<unsigned>(p.slots));
-  const int pack0 = static_cast<int>(blockIdx.x / static_cast<unsigned>(p.slots)) * p.pack;
+  int slot, head;
+  mha_unit(blockIdx.x, p.slots, p.heads, p.heads_near, slot, head);
+  const int pack0 = head * p.pack;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 3; ++i) {
@@ -345,7 +347,7 @@ __global__ void __launch_bounds__(MhaDqShape<DQK>::kThreads, 1) dense_mha_dq_ker
     tmem_relinquish();
   }
   if (warp == 9) {
-    const MhaWork w = mha_find(p.cu_q, p.cu_kv, p.batch, p.total_q, p.total_kv, slot, p.tok_tile, false, true);
+    const MhaWork w = mha_find<false>(p.cu_q, p.cu_kv, p.batch, p.total_q, p.total_kv, slot, p.tok_tile, true);
     if (lane_id() == 0) m.work = w;
   }
   tc_fence_before();
@@ -711,8 +713,8 @@ __global__ void __launch_bounds__(MhaDkvShape<DQK>::kThreads, 1) dense_mha_dkv_k
   MhaDkvMisc& m = *reinterpret_cast<MhaDkvMisc*>(sbase + C::kMiscOff);
   const int warp = static_cast<int>(threadIdx.x >> 5);
   const uint32_t sb = smem_u32(sbase);
-  const int slot = static_cast<int>(blockIdx.x % static_cast<unsigned>(p.slots));
-  const int kvh = static_cast<int>(blockIdx.x / static_cast<unsigned>(p.slots));
+  int slot, kvh;
+  mha_unit(blockIdx.x, p.slots, p.heads, p.heads_near, slot, kvh);
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 4; ++i) {
@@ -746,7 +748,7 @@ __global__ void __launch_bounds__(MhaDkvShape<DQK>::kThreads, 1) dense_mha_dkv_k
     tmem_relinquish();
   }
   if (warp == 9) {
-    const MhaWork w = mha_find(p.cu_q, p.cu_kv, p.batch, p.total_q, p.total_kv, slot, kMhaTile, true, true);
+    const MhaWork w = mha_find<true>(p.cu_q, p.cu_kv, p.batch, p.total_q, p.total_kv, slot, p.tok_tile, true);
     if (lane_id() == 0) m.work = w;
   }
   if (p.pack * p.tok_tile < C::kN) {

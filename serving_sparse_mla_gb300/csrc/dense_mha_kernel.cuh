@@ -44,6 +44,7 @@ namespace smla {
 
 constexpr int kMhaTile = 128;              // query rows of a tile, keys of a block
 constexpr int kMhaDv = 128;
+constexpr int kMhaMaxCluster = 16;
 constexpr uint32_t kMhaUnit = 16384;       // bytes of a ring unit, and of 64 columns of a Q tile
 constexpr float kMhaLazy = 8.f;            // log2 of the growth of a maximum that O is rescaled for
 
@@ -59,6 +60,7 @@ struct MhaFwdParams {
   int batch, total_q, total_kv, h_q, group; // query heads per key head
   int pack, tok_tile;                      // a tile is tok_tile tokens x pack heads
   int slots;                               // tiles (of NT) per head pack that the grid has room for
+  int packs, packs_near;                   // head packs; of so many at a time the tiles go from the longest to the shortest
   int cluster;                             // CTAs that share a tile's keys out (one tile a CTA; else 1)
   float scale_log2;
   const __nv_bfloat16* v;                  // row (t, h) at v + t v_tok + h v_head
@@ -84,34 +86,82 @@ struct MhaWork {
   int rest;             // rows behind the last sequence (k0 = k1 = 0)
 };
 
-// Tile `slot` of all sequences' tiles of `per` rows (of the queries, or of the keys with
-// `keys`), laid end to end, a sequence's last tile first: that is its longest under the
-// causal mask for queries (and its shortest for keys, so there the first comes first).
-// Behind them come the rows of no sequence where `rest` is set.  One warp, all lanes.
+// The tiles of one sequence that have more than `blocks` blocks of work (-1: all).
+//   queries: tiles of `per` rows; a block is 128 of the keys that the last row sees
+//   keys:    tiles of 128 rows; a block is `per` of the queries that see the first row
+template <bool KEYS>
+__device__ __forceinline__ int mha_tiles_above(int lq, int lk, int per, int blocks) {
+  if constexpr (KEYS) {
+    const int tiles = (lk + kMhaTile - 1) / kMhaTile;
+    if (blocks < 0) return tiles;
+    const long long seen = lq - static_cast<long long>(blocks) * per;   // the first row's queries start before this one
+    if (seen <= 0) return 0;
+    const long long n = (seen + lk - lq + kMhaTile - 1) / kMhaTile;
+    return n < 0 ? 0 : (n < tiles ? static_cast<int>(n) : tiles);
+  } else {
+    const int tiles = (lq + per - 1) / per;
+    if (blocks < 0) return tiles;
+    const long long past = static_cast<long long>(blocks) * kMhaTile + lq - lk;   // the last row is behind this one
+    if (past >= lq) return 0;
+    return past <= 0 ? tiles : tiles - static_cast<int>(past / per);
+  }
+}
+
+constexpr int kMhaSortBatch = 128;   // sequences up to which tiles are handed out by their work
+
+// Tile `slot` of all sequences' tiles, the ones with most work first (of many sequences: in
+// their order).  Behind them come the rows of no sequence where `rest` is set.  One warp,
+// all lanes.
+template <bool KEYS>
 __device__ __forceinline__ MhaWork mha_find(const int32_t* cu_q, const int32_t* cu_kv, int batch, int total_q,
-                                            int total_kv, int slot, int per, bool keys, bool rest) {
+                                            int total_kv, int slot, int per, bool rest) {
   MhaWork w = {0, 0, 0, 0, 0, 0};
+  const int rows = KEYS ? kMhaTile : per;
   if (cu_q == nullptr) {
-    w.q1 = total_q;
-    w.k1 = total_kv;
-    const int tiles = ((keys ? total_kv : total_q) + per - 1) / per;
-    w.tile = keys ? slot : tiles - 1 - slot;
-    if (slot >= tiles) w.q1 = w.k1 = 0;
+    const int tiles = ((KEYS ? total_kv : total_q) + rows - 1) / rows;
+    if (slot < tiles) {
+      w.q1 = total_q;
+      w.k1 = total_kv;
+      w.tile = KEYS ? slot : tiles - 1 - slot;
+    }
     return w;
   }
   const int lane = static_cast<int>(lane_id());
-  int before = 0, end = 0;   // tiles of the sequences so far, the largest end of their rows
-  for (int base = 0; base < batch; base += 32) {
-    const int b = base + lane;
-    int q0 = 0, q1 = 0, k0 = 0, k1 = 0;
-    if (b < batch) {
-      q0 = mha_offset(cu_q, b, total_q);
-      q1 = max(q0, mha_offset(cu_q, b + 1, total_q));
-      k0 = mha_offset(cu_kv, b, total_kv);
-      k1 = max(k0, mha_offset(cu_kv, b + 1, total_kv));
+  auto seq = [&](int b) -> int4 {
+    if (b >= batch) return make_int4(0, 0, 0, 0);
+    const int q0 = mha_offset(cu_q, b, total_q), k0 = mha_offset(cu_kv, b, total_kv);
+    return make_int4(q0, max(q0, mha_offset(cu_q, b + 1, total_q)), k0, max(k0, mha_offset(cu_kv, b + 1, total_kv)));
+  };
+  const int4 mine = seq(lane);   // of the first 32, which are often all
+  auto above = [&](const int4& x, int blocks) { return mha_tiles_above<KEYS>(x.y - x.x, x.w - x.z, per, blocks); };
+  auto all_above = [&](int blocks) {
+    int n = __reduce_add_sync(0xffffffffu, above(mine, blocks));
+    for (int base = 32; base < batch; base += 32) n += __reduce_add_sync(0xffffffffu, above(seq(base + lane), blocks));
+    return n;
+  };
+  // the tiles before this one have more than `blocks` blocks, or as many and lie in earlier sequences
+  int blocks = -1, before = 0;
+  if (batch <= kMhaSortBatch) {
+    int longest = 0;
+    for (int base = 0; base < batch; base += 32) {
+      const int4 x = base == 0 ? mine : seq(base + lane);
+      longest = max(longest, __reduce_max_sync(0xffffffffu, KEYS ? (x.y - x.x + per - 1) / per : (x.w - x.z + 127) / 128));
     }
-    const int tiles = ((keys ? k1 - k0 : q1 - q0) + per - 1) / per;
-    int incl = tiles;
+    int lo = 0, hi = longest;   // the fewest blocks that at most `slot` tiles exceed
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (all_above(mid) <= slot) hi = mid;
+      else lo = mid + 1;
+    }
+    blocks = lo;
+    before = all_above(blocks);
+  }
+  int end = 0;   // of the sequences' rows
+  for (int base = 0; base < batch; base += 32) {
+    const int4 x = base == 0 ? mine : seq(base + lane);
+    const int more = blocks < 0 ? 0 : above(x, blocks);
+    const int n = above(x, blocks - 1) - more;   // of so many blocks (or, unsorted, all)
+    int incl = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int y = __shfl_up_sync(0xffffffffu, incl, o);
@@ -120,21 +170,22 @@ __device__ __forceinline__ MhaWork mha_find(const int32_t* cu_q, const int32_t* 
     const uint32_t past = __ballot_sync(0xffffffffu, before + incl > slot);
     if (past != 0u) {
       const int at = __ffs(past) - 1;
-      w.q0 = __shfl_sync(0xffffffffu, q0, at);
-      w.q1 = __shfl_sync(0xffffffffu, q1, at);
-      w.k0 = __shfl_sync(0xffffffffu, k0, at);
-      w.k1 = __shfl_sync(0xffffffffu, k1, at);
-      const int first = before + __shfl_sync(0xffffffffu, incl - tiles, at);
-      w.tile = keys ? slot - first : first + __shfl_sync(0xffffffffu, tiles, at) - 1 - slot;
+      w.q0 = __shfl_sync(0xffffffffu, x.x, at);
+      w.q1 = __shfl_sync(0xffffffffu, x.y, at);
+      w.k0 = __shfl_sync(0xffffffffu, x.z, at);
+      w.k1 = __shfl_sync(0xffffffffu, x.w, at);
+      const int nth = slot - before - __shfl_sync(0xffffffffu, incl - n, at) + __shfl_sync(0xffffffffu, more, at);
+      // the most work is in a sequence's last tile of queries, in its first of keys
+      w.tile = KEYS ? nth : (w.q1 - w.q0 + per - 1) / per - 1 - nth;
       return w;
     }
     before += __shfl_sync(0xffffffffu, incl, 31);
-    end = max(end, __reduce_max_sync(0xffffffffu, keys ? k1 : q1));
+    end = max(end, __reduce_max_sync(0xffffffffu, KEYS ? x.w : x.y));
   }
-  const int total = keys ? total_kv : total_q;
-  const int tile = slot - before;
-  if (rest && tile < (total - end + per - 1) / per) {
-    if (keys) {
+  const int total = KEYS ? total_kv : total_q;
+  const int tile = slot - (batch <= kMhaSortBatch ? all_above(-1) : before);
+  if (rest && tile < (total - end + rows - 1) / rows) {
+    if (KEYS) {
       w.k0 = end;
       w.k1 = total;
     } else {
@@ -145,6 +196,16 @@ __device__ __forceinline__ MhaWork mha_find(const int32_t* cu_q, const int32_t* 
     w.rest = 1;
   }
   return w;
+}
+
+// Unit -> tile and head (pack): `near` heads at a time, side by side, so that their longest
+// tiles come first while what they read stays in L2.
+__device__ __forceinline__ void mha_unit(unsigned unit, int slots, int heads, int near, int& slot, int& head) {
+  const unsigned per = static_cast<unsigned>(slots) * static_cast<unsigned>(near);
+  const unsigned first = unit / per * static_cast<unsigned>(near);
+  const unsigned wide = min(static_cast<unsigned>(near), static_cast<unsigned>(heads) - first);
+  slot = static_cast<int>(unit % per / wide);
+  head = static_cast<int>(first + unit % per % wide);
 }
 
 // ------------------------------------------------------------------ PTX
@@ -275,9 +336,10 @@ __device__ __forceinline__ void add2(float& a0, float& a1, float b0, float b1) {
 // ------------------------------------------------------------------ forward
 
 constexpr int kMhaMaxUnits = 12;
+constexpr int kMhaFree = 4;   // a block's release is told on one of so many barriers in turn: more than the ring has blocks
 
 struct __align__(16) MhaMisc {
-  uint64_t q_full[2], full[kMhaMaxUnits], empty[kMhaMaxUnits], s_full[2], p_full[2], o_full[2], o_step, drain;
+  uint64_t q_full[2], full[kMhaMaxUnits], k_free[kMhaFree], v_free[kMhaFree], s_full[2], p_full[2], o_full[2], o_step, drain;
   uint32_t tmem_base;
   int abort_flag;
   int prior_error;
@@ -351,27 +413,29 @@ struct MhaRing {
   }
 };
 
+// The blocks in the order of their use: K 0, V 0, K 1, V 1, ...; with `ahead` 2: K 0, K 1,
+// V 0, K 2, V 1, ...
+struct MhaOrder {
+  bool value = false;   // of V
+  int block = 0;
+  __device__ __forceinline__ void next(int ahead, int most) {
+    if (!value && ahead == 2 && block == 0 && most > 1) block = 1;
+    else if (!value) {
+      value = true;
+      block = max(0, block + 1 - ahead);
+    } else if (block + ahead < most) {
+      value = false;
+      block += ahead;
+    } else ++block;
+  }
+};
+
 template <int DQK, int NT>
 __device__ __forceinline__ bool mha_load(const MhaFwdParams& p, MhaMisc& m, uint32_t sb, const MhaWork& w,
                                          const MhaSpan<NT>& s, int pack0, int kvh, uint32_t& fills) {
   using C = MhaFwdShape<DQK, NT>;
   const volatile int* ab = &m.abort_flag;
   const uint64_t deadline = global_timer_ns() + p.timeout_ns;
-  MhaRing<C::kUnits> r;
-  auto take = [&]() -> bool {
-    return mbar_wait(smem_u32(&m.empty[r.at]), r.turn ^ 1u, deadline, ab);
-  };
-  auto load_k = [&](int j) -> bool {
-    for (int c = 0; c < C::kSub; ++c) {
-      if (!take()) return false;
-      const uint32_t bar = smem_u32(&m.full[r.at]);
-      mbar_arrive_expect_tx(bar, kMhaUnit);
-      tma_load_3d(sb + C::kQBytes + r.at * kMhaUnit, &p.map_k, 64 * c, kvh, w.k0 + (s.from + j) * kMhaTile, bar);
-      ++fills;
-      r.next();
-    }
-    return true;
-  };
   auto load_q = [&](int t) {
     const uint32_t bar = smem_u32(&m.q_full[t]);
     const uint32_t bytes = static_cast<uint32_t>(p.pack * p.tok_tile) * 128u;
@@ -380,20 +444,34 @@ __device__ __forceinline__ bool mha_load(const MhaFwdParams& p, MhaMisc& m, uint
       tma_load_3d(sb + (t * C::kSub + c) * kMhaUnit, &p.map_q, 64 * c, pack0, w.q0 + s.t0[t], bar);
   };
   if (s.blocks[0] > 0) load_q(0);
-  if (!load_k(0)) return false;
-  if (NT > 1 && s.blocks[NT - 1] > 0) load_q(NT - 1);
-  if (C::kAhead > 1 && s.most > 1 && !load_k(1)) return false;
-  for (int j = 0; j < s.most; ++j) {
-    for (int c = 0; c < 2; ++c) {
-      if (!take()) return false;
+  MhaRing<C::kUnits> r;
+  MhaOrder now, old;       // the block that is loaded, the one whose units come free next
+  int old_left = 0;        // units of `old` that are free and not yet filled
+  for (int n = 0; n < 2 * s.most; ++n) {
+    for (int c = 0; c < (now.value ? 2 : C::kSub); ++c) {
+      if (fills >= static_cast<uint32_t>(C::kUnits)) {
+        if (old_left == 0) {
+          uint64_t* bar = old.value ? &m.v_free[old.block % kMhaFree] : &m.k_free[old.block % kMhaFree];
+          if (!mbar_wait(smem_u32(bar), old.block / kMhaFree & 1, deadline, ab)) return false;
+          old_left = old.value ? 2 : C::kSub;
+          old.next(C::kAhead, s.most);
+        }
+        --old_left;
+      }
       const uint32_t bar = smem_u32(&m.full[r.at]), dst = sb + C::kQBytes + r.at * kMhaUnit;
+      const int row = w.k0 + (s.from + now.block) * kMhaTile;
       mbar_arrive_expect_tx(bar, kMhaUnit);
-      tma_load_3d(dst, &p.map_v, 0, kvh, w.k0 + (s.from + j) * kMhaTile + 64 * c, bar);
-      tma_load_3d(dst + kMhaUnit / 2, &p.map_v, 64, kvh, w.k0 + (s.from + j) * kMhaTile + 64 * c, bar);
+      if (now.value) {
+        tma_load_3d(dst, &p.map_v, 0, kvh, row + 64 * c, bar);
+        tma_load_3d(dst + kMhaUnit / 2, &p.map_v, 64, kvh, row + 64 * c, bar);
+      } else {
+        tma_load_3d(dst, &p.map_k, 64 * c, kvh, row, bar);
+      }
       ++fills;
       r.next();
     }
-    if (j + C::kAhead < s.most && !load_k(j + C::kAhead)) return false;
+    if (n == 0 && NT > 1 && s.blocks[NT - 1] > 0) load_q(NT - 1);
+    now.next(C::kAhead, s.most);
   }
   return true;
 }
@@ -412,9 +490,9 @@ __device__ __forceinline__ bool mha_mma(const MhaFwdParams& p, MhaMisc& m, uint3
   auto wait_unit = [&](const MhaRing<C::kUnits>& u) -> bool {
     return mbar_wait(smem_u32(&m.full[u.at]), u.turn, deadline, ab);
   };
-  // S (columns `to`, barrier `bar`) = Q_t K^T of the block at `u`; `first`: its units have not been waited for, `last`:
+  // S (columns `to`, barrier `bar`) = Q_t K^T of block j at `u`; `first`: its units have not been waited for, `last`:
   // they are free behind it
-  auto scores = [&](int t, uint32_t to, uint64_t* bar, MhaRing<C::kUnits> u, bool first, bool last) -> bool {
+  auto scores = [&](int t, uint32_t to, uint64_t* bar, int j, MhaRing<C::kUnits> u, bool first, bool last) -> bool {
 #pragma unroll
     for (int c = 0; c < C::kSub; ++c) {
       if (first && !wait_unit(u)) return false;
@@ -422,10 +500,10 @@ __device__ __forceinline__ bool mha_mma(const MhaFwdParams& p, MhaMisc& m, uint3
 #pragma unroll
       for (int kk = 0; kk < 4; ++kk)
         mma_bf16_ss(tmem + to, desc_plus(a, kk * 32), desc_plus(b, kk * 32), kIdescS, c + kk > 0 ? 1u : 0u);
-      if (last) mma_commit(smem_u32(&m.empty[u.at]));
       u.next();
     }
     mma_commit(smem_u32(bar));
+    if (last) mma_commit(smem_u32(&m.k_free[j % kMhaFree]));
     return true;
   };
   // O_t += P (columns `from`) V of block j at `u`
@@ -438,9 +516,9 @@ __device__ __forceinline__ bool mha_mma(const MhaFwdParams& p, MhaMisc& m, uint3
       for (int kk = 0; kk < 4; ++kk)
         mma_bf16_ts(tmem + C::kO + t * kMhaDv, tmem + from + 8 * (4 * c + kk), desc_plus(b, kk * 2048), kIdescO,
                     j + c + kk > 0 ? 1u : 0u);
-      if (last) mma_commit(smem_u32(&m.empty[u.at]));
       u.next();
     }
+    if (last) mma_commit(smem_u32(&m.v_free[j % kMhaFree]));
     return true;
   };
   if constexpr (NT == 1) {
@@ -448,7 +526,7 @@ __device__ __forceinline__ bool mha_mma(const MhaFwdParams& p, MhaMisc& m, uint3
     // the one before
     if (!mbar_wait(smem_u32(&m.q_full[0]), 0, deadline, ab)) return false;
     for (int j = 0; j < 2 && j < s.most; ++j) {
-      if (!scores(0, kMhaTile * j, &m.s_full[j], r, true, true)) return false;
+      if (!scores(0, kMhaTile * j, &m.s_full[j], j, r, true, true)) return false;
       r.skip(C::kSub);
     }
     for (int j = 0; j < s.most; ++j) {
@@ -459,7 +537,7 @@ __device__ __forceinline__ bool mha_mma(const MhaFwdParams& p, MhaMisc& m, uint3
       mma_commit(smem_u32(j + 1 < s.most ? &m.o_step : &m.o_full[0]));
       r.skip(2);
       if (j + 2 < s.most) {
-        if (!scores(0, kMhaTile * buf, &m.s_full[buf], r, true, true)) return false;
+        if (!scores(0, kMhaTile * buf, &m.s_full[buf], j + 2, r, true, true)) return false;
         r.skip(C::kSub);
       }
     }
@@ -469,7 +547,7 @@ __device__ __forceinline__ bool mha_mma(const MhaFwdParams& p, MhaMisc& m, uint3
       if (s.blocks[t] == 0) continue;
       if (!mbar_wait(smem_u32(&m.q_full[t]), 0, deadline, ab)) return false;
       const bool alone = s.blocks[1 - t] == 0;
-      if (!scores(t, kMhaTile * t, &m.s_full[t], r, t == 0 || alone, t == 1 || alone)) return false;
+      if (!scores(t, kMhaTile * t, &m.s_full[t], 0, r, t == 0 || alone, t == 1 || alone)) return false;
     }
     r.skip(C::kSub);
     for (int j = 0; j < s.most; ++j) {
@@ -483,7 +561,7 @@ __device__ __forceinline__ bool mha_mma(const MhaFwdParams& p, MhaMisc& m, uint3
         tc_fence_after();
         if (!weighted(t, kMhaTile * t, j, r, t == 0 || alone, t == 1 || alone)) return false;
         if (j + 1 == s.blocks[t]) mma_commit(smem_u32(&m.o_full[t]));
-        else if (!scores(t, kMhaTile * t, &m.s_full[t], rk, t == 0 || alone_k, t == 1 || alone_k)) return false;
+        else if (!scores(t, kMhaTile * t, &m.s_full[t], j + 1, rk, t == 0 || alone_k, t == 1 || alone_k)) return false;
       }
       r = rk;
       if (j + 1 < s.most) r.skip(C::kSub);
@@ -662,44 +740,51 @@ __device__ __forceinline__ bool mha_softmax(const MhaFwdParams& p, MhaMisc& m, u
   return true;
 }
 
-// The parts that a cluster's CTAs have left of a tile, joined: a warp takes a row, four
-// columns a lane, parts in the order of their keys.
-template <int DQK>
-__device__ __forceinline__ void mha_join(const MhaFwdParams& p, MhaMisc& m, uint32_t sb, const MhaWork& w,
-                                         const MhaSpan<1>& s, int pack0, int rank) {
+// The parts that a cluster's CTAs have left of a tile, joined in the order of their keys:
+// W columns a thread.  Reads of another CTA's memory take about a microsecond, so there
+// should be few steps of them: many columns a thread for many rows, few for few.
+template <int DQK, int W>
+__device__ __forceinline__ void mha_join(const MhaFwdParams& p, MhaMisc& m, uint32_t sb, const MhaWork& w, int t0, int rows,
+                                         int pack0, int rank) {
   using C = MhaFwdShape<DQK, 1>;
-  const int lane = static_cast<int>(lane_id()), warp = static_cast<int>(threadIdx.x >> 5);
-  const int rows = min(p.tok_tile, w.q1 - w.q0 - s.t0[0]) * p.pack;
-  for (int row = rank * 4 + warp; row < rows; row += 4 * p.cluster) {
-    float2 mine = make_float2(-INFINITY, 0.f);
-    if (lane < p.cluster) {
-      const uint32_t at = cluster_addr(smem_u32(&m.part[row]), lane);
-      mine = make_float2(ld_cluster_f(at), ld_cluster_f(at + 4));
-    }
-    float top = mine.x;
+  constexpr int kPerRow = kMhaDv / W, kRows = 128 / kPerRow;
+  const int col = static_cast<int>(threadIdx.x) % kPerRow * W;
+  for (int row = rank * kRows + static_cast<int>(threadIdx.x) / kPerRow; row < rows; row += kRows * p.cluster) {
+    const uint32_t stat = smem_u32(&m.part[row]), at = sb + C::kQBytes + static_cast<uint32_t>(row * kMhaPartRow + col) * 4u;
+    float top = -INFINITY, sum = 0.f, acc[W];
 #pragma unroll
-    for (int i = 16; i > 0; i >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, i));
-    const float weight = mine.y == 0.f ? 0.f : fast_exp2(mine.x - top);   // a sum that is NaN passes it on
-    const float sum = warp_sum(weight * mine.y);
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    const uint32_t at = sb + C::kQBytes + static_cast<uint32_t>(row * kMhaPartRow + 4 * lane) * 4u;
-#pragma unroll 4
+    for (int i = 0; i < kMhaMaxCluster; ++i)
+      if (i < p.cluster) top = fmaxf(top, ld_cluster_f(cluster_addr(stat, i)));
+#pragma unroll
+    for (int k = 0; k < W; ++k) acc[k] = 0.f;
+#pragma unroll W > 4 ? 2 : 8
     for (int i = 0; i < p.cluster; ++i) {
-      const float f = __shfl_sync(0xffffffffu, weight, i);
-      const float4 x = ld_cluster_f4(cluster_addr(at, i));
-      if (f != 0.f) {
-        acc.x += f * x.x;
-        acc.y += f * x.y;
-        acc.z += f * x.z;
-        acc.w += f * x.w;
+      const uint32_t peer = cluster_addr(stat, i), from = cluster_addr(at, i);
+      const float own = ld_cluster_f(peer), own_sum = ld_cluster_f(peer + 4);
+      float4 x[W / 4];
+#pragma unroll
+      for (int k = 0; k < W / 4; ++k) x[k] = ld_cluster_f4(from + 16 * k);
+      const float f = own_sum == 0.f ? 0.f : fast_exp2(own - top);   // a sum that is NaN passes it on
+      sum += f * own_sum;
+      if (f == 0.f) continue;
+#pragma unroll
+      for (int k = 0; k < W / 4; ++k) {
+        acc[4 * k] += f * x[k].x;
+        acc[4 * k + 1] += f * x[k].y;
+        acc[4 * k + 2] += f * x[k].z;
+        acc[4 * k + 3] += f * x[k].w;
       }
     }
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    const size_t out = static_cast<size_t>(w.q0 + s.t0[0] + row / p.pack) * p.h_q + pack0 + row % p.pack;
-    if (!w.rest || (p.fill & 1))
-      *reinterpret_cast<uint2*>(p.out + out * kMhaDv + 4 * lane) =
-          make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-    if (lane == 0 && (!w.rest || (p.fill & 2)))
+    const size_t out = static_cast<size_t>(w.q0 + t0 + row / p.pack) * p.h_q + pack0 + row % p.pack;
+    if (!w.rest || (p.fill & 1)) {
+      uint2* o = reinterpret_cast<uint2*>(p.out + out * kMhaDv + col);
+#pragma unroll
+      for (int k = 0; k < W / 4; ++k)
+        o[k] = make_uint2(pack_bf16x2(acc[4 * k] * inv, acc[4 * k + 1] * inv),
+                          pack_bf16x2(acc[4 * k + 2] * inv, acc[4 * k + 3] * inv));
+    }
+    if (col == 0 && (!w.rest || (p.fill & 2)))
       p.lse[out] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
   }
 }
@@ -715,13 +800,15 @@ __global__ void __launch_bounds__(MhaFwdShape<DQK, NT>::kThreads, 1) dense_mha_f
   const uint32_t sb = smem_u32(sbase);
   const unsigned unit = NT == 1 ? blockIdx.x / static_cast<unsigned>(p.cluster) : blockIdx.x;
   const int rank = NT == 1 ? static_cast<int>(blockIdx.x % static_cast<unsigned>(p.cluster)) : 0;
-  const int slot = static_cast<int>(unit % static_cast<unsigned>(p.slots));
-  const int pack0 = static_cast<int>(unit / static_cast<unsigned>(p.slots)) * p.pack;
+  int slot, head;
+  mha_unit(unit, p.slots, p.packs, p.packs_near, slot, head);
+  const int pack0 = head * p.pack;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < C::kUnits; ++i) {
-      mbar_init(smem_u32(&m.full[i]), 1);
-      mbar_init(smem_u32(&m.empty[i]), 1);
+    for (int i = 0; i < C::kUnits; ++i) mbar_init(smem_u32(&m.full[i]), 1);
+    for (int i = 0; i < kMhaFree; ++i) {
+      mbar_init(smem_u32(&m.k_free[i]), 1);
+      mbar_init(smem_u32(&m.v_free[i]), 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&m.q_full[i]), 1);
@@ -744,7 +831,7 @@ __global__ void __launch_bounds__(MhaFwdShape<DQK, NT>::kThreads, 1) dense_mha_f
     tmem_relinquish();
   }
   if (warp == 4 * NT + 1) {
-    const MhaWork w = mha_find(p.cu_q, p.cu_kv, p.batch, p.total_q, p.total_kv, slot, NT * p.tok_tile, false, p.fill != 0);
+    const MhaWork w = mha_find<false>(p.cu_q, p.cu_kv, p.batch, p.total_q, p.total_kv, slot, NT * p.tok_tile, p.fill != 0);
     if (lane_id() == 0) m.work = w;
   }
   tc_fence_before();
@@ -786,8 +873,11 @@ __global__ void __launch_bounds__(MhaFwdShape<DQK, NT>::kThreads, 1) dense_mha_f
   if constexpr (NT == 1) {
     if (p.cluster > 1) {
       cluster_sync();   // every CTA's part is there
-      if (warp < 4 && m.prior_error == 0 && m.abort_flag == 0 && w.q1 > w.q0)
-        mha_join<DQK>(p, m, sb, w, MhaSpan<1>(p, w, rank), pack0, rank);
+      if (warp < 4 && m.prior_error == 0 && m.abort_flag == 0 && w.q1 > w.q0) {
+        const int t0 = w.tile * p.tok_tile, rows = min(p.tok_tile, w.q1 - w.q0 - t0) * p.pack;
+        if (rows <= 4 * p.cluster) mha_join<DQK, 4>(p, m, sb, w, t0, rows, pack0, rank);
+        else mha_join<DQK, 32>(p, m, sb, w, t0, rows, pack0, rank);
+      }
       cluster_sync();   // no CTA leaves while another reads its part
     }
   }

@@ -208,7 +208,6 @@ sparse_mla_status_t mha_map(CUtensorMap* map, const MhaRows& r, int total, int h
 }
 
 constexpr int kMhaClusterSizes = 4;   // 16, 8, 4 and 2 CTAs
-constexpr int kMhaMaxCluster = 16;
 
 struct MhaState {
   bool set = false;
@@ -245,7 +244,7 @@ bool mha_setup(int* clusters) {
   if (ok) {
     refused = cudaFuncSetAttribute(one, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess;
     for (int i = 0; i < kMhaClusterSizes; ++i) {
-      const int c = kMhaMaxCluster >> i;
+      const int c = smla::kMhaMaxCluster >> i;
       cudaLaunchConfig_t cfg = {};
       cudaLaunchAttribute attr = {};
       mha_cluster_config<DQK>(&cfg, &attr, static_cast<unsigned>(c), c);
@@ -287,11 +286,11 @@ MhaPlan mha_plan(int total_q, int total_kv, int batch, bool packed, bool rest, i
   auto units = [&](int tiles) { return std::ceil(lq / (tok_tile * tiles)) * batch * packs; };
   MhaPlan best = {2, 1, 0};
   double least = std::max(longest, units(2) * mean / sms);
-  for (int c = 1; c <= kMhaMaxCluster; c *= 2) {
+  for (int c = 1; c <= smla::kMhaMaxCluster; c *= 2) {
     if (c > 1) {
       int held = 0;
       for (int i = 0; i < kMhaClusterSizes; ++i)
-        if (kMhaMaxCluster >> i == c) held = clusters[i];
+        if (smla::kMhaMaxCluster >> i == c) held = clusters[i];
       if (units(1) > held || longest < 2 * c) continue;
     }
     const double t = std::max(std::ceil(longest / c), units(1) * mean / sms) + (c > 1 ? 1.0 : 0.0);
@@ -316,6 +315,11 @@ cudaError_t mha_fwd_launch(const smla::MhaFwdParams& p, const MhaPlan& plan, uns
   mha_cluster_config<DQK>(&cfg, &attr, ctas, plan.cluster);
   cfg.stream = cs;
   return cudaLaunchKernelEx(&cfg, smla::dense_mha_fwd_kernel<DQK, 1>, p);
+}
+
+// As many heads side by side as have what their tiles read, `bytes` each, in half of L2.
+int mha_near(int heads, double bytes) {
+  return static_cast<int>(std::max(1.0, std::min(static_cast<double>(heads), 6.4e7 / (bytes + 1))));
 }
 
 // dq (and D into the workspace), then dk and dv.
@@ -373,6 +377,8 @@ sparse_mla_status_t mha_bwd_launch(const MhaRows& q, const MhaRows& k, const Mha
     const long long slots = mha_slots(total_q, p.tok_tile, seqs, seqs > 0), ctas = slots * (h_q / p.pack);
     if (ctas > INT_MAX) return SPARSE_MLA_ERR_INVALID_ARG;
     p.slots = static_cast<int>(slots);
+    p.heads = h_q / p.pack;
+    p.heads_near = mha_near(p.heads, static_cast<double>(total_kv) * (DQK + smla::kMhaDv) * 2 * p.pack / p.group);
     smla::dense_mha_dq_kernel<DQK><<<static_cast<unsigned>(ctas), C::kThreads, C::kBytes, cs>>>(p);
     if (cudaGetLastError() != cudaSuccess) return SPARSE_MLA_ERR_CUDA;
   }
@@ -382,6 +388,8 @@ sparse_mla_status_t mha_bwd_launch(const MhaRows& q, const MhaRows& k, const Mha
     const long long slots = mha_slots(total_kv, smla::kMhaTile, seqs, seqs > 0), ctas = slots * h_kv;
     if (ctas > INT_MAX) return SPARSE_MLA_ERR_INVALID_ARG;
     p.slots = static_cast<int>(slots);
+    p.heads = h_kv;
+    p.heads_near = mha_near(h_kv, static_cast<double>(total_q) * (DQK + smla::kMhaDv) * 2 * p.group);
     smla::dense_mha_dkv_kernel<DQK><<<static_cast<unsigned>(ctas), C::kThreads, C::kBytes, cs>>>(p);
     if (cudaGetLastError() != cudaSuccess) return SPARSE_MLA_ERR_CUDA;
   }
@@ -442,6 +450,8 @@ sparse_mla_status_t dense_mha_fwd(const void* q, long long q_tok_stride, long lo
   const MhaPlan plan = mha_plan(total_q, total_kv, p.batch, cu_seqlens_q != nullptr, p.fill != 0, h_q / p.pack, p.tok_tile,
                                 sms, state->clusters[d_qk == 192 ? 0 : 1]);
   p.cluster = plan.cluster;
+  p.packs = h_q / p.pack;
+  p.packs_near = mha_near(p.packs, static_cast<double>(total_kv) * (d_qk + d_v) * 2 * p.pack / group);
   const long long ctas = plan.slots * (h_q / p.pack) * plan.cluster;
   if (ctas > INT_MAX) return SPARSE_MLA_ERR_INVALID_ARG;
   p.slots = static_cast<int>(plan.slots);
