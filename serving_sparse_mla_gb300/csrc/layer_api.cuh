@@ -215,9 +215,8 @@ struct MhaState {
 };
 MhaState g_mha[kMaxDevices];   // under g_mu
 
-template <int DQK>
+template <class C>
 void mha_cluster_config(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attr, unsigned ctas, int cluster) {
-  using C = smla::MhaFwdShape<DQK, 1>;
   cfg->gridDim = dim3(ctas);
   cfg->blockDim = dim3(C::kThreads);
   cfg->dynamicSmemBytes = C::kBytes;
@@ -235,11 +234,13 @@ bool mha_setup(int* clusters) {
   auto memory = [](const void* kernel, int bytes) {
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess;
   };
-  const void* one = reinterpret_cast<const void*>(smla::dense_mha_fwd_kernel<DQK, 1>);
-  const bool ok = memory(one, smla::MhaFwdShape<DQK, 1>::kBytes) &&
-                  memory(reinterpret_cast<const void*>(smla::dense_mha_fwd_kernel<DQK, 2>), smla::MhaFwdShape<DQK, 2>::kBytes) &&
-                  memory(reinterpret_cast<const void*>(smla::dense_mha_dq_kernel<DQK>), smla::MhaDqShape<DQK>::kBytes) &&
-                  memory(reinterpret_cast<const void*>(smla::dense_mha_dkv_kernel<DQK>), smla::MhaDkvShape<DQK>::kBytes);
+  auto address = [](auto* kernel) { return reinterpret_cast<const void*>(kernel); };
+  const void* one = address(smla::dense_mha_fwd_kernel<DQK, 1, false>);
+  const bool ok = memory(one, smla::MhaFwdShape<DQK, 1, false>::kBytes) &&
+                  memory(address(smla::dense_mha_fwd_kernel<DQK, 2, false>), smla::MhaFwdShape<DQK, 2, false>::kBytes) &&
+                  memory(address(smla::dense_mha_fwd_kernel<DQK, 2, true>), smla::MhaFwdShape<DQK, 2, true>::kBytes) &&
+                  memory(address(smla::dense_mha_dq_kernel<DQK>), smla::MhaDqShape<DQK>::kBytes) &&
+                  memory(address(smla::dense_mha_dkv_kernel<DQK>), smla::MhaDkvShape<DQK>::kBytes);
   bool refused = false;
   if (ok) {
     refused = cudaFuncSetAttribute(one, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess;
@@ -247,8 +248,8 @@ bool mha_setup(int* clusters) {
       const int c = smla::kMhaMaxCluster >> i;
       cudaLaunchConfig_t cfg = {};
       cudaLaunchAttribute attr = {};
-      mha_cluster_config<DQK>(&cfg, &attr, static_cast<unsigned>(c), c);
-      if (cudaOccupancyMaxActiveClusters(&clusters[i], smla::dense_mha_fwd_kernel<DQK, 1>, &cfg) != cudaSuccess) {
+      mha_cluster_config<smla::MhaFwdShape<DQK, 1, false>>(&cfg, &attr, static_cast<unsigned>(c), c);
+      if (cudaOccupancyMaxActiveClusters(&clusters[i], smla::dense_mha_fwd_kernel<DQK, 1, false>, &cfg) != cudaSuccess) {
         clusters[i] = 0;
         refused = true;
       }
@@ -270,7 +271,8 @@ sparse_mla_status_t mha_device_setup(const MhaState** state) {
   return st.set ? SPARSE_MLA_OK : SPARSE_MLA_ERR_CUDA;
 }
 
-// How the forward's work is laid out: tiles per CTA and CTAs that share a tile's keys.
+// How the forward's work is laid out: tiles per CTA (4: two CTAs with two each that share
+// their products) and CTAs of a cluster.
 struct MhaPlan {
   int tiles, cluster;
   long long slots;
@@ -299,22 +301,26 @@ MhaPlan mha_plan(int total_q, int total_kv, int batch, bool packed, bool rest, i
       best = {1, c, 0};
     }
   }
+  // pairs where there are rows enough for all of them: the same blocks with half of the copies and of B's reads
+  if (best.tiles == 2 && units(4) * 2 >= 2 * sms && lq >= 8.0 * tok_tile) best = {4, 2, 0};
   best.slots = mha_slots(total_q, tok_tile * best.tiles, packed ? batch : 0, rest);
   return best;
 }
 
-template <int DQK>
-cudaError_t mha_fwd_launch(const smla::MhaFwdParams& p, const MhaPlan& plan, unsigned ctas, cudaStream_t cs) {
-  if (plan.tiles == 2) {
-    using C = smla::MhaFwdShape<DQK, 2>;
-    smla::dense_mha_fwd_kernel<DQK, 2><<<ctas, C::kThreads, C::kBytes, cs>>>(p);
-    return cudaGetLastError();
-  }
+template <int DQK, int NT, bool PAIR>
+cudaError_t mha_fwd_launch_as(const smla::MhaFwdParams& p, unsigned ctas, cudaStream_t cs) {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr = {};
-  mha_cluster_config<DQK>(&cfg, &attr, ctas, plan.cluster);
+  mha_cluster_config<smla::MhaFwdShape<DQK, NT, PAIR>>(&cfg, &attr, ctas, p.cluster);
   cfg.stream = cs;
-  return cudaLaunchKernelEx(&cfg, smla::dense_mha_fwd_kernel<DQK, 1>, p);
+  return cudaLaunchKernelEx(&cfg, smla::dense_mha_fwd_kernel<DQK, NT, PAIR>, p);
+}
+
+template <int DQK>
+cudaError_t mha_fwd_launch(const smla::MhaFwdParams& p, int tiles, unsigned ctas, cudaStream_t cs) {
+  return tiles == 1   ? mha_fwd_launch_as<DQK, 1, false>(p, ctas, cs)
+         : tiles == 2 ? mha_fwd_launch_as<DQK, 2, false>(p, ctas, cs)
+                      : mha_fwd_launch_as<DQK, 2, true>(p, ctas, cs);
 }
 
 // As many heads side by side as have what their tiles read, `bytes` each, in half of L2.
@@ -424,13 +430,6 @@ sparse_mla_status_t dense_mha_fwd(const void* q, long long q_tok_stride, long lo
   p.pack = mha_pack(group, smla::kMhaTile);
   p.tok_tile = smla::kMhaTile / p.pack;
   if ((st = mha_map(&p.map_q, rq, total_q, h_q, d_qk, p.pack, p.tok_tile)) != SPARSE_MLA_OK) return st;
-  // without keys nothing is loaded: any map does
-  const bool keys = total_kv > 0;
-  if ((st = mha_map(&p.map_k, keys ? rk : rq, keys ? total_kv : total_q, keys ? h_kv : h_q, d_qk, 1, smla::kMhaTile)) !=
-          SPARSE_MLA_OK ||
-      (st = mha_map(&p.map_v, keys ? rv : rq, keys ? total_kv : total_q, keys ? h_kv : h_q, smla::kMhaDv, 1,
-                    smla::kMhaTile / 2)) != SPARSE_MLA_OK)
-    return st;
   p.cu_q = cu_seqlens_q;
   p.cu_kv = cu_seqlens_kv;
   p.batch = cu_seqlens_q ? batch : 1;
@@ -449,6 +448,14 @@ sparse_mla_status_t dense_mha_fwd(const void* q, long long q_tok_stride, long lo
   p.timeout_ns = t ? t : kDefaultTimeoutNs;
   const MhaPlan plan = mha_plan(total_q, total_kv, p.batch, cu_seqlens_q != nullptr, p.fill != 0, h_q / p.pack, p.tok_tile,
                                 sms, state->clusters[d_qk == 192 ? 0 : 1]);
+  // without keys nothing is loaded: any map does
+  const bool keys = total_kv > 0;
+  if ((st = mha_map(&p.map_k, keys ? rk : rq, keys ? total_kv : total_q, keys ? h_kv : h_q, d_qk, 1,
+                    plan.tiles == 4 ? smla::kMhaTile / 2 : smla::kMhaTile)) !=
+          SPARSE_MLA_OK ||
+      (st = mha_map(&p.map_v, keys ? rv : rq, keys ? total_kv : total_q, keys ? h_kv : h_q, smla::kMhaDv, 1,
+                    smla::kMhaTile / 2)) != SPARSE_MLA_OK)
+    return st;
   p.cluster = plan.cluster;
   p.packs = h_q / p.pack;
   p.packs_near = mha_near(p.packs, static_cast<double>(total_kv) * (d_qk + d_v) * 2 * p.pack / group);
@@ -456,8 +463,8 @@ sparse_mla_status_t dense_mha_fwd(const void* q, long long q_tok_stride, long lo
   if (ctas > INT_MAX) return SPARSE_MLA_ERR_INVALID_ARG;
   p.slots = static_cast<int>(plan.slots);
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = d_qk == 192 ? mha_fwd_launch<192>(p, plan, static_cast<unsigned>(ctas), cs)
-                                    : mha_fwd_launch<128>(p, plan, static_cast<unsigned>(ctas), cs);
+  const cudaError_t e = d_qk == 192 ? mha_fwd_launch<192>(p, plan.tiles, static_cast<unsigned>(ctas), cs)
+                                    : mha_fwd_launch<128>(p, plan.tiles, static_cast<unsigned>(ctas), cs);
   return e == cudaSuccess ? SPARSE_MLA_OK : SPARSE_MLA_ERR_CUDA;
 }
 

@@ -369,3 +369,29 @@ def test_few_rows_and_values_that_are_not_finite(smla, what):
     bad[60:, :, 7] = True
     bad[:, 1, 9] = True
     assert not out[bad].isfinite().any() and torch.equal(out[~bad], want[0][~bad])
+
+
+@pytest.mark.parametrize("d,h,hk,lq,lk", [
+    (192, 64, 64, [1100], [1100]), (128, 64, 8, [1300], [1300]), (192, 64, 8, [900, 1300, 600], [1000, 1300, 700]),
+    (128, 160, 32, [513], [900]), (192, 96, 96, [700, 1025], [640, 1025]), (128, 128, 1, [700], [700])])
+def test_many_tiles(smla, d, h, hk, lq, lk):
+    """Pairs of CTAs that share their products; rows that end in either CTA's tiles, and before them."""
+    _run(smla, h + lq[0], lq, lk, h, hk, d, tail=3)
+
+
+@pytest.mark.parametrize("what", [NAN, INF])
+@pytest.mark.parametrize("at", [300, 511, 512, 1000])
+def test_many_tiles_and_hidden_values_that_are_not_finite(smla, at, what):
+    n, h = 1050, 64
+    q, k, v, *_ = _inputs(16, [n], [n], h, h, 128)
+    want = smla.dense_mha_fwd(q, k, v, 0.1)
+    v2, k2 = v.clone(), k.clone()
+    v2[at, :, 5::60] = what
+    k2[at, :, 3] = what
+    out, lse = smla.dense_mha_fwd(q, k, v2, 0.1)
+    cols = torch.zeros(128, dtype=torch.bool, device=DEV)
+    cols[5::60] = True
+    assert torch.equal(lse, want[1]) and torch.equal(out[:at], want[0][:at])
+    assert torch.equal(out[..., ~cols], want[0][..., ~cols]) and not out[at:][..., cols].isfinite().any()
+    out, lse = smla.dense_mha_fwd(q, k2, v2, 0.1)
+    assert torch.equal(lse[:at], want[1][:at]) and torch.equal(out[:at], want[0][:at])
