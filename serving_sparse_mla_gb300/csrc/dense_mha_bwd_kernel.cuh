@@ -150,67 +150,68 @@ __device__ __forceinline__ bool mha_dq_load(const MhaBwdParams& p, MhaDqMisc& m,
 }
 
 template <int DQK>
-__device__ __forceinline__ bool mha_dq_mma(const MhaBwdParams& p, MhaDqMisc& m, uint32_t sb, uint32_t tmem, int blocks) {
+__device__ __forceinline__ bool mha_dq_mma(const MhaBwdParams& p, MhaDqMisc& m, uint32_t sb, int blocks) {
   using C = MhaDqShape<DQK>;
   constexpr uint32_t kIdescS = idesc_bf16_f32(kMhaTile, kMhaTile, false, false);
   constexpr uint32_t kIdescQ = idesc_bf16_f32(kMhaTile, DQK, false, true);
   const uint64_t q_desc = smem_desc(sb, 16, 1024, SWZ_128B), k_desc = smem_desc(sb + C::kKOff, 16, 1024, SWZ_128B),
                  kt_desc = smem_desc(sb + C::kKOff, kMhaUnit, 1024, SWZ_128B),   // its rows as columns
                  v_desc = smem_desc(sb + C::kVOff, 16, 1024, SWZ_128B);
+  const uint32_t chosen = elect_one();
   const volatile int* ab = &m.abort_flag;
   const uint64_t deadline = global_timer_ns() + p.timeout_ns;
   auto scores = [&](int j) -> bool {
     const int st = j % C::kKStages;
-    if (!mbar_wait(smem_u32(&m.k_full[st]), j / C::kKStages & 1, deadline, ab)) return false;
+    if (!warp_wait(smem_u32(&m.k_full[st]), j / C::kKStages & 1, deadline, ab)) return false;
     const uint64_t k = desc_plus(k_desc, st * C::kKBytes);
 #pragma unroll
     for (int kk = 0; kk < DQK / 16; ++kk) {
       const uint32_t off = (kk >> 2) * kMhaUnit + (kk & 3) * 32;
-      mma_bf16_ss(tmem + C::kS, desc_plus(q_desc, off), desc_plus(k, off), kIdescS, kk > 0 ? 1u : 0u);
+      mma_ss(chosen, C::kS, desc_plus(q_desc, off), desc_plus(k, off), kIdescS, kk > 0 ? 1u : 0u);
     }
-    mma_commit(smem_u32(&m.s_full));
+    commit_to(chosen, &m.s_full);
     return true;
   };
   auto values = [&](int j) -> bool {
     const int st = j % C::kVStages;
-    if (!mbar_wait(smem_u32(&m.v_full[st]), j / C::kVStages & 1, deadline, ab)) return false;
+    if (!warp_wait(smem_u32(&m.v_full[st]), j / C::kVStages & 1, deadline, ab)) return false;
     const uint64_t v = desc_plus(v_desc, st * C::kVBytes);
 #pragma unroll
     for (int kk = 0; kk < kMhaDv / 16; ++kk)
-      mma_bf16_ts(tmem + C::kT, tmem + C::kDo + 8 * kk, desc_plus(v, (kk >> 2) * kMhaUnit + (kk & 3) * 32), kIdescS,
+      mma_ts(chosen, C::kT, C::kDo + 8 * kk, desc_plus(v, (kk >> 2) * kMhaUnit + (kk & 3) * 32), kIdescS,
                   kk > 0 ? 1u : 0u);
-    mma_commit(smem_u32(&m.v_empty[st]));
-    mma_commit(smem_u32(&m.t_full));
+    commit_to(chosen, &m.v_empty[st]);
+    commit_to(chosen, &m.t_full);
     return true;
   };
-  if (!mbar_wait(smem_u32(&m.q_full), 0, deadline, ab)) return false;
+  if (!warp_wait(smem_u32(&m.q_full), 0, deadline, ab)) return false;
   if (!scores(0)) return false;
-  if (!mbar_wait(smem_u32(&m.do_ready), 0, deadline, ab)) return false;
+  if (!warp_wait(smem_u32(&m.do_ready), 0, deadline, ab)) return false;
   tc_fence_after();
   if (!values(0)) return false;
   if (blocks > 1) {
-    if (!mbar_wait(smem_u32(&m.s_free), 0, deadline, ab)) return false;
+    if (!warp_wait(smem_u32(&m.s_free), 0, deadline, ab)) return false;
     tc_fence_after();
     if (!scores(1)) return false;
   }
   for (int j = 0; j < blocks; ++j) {
-    if (!mbar_wait(smem_u32(&m.ds_full), j & 1, deadline, ab)) return false;
+    if (!warp_wait(smem_u32(&m.ds_full), j & 1, deadline, ab)) return false;
     tc_fence_after();
     const int st = j % C::kKStages;
     const uint64_t k = desc_plus(kt_desc, st * C::kKBytes);
 #pragma unroll
     for (int kk = 0; kk < kMhaTile / 16; ++kk)   // either half's dS is in its own columns
-      mma_bf16_ts(tmem + C::kDq, tmem + C::kT + 64 * (kk >> 2) + 8 * (kk & 3), desc_plus(k, kk * 2048), kIdescQ,
+      mma_ts(chosen, C::kDq, C::kT + 64 * (kk >> 2) + 8 * (kk & 3), desc_plus(k, kk * 2048), kIdescQ,
                   j + kk > 0 ? 1u : 0u);
-    mma_commit(smem_u32(&m.k_empty[st]));
+    commit_to(chosen, &m.k_empty[st]);
     if (j + 1 < blocks && !values(j + 1)) return false;
     if (j + 2 < blocks) {
-      if (!mbar_wait(smem_u32(&m.s_free), (j + 1) & 1, deadline, ab)) return false;
+      if (!warp_wait(smem_u32(&m.s_free), (j + 1) & 1, deadline, ab)) return false;
       tc_fence_after();
       if (!scores(j + 2)) return false;
     }
   }
-  mma_commit(smem_u32(&m.dq_full));
+  commit_to(chosen, &m.dq_full);
   return true;
 }
 
@@ -363,13 +364,13 @@ __global__ void __launch_bounds__(MhaDqShape<DQK>::kThreads, 1) dense_mha_dq_ker
     const int never = 0;
     if (warp < 8) {
       if (!mha_dq_rows<DQK>(p, m, sb, tmem, w, t0, blocks, pack0)) mha_bwd_raise(m, kErrMhaDqRowsWait);
+    } else if (warp == 8 && blocks > 0) {
+      if (!mha_dq_mma<DQK>(p, m, sb, blocks)) mha_bwd_raise(m, kErrMhaDqMmaWait);
+      commit_to(elect_one(), &m.drain);   // every MMA issued completes before TMEM is freed
+      mbar_wait(smem_u32(&m.drain), 0, global_timer_ns() + 100000000ull, &never);
     } else if (blocks > 0) {
       if (lane_id() == 0) {
-        if (warp == 8) {
-          if (!mha_dq_mma<DQK>(p, m, sb, tmem, blocks)) mha_bwd_raise(m, kErrMhaDqMmaWait);
-          mma_commit(smem_u32(&m.drain));   // every MMA issued completes before TMEM is freed
-          mbar_wait(smem_u32(&m.drain), 0, global_timer_ns() + 100000000ull, &never);
-        } else {
+        {
           int kf = 0, vf = 0;
           if (!mha_dq_load<DQK>(p, m, sb, w, t0, blocks, pack0, kf, vf)) mha_bwd_raise(m, kErrMhaDqLoadWait);
           // every copy issued has landed before the CTA exits
@@ -473,7 +474,7 @@ __device__ __forceinline__ bool mha_dkv_load(const MhaBwdParams& p, MhaDkvMisc& 
 }
 
 template <int DQK>
-__device__ __forceinline__ bool mha_dkv_mma(const MhaBwdParams& p, MhaDkvMisc& m, uint32_t sb, uint32_t tmem, int total) {
+__device__ __forceinline__ bool mha_dkv_mma(const MhaBwdParams& p, MhaDkvMisc& m, uint32_t sb, int total) {
   using C = MhaDkvShape<DQK>;
   constexpr uint32_t kIdescS = idesc_bf16_f32(kMhaTile, C::kN, false, false);
   constexpr uint32_t kIdescV = idesc_bf16_f32(kMhaTile, kMhaDv, false, true);
@@ -482,32 +483,33 @@ __device__ __forceinline__ bool mha_dkv_mma(const MhaBwdParams& p, MhaDkvMisc& m
                  q_desc = smem_desc(sb + C::kQOff, 16, 1024, SWZ_128B), g_desc = smem_desc(sb + C::kDoOff, 16, 1024, SWZ_128B),
                  qt_desc = smem_desc(sb + C::kQOff, C::kQUnit, 1024, SWZ_128B),    // their rows as columns
                  gt_desc = smem_desc(sb + C::kDoOff, C::kQUnit, 1024, SWZ_128B);
+  const uint32_t chosen = elect_one();
   const volatile int* ab = &m.abort_flag;
   const uint64_t deadline = global_timer_ns() + p.timeout_ns;
   auto scores = [&](int j) -> bool {
     const int st = j % C::kStages;
-    if (!mbar_wait(smem_u32(&m.q_full[st]), j / C::kStages & 1, deadline, ab)) return false;
+    if (!warp_wait(smem_u32(&m.q_full[st]), j / C::kStages & 1, deadline, ab)) return false;
     const uint64_t q = desc_plus(q_desc, st * C::kQBytes);
 #pragma unroll
     for (int kk = 0; kk < DQK / 16; ++kk)
-      mma_bf16_ss(tmem + C::kS, desc_plus(k_desc, (kk >> 2) * kMhaUnit + (kk & 3) * 32),
+      mma_ss(chosen, C::kS, desc_plus(k_desc, (kk >> 2) * kMhaUnit + (kk & 3) * 32),
                   desc_plus(q, (kk >> 2) * C::kQUnit + (kk & 3) * 32), kIdescS, kk > 0 ? 1u : 0u);
-    mma_commit(smem_u32(&m.s_full));
+    commit_to(chosen, &m.s_full);
     return true;
   };
   auto values = [&](int j) -> bool {
     const int st = j % C::kStages;
-    if (!mbar_wait(smem_u32(&m.do_full[st]), j / C::kStages & 1, deadline, ab)) return false;
+    if (!warp_wait(smem_u32(&m.do_full[st]), j / C::kStages & 1, deadline, ab)) return false;
     const uint64_t g = desc_plus(g_desc, st * C::kDoBytes);
 #pragma unroll
     for (int kk = 0; kk < kMhaDv / 16; ++kk) {
       const uint64_t b = desc_plus(g, (kk >> 2) * C::kQUnit + (kk & 3) * 32);
       if (C::kVTmem)
-        mma_bf16_ts(tmem + C::kT, tmem + C::kV + 8 * kk, b, kIdescS, kk > 0 ? 1u : 0u);
+        mma_ts(chosen, C::kT, C::kV + 8 * kk, b, kIdescS, kk > 0 ? 1u : 0u);
       else
-        mma_bf16_ss(tmem + C::kT, desc_plus(v_desc, (kk >> 2) * kMhaUnit + (kk & 3) * 32), b, kIdescS, kk > 0 ? 1u : 0u);
+        mma_ss(chosen, C::kT, desc_plus(v_desc, (kk >> 2) * kMhaUnit + (kk & 3) * 32), b, kIdescS, kk > 0 ? 1u : 0u);
     }
-    mma_commit(smem_u32(&m.t_full));
+    commit_to(chosen, &m.t_full);
     return true;
   };
   // either half's P^T and dS^T are at the start of its own columns
@@ -515,34 +517,34 @@ __device__ __forceinline__ bool mha_dkv_mma(const MhaBwdParams& p, MhaDkvMisc& m
     constexpr int kHalf = C::kN / 32;
     return static_cast<uint32_t>(kk < kHalf ? 8 * kk : C::kN / 2 + 8 * (kk - kHalf));
   };
-  if (!mbar_wait(smem_u32(&m.k_full), 0, deadline, ab)) return false;
+  if (!warp_wait(smem_u32(&m.k_full), 0, deadline, ab)) return false;
   if (!scores(0)) return false;
   if (C::kVTmem) {
-    if (!mbar_wait(smem_u32(&m.v_ready), 0, deadline, ab)) return false;
+    if (!warp_wait(smem_u32(&m.v_ready), 0, deadline, ab)) return false;
     tc_fence_after();
   }
   if (!values(0)) return false;
   for (int j = 0; j < total; ++j) {
     const int st = j % C::kStages;
-    if (!mbar_wait(smem_u32(&m.p_full), j & 1, deadline, ab)) return false;
+    if (!warp_wait(smem_u32(&m.p_full), j & 1, deadline, ab)) return false;
     tc_fence_after();
     const uint64_t g = desc_plus(gt_desc, st * C::kDoBytes), q = desc_plus(qt_desc, st * C::kQBytes);
 #pragma unroll
     for (int kk = 0; kk < C::kN / 16; ++kk)
-      mma_bf16_ts(tmem + C::kDv, tmem + C::kS + step_at(kk), desc_plus(g, kk * 2048), kIdescV,
+      mma_ts(chosen, C::kDv, C::kS + step_at(kk), desc_plus(g, kk * 2048), kIdescV,
                   j + kk > 0 ? 1u : 0u);
-    mma_commit(smem_u32(&m.do_empty[st]));
+    commit_to(chosen, &m.do_empty[st]);
     if (j + 1 < total && !scores(j + 1)) return false;
-    if (!mbar_wait(smem_u32(&m.ds_full), j & 1, deadline, ab)) return false;
+    if (!warp_wait(smem_u32(&m.ds_full), j & 1, deadline, ab)) return false;
     tc_fence_after();
 #pragma unroll
     for (int kk = 0; kk < C::kN / 16; ++kk)
-      mma_bf16_ts(tmem + C::kDk, tmem + C::kT + step_at(kk), desc_plus(q, kk * 2048), kIdescK,
+      mma_ts(chosen, C::kDk, C::kT + step_at(kk), desc_plus(q, kk * 2048), kIdescK,
                   j + kk > 0 ? 1u : 0u);
-    mma_commit(smem_u32(&m.q_empty[st]));
+    commit_to(chosen, &m.q_empty[st]);
     if (j + 1 < total && !values(j + 1)) return false;
   }
-  mma_commit(smem_u32(&m.out_full));
+  commit_to(chosen, &m.out_full);
   return true;
 }
 
@@ -771,12 +773,12 @@ __global__ void __launch_bounds__(MhaDkvShape<DQK>::kThreads, 1) dense_mha_dkv_k
     } else if (s.total > 0) {
       if (warp == 10) {
         if (!mha_dkv_stats<DQK>(p, m, w, s, kvh)) mha_bwd_raise(m, kErrMhaDkvStatWait);
+      } else if (warp == 8) {
+        if (!mha_dkv_mma<DQK>(p, m, sb, s.total)) mha_bwd_raise(m, kErrMhaDkvMmaWait);
+        commit_to(elect_one(), &m.drain);   // every MMA issued completes before TMEM is freed
+        mbar_wait(smem_u32(&m.drain), 0, global_timer_ns() + 100000000ull, &never);
       } else if (lane_id() == 0) {
-        if (warp == 8) {
-          if (!mha_dkv_mma<DQK>(p, m, sb, tmem, s.total)) mha_bwd_raise(m, kErrMhaDkvMmaWait);
-          mma_commit(smem_u32(&m.drain));   // every MMA issued completes before TMEM is freed
-          mbar_wait(smem_u32(&m.drain), 0, global_timer_ns() + 100000000ull, &never);
-        } else {
+        {
           int qf = 0, df = 0;
           if (!mha_dkv_load<DQK>(p, m, sb, w, s, kvh, qf, df)) mha_bwd_raise(m, kErrMhaDkvLoadWait);
           // every copy issued has landed before the CTA exits

@@ -45,7 +45,7 @@ namespace smla {
 constexpr int kMhaTile = 128;              // query rows of a tile, keys of a block
 constexpr int kMhaDv = 128;
 constexpr int kMhaMaxCluster = 16;
-constexpr uint32_t kMhaUnit = 16384;       // bytes of 64 columns of 128 rows
+constexpr uint32_t kMhaUnit = 16384;       // bytes of a ring unit, and of 64 columns of a Q tile
 constexpr float kMhaLazy = 8.f;            // log2 of the growth of a maximum that O is rescaled for
 
 enum MhaErrCode : int {
@@ -217,15 +217,56 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, int 
       : "memory");
 }
 
-// D[tmem] (+)= A[tmem] * B[smem]: A's row i in lane i, two bf16 values per column.
-__device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                            uint32_t accumulate) {
+// Products are issued by a whole warp of which one thread is chosen: control and addresses
+// are then the same for all of its threads, and the compiler keeps them in the registers
+// that the instruction takes them from (one thread by itself needed 60 to 90 cycles more
+// for each product, about as long as the product takes).
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t chosen;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(chosen));
+  return chosen;
+}
+
+// mbar_wait by all threads of a warp, with the same result for all.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint64_t deadline_ns,
+                                          const volatile int* abort_flag) {
+  while (!__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) {
+    if (__any_sync(0xffffffffu, *abort_flag != 0 || global_timer_ns() > deadline_ns)) return false;
+  }
+  return true;
+}
+
+// D[tmem] (+)= A * B[smem] by the chosen thread, A in shared memory or (a row per lane, two
+// bf16 values per column) in TMEM.
+__device__ __forceinline__ void mma_ss(uint32_t chosen, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                       uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
-      ::"r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+      ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(chosen) : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t chosen, uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                       uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+      ::"r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(chosen) : "memory");
+}
+// Arrive on an mbarrier when every product that the chosen thread has issued so far has completed.
+__device__ __forceinline__ void commit_to(uint32_t chosen, uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}"
+      ::"r"(smem_u32(bar)), "r"(chosen) : "memory");
 }
 
 // The descriptor of an operand `bytes` further on in shared memory (below 256 KB, so the
@@ -305,63 +346,6 @@ __device__ __forceinline__ void tmem_load128(uint32_t taddr, float* v) {
       : "r"(taddr));
 }
 
-// ---- two CTAs that share their products (cta_group::2): M = 256, either CTA's 128 rows of A and
-// of D, and half of B, in its own memory; the even CTA of the pair issues
-__device__ __forceinline__ void tmem_alloc_pair(uint32_t dst_smem, uint32_t ncols) {
-  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem), "r"(ncols) : "memory");
-}
-__device__ __forceinline__ void tmem_relinquish_pair() {
-  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
-  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
-}
-__device__ __forceinline__ void mma_pair_bf16_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                                 uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
-      ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-__device__ __forceinline__ void mma_pair_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                                 uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
-      ::"r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-// Arrive on the mbarrier at this address in both CTAs when every product issued so far has completed.
-__device__ __forceinline__ void mma_commit_pair(uint32_t bar) {
-  asm volatile(
-      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
-      ::"r"(bar), "h"(static_cast<uint16_t>(3))
-      : "memory");
-}
-// Arrive on a barrier of another CTA of the cluster (an address of cluster_addr's).
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
-}
-// mbar_wait for a barrier that another CTA arrives on.
-__device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity, uint64_t deadline_ns,
-                                                  const volatile int* abort_flag) {
-  for (;;) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity), "r"(200000u)
-        : "memory");
-    if (ok) return true;
-    if (*abort_flag || global_timer_ns() > deadline_ns) return false;
-  }
-}
-
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -392,12 +376,11 @@ __device__ __forceinline__ void add2(float& a0, float& a1, float b0, float b1) {
 
 // ------------------------------------------------------------------ forward
 
-constexpr int kMhaMaxUnits = 18;
-constexpr int kMhaFree = 6;   // a block's release is told on one of so many barriers in turn: more than the ring has blocks
+constexpr int kMhaMaxUnits = 12;
+constexpr int kMhaFree = 4;   // a block's release is told on one of so many barriers in turn: more than the ring has blocks
 
 struct __align__(16) MhaMisc {
   uint64_t q_full[2], full[kMhaMaxUnits], k_free[kMhaFree], v_free[kMhaFree], s_full[2], p_full[2], o_full[2], o_step, drain;
-  uint64_t peer_q[2], peer_k[kMhaFree], peer_v[kMhaFree];   // a pair: the other CTA's copies have landed
   uint32_t tmem_base;
   int abort_flag;
   int prior_error;
@@ -408,15 +391,14 @@ struct __align__(16) MhaMisc {
 constexpr int kMhaPartRow = kMhaDv + 4;   // floats of a row that is joined; neighbours in other banks
 
 // Shared memory: Q (NT tiles), then the ring.
-template <int DQK, int NT, bool PAIR>
+template <int DQK, int NT>
 struct MhaFwdShape {
   static constexpr int kSub = DQK / 64;                        // 64-column units of a K block or Q tile
   static constexpr uint32_t kQBytes = NT * kSub * kMhaUnit;
   static constexpr int kFree = kMaxSmem - 1024 - static_cast<int>(sizeof(MhaMisc)) - static_cast<int>(kQBytes);
-  static constexpr uint32_t kUnit = PAIR ? kMhaUnit / 2 : kMhaUnit;   // bytes of a ring unit
-  static constexpr int kFit = kFree / static_cast<int>(kUnit), kMost = PAIR ? kMhaMaxUnits : 12;
-  static constexpr int kUnits = kFit < kMost ? kFit : kMost;
-  static constexpr uint32_t kMiscOff = kQBytes + kUnits * kUnit;
+  static constexpr int kFit = kFree / static_cast<int>(kMhaUnit);
+  static constexpr int kUnits = kFit < kMhaMaxUnits ? kFit : kMhaMaxUnits;
+  static constexpr uint32_t kMiscOff = kQBytes + kUnits * kMhaUnit;
   static constexpr int kBytes = static_cast<int>(kMiscOff) + static_cast<int>(sizeof(MhaMisc)) + 1024;
   static constexpr int kAhead = NT == 1 ? 2 : 1;               // key blocks whose scores are ahead of the weights
   static constexpr int kThreads = NT * 128 + 64;               // two tiles: 200 registers each, no more than their rows take
@@ -424,26 +406,24 @@ struct MhaFwdShape {
   static constexpr uint32_t kO = 256;                          // columns of TMEM: two S of 128 each, then O
   static_assert(kUnits >= kSub + 4, "a K block and two V blocks");
   static_assert(kBytes <= kMaxSmem, "shared memory");
-  static_assert(kUnits * kUnit >= kMhaTile * kMhaPartRow * 4, "rows that are joined");
+  static_assert(kUnits * kMhaUnit >= kMhaTile * kMhaPartRow * 4, "rows that are joined");
 };
 
 // What one CTA does: keys' blocks of each of its tiles.
-template <int NT, bool PAIR>
+template <int NT>
 struct MhaSpan {
-  int low[NT];     // first token of the product's rows, in the sequence (of a pair of CTAs: of the first's)
-  int t0[NT];      // of this CTA's
-  int blocks[NT];  // blocks of 128 keys that the product's rows see (of which this CTA takes them)
+  int t0[NT];      // first token of the tile, in the sequence
+  int blocks[NT];  // blocks of 128 keys that its rows see (of which this CTA takes them)
   int from;        // the first of them
   int most;
   __device__ __forceinline__ MhaSpan(const MhaFwdParams& p, const MhaWork& w, int rank) {
-    const int lq = w.q1 - w.q0, lk = w.k1 - w.k0, rows = (PAIR ? 2 : 1) * p.tok_tile;
+    const int lq = w.q1 - w.q0, lk = w.k1 - w.k0;
     most = 0;
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      low[t] = (w.tile * NT + t) * rows;
-      t0[t] = low[t] + (PAIR ? rank * p.tok_tile : 0);
-      const int last = min(low[t] + rows, lq) - 1;
-      const int sees = low[t] < lq ? last + lk - lq + 1 : 0;   // of its last row
+      t0[t] = (w.tile * NT + t) * p.tok_tile;
+      const int last = min(t0[t] + p.tok_tile, lq) - 1;
+      const int sees = t0[t] < lq ? last + lk - lq + 1 : 0;   // of its last row
       blocks[t] = sees > 0 ? (sees + kMhaTile - 1) / kMhaTile : 0;
       most = max(most, blocks[t]);
     }
@@ -491,10 +471,10 @@ struct MhaOrder {
   }
 };
 
-template <int DQK, int NT, bool PAIR>
+template <int DQK, int NT>
 __device__ __forceinline__ bool mha_load(const MhaFwdParams& p, MhaMisc& m, uint32_t sb, const MhaWork& w,
-                                         const MhaSpan<NT, PAIR>& s, int pack0, int kvh, int rank, uint32_t& fills) {
-  using C = MhaFwdShape<DQK, NT, PAIR>;
+                                         const MhaSpan<NT>& s, int pack0, int kvh, uint32_t& fills) {
+  using C = MhaFwdShape<DQK, NT>;
   const volatile int* ab = &m.abort_flag;
   const uint64_t deadline = global_timer_ns() + p.timeout_ns;
   auto load_q = [&](int t) {
@@ -519,16 +499,14 @@ __device__ __forceinline__ bool mha_load(const MhaFwdParams& p, MhaMisc& m, uint
         }
         --old_left;
       }
-      const uint32_t bar = smem_u32(&m.full[r.at]), dst = sb + C::kQBytes + r.at * C::kUnit;
+      const uint32_t bar = smem_u32(&m.full[r.at]), dst = sb + C::kQBytes + r.at * kMhaUnit;
       const int row = w.k0 + (s.from + now.block) * kMhaTile;
-      mbar_arrive_expect_tx(bar, C::kUnit);
-      if (!now.value) {   // a pair: its half of the keys
-        tma_load_3d(dst, &p.map_k, 64 * c, kvh, row + (PAIR ? 64 * rank : 0), bar);
-      } else if (PAIR) {  // its half of the columns
-        tma_load_3d(dst, &p.map_v, 64 * rank, kvh, row + 64 * c, bar);
-      } else {
+      mbar_arrive_expect_tx(bar, kMhaUnit);
+      if (now.value) {
         tma_load_3d(dst, &p.map_v, 0, kvh, row + 64 * c, bar);
         tma_load_3d(dst + kMhaUnit / 2, &p.map_v, 64, kvh, row + 64 * c, bar);
+      } else {
+        tma_load_3d(dst, &p.map_k, 64 * c, kvh, row, bar);
       }
       ++fills;
       r.next();
@@ -539,37 +517,33 @@ __device__ __forceinline__ bool mha_load(const MhaFwdParams& p, MhaMisc& m, uint
   return true;
 }
 
-template <int DQK, int NT, bool PAIR>
-__device__ __forceinline__ bool mha_mma(const MhaFwdParams& p, MhaMisc& m, uint32_t sb, uint32_t tmem,
-                                        const MhaSpan<NT, PAIR>& s) {
-  using C = MhaFwdShape<DQK, NT, PAIR>;
-  constexpr int kRows = PAIR ? 2 * kMhaTile : kMhaTile;
-  constexpr uint32_t kIdescS = idesc_bf16_f32(kRows, kMhaTile, false, false);
-  constexpr uint32_t kIdescO = idesc_bf16_f32(kRows, kMhaDv, false, true);
+template <int DQK, int NT>
+__device__ __forceinline__ bool mha_mma(const MhaFwdParams& p, MhaMisc& m, uint32_t sb,
+                                        const MhaSpan<NT>& s) {
+  using C = MhaFwdShape<DQK, NT>;
+  constexpr uint32_t kIdescS = idesc_bf16_f32(kMhaTile, kMhaTile, false, false);
+  constexpr uint32_t kIdescO = idesc_bf16_f32(kMhaTile, kMhaDv, false, true);
   const volatile int* ab = &m.abort_flag;
   const uint64_t deadline = global_timer_ns() + p.timeout_ns;
-  auto commit = [&](uint64_t* bar) {
-    if (PAIR) mma_commit_pair(smem_u32(bar));
-    else mma_commit(smem_u32(bar));
-  };
+  const uint32_t chosen = elect_one();
+  auto commit = [&](uint64_t* bar) { commit_to(chosen, bar); };
   const uint64_t q_desc = smem_desc(sb, 16, 1024, SWZ_128B), k_desc = smem_desc(sb + C::kQBytes, 16, 1024, SWZ_128B),
                  v_desc = smem_desc(sb + C::kQBytes, kMhaUnit / 2, 1024, SWZ_128B);
+  // TMEM is taken whole, so its columns start at 0
   MhaRing<C::kUnits> r;   // the units in the order of their use
   auto wait_unit = [&](const MhaRing<C::kUnits>& u) -> bool {
-    return mbar_wait(smem_u32(&m.full[u.at]), u.turn, deadline, ab);
+    return warp_wait(smem_u32(&m.full[u.at]), u.turn, deadline, ab);
   };
   // S (columns `to`, barrier `bar`) = Q_t K^T of block j at `u`; `first`: its units have not been waited for, `last`:
   // they are free behind it
   auto scores = [&](int t, uint32_t to, uint64_t* bar, int j, MhaRing<C::kUnits> u, bool first, bool last) -> bool {
-    if (PAIR && first && !mbar_wait_cluster(smem_u32(&m.peer_k[j % kMhaFree]), j / kMhaFree & 1, deadline, ab)) return false;
 #pragma unroll
     for (int c = 0; c < C::kSub; ++c) {
       if (first && !wait_unit(u)) return false;
-      const uint64_t a = desc_plus(q_desc, (t * C::kSub + c) * kMhaUnit), b = desc_plus(k_desc, u.at * C::kUnit);
+      const uint64_t a = desc_plus(q_desc, (t * C::kSub + c) * kMhaUnit), b = desc_plus(k_desc, u.at * kMhaUnit);
 #pragma unroll
       for (int kk = 0; kk < 4; ++kk)
-        if (PAIR) mma_pair_bf16_ss(tmem + to, desc_plus(a, kk * 32), desc_plus(b, kk * 32), kIdescS, c + kk > 0 ? 1u : 0u);
-        else mma_bf16_ss(tmem + to, desc_plus(a, kk * 32), desc_plus(b, kk * 32), kIdescS, c + kk > 0 ? 1u : 0u);
+        mma_ss(chosen, to, desc_plus(a, kk * 32), desc_plus(b, kk * 32), kIdescS, c + kk > 0 ? 1u : 0u);
       u.next();
     }
     commit(bar);
@@ -578,17 +552,14 @@ __device__ __forceinline__ bool mha_mma(const MhaFwdParams& p, MhaMisc& m, uint3
   };
   // O_t += P (columns `from`) V of block j at `u`
   auto weighted = [&](int t, uint32_t from, int j, MhaRing<C::kUnits> u, bool first, bool last) -> bool {
-    if (PAIR && first && !mbar_wait_cluster(smem_u32(&m.peer_v[j % kMhaFree]), j / kMhaFree & 1, deadline, ab)) return false;
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
       if (first && !wait_unit(u)) return false;
-      const uint64_t b = desc_plus(v_desc, u.at * C::kUnit);
+      const uint64_t b = desc_plus(v_desc, u.at * kMhaUnit);
 #pragma unroll
-      for (int kk = 0; kk < 4; ++kk) {
-        const uint32_t o = tmem + C::kO + t * kMhaDv, w = tmem + from + 8 * (4 * c + kk), more = j + c + kk > 0 ? 1u : 0u;
-        if (PAIR) mma_pair_bf16_ts(o, w, desc_plus(b, kk * 2048), kIdescO, more);
-        else mma_bf16_ts(o, w, desc_plus(b, kk * 2048), kIdescO, more);
-      }
+      for (int kk = 0; kk < 4; ++kk)
+        mma_ts(chosen, C::kO + t * kMhaDv, from + 8 * (4 * c + kk), desc_plus(b, kk * 2048), kIdescO,
+                     j + c + kk > 0 ? 1u : 0u);
       u.next();
     }
     if (last) commit(&m.v_free[j % kMhaFree]);
@@ -597,17 +568,17 @@ __device__ __forceinline__ bool mha_mma(const MhaFwdParams& p, MhaMisc& m, uint3
   if constexpr (NT == 1) {
     // two S in turn: block j + 2's scores follow block j's weights, so that a block's are there when the softmax has done
     // the one before
-    if (!mbar_wait(smem_u32(&m.q_full[0]), 0, deadline, ab)) return false;
+    if (!warp_wait(smem_u32(&m.q_full[0]), 0, deadline, ab)) return false;
     for (int j = 0; j < 2 && j < s.most; ++j) {
       if (!scores(0, kMhaTile * j, &m.s_full[j], j, r, true, true)) return false;
       r.skip(C::kSub);
     }
     for (int j = 0; j < s.most; ++j) {
       const int buf = j & 1;
-      if (!mbar_wait(smem_u32(&m.p_full[buf]), j >> 1 & 1, deadline, ab)) return false;
+      if (!warp_wait(smem_u32(&m.p_full[buf]), j >> 1 & 1, deadline, ab)) return false;
       tc_fence_after();
       if (!weighted(0, kMhaTile * buf, j, r, true, true)) return false;
-      mma_commit(smem_u32(j + 1 < s.most ? &m.o_step : &m.o_full[0]));
+      commit(j + 1 < s.most ? &m.o_step : &m.o_full[0]);
       r.skip(2);
       if (j + 2 < s.most) {
         if (!scores(0, kMhaTile * buf, &m.s_full[buf], j + 2, r, true, true)) return false;
@@ -618,8 +589,7 @@ __device__ __forceinline__ bool mha_mma(const MhaFwdParams& p, MhaMisc& m, uint3
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
       if (s.blocks[t] == 0) continue;
-      if (!mbar_wait(smem_u32(&m.q_full[t]), 0, deadline, ab)) return false;
-      if (PAIR && !mbar_wait_cluster(smem_u32(&m.peer_q[t]), 0, deadline, ab)) return false;
+      if (!warp_wait(smem_u32(&m.q_full[t]), 0, deadline, ab)) return false;
       const bool alone = s.blocks[1 - t] == 0;
       if (!scores(t, kMhaTile * t, &m.s_full[t], 0, r, t == 0 || alone, t == 1 || alone)) return false;
     }
@@ -631,9 +601,7 @@ __device__ __forceinline__ bool mha_mma(const MhaFwdParams& p, MhaMisc& m, uint3
       for (int t = 0; t < 2; ++t) {
         if (j >= s.blocks[t]) continue;
         const bool alone = j >= s.blocks[1 - t], alone_k = j + 1 >= s.blocks[1 - t];
-        if (PAIR ? !mbar_wait_cluster(smem_u32(&m.p_full[t]), j & 1, deadline, ab)
-                 : !mbar_wait(smem_u32(&m.p_full[t]), j & 1, deadline, ab))
-          return false;
+        if (!warp_wait(smem_u32(&m.p_full[t]), j & 1, deadline, ab)) return false;
         tc_fence_after();
         if (!weighted(t, kMhaTile * t, j, r, t == 0 || alone, t == 1 || alone)) return false;
         if (j + 1 == s.blocks[t]) commit(&m.o_full[t]);
@@ -642,34 +610,6 @@ __device__ __forceinline__ bool mha_mma(const MhaFwdParams& p, MhaMisc& m, uint3
       r = rk;
       if (j + 1 < s.most) r.skip(C::kSub);
     }
-  }
-  return true;
-}
-
-// The second CTA of a pair tells the first, which issues the products of both, that its
-// own copies have landed.
-template <int DQK>
-__device__ __forceinline__ bool mha_tell_peer(const MhaFwdParams& p, MhaMisc& m, const MhaSpan<2, true>& s) {
-  using C = MhaFwdShape<DQK, 2, true>;
-  const volatile int* ab = &m.abort_flag;
-  const uint64_t deadline = global_timer_ns() + p.timeout_ns;
-  MhaRing<C::kUnits> r;
-  MhaOrder now;
-  auto tell_q = [&](int t) -> bool {
-    if (s.blocks[t] == 0) return true;
-    if (!mbar_wait(smem_u32(&m.q_full[t]), 0, deadline, ab)) return false;
-    mbar_arrive_cluster(cluster_addr(smem_u32(&m.peer_q[t]), 0));
-    return true;
-  };
-  if (!tell_q(0)) return false;
-  for (int n = 0; n < 2 * s.most; ++n) {
-    for (int c = 0; c < (now.value ? 2 : C::kSub); ++c) {
-      if (!mbar_wait(smem_u32(&m.full[r.at]), r.turn, deadline, ab)) return false;
-      r.next();
-    }
-    mbar_arrive_cluster(cluster_addr(smem_u32(now.value ? &m.peer_v[now.block % kMhaFree] : &m.peer_k[now.block % kMhaFree]), 0));
-    if (n == 0 && !tell_q(1)) return false;
-    now.next(C::kAhead, s.most);
   }
   return true;
 }
@@ -705,10 +645,10 @@ __device__ __forceinline__ bool mha_clear(uint32_t tile, uint32_t bytes) {
 }
 
 // One thread per row of tile t.
-template <int DQK, int NT, bool PAIR>
+template <int DQK, int NT>
 __device__ __forceinline__ bool mha_softmax(const MhaFwdParams& p, MhaMisc& m, uint8_t* sbase, uint32_t sb, uint32_t tmem,
-                                            const MhaWork& w, const MhaSpan<NT, PAIR>& s, int pack0, int t) {
-  using C = MhaFwdShape<DQK, NT, PAIR>;
+                                            const MhaWork& w, const MhaSpan<NT>& s, int pack0, int t) {
+  using C = MhaFwdShape<DQK, NT>;
   const volatile int* ab = &m.abort_flag;
   const uint64_t deadline = global_timer_ns() + p.timeout_ns;
   const int row = static_cast<int>(threadIdx.x) & 127;
@@ -716,7 +656,7 @@ __device__ __forceinline__ bool mha_softmax(const MhaFwdParams& p, MhaMisc& m, u
   const int tok = s.t0[t] + row / p.pack;
   const bool live = row < p.pack * p.tok_tile && tok < lq;
   const int blocks = s.blocks[t];
-  const int whole = max(0, s.low[t] + lk - lq + 1) / kMhaTile - s.from;   // blocks that every row sees all of
+  const int whole = max(0, s.t0[t] + lk - lq + 1) / kMhaTile - s.from;   // blocks that every row sees all of
   const uint32_t quarter = static_cast<uint32_t>((row >> 5) * 32) << 16;
   const uint32_t to = tmem + quarter + C::kO + t * kMhaDv;
   const float c = p.scale_log2;
@@ -728,7 +668,7 @@ __device__ __forceinline__ bool mha_softmax(const MhaFwdParams& p, MhaMisc& m, u
       for (int i = 0; i < 2; ++i) {   // the block's V: units behind those of the K before it and of the V before it
         const uint32_t n = static_cast<uint32_t>(min(j + C::kAhead, s.most) * C::kSub + 2 * j + i);
         if (!mbar_wait(smem_u32(&m.full[n % C::kUnits]), n / C::kUnits & 1u, deadline, ab)) return false;
-        if (mha_clear(sb + C::kQBytes + n % C::kUnits * C::kUnit, C::kUnit)) m.cleared = 1;
+        if (mha_clear(sb + C::kQBytes + n % C::kUnits * kMhaUnit, kMhaUnit)) m.cleared = 1;
       }
     }
     if (!mbar_wait(smem_u32(&m.s_full[buf]), par, deadline, ab)) return false;
@@ -788,10 +728,7 @@ __device__ __forceinline__ bool mha_softmax(const MhaFwdParams& p, MhaMisc& m, u
     tmem_wait_st();
     tc_fence_before();
     __syncwarp();
-    if (lane_id() == 0) {
-      if (PAIR) mbar_arrive_cluster(cluster_addr(smem_u32(&m.p_full[buf]), 0));
-      else mbar_arrive(smem_u32(&m.p_full[buf]));
-    }
+    if (lane_id() == 0) mbar_arrive(smem_u32(&m.p_full[buf]));
     add2(add[0], add[1], add[2], add[3]);
     add2(add[4], add[5], add[6], add[7]);
     add2(add[0], add[1], add[4], add[5]);
@@ -825,13 +762,9 @@ __device__ __forceinline__ bool mha_softmax(const MhaFwdParams& p, MhaMisc& m, u
       for (int k = 0; k < 4; ++k) *reinterpret_cast<uint4*>(o + 32 * i + 8 * k) = pack8(x + 8 * k);
     }
   }
-  int cleared = blocks > 0 ? *reinterpret_cast<volatile int*>(&m.cleared) : 0;
-  if (PAIR && blocks > 0)   // half of the columns are the other CTA's
-    cleared |= __float_as_int(ld_cluster_f(cluster_addr(smem_u32(&m.cleared), 0))) |
-               __float_as_int(ld_cluster_f(cluster_addr(smem_u32(&m.cleared), 1)));
-  if (store_o && cleared) {
+  if (blocks > 0 && store_o && *reinterpret_cast<volatile int*>(&m.cleared)) {
     // columns where a key that the row sees is not finite, among the blocks that were looked over
-    const int first = max(max(0, s.low[0] + lk - lq + 1) / kMhaTile, s.from) * kMhaTile;
+    const int first = max(max(0, s.t0[0] + lk - lq + 1) / kMhaTile, s.from) * kMhaTile;
     const int end = min(tok + lk - lq + 1, (s.from + blocks) * kMhaTile);
     const __nv_bfloat16* values = p.v + w.k0 * p.v_tok + pack0 / p.group * p.v_head;
 #pragma unroll 1
@@ -857,7 +790,7 @@ __device__ __forceinline__ bool mha_softmax(const MhaFwdParams& p, MhaMisc& m, u
 template <int DQK, int W>
 __device__ __forceinline__ void mha_join(const MhaFwdParams& p, MhaMisc& m, uint32_t sb, const MhaWork& w, int t0, int rows,
                                          int pack0, int rank) {
-  using C = MhaFwdShape<DQK, 1, false>;
+  using C = MhaFwdShape<DQK, 1>;
   constexpr int kPerRow = kMhaDv / W, kRows = 128 / kPerRow;
   const int col = static_cast<int>(threadIdx.x) % kPerRow * W;
   for (int row = rank * kRows + static_cast<int>(threadIdx.x) / kPerRow; row < rows; row += kRows * p.cluster) {
@@ -900,17 +833,17 @@ __device__ __forceinline__ void mha_join(const MhaFwdParams& p, MhaMisc& m, uint
   }
 }
 
-template <int DQK, int NT, bool PAIR>
-__global__ void __launch_bounds__(MhaFwdShape<DQK, NT, PAIR>::kThreads, 1) dense_mha_fwd_kernel(
+template <int DQK, int NT>
+__global__ void __launch_bounds__(MhaFwdShape<DQK, NT>::kThreads, 1) dense_mha_fwd_kernel(
     const __grid_constant__ MhaFwdParams p) {
-  using C = MhaFwdShape<DQK, NT, PAIR>;
+  using C = MhaFwdShape<DQK, NT>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sbase = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   MhaMisc& m = *reinterpret_cast<MhaMisc*>(sbase + C::kMiscOff);
   const int warp = static_cast<int>(threadIdx.x >> 5);
   const uint32_t sb = smem_u32(sbase);
   // CTAs of a cluster are neighbours
-  const unsigned ctas = NT == 1 || PAIR ? static_cast<unsigned>(p.cluster) : 1u, unit = blockIdx.x / ctas;
+  const unsigned ctas = NT == 1 ? static_cast<unsigned>(p.cluster) : 1u, unit = blockIdx.x / ctas;
   const int rank = static_cast<int>(blockIdx.x % ctas);
   int slot, head;
   mha_unit(unit, p.slots, p.packs, p.packs_near, slot, head);
@@ -925,18 +858,10 @@ __global__ void __launch_bounds__(MhaFwdShape<DQK, NT, PAIR>::kThreads, 1) dense
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&m.q_full[i]), 1);
       mbar_init(smem_u32(&m.s_full[i]), 1);
-      mbar_init(smem_u32(&m.p_full[i]), PAIR ? 8 : 4);   // one arrival per softmax warp
+      mbar_init(smem_u32(&m.p_full[i]), 4);   // one arrival per softmax warp
       mbar_init(smem_u32(&m.o_full[i]), 1);
     }
     mbar_init(smem_u32(&m.o_step), 1);
-    if (PAIR) {
-      for (int i = 0; i < kMhaFree; ++i) {
-        mbar_init(smem_u32(&m.peer_k[i]), 1);
-        mbar_init(smem_u32(&m.peer_v[i]), 1);
-      }
-      mbar_init(smem_u32(&m.peer_q[0]), 1);
-      mbar_init(smem_u32(&m.peer_q[1]), 1);
-    }
     mbar_init(smem_u32(&m.drain), 1);
     m.abort_flag = 0;
     m.cleared = 0;
@@ -947,46 +872,35 @@ __global__ void __launch_bounds__(MhaFwdShape<DQK, NT, PAIR>::kThreads, 1) dense
     prefetch_tmap(&p.map_v);
   }
   if (warp == 4 * NT) {
-    if (PAIR) {
-      tmem_alloc_pair(smem_u32(&m.tmem_base), C::kTmemCols);
-      tmem_relinquish_pair();
-    } else {
-      tmem_alloc(smem_u32(&m.tmem_base), C::kTmemCols);
-      tmem_relinquish();
-    }
+    tmem_alloc(smem_u32(&m.tmem_base), C::kTmemCols);
+    tmem_relinquish();
   }
   if (warp == 4 * NT + 1) {
-    const MhaWork w = mha_find<false>(p.cu_q, p.cu_kv, p.batch, p.total_q, p.total_kv, slot,
-                                      (PAIR ? 2 : 1) * NT * p.tok_tile, p.fill != 0);
+    const MhaWork w = mha_find<false>(p.cu_q, p.cu_kv, p.batch, p.total_q, p.total_kv, slot, NT * p.tok_tile,
+                                      p.fill != 0);
     if (lane_id() == 0) m.work = w;
   }
   tc_fence_before();
   __syncthreads();
-  if (PAIR) cluster_sync();   // the other CTA's barriers are set up
   tc_fence_after();
   const uint32_t tmem = m.tmem_base;
   const MhaWork w = m.work;
 
   if (m.prior_error == 0 && w.q1 > w.q0) {
-    const MhaSpan<NT, PAIR> s(p, w, rank);
+    const MhaSpan<NT> s(p, w, rank);
     if (warp < 4 * NT) {
-      if (!mha_softmax<DQK, NT, PAIR>(p, m, sbase, sb, tmem, w, s, pack0, warp >> 2)) mha_raise(m, kErrMhaSoftmaxWait);
+      if (!mha_softmax<DQK, NT>(p, m, sbase, sb, tmem, w, s, pack0, warp >> 2)) mha_raise(m, kErrMhaSoftmaxWait);
     } else {
-      if (s.most > 0 && lane_id() == 0) {
-        const int never = 0;
-        if (warp == 4 * NT && PAIR && rank == 1) {
-          if constexpr (PAIR) {
-            if (!mha_tell_peer<DQK>(p, m, s)) mha_raise(m, kErrMhaMmaWait);
-          }
-        } else if (warp == 4 * NT) {
-          if (!mha_mma<DQK, NT, PAIR>(p, m, sb, tmem, s)) mha_raise(m, kErrMhaMmaWait);
-          // every MMA issued completes before TMEM is freed
-          if (PAIR) mma_commit_pair(smem_u32(&m.drain));
-          else mma_commit(smem_u32(&m.drain));
-          mbar_wait(smem_u32(&m.drain), 0, global_timer_ns() + 100000000ull, &never);
-        } else if (warp == 4 * NT + 1) {
+      const int never = 0;
+      if (s.most > 0 && warp == 4 * NT) {
+        if (!mha_mma<DQK, NT>(p, m, sb, s)) mha_raise(m, kErrMhaMmaWait);
+        // every MMA issued completes before TMEM is freed
+        commit_to(elect_one(), &m.drain);
+        mbar_wait(smem_u32(&m.drain), 0, global_timer_ns() + 100000000ull, &never);
+      } else if (s.most > 0 && lane_id() == 0) {
+        {
           uint32_t fills = 0;
-          if (!mha_load<DQK, NT, PAIR>(p, m, sb, w, s, pack0, pack0 / p.group, rank, fills)) mha_raise(m, kErrMhaLoadWait);
+          if (!mha_load<DQK, NT>(p, m, sb, w, s, pack0, pack0 / p.group, fills)) mha_raise(m, kErrMhaLoadWait);
           // every copy issued has landed before the CTA exits (only a unit's last fill can be in flight)
           const uint64_t dl = global_timer_ns() + 100000000ull;
           for (int t = 0; t < NT; ++t)
@@ -1001,13 +915,7 @@ __global__ void __launch_bounds__(MhaFwdShape<DQK, NT, PAIR>::kThreads, 1) dense
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if constexpr (PAIR) {
-    cluster_sync();   // the products of both CTAs have ended, and what one tells the other has arrived
-    if (warp == 4 * NT) tmem_dealloc_pair(tmem, C::kTmemCols);
-    cluster_sync();
-  } else if (warp == 4 * NT) {
-    tmem_dealloc(tmem, C::kTmemCols);
-  }
+  if (warp == 4 * NT) tmem_dealloc(tmem, C::kTmemCols);
   if constexpr (NT == 1) {
     if (p.cluster > 1) {
       cluster_sync();   // every CTA's part is there

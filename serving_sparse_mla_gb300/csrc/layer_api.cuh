@@ -235,10 +235,9 @@ bool mha_setup(int* clusters) {
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess;
   };
   auto address = [](auto* kernel) { return reinterpret_cast<const void*>(kernel); };
-  const void* one = address(smla::dense_mha_fwd_kernel<DQK, 1, false>);
-  const bool ok = memory(one, smla::MhaFwdShape<DQK, 1, false>::kBytes) &&
-                  memory(address(smla::dense_mha_fwd_kernel<DQK, 2, false>), smla::MhaFwdShape<DQK, 2, false>::kBytes) &&
-                  memory(address(smla::dense_mha_fwd_kernel<DQK, 2, true>), smla::MhaFwdShape<DQK, 2, true>::kBytes) &&
+  const void* one = address(smla::dense_mha_fwd_kernel<DQK, 1>);
+  const bool ok = memory(one, smla::MhaFwdShape<DQK, 1>::kBytes) &&
+                  memory(address(smla::dense_mha_fwd_kernel<DQK, 2>), smla::MhaFwdShape<DQK, 2>::kBytes) &&
                   memory(address(smla::dense_mha_dq_kernel<DQK>), smla::MhaDqShape<DQK>::kBytes) &&
                   memory(address(smla::dense_mha_dkv_kernel<DQK>), smla::MhaDkvShape<DQK>::kBytes);
   bool refused = false;
@@ -248,8 +247,8 @@ bool mha_setup(int* clusters) {
       const int c = smla::kMhaMaxCluster >> i;
       cudaLaunchConfig_t cfg = {};
       cudaLaunchAttribute attr = {};
-      mha_cluster_config<smla::MhaFwdShape<DQK, 1, false>>(&cfg, &attr, static_cast<unsigned>(c), c);
-      if (cudaOccupancyMaxActiveClusters(&clusters[i], smla::dense_mha_fwd_kernel<DQK, 1, false>, &cfg) != cudaSuccess) {
+      mha_cluster_config<smla::MhaFwdShape<DQK, 1>>(&cfg, &attr, static_cast<unsigned>(c), c);
+      if (cudaOccupancyMaxActiveClusters(&clusters[i], smla::dense_mha_fwd_kernel<DQK, 1>, &cfg) != cudaSuccess) {
         clusters[i] = 0;
         refused = true;
       }
@@ -271,8 +270,7 @@ sparse_mla_status_t mha_device_setup(const MhaState** state) {
   return st.set ? SPARSE_MLA_OK : SPARSE_MLA_ERR_CUDA;
 }
 
-// How the forward's work is laid out: tiles per CTA (4: two CTAs with two each that share
-// their products) and CTAs of a cluster.
+// How the forward's work is laid out: tiles per CTA and CTAs that share a tile's keys.
 struct MhaPlan {
   int tiles, cluster;
   long long slots;
@@ -301,26 +299,17 @@ MhaPlan mha_plan(int total_q, int total_kv, int batch, bool packed, bool rest, i
       best = {1, c, 0};
     }
   }
-  // pairs where there are rows enough for all of them: the same blocks with half of the copies and of B's reads
-  if (best.tiles == 2 && units(4) * 2 >= 2 * sms && lq >= 8.0 * tok_tile) best = {4, 2, 0};
   best.slots = mha_slots(total_q, tok_tile * best.tiles, packed ? batch : 0, rest);
   return best;
 }
 
-template <int DQK, int NT, bool PAIR>
-cudaError_t mha_fwd_launch_as(const smla::MhaFwdParams& p, unsigned ctas, cudaStream_t cs) {
+template <int DQK, int NT>
+cudaError_t mha_fwd_launch(const smla::MhaFwdParams& p, unsigned ctas, cudaStream_t cs) {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr = {};
-  mha_cluster_config<smla::MhaFwdShape<DQK, NT, PAIR>>(&cfg, &attr, ctas, p.cluster);
+  mha_cluster_config<smla::MhaFwdShape<DQK, NT>>(&cfg, &attr, ctas, p.cluster);
   cfg.stream = cs;
-  return cudaLaunchKernelEx(&cfg, smla::dense_mha_fwd_kernel<DQK, NT, PAIR>, p);
-}
-
-template <int DQK>
-cudaError_t mha_fwd_launch(const smla::MhaFwdParams& p, int tiles, unsigned ctas, cudaStream_t cs) {
-  return tiles == 1   ? mha_fwd_launch_as<DQK, 1, false>(p, ctas, cs)
-         : tiles == 2 ? mha_fwd_launch_as<DQK, 2, false>(p, ctas, cs)
-                      : mha_fwd_launch_as<DQK, 2, true>(p, ctas, cs);
+  return cudaLaunchKernelEx(&cfg, smla::dense_mha_fwd_kernel<DQK, NT>, p);
 }
 
 // As many heads side by side as have what their tiles read, `bytes` each, in half of L2.
@@ -450,8 +439,7 @@ sparse_mla_status_t dense_mha_fwd(const void* q, long long q_tok_stride, long lo
                                 sms, state->clusters[d_qk == 192 ? 0 : 1]);
   // without keys nothing is loaded: any map does
   const bool keys = total_kv > 0;
-  if ((st = mha_map(&p.map_k, keys ? rk : rq, keys ? total_kv : total_q, keys ? h_kv : h_q, d_qk, 1,
-                    plan.tiles == 4 ? smla::kMhaTile / 2 : smla::kMhaTile)) !=
+  if ((st = mha_map(&p.map_k, keys ? rk : rq, keys ? total_kv : total_q, keys ? h_kv : h_q, d_qk, 1, smla::kMhaTile)) !=
           SPARSE_MLA_OK ||
       (st = mha_map(&p.map_v, keys ? rv : rq, keys ? total_kv : total_q, keys ? h_kv : h_q, smla::kMhaDv, 1,
                     smla::kMhaTile / 2)) != SPARSE_MLA_OK)
@@ -463,8 +451,9 @@ sparse_mla_status_t dense_mha_fwd(const void* q, long long q_tok_stride, long lo
   if (ctas > INT_MAX) return SPARSE_MLA_ERR_INVALID_ARG;
   p.slots = static_cast<int>(plan.slots);
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = d_qk == 192 ? mha_fwd_launch<192>(p, plan.tiles, static_cast<unsigned>(ctas), cs)
-                                    : mha_fwd_launch<128>(p, plan.tiles, static_cast<unsigned>(ctas), cs);
+  const unsigned n = static_cast<unsigned>(ctas);
+  const cudaError_t e = d_qk == 192 ? (plan.tiles == 2 ? mha_fwd_launch<192, 2>(p, n, cs) : mha_fwd_launch<192, 1>(p, n, cs))
+                                    : (plan.tiles == 2 ? mha_fwd_launch<128, 2>(p, n, cs) : mha_fwd_launch<128, 1>(p, n, cs));
   return e == cudaSuccess ? SPARSE_MLA_OK : SPARSE_MLA_ERR_CUDA;
 }
 
