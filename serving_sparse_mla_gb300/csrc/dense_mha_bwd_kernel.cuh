@@ -19,9 +19,10 @@
 //                  block, so that P is formed while T is, and dS while the next S is
 //   warp 9         one thread issues the TMA loads (K three blocks deep)
 //
-// dense_mha_dkv_kernel: a tile of 128 keys against the query rows that see them, N at a
-// time (128; at 192 columns 64, with V in TMEM: 128 + 192 columns of accumulators leave
-// 192), of every head of the group.
+// dense_mha_dkv_kernel: a tile of 128 keys against the query rows that see them, 64 at a
+// time, of every head of the group.  V, and K at 128 columns, are A of their products from
+// TMEM: shared memory gives 128 bytes a cycle, which a product with both operands there
+// takes alone.
 //   warps 0 .. 7   a thread per key and half of the columns: P^T and dS^T in TMEM, in the
 //                  columns of the products that they come from
 //   warp 8         S^T = K Q^T,  T^T = V dout^T,  dV += P^T dout,  dK += dS^T Q
@@ -57,8 +58,8 @@ struct MhaBwdParams {
   int slots;                               // tiles per head (pack) that the grid has room for
   int heads, heads_near;                   // head packs (of keys: heads); of so many at a time the longest tiles come first
   float scale, scale_log2;
-  const __nv_bfloat16 *v, *dout;           // row (t, h) at v + t v_tok + h v_head
-  long long v_tok, v_head, do_tok, do_head;
+  const __nv_bfloat16 *k, *v, *dout;       // row (t, h) at v + t v_tok + h v_head
+  long long k_tok, k_head, v_tok, v_head, do_tok, do_head;
   const __nv_bfloat16* out;                // [total_q, h_q, 128]
   const float* lse;                        // [total_q, h_q]
   float* delta;                            // [total_q, h_q]: D
@@ -396,7 +397,7 @@ __global__ void __launch_bounds__(MhaDqShape<DQK>::kThreads, 1) dense_mha_dq_ker
 constexpr int kMhaStats = 4;   // query blocks whose lse and D are held
 
 struct __align__(16) MhaDkvMisc {
-  uint64_t k_full, v_ready, q_full[4], q_empty[4], do_full[4], do_empty[4], stat_full[kMhaStats], stat_empty[kMhaStats];
+  uint64_t k_full, kv_ready, q_full[4], q_empty[4], do_full[4], do_empty[4], stat_full[kMhaStats], stat_empty[kMhaStats];
   uint64_t s_full, p_full, t_full, ds_full, out_full, drain;
   uint32_t tmem_base;
   int abort_flag;
@@ -408,21 +409,20 @@ struct __align__(16) MhaDkvMisc {
 
 template <int DQK>
 struct MhaDkvShape {
-  static constexpr int kN = DQK == 192 ? 64 : 128;             // query rows of a block
-  static constexpr bool kVTmem = DQK == 192;
+  static constexpr int kN = 64;                                // query rows of a block
+  static constexpr bool kKTmem = DQK == 128;                   // K as A of S^T in TMEM, as V is of T^T
   static constexpr int kSub = DQK / 64;
-  static constexpr int kStages = DQK == 192 ? 4 : 2;
+  static constexpr int kStages = 4;
   static constexpr uint32_t kQUnit = kN * 128;                 // 64 columns of a block
   static constexpr uint32_t kQBytes = kSub * kQUnit, kDoBytes = 2 * kQUnit;
-  static constexpr uint32_t kVOff = kSub * kMhaUnit;
-  static constexpr uint32_t kQOff = kVOff + (kVTmem ? 0 : 2 * kMhaUnit), kDoOff = kQOff + kStages * kQBytes;
+  static constexpr uint32_t kQOff = kKTmem ? 0 : kSub * kMhaUnit, kDoOff = kQOff + kStages * kQBytes;
   static constexpr uint32_t kMiscOff = kDoOff + kStages * kDoBytes;
   static constexpr int kBytes = static_cast<int>(kMiscOff) + static_cast<int>(sizeof(MhaDkvMisc)) + 1024;
   static constexpr int kThreads = 11 * 32;
   // columns of TMEM
-  static constexpr uint32_t kDv = 0, kDk = 128, kS = 128 + DQK, kT = kS + kN, kV = kT + kN;
+  static constexpr uint32_t kDv = 0, kDk = 128, kS = 128 + DQK, kT = kS + kN, kV = kT + kN, kK = kV + 64;
   static_assert(kBytes <= kMaxSmem, "shared memory");
-  static_assert(kT + kN + (kVTmem ? 64 : 0) <= 512, "TMEM");
+  static_assert(kV + 64 + (kKTmem ? 64 : 0) <= 512, "TMEM");
 };
 
 // The query blocks of one key tile: blocks of tok_tile tokens from the first that sees
@@ -443,12 +443,12 @@ __device__ __forceinline__ bool mha_dkv_load(const MhaBwdParams& p, MhaDkvMisc& 
   using C = MhaDkvShape<DQK>;
   const volatile int* ab = &m.abort_flag;
   const uint64_t deadline = global_timer_ns() + p.timeout_ns;
-  const int row = w.k0 + w.tile * kMhaTile;
-  const uint32_t kb = smem_u32(&m.k_full);
-  mbar_arrive_expect_tx(kb, (C::kSub + (C::kVTmem ? 0 : 2)) * kMhaUnit);
-  for (int c = 0; c < C::kSub; ++c) tma_load_3d(sb + c * kMhaUnit, &p.map_k, 64 * c, kvh, row, kb);
-  if (!C::kVTmem)
-    for (int c = 0; c < 2; ++c) tma_load_3d(sb + C::kVOff + c * kMhaUnit, &p.map_v, 64 * c, kvh, row, kb);
+  if (!C::kKTmem) {
+    const uint32_t kb = smem_u32(&m.k_full);
+    mbar_arrive_expect_tx(kb, C::kSub * kMhaUnit);
+    for (int c = 0; c < C::kSub; ++c)
+      tma_load_3d(sb + c * kMhaUnit, &p.map_k, 64 * c, kvh, w.k0 + w.tile * kMhaTile, kb);
+  }
   const uint32_t bytes = static_cast<uint32_t>(p.pack * p.tok_tile) * 128u;
   int head = kvh * p.group, b = 0;
   for (int j = 0; j < s.total; ++j) {
@@ -479,8 +479,7 @@ __device__ __forceinline__ bool mha_dkv_mma(const MhaBwdParams& p, MhaDkvMisc& m
   constexpr uint32_t kIdescS = idesc_bf16_f32(kMhaTile, C::kN, false, false);
   constexpr uint32_t kIdescV = idesc_bf16_f32(kMhaTile, kMhaDv, false, true);
   constexpr uint32_t kIdescK = idesc_bf16_f32(kMhaTile, DQK, false, true);
-  const uint64_t k_desc = smem_desc(sb, 16, 1024, SWZ_128B), v_desc = smem_desc(sb + C::kVOff, 16, 1024, SWZ_128B),
-                 q_desc = smem_desc(sb + C::kQOff, 16, 1024, SWZ_128B), g_desc = smem_desc(sb + C::kDoOff, 16, 1024, SWZ_128B),
+  const uint64_t k_desc = smem_desc(sb, 16, 1024, SWZ_128B), q_desc = smem_desc(sb + C::kQOff, 16, 1024, SWZ_128B), g_desc = smem_desc(sb + C::kDoOff, 16, 1024, SWZ_128B),
                  qt_desc = smem_desc(sb + C::kQOff, C::kQUnit, 1024, SWZ_128B),    // their rows as columns
                  gt_desc = smem_desc(sb + C::kDoOff, C::kQUnit, 1024, SWZ_128B);
   const uint32_t chosen = elect_one();
@@ -491,9 +490,11 @@ __device__ __forceinline__ bool mha_dkv_mma(const MhaBwdParams& p, MhaDkvMisc& m
     if (!warp_wait(smem_u32(&m.q_full[st]), j / C::kStages & 1, deadline, ab)) return false;
     const uint64_t q = desc_plus(q_desc, st * C::kQBytes);
 #pragma unroll
-    for (int kk = 0; kk < DQK / 16; ++kk)
-      mma_ss(chosen, C::kS, desc_plus(k_desc, (kk >> 2) * kMhaUnit + (kk & 3) * 32),
-                  desc_plus(q, (kk >> 2) * C::kQUnit + (kk & 3) * 32), kIdescS, kk > 0 ? 1u : 0u);
+    for (int kk = 0; kk < DQK / 16; ++kk) {
+      const uint64_t b = desc_plus(q, (kk >> 2) * C::kQUnit + (kk & 3) * 32);
+      if (C::kKTmem) mma_ts(chosen, C::kS, C::kK + 8 * kk, b, kIdescS, kk > 0 ? 1u : 0u);
+      else mma_ss(chosen, C::kS, desc_plus(k_desc, (kk >> 2) * kMhaUnit + (kk & 3) * 32), b, kIdescS, kk > 0 ? 1u : 0u);
+    }
     commit_to(chosen, &m.s_full);
     return true;
   };
@@ -502,13 +503,8 @@ __device__ __forceinline__ bool mha_dkv_mma(const MhaBwdParams& p, MhaDkvMisc& m
     if (!warp_wait(smem_u32(&m.do_full[st]), j / C::kStages & 1, deadline, ab)) return false;
     const uint64_t g = desc_plus(g_desc, st * C::kDoBytes);
 #pragma unroll
-    for (int kk = 0; kk < kMhaDv / 16; ++kk) {
-      const uint64_t b = desc_plus(g, (kk >> 2) * C::kQUnit + (kk & 3) * 32);
-      if (C::kVTmem)
-        mma_ts(chosen, C::kT, C::kV + 8 * kk, b, kIdescS, kk > 0 ? 1u : 0u);
-      else
-        mma_ss(chosen, C::kT, desc_plus(v_desc, (kk >> 2) * kMhaUnit + (kk & 3) * 32), b, kIdescS, kk > 0 ? 1u : 0u);
-    }
+    for (int kk = 0; kk < kMhaDv / 16; ++kk)
+      mma_ts(chosen, C::kT, C::kV + 8 * kk, desc_plus(g, (kk >> 2) * C::kQUnit + (kk & 3) * 32), kIdescS, kk > 0 ? 1u : 0u);
     commit_to(chosen, &m.t_full);
     return true;
   };
@@ -517,13 +513,10 @@ __device__ __forceinline__ bool mha_dkv_mma(const MhaBwdParams& p, MhaDkvMisc& m
     constexpr int kHalf = C::kN / 32;
     return static_cast<uint32_t>(kk < kHalf ? 8 * kk : C::kN / 2 + 8 * (kk - kHalf));
   };
-  if (!warp_wait(smem_u32(&m.k_full), 0, deadline, ab)) return false;
-  if (!scores(0)) return false;
-  if (C::kVTmem) {
-    if (!warp_wait(smem_u32(&m.v_ready), 0, deadline, ab)) return false;
-    tc_fence_after();
-  }
-  if (!values(0)) return false;
+  if (!C::kKTmem && !warp_wait(smem_u32(&m.k_full), 0, deadline, ab)) return false;
+  if (!warp_wait(smem_u32(&m.kv_ready), 0, deadline, ab)) return false;
+  tc_fence_after();
+  if (!scores(0) || !values(0)) return false;
   for (int j = 0; j < total; ++j) {
     const int st = j % C::kStages;
     if (!warp_wait(smem_u32(&m.p_full), j & 1, deadline, ab)) return false;
@@ -601,16 +594,19 @@ __device__ __forceinline__ bool mha_dkv_rows(const MhaBwdParams& p, MhaDkvMisc& 
   const int key = w.tile * kMhaTile + row;
   const bool live = key < lk;
   const uint32_t lane0 = tmem + (static_cast<uint32_t>((row >> 5) * 32) << 16);
-  if (C::kVTmem && s.total > 0) {
-    uint4 v[8];
-    const uint4* vp = reinterpret_cast<const uint4*>(p.v + (w.k0 + key) * p.v_tok + kvh * p.v_head + 64 * half);
+  if (s.total > 0) {
+    auto take = [&](const __nv_bfloat16* from, uint32_t column) {
+      uint4 x[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = live ? __ldg(vp + i) : make_uint4(0, 0, 0, 0);
-    mha_row_to_tmem(lane0 + C::kV + 32 * half, v);
+      for (int i = 0; i < 8; ++i) x[i] = live ? __ldg(reinterpret_cast<const uint4*>(from) + i) : make_uint4(0, 0, 0, 0);
+      mha_row_to_tmem(lane0 + column + 32 * half, x);
+    };
+    take(p.v + (w.k0 + key) * p.v_tok + kvh * p.v_head + 64 * half, C::kV);
+    if constexpr (C::kKTmem) take(p.k + (w.k0 + key) * p.k_tok + kvh * p.k_head + 64 * half, C::kK);
     tmem_wait_st();
     tc_fence_before();
     __syncwarp();
-    if (lane_id() == 0) mbar_arrive(smem_u32(&m.v_ready));
+    if (lane_id() == 0) mbar_arrive(smem_u32(&m.kv_ready));
   }
   const int last_key = min((w.tile + 1) * kMhaTile, lk) - 1;
   const uint32_t ts = lane0 + C::kS + kHalf * half, tt = lane0 + C::kT + kHalf * half;
@@ -730,7 +726,7 @@ __global__ void __launch_bounds__(MhaDkvShape<DQK>::kThreads, 1) dense_mha_dkv_k
       mbar_init(smem_u32(&m.stat_empty[i]), 8);   // one arrival per row warp
     }
     mbar_init(smem_u32(&m.k_full), 1);
-    mbar_init(smem_u32(&m.v_ready), 8);
+    mbar_init(smem_u32(&m.kv_ready), 8);
     mbar_init(smem_u32(&m.s_full), 1);
     mbar_init(smem_u32(&m.p_full), 8);
     mbar_init(smem_u32(&m.t_full), 1);
@@ -783,7 +779,7 @@ __global__ void __launch_bounds__(MhaDkvShape<DQK>::kThreads, 1) dense_mha_dkv_k
           if (!mha_dkv_load<DQK>(p, m, sb, w, s, kvh, qf, df)) mha_bwd_raise(m, kErrMhaDkvLoadWait);
           // every copy issued has landed before the CTA exits
           const uint64_t dl = global_timer_ns() + 100000000ull;
-          mbar_wait(smem_u32(&m.k_full), 0, dl, &never);
+          if (!C::kKTmem) mbar_wait(smem_u32(&m.k_full), 0, dl, &never);
           for (int i = max(0, qf - C::kStages); i < qf; ++i)
             mbar_wait(smem_u32(&m.q_full[i % C::kStages]), i / C::kStages & 1, dl, &never);
           for (int i = max(0, df - C::kStages); i < df; ++i)

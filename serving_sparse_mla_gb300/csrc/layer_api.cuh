@@ -335,6 +335,9 @@ sparse_mla_status_t mha_bwd_launch(const MhaRows& q, const MhaRows& k, const Mha
   p.group = h_q / h_kv;
   p.scale = sm_scale;
   p.scale_log2 = mha_scale_log2(sm_scale);
+  p.k = static_cast<const __nv_bfloat16*>(k.p);
+  p.k_tok = k.tok;
+  p.k_head = k.head;
   p.v = static_cast<const __nv_bfloat16*>(v.p);
   p.v_tok = v.tok;
   p.v_head = v.head;
