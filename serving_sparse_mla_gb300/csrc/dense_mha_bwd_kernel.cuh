@@ -10,24 +10,26 @@
 // across CTAs in an order that changes).
 //
 // dense_mha_dq_kernel: a tile of 128 query rows ((token, head) pairs, as in the forward)
-// against the keys that they see, 128 at a time.
+// against the keys that they see, 128 (at 192 columns 96) at a time.
 //   warps 0 .. 7   a thread per row and half of the columns.  First dout's row into TMEM
-//                  (A of the second product) and D; then per block P from S, dS from
-//                  dout V^T into the latter's columns; dq's rows at the end
-//   warp 8         one thread issues   S = Q K^T,  T = dout V^T,  dQ += dS K
-//                  in the order T(j + 1), S(j + 2), dQ(j + 1): S is ahead of its use by a
-//                  block, so that P is formed while T is, and dS while the next S is
+//                  (A of the second product) and D; then per block P from S, and dS from
+//                  P and T; dq's rows at the end
+//   warp 8         issues   S = Q K^T,  T = dout V^T,  dQ += dS K
 //   warp 9         one thread issues the TMA loads (K three blocks deep)
 //
 // dense_mha_dkv_kernel: a tile of 128 keys against the query rows that see them, 64 at a
-// time, of every head of the group.  V, and K at 128 columns, are A of their products from
-// TMEM: shared memory gives 128 bytes a cycle, which a product with both operands there
-// takes alone.
-//   warps 0 .. 7   a thread per key and half of the columns: P^T and dS^T in TMEM, in the
-//                  columns of the products that they come from
+// time, of every head of the group.
+//   warps 0 .. 7   a thread per key and half of the columns: P^T and dS^T
 //   warp 8         S^T = K Q^T,  T^T = V dout^T,  dV += P^T dout,  dK += dS^T Q
 //   warp 9         the TMA loads
 //   warp 10        the rows' lse and D into shared memory
+//
+// A signal from the tensor core to the threads that wait for it and back takes about 1000
+// cycles, as long as two products of a block.  So P and dS have columns of their own in
+// TMEM, and the next block's S and T are formed as soon as this one's have been read: with
+// P and dS in the columns of S and T a block of 64 rows took 2250 cycles, of which its
+// products are 1024.  That is what sets the blocks: at 192 columns 96 keys (dq; 2 x 96 + 48
+// + 192 + 64 columns of TMEM) and 64 query rows.
 //
 // All waits are bounded, as in the forward.
 #pragma once
@@ -94,7 +96,7 @@ __device__ __forceinline__ void mha_store_sums(__nv_bfloat16* row, uint32_t tadd
 // ------------------------------------------------------------------ dq
 
 struct __align__(16) MhaDqMisc {
-  uint64_t q_full, k_full[3], k_empty[3], v_full[3], v_empty[3], do_ready, s_full, s_free, t_full, ds_full, dq_full, drain;
+  uint64_t q_full, k_full[3], k_empty[3], v_full[3], v_empty[3], do_ready, s_full, s_free, t_full, t_free, ds_full, dq_full, drain;
   uint32_t tmem_base;
   int abort_flag;
   int prior_error;
@@ -104,16 +106,19 @@ struct __align__(16) MhaDqMisc {
 
 template <int DQK>
 struct MhaDqShape {
+  static constexpr int kN = DQK == 192 ? 96 : 128;             // keys of a block
   static constexpr int kSub = DQK / 64;
-  static constexpr int kKStages = 3, kVStages = DQK == 192 ? 1 : 3;
-  static constexpr uint32_t kKBytes = kSub * kMhaUnit, kVBytes = 2 * kMhaUnit;
+  static constexpr int kKStages = 3, kVStages = 2;
+  static constexpr uint32_t kKUnit = kN * 128;                 // 64 columns of a block
+  static constexpr uint32_t kKBytes = kSub * kKUnit, kVBytes = 2 * kKUnit;
   static constexpr uint32_t kKOff = kSub * kMhaUnit, kVOff = kKOff + kKStages * kKBytes;
   static constexpr uint32_t kMiscOff = kVOff + kVStages * kVBytes;
   static constexpr int kBytes = static_cast<int>(kMiscOff) + static_cast<int>(sizeof(MhaDqMisc)) + 1024;
   static constexpr int kThreads = 10 * 32;
   // columns of TMEM
-  static constexpr uint32_t kS = 0, kT = 128, kDq = 256, kDo = 448;
+  static constexpr uint32_t kS = 0, kT = kN, kDq = 2 * kN, kDs = kDq + DQK, kDo = 448;
   static_assert(kBytes <= kMaxSmem, "shared memory");
+  static_assert(kDs + kN / 2 <= kDo, "TMEM");
 };
 
 template <class Misc>
@@ -133,19 +138,19 @@ __device__ __forceinline__ bool mha_dq_load(const MhaBwdParams& p, MhaDqMisc& m,
   mbar_arrive_expect_tx(bar, C::kSub * static_cast<uint32_t>(p.pack * p.tok_tile) * 128u);
   for (int c = 0; c < C::kSub; ++c) tma_load_3d(sb + c * kMhaUnit, &p.map_q, 64 * c, pack0, w.q0 + t0, bar);
   for (int j = 0; j < blocks; ++j) {
-    const int ks = j % C::kKStages, vs = j % C::kVStages, row = w.k0 + j * kMhaTile;
+    const int ks = j % C::kKStages, vs = j % C::kVStages, row = w.k0 + j * C::kN;
     if (!mbar_wait(smem_u32(&m.k_empty[ks]), (j / C::kKStages & 1) ^ 1, deadline, ab)) return false;
     bar = smem_u32(&m.k_full[ks]);
     mbar_arrive_expect_tx(bar, C::kKBytes);
     ++k_fills;
     for (int c = 0; c < C::kSub; ++c)
-      tma_load_3d(sb + C::kKOff + ks * C::kKBytes + c * kMhaUnit, &p.map_k, 64 * c, kvh, row, bar);
+      tma_load_3d(sb + C::kKOff + ks * C::kKBytes + c * C::kKUnit, &p.map_k, 64 * c, kvh, row, bar);
     if (!mbar_wait(smem_u32(&m.v_empty[vs]), (j / C::kVStages & 1) ^ 1, deadline, ab)) return false;
     bar = smem_u32(&m.v_full[vs]);
     mbar_arrive_expect_tx(bar, C::kVBytes);
     ++v_fills;
     for (int c = 0; c < 2; ++c)
-      tma_load_3d(sb + C::kVOff + vs * C::kVBytes + c * kMhaUnit, &p.map_v, 64 * c, kvh, row, bar);
+      tma_load_3d(sb + C::kVOff + vs * C::kVBytes + c * C::kKUnit, &p.map_v, 64 * c, kvh, row, bar);
   }
   return true;
 }
@@ -153,10 +158,10 @@ __device__ __forceinline__ bool mha_dq_load(const MhaBwdParams& p, MhaDqMisc& m,
 template <int DQK>
 __device__ __forceinline__ bool mha_dq_mma(const MhaBwdParams& p, MhaDqMisc& m, uint32_t sb, int blocks) {
   using C = MhaDqShape<DQK>;
-  constexpr uint32_t kIdescS = idesc_bf16_f32(kMhaTile, kMhaTile, false, false);
+  constexpr uint32_t kIdescS = idesc_bf16_f32(kMhaTile, C::kN, false, false);
   constexpr uint32_t kIdescQ = idesc_bf16_f32(kMhaTile, DQK, false, true);
   const uint64_t q_desc = smem_desc(sb, 16, 1024, SWZ_128B), k_desc = smem_desc(sb + C::kKOff, 16, 1024, SWZ_128B),
-                 kt_desc = smem_desc(sb + C::kKOff, kMhaUnit, 1024, SWZ_128B),   // its rows as columns
+                 kt_desc = smem_desc(sb + C::kKOff, C::kKUnit, 1024, SWZ_128B),   // its rows as columns
                  v_desc = smem_desc(sb + C::kVOff, 16, 1024, SWZ_128B);
   const uint32_t chosen = elect_one();
   const volatile int* ab = &m.abort_flag;
@@ -166,10 +171,9 @@ __device__ __forceinline__ bool mha_dq_mma(const MhaBwdParams& p, MhaDqMisc& m, 
     if (!warp_wait(smem_u32(&m.k_full[st]), j / C::kKStages & 1, deadline, ab)) return false;
     const uint64_t k = desc_plus(k_desc, st * C::kKBytes);
 #pragma unroll
-    for (int kk = 0; kk < DQK / 16; ++kk) {
-      const uint32_t off = (kk >> 2) * kMhaUnit + (kk & 3) * 32;
-      mma_ss(chosen, C::kS, desc_plus(q_desc, off), desc_plus(k, off), kIdescS, kk > 0 ? 1u : 0u);
-    }
+    for (int kk = 0; kk < DQK / 16; ++kk)
+      mma_ss(chosen, C::kS, desc_plus(q_desc, (kk >> 2) * kMhaUnit + (kk & 3) * 32),
+             desc_plus(k, (kk >> 2) * C::kKUnit + (kk & 3) * 32), kIdescS, kk > 0 ? 1u : 0u);
     commit_to(chosen, &m.s_full);
     return true;
   };
@@ -179,8 +183,7 @@ __device__ __forceinline__ bool mha_dq_mma(const MhaBwdParams& p, MhaDqMisc& m, 
     const uint64_t v = desc_plus(v_desc, st * C::kVBytes);
 #pragma unroll
     for (int kk = 0; kk < kMhaDv / 16; ++kk)
-      mma_ts(chosen, C::kT, C::kDo + 8 * kk, desc_plus(v, (kk >> 2) * kMhaUnit + (kk & 3) * 32), kIdescS,
-                  kk > 0 ? 1u : 0u);
+      mma_ts(chosen, C::kT, C::kDo + 8 * kk, desc_plus(v, (kk >> 2) * C::kKUnit + (kk & 3) * 32), kIdescS, kk > 0 ? 1u : 0u);
     commit_to(chosen, &m.v_empty[st]);
     commit_to(chosen, &m.t_full);
     return true;
@@ -190,27 +193,24 @@ __device__ __forceinline__ bool mha_dq_mma(const MhaBwdParams& p, MhaDqMisc& m, 
   if (!warp_wait(smem_u32(&m.do_ready), 0, deadline, ab)) return false;
   tc_fence_after();
   if (!values(0)) return false;
-  if (blocks > 1) {
-    if (!warp_wait(smem_u32(&m.s_free), 0, deadline, ab)) return false;
-    tc_fence_after();
-    if (!scores(1)) return false;
-  }
   for (int j = 0; j < blocks; ++j) {
+    // the next block's S and T as soon as this one's have been read, then dQ when dS is there
+    if (j + 1 < blocks) {
+      if (!warp_wait(smem_u32(&m.s_free), j & 1, deadline, ab)) return false;
+      tc_fence_after();
+      if (!scores(j + 1)) return false;
+      if (!warp_wait(smem_u32(&m.t_free), j & 1, deadline, ab)) return false;
+      tc_fence_after();
+      if (!values(j + 1)) return false;
+    }
     if (!warp_wait(smem_u32(&m.ds_full), j & 1, deadline, ab)) return false;
     tc_fence_after();
     const int st = j % C::kKStages;
     const uint64_t k = desc_plus(kt_desc, st * C::kKBytes);
 #pragma unroll
-    for (int kk = 0; kk < kMhaTile / 16; ++kk)   // either half's dS is in its own columns
-      mma_ts(chosen, C::kDq, C::kT + 64 * (kk >> 2) + 8 * (kk & 3), desc_plus(k, kk * 2048), kIdescQ,
-                  j + kk > 0 ? 1u : 0u);
+    for (int kk = 0; kk < C::kN / 16; ++kk)
+      mma_ts(chosen, C::kDq, C::kDs + 8 * kk, desc_plus(k, kk * 2048), kIdescQ, j + kk > 0 ? 1u : 0u);
     commit_to(chosen, &m.k_empty[st]);
-    if (j + 1 < blocks && !values(j + 1)) return false;
-    if (j + 2 < blocks) {
-      if (!warp_wait(smem_u32(&m.s_free), (j + 1) & 1, deadline, ab)) return false;
-      tc_fence_after();
-      if (!scores(j + 2)) return false;
-    }
   }
   commit_to(chosen, &m.dq_full);
   return true;
@@ -258,13 +258,15 @@ __device__ __forceinline__ bool mha_dq_rows(const MhaBwdParams& p, MhaDqMisc& m,
     delta = m.part[0][row] + m.part[1][row];
     if (live && half == 0) p.delta[at] = delta;
   }
-  const int whole = max(0, t0 + lk - lq + 1) / kMhaTile;
-  const uint32_t ts = lane0 + C::kS + 64 * half, tt = lane0 + C::kT + 64 * half;
+  constexpr int kHalf = C::kN / 2;
+  const int whole = max(0, t0 + lk - lq + 1) / C::kN;
+  const uint32_t ts = lane0 + C::kS + kHalf * half, tt = lane0 + C::kT + kHalf * half,
+                 td = lane0 + C::kDs + kHalf / 2 * half;
   for (int j = 0; j < blocks; ++j) {
     if (!mbar_wait(smem_u32(&m.s_full), j & 1, deadline, ab)) return false;
     tc_fence_after();
-    float s[64];
-    tmem_load64(ts, s);
+    float s[kHalf], x[kHalf];
+    tmem_load<kHalf>(ts, s);
     tc_fence_before();
     __syncwarp();
     if (lane_id() == 0) mbar_arrive(smem_u32(&m.s_free));
@@ -274,29 +276,29 @@ __device__ __forceinline__ bool mha_dq_rows(const MhaBwdParams& p, MhaDqMisc& m,
       if (!mbar_wait(smem_u32(&m.k_full[st]), j / C::kKStages & 1, deadline, ab)) return false;
       mha_clear(sb + C::kKOff + st * C::kKBytes, C::kKBytes);
     }
-    const int sees = edge ? tok + lk - lq + 1 - j * kMhaTile - 64 * half : 64;
+    const int sees = edge ? tok + lk - lq + 1 - j * C::kN - kHalf * half : kHalf;
 #pragma unroll
-    for (int i = 0; i < 64; i += 2) {
+    for (int i = 0; i < kHalf; i += 2) {
       scale_shift2(s[i], s[i + 1], p.scale_log2, -lse2);
       s[i] = fast_exp2(s[i]);
       s[i + 1] = fast_exp2(s[i + 1]);
     }
     if (!mbar_wait(smem_u32(&m.t_full), j & 1, deadline, ab)) return false;
     tc_fence_after();
+    tmem_load<kHalf>(tt, x);
+    tc_fence_before();
+    __syncwarp();
+    if (lane_id() == 0) mbar_arrive(smem_u32(&m.t_free));
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      float x[32];
-      tmem_load32(tt + 32 * c, x);
+    for (int i = 0; i < kHalf; ++i) x[i] = s[i] * (x[i] - delta);
+    if (edge) {
 #pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        x[i] = s[32 * c + i] * (x[i] - delta);
-        if (edge) x[i] = 32 * c + i < sees ? x[i] : 0.f;
-      }
-      float pk[16];
-#pragma unroll
-      for (int i = 0; i < 16; ++i) pk[i] = __uint_as_float(pack_bf16x2(x[2 * i], x[2 * i + 1]));
-      tmem_st16(tt + 16 * c, pk);   // columns that have been read
+      for (int i = 0; i < kHalf; ++i) x[i] = i < sees ? x[i] : 0.f;
     }
+    // the product with the dS before has ended when that block's keys are free
+    if (j > 0 && !mbar_wait(smem_u32(&m.k_empty[(j - 1) % C::kKStages]), (j - 1) / C::kKStages & 1, deadline, ab)) return false;
+    tc_fence_after();
+    tmem_store_bf16<kHalf>(td, x);
     tmem_wait_st();
     tc_fence_before();
     __syncwarp();
@@ -334,6 +336,7 @@ __global__ void __launch_bounds__(MhaDqShape<DQK>::kThreads, 1) dense_mha_dq_ker
     mbar_init(smem_u32(&m.s_full), 1);
     mbar_init(smem_u32(&m.s_free), 8);
     mbar_init(smem_u32(&m.t_full), 1);
+    mbar_init(smem_u32(&m.t_free), 8);
     mbar_init(smem_u32(&m.ds_full), 8);
     mbar_init(smem_u32(&m.dq_full), 1);
     mbar_init(smem_u32(&m.drain), 1);
@@ -361,7 +364,7 @@ __global__ void __launch_bounds__(MhaDqShape<DQK>::kThreads, 1) dense_mha_dq_ker
   if (m.prior_error == 0 && w.q1 > w.q0) {
     const int lq = w.q1 - w.q0, t0 = w.tile * p.tok_tile;
     const int sees = min(t0 + p.tok_tile, lq) + (w.k1 - w.k0) - lq;   // of the tile's last row
-    const int blocks = sees > 0 ? (sees + kMhaTile - 1) / kMhaTile : 0;
+    const int blocks = sees > 0 ? (sees + C::kN - 1) / C::kN : 0;
     const int never = 0;
     if (warp < 8) {
       if (!mha_dq_rows<DQK>(p, m, sb, tmem, w, t0, blocks, pack0)) mha_bwd_raise(m, kErrMhaDqRowsWait);
@@ -397,8 +400,8 @@ __global__ void __launch_bounds__(MhaDqShape<DQK>::kThreads, 1) dense_mha_dq_ker
 constexpr int kMhaStats = 4;   // query blocks whose lse and D are held
 
 struct __align__(16) MhaDkvMisc {
-  uint64_t k_full, kv_ready, q_full[4], q_empty[4], do_full[4], do_empty[4], stat_full[kMhaStats], stat_empty[kMhaStats];
-  uint64_t s_full, p_full, t_full, ds_full, out_full, drain;
+  uint64_t k_full, k_ready, q_full[4], q_empty[4], do_full[4], do_empty[4], stat_full[kMhaStats], stat_empty[kMhaStats];
+  uint64_t s_full, s_free, p_full, t_full, t_free, ds_full, out_full, drain;
   uint32_t tmem_base;
   int abort_flag;
   int prior_error;
@@ -410,19 +413,20 @@ struct __align__(16) MhaDkvMisc {
 template <int DQK>
 struct MhaDkvShape {
   static constexpr int kN = 64;                                // query rows of a block
-  static constexpr bool kKTmem = DQK == 128;                   // K as A of S^T in TMEM, as V is of T^T
+  static constexpr bool kKTmem = DQK == 128;                   // K, A of S^T, in TMEM
   static constexpr int kSub = DQK / 64;
-  static constexpr int kStages = 4;
+  static constexpr int kStages = DQK == 192 ? 3 : 4;
   static constexpr uint32_t kQUnit = kN * 128;                 // 64 columns of a block
   static constexpr uint32_t kQBytes = kSub * kQUnit, kDoBytes = 2 * kQUnit;
-  static constexpr uint32_t kQOff = kKTmem ? 0 : kSub * kMhaUnit, kDoOff = kQOff + kStages * kQBytes;
+  static constexpr uint32_t kVOff = kKTmem ? 0 : kSub * kMhaUnit;
+  static constexpr uint32_t kQOff = kVOff + 2 * kMhaUnit, kDoOff = kQOff + kStages * kQBytes;
   static constexpr uint32_t kMiscOff = kDoOff + kStages * kDoBytes;
   static constexpr int kBytes = static_cast<int>(kMiscOff) + static_cast<int>(sizeof(MhaDkvMisc)) + 1024;
   static constexpr int kThreads = 11 * 32;
   // columns of TMEM
-  static constexpr uint32_t kDv = 0, kDk = 128, kS = 128 + DQK, kT = kS + kN, kV = kT + kN, kK = kV + 64;
+  static constexpr uint32_t kDv = 0, kDk = 128, kS = 128 + DQK, kT = kS + kN, kP = kT + kN, kDs = kP + kN / 2, kK = 448;
   static_assert(kBytes <= kMaxSmem, "shared memory");
-  static_assert(kV + 64 + (kKTmem ? 64 : 0) <= 512, "TMEM");
+  static_assert(kDs + kN / 2 <= (kKTmem ? kK : 512), "TMEM");
 };
 
 // The query blocks of one key tile: blocks of tok_tile tokens from the first that sees
@@ -443,12 +447,11 @@ __device__ __forceinline__ bool mha_dkv_load(const MhaBwdParams& p, MhaDkvMisc& 
   using C = MhaDkvShape<DQK>;
   const volatile int* ab = &m.abort_flag;
   const uint64_t deadline = global_timer_ns() + p.timeout_ns;
-  if (!C::kKTmem) {
-    const uint32_t kb = smem_u32(&m.k_full);
-    mbar_arrive_expect_tx(kb, C::kSub * kMhaUnit);
-    for (int c = 0; c < C::kSub; ++c)
-      tma_load_3d(sb + c * kMhaUnit, &p.map_k, 64 * c, kvh, w.k0 + w.tile * kMhaTile, kb);
-  }
+  const uint32_t kb = smem_u32(&m.k_full);
+  mbar_arrive_expect_tx(kb, (C::kKTmem ? 2 : C::kSub + 2) * kMhaUnit);
+  for (int c = 0; c < C::kSub && !C::kKTmem; ++c)
+    tma_load_3d(sb + c * kMhaUnit, &p.map_k, 64 * c, kvh, w.k0 + w.tile * kMhaTile, kb);
+  for (int c = 0; c < 2; ++c) tma_load_3d(sb + C::kVOff + c * kMhaUnit, &p.map_v, 64 * c, kvh, w.k0 + w.tile * kMhaTile, kb);
   const uint32_t bytes = static_cast<uint32_t>(p.pack * p.tok_tile) * 128u;
   int head = kvh * p.group, b = 0;
   for (int j = 0; j < s.total; ++j) {
@@ -479,7 +482,8 @@ __device__ __forceinline__ bool mha_dkv_mma(const MhaBwdParams& p, MhaDkvMisc& m
   constexpr uint32_t kIdescS = idesc_bf16_f32(kMhaTile, C::kN, false, false);
   constexpr uint32_t kIdescV = idesc_bf16_f32(kMhaTile, kMhaDv, false, true);
   constexpr uint32_t kIdescK = idesc_bf16_f32(kMhaTile, DQK, false, true);
-  const uint64_t k_desc = smem_desc(sb, 16, 1024, SWZ_128B), q_desc = smem_desc(sb + C::kQOff, 16, 1024, SWZ_128B), g_desc = smem_desc(sb + C::kDoOff, 16, 1024, SWZ_128B),
+  const uint64_t k_desc = smem_desc(sb, 16, 1024, SWZ_128B), v_desc = smem_desc(sb + C::kVOff, 16, 1024, SWZ_128B),
+                 q_desc = smem_desc(sb + C::kQOff, 16, 1024, SWZ_128B), g_desc = smem_desc(sb + C::kDoOff, 16, 1024, SWZ_128B),
                  qt_desc = smem_desc(sb + C::kQOff, C::kQUnit, 1024, SWZ_128B),    // their rows as columns
                  gt_desc = smem_desc(sb + C::kDoOff, C::kQUnit, 1024, SWZ_128B);
   const uint32_t chosen = elect_one();
@@ -504,38 +508,41 @@ __device__ __forceinline__ bool mha_dkv_mma(const MhaBwdParams& p, MhaDkvMisc& m
     const uint64_t g = desc_plus(g_desc, st * C::kDoBytes);
 #pragma unroll
     for (int kk = 0; kk < kMhaDv / 16; ++kk)
-      mma_ts(chosen, C::kT, C::kV + 8 * kk, desc_plus(g, (kk >> 2) * C::kQUnit + (kk & 3) * 32), kIdescS, kk > 0 ? 1u : 0u);
+      mma_ss(chosen, C::kT, desc_plus(v_desc, (kk >> 2) * kMhaUnit + (kk & 3) * 32),
+             desc_plus(g, (kk >> 2) * C::kQUnit + (kk & 3) * 32), kIdescS, kk > 0 ? 1u : 0u);
     commit_to(chosen, &m.t_full);
     return true;
   };
-  // either half's P^T and dS^T are at the start of its own columns
-  auto step_at = [](int kk) -> uint32_t {
-    constexpr int kHalf = C::kN / 32;
-    return static_cast<uint32_t>(kk < kHalf ? 8 * kk : C::kN / 2 + 8 * (kk - kHalf));
-  };
-  if (!C::kKTmem && !warp_wait(smem_u32(&m.k_full), 0, deadline, ab)) return false;
-  if (!warp_wait(smem_u32(&m.kv_ready), 0, deadline, ab)) return false;
+  if (!warp_wait(smem_u32(&m.k_full), 0, deadline, ab)) return false;
+  if (C::kKTmem && !warp_wait(smem_u32(&m.k_ready), 0, deadline, ab)) return false;
   tc_fence_after();
   if (!scores(0) || !values(0)) return false;
   for (int j = 0; j < total; ++j) {
+    // the next block's S and T as soon as this one's have been read; dV and dK when P and dS are there
     const int st = j % C::kStages;
+    const uint64_t g = desc_plus(gt_desc, st * C::kDoBytes), q = desc_plus(qt_desc, st * C::kQBytes);
+    if (j + 1 < total) {
+      if (!warp_wait(smem_u32(&m.s_free), j & 1, deadline, ab)) return false;
+      tc_fence_after();
+      if (!scores(j + 1)) return false;
+    }
     if (!warp_wait(smem_u32(&m.p_full), j & 1, deadline, ab)) return false;
     tc_fence_after();
-    const uint64_t g = desc_plus(gt_desc, st * C::kDoBytes), q = desc_plus(qt_desc, st * C::kQBytes);
 #pragma unroll
     for (int kk = 0; kk < C::kN / 16; ++kk)
-      mma_ts(chosen, C::kDv, C::kS + step_at(kk), desc_plus(g, kk * 2048), kIdescV,
-                  j + kk > 0 ? 1u : 0u);
+      mma_ts(chosen, C::kDv, C::kP + 8 * kk, desc_plus(g, kk * 2048), kIdescV, j + kk > 0 ? 1u : 0u);
     commit_to(chosen, &m.do_empty[st]);
-    if (j + 1 < total && !scores(j + 1)) return false;
+    if (j + 1 < total) {
+      if (!warp_wait(smem_u32(&m.t_free), j & 1, deadline, ab)) return false;
+      tc_fence_after();
+      if (!values(j + 1)) return false;
+    }
     if (!warp_wait(smem_u32(&m.ds_full), j & 1, deadline, ab)) return false;
     tc_fence_after();
 #pragma unroll
     for (int kk = 0; kk < C::kN / 16; ++kk)
-      mma_ts(chosen, C::kDk, C::kT + step_at(kk), desc_plus(q, kk * 2048), kIdescK,
-                  j + kk > 0 ? 1u : 0u);
+      mma_ts(chosen, C::kDk, C::kDs + 8 * kk, desc_plus(q, kk * 2048), kIdescK, j + kk > 0 ? 1u : 0u);
     commit_to(chosen, &m.q_empty[st]);
-    if (j + 1 < total && !values(j + 1)) return false;
   }
   commit_to(chosen, &m.out_full);
   return true;
@@ -594,22 +601,20 @@ __device__ __forceinline__ bool mha_dkv_rows(const MhaBwdParams& p, MhaDkvMisc& 
   const int key = w.tile * kMhaTile + row;
   const bool live = key < lk;
   const uint32_t lane0 = tmem + (static_cast<uint32_t>((row >> 5) * 32) << 16);
-  if (s.total > 0) {
-    auto take = [&](const __nv_bfloat16* from, uint32_t column) {
-      uint4 x[8];
+  if (C::kKTmem && s.total > 0) {
+    uint4 k[8];
+    const uint4* kp = reinterpret_cast<const uint4*>(p.k + (w.k0 + key) * p.k_tok + kvh * p.k_head + 64 * half);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = live ? __ldg(reinterpret_cast<const uint4*>(from) + i) : make_uint4(0, 0, 0, 0);
-      mha_row_to_tmem(lane0 + column + 32 * half, x);
-    };
-    take(p.v + (w.k0 + key) * p.v_tok + kvh * p.v_head + 64 * half, C::kV);
-    if constexpr (C::kKTmem) take(p.k + (w.k0 + key) * p.k_tok + kvh * p.k_head + 64 * half, C::kK);
+    for (int i = 0; i < 8; ++i) k[i] = live ? __ldg(kp + i) : make_uint4(0, 0, 0, 0);
+    mha_row_to_tmem(lane0 + C::kK + 32 * half, k);
     tmem_wait_st();
     tc_fence_before();
     __syncwarp();
-    if (lane_id() == 0) mbar_arrive(smem_u32(&m.kv_ready));
+    if (lane_id() == 0) mbar_arrive(smem_u32(&m.k_ready));
   }
   const int last_key = min((w.tile + 1) * kMhaTile, lk) - 1;
-  const uint32_t ts = lane0 + C::kS + kHalf * half, tt = lane0 + C::kT + kHalf * half;
+  const uint32_t ts = lane0 + C::kS + kHalf * half, tt = lane0 + C::kT + kHalf * half,
+                 tp = lane0 + C::kP + kHalf / 2 * half, td = lane0 + C::kDs + kHalf / 2 * half;
   int b = 0;
   for (int j = 0; j < s.total; ++j) {
     const int t0 = s.first + b * p.tok_tile;
@@ -618,20 +623,22 @@ __device__ __forceinline__ bool mha_dkv_rows(const MhaBwdParams& p, MhaDkvMisc& 
     // the columns that see this thread's key
     const int lo = edge ? p.pack * (key - (lk - lq) - t0) - kHalf * half : 0;
     const int hi = edge ? p.pack * (lq - t0) - kHalf * half : kHalf;
-    const int st = j % kMhaStats;
+    const int st = j % kMhaStats, qs = j % C::kStages, turn = j / C::kStages & 1;
+    // where the block before is: its products with P and dS have ended when its dout and Q are free
+    const int before = (j - 1) % C::kStages, turn_before = (j - 1) / C::kStages & 1;
     if (!mbar_wait(smem_u32(&m.s_full), j & 1, deadline, ab)) return false;
     tc_fence_after();
-    float x[kHalf];
-    if constexpr (kHalf == 64) tmem_load64(ts, x);
-    else tmem_load32(ts, x);
+    float x[kHalf], y[kHalf];
+    tmem_load<kHalf>(ts, x);
+    tc_fence_before();
+    __syncwarp();
+    if (lane_id() == 0) mbar_arrive(smem_u32(&m.s_free));
     if (!mbar_wait(smem_u32(&m.stat_full[st]), j / kMhaStats & 1, deadline, ab)) return false;
     if (edge) {
       // the products with P and dS must not meet what is not finite in a row that does not
       // see a key; the product that gives T has read dout by then
       if (!mbar_wait(smem_u32(&m.t_full), j & 1, deadline, ab)) return false;
-      const int qs = j % C::kStages;
-      if (!mbar_wait(smem_u32(&m.q_full[qs]), j / C::kStages & 1, deadline, ab) ||
-          !mbar_wait(smem_u32(&m.do_full[qs]), j / C::kStages & 1, deadline, ab))
+      if (!mbar_wait(smem_u32(&m.q_full[qs]), turn, deadline, ab) || !mbar_wait(smem_u32(&m.do_full[qs]), turn, deadline, ab))
         return false;
       mha_clear(sb + C::kQOff + qs * C::kQBytes, C::kQBytes);
       mha_clear(sb + C::kDoOff + qs * C::kDoBytes, C::kDoBytes);
@@ -649,41 +656,35 @@ __device__ __forceinline__ bool mha_dkv_rows(const MhaBwdParams& p, MhaDkvMisc& 
 #pragma unroll
       for (int i = 0; i < kHalf; ++i) x[i] = i >= lo && i < hi ? x[i] : 0.f;
     }
-#pragma unroll
-    for (int c = 0; c < kHalf; c += 32) {
-      float pk[16];
-#pragma unroll
-      for (int i = 0; i < 16; ++i) pk[i] = __uint_as_float(pack_bf16x2(x[c + 2 * i], x[c + 2 * i + 1]));
-      tmem_st16(ts + c / 2, pk);
-    }
+    if (j > 0 && !mbar_wait(smem_u32(&m.do_empty[before]), turn_before, deadline, ab)) return false;
+    tc_fence_after();
+    tmem_store_bf16<kHalf>(tp, x);
     tmem_wait_st();
     tc_fence_before();
     __syncwarp();
     if (lane_id() == 0) mbar_arrive(smem_u32(&m.p_full));
     if (!mbar_wait(smem_u32(&m.t_full), j & 1, deadline, ab)) return false;
     tc_fence_after();
+    tmem_load<kHalf>(tt, y);
+    tc_fence_before();
+    __syncwarp();
+    if (lane_id() == 0) mbar_arrive(smem_u32(&m.t_free));
     const float4* d4 = reinterpret_cast<const float4*>(&m.delta[st][kHalf * half]);
 #pragma unroll
-    for (int c = 0; c < kHalf; c += 32) {
-      float y[32];
-      tmem_load32(tt + c, y);
-#pragma unroll
-      for (int i = 0; i < 32; i += 4) {
-        const float4 d = d4[(c + i) >> 2];
-        y[i] = x[c + i] * (y[i] - d.x);
-        y[i + 1] = x[c + i + 1] * (y[i + 1] - d.y);
-        y[i + 2] = x[c + i + 2] * (y[i + 2] - d.z);
-        y[i + 3] = x[c + i + 3] * (y[i + 3] - d.w);
-      }
-      if (edge) {
-#pragma unroll
-        for (int i = 0; i < 32; ++i) y[i] = c + i >= lo && c + i < hi ? y[i] : 0.f;
-      }
-      float pk[16];
-#pragma unroll
-      for (int i = 0; i < 16; ++i) pk[i] = __uint_as_float(pack_bf16x2(y[2 * i], y[2 * i + 1]));
-      tmem_st16(tt + c / 2, pk);   // columns that have been read
+    for (int i = 0; i < kHalf; i += 4) {
+      const float4 d = d4[i >> 2];
+      y[i] = x[i] * (y[i] - d.x);
+      y[i + 1] = x[i + 1] * (y[i + 1] - d.y);
+      y[i + 2] = x[i + 2] * (y[i + 2] - d.z);
+      y[i + 3] = x[i + 3] * (y[i + 3] - d.w);
     }
+    if (edge) {
+#pragma unroll
+      for (int i = 0; i < kHalf; ++i) y[i] = i >= lo && i < hi ? y[i] : 0.f;
+    }
+    if (j > 0 && !mbar_wait(smem_u32(&m.q_empty[before]), turn_before, deadline, ab)) return false;
+    tc_fence_after();
+    tmem_store_bf16<kHalf>(td, y);
     tmem_wait_st();
     tc_fence_before();
     __syncwarp();
@@ -726,10 +727,12 @@ __global__ void __launch_bounds__(MhaDkvShape<DQK>::kThreads, 1) dense_mha_dkv_k
       mbar_init(smem_u32(&m.stat_empty[i]), 8);   // one arrival per row warp
     }
     mbar_init(smem_u32(&m.k_full), 1);
-    mbar_init(smem_u32(&m.kv_ready), 8);
+    mbar_init(smem_u32(&m.k_ready), 8);
     mbar_init(smem_u32(&m.s_full), 1);
+    mbar_init(smem_u32(&m.s_free), 8);
     mbar_init(smem_u32(&m.p_full), 8);
     mbar_init(smem_u32(&m.t_full), 1);
+    mbar_init(smem_u32(&m.t_free), 8);
     mbar_init(smem_u32(&m.ds_full), 8);
     mbar_init(smem_u32(&m.out_full), 1);
     mbar_init(smem_u32(&m.drain), 1);
@@ -779,7 +782,7 @@ __global__ void __launch_bounds__(MhaDkvShape<DQK>::kThreads, 1) dense_mha_dkv_k
           if (!mha_dkv_load<DQK>(p, m, sb, w, s, kvh, qf, df)) mha_bwd_raise(m, kErrMhaDkvLoadWait);
           // every copy issued has landed before the CTA exits
           const uint64_t dl = global_timer_ns() + 100000000ull;
-          if (!C::kKTmem) mbar_wait(smem_u32(&m.k_full), 0, dl, &never);
+          mbar_wait(smem_u32(&m.k_full), 0, dl, &never);
           for (int i = max(0, qf - C::kStages); i < qf; ++i)
             mbar_wait(smem_u32(&m.q_full[i % C::kStages]), i / C::kStages & 1, dl, &never);
           for (int i = max(0, df - C::kStages); i < df; ++i)

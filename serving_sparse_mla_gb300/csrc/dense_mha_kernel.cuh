@@ -346,6 +346,48 @@ __device__ __forceinline__ void tmem_load128(uint32_t taddr, float* v) {
       : "r"(taddr));
 }
 
+__device__ __forceinline__ void tmem_load48(uint32_t taddr, float* v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {"
+      "%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31"
+      "}, [%48];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {"
+      "%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47"
+      "}, [%49];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]),
+        "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]),
+        "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]),
+        "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31]),
+        "=f"(v[32]), "=f"(v[33]), "=f"(v[34]), "=f"(v[35]), "=f"(v[36]), "=f"(v[37]), "=f"(v[38]), "=f"(v[39]),
+        "=f"(v[40]), "=f"(v[41]), "=f"(v[42]), "=f"(v[43]), "=f"(v[44]), "=f"(v[45]), "=f"(v[46]), "=f"(v[47])
+      : "r"(taddr), "r"(taddr + 32));
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const float* v) {
+  const uint32_t* r = reinterpret_cast<const uint32_t*>(v);
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+               ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+// N (32, 48 or 64) columns of this thread's lane, all at once.
+template <int N>
+__device__ __forceinline__ void tmem_load(uint32_t taddr, float* v) {
+  if constexpr (N == 64) tmem_load64(taddr, v);
+  else if constexpr (N == 48) tmem_load48(taddr, v);
+  else tmem_load32(taddr, v);
+}
+// N values rounded to bf16 into N / 2 columns.
+template <int N>
+__device__ __forceinline__ void tmem_store_bf16(uint32_t taddr, const float* x) {
+  float pk[N / 2];
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i) pk[i] = __uint_as_float(pack_bf16x2(x[2 * i], x[2 * i + 1]));
+#pragma unroll
+  for (int i = 0; i < N / 32; ++i) tmem_st16(taddr + 16 * i, pk + 16 * i);
+  if constexpr (N % 32 != 0) tmem_st8(taddr + N / 2 - 8, pk + N / 2 - 8);
+}
+
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));

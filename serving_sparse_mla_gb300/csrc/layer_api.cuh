@@ -359,19 +359,18 @@ sparse_mla_status_t mha_bwd_launch(const MhaRows& q, const MhaRows& k, const Mha
   const MhaRows &mk = both ? k : (total_q > 0 ? q : k), &mv = both ? v : mk, &mq = both ? q : mk, &mg = both ? g : mk;
   const int tk = both ? total_kv : (total_q > 0 ? total_q : total_kv), hk = both || total_q == 0 ? h_kv : h_q;
   const int tq = both ? total_q : tk, hq = both ? h_q : hk, dv_cols = both ? smla::kMhaDv : DQK;
-  if ((st = mha_map(&p.map_k, mk, tk, hk, DQK, 1, smla::kMhaTile)) != SPARSE_MLA_OK ||
-      (st = mha_map(&p.map_v, mv, tk, hk, dv_cols, 1, smla::kMhaTile)) != SPARSE_MLA_OK)
-    return st;
-  auto queries = [&](int rows) {
+  auto maps = [&](int rows, int keys) {   // of a query block and a key block
     p.pack = mha_pack(p.group, rows);
     p.tok_tile = rows / p.pack;
-    if ((st = mha_map(&p.map_q, mq, tq, hq, DQK, p.pack, p.tok_tile)) == SPARSE_MLA_OK)
-      st = mha_map(&p.map_do, mg, tq, hq, dv_cols, p.pack, p.tok_tile);
+    if ((st = mha_map(&p.map_q, mq, tq, hq, DQK, p.pack, p.tok_tile)) == SPARSE_MLA_OK &&
+        (st = mha_map(&p.map_do, mg, tq, hq, dv_cols, p.pack, p.tok_tile)) == SPARSE_MLA_OK &&
+        (st = mha_map(&p.map_k, mk, tk, hk, DQK, 1, keys)) == SPARSE_MLA_OK)
+      st = mha_map(&p.map_v, mv, tk, hk, dv_cols, 1, keys);
     return st == SPARSE_MLA_OK;
   };
   if (total_q > 0) {
     using C = smla::MhaDqShape<DQK>;
-    if (!queries(smla::kMhaTile)) return st;
+    if (!maps(smla::kMhaTile, C::kN)) return st;
     const long long slots = mha_slots(total_q, p.tok_tile, seqs, seqs > 0), ctas = slots * (h_q / p.pack);
     if (ctas > INT_MAX) return SPARSE_MLA_ERR_INVALID_ARG;
     p.slots = static_cast<int>(slots);
@@ -382,7 +381,7 @@ sparse_mla_status_t mha_bwd_launch(const MhaRows& q, const MhaRows& k, const Mha
   }
   if (total_kv > 0) {
     using C = smla::MhaDkvShape<DQK>;
-    if (!queries(C::kN)) return st;
+    if (!maps(C::kN, smla::kMhaTile)) return st;
     const long long slots = mha_slots(total_kv, smla::kMhaTile, seqs, seqs > 0), ctas = slots * h_kv;
     if (ctas > INT_MAX) return SPARSE_MLA_ERR_INVALID_ARG;
     p.slots = static_cast<int>(slots);
