@@ -320,6 +320,7 @@ __global__ void __launch_bounds__(MhaDqShape<DQK>::kThreads, 1) dense_mha_dq_ker
   MhaDqMisc& m = *reinterpret_cast<MhaDqMisc*>(sbase + C::kMiscOff);
   const int warp = static_cast<int>(threadIdx.x >> 5);
   const uint32_t sb = smem_u32(sbase);
+  asm volatile("griddepcontrol.launch_dependents;");   // dk's and dv's kernel may be set up (it waits for this grid's end)
   int slot, head;
   mha_unit(blockIdx.x, p.slots, p.heads, p.heads_near, slot, head);
   const int pack0 = head * p.pack;
@@ -569,7 +570,7 @@ __device__ __forceinline__ bool mha_dkv_stats(const MhaBwdParams& p, MhaDkvMisc&
       if (r < p.pack * p.tok_tile && tok < lq) {
         const size_t at = static_cast<size_t>(w.q0 + tok) * p.h_q + head + r % p.pack;
         l[i] = __ldg(p.lse + at) * 1.4426950408889634f;
-        d[i] = __ldg(p.delta + at);
+        d[i] = __ldcg(p.delta + at);
         if (!(fabsf(d[i]) <= 3.402823466e38f)) l[i] = __uint_as_float(0x7fc00000u);
       }
     }
@@ -764,6 +765,8 @@ __global__ void __launch_bounds__(MhaDkvShape<DQK>::kThreads, 1) dense_mha_dkv_k
   const uint32_t tmem = m.tmem_base;
   const MhaWork w = m.work;
 
+  // D is there, and dq too when this grid ends
+  if (warp == 10) asm volatile("griddepcontrol.wait;" ::: "memory");
   if (m.prior_error == 0 && w.k1 > w.k0) {
     const MhaQueries s(p, w);
     const int never = 0;

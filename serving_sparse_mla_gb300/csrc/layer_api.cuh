@@ -312,9 +312,11 @@ cudaError_t mha_fwd_launch(const smla::MhaFwdParams& p, unsigned ctas, cudaStrea
   return cudaLaunchKernelEx(&cfg, smla::dense_mha_fwd_kernel<DQK, NT>, p);
 }
 
-// As many heads side by side as have what their tiles read, `bytes` each, in half of L2.
+// As many heads side by side as have what their tiles read, `bytes` each, in most of L2;
+// equal shares of all.
 int mha_near(int heads, double bytes) {
-  return static_cast<int>(std::max(1.0, std::min(static_cast<double>(heads), 6.4e7 / (bytes + 1))));
+  const double turns = std::ceil(heads * (bytes + 1) / 1e8);
+  return static_cast<int>(std::ceil(heads / std::min(turns, static_cast<double>(heads))));
 }
 
 // dq (and D into the workspace), then dk and dv.
@@ -387,8 +389,18 @@ sparse_mla_status_t mha_bwd_launch(const MhaRows& q, const MhaRows& k, const Mha
     p.slots = static_cast<int>(slots);
     p.heads = h_kv;
     p.heads_near = mha_near(h_kv, static_cast<double>(total_q) * (DQK + smla::kMhaDv) * 2 * p.group);
-    smla::dense_mha_dkv_kernel<DQK><<<static_cast<unsigned>(ctas), C::kThreads, C::kBytes, cs>>>(p);
-    if (cudaGetLastError() != cudaSuccess) return SPARSE_MLA_ERR_CUDA;
+    // its CTAs may take the SMs that the last tiles of dq leave (and themselves wait for D)
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+    cfg.blockDim = dim3(C::kThreads);
+    cfg.dynamicSmemBytes = C::kBytes;
+    cfg.stream = cs;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = total_q > 0 ? 1 : 0;
+    if (cudaLaunchKernelEx(&cfg, smla::dense_mha_dkv_kernel<DQK>, p) != cudaSuccess) return SPARSE_MLA_ERR_CUDA;
   }
   return SPARSE_MLA_OK;
 }
