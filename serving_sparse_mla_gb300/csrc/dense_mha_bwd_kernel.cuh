@@ -14,13 +14,13 @@
 //   warps 0 .. 7   a thread per row and half of the columns.  First dout's row into TMEM
 //                  (A of the second product) and D; then per block P from S, and dS from
 //                  P and T; dq's rows at the end
-//   warp 8         issues   S = Q K^T,  T = dout V^T,  dQ += dS K
+//   warps 8, 10    issue   S = Q K^T and T = dout V^T;   dQ += dS K
 //   warp 9         one thread issues the TMA loads (K three blocks deep)
 //
 // dense_mha_dkv_kernel: a tile of 128 keys against the query rows that see them, 64 at a
 // time, of every head of the group.
 //   warps 0 .. 7   a thread per key and half of the columns: P^T and dS^T
-//   warp 8         S^T = K Q^T,  T^T = V dout^T,  dV += P^T dout,  dK += dS^T Q
+//   warps 8, 11    issue   S^T = K Q^T and T^T = V dout^T;   dV += P^T dout and dK += dS^T Q
 //   warp 9         the TMA loads
 //   warp 10        the rows' lse and D into shared memory
 //
@@ -96,7 +96,7 @@ __device__ __forceinline__ void mha_store_sums(__nv_bfloat16* row, uint32_t tadd
 // ------------------------------------------------------------------ dq
 
 struct __align__(16) MhaDqMisc {
-  uint64_t q_full, k_full[3], k_empty[3], v_full[3], v_empty[3], do_ready, s_full, s_free, t_full, t_free, ds_full, dq_full, drain;
+  uint64_t q_full, k_full[3], k_empty[3], v_full[3], v_empty[3], do_ready, s_full, s_free, t_full, t_free, ds_full, dq_full, drain[2];
   uint32_t tmem_base;
   int abort_flag;
   int prior_error;
@@ -114,7 +114,7 @@ struct MhaDqShape {
   static constexpr uint32_t kKOff = kSub * kMhaUnit, kVOff = kKOff + kKStages * kKBytes;
   static constexpr uint32_t kMiscOff = kVOff + kVStages * kVBytes;
   static constexpr int kBytes = static_cast<int>(kMiscOff) + static_cast<int>(sizeof(MhaDqMisc)) + 1024;
-  static constexpr int kThreads = 10 * 32;
+  static constexpr int kThreads = 11 * 32;
   // columns of TMEM
   static constexpr uint32_t kS = 0, kT = kN, kDq = 2 * kN, kDs = kDq + DQK, kDo = 448;
   static_assert(kBytes <= kMaxSmem, "shared memory");
@@ -155,62 +155,59 @@ __device__ __forceinline__ bool mha_dq_load(const MhaBwdParams& p, MhaDqMisc& m,
   return true;
 }
 
+// S and T of the blocks, each as soon as the one before has been read.
 template <int DQK>
-__device__ __forceinline__ bool mha_dq_mma(const MhaBwdParams& p, MhaDqMisc& m, uint32_t sb, int blocks) {
+__device__ __forceinline__ bool mha_dq_scores(const MhaBwdParams& p, MhaDqMisc& m, uint32_t sb, int blocks) {
   using C = MhaDqShape<DQK>;
-  constexpr uint32_t kIdescS = idesc_bf16_f32(kMhaTile, C::kN, false, false);
-  constexpr uint32_t kIdescQ = idesc_bf16_f32(kMhaTile, DQK, false, true);
+  constexpr uint32_t kIdesc = idesc_bf16_f32(kMhaTile, C::kN, false, false);
   const uint64_t q_desc = smem_desc(sb, 16, 1024, SWZ_128B), k_desc = smem_desc(sb + C::kKOff, 16, 1024, SWZ_128B),
-                 kt_desc = smem_desc(sb + C::kKOff, C::kKUnit, 1024, SWZ_128B),   // its rows as columns
                  v_desc = smem_desc(sb + C::kVOff, 16, 1024, SWZ_128B);
   const uint32_t chosen = elect_one();
   const volatile int* ab = &m.abort_flag;
   const uint64_t deadline = global_timer_ns() + p.timeout_ns;
-  auto scores = [&](int j) -> bool {
-    const int st = j % C::kKStages;
-    if (!warp_wait(smem_u32(&m.k_full[st]), j / C::kKStages & 1, deadline, ab)) return false;
-    const uint64_t k = desc_plus(k_desc, st * C::kKBytes);
+  if (!warp_wait(smem_u32(&m.q_full), 0, deadline, ab)) return false;
+  for (int j = 0; j < blocks; ++j) {
+    const int ks = j % C::kKStages, vs = j % C::kVStages;
+    if (!warp_wait(smem_u32(&m.k_full[ks]), j / C::kKStages & 1, deadline, ab)) return false;
+    if (j > 0 && !warp_wait(smem_u32(&m.s_free), (j - 1) & 1, deadline, ab)) return false;
+    tc_fence_after();
+    const uint64_t k = desc_plus(k_desc, ks * C::kKBytes), v = desc_plus(v_desc, vs * C::kVBytes);
 #pragma unroll
     for (int kk = 0; kk < DQK / 16; ++kk)
       mma_ss(chosen, C::kS, desc_plus(q_desc, (kk >> 2) * kMhaUnit + (kk & 3) * 32),
-             desc_plus(k, (kk >> 2) * C::kKUnit + (kk & 3) * 32), kIdescS, kk > 0 ? 1u : 0u);
+             desc_plus(k, (kk >> 2) * C::kKUnit + (kk & 3) * 32), kIdesc, kk > 0 ? 1u : 0u);
     commit_to(chosen, &m.s_full);
-    return true;
-  };
-  auto values = [&](int j) -> bool {
-    const int st = j % C::kVStages;
-    if (!warp_wait(smem_u32(&m.v_full[st]), j / C::kVStages & 1, deadline, ab)) return false;
-    const uint64_t v = desc_plus(v_desc, st * C::kVBytes);
+    if (!warp_wait(smem_u32(&m.v_full[vs]), j / C::kVStages & 1, deadline, ab)) return false;
+    if (!warp_wait(smem_u32(j == 0 ? &m.do_ready : &m.t_free), j == 0 ? 0 : (j - 1) & 1, deadline, ab)) return false;
+    tc_fence_after();
 #pragma unroll
     for (int kk = 0; kk < kMhaDv / 16; ++kk)
-      mma_ts(chosen, C::kT, C::kDo + 8 * kk, desc_plus(v, (kk >> 2) * C::kKUnit + (kk & 3) * 32), kIdescS, kk > 0 ? 1u : 0u);
-    commit_to(chosen, &m.v_empty[st]);
+      mma_ts(chosen, C::kT, C::kDo + 8 * kk, desc_plus(v, (kk >> 2) * C::kKUnit + (kk & 3) * 32), kIdesc, kk > 0 ? 1u : 0u);
     commit_to(chosen, &m.t_full);
-    return true;
-  };
-  if (!warp_wait(smem_u32(&m.q_full), 0, deadline, ab)) return false;
-  if (!scores(0)) return false;
-  if (!warp_wait(smem_u32(&m.do_ready), 0, deadline, ab)) return false;
-  tc_fence_after();
-  if (!values(0)) return false;
+    commit_to(chosen, &m.v_empty[vs]);
+  }
+  return true;
+}
+
+// dQ += dS K of the blocks.
+template <int DQK>
+__device__ __forceinline__ bool mha_dq_sums(const MhaBwdParams& p, MhaDqMisc& m, uint32_t sb, int blocks) {
+  using C = MhaDqShape<DQK>;
+  constexpr uint32_t kIdesc = idesc_bf16_f32(kMhaTile, DQK, false, true);
+  const uint64_t k_desc = smem_desc(sb + C::kKOff, C::kKUnit, 1024, SWZ_128B);   // its rows as columns
+  const uint32_t chosen = elect_one();
+  const volatile int* ab = &m.abort_flag;
+  const uint64_t deadline = global_timer_ns() + p.timeout_ns;
   for (int j = 0; j < blocks; ++j) {
-    // the next block's S and T as soon as this one's have been read, then dQ when dS is there
-    if (j + 1 < blocks) {
-      if (!warp_wait(smem_u32(&m.s_free), j & 1, deadline, ab)) return false;
-      tc_fence_after();
-      if (!scores(j + 1)) return false;
-      if (!warp_wait(smem_u32(&m.t_free), j & 1, deadline, ab)) return false;
-      tc_fence_after();
-      if (!values(j + 1)) return false;
-    }
+    const int ks = j % C::kKStages;
+    const uint64_t k = desc_plus(k_desc, ks * C::kKBytes);
     if (!warp_wait(smem_u32(&m.ds_full), j & 1, deadline, ab)) return false;
+    if (!warp_wait(smem_u32(&m.k_full[ks]), j / C::kKStages & 1, deadline, ab)) return false;   // long past
     tc_fence_after();
-    const int st = j % C::kKStages;
-    const uint64_t k = desc_plus(kt_desc, st * C::kKBytes);
 #pragma unroll
     for (int kk = 0; kk < C::kN / 16; ++kk)
-      mma_ts(chosen, C::kDq, C::kDs + 8 * kk, desc_plus(k, kk * 2048), kIdescQ, j + kk > 0 ? 1u : 0u);
-    commit_to(chosen, &m.k_empty[st]);
+      mma_ts(chosen, C::kDq, C::kDs + 8 * kk, desc_plus(k, kk * 2048), kIdesc, j + kk > 0 ? 1u : 0u);
+    commit_to(chosen, &m.k_empty[ks]);
   }
   commit_to(chosen, &m.dq_full);
   return true;
@@ -340,7 +337,8 @@ __global__ void __launch_bounds__(MhaDqShape<DQK>::kThreads, 1) dense_mha_dq_ker
     mbar_init(smem_u32(&m.t_free), 8);
     mbar_init(smem_u32(&m.ds_full), 8);
     mbar_init(smem_u32(&m.dq_full), 1);
-    mbar_init(smem_u32(&m.drain), 1);
+    mbar_init(smem_u32(&m.drain[0]), 1);
+    mbar_init(smem_u32(&m.drain[1]), 1);
     m.abort_flag = 0;
     m.prior_error = *reinterpret_cast<volatile int*>(&g_device_error);
     fence_mbar_init();
@@ -369,10 +367,12 @@ __global__ void __launch_bounds__(MhaDqShape<DQK>::kThreads, 1) dense_mha_dq_ker
     const int never = 0;
     if (warp < 8) {
       if (!mha_dq_rows<DQK>(p, m, sb, tmem, w, t0, blocks, pack0)) mha_bwd_raise(m, kErrMhaDqRowsWait);
-    } else if (warp == 8 && blocks > 0) {
-      if (!mha_dq_mma<DQK>(p, m, sb, blocks)) mha_bwd_raise(m, kErrMhaDqMmaWait);
-      commit_to(elect_one(), &m.drain);   // every MMA issued completes before TMEM is freed
-      mbar_wait(smem_u32(&m.drain), 0, global_timer_ns() + 100000000ull, &never);
+    } else if ((warp == 8 || warp == 10) && blocks > 0) {
+      if (!(warp == 8 ? mha_dq_scores<DQK>(p, m, sb, blocks) : mha_dq_sums<DQK>(p, m, sb, blocks)))
+        mha_bwd_raise(m, kErrMhaDqMmaWait);
+      uint64_t* drain = &m.drain[warp == 8 ? 0 : 1];
+      commit_to(elect_one(), drain);   // every MMA issued completes before TMEM is freed
+      mbar_wait(smem_u32(drain), 0, global_timer_ns() + 100000000ull, &never);
     } else if (blocks > 0) {
       if (lane_id() == 0) {
         {
@@ -401,8 +401,8 @@ __global__ void __launch_bounds__(MhaDqShape<DQK>::kThreads, 1) dense_mha_dq_ker
 constexpr int kMhaStats = 4;   // query blocks whose lse and D are held
 
 struct __align__(16) MhaDkvMisc {
-  uint64_t k_full, k_ready, q_full[4], q_empty[4], do_full[4], do_empty[4], stat_full[kMhaStats], stat_empty[kMhaStats];
-  uint64_t s_full, s_free, p_full, t_full, t_free, ds_full, out_full, drain;
+  uint64_t k_full, k_ready, q_full[4], do_full[4], empty[4], stat_full[kMhaStats], stat_empty[kMhaStats];
+  uint64_t s_full, s_free, p_full, t_full, t_free, ds_full, out_full, drain[2];
   uint32_t tmem_base;
   int abort_flag;
   int prior_error;
@@ -423,7 +423,7 @@ struct MhaDkvShape {
   static constexpr uint32_t kQOff = kVOff + 2 * kMhaUnit, kDoOff = kQOff + kStages * kQBytes;
   static constexpr uint32_t kMiscOff = kDoOff + kStages * kDoBytes;
   static constexpr int kBytes = static_cast<int>(kMiscOff) + static_cast<int>(sizeof(MhaDkvMisc)) + 1024;
-  static constexpr int kThreads = 11 * 32;
+  static constexpr int kThreads = 12 * 32;
   // columns of TMEM
   static constexpr uint32_t kDv = 0, kDk = 128, kS = 128 + DQK, kT = kS + kN, kP = kT + kN, kDs = kP + kN / 2, kK = 448;
   static_assert(kBytes <= kMaxSmem, "shared memory");
@@ -444,7 +444,7 @@ struct MhaQueries {
 
 template <int DQK>
 __device__ __forceinline__ bool mha_dkv_load(const MhaBwdParams& p, MhaDkvMisc& m, uint32_t sb, const MhaWork& w,
-                                             const MhaQueries& s, int kvh, int& q_fills, int& do_fills) {
+                                             const MhaQueries& s, int kvh, int& fills) {
   using C = MhaDkvShape<DQK>;
   const volatile int* ab = &m.abort_flag;
   const uint64_t deadline = global_timer_ns() + p.timeout_ns;
@@ -457,16 +457,14 @@ __device__ __forceinline__ bool mha_dkv_load(const MhaBwdParams& p, MhaDkvMisc& 
   int head = kvh * p.group, b = 0;
   for (int j = 0; j < s.total; ++j) {
     const int st = j % C::kStages, par = j / C::kStages & 1, tok = w.q0 + s.first + b * p.tok_tile;
-    if (!mbar_wait(smem_u32(&m.q_empty[st]), par ^ 1, deadline, ab)) return false;
+    if (!mbar_wait(smem_u32(&m.empty[st]), par ^ 1, deadline, ab)) return false;
     uint32_t bar = smem_u32(&m.q_full[st]);
     mbar_arrive_expect_tx(bar, C::kSub * bytes);
-    ++q_fills;
     for (int c = 0; c < C::kSub; ++c)
       tma_load_3d(sb + C::kQOff + st * C::kQBytes + c * C::kQUnit, &p.map_q, 64 * c, head, tok, bar);
-    if (!mbar_wait(smem_u32(&m.do_empty[st]), par ^ 1, deadline, ab)) return false;
     bar = smem_u32(&m.do_full[st]);
     mbar_arrive_expect_tx(bar, 2 * bytes);
-    ++do_fills;
+    ++fills;
     for (int c = 0; c < 2; ++c)
       tma_load_3d(sb + C::kDoOff + st * C::kDoBytes + c * C::kQUnit, &p.map_do, 64 * c, head, tok, bar);
     if (++b == s.blocks) {
@@ -477,73 +475,71 @@ __device__ __forceinline__ bool mha_dkv_load(const MhaBwdParams& p, MhaDkvMisc& 
   return true;
 }
 
+// S^T and T^T of the blocks, each as soon as the one before has been read.
 template <int DQK>
-__device__ __forceinline__ bool mha_dkv_mma(const MhaBwdParams& p, MhaDkvMisc& m, uint32_t sb, int total) {
+__device__ __forceinline__ bool mha_dkv_scores(const MhaBwdParams& p, MhaDkvMisc& m, uint32_t sb, int total) {
   using C = MhaDkvShape<DQK>;
-  constexpr uint32_t kIdescS = idesc_bf16_f32(kMhaTile, C::kN, false, false);
-  constexpr uint32_t kIdescV = idesc_bf16_f32(kMhaTile, kMhaDv, false, true);
-  constexpr uint32_t kIdescK = idesc_bf16_f32(kMhaTile, DQK, false, true);
+  constexpr uint32_t kIdesc = idesc_bf16_f32(kMhaTile, C::kN, false, false);
   const uint64_t k_desc = smem_desc(sb, 16, 1024, SWZ_128B), v_desc = smem_desc(sb + C::kVOff, 16, 1024, SWZ_128B),
-                 q_desc = smem_desc(sb + C::kQOff, 16, 1024, SWZ_128B), g_desc = smem_desc(sb + C::kDoOff, 16, 1024, SWZ_128B),
-                 qt_desc = smem_desc(sb + C::kQOff, C::kQUnit, 1024, SWZ_128B),    // their rows as columns
-                 gt_desc = smem_desc(sb + C::kDoOff, C::kQUnit, 1024, SWZ_128B);
+                 q_desc = smem_desc(sb + C::kQOff, 16, 1024, SWZ_128B), g_desc = smem_desc(sb + C::kDoOff, 16, 1024, SWZ_128B);
   const uint32_t chosen = elect_one();
   const volatile int* ab = &m.abort_flag;
   const uint64_t deadline = global_timer_ns() + p.timeout_ns;
-  auto scores = [&](int j) -> bool {
-    const int st = j % C::kStages;
-    if (!warp_wait(smem_u32(&m.q_full[st]), j / C::kStages & 1, deadline, ab)) return false;
-    const uint64_t q = desc_plus(q_desc, st * C::kQBytes);
+  if (!warp_wait(smem_u32(&m.k_full), 0, deadline, ab)) return false;
+  if (C::kKTmem && !warp_wait(smem_u32(&m.k_ready), 0, deadline, ab)) return false;
+  for (int j = 0; j < total; ++j) {
+    const int st = j % C::kStages, turn = j / C::kStages & 1;
+    const uint64_t q = desc_plus(q_desc, st * C::kQBytes), g = desc_plus(g_desc, st * C::kDoBytes);
+    if (!warp_wait(smem_u32(&m.q_full[st]), turn, deadline, ab)) return false;
+    if (j > 0 && !warp_wait(smem_u32(&m.s_free), (j - 1) & 1, deadline, ab)) return false;
+    tc_fence_after();
 #pragma unroll
     for (int kk = 0; kk < DQK / 16; ++kk) {
       const uint64_t b = desc_plus(q, (kk >> 2) * C::kQUnit + (kk & 3) * 32);
-      if (C::kKTmem) mma_ts(chosen, C::kS, C::kK + 8 * kk, b, kIdescS, kk > 0 ? 1u : 0u);
-      else mma_ss(chosen, C::kS, desc_plus(k_desc, (kk >> 2) * kMhaUnit + (kk & 3) * 32), b, kIdescS, kk > 0 ? 1u : 0u);
+      if (C::kKTmem) mma_ts(chosen, C::kS, C::kK + 8 * kk, b, kIdesc, kk > 0 ? 1u : 0u);
+      else mma_ss(chosen, C::kS, desc_plus(k_desc, (kk >> 2) * kMhaUnit + (kk & 3) * 32), b, kIdesc, kk > 0 ? 1u : 0u);
     }
     commit_to(chosen, &m.s_full);
-    return true;
-  };
-  auto values = [&](int j) -> bool {
-    const int st = j % C::kStages;
-    if (!warp_wait(smem_u32(&m.do_full[st]), j / C::kStages & 1, deadline, ab)) return false;
-    const uint64_t g = desc_plus(g_desc, st * C::kDoBytes);
+    if (!warp_wait(smem_u32(&m.do_full[st]), turn, deadline, ab)) return false;
+    if (j > 0 && !warp_wait(smem_u32(&m.t_free), (j - 1) & 1, deadline, ab)) return false;
+    tc_fence_after();
 #pragma unroll
     for (int kk = 0; kk < kMhaDv / 16; ++kk)
       mma_ss(chosen, C::kT, desc_plus(v_desc, (kk >> 2) * kMhaUnit + (kk & 3) * 32),
-             desc_plus(g, (kk >> 2) * C::kQUnit + (kk & 3) * 32), kIdescS, kk > 0 ? 1u : 0u);
+             desc_plus(g, (kk >> 2) * C::kQUnit + (kk & 3) * 32), kIdesc, kk > 0 ? 1u : 0u);
     commit_to(chosen, &m.t_full);
-    return true;
-  };
-  if (!warp_wait(smem_u32(&m.k_full), 0, deadline, ab)) return false;
-  if (C::kKTmem && !warp_wait(smem_u32(&m.k_ready), 0, deadline, ab)) return false;
-  tc_fence_after();
-  if (!scores(0) || !values(0)) return false;
+  }
+  return true;
+}
+
+// dV += P^T dout and dK += dS^T Q of the blocks.  A block's copies are free behind them: S
+// and T have been read by then.
+template <int DQK>
+__device__ __forceinline__ bool mha_dkv_sums(const MhaBwdParams& p, MhaDkvMisc& m, uint32_t sb, int total) {
+  using C = MhaDkvShape<DQK>;
+  constexpr uint32_t kIdescV = idesc_bf16_f32(kMhaTile, kMhaDv, false, true);
+  constexpr uint32_t kIdescK = idesc_bf16_f32(kMhaTile, DQK, false, true);
+  const uint64_t q_desc = smem_desc(sb + C::kQOff, C::kQUnit, 1024, SWZ_128B),    // their rows as columns
+                 g_desc = smem_desc(sb + C::kDoOff, C::kQUnit, 1024, SWZ_128B);
+  const uint32_t chosen = elect_one();
+  const volatile int* ab = &m.abort_flag;
+  const uint64_t deadline = global_timer_ns() + p.timeout_ns;
   for (int j = 0; j < total; ++j) {
-    // the next block's S and T as soon as this one's have been read; dV and dK when P and dS are there
-    const int st = j % C::kStages;
-    const uint64_t g = desc_plus(gt_desc, st * C::kDoBytes), q = desc_plus(qt_desc, st * C::kQBytes);
-    if (j + 1 < total) {
-      if (!warp_wait(smem_u32(&m.s_free), j & 1, deadline, ab)) return false;
-      tc_fence_after();
-      if (!scores(j + 1)) return false;
-    }
+    const int st = j % C::kStages, turn = j / C::kStages & 1;
+    const uint64_t q = desc_plus(q_desc, st * C::kQBytes), g = desc_plus(g_desc, st * C::kDoBytes);
     if (!warp_wait(smem_u32(&m.p_full), j & 1, deadline, ab)) return false;
+    if (!warp_wait(smem_u32(&m.do_full[st]), turn, deadline, ab)) return false;
     tc_fence_after();
 #pragma unroll
     for (int kk = 0; kk < C::kN / 16; ++kk)
       mma_ts(chosen, C::kDv, C::kP + 8 * kk, desc_plus(g, kk * 2048), kIdescV, j + kk > 0 ? 1u : 0u);
-    commit_to(chosen, &m.do_empty[st]);
-    if (j + 1 < total) {
-      if (!warp_wait(smem_u32(&m.t_free), j & 1, deadline, ab)) return false;
-      tc_fence_after();
-      if (!values(j + 1)) return false;
-    }
     if (!warp_wait(smem_u32(&m.ds_full), j & 1, deadline, ab)) return false;
+    if (!warp_wait(smem_u32(&m.q_full[st]), turn, deadline, ab)) return false;   // long past
     tc_fence_after();
 #pragma unroll
     for (int kk = 0; kk < C::kN / 16; ++kk)
       mma_ts(chosen, C::kDk, C::kDs + 8 * kk, desc_plus(q, kk * 2048), kIdescK, j + kk > 0 ? 1u : 0u);
-    commit_to(chosen, &m.q_empty[st]);
+    commit_to(chosen, &m.empty[st]);
   }
   commit_to(chosen, &m.out_full);
   return true;
@@ -625,7 +621,7 @@ __device__ __forceinline__ bool mha_dkv_rows(const MhaBwdParams& p, MhaDkvMisc& 
     const int lo = edge ? p.pack * (key - (lk - lq) - t0) - kHalf * half : 0;
     const int hi = edge ? p.pack * (lq - t0) - kHalf * half : kHalf;
     const int st = j % kMhaStats, qs = j % C::kStages, turn = j / C::kStages & 1;
-    // where the block before is: its products with P and dS have ended when its dout and Q are free
+    // where the block before is: its products with P and dS have ended when it is free
     const int before = (j - 1) % C::kStages, turn_before = (j - 1) / C::kStages & 1;
     if (!mbar_wait(smem_u32(&m.s_full), j & 1, deadline, ab)) return false;
     tc_fence_after();
@@ -657,7 +653,7 @@ __device__ __forceinline__ bool mha_dkv_rows(const MhaBwdParams& p, MhaDkvMisc& 
 #pragma unroll
       for (int i = 0; i < kHalf; ++i) x[i] = i >= lo && i < hi ? x[i] : 0.f;
     }
-    if (j > 0 && !mbar_wait(smem_u32(&m.do_empty[before]), turn_before, deadline, ab)) return false;
+    if (j > 0 && !mbar_wait(smem_u32(&m.empty[before]), turn_before, deadline, ab)) return false;
     tc_fence_after();
     tmem_store_bf16<kHalf>(tp, x);
     tmem_wait_st();
@@ -683,8 +679,6 @@ __device__ __forceinline__ bool mha_dkv_rows(const MhaBwdParams& p, MhaDkvMisc& 
 #pragma unroll
       for (int i = 0; i < kHalf; ++i) y[i] = i >= lo && i < hi ? y[i] : 0.f;
     }
-    if (j > 0 && !mbar_wait(smem_u32(&m.q_empty[before]), turn_before, deadline, ab)) return false;
-    tc_fence_after();
     tmem_store_bf16<kHalf>(td, y);
     tmem_wait_st();
     tc_fence_before();
@@ -719,9 +713,8 @@ __global__ void __launch_bounds__(MhaDkvShape<DQK>::kThreads, 1) dense_mha_dkv_k
   if (threadIdx.x == 0) {
     for (int i = 0; i < 4; ++i) {
       mbar_init(smem_u32(&m.q_full[i]), 1);
-      mbar_init(smem_u32(&m.q_empty[i]), 1);
       mbar_init(smem_u32(&m.do_full[i]), 1);
-      mbar_init(smem_u32(&m.do_empty[i]), 1);
+      mbar_init(smem_u32(&m.empty[i]), 1);
     }
     for (int i = 0; i < kMhaStats; ++i) {
       mbar_init(smem_u32(&m.stat_full[i]), 1);
@@ -736,7 +729,8 @@ __global__ void __launch_bounds__(MhaDkvShape<DQK>::kThreads, 1) dense_mha_dkv_k
     mbar_init(smem_u32(&m.t_free), 8);
     mbar_init(smem_u32(&m.ds_full), 8);
     mbar_init(smem_u32(&m.out_full), 1);
-    mbar_init(smem_u32(&m.drain), 1);
+    mbar_init(smem_u32(&m.drain[0]), 1);
+    mbar_init(smem_u32(&m.drain[1]), 1);
     m.abort_flag = 0;
     m.prior_error = *reinterpret_cast<volatile int*>(&g_device_error);
     fence_mbar_init();
@@ -775,21 +769,23 @@ __global__ void __launch_bounds__(MhaDkvShape<DQK>::kThreads, 1) dense_mha_dkv_k
     } else if (s.total > 0) {
       if (warp == 10) {
         if (!mha_dkv_stats<DQK>(p, m, w, s, kvh)) mha_bwd_raise(m, kErrMhaDkvStatWait);
-      } else if (warp == 8) {
-        if (!mha_dkv_mma<DQK>(p, m, sb, s.total)) mha_bwd_raise(m, kErrMhaDkvMmaWait);
-        commit_to(elect_one(), &m.drain);   // every MMA issued completes before TMEM is freed
-        mbar_wait(smem_u32(&m.drain), 0, global_timer_ns() + 100000000ull, &never);
+      } else if (warp == 8 || warp == 11) {
+        if (!(warp == 8 ? mha_dkv_scores<DQK>(p, m, sb, s.total) : mha_dkv_sums<DQK>(p, m, sb, s.total)))
+          mha_bwd_raise(m, kErrMhaDkvMmaWait);
+        uint64_t* drain = &m.drain[warp == 8 ? 0 : 1];
+        commit_to(elect_one(), drain);   // every MMA issued completes before TMEM is freed
+        mbar_wait(smem_u32(drain), 0, global_timer_ns() + 100000000ull, &never);
       } else if (lane_id() == 0) {
         {
-          int qf = 0, df = 0;
-          if (!mha_dkv_load<DQK>(p, m, sb, w, s, kvh, qf, df)) mha_bwd_raise(m, kErrMhaDkvLoadWait);
+          int fills = 0;
+          if (!mha_dkv_load<DQK>(p, m, sb, w, s, kvh, fills)) mha_bwd_raise(m, kErrMhaDkvLoadWait);
           // every copy issued has landed before the CTA exits
           const uint64_t dl = global_timer_ns() + 100000000ull;
           mbar_wait(smem_u32(&m.k_full), 0, dl, &never);
-          for (int i = max(0, qf - C::kStages); i < qf; ++i)
+          for (int i = max(0, fills - C::kStages); i < fills; ++i) {
             mbar_wait(smem_u32(&m.q_full[i % C::kStages]), i / C::kStages & 1, dl, &never);
-          for (int i = max(0, df - C::kStages); i < df; ++i)
             mbar_wait(smem_u32(&m.do_full[i % C::kStages]), i / C::kStages & 1, dl, &never);
+          }
         }
       }
       __syncwarp();
