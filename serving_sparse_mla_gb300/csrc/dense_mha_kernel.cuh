@@ -722,13 +722,13 @@ __device__ __forceinline__ bool mha_softmax(const MhaFwdParams& p, MhaMisc& m, u
 #pragma unroll
       for (int i = 0; i < kMhaTile; ++i) v[i] = i < sees ? v[i] : -INFINITY;
     }
-    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+    float mx[4] = {v[0], v[1], v[2], v[3]};
 #pragma unroll
-    for (int i = 0; i < kMhaTile; i += 8) {
+    for (int i = 4; i < kMhaTile - 4; i += 8) {
 #pragma unroll
       for (int k = 0; k < 4; ++k) mx[k] = max3(mx[k], v[i + 2 * k], v[i + 2 * k + 1]);
     }
-    const float now = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
+    const float now = max3(max3(max3(mx[0], mx[1], mx[2]), max3(mx[3], v[124], v[125]), v[126]), v[127], v[127]);
     const bool grown = (now - top) * c > kMhaLazy;
     if (__any_sync(0xffffffffu, grown)) {
       // O is this warp's to change once the product before has ended: with two tiles the block's scores came after it
@@ -752,7 +752,7 @@ __device__ __forceinline__ bool mha_softmax(const MhaFwdParams& p, MhaMisc& m, u
       }
     }
     const float shift = top == -INFINITY ? 0.f : -top * c;
-    float add[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    float add[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < kMhaTile; i += 32) {
       float pk[16];
@@ -762,7 +762,7 @@ __device__ __forceinline__ bool mha_softmax(const MhaFwdParams& p, MhaMisc& m, u
         scale_shift2(a, b, c, shift);
         a = fast_exp2(a);
         b = fast_exp2(b);
-        add2(add[k & 6], add[(k & 6) + 1], a, b);
+        add2(add[k & 2], add[(k & 2) + 1], a, b);
         pk[k >> 1] = __uint_as_float(pack_bf16x2(a, b));
       }
       tmem_st16(ts + (i >> 1), pk);
@@ -772,8 +772,6 @@ __device__ __forceinline__ bool mha_softmax(const MhaFwdParams& p, MhaMisc& m, u
     __syncwarp();
     if (lane_id() == 0) mbar_arrive(smem_u32(&m.p_full[buf]));
     add2(add[0], add[1], add[2], add[3]);
-    add2(add[4], add[5], add[6], add[7]);
-    add2(add[0], add[1], add[4], add[5]);
     sum += add[0] + add[1];
   }
   const size_t at = live ? static_cast<size_t>(w.q0 + tok) * p.h_q + pack0 + row % p.pack : 0;

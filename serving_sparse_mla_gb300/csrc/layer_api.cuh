@@ -207,11 +207,10 @@ sparse_mla_status_t mha_map(CUtensorMap* map, const MhaRows& r, int total, int h
   return e == CUDA_SUCCESS ? SPARSE_MLA_OK : SPARSE_MLA_ERR_INVALID_ARG;
 }
 
-constexpr int kMhaClusterSizes = 4;   // 16, 8, 4 and 2 CTAs
 
 struct MhaState {
   bool set = false;
-  int clusters[2][kMhaClusterSizes] = {};   // at 192 and 128 columns: clusters of one-tile CTAs held at once
+  int clusters[2][smla::kMhaMaxCluster + 1] = {};   // at 192 and 128 columns: clusters of so many one-tile CTAs held at once
 };
 MhaState g_mha[kMaxDevices];   // under g_mu
 
@@ -243,13 +242,12 @@ bool mha_setup(int* clusters) {
   bool refused = false;
   if (ok) {
     refused = cudaFuncSetAttribute(one, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess;
-    for (int i = 0; i < kMhaClusterSizes; ++i) {
-      const int c = smla::kMhaMaxCluster >> i;
+    for (int c = 2; c <= smla::kMhaMaxCluster; ++c) {
       cudaLaunchConfig_t cfg = {};
       cudaLaunchAttribute attr = {};
       mha_cluster_config<smla::MhaFwdShape<DQK, 1>>(&cfg, &attr, static_cast<unsigned>(c), c);
-      if (cudaOccupancyMaxActiveClusters(&clusters[i], smla::dense_mha_fwd_kernel<DQK, 1>, &cfg) != cudaSuccess) {
-        clusters[i] = 0;
+      if (cudaOccupancyMaxActiveClusters(&clusters[c], smla::dense_mha_fwd_kernel<DQK, 1>, &cfg) != cudaSuccess) {
+        clusters[c] = 0;
         refused = true;
       }
     }
@@ -286,13 +284,8 @@ MhaPlan mha_plan(int total_q, int total_kv, int batch, bool packed, bool rest, i
   auto units = [&](int tiles) { return std::ceil(lq / (tok_tile * tiles)) * batch * packs; };
   MhaPlan best = {2, 1, 0};
   double least = std::max(longest, units(2) * mean / sms);
-  for (int c = 1; c <= smla::kMhaMaxCluster; c *= 2) {
-    if (c > 1) {
-      int held = 0;
-      for (int i = 0; i < kMhaClusterSizes; ++i)
-        if (smla::kMhaMaxCluster >> i == c) held = clusters[i];
-      if (units(1) > held || longest < 2 * c) continue;
-    }
+  for (int c = 1; c <= smla::kMhaMaxCluster; ++c) {
+    if (c > 1 && (units(1) > clusters[c] || longest < 2 * c)) continue;
     const double t = std::max(std::ceil(longest / c), units(1) * mean / sms) + (c > 1 ? 1.0 : 0.0);
     if (t < least) {
       least = t;
