@@ -351,7 +351,7 @@ __global__ void __launch_bounds__(MhaDqShape<DQK>::kThreads, 1) dense_mha_dq_ker
     tmem_relinquish();
   }
   if (warp == 9) {
-    const MhaWork w = mha_find<false>(p.cu_q, p.cu_kv, p.batch, p.total_q, p.total_kv, slot, p.tok_tile, true);
+    const MhaWork w = mha_find<false>(p.cu_q, p.cu_kv, p.batch, p.total_q, p.total_kv, slot, p.tok_tile);
     if (lane_id() == 0) m.work = w;
   }
   tc_fence_before();
@@ -360,6 +360,9 @@ __global__ void __launch_bounds__(MhaDqShape<DQK>::kThreads, 1) dense_mha_dq_ker
   const uint32_t tmem = m.tmem_base;
   const MhaWork w = m.work;
 
+  // rows of no sequence
+  if (warp == 9 && w.end < p.total_q && m.prior_error == 0)
+    mha_fill_rows(p.dq, static_cast<long long>(p.h_q) * (DQK / 2), w.end, p.total_q, 0u);
   if (m.prior_error == 0 && w.q1 > w.q0) {
     const int lq = w.q1 - w.q0, t0 = w.tile * p.tok_tile;
     const int sees = min(t0 + p.tok_tile, lq) + (w.k1 - w.k0) - lq;   // of the tile's last row
@@ -744,7 +747,7 @@ __global__ void __launch_bounds__(MhaDkvShape<DQK>::kThreads, 1) dense_mha_dkv_k
     tmem_relinquish();
   }
   if (warp == 9) {
-    const MhaWork w = mha_find<true>(p.cu_q, p.cu_kv, p.batch, p.total_q, p.total_kv, slot, p.tok_tile, true);
+    const MhaWork w = mha_find<true>(p.cu_q, p.cu_kv, p.batch, p.total_q, p.total_kv, slot, p.tok_tile);
     if (lane_id() == 0) m.work = w;
   }
   if (p.pack * p.tok_tile < C::kN) {
@@ -759,6 +762,11 @@ __global__ void __launch_bounds__(MhaDkvShape<DQK>::kThreads, 1) dense_mha_dkv_k
   const uint32_t tmem = m.tmem_base;
   const MhaWork w = m.work;
 
+  // rows of no sequence
+  if (warp == 9 && w.end < p.total_kv && m.prior_error == 0) {
+    mha_fill_rows(p.dk, static_cast<long long>(p.h_kv) * (DQK / 2), w.end, p.total_kv, 0u);
+    mha_fill_rows(p.dv, static_cast<long long>(p.h_kv) * (kMhaDv / 2), w.end, p.total_kv, 0u);
+  }
   // D is there, and dq too when this grid ends
   if (warp == 10) asm volatile("griddepcontrol.wait;" ::: "memory");
   if (m.prior_error == 0 && w.k1 > w.k0) {

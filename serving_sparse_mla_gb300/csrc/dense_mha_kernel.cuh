@@ -83,7 +83,7 @@ __device__ __forceinline__ int mha_offset(const int32_t* cu, int b, int total) {
 struct MhaWork {
   int q0, q1, k0, k1;   // q1 <= q0: nothing to do
   int tile;             // from the sequence's first row
-  int rest;             // rows behind the last sequence (k0 = k1 = 0)
+  int end;              // of the sequences' rows: the ones behind belong to none
 };
 
 // The tiles of one sequence that have more than `blocks` blocks of work (-1: all).
@@ -91,34 +91,28 @@ struct MhaWork {
 //   keys:    tiles of 128 rows; a block is `per` of the queries that see the first row
 template <bool KEYS>
 __device__ __forceinline__ int mha_tiles_above(int lq, int lk, int per, int blocks) {
+  const int rows = KEYS ? kMhaTile : per;
+  const int tiles = static_cast<int>(static_cast<unsigned>((KEYS ? lk : lq) + rows - 1) / static_cast<unsigned>(rows));
+  if (blocks < 0) return tiles;
   if constexpr (KEYS) {
-    const int tiles = (lk + kMhaTile - 1) / kMhaTile;
-    if (blocks < 0) return tiles;
-    const long long seen = lq - static_cast<long long>(blocks) * per;   // the first row's queries start before this one
-    if (seen <= 0) return 0;
-    const long long n = (seen + lk - lq + kMhaTile - 1) / kMhaTile;
-    return n < 0 ? 0 : (n < tiles ? static_cast<int>(n) : tiles);
+    const int seen = lq - blocks * per;   // the first row's queries start before this one
+    return seen <= 0 ? 0 : min(tiles, max(0, (seen + lk - lq + kMhaTile - 1) >> 7));
   } else {
-    const int tiles = (lq + per - 1) / per;
-    if (blocks < 0) return tiles;
-    const long long past = static_cast<long long>(blocks) * kMhaTile + lq - lk;   // the last row is behind this one
-    if (past >= lq) return 0;
-    return past <= 0 ? tiles : tiles - static_cast<int>(past / per);
+    const int past = blocks * kMhaTile + lq - lk;   // the last row is behind this one
+    return past >= lq ? 0 : (past <= 0 ? tiles : tiles - static_cast<int>(static_cast<unsigned>(past) / static_cast<unsigned>(per)));
   }
 }
 
 constexpr int kMhaSortBatch = 128;   // sequences up to which tiles are handed out by their work
 
 // Tile `slot` of all sequences' tiles, the ones with most work first (of many sequences: in
-// their order).  Behind them come the rows of no sequence where `rest` is set.  One warp,
-// all lanes.
+// their order); q1 = k1 = 0 where there are not so many.  One warp, all lanes.
 template <bool KEYS>
 __device__ __forceinline__ MhaWork mha_find(const int32_t* cu_q, const int32_t* cu_kv, int batch, int total_q,
-                                            int total_kv, int slot, int per, bool rest) {
-  MhaWork w = {0, 0, 0, 0, 0, 0};
-  const int rows = KEYS ? kMhaTile : per;
+                                            int total_kv, int slot, int per) {
+  MhaWork w = {0, 0, 0, 0, 0, KEYS ? total_kv : total_q};
   if (cu_q == nullptr) {
-    const int tiles = ((KEYS ? total_kv : total_q) + rows - 1) / rows;
+    const int tiles = mha_tiles_above<KEYS>(total_q, total_kv, per, -1);
     if (slot < tiles) {
       w.q1 = total_q;
       w.k1 = total_kv;
@@ -139,14 +133,16 @@ __device__ __forceinline__ MhaWork mha_find(const int32_t* cu_q, const int32_t* 
     for (int base = 32; base < batch; base += 32) n += __reduce_add_sync(0xffffffffu, above(seq(base + lane), blocks));
     return n;
   };
+  int longest = 0;   // most blocks of a tile, or more
+  w.end = 0;
+  for (int base = 0; base < batch; base += 32) {
+    const int4 x = base == 0 ? mine : seq(base + lane);
+    longest = max(longest, __reduce_max_sync(0xffffffffu, KEYS ? (x.y - x.x + per - 1) / per : (x.w - x.z + 127) / 128));
+    w.end = max(w.end, __reduce_max_sync(0xffffffffu, KEYS ? x.w : x.y));
+  }
   // the tiles before this one have more than `blocks` blocks, or as many and lie in earlier sequences
   int blocks = -1, before = 0;
-  if (batch <= kMhaSortBatch) {
-    int longest = 0;
-    for (int base = 0; base < batch; base += 32) {
-      const int4 x = base == 0 ? mine : seq(base + lane);
-      longest = max(longest, __reduce_max_sync(0xffffffffu, KEYS ? (x.y - x.x + per - 1) / per : (x.w - x.z + 127) / 128));
-    }
+  if (batch > 1 && batch <= kMhaSortBatch) {
     int lo = 0, hi = longest;   // the fewest blocks that at most `slot` tiles exceed
     while (lo < hi) {
       const int mid = (lo + hi) >> 1;
@@ -156,7 +152,6 @@ __device__ __forceinline__ MhaWork mha_find(const int32_t* cu_q, const int32_t* 
     blocks = lo;
     before = all_above(blocks);
   }
-  int end = 0;   // of the sequences' rows
   for (int base = 0; base < batch; base += 32) {
     const int4 x = base == 0 ? mine : seq(base + lane);
     const int more = blocks < 0 ? 0 : above(x, blocks);
@@ -176,26 +171,19 @@ __device__ __forceinline__ MhaWork mha_find(const int32_t* cu_q, const int32_t* 
       w.k1 = __shfl_sync(0xffffffffu, x.w, at);
       const int nth = slot - before - __shfl_sync(0xffffffffu, incl - n, at) + __shfl_sync(0xffffffffu, more, at);
       // the most work is in a sequence's last tile of queries, in its first of keys
-      w.tile = KEYS ? nth : (w.q1 - w.q0 + per - 1) / per - 1 - nth;
+      w.tile = KEYS ? nth : mha_tiles_above<KEYS>(w.q1 - w.q0, w.k1 - w.k0, per, -1) - 1 - nth;
       return w;
     }
     before += __shfl_sync(0xffffffffu, incl, 31);
-    end = max(end, __reduce_max_sync(0xffffffffu, KEYS ? x.w : x.y));
-  }
-  const int total = KEYS ? total_kv : total_q;
-  const int tile = slot - (batch <= kMhaSortBatch ? all_above(-1) : before);
-  if (rest && tile < (total - end + rows - 1) / rows) {
-    if (KEYS) {
-      w.k0 = end;
-      w.k1 = total;
-    } else {
-      w.q0 = end;
-      w.q1 = total;
-    }
-    w.tile = tile;
-    w.rest = 1;
   }
   return w;
+}
+
+// Rows first .. total - 1 of an output [total, words of 4 bytes] filled with a word, a share
+// of them by each CTA of the grid.  One warp.
+__device__ __forceinline__ void mha_fill_rows(void* out, long long words, int first, int total, uint32_t word) {
+  for (long long r = static_cast<long long>(first) + blockIdx.x; r < total; r += gridDim.x)
+    for (long long i = lane_id(); i < words; i += 32) static_cast<uint32_t*>(out)[r * words + i] = word;
 }
 
 // Unit -> tile and head (pack): `near` heads at a time, side by side, so that their longest
@@ -781,8 +769,7 @@ __device__ __forceinline__ bool mha_softmax(const MhaFwdParams& p, MhaMisc& m, u
     tc_fence_after();
   }
   const bool join = NT == 1 && p.cluster > 1;
-  const bool store_o = live && (!w.rest || (p.fill & 1)), store_l = live && (!w.rest || (p.fill & 2)) && !join;
-  if (store_l) p.lse[at] = sum == 0.f ? -INFINITY : (top * c + log2f(sum)) * 0.6931471805599453f;
+  if (live && !join) p.lse[at] = sum == 0.f ? -INFINITY : (top * c + log2f(sum)) * 0.6931471805599453f;
   // the products and loads are done: the ring's memory holds the rows that are joined
   float* part = reinterpret_cast<float*>(sbase + C::kQBytes) + row * kMhaPartRow;
   if (join) m.part[row] = make_float2(sum == 0.f ? -INFINITY : top * c, sum);
@@ -797,12 +784,12 @@ __device__ __forceinline__ bool mha_softmax(const MhaFwdParams& p, MhaMisc& m, u
 #pragma unroll
       for (int k = 0; k < 32; k += 4)
         *reinterpret_cast<float4*>(part + 32 * i + k) = make_float4(x[k], x[k + 1], x[k + 2], x[k + 3]);
-    } else if (store_o) {
+    } else if (live) {
 #pragma unroll
       for (int k = 0; k < 4; ++k) *reinterpret_cast<uint4*>(o + 32 * i + 8 * k) = pack8(x + 8 * k);
     }
   }
-  if (blocks > 0 && store_o && *reinterpret_cast<volatile int*>(&m.cleared)) {
+  if (blocks > 0 && live && *reinterpret_cast<volatile int*>(&m.cleared)) {
     // columns where a key that the row sees is not finite, among the blocks that were looked over
     const int first = max(max(0, s.t0[0] + lk - lq + 1) / kMhaTile, s.from) * kMhaTile;
     const int end = min(tok + lk - lq + 1, (s.from + blocks) * kMhaTile);
@@ -861,14 +848,12 @@ __device__ __forceinline__ void mha_join(const MhaFwdParams& p, MhaMisc& m, uint
     }
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
     const size_t out = static_cast<size_t>(w.q0 + t0 + row / p.pack) * p.h_q + pack0 + row % p.pack;
-    if (!w.rest || (p.fill & 1)) {
-      uint2* o = reinterpret_cast<uint2*>(p.out + out * kMhaDv + col);
+    uint2* o = reinterpret_cast<uint2*>(p.out + out * kMhaDv + col);
 #pragma unroll
-      for (int k = 0; k < W / 4; ++k)
-        o[k] = make_uint2(pack_bf16x2(acc[4 * k] * inv, acc[4 * k + 1] * inv),
-                          pack_bf16x2(acc[4 * k + 2] * inv, acc[4 * k + 3] * inv));
-    }
-    if (col == 0 && (!w.rest || (p.fill & 2)))
+    for (int k = 0; k < W / 4; ++k)
+      o[k] = make_uint2(pack_bf16x2(acc[4 * k] * inv, acc[4 * k + 1] * inv),
+                        pack_bf16x2(acc[4 * k + 2] * inv, acc[4 * k + 3] * inv));
+    if (col == 0)
       p.lse[out] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
   }
 }
@@ -916,8 +901,7 @@ __global__ void __launch_bounds__(MhaFwdShape<DQK, NT>::kThreads, 1) dense_mha_f
     tmem_relinquish();
   }
   if (warp == 4 * NT + 1) {
-    const MhaWork w = mha_find<false>(p.cu_q, p.cu_kv, p.batch, p.total_q, p.total_kv, slot, NT * p.tok_tile,
-                                      p.fill != 0);
+    const MhaWork w = mha_find<false>(p.cu_q, p.cu_kv, p.batch, p.total_q, p.total_kv, slot, NT * p.tok_tile);
     if (lane_id() == 0) m.work = w;
   }
   tc_fence_before();
@@ -926,6 +910,10 @@ __global__ void __launch_bounds__(MhaFwdShape<DQK, NT>::kThreads, 1) dense_mha_f
   const uint32_t tmem = m.tmem_base;
   const MhaWork w = m.work;
 
+  if (warp == 4 * NT + 1 && p.fill != 0 && w.end < p.total_q && m.prior_error == 0) {
+    if (p.fill & 1) mha_fill_rows(p.out, static_cast<long long>(p.h_q) * (kMhaDv / 2), w.end, p.total_q, 0u);
+    if (p.fill & 2) mha_fill_rows(p.lse, p.h_q, w.end, p.total_q, 0xff800000u);
+  }
   if (m.prior_error == 0 && w.q1 > w.q0) {
     const MhaSpan<NT> s(p, w, rank);
     if (warp < 4 * NT) {

@@ -175,11 +175,11 @@ int mha_pack(int group, int rows) {
   return 1;
 }
 
-// Tiles of `per` rows that any `batch` sequences of `total` rows in all have at most
-// (0: one dense sequence), and the rows behind them.
-long long mha_slots(int total, int per, int batch, bool rest) {
-  if (batch == 0) return (total + per - 1LL) / per;
-  return total / per + static_cast<long long>(batch < total ? batch : total) + (rest ? 1 : 0);
+// Tiles of `per` rows that any `batch` sequences of `total` rows (> 0) in all have at most
+// (0: one dense sequence): one for each that has rows, and one for each `per` rows more.
+long long mha_slots(int total, int per, int batch) {
+  const long long n = batch < 1 ? 1 : (batch < total ? batch : total);
+  return (total - n) / per + n;
 }
 
 // exp's scale in powers of two; kept off zero so that a hidden key's -inf stays one.
@@ -277,7 +277,7 @@ struct MhaPlan {
 // The layout whose slowest CTA has the least to do, by the sequences' mean lengths: key
 // blocks one after the other, of a longest tile and of the card's mean.  A CTA of two
 // tiles takes about as long for a block of both as one of a single tile for its own.
-MhaPlan mha_plan(int total_q, int total_kv, int batch, bool packed, bool rest, int packs, int tok_tile, int sms,
+MhaPlan mha_plan(int total_q, int total_kv, int batch, bool packed, int packs, int tok_tile, int sms,
                  const int* clusters) {
   const double lq = static_cast<double>(total_q) / batch, lk = static_cast<double>(total_kv) / batch;
   const double longest = std::ceil(lk / smla::kMhaTile), mean = (lk - std::min(lq, lk) / 2) / smla::kMhaTile + 0.5;
@@ -292,7 +292,7 @@ MhaPlan mha_plan(int total_q, int total_kv, int batch, bool packed, bool rest, i
       best = {1, c, 0};
     }
   }
-  best.slots = mha_slots(total_q, tok_tile * best.tiles, packed ? batch : 0, rest);
+  best.slots = mha_slots(total_q, tok_tile * best.tiles, packed ? batch : 0);
   return best;
 }
 
@@ -366,7 +366,7 @@ sparse_mla_status_t mha_bwd_launch(const MhaRows& q, const MhaRows& k, const Mha
   if (total_q > 0) {
     using C = smla::MhaDqShape<DQK>;
     if (!maps(smla::kMhaTile, C::kN)) return st;
-    const long long slots = mha_slots(total_q, p.tok_tile, seqs, seqs > 0), ctas = slots * (h_q / p.pack);
+    const long long slots = mha_slots(total_q, p.tok_tile, seqs), ctas = slots * (h_q / p.pack);
     if (ctas > INT_MAX) return SPARSE_MLA_ERR_INVALID_ARG;
     p.slots = static_cast<int>(slots);
     p.heads = h_q / p.pack;
@@ -377,7 +377,7 @@ sparse_mla_status_t mha_bwd_launch(const MhaRows& q, const MhaRows& k, const Mha
   if (total_kv > 0) {
     using C = smla::MhaDkvShape<DQK>;
     if (!maps(C::kN, smla::kMhaTile)) return st;
-    const long long slots = mha_slots(total_kv, smla::kMhaTile, seqs, seqs > 0), ctas = slots * h_kv;
+    const long long slots = mha_slots(total_kv, smla::kMhaTile, seqs), ctas = slots * h_kv;
     if (ctas > INT_MAX) return SPARSE_MLA_ERR_INVALID_ARG;
     p.slots = static_cast<int>(slots);
     p.heads = h_kv;
@@ -442,7 +442,7 @@ sparse_mla_status_t dense_mha_fwd(const void* q, long long q_tok_stride, long lo
   p.fill = cu_seqlens_q ? fill : 0;
   const unsigned long long t = g_timeout_ns.load();
   p.timeout_ns = t ? t : kDefaultTimeoutNs;
-  const MhaPlan plan = mha_plan(total_q, total_kv, p.batch, cu_seqlens_q != nullptr, p.fill != 0, h_q / p.pack, p.tok_tile,
+  const MhaPlan plan = mha_plan(total_q, total_kv, p.batch, cu_seqlens_q != nullptr, h_q / p.pack, p.tok_tile,
                                 sms, state->clusters[d_qk == 192 ? 0 : 1]);
   // without keys nothing is loaded: any map does
   const bool keys = total_kv > 0;
