@@ -52,7 +52,7 @@ enum MhaBwdErrCode : int {
 };
 
 struct MhaBwdParams {
-  CUtensorMap map_q, map_do;               // [token, head, d]: boxes 64 x pack x tok_tile
+  CUtensorMap map_q, map_do, map_o;        // [token, head, d]: boxes 64 x pack x tok_tile
   CUtensorMap map_k, map_v;                // boxes 64 x 1 x 128
   const int32_t *cu_q, *cu_kv;             // [batch + 1], null for one dense sequence
   int batch, total_q, total_kv, h_q, h_kv, group;
@@ -60,9 +60,8 @@ struct MhaBwdParams {
   int slots;                               // tiles per head (pack) that the grid has room for
   int heads, heads_near;                   // head packs (of keys: heads); of so many at a time the longest tiles come first
   float scale, scale_log2;
-  const __nv_bfloat16 *k, *v, *dout;       // row (t, h) at v + t v_tok + h v_head
-  long long k_tok, k_head, v_tok, v_head, do_tok, do_head;
-  const __nv_bfloat16* out;                // [total_q, h_q, 128]
+  const __nv_bfloat16* k;                  // row (t, h) at k + t k_tok + h k_head
+  long long k_tok, k_head;
   const float* lse;                        // [total_q, h_q]
   float* delta;                            // [total_q, h_q]: D
   __nv_bfloat16 *dq, *dk, *dv;             // [total, h, d]
@@ -76,27 +75,10 @@ __device__ __forceinline__ void mha_row_to_tmem(uint32_t taddr, const uint4 (&x)
   tmem_st16(taddr + 16, f + 16);
 }
 
-// Columns 0 .. 32 n - 1 of this thread's TMEM lane times `f` into a bf16 row (zeros where
-// there are no sums).
-template <int N>
-__device__ __forceinline__ void mha_store_sums(__nv_bfloat16* row, uint32_t taddr, float f, bool sums, bool live) {
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    float x[32];
-    if (sums) tmem_load32(taddr + 32 * i, x);
-#pragma unroll
-    for (int k = 0; k < 32; ++k) x[k] = sums ? x[k] * f : 0.f;
-    if (live) {
-#pragma unroll
-      for (int k = 0; k < 4; ++k) *reinterpret_cast<uint4*>(row + 32 * i + 8 * k) = pack8(x + 8 * k);
-    }
-  }
-}
-
 // ------------------------------------------------------------------ dq
 
 struct __align__(16) MhaDqMisc {
-  uint64_t q_full, k_full[3], k_empty[3], v_full[3], v_empty[3], do_ready, s_full, s_free, t_full, t_free, ds_full, dq_full, drain[2];
+  uint64_t q_full, o_full, k_full[3], k_empty[3], v_full[3], v_empty[3], do_ready, s_full, s_free, t_full, t_free, ds_full, dq_full, drain[2];
   uint32_t tmem_base;
   int abort_flag;
   int prior_error;
@@ -112,13 +94,17 @@ struct MhaDqShape {
   static constexpr uint32_t kKUnit = kN * 128;                 // 64 columns of a block
   static constexpr uint32_t kKBytes = kSub * kKUnit, kVBytes = 2 * kKUnit;
   static constexpr uint32_t kKOff = kSub * kMhaUnit, kVOff = kKOff + kKStages * kKBytes;
-  static constexpr uint32_t kMiscOff = kVOff + kVStages * kVBytes;
+  // dout and out, until they have been read: in the last stage of K, and behind the first of V
+  static constexpr uint32_t kDoOff = kKOff + 2 * kKBytes, kOOff = kVOff + kVBytes;
+  static constexpr uint32_t kMiscOff = kOOff + (kVBytes > 2 * kMhaUnit ? kVBytes : 2 * kMhaUnit);
   static constexpr int kBytes = static_cast<int>(kMiscOff) + static_cast<int>(sizeof(MhaDqMisc)) + 1024;
   static constexpr int kThreads = 11 * 32;
+  static_assert(kVStages == 2 && kKStages == 3 && kKBytes >= 2 * kMhaUnit, "dout and out");
   // columns of TMEM
   static constexpr uint32_t kS = 0, kT = kN, kDq = 2 * kN, kDs = kDq + DQK, kDo = 448;
   static_assert(kBytes <= kMaxSmem, "shared memory");
   static_assert(kDs + kN / 2 <= kDo, "TMEM");
+  static_assert(kMiscOff >= 256 * mha_stage_row<DQK / 64>(), "stage");
 };
 
 template <class Misc>
@@ -137,7 +123,16 @@ __device__ __forceinline__ bool mha_dq_load(const MhaBwdParams& p, MhaDqMisc& m,
   uint32_t bar = smem_u32(&m.q_full);
   mbar_arrive_expect_tx(bar, C::kSub * static_cast<uint32_t>(p.pack * p.tok_tile) * 128u);
   for (int c = 0; c < C::kSub; ++c) tma_load_3d(sb + c * kMhaUnit, &p.map_q, 64 * c, pack0, w.q0 + t0, bar);
+  // dout and out for the threads, where block 2's keys and block 1's values come later
+  const uint32_t bytes = static_cast<uint32_t>(p.pack * p.tok_tile) * 128u;
+  bar = smem_u32(&m.o_full);
+  mbar_arrive_expect_tx(bar, 4 * bytes);
+  for (int c = 0; c < 2; ++c) {
+    tma_load_3d(sb + C::kDoOff + c * kMhaUnit, &p.map_do, 64 * c, pack0, w.q0 + t0, bar);
+    tma_load_3d(sb + C::kOOff + c * kMhaUnit, &p.map_o, 64 * c, pack0, w.q0 + t0, bar);
+  }
   for (int j = 0; j < blocks; ++j) {
+    if (j == 1 && !mbar_wait(smem_u32(&m.do_ready), 0, deadline, ab)) return false;
     const int ks = j % C::kKStages, vs = j % C::kVStages, row = w.k0 + j * C::kN;
     if (!mbar_wait(smem_u32(&m.k_empty[ks]), (j / C::kKStages & 1) ^ 1, deadline, ab)) return false;
     bar = smem_u32(&m.k_full[ks]);
@@ -229,21 +224,20 @@ __device__ __forceinline__ bool mha_dq_rows(const MhaBwdParams& p, MhaDqMisc& m,
   if (blocks > 0) {
     uint4 g[8];
     float dot = 0.f;
+    if (live) lse2 = p.lse[at] * 1.4426950408889634f;
+    const bool there = mbar_wait(smem_u32(&m.o_full), 0, deadline, ab);   // all threads go on to their barrier
+    const uint32_t from = sb + half * kMhaUnit + row * 128;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) g[i] = make_uint4(0, 0, 0, 0);
-    if (live) {
-      const uint4* gp = reinterpret_cast<const uint4*>(p.dout + (w.q0 + tok) * p.do_tok + head * p.do_head + 64 * half);
-      const uint4* op = reinterpret_cast<const uint4*>(p.out + at * kMhaDv + 64 * half);
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t at16 = static_cast<uint32_t>((i ^ (row & 7)) * 16);   // 128B swizzle
+      uint4 x = ld_shared_v4(from + C::kOOff + at16);
+      g[i] = live ? ld_shared_v4(from + C::kDoOff + at16) : make_uint4(0, 0, 0, 0);
+      if (!live) x = make_uint4(0, 0, 0, 0);
+      float a[8], b[8];
+      unpack8(g[i], a);
+      unpack8(x, b);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        g[i] = __ldg(gp + i);
-        float a[8], b[8];
-        unpack8(g[i], a);
-        unpack8(__ldg(op + i), b);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) dot += a[k] * b[k];
-      }
-      lse2 = p.lse[at] * 1.4426950408889634f;
+      for (int k = 0; k < 8; ++k) dot += a[k] * b[k];
     }
     mha_row_to_tmem(lane0 + C::kDo + 32 * half, g);
     tmem_wait_st();
@@ -252,6 +246,7 @@ __device__ __forceinline__ bool mha_dq_rows(const MhaBwdParams& p, MhaDqMisc& m,
     if (lane_id() == 0) mbar_arrive(smem_u32(&m.do_ready));
     m.part[half][row] = dot;
     named_bar_sync(1, 256);
+    if (!there) return false;
     delta = m.part[0][row] + m.part[1][row];
     if (live && half == 0) p.delta[at] = delta;
   }
@@ -305,7 +300,10 @@ __device__ __forceinline__ bool mha_dq_rows(const MhaBwdParams& p, MhaDqMisc& m,
     if (!mbar_wait(smem_u32(&m.dq_full), 0, deadline, ab)) return false;
     tc_fence_after();
   }
-  mha_store_sums<DQK / 64>(p.dq + at * DQK + half * (DQK / 2), lane0 + C::kDq + half * (DQK / 2), p.scale, blocks > 0, live);
+  // Q and K are not needed any more: their memory is the stage
+  mha_store_sums<DQK / 64>(p.dq + at * DQK + half * (DQK / 2), sb + threadIdx.x * mha_stage_row<DQK / 64>(),
+                           lane0 + C::kDq + half * (DQK / 2), p.scale, blocks > 0, live);
+  bulk_wait();
   return true;
 }
 
@@ -330,6 +328,7 @@ __global__ void __launch_bounds__(MhaDqShape<DQK>::kThreads, 1) dense_mha_dq_ker
       mbar_init(smem_u32(&m.v_empty[i]), 1);
     }
     mbar_init(smem_u32(&m.q_full), 1);
+    mbar_init(smem_u32(&m.o_full), 1);
     mbar_init(smem_u32(&m.do_ready), 8);   // one arrival per row warp
     mbar_init(smem_u32(&m.s_full), 1);
     mbar_init(smem_u32(&m.s_free), 8);
@@ -384,6 +383,7 @@ __global__ void __launch_bounds__(MhaDqShape<DQK>::kThreads, 1) dense_mha_dq_ker
           // every copy issued has landed before the CTA exits
           const uint64_t dl = global_timer_ns() + 100000000ull;
           mbar_wait(smem_u32(&m.q_full), 0, dl, &never);
+          mbar_wait(smem_u32(&m.o_full), 0, dl, &never);
           for (int i = max(0, kf - C::kKStages); i < kf; ++i)
             mbar_wait(smem_u32(&m.k_full[i % C::kKStages]), i / C::kKStages & 1, dl, &never);
           for (int i = max(0, vf - C::kVStages); i < vf; ++i)
@@ -431,6 +431,7 @@ struct MhaDkvShape {
   static constexpr uint32_t kDv = 0, kDk = 128, kS = 128 + DQK, kT = kS + kN, kP = kT + kN, kDs = kP + kN / 2, kK = 448;
   static_assert(kBytes <= kMaxSmem, "shared memory");
   static_assert(kDs + kN / 2 <= (kKTmem ? kK : 512), "TMEM");
+  static_assert(kMiscOff >= 256 * (mha_stage_row<2>() + mha_stage_row<DQK / 64>()), "stage");
 };
 
 // The query blocks of one key tile: blocks of tok_tile tokens from the first that sees
@@ -696,8 +697,13 @@ __device__ __forceinline__ bool mha_dkv_rows(const MhaBwdParams& p, MhaDkvMisc& 
     tc_fence_after();
   }
   const size_t at = live ? static_cast<size_t>(w.k0 + key) * p.h_kv + kvh : 0;
-  mha_store_sums<2>(p.dv + at * kMhaDv + 64 * half, lane0 + C::kDv + 64 * half, 1.f, s.total > 0, live);
-  mha_store_sums<DQK / 64>(p.dk + at * DQK + half * (DQK / 2), lane0 + C::kDk + half * (DQK / 2), p.scale, s.total > 0, live);
+  // the copies are not needed any more: their memory is the stage
+  mha_store_sums<2>(p.dv + at * kMhaDv + 64 * half, sb + threadIdx.x * mha_stage_row<2>(), lane0 + C::kDv + 64 * half, 1.f,
+                    s.total > 0, live);
+  mha_store_sums<DQK / 64>(p.dk + at * DQK + half * (DQK / 2),
+                           sb + 256 * mha_stage_row<2>() + threadIdx.x * mha_stage_row<DQK / 64>(),
+                           lane0 + C::kDk + half * (DQK / 2), p.scale, s.total > 0, live);
+  bulk_wait();
   return true;
 }
 

@@ -376,6 +376,50 @@ __device__ __forceinline__ void tmem_store_bf16(uint32_t taddr, const float* x) 
   if constexpr (N % 32 != 0) tmem_st8(taddr + N / 2 - 8, pk + N / 2 - 8);
 }
 
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+  return v;
+}
+
+// `bytes` (a multiple of 16) of this CTA's shared memory to global memory, in the background;
+// the thread's copies so far have ended.
+__device__ __forceinline__ void bulk_store(void* to, uint32_t from, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;"
+               ::"l"(reinterpret_cast<uint64_t>(to)), "r"(from), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void bulk_wait() {
+  asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group 0;" ::: "memory");
+}
+
+// 32 N columns of this thread's TMEM lane times `f` as a bf16 row (zeros where there are no
+// sums), put together in its own part of shared memory (`stage`) and copied from there:
+// stored by the threads themselves, 32 rows' pieces of 16 bytes at a time, a tile's rows
+// take about 2 us of the CTA's time.  Rows of the stage are 64 N + 16 bytes apart:
+// neighbours are in other banks.  `sums` is the same for a whole warp.
+template <int N>
+__device__ __forceinline__ void mha_store_sums(__nv_bfloat16* row, uint32_t stage, uint32_t taddr, float f, bool sums,
+                                               bool live) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    float x[32];
+    if (sums) tmem_load32(taddr + 32 * i, x);
+#pragma unroll
+    for (int k = 0; k < 32; ++k) x[k] = sums ? x[k] * f : 0.f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint4 v = pack8(x + 8 * k);
+      st_shared_v4(stage + 64 * i + 16 * k, v.x, v.y, v.z, v.w);
+    }
+  }
+  fence_proxy_async_smem();
+  if (live) bulk_store(row, stage, 64 * N);
+}
+template <int N>
+__device__ constexpr uint32_t mha_stage_row() {
+  return 64 * N + 16;
+}
+
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -772,21 +816,26 @@ __device__ __forceinline__ bool mha_softmax(const MhaFwdParams& p, MhaMisc& m, u
   if (live && !join) p.lse[at] = sum == 0.f ? -INFINITY : (top * c + log2f(sum)) * 0.6931471805599453f;
   // the products and loads are done: the ring's memory holds the rows that are joined
   float* part = reinterpret_cast<float*>(sbase + C::kQBytes) + row * kMhaPartRow;
-  if (join) m.part[row] = make_float2(sum == 0.f ? -INFINITY : top * c, sum);
-  const float inv = sum == 0.f ? 0.f : (join ? 1.f : 1.f / sum);
+  if (join) {
+    m.part[row] = make_float2(sum == 0.f ? -INFINITY : top * c, sum);
 #pragma unroll
-  for (int i = 0; i < kMhaDv / 32; ++i) {
-    float x[32];
-    if (blocks > 0) tmem_load32(to + 32 * i, x);
-#pragma unroll
-    for (int k = 0; k < 32; ++k) x[k] = sum == 0.f ? 0.f : x[k] * inv;
-    if (join) {
+    for (int i = 0; i < kMhaDv / 32; ++i) {
+      float x[32];
+      if (blocks > 0) tmem_load32(to + 32 * i, x);
 #pragma unroll
       for (int k = 0; k < 32; k += 4)
-        *reinterpret_cast<float4*>(part + 32 * i + k) = make_float4(x[k], x[k + 1], x[k + 2], x[k + 3]);
-    } else if (live) {
+        *reinterpret_cast<float4*>(part + 32 * i + k) =
+            sum == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(x[k], x[k + 1], x[k + 2], x[k + 3]);
+    }
+  } else {
+    // the tile's Q is not needed any more: its memory is the stage, at 128 columns for half a row at a time
+    constexpr int kPieces = C::kSub * kMhaUnit >= kMhaTile * mha_stage_row<4>() ? 1 : 2, kCols = kMhaDv / kPieces;
+    const uint32_t stage = sb + t * C::kSub * kMhaUnit + row * mha_stage_row<kCols / 32>();
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) *reinterpret_cast<uint4*>(o + 32 * i + 8 * k) = pack8(x + 8 * k);
+    for (int i = 0; i < kPieces; ++i) {
+      mha_store_sums<kCols / 32>(o + kCols * i, stage, to + kCols * i, inv, blocks > 0, live);
+      bulk_wait();
     }
   }
   if (blocks > 0 && live && *reinterpret_cast<volatile int*>(&m.cleared)) {

@@ -333,13 +333,6 @@ sparse_mla_status_t mha_bwd_launch(const MhaRows& q, const MhaRows& k, const Mha
   p.k = static_cast<const __nv_bfloat16*>(k.p);
   p.k_tok = k.tok;
   p.k_head = k.head;
-  p.v = static_cast<const __nv_bfloat16*>(v.p);
-  p.v_tok = v.tok;
-  p.v_head = v.head;
-  p.dout = static_cast<const __nv_bfloat16*>(g.p);
-  p.do_tok = g.tok;
-  p.do_head = g.head;
-  p.out = static_cast<const __nv_bfloat16*>(out);
   p.lse = lse;
   p.delta = static_cast<float*>(workspace);
   p.dq = static_cast<__nv_bfloat16*>(dq);
@@ -352,6 +345,7 @@ sparse_mla_status_t mha_bwd_launch(const MhaRows& q, const MhaRows& k, const Mha
   // without rows on one side nothing of it is loaded: any map does
   const bool both = total_q > 0 && total_kv > 0;
   const MhaRows &mk = both ? k : (total_q > 0 ? q : k), &mv = both ? v : mk, &mq = both ? q : mk, &mg = both ? g : mk;
+  const MhaRows mo = both ? MhaRows{out, static_cast<long long>(h_q) * smla::kMhaDv, smla::kMhaDv} : mk;
   const int tk = both ? total_kv : (total_q > 0 ? total_q : total_kv), hk = both || total_q == 0 ? h_kv : h_q;
   const int tq = both ? total_q : tk, hq = both ? h_q : hk, dv_cols = both ? smla::kMhaDv : DQK;
   auto maps = [&](int rows, int keys) {   // of a query block and a key block
@@ -359,6 +353,7 @@ sparse_mla_status_t mha_bwd_launch(const MhaRows& q, const MhaRows& k, const Mha
     p.tok_tile = rows / p.pack;
     if ((st = mha_map(&p.map_q, mq, tq, hq, DQK, p.pack, p.tok_tile)) == SPARSE_MLA_OK &&
         (st = mha_map(&p.map_do, mg, tq, hq, dv_cols, p.pack, p.tok_tile)) == SPARSE_MLA_OK &&
+        (st = mha_map(&p.map_o, mo, tq, hq, dv_cols, p.pack, p.tok_tile)) == SPARSE_MLA_OK &&
         (st = mha_map(&p.map_k, mk, tk, hk, DQK, 1, keys)) == SPARSE_MLA_OK)
       st = mha_map(&p.map_v, mv, tk, hk, dv_cols, 1, keys);
     return st == SPARSE_MLA_OK;
