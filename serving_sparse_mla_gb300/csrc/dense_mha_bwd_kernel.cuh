@@ -225,7 +225,7 @@ __device__ __forceinline__ bool mha_dq_rows(const MhaBwdParams& p, MhaDqMisc& m,
     uint4 g[8];
     float dot = 0.f;
     if (live) lse2 = p.lse[at] * 1.4426950408889634f;
-    const bool there = mbar_wait(smem_u32(&m.o_full), 0, deadline, ab);   // all threads go on to their barrier
+    const bool there = warp_wait(smem_u32(&m.o_full), 0, deadline, ab);   // all threads go on to their barrier
     const uint32_t from = sb + half * kMhaUnit + row * 128;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -255,7 +255,7 @@ __device__ __forceinline__ bool mha_dq_rows(const MhaBwdParams& p, MhaDqMisc& m,
   const uint32_t ts = lane0 + C::kS + kHalf * half, tt = lane0 + C::kT + kHalf * half,
                  td = lane0 + C::kDs + kHalf / 2 * half;
   for (int j = 0; j < blocks; ++j) {
-    if (!mbar_wait(smem_u32(&m.s_full), j & 1, deadline, ab)) return false;
+    if (!warp_wait(smem_u32(&m.s_full), j & 1, deadline, ab)) return false;
     tc_fence_after();
     float s[kHalf], x[kHalf];
     tmem_load<kHalf>(ts, s);
@@ -265,7 +265,7 @@ __device__ __forceinline__ bool mha_dq_rows(const MhaBwdParams& p, MhaDqMisc& m,
     const bool edge = j >= whole;
     if (edge) {   // the product with dS must not meet what is not finite in a hidden key
       const int st = j % C::kKStages;
-      if (!mbar_wait(smem_u32(&m.k_full[st]), j / C::kKStages & 1, deadline, ab)) return false;
+      if (!warp_wait(smem_u32(&m.k_full[st]), j / C::kKStages & 1, deadline, ab)) return false;
       mha_clear(sb + C::kKOff + st * C::kKBytes, C::kKBytes);
     }
     const int sees = edge ? tok + lk - lq + 1 - j * C::kN - kHalf * half : kHalf;
@@ -275,7 +275,7 @@ __device__ __forceinline__ bool mha_dq_rows(const MhaBwdParams& p, MhaDqMisc& m,
       s[i] = fast_exp2(s[i]);
       s[i + 1] = fast_exp2(s[i + 1]);
     }
-    if (!mbar_wait(smem_u32(&m.t_full), j & 1, deadline, ab)) return false;
+    if (!warp_wait(smem_u32(&m.t_full), j & 1, deadline, ab)) return false;
     tc_fence_after();
     tmem_load<kHalf>(tt, x);
     tc_fence_before();
@@ -288,7 +288,7 @@ __device__ __forceinline__ bool mha_dq_rows(const MhaBwdParams& p, MhaDqMisc& m,
       for (int i = 0; i < kHalf; ++i) x[i] = i < sees ? x[i] : 0.f;
     }
     // the product with the dS before has ended when that block's keys are free
-    if (j > 0 && !mbar_wait(smem_u32(&m.k_empty[(j - 1) % C::kKStages]), (j - 1) / C::kKStages & 1, deadline, ab)) return false;
+    if (j > 0 && !warp_wait(smem_u32(&m.k_empty[(j - 1) % C::kKStages]), (j - 1) / C::kKStages & 1, deadline, ab)) return false;
     tc_fence_after();
     tmem_store_bf16<kHalf>(td, x);
     tmem_wait_st();
@@ -297,7 +297,7 @@ __device__ __forceinline__ bool mha_dq_rows(const MhaBwdParams& p, MhaDqMisc& m,
     if (lane_id() == 0) mbar_arrive(smem_u32(&m.ds_full));
   }
   if (blocks > 0) {
-    if (!mbar_wait(smem_u32(&m.dq_full), 0, deadline, ab)) return false;
+    if (!warp_wait(smem_u32(&m.dq_full), 0, deadline, ab)) return false;
     tc_fence_after();
   }
   // Q and K are not needed any more: their memory is the stage
@@ -574,7 +574,7 @@ __device__ __forceinline__ bool mha_dkv_stats(const MhaBwdParams& p, MhaDkvMisc&
         if (!(fabsf(d[i]) <= 3.402823466e38f)) l[i] = __uint_as_float(0x7fc00000u);
       }
     }
-    if (!mbar_wait(smem_u32(&m.stat_empty[st]), (j / kMhaStats & 1) ^ 1, deadline, ab)) return false;
+    if (!warp_wait(smem_u32(&m.stat_empty[st]), (j / kMhaStats & 1) ^ 1, deadline, ab)) return false;
 #pragma unroll
     for (int i = 0; i < C::kN / 32; ++i) {
       m.lse2[st][32 * i + lane] = l[i];
@@ -627,19 +627,19 @@ __device__ __forceinline__ bool mha_dkv_rows(const MhaBwdParams& p, MhaDkvMisc& 
     const int st = j % kMhaStats, qs = j % C::kStages, turn = j / C::kStages & 1;
     // where the block before is: its products with P and dS have ended when it is free
     const int before = (j - 1) % C::kStages, turn_before = (j - 1) / C::kStages & 1;
-    if (!mbar_wait(smem_u32(&m.s_full), j & 1, deadline, ab)) return false;
+    if (!warp_wait(smem_u32(&m.s_full), j & 1, deadline, ab)) return false;
     tc_fence_after();
     float x[kHalf], y[kHalf];
     tmem_load<kHalf>(ts, x);
     tc_fence_before();
     __syncwarp();
     if (lane_id() == 0) mbar_arrive(smem_u32(&m.s_free));
-    if (!mbar_wait(smem_u32(&m.stat_full[st]), j / kMhaStats & 1, deadline, ab)) return false;
+    if (!warp_wait(smem_u32(&m.stat_full[st]), j / kMhaStats & 1, deadline, ab)) return false;
     if (edge) {
       // the products with P and dS must not meet what is not finite in a row that does not
       // see a key; the product that gives T has read dout by then
-      if (!mbar_wait(smem_u32(&m.t_full), j & 1, deadline, ab)) return false;
-      if (!mbar_wait(smem_u32(&m.q_full[qs]), turn, deadline, ab) || !mbar_wait(smem_u32(&m.do_full[qs]), turn, deadline, ab))
+      if (!warp_wait(smem_u32(&m.t_full), j & 1, deadline, ab)) return false;
+      if (!warp_wait(smem_u32(&m.q_full[qs]), turn, deadline, ab) || !warp_wait(smem_u32(&m.do_full[qs]), turn, deadline, ab))
         return false;
       mha_clear(sb + C::kQOff + qs * C::kQBytes, C::kQBytes);
       mha_clear(sb + C::kDoOff + qs * C::kDoBytes, C::kDoBytes);
@@ -657,14 +657,14 @@ __device__ __forceinline__ bool mha_dkv_rows(const MhaBwdParams& p, MhaDkvMisc& 
 #pragma unroll
       for (int i = 0; i < kHalf; ++i) x[i] = i >= lo && i < hi ? x[i] : 0.f;
     }
-    if (j > 0 && !mbar_wait(smem_u32(&m.empty[before]), turn_before, deadline, ab)) return false;
+    if (j > 0 && !warp_wait(smem_u32(&m.empty[before]), turn_before, deadline, ab)) return false;
     tc_fence_after();
     tmem_store_bf16<kHalf>(tp, x);
     tmem_wait_st();
     tc_fence_before();
     __syncwarp();
     if (lane_id() == 0) mbar_arrive(smem_u32(&m.p_full));
-    if (!mbar_wait(smem_u32(&m.t_full), j & 1, deadline, ab)) return false;
+    if (!warp_wait(smem_u32(&m.t_full), j & 1, deadline, ab)) return false;
     tc_fence_after();
     tmem_load<kHalf>(tt, y);
     tc_fence_before();
@@ -693,7 +693,7 @@ __device__ __forceinline__ bool mha_dkv_rows(const MhaBwdParams& p, MhaDkvMisc& 
     }
   }
   if (s.total > 0) {
-    if (!mbar_wait(smem_u32(&m.out_full), 0, deadline, ab)) return false;
+    if (!warp_wait(smem_u32(&m.out_full), 0, deadline, ab)) return false;
     tc_fence_after();
   }
   const size_t at = live ? static_cast<size_t>(w.k0 + key) * p.h_kv + kvh : 0;

@@ -741,11 +741,11 @@ __device__ __forceinline__ bool mha_softmax(const MhaFwdParams& p, MhaMisc& m, u
     if (j >= whole) {
       for (int i = 0; i < 2; ++i) {   // the block's V: units behind those of the K before it and of the V before it
         const uint32_t n = static_cast<uint32_t>(min(j + C::kAhead, s.most) * C::kSub + 2 * j + i);
-        if (!mbar_wait(smem_u32(&m.full[n % C::kUnits]), n / C::kUnits & 1u, deadline, ab)) return false;
+        if (!warp_wait(smem_u32(&m.full[n % C::kUnits]), n / C::kUnits & 1u, deadline, ab)) return false;
         if (mha_clear(sb + C::kQBytes + n % C::kUnits * kMhaUnit, kMhaUnit)) m.cleared = 1;
       }
     }
-    if (!mbar_wait(smem_u32(&m.s_full[buf]), par, deadline, ab)) return false;
+    if (!warp_wait(smem_u32(&m.s_full[buf]), par, deadline, ab)) return false;
     tc_fence_after();
     float v[kMhaTile];
     tmem_load128(ts, v);
@@ -765,7 +765,7 @@ __device__ __forceinline__ bool mha_softmax(const MhaFwdParams& p, MhaMisc& m, u
     if (__any_sync(0xffffffffu, grown)) {
       // O is this warp's to change once the product before has ended: with two tiles the block's scores came after it
       if (NT == 1 && j > 0) {
-        if (!mbar_wait(smem_u32(&m.o_step), (j - 1) & 1, deadline, ab)) return false;
+        if (!warp_wait(smem_u32(&m.o_step), (j - 1) & 1, deadline, ab)) return false;
         tc_fence_after();
       }
       const float f = grown ? fast_exp2((top - now) * c) : 1.f;
@@ -809,7 +809,7 @@ __device__ __forceinline__ bool mha_softmax(const MhaFwdParams& p, MhaMisc& m, u
   const size_t at = live ? static_cast<size_t>(w.q0 + tok) * p.h_q + pack0 + row % p.pack : 0;
   __nv_bfloat16* o = p.out + at * kMhaDv;
   if (blocks > 0) {
-    if (!mbar_wait(smem_u32(&m.o_full[t]), 0, deadline, ab)) return false;
+    if (!warp_wait(smem_u32(&m.o_full[t]), 0, deadline, ab)) return false;
     tc_fence_after();
   }
   const bool join = NT == 1 && p.cluster > 1;
