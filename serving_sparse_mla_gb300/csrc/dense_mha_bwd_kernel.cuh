@@ -266,7 +266,7 @@ __device__ __forceinline__ bool mha_dq_rows(const MhaBwdParams& p, MhaDqMisc& m,
     if (edge) {   // the product with dS must not meet what is not finite in a hidden key
       const int st = j % C::kKStages;
       if (!warp_wait(smem_u32(&m.k_full[st]), j / C::kKStages & 1, deadline, ab)) return false;
-      mha_clear(sb + C::kKOff + st * C::kKBytes, C::kKBytes);
+      mha_clear<256>(sb + C::kKOff + st * C::kKBytes, C::kKBytes);
     }
     const int sees = edge ? tok + lk - lq + 1 - j * C::kN - kHalf * half : kHalf;
 #pragma unroll
@@ -405,7 +405,7 @@ constexpr int kMhaStats = 4;   // query blocks whose lse and D are held
 
 struct __align__(16) MhaDkvMisc {
   uint64_t k_full, k_ready, q_full[4], do_full[4], empty[4], stat_full[kMhaStats], stat_empty[kMhaStats];
-  uint64_t s_full, s_free, p_full, t_full, t_free, ds_full, out_full, drain[2];
+  uint64_t s_full, s_free, p_full, p_free, t_full, t_free, ds_full, out_full, drain[2];
   uint32_t tmem_base;
   int abort_flag;
   int prior_error;
@@ -537,6 +537,7 @@ __device__ __forceinline__ bool mha_dkv_sums(const MhaBwdParams& p, MhaDkvMisc& 
 #pragma unroll
     for (int kk = 0; kk < C::kN / 16; ++kk)
       mma_ts(chosen, C::kDv, C::kP + 8 * kk, desc_plus(g, kk * 2048), kIdescV, j + kk > 0 ? 1u : 0u);
+    commit_to(chosen, &m.p_free);
     if (!warp_wait(smem_u32(&m.ds_full), j & 1, deadline, ab)) return false;
     if (!warp_wait(smem_u32(&m.q_full[st]), turn, deadline, ab)) return false;   // long past
     tc_fence_after();
@@ -625,7 +626,7 @@ __device__ __forceinline__ bool mha_dkv_rows(const MhaBwdParams& p, MhaDkvMisc& 
     const int lo = edge ? p.pack * (key - (lk - lq) - t0) - kHalf * half : 0;
     const int hi = edge ? p.pack * (lq - t0) - kHalf * half : kHalf;
     const int st = j % kMhaStats, qs = j % C::kStages, turn = j / C::kStages & 1;
-    // where the block before is: its products with P and dS have ended when it is free
+    // where the block before is: its product with dS has ended when it is free
     const int before = (j - 1) % C::kStages, turn_before = (j - 1) / C::kStages & 1;
     if (!warp_wait(smem_u32(&m.s_full), j & 1, deadline, ab)) return false;
     tc_fence_after();
@@ -641,8 +642,8 @@ __device__ __forceinline__ bool mha_dkv_rows(const MhaBwdParams& p, MhaDkvMisc& 
       if (!warp_wait(smem_u32(&m.t_full), j & 1, deadline, ab)) return false;
       if (!warp_wait(smem_u32(&m.q_full[qs]), turn, deadline, ab) || !warp_wait(smem_u32(&m.do_full[qs]), turn, deadline, ab))
         return false;
-      mha_clear(sb + C::kQOff + qs * C::kQBytes, C::kQBytes);
-      mha_clear(sb + C::kDoOff + qs * C::kDoBytes, C::kDoBytes);
+      mha_clear<256>(sb + C::kQOff + qs * C::kQBytes, C::kQBytes);
+      mha_clear<256>(sb + C::kDoOff + qs * C::kDoBytes, C::kDoBytes);
     }
     const float4* l4 = reinterpret_cast<const float4*>(&m.lse2[st][kHalf * half]);
 #pragma unroll
@@ -657,7 +658,7 @@ __device__ __forceinline__ bool mha_dkv_rows(const MhaBwdParams& p, MhaDkvMisc& 
 #pragma unroll
       for (int i = 0; i < kHalf; ++i) x[i] = i >= lo && i < hi ? x[i] : 0.f;
     }
-    if (j > 0 && !warp_wait(smem_u32(&m.empty[before]), turn_before, deadline, ab)) return false;
+    if (j > 0 && !warp_wait(smem_u32(&m.p_free), (j - 1) & 1, deadline, ab)) return false;
     tc_fence_after();
     tmem_store_bf16<kHalf>(tp, x);
     tmem_wait_st();
@@ -683,6 +684,8 @@ __device__ __forceinline__ bool mha_dkv_rows(const MhaBwdParams& p, MhaDkvMisc& 
 #pragma unroll
       for (int i = 0; i < kHalf; ++i) y[i] = i >= lo && i < hi ? y[i] : 0.f;
     }
+    if (j > 0 && !warp_wait(smem_u32(&m.empty[before]), turn_before, deadline, ab)) return false;
+    tc_fence_after();
     tmem_store_bf16<kHalf>(td, y);
     tmem_wait_st();
     tc_fence_before();
@@ -734,6 +737,7 @@ __global__ void __launch_bounds__(MhaDkvShape<DQK>::kThreads, 1) dense_mha_dkv_k
     mbar_init(smem_u32(&m.s_full), 1);
     mbar_init(smem_u32(&m.s_free), 8);
     mbar_init(smem_u32(&m.p_full), 8);
+    mbar_init(smem_u32(&m.p_free), 1);
     mbar_init(smem_u32(&m.t_full), 1);
     mbar_init(smem_u32(&m.t_free), 8);
     mbar_init(smem_u32(&m.ds_full), 8);

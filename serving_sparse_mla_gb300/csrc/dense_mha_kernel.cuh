@@ -690,11 +690,12 @@ __device__ __forceinline__ bool mha_mma(const MhaFwdParams& p, MhaMisc& m, uint3
 
 // A hidden key's weight is 0, but 0 times an infinity or a NaN is a NaN: before a product
 // with a block that some rows do not see all of, values that are not finite are taken
-// out of it.  Each of 128 threads looks over an eighth of a KB of `bytes`, a multiple of
-// 2 KB; true where it found some.
+// out of it.  Each of N threads (the CTA's first, or the N behind them) looks over its share
+// of `bytes`, a multiple of 2 KB; true where it found some.
+template <int N>
 __device__ __forceinline__ bool mha_clear(uint32_t tile, uint32_t bytes) {
   uint32_t seen = 0;
-  for (uint32_t at = (threadIdx.x & 127u) * 16; at < bytes; at += 2048) {
+  for (uint32_t at = threadIdx.x % N * 16; at < bytes; at += N * 16) {
     uint32_t x[4];
     asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                  : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]) : "r"(tile + at));
@@ -703,7 +704,7 @@ __device__ __forceinline__ bool mha_clear(uint32_t tile, uint32_t bytes) {
     for (int i = 0; i < 4; ++i) seen |= (x[i] & 0x7fff7fffu) + 0x00800080u;
   }
   if ((seen & 0x80008000u) == 0u) return false;
-  for (uint32_t at = (threadIdx.x & 127u) * 16; at < bytes; at += 2048) {
+  for (uint32_t at = threadIdx.x % N * 16; at < bytes; at += N * 16) {
     uint32_t x[4];
     asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                  : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]) : "r"(tile + at));
@@ -742,7 +743,7 @@ __device__ __forceinline__ bool mha_softmax(const MhaFwdParams& p, MhaMisc& m, u
       for (int i = 0; i < 2; ++i) {   // the block's V: units behind those of the K before it and of the V before it
         const uint32_t n = static_cast<uint32_t>(min(j + C::kAhead, s.most) * C::kSub + 2 * j + i);
         if (!warp_wait(smem_u32(&m.full[n % C::kUnits]), n / C::kUnits & 1u, deadline, ab)) return false;
-        if (mha_clear(sb + C::kQBytes + n % C::kUnits * kMhaUnit, kMhaUnit)) m.cleared = 1;
+        if (mha_clear<128>(sb + C::kQBytes + n % C::kUnits * kMhaUnit, kMhaUnit)) m.cleared = 1;
       }
     }
     if (!warp_wait(smem_u32(&m.s_full[buf]), par, deadline, ab)) return false;
