@@ -490,6 +490,18 @@ def _launch(go, dev, stream, where: str):
     return results
 
 
+def _run(call, dev, stream, where: str, *args):
+    """call(stream handle, *args) -> (status, results), as _launch has it, without a closure."""
+    if stream is None and dev.index == torch._C._cuda_getDevice():
+        st, results = call(torch._C._cuda_getCurrentRawStream(dev.index), *args)
+    else:
+        with _launch_on(dev, stream) as cs:
+            st, results = call(cs, *args)
+    if st != 0:
+        raise SparseMLAError(st, where)
+    return results
+
+
 def decode_fp4_workspace_size(batch: int, s_next: int, h_q: int, topk: int, d_v: int = 512) -> int:
     """Bytes sparse_mla_decode_fp4 needs on the current device."""
     return int(load().sparse_mla_decode_fp4_workspace_size(batch, s_next, h_q, d_v, topk))
@@ -703,10 +715,6 @@ def mla_norm_rope_bwd(q, kv, positions, cos_sin, dq, dkv, q_weight=None, kv_weig
 
 def _wide_rows(t: torch.Tensor, n: int, d: int, name: str, dev) -> int:
     """Row stride in elements of bf16 rows [n, d], contiguous in themselves, each on 16 bytes."""
-    if t.is_cuda and t.dtype is _BF16 and t.device == dev and t.shape == (n, d):
-        step, one = t.stride()
-        if one == 1 and not step & 7 and not t.data_ptr() & 15:
-            return step
     _on_cuda(t, name)
     if t.dtype != _BF16:
         raise ValueError(f"{name} must be {_BF16}, got {t.dtype}")
@@ -719,12 +727,36 @@ def _wide_rows(t: torch.Tensor, n: int, d: int, name: str, dev) -> int:
     return step
 
 
-def _norm_weight(weight: torch.Tensor, d: int, dev) -> None:
-    if weight.dtype is _BF16 and weight.device == dev and weight.is_contiguous() and weight.numel() == d and weight.is_cuda:
-        return
+def _norm_rows(x, weight, others, names):
+    """(n, d, device, row strides of x and of the others) of checked rows [n, d] and their weight [d]."""
+    shape, dev = x.shape, x.device
+    if len(shape) != 2:
+        raise ValueError(f"{names[0]} must be [n, d], got {tuple(shape)}")
+    n, d = shape
+    step, one = x.stride()
+    bits = step & 7 | x.data_ptr() & 15
+    good = (x.is_cuda and x.dtype is _BF16 and one == 1 and weight.dtype is _BF16 and weight.device == dev
+            and weight.numel() == d and weight.is_contiguous())
+    steps = [step]
+    for t in others:
+        if t is None:
+            steps.append(0)
+            continue
+        if not (t.dtype is _BF16 and t.device == dev and t.shape == shape):
+            good = False
+            break
+        step, one = t.stride()
+        good = good and one == 1
+        bits |= step & 7 | t.data_ptr() & 15
+        steps.append(step)
+    if good and not bits:
+        return n, d, dev, steps
+    steps = [_wide_rows(x, n, d, names[0], dev)]
     _given(weight, _BF16, "weight", d, dev)
     if weight.numel() != d:
         raise ValueError(f"weight must hold {d} values, got {weight.numel()}")
+    steps += [0 if t is None else _wide_rows(t, n, d, name, dev) for t, name in zip(others, names[1:])]
+    return n, d, dev, steps
 
 
 def _apart(out: Optional[torch.Tensor], name: str, size: int, inputs, same=()) -> None:
@@ -759,14 +791,7 @@ def mla_add_norm(x, weight, residual=None, eps: float = 1e-6, group: Optional[in
     row.  -> (out [n, d], scales [n, ceil(d / 128)] or [n, 1] fp32 or None,
     residual_out [n, d] bf16: z, or x itself where no residual is given).
     residual_out may be x or residual."""
-    lib = load()
-    if x.dim() != 2:
-        raise ValueError(f"x must be [n, d], got {tuple(x.shape)}")
-    n, d = x.shape
-    dev = x.device
-    x_step = _wide_rows(x, n, d, "x", dev)
-    _norm_weight(weight, d, dev)
-    res_step = 0 if residual is None else _wide_rows(residual, n, d, "residual", dev)
+    n, d, dev, (x_step, res_step) = _norm_rows(x, weight, (residual,), ("x", "residual"))
     if group is None:
         form, n_scales, kind, width = 0, 0, _BF16, 2
     elif group == 128 or group == 0:
@@ -787,18 +812,25 @@ def mla_add_norm(x, weight, residual=None, eps: float = 1e-6, group: Optional[in
         _apart(out, "out", width * n * d, reads)
         _apart(scales, "scales", 4 * n * n_scales, reads + ((out, 0, "out"),))
 
-    def go(cs):
-        o = torch.empty((n, d), dtype=kind, device=dev) if out is None else out
-        sc = torch.empty((n, n_scales), dtype=_F32, device=dev) if form and scales is None else scales
-        if residual is None:
-            z, res_at, z_at = x, None, None
-        else:
-            z = torch.empty((n, d), dtype=_BF16, device=dev) if residual_out is None else residual_out
-            res_at, z_at = residual.data_ptr(), z.data_ptr()
-        return lib.mla_add_norm(x.data_ptr(), x_step, res_at, res_step, weight.data_ptr(), eps, o.data_ptr(),
-                                sc.data_ptr() if form else None, form, z_at, n, d, cs), (o, sc, z)
+    return _run(_add_norm, dev, stream, "mla_add_norm", x, x_step, residual, res_step, weight, eps, out, scales, form,
+                n_scales, kind, residual_out, n, d)
 
-    return _launch(go, dev, stream, "mla_add_norm")
+
+def _add_norm(cs, x, x_step, residual, res_step, weight, eps, out, scales, form, n_scales, kind, z, n, d):
+    dev = x.device
+    if out is None:
+        out = torch.empty((n, d), dtype=kind, device=dev)
+    if form and scales is None:
+        scales = torch.empty((n, n_scales), dtype=_F32, device=dev)
+    res_at = z_at = None
+    if residual is None:
+        z = x
+    else:
+        if z is None:
+            z = torch.empty((n, d), dtype=_BF16, device=dev)
+        res_at, z_at = residual.data_ptr(), z.data_ptr()
+    return load().mla_add_norm(x.data_ptr(), x_step, res_at, res_step, weight.data_ptr(), eps, out.data_ptr(),
+                               scales.data_ptr() if form else None, form, z_at, n, d, cs), (out, scales, z)
 
 
 def add_norm_bwd_workspace_size(n: int, d: int) -> int:
@@ -813,15 +845,7 @@ def mla_add_norm_bwd(z, weight, dout, dresidual=None, eps: float = 1e-6, workspa
     layers (or None), all bf16, rows strided as they are -> (dx [n, d] bf16, the
     gradient of x and of the residual alike, dweight [d] fp32).  dx may be dout or
     dresidual."""
-    lib = load()
-    if z.dim() != 2:
-        raise ValueError(f"z must be [n, d], got {tuple(z.shape)}")
-    n, d = z.shape
-    dev = z.device
-    z_step = _wide_rows(z, n, d, "z", dev)
-    _norm_weight(weight, d, dev)
-    g_step = _wide_rows(dout, n, d, "dout", dev)
-    r_step = 0 if dresidual is None else _wide_rows(dresidual, n, d, "dresidual", dev)
+    n, d, dev, (z_step, g_step, r_step) = _norm_rows(z, weight, (dout, dresidual), ("z", "dout", "dresidual"))
     if dx is not None or dweight is not None or workspace is not None:
         _given(dx, _BF16, "dx", n * d, dev)
         _given(dweight, _F32, "dweight", d, dev)
@@ -833,17 +857,21 @@ def mla_add_norm_bwd(z, weight, dout, dresidual=None, eps: float = 1e-6, workspa
         if workspace is not None:
             _apart(workspace, "workspace", workspace.numel() * workspace.element_size(), reads + ((dweight, 0, "dweight"),))
 
-    def go(cs):
-        gx = torch.empty((n, d), dtype=_BF16, device=dev) if dx is None else dx
-        gw = torch.empty(d, dtype=_F32, device=dev) if dweight is None else dweight
-        ws = workspace
-        if ws is None:
-            ws = torch.empty(max(16, lib.mla_add_norm_bwd_workspace_size(n, d)), dtype=_U8, device=dev)
-        return lib.mla_add_norm_bwd(z.data_ptr(), z_step, weight.data_ptr(), eps, dout.data_ptr(), g_step,
-                                    _at(dresidual), r_step, gx.data_ptr(), gw.data_ptr(), n, d, ws.data_ptr(),
-                                    ws.numel() * ws.element_size(), cs), (gx, gw)
+    return _run(_add_norm_bwd, dev, stream, "mla_add_norm_bwd", z, z_step, weight, eps, dout, g_step, dresidual, r_step, dx,
+                dweight, workspace, n, d)
 
-    return _launch(go, dev, stream, "mla_add_norm_bwd")
+
+def _add_norm_bwd(cs, z, z_step, weight, eps, dout, g_step, dresidual, r_step, dx, dweight, ws, n, d):
+    lib, dev = load(), z.device
+    if dx is None:
+        dx = torch.empty((n, d), dtype=_BF16, device=dev)
+    if dweight is None:
+        dweight = torch.empty(d, dtype=_F32, device=dev)
+    if ws is None:
+        ws = torch.empty(max(16, lib.mla_add_norm_bwd_workspace_size(n, d)), dtype=_U8, device=dev)
+    return lib.mla_add_norm_bwd(z.data_ptr(), z_step, weight.data_ptr(), eps, dout.data_ptr(), g_step, _at(dresidual),
+                                r_step, dx.data_ptr(), dweight.data_ptr(), n, d, ws.data_ptr(),
+                                ws.numel() * ws.element_size(), cs), (dx, dweight)
 
 
 # ---------------------------------------------------------------- dense causal attention
@@ -917,21 +945,27 @@ def dense_mha_fwd(q, k, v, sm_scale, cu_seqlens_q=None, cu_seqlens_kv=None, out:
     sequence); a sequence's queries are its last positions.  -> (out [total_q, h_q,
     128] bf16, lse [total_q, h_q] fp32).  Rows behind the last sequence are left as
     they were in outputs that are given, zeros and -inf in those made here."""
-    lib = load()
     total_q, total_kv, h_q, h_kv, d_qk, d_v, batch, dev, steps = _mha_args(q, k, v, cu_seqlens_q, cu_seqlens_kv)
-    _given(out, _BF16, "out", total_q * h_q * d_v, dev)
-    _given(lse, _F32, "lse", total_q * h_q, dev)
+    if out is not None:
+        _given(out, _BF16, "out", total_q * h_q * d_v, dev)
+    if lse is not None:
+        _given(lse, _F32, "lse", total_q * h_q, dev)
     fill = (_MHA_FILL_OUT if out is None else 0) | (_MHA_FILL_LSE if lse is None else 0)
 
-    def go(cs):
-        o = torch.empty((total_q, h_q, d_v), dtype=_BF16, device=dev) if out is None else out
-        ls = torch.empty((total_q, h_q), dtype=_F32, device=dev) if lse is None else lse
-        return lib.dense_mha_fwd(q.data_ptr(), steps[0], steps[1], k.data_ptr(), steps[2], steps[3], v.data_ptr(),
-                                 steps[4], steps[5], _at(cu_seqlens_q), _at(cu_seqlens_kv), batch, sm_scale,
-                                 o.data_ptr(), ls.data_ptr(), fill, total_q, total_kv, h_q, h_kv, d_qk, d_v,
-                                 cs), (o, ls)
+    return _run(_mha_fwd, dev, stream, "dense_mha_fwd", q, k, v, steps, cu_seqlens_q, cu_seqlens_kv, batch, sm_scale, out,
+                lse, fill, total_q, total_kv, h_q, h_kv, d_qk, d_v)
 
-    return _launch(go, dev, stream, "dense_mha_fwd")
+
+def _mha_fwd(cs, q, k, v, steps, cu_q, cu_kv, batch, sm_scale, out, lse, fill, total_q, total_kv, h_q, h_kv, d_qk, d_v):
+    dev = q.device
+    if out is None:
+        out = torch.empty((total_q, h_q, d_v), dtype=_BF16, device=dev)
+    if lse is None:
+        lse = torch.empty((total_q, h_q), dtype=_F32, device=dev)
+    qt, qh, kt, kh, vt, vh = steps
+    return load().dense_mha_fwd(q.data_ptr(), qt, qh, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, _at(cu_q), _at(cu_kv),
+                                batch, sm_scale, out.data_ptr(), lse.data_ptr(), fill, total_q, total_kv, h_q, h_kv, d_qk,
+                                d_v, cs), (out, lse)
 
 
 def dense_mha_bwd_workspace_size(total_q: int, total_kv: int, batch: int, h_q: int, h_kv: int, d_qk: int,
@@ -946,33 +980,38 @@ def dense_mha_bwd(q, k, v, sm_scale, out, lse, dout, cu_seqlens_q=None, cu_seqle
     """Gradients of dense_mha_fwd from its out and lse and the gradient dout [total_q,
     h_q, 128] bf16 of out -> (dq, dk, dv), bf16, dense, of the shapes of q, k and v.
     Rows behind the last sequence get zeros."""
-    lib = load()
     total_q, total_kv, h_q, h_kv, d_qk, d_v, batch, dev, steps = _mha_args(q, k, v, cu_seqlens_q, cu_seqlens_kv)
     _given(out, _BF16, "out", total_q * h_q * d_v, dev)
     _given(lse, _F32, "lse", total_q * h_q, dev)
     steps += _heads(dout, "dout", dev)
-    if tuple(dout.shape) != (total_q, h_q, d_v):
+    if dout.shape != (total_q, h_q, d_v):
         raise ValueError(f"dout must be [{total_q}, {h_q}, {d_v}], got {tuple(dout.shape)}")
-    _given(dq, _BF16, "dq", total_q * h_q * d_qk, dev)
-    _given(dk, _BF16, "dk", total_kv * h_kv * d_qk, dev)
-    _given(dv, _BF16, "dv", total_kv * h_kv * d_v, dev)
-    _workspace(workspace, dev)
+    if dq is not None or dk is not None or dv is not None or workspace is not None:
+        _given(dq, _BF16, "dq", total_q * h_q * d_qk, dev)
+        _given(dk, _BF16, "dk", total_kv * h_kv * d_qk, dev)
+        _given(dv, _BF16, "dv", total_kv * h_kv * d_v, dev)
+        _workspace(workspace, dev)
+    return _run(_mha_bwd, dev, stream, "dense_mha_bwd", q, k, v, steps, cu_seqlens_q, cu_seqlens_kv, batch, sm_scale, out,
+                lse, dout, dq, dk, dv, workspace, total_q, total_kv, h_q, h_kv, d_qk, d_v)
 
-    def go(cs):
-        gq = torch.empty((total_q, h_q, d_qk), dtype=_BF16, device=dev) if dq is None else dq
-        gk = torch.empty((total_kv, h_kv, d_qk), dtype=_BF16, device=dev) if dk is None else dk
-        gv = torch.empty((total_kv, h_kv, d_v), dtype=_BF16, device=dev) if dv is None else dv
-        ws = workspace
-        if ws is None:
-            need = lib.dense_mha_bwd_workspace_size(total_q, total_kv, batch, h_q, h_kv, d_qk, d_v)
-            ws = torch.empty(max(16, need), dtype=_U8, device=dev)
-        return lib.dense_mha_bwd(q.data_ptr(), steps[0], steps[1], k.data_ptr(), steps[2], steps[3], v.data_ptr(),
-                                 steps[4], steps[5], _at(cu_seqlens_q), _at(cu_seqlens_kv), batch, sm_scale,
-                                 out.data_ptr(), lse.data_ptr(), dout.data_ptr(), steps[6], steps[7], gq.data_ptr(),
-                                 gk.data_ptr(), gv.data_ptr(), total_q, total_kv, h_q, h_kv, d_qk, d_v,
-                                 ws.data_ptr(), ws.numel() * ws.element_size(), cs), (gq, gk, gv)
 
-    return _launch(go, dev, stream, "dense_mha_bwd")
+def _mha_bwd(cs, q, k, v, steps, cu_q, cu_kv, batch, sm_scale, out, lse, dout, dq, dk, dv, ws, total_q, total_kv, h_q, h_kv,
+             d_qk, d_v):
+    lib, dev = load(), q.device
+    if dq is None:
+        dq = torch.empty((total_q, h_q, d_qk), dtype=_BF16, device=dev)
+    if dk is None:
+        dk = torch.empty((total_kv, h_kv, d_qk), dtype=_BF16, device=dev)
+    if dv is None:
+        dv = torch.empty((total_kv, h_kv, d_v), dtype=_BF16, device=dev)
+    if ws is None:
+        need = lib.dense_mha_bwd_workspace_size(total_q, total_kv, batch, h_q, h_kv, d_qk, d_v)
+        ws = torch.empty(max(16, need), dtype=_U8, device=dev)
+    qt, qh, kt, kh, vt, vh, gt, gh = steps
+    return lib.dense_mha_bwd(q.data_ptr(), qt, qh, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, _at(cu_q), _at(cu_kv), batch,
+                             sm_scale, out.data_ptr(), lse.data_ptr(), dout.data_ptr(), gt, gh, dq.data_ptr(),
+                             dk.data_ptr(), dv.data_ptr(), total_q, total_kv, h_q, h_kv, d_qk, d_v, ws.data_ptr(),
+                             ws.numel() * ws.element_size(), cs), (dq, dk, dv)
 
 
 # ---------------------------------------------------------------- debug: valid entries per token
