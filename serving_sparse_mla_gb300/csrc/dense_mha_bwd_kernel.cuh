@@ -58,7 +58,8 @@ struct MhaBwdParams {
   int batch, total_q, total_kv, h_q, h_kv, group;
   int pack, tok_tile;                      // rows of a query tile: tok_tile tokens x pack heads
   int slots;                               // tiles per head (pack) that the grid has room for
-  int heads, heads_near;                   // head packs (of keys: heads); of so many at a time the longest tiles come first
+  int heads;                               // head packs (of keys: heads)
+  MhaHeads order;
   float scale, scale_log2;
   const __nv_bfloat16* k;                  // row (t, h) at k + t k_tok + h k_head
   long long k_tok, k_head;
@@ -271,7 +272,7 @@ __device__ __forceinline__ bool mha_dq_rows(const MhaBwdParams& p, MhaDqMisc& m,
     const int sees = edge ? tok + lk - lq + 1 - j * C::kN - kHalf * half : kHalf;
 #pragma unroll
     for (int i = 0; i < kHalf; i += 2) {
-      scale_shift2(s[i], s[i + 1], p.scale_log2, -lse2);
+      scale_shift2(s[i], s[i + 1], p.scale_log2, -lse2, -lse2);
       s[i] = fast_exp2(s[i]);
       s[i + 1] = fast_exp2(s[i + 1]);
     }
@@ -282,7 +283,7 @@ __device__ __forceinline__ bool mha_dq_rows(const MhaBwdParams& p, MhaDqMisc& m,
     __syncwarp();
     if (lane_id() == 0) mbar_arrive(smem_u32(&m.t_free));
 #pragma unroll
-    for (int i = 0; i < kHalf; ++i) x[i] = s[i] * (x[i] - delta);
+    for (int i = 0; i < kHalf; i += 2) weigh2(s[i], s[i + 1], x[i], x[i + 1], -delta, -delta);
     if (edge) {
 #pragma unroll
       for (int i = 0; i < kHalf; ++i) x[i] = i < sees ? x[i] : 0.f;
@@ -317,7 +318,7 @@ __global__ void __launch_bounds__(MhaDqShape<DQK>::kThreads, 1) dense_mha_dq_ker
   const uint32_t sb = smem_u32(sbase);
   asm volatile("griddepcontrol.launch_dependents;");   // dk's and dv's kernel may be set up (it waits for this grid's end)
   int slot, head;
-  mha_unit(blockIdx.x, p.slots, p.heads, p.heads_near, slot, head);
+  mha_unit(blockIdx.x, p.slots, p.heads, p.order, slot, head);
   const int pack0 = head * p.pack;
 
   if (threadIdx.x == 0) {
@@ -401,17 +402,15 @@ __global__ void __launch_bounds__(MhaDqShape<DQK>::kThreads, 1) dense_mha_dq_ker
 
 // ------------------------------------------------------------------ dk, dv
 
-constexpr int kMhaStats = 4;   // query blocks whose lse and D are held
-
 struct __align__(16) MhaDkvMisc {
-  uint64_t k_full, k_ready, q_full[4], do_full[4], empty[4], stat_full[kMhaStats], stat_empty[kMhaStats];
+  uint64_t k_full, k_ready, q_full[4], do_full[4], empty[4];
   uint64_t s_full, s_free, p_full, p_free, t_full, t_free, ds_full, out_full, drain[2];
   uint32_t tmem_base;
   int abort_flag;
   int prior_error;
   MhaWork work;
-  alignas(16) float lse2[kMhaStats][kMhaTile];    // read four at a time
-  alignas(16) float delta[kMhaStats][kMhaTile];
+  alignas(16) float shift[4][64];     // -lse in powers of two and -D of a block's rows, read four at a time
+  alignas(16) float minus_d[4][64];
 };
 
 template <int DQK>
@@ -427,6 +426,7 @@ struct MhaDkvShape {
   static constexpr uint32_t kMiscOff = kDoOff + kStages * kDoBytes;
   static constexpr int kBytes = static_cast<int>(kMiscOff) + static_cast<int>(sizeof(MhaDkvMisc)) + 1024;
   static constexpr int kThreads = 12 * 32;
+  static_assert(kN == 64 && kStages <= 4, "rows and barriers of MhaDkvMisc");
   // columns of TMEM
   static constexpr uint32_t kDv = 0, kDk = 128, kS = 128 + DQK, kT = kS + kN, kP = kT + kN, kDs = kP + kN / 2, kK = 448;
   static_assert(kBytes <= kMaxSmem, "shared memory");
@@ -458,10 +458,10 @@ __device__ __forceinline__ bool mha_dkv_load(const MhaBwdParams& p, MhaDkvMisc& 
     tma_load_3d(sb + c * kMhaUnit, &p.map_k, 64 * c, kvh, w.k0 + w.tile * kMhaTile, kb);
   for (int c = 0; c < 2; ++c) tma_load_3d(sb + C::kVOff + c * kMhaUnit, &p.map_v, 64 * c, kvh, w.k0 + w.tile * kMhaTile, kb);
   const uint32_t bytes = static_cast<uint32_t>(p.pack * p.tok_tile) * 128u;
-  int head = kvh * p.group, b = 0;
+  int head = kvh * p.group, b = 0, st = 0, turn = 0;
   for (int j = 0; j < s.total; ++j) {
-    const int st = j % C::kStages, par = j / C::kStages & 1, tok = w.q0 + s.first + b * p.tok_tile;
-    if (!mbar_wait(smem_u32(&m.empty[st]), par ^ 1, deadline, ab)) return false;
+    const int tok = w.q0 + s.first + b * p.tok_tile;
+    if (!mbar_wait(smem_u32(&m.empty[st]), turn ^ 1, deadline, ab)) return false;
     uint32_t bar = smem_u32(&m.q_full[st]);
     mbar_arrive_expect_tx(bar, C::kSub * bytes);
     for (int c = 0; c < C::kSub; ++c)
@@ -471,6 +471,10 @@ __device__ __forceinline__ bool mha_dkv_load(const MhaBwdParams& p, MhaDkvMisc& 
     ++fills;
     for (int c = 0; c < 2; ++c)
       tma_load_3d(sb + C::kDoOff + st * C::kDoBytes + c * C::kQUnit, &p.map_do, 64 * c, head, tok, bar);
+    if (++st == C::kStages) {
+      st = 0;
+      turn ^= 1;
+    }
     if (++b == s.blocks) {
       b = 0;
       head += p.pack;
@@ -491,8 +495,8 @@ __device__ __forceinline__ bool mha_dkv_scores(const MhaBwdParams& p, MhaDkvMisc
   const uint64_t deadline = global_timer_ns() + p.timeout_ns;
   if (!warp_wait(smem_u32(&m.k_full), 0, deadline, ab)) return false;
   if (C::kKTmem && !warp_wait(smem_u32(&m.k_ready), 0, deadline, ab)) return false;
+  int st = 0, turn = 0;
   for (int j = 0; j < total; ++j) {
-    const int st = j % C::kStages, turn = j / C::kStages & 1;
     const uint64_t q = desc_plus(q_desc, st * C::kQBytes), g = desc_plus(g_desc, st * C::kDoBytes);
     if (!warp_wait(smem_u32(&m.q_full[st]), turn, deadline, ab)) return false;
     if (j > 0 && !warp_wait(smem_u32(&m.s_free), (j - 1) & 1, deadline, ab)) return false;
@@ -512,6 +516,10 @@ __device__ __forceinline__ bool mha_dkv_scores(const MhaBwdParams& p, MhaDkvMisc
       mma_ss(chosen, C::kT, desc_plus(v_desc, (kk >> 2) * kMhaUnit + (kk & 3) * 32),
              desc_plus(g, (kk >> 2) * C::kQUnit + (kk & 3) * 32), kIdesc, kk > 0 ? 1u : 0u);
     commit_to(chosen, &m.t_full);
+    if (++st == C::kStages) {
+      st = 0;
+      turn ^= 1;
+    }
   }
   return true;
 }
@@ -528,8 +536,8 @@ __device__ __forceinline__ bool mha_dkv_sums(const MhaBwdParams& p, MhaDkvMisc& 
   const uint32_t chosen = elect_one();
   const volatile int* ab = &m.abort_flag;
   const uint64_t deadline = global_timer_ns() + p.timeout_ns;
+  int st = 0, turn = 0;
   for (int j = 0; j < total; ++j) {
-    const int st = j % C::kStages, turn = j / C::kStages & 1;
     const uint64_t q = desc_plus(q_desc, st * C::kQBytes), g = desc_plus(g_desc, st * C::kDoBytes);
     if (!warp_wait(smem_u32(&m.p_full), j & 1, deadline, ab)) return false;
     if (!warp_wait(smem_u32(&m.do_full[st]), turn, deadline, ab)) return false;
@@ -545,13 +553,18 @@ __device__ __forceinline__ bool mha_dkv_sums(const MhaBwdParams& p, MhaDkvMisc& 
     for (int kk = 0; kk < C::kN / 16; ++kk)
       mma_ts(chosen, C::kDk, C::kDs + 8 * kk, desc_plus(q, kk * 2048), kIdescK, j + kk > 0 ? 1u : 0u);
     commit_to(chosen, &m.empty[st]);
+    if (++st == C::kStages) {
+      st = 0;
+      turn ^= 1;
+    }
   }
   commit_to(chosen, &m.out_full);
   return true;
 }
 
-// The rows' lse (in powers of two) and D; where D is not finite the row's gradient was
-// not, and its weights become NaN.  Rows of no token weigh nothing.
+// The rows' lse (in powers of two) and D, there with the block's copy of Q; where D is not
+// finite the row's gradient was not, and its weights become NaN.  Rows of no token weigh
+// nothing.
 template <int DQK>
 __device__ __forceinline__ bool mha_dkv_stats(const MhaBwdParams& p, MhaDkvMisc& m, const MhaWork& w, const MhaQueries& s,
                                               int kvh) {
@@ -559,30 +572,33 @@ __device__ __forceinline__ bool mha_dkv_stats(const MhaBwdParams& p, MhaDkvMisc&
   const volatile int* ab = &m.abort_flag;
   const uint64_t deadline = global_timer_ns() + p.timeout_ns;
   const int lane = static_cast<int>(lane_id()), lq = w.q1 - w.q0;
-  int head = kvh * p.group, b = 0;
+  int head = kvh * p.group, b = 0, st = 0, turn = 0;
   for (int j = 0; j < s.total; ++j) {
-    const int st = j % kMhaStats;
     float l[C::kN / 32], d[C::kN / 32];
 #pragma unroll
     for (int i = 0; i < C::kN / 32; ++i) {
       const int r = 32 * i + lane, tok = s.first + b * p.tok_tile + r / p.pack;
-      l[i] = INFINITY;
+      l[i] = -INFINITY;
       d[i] = 0.f;
       if (r < p.pack * p.tok_tile && tok < lq) {
         const size_t at = static_cast<size_t>(w.q0 + tok) * p.h_q + head + r % p.pack;
-        l[i] = __ldg(p.lse + at) * 1.4426950408889634f;
-        d[i] = __ldcg(p.delta + at);
+        l[i] = __ldg(p.lse + at) * -1.4426950408889634f;
+        d[i] = -__ldcg(p.delta + at);
         if (!(fabsf(d[i]) <= 3.402823466e38f)) l[i] = __uint_as_float(0x7fc00000u);
       }
     }
-    if (!warp_wait(smem_u32(&m.stat_empty[st]), (j / kMhaStats & 1) ^ 1, deadline, ab)) return false;
+    if (!warp_wait(smem_u32(&m.empty[st]), turn ^ 1, deadline, ab)) return false;
 #pragma unroll
     for (int i = 0; i < C::kN / 32; ++i) {
-      m.lse2[st][32 * i + lane] = l[i];
-      m.delta[st][32 * i + lane] = d[i];
+      m.shift[st][32 * i + lane] = l[i];
+      m.minus_d[st][32 * i + lane] = d[i];
     }
     __syncwarp();
-    if (lane == 0) mbar_arrive(smem_u32(&m.stat_full[st]));
+    if (lane == 0) mbar_arrive(smem_u32(&m.q_full[st]));
+    if (++st == C::kStages) {
+      st = 0;
+      turn ^= 1;
+    }
     if (++b == s.blocks) {
       b = 0;
       head += p.pack;
@@ -617,7 +633,7 @@ __device__ __forceinline__ bool mha_dkv_rows(const MhaBwdParams& p, MhaDkvMisc& 
   const int last_key = min((w.tile + 1) * kMhaTile, lk) - 1;
   const uint32_t ts = lane0 + C::kS + kHalf * half, tt = lane0 + C::kT + kHalf * half,
                  tp = lane0 + C::kP + kHalf / 2 * half, td = lane0 + C::kDs + kHalf / 2 * half;
-  int b = 0;
+  int b = 0, st = 0, turn = 0, before = 0, turn_before = 0;   // where the block is, and the one before
   for (int j = 0; j < s.total; ++j) {
     const int t0 = s.first + b * p.tok_tile;
     if (++b == s.blocks) b = 0;
@@ -625,9 +641,6 @@ __device__ __forceinline__ bool mha_dkv_rows(const MhaBwdParams& p, MhaDkvMisc& 
     // the columns that see this thread's key
     const int lo = edge ? p.pack * (key - (lk - lq) - t0) - kHalf * half : 0;
     const int hi = edge ? p.pack * (lq - t0) - kHalf * half : kHalf;
-    const int st = j % kMhaStats, qs = j % C::kStages, turn = j / C::kStages & 1;
-    // where the block before is: its product with dS has ended when it is free
-    const int before = (j - 1) % C::kStages, turn_before = (j - 1) / C::kStages & 1;
     if (!warp_wait(smem_u32(&m.s_full), j & 1, deadline, ab)) return false;
     tc_fence_after();
     float x[kHalf], y[kHalf];
@@ -635,24 +648,24 @@ __device__ __forceinline__ bool mha_dkv_rows(const MhaBwdParams& p, MhaDkvMisc& 
     tc_fence_before();
     __syncwarp();
     if (lane_id() == 0) mbar_arrive(smem_u32(&m.s_free));
-    if (!warp_wait(smem_u32(&m.stat_full[st]), j / kMhaStats & 1, deadline, ab)) return false;
     if (edge) {
       // the products with P and dS must not meet what is not finite in a row that does not
       // see a key; the product that gives T has read dout by then
       if (!warp_wait(smem_u32(&m.t_full), j & 1, deadline, ab)) return false;
-      if (!warp_wait(smem_u32(&m.q_full[qs]), turn, deadline, ab) || !warp_wait(smem_u32(&m.do_full[qs]), turn, deadline, ab))
+      if (!warp_wait(smem_u32(&m.q_full[st]), turn, deadline, ab) || !warp_wait(smem_u32(&m.do_full[st]), turn, deadline, ab))
         return false;
-      mha_clear<256>(sb + C::kQOff + qs * C::kQBytes, C::kQBytes);
-      mha_clear<256>(sb + C::kDoOff + qs * C::kDoBytes, C::kDoBytes);
+      mha_clear<256>(sb + C::kQOff + st * C::kQBytes, C::kQBytes);
+      mha_clear<256>(sb + C::kDoOff + st * C::kDoBytes, C::kDoBytes);
     }
-    const float4* l4 = reinterpret_cast<const float4*>(&m.lse2[st][kHalf * half]);
+    // they came with Q, which S has read
+    const float4* l4 = reinterpret_cast<const float4*>(&m.shift[st][kHalf * half]);
 #pragma unroll
     for (int i = 0; i < kHalf; i += 4) {
       const float4 l = l4[i >> 2];
-      x[i] = fast_exp2(fmaf(x[i], p.scale_log2, -l.x));
-      x[i + 1] = fast_exp2(fmaf(x[i + 1], p.scale_log2, -l.y));
-      x[i + 2] = fast_exp2(fmaf(x[i + 2], p.scale_log2, -l.z));
-      x[i + 3] = fast_exp2(fmaf(x[i + 3], p.scale_log2, -l.w));
+      scale_shift2(x[i], x[i + 1], p.scale_log2, l.x, l.y);
+      scale_shift2(x[i + 2], x[i + 3], p.scale_log2, l.z, l.w);
+#pragma unroll
+      for (int n = 0; n < 4; ++n) x[i + n] = fast_exp2(x[i + n]);
     }
     if (edge) {
 #pragma unroll
@@ -671,28 +684,30 @@ __device__ __forceinline__ bool mha_dkv_rows(const MhaBwdParams& p, MhaDkvMisc& 
     tc_fence_before();
     __syncwarp();
     if (lane_id() == 0) mbar_arrive(smem_u32(&m.t_free));
-    const float4* d4 = reinterpret_cast<const float4*>(&m.delta[st][kHalf * half]);
+    const float4* d4 = reinterpret_cast<const float4*>(&m.minus_d[st][kHalf * half]);
 #pragma unroll
     for (int i = 0; i < kHalf; i += 4) {
       const float4 d = d4[i >> 2];
-      y[i] = x[i] * (y[i] - d.x);
-      y[i + 1] = x[i + 1] * (y[i + 1] - d.y);
-      y[i + 2] = x[i + 2] * (y[i + 2] - d.z);
-      y[i + 3] = x[i + 3] * (y[i + 3] - d.w);
+      weigh2(x[i], x[i + 1], y[i], y[i + 1], d.x, d.y);
+      weigh2(x[i + 2], x[i + 3], y[i + 2], y[i + 3], d.z, d.w);
     }
     if (edge) {
 #pragma unroll
       for (int i = 0; i < kHalf; ++i) y[i] = i >= lo && i < hi ? y[i] : 0.f;
     }
+    // the product with the dS before has ended when that block is free
     if (j > 0 && !warp_wait(smem_u32(&m.empty[before]), turn_before, deadline, ab)) return false;
     tc_fence_after();
     tmem_store_bf16<kHalf>(td, y);
     tmem_wait_st();
     tc_fence_before();
     __syncwarp();
-    if (lane_id() == 0) {
-      mbar_arrive(smem_u32(&m.ds_full));
-      mbar_arrive(smem_u32(&m.stat_empty[st]));
+    if (lane_id() == 0) mbar_arrive(smem_u32(&m.ds_full));
+    before = st;
+    turn_before = turn;
+    if (++st == C::kStages) {
+      st = 0;
+      turn ^= 1;
     }
   }
   if (s.total > 0) {
@@ -720,20 +735,16 @@ __global__ void __launch_bounds__(MhaDkvShape<DQK>::kThreads, 1) dense_mha_dkv_k
   const int warp = static_cast<int>(threadIdx.x >> 5);
   const uint32_t sb = smem_u32(sbase);
   int slot, kvh;
-  mha_unit(blockIdx.x, p.slots, p.heads, p.heads_near, slot, kvh);
+  mha_unit(blockIdx.x, p.slots, p.heads, p.order, slot, kvh);
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 4; ++i) {
-      mbar_init(smem_u32(&m.q_full[i]), 1);
+      mbar_init(smem_u32(&m.q_full[i]), 2);   // the copy and its rows' numbers
       mbar_init(smem_u32(&m.do_full[i]), 1);
       mbar_init(smem_u32(&m.empty[i]), 1);
     }
-    for (int i = 0; i < kMhaStats; ++i) {
-      mbar_init(smem_u32(&m.stat_full[i]), 1);
-      mbar_init(smem_u32(&m.stat_empty[i]), 8);   // one arrival per row warp
-    }
     mbar_init(smem_u32(&m.k_full), 1);
-    mbar_init(smem_u32(&m.k_ready), 8);
+    mbar_init(smem_u32(&m.k_ready), 8);   // one arrival per row warp
     mbar_init(smem_u32(&m.s_full), 1);
     mbar_init(smem_u32(&m.s_free), 8);
     mbar_init(smem_u32(&m.p_full), 8);

@@ -54,13 +54,21 @@ enum MhaErrCode : int {
   kErrMhaSoftmaxWait = 0x703,
 };
 
+// Heads (packs of them) whose tiles run side by side, the longest first: `near` at a time, so
+// that what they read stays close, and behind the first `lead` all of the rest, so that the
+// SMs end together.
+struct MhaHeads {
+  int near, lead;
+};
+
 struct MhaFwdParams {
   CUtensorMap map_q, map_k, map_v;         // [token, head, d]: boxes 64 x pack x tok_tile, 64 x 1 x 128, 64 x 1 x 64
   const int32_t *cu_q, *cu_kv;             // [batch + 1], null for one dense sequence
   int batch, total_q, total_kv, h_q, group; // query heads per key head
   int pack, tok_tile;                      // a tile is tok_tile tokens x pack heads
   int slots;                               // tiles (of NT) per head pack that the grid has room for
-  int packs, packs_near;                   // head packs; of so many at a time the tiles go from the longest to the shortest
+  int packs;                               // head packs
+  MhaHeads order;
   int cluster;                             // CTAs that share a tile's keys out (one tile a CTA; else 1)
   float scale_log2;
   const __nv_bfloat16* v;                  // row (t, h) at v + t v_tok + h v_head
@@ -186,14 +194,18 @@ __device__ __forceinline__ void mha_fill_rows(void* out, long long words, int fi
     for (long long i = lane_id(); i < words; i += 32) static_cast<uint32_t*>(out)[r * words + i] = word;
 }
 
-// Unit -> tile and head (pack): `near` heads at a time, side by side, so that their longest
-// tiles come first while what they read stays in L2.
-__device__ __forceinline__ void mha_unit(unsigned unit, int slots, int heads, int near, int& slot, int& head) {
-  const unsigned per = static_cast<unsigned>(slots) * static_cast<unsigned>(near);
-  const unsigned first = unit / per * static_cast<unsigned>(near);
-  const unsigned wide = min(static_cast<unsigned>(near), static_cast<unsigned>(heads) - first);
-  slot = static_cast<int>(unit % per / wide);
-  head = static_cast<int>(first + unit % per % wide);
+// Unit -> tile and head (pack).
+__device__ __forceinline__ void mha_unit(unsigned unit, int slots, int heads, const MhaHeads& h, int& slot, int& head) {
+  const unsigned lead = static_cast<unsigned>(h.lead) * static_cast<unsigned>(slots);
+  unsigned first = static_cast<unsigned>(h.lead), wide = static_cast<unsigned>(heads - h.lead), at = unit - lead;
+  if (unit < lead) {
+    wide = static_cast<unsigned>(h.near);
+    const unsigned per = static_cast<unsigned>(slots) * wide;
+    first = unit / per * wide;
+    at = unit % per;
+  }
+  slot = static_cast<int>(at / wide);
+  head = static_cast<int>(first + at % wide);
 }
 
 // ------------------------------------------------------------------ PTX
@@ -426,16 +438,27 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return d;
 }
 
-// (a0, a1) * b + c, packed.
-__device__ __forceinline__ void scale_shift2(float& a0, float& a1, float b, float c) {
+// (a0, a1) * b + (c0, c1) and (a0, a1) * ((b0, b1) + (c0, c1)), packed.
+__device__ __forceinline__ void scale_shift2(float& a0, float& a1, float b, float c0, float c1) {
   asm("{\n\t.reg .b64 pa, pb, pc;\n\t"
       "mov.b64 pa, {%0, %1};\n\t"
       "mov.b64 pb, {%2, %2};\n\t"
-      "mov.b64 pc, {%3, %3};\n\t"
+      "mov.b64 pc, {%3, %4};\n\t"
       "fma.rn.f32x2 pa, pa, pb, pc;\n\t"
       "mov.b64 {%0, %1}, pa;\n\t}"
       : "+f"(a0), "+f"(a1)
-      : "f"(b), "f"(c));
+      : "f"(b), "f"(c0), "f"(c1));
+}
+__device__ __forceinline__ void weigh2(float a0, float a1, float& b0, float& b1, float c0, float c1) {
+  asm("{\n\t.reg .b64 pa, pb, pc;\n\t"
+      "mov.b64 pa, {%2, %3};\n\t"
+      "mov.b64 pb, {%0, %1};\n\t"
+      "mov.b64 pc, {%4, %5};\n\t"
+      "add.rn.f32x2 pb, pb, pc;\n\t"
+      "mul.rn.f32x2 pb, pa, pb;\n\t"
+      "mov.b64 {%0, %1}, pb;\n\t}"
+      : "+f"(b0), "+f"(b1)
+      : "f"(a0), "f"(a1), "f"(c0), "f"(c1));
 }
 
 __device__ __forceinline__ void add2(float& a0, float& a1, float b0, float b1) {
@@ -792,7 +815,7 @@ __device__ __forceinline__ bool mha_softmax(const MhaFwdParams& p, MhaMisc& m, u
 #pragma unroll
       for (int k = 0; k < 32; k += 2) {
         float &a = v[i + k], &b = v[i + k + 1];
-        scale_shift2(a, b, c, shift);
+        scale_shift2(a, b, c, shift, shift);
         a = fast_exp2(a);
         b = fast_exp2(b);
         add2(add[k & 2], add[(k & 2) + 1], a, b);
@@ -921,7 +944,7 @@ __global__ void __launch_bounds__(MhaFwdShape<DQK, NT>::kThreads, 1) dense_mha_f
   const unsigned ctas = NT == 1 ? static_cast<unsigned>(p.cluster) : 1u, unit = blockIdx.x / ctas;
   const int rank = static_cast<int>(blockIdx.x % ctas);
   int slot, head;
-  mha_unit(unit, p.slots, p.packs, p.packs_near, slot, head);
+  mha_unit(unit, p.slots, p.packs, p.order, slot, head);
   const int pack0 = head * p.pack;
 
   if (threadIdx.x == 0) {

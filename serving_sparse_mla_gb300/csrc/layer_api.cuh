@@ -305,11 +305,20 @@ cudaError_t mha_fwd_launch(const smla::MhaFwdParams& p, unsigned ctas, cudaStrea
   return cudaLaunchKernelEx(&cfg, smla::dense_mha_fwd_kernel<DQK, NT>, p);
 }
 
-// As many heads side by side as have what their tiles read, `bytes` each, in most of L2;
-// equal shares of all.
-int mha_near(int heads, double bytes) {
-  const double turns = std::ceil(heads * (bytes + 1) / 1e8);
-  return static_cast<int>(std::ceil(heads / std::min(turns, static_cast<double>(heads))));
+// How many heads' tiles run side by side, of which each head's read `bytes`: as many as come
+// to `most` (one at least), so that the tiles find each other's reads in the near half of L2;
+// the last ones, two tiles an SM, all together, so that the SMs end together.
+// Measured (us, 192 columns, 8192 tokens; all heads that 100 MB hold / 24 MB / 11 MB):
+//   dk and dv, 32 heads   1393 / 1015 / 966     64 heads   2712 / 2020 / 1950
+//   dq, 32 heads           675 /  632 / 635     out, 64 heads   884 / 866 / 867
+// The tail (1, 2, 4 tiles an SM): nine texts up to 2119, 40 heads on 8, dk and dv 355, 316,
+// 351; 32 heads on 8 of 8192 tokens 812, 900, 890.
+constexpr double kMhaNearKeys = 2.4e7, kMhaNearRows = 1.1e7;
+smla::MhaHeads mha_order(int heads, double bytes, double most, long long slots, int sms) {
+  const double near = std::max(1.0, std::min<double>(heads, std::floor(most / (bytes + 1))));
+  const double last = std::max(near, std::ceil(2.0 * sms / std::max<double>(slots, 1)));
+  const int n = static_cast<int>(near);
+  return {n, last < heads ? (heads - static_cast<int>(last)) / n * n : 0};
 }
 
 // dq (and D into the workspace), then dk and dv.
@@ -317,7 +326,7 @@ template <int DQK>
 sparse_mla_status_t mha_bwd_launch(const MhaRows& q, const MhaRows& k, const MhaRows& v, const MhaRows& g,
                                    const int32_t* cu_q, const int32_t* cu_kv, int batch, float sm_scale, const void* out,
                                    const float* lse, void* dq, void* dk, void* dv, int total_q, int total_kv, int h_q,
-                                   int h_kv, void* workspace, cudaStream_t cs) {
+                                   int h_kv, void* workspace, int sms, cudaStream_t cs) {
   smla::MhaBwdParams p;
   std::memset(&p, 0, sizeof(p));
   p.cu_q = cu_q;
@@ -365,7 +374,8 @@ sparse_mla_status_t mha_bwd_launch(const MhaRows& q, const MhaRows& k, const Mha
     if (ctas > INT_MAX) return SPARSE_MLA_ERR_INVALID_ARG;
     p.slots = static_cast<int>(slots);
     p.heads = h_q / p.pack;
-    p.heads_near = mha_near(p.heads, static_cast<double>(total_kv) * (DQK + smla::kMhaDv) * 2 * p.pack / p.group);
+    p.order = mha_order(p.heads, static_cast<double>(total_kv) * (DQK + smla::kMhaDv) * 2 * p.pack / p.group,
+                        kMhaNearKeys, slots, sms);
     smla::dense_mha_dq_kernel<DQK><<<static_cast<unsigned>(ctas), C::kThreads, C::kBytes, cs>>>(p);
     if (cudaGetLastError() != cudaSuccess) return SPARSE_MLA_ERR_CUDA;
   }
@@ -376,7 +386,8 @@ sparse_mla_status_t mha_bwd_launch(const MhaRows& q, const MhaRows& k, const Mha
     if (ctas > INT_MAX) return SPARSE_MLA_ERR_INVALID_ARG;
     p.slots = static_cast<int>(slots);
     p.heads = h_kv;
-    p.heads_near = mha_near(h_kv, static_cast<double>(total_q) * (DQK + smla::kMhaDv) * 2 * p.group);
+    p.order = mha_order(h_kv, static_cast<double>(total_q) * (DQK + smla::kMhaDv) * 2 * p.group,
+                        kMhaNearRows, slots, sms);
     // its CTAs may take the SMs that the last tiles of dq leave (and themselves wait for D)
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr = {};
@@ -448,7 +459,8 @@ sparse_mla_status_t dense_mha_fwd(const void* q, long long q_tok_stride, long lo
     return st;
   p.cluster = plan.cluster;
   p.packs = h_q / p.pack;
-  p.packs_near = mha_near(p.packs, static_cast<double>(total_kv) * (d_qk + d_v) * 2 * p.pack / group);
+  p.order = mha_order(p.packs, static_cast<double>(total_kv) * (d_qk + d_v) * 2 * p.pack / group, kMhaNearKeys,
+                      plan.slots, sms);
   const long long ctas = plan.slots * (h_q / p.pack) * plan.cluster;
   if (ctas > INT_MAX) return SPARSE_MLA_ERR_INVALID_ARG;
   p.slots = static_cast<int>(plan.slots);
@@ -491,9 +503,11 @@ sparse_mla_status_t dense_mha_bwd(const void* q, long long q_tok_stride, long lo
   const MhaState* state = nullptr;
   if ((st = mha_device_setup(&state)) != SPARSE_MLA_OK) return st;
   return d_qk == 192 ? mha_bwd_launch<192>(rq, rk, rv, rg, cu_seqlens_q, cu_seqlens_kv, batch, sm_scale, out, lse, dq, dk,
-                                           dv, total_q, total_kv, h_q, h_kv, workspace, static_cast<cudaStream_t>(stream))
+                                           dv, total_q, total_kv, h_q, h_kv, workspace, sms,
+                                           static_cast<cudaStream_t>(stream))
                      : mha_bwd_launch<128>(rq, rk, rv, rg, cu_seqlens_q, cu_seqlens_kv, batch, sm_scale, out, lse, dq, dk,
-                                           dv, total_q, total_kv, h_q, h_kv, workspace, static_cast<cudaStream_t>(stream));
+                                           dv, total_q, total_kv, h_q, h_kv, workspace, sms,
+                                           static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"
