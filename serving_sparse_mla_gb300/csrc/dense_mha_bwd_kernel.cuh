@@ -57,6 +57,7 @@ struct MhaBwdParams {
   const int32_t *cu_q, *cu_kv;             // [batch + 1], null for one dense sequence
   int batch, total_q, total_kv, h_q, h_kv, group;
   int pack, tok_tile;                      // rows of a query tile: tok_tile tokens x pack heads
+  MhaDiv per;                              // tok_tile
   int slots;                               // tiles per head (pack) that the grid has room for
   int heads;                               // head packs (of keys: heads)
   MhaHeads order;
@@ -343,6 +344,8 @@ __global__ void __launch_bounds__(MhaDqShape<DQK>::kThreads, 1) dense_mha_dq_ker
     m.prior_error = *reinterpret_cast<volatile int*>(&g_device_error);
     fence_mbar_init();
     prefetch_tmap(&p.map_q);
+    prefetch_tmap(&p.map_do);
+    prefetch_tmap(&p.map_o);
     prefetch_tmap(&p.map_k);
     prefetch_tmap(&p.map_v);
   }
@@ -351,7 +354,7 @@ __global__ void __launch_bounds__(MhaDqShape<DQK>::kThreads, 1) dense_mha_dq_ker
     tmem_relinquish();
   }
   if (warp == 9) {
-    const MhaWork w = mha_find<false>(p.cu_q, p.cu_kv, p.batch, p.total_q, p.total_kv, slot, p.tok_tile);
+    const MhaWork w = mha_find<false>(p.cu_q, p.cu_kv, p.batch, p.total_q, p.total_kv, slot, p.per);
     if (lane_id() == 0) m.work = w;
   }
   tc_fence_before();
@@ -768,7 +771,7 @@ __global__ void __launch_bounds__(MhaDkvShape<DQK>::kThreads, 1) dense_mha_dkv_k
     tmem_relinquish();
   }
   if (warp == 9) {
-    const MhaWork w = mha_find<true>(p.cu_q, p.cu_kv, p.batch, p.total_q, p.total_kv, slot, p.tok_tile);
+    const MhaWork w = mha_find<true>(p.cu_q, p.cu_kv, p.batch, p.total_q, p.total_kv, slot, p.per);
     if (lane_id() == 0) m.work = w;
   }
   if (p.pack * p.tok_tile < C::kN) {

@@ -54,6 +54,14 @@ enum MhaErrCode : int {
   kErrMhaSoftmaxWait = 0x703,
 };
 
+// n / d for n < 2^31 as n m >> s: with s = 31 + log2 d (rounded up) and m = 2^s / d + 1
+// (rounded down), m d is above 2^s by d <= 2^(s - 31) at most.
+struct MhaDiv {
+  unsigned long long m;
+  int d, s;
+  __device__ __forceinline__ int of(int n) const { return static_cast<int>(static_cast<unsigned>(n) * m >> s); }
+};
+
 // Heads (packs of them) whose tiles run side by side, the longest first: `near` at a time, so
 // that what they read stays close, and behind the first `lead` all of the rest, so that the
 // SMs end together.
@@ -66,6 +74,7 @@ struct MhaFwdParams {
   const int32_t *cu_q, *cu_kv;             // [batch + 1], null for one dense sequence
   int batch, total_q, total_kv, h_q, group; // query heads per key head
   int pack, tok_tile;                      // a tile is tok_tile tokens x pack heads
+  MhaDiv per;                              // tokens of a CTA (NT tiles)
   int slots;                               // tiles (of NT) per head pack that the grid has room for
   int packs;                               // head packs
   MhaHeads order;
@@ -98,16 +107,15 @@ struct MhaWork {
 //   queries: tiles of `per` rows; a block is 128 of the keys that the last row sees
 //   keys:    tiles of 128 rows; a block is `per` of the queries that see the first row
 template <bool KEYS>
-__device__ __forceinline__ int mha_tiles_above(int lq, int lk, int per, int blocks) {
-  const int rows = KEYS ? kMhaTile : per;
-  const int tiles = static_cast<int>(static_cast<unsigned>((KEYS ? lk : lq) + rows - 1) / static_cast<unsigned>(rows));
-  if (blocks < 0) return tiles;
+__device__ __forceinline__ int mha_tiles_above(int lq, int lk, const MhaDiv& per, int blocks) {
   if constexpr (KEYS) {
-    const int seen = lq - blocks * per;   // the first row's queries start before this one
-    return seen <= 0 ? 0 : min(tiles, max(0, (seen + lk - lq + kMhaTile - 1) >> 7));
+    const int tiles = (lk + kMhaTile - 1) >> 7;
+    const int seen = lq - blocks * per.d;   // the first row's queries start before this one
+    return blocks < 0 ? tiles : (seen <= 0 ? 0 : min(tiles, max(0, (seen + lk - lq + kMhaTile - 1) >> 7)));
   } else {
+    const int tiles = per.of(lq + per.d - 1);
     const int past = blocks * kMhaTile + lq - lk;   // the last row is behind this one
-    return past >= lq ? 0 : (past <= 0 ? tiles : tiles - static_cast<int>(static_cast<unsigned>(past) / static_cast<unsigned>(per)));
+    return blocks < 0 || past <= 0 ? tiles : (past >= lq ? 0 : tiles - per.of(past));
   }
 }
 
@@ -117,7 +125,7 @@ constexpr int kMhaSortBatch = 128;   // sequences up to which tiles are handed o
 // their order); q1 = k1 = 0 where there are not so many.  One warp, all lanes.
 template <bool KEYS>
 __device__ __forceinline__ MhaWork mha_find(const int32_t* cu_q, const int32_t* cu_kv, int batch, int total_q,
-                                            int total_kv, int slot, int per) {
+                                            int total_kv, int slot, const MhaDiv& per) {
   MhaWork w = {0, 0, 0, 0, 0, KEYS ? total_kv : total_q};
   if (cu_q == nullptr) {
     const int tiles = mha_tiles_above<KEYS>(total_q, total_kv, per, -1);
@@ -136,29 +144,37 @@ __device__ __forceinline__ MhaWork mha_find(const int32_t* cu_q, const int32_t* 
   };
   const int4 mine = seq(lane);   // of the first 32, which are often all
   auto above = [&](const int4& x, int blocks) { return mha_tiles_above<KEYS>(x.y - x.x, x.w - x.z, per, blocks); };
-  auto all_above = [&](int blocks) {
-    int n = __reduce_add_sync(0xffffffffu, above(mine, blocks));
-    for (int base = 32; base < batch; base += 32) n += __reduce_add_sync(0xffffffffu, above(seq(base + lane), blocks));
-    return n;
-  };
   int longest = 0;   // most blocks of a tile, or more
   w.end = 0;
   for (int base = 0; base < batch; base += 32) {
     const int4 x = base == 0 ? mine : seq(base + lane);
-    longest = max(longest, __reduce_max_sync(0xffffffffu, KEYS ? (x.y - x.x + per - 1) / per : (x.w - x.z + 127) / 128));
+    longest = max(longest, __reduce_max_sync(0xffffffffu, KEYS ? per.of(x.y - x.x + per.d - 1) : (x.w - x.z + 127) >> 7));
     w.end = max(w.end, __reduce_max_sync(0xffffffffu, KEYS ? x.w : x.y));
   }
   // the tiles before this one have more than `blocks` blocks, or as many and lie in earlier sequences
   int blocks = -1, before = 0;
   if (batch > 1 && batch <= kMhaSortBatch) {
-    int lo = 0, hi = longest;   // the fewest blocks that at most `slot` tiles exceed
+    // the fewest blocks that at most `slot` tiles exceed, by 32 guesses at a time
+    int lo = 0, hi = longest;
     while (lo < hi) {
-      const int mid = (lo + hi) >> 1;
-      if (all_above(mid) <= slot) hi = mid;
-      else lo = mid + 1;
+      const int step = (hi - lo + 31) >> 5, guess = min(hi, lo + lane * step);
+      int n = 0;
+      for (int base = 0; base < batch; base += 32) {
+        const int4 x = base == 0 ? mine : seq(base + lane);
+        const int lq = x.y - x.x, lk = x.w - x.z;
+        for (int i = 0; i < min(32, batch - base); ++i)
+          n += mha_tiles_above<KEYS>(__shfl_sync(0xffffffffu, lq, i), __shfl_sync(0xffffffffu, lk, i), per, guess);
+      }
+      const uint32_t few = __ballot_sync(0xffffffffu, n <= slot);
+      const int at = few != 0u ? __ffs(few) - 1 : 32;
+      const int next = at > 0 ? __shfl_sync(0xffffffffu, guess, at - 1) + 1 : lo;
+      if (at < 32) {
+        hi = __shfl_sync(0xffffffffu, guess, at);
+        before = __shfl_sync(0xffffffffu, n, at);
+      }
+      lo = min(next, hi);
     }
-    blocks = lo;
-    before = all_above(blocks);
+    blocks = hi;
   }
   for (int base = 0; base < batch; base += 32) {
     const int4 x = base == 0 ? mine : seq(base + lane);
@@ -974,7 +990,7 @@ __global__ void __launch_bounds__(MhaFwdShape<DQK, NT>::kThreads, 1) dense_mha_f
     tmem_relinquish();
   }
   if (warp == 4 * NT + 1) {
-    const MhaWork w = mha_find<false>(p.cu_q, p.cu_kv, p.batch, p.total_q, p.total_kv, slot, NT * p.tok_tile);
+    const MhaWork w = mha_find<false>(p.cu_q, p.cu_kv, p.batch, p.total_q, p.total_kv, slot, p.per);
     if (lane_id() == 0) m.work = w;
   }
   tc_fence_before();

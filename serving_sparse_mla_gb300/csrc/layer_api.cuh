@@ -175,6 +175,12 @@ int mha_pack(int group, int rows) {
   return 1;
 }
 
+smla::MhaDiv mha_div(int d) {
+  int log = 0;
+  while (1 << log < d) ++log;
+  return {(1ull << (31 + log)) / static_cast<unsigned>(d) + 1, d, 31 + log};
+}
+
 // Tiles of `per` rows that any `batch` sequences of `total` rows (> 0) in all have at most
 // (0: one dense sequence): one for each that has rows, and one for each `per` rows more.
 long long mha_slots(int total, int per, int batch) {
@@ -360,6 +366,7 @@ sparse_mla_status_t mha_bwd_launch(const MhaRows& q, const MhaRows& k, const Mha
   auto maps = [&](int rows, int keys) {   // of a query block and a key block
     p.pack = mha_pack(p.group, rows);
     p.tok_tile = rows / p.pack;
+    p.per = mha_div(p.tok_tile);
     if ((st = mha_map(&p.map_q, mq, tq, hq, DQK, p.pack, p.tok_tile)) == SPARSE_MLA_OK &&
         (st = mha_map(&p.map_do, mg, tq, hq, dv_cols, p.pack, p.tok_tile)) == SPARSE_MLA_OK &&
         (st = mha_map(&p.map_o, mo, tq, hq, dv_cols, p.pack, p.tok_tile)) == SPARSE_MLA_OK &&
@@ -458,6 +465,7 @@ sparse_mla_status_t dense_mha_fwd(const void* q, long long q_tok_stride, long lo
                     smla::kMhaTile / 2)) != SPARSE_MLA_OK)
     return st;
   p.cluster = plan.cluster;
+  p.per = mha_div(p.tok_tile * plan.tiles);
   p.packs = h_q / p.pack;
   p.order = mha_order(p.packs, static_cast<double>(total_kv) * (d_qk + d_v) * 2 * p.pack / group, kMhaNearKeys,
                       plan.slots, sms);
