@@ -936,6 +936,28 @@ def _mha_args(q, k, v, cu_seqlens_q, cu_seqlens_kv):
 _MHA_FILL_OUT, _MHA_FILL_LSE = 1, 2
 
 
+def _span(t: torch.Tensor):
+    """First and last byte (exclusive) that a tensor's values lie in; its strides are not negative."""
+    at = t.data_ptr()
+    if t.numel() == 0:
+        return at, at
+    return at, at + t.element_size() * (1 + sum((n - 1) * s for n, s in zip(t.shape, t.stride())))
+
+
+def _separate(outs, reads) -> None:
+    """Given outputs (tensor or None, bytes written, name) may not meet each other or what the
+    call reads (tensor or None, name): a tile's rows are written while others still read."""
+    taken = [(*_span(t), name) for t, name in reads if t is not None]
+    for t, size, name in outs:
+        if t is None:
+            continue
+        at = t.data_ptr()
+        for lo, hi, what in taken:
+            if at < hi and lo < at + size:
+                raise ValueError(f"{name} shares memory with {what}")
+        taken.append((at, at + size, name))
+
+
 def dense_mha_fwd(q, k, v, sm_scale, cu_seqlens_q=None, cu_seqlens_kv=None, out: Optional[torch.Tensor] = None,
                   lse: Optional[torch.Tensor] = None, stream=None):
     """Causal attention over whole prompts in the heads' own space: q [total_q, h_q,
@@ -944,12 +966,14 @@ def dense_mha_fwd(q, k, v, sm_scale, cu_seqlens_q=None, cu_seqlens_kv=None, out:
     cu_seqlens_q / cu_seqlens_kv int32 [batch + 1] for packed sequences (neither: one
     sequence); a sequence's queries are its last positions.  -> (out [total_q, h_q,
     128] bf16, lse [total_q, h_q] fp32).  Rows behind the last sequence are left as
-    they were in outputs that are given, zeros and -inf in those made here."""
+    they were in outputs that are given, zeros and -inf in those made here.  Outputs that
+    are given share no memory with each other or the inputs."""
     total_q, total_kv, h_q, h_kv, d_qk, d_v, batch, dev, steps = _mha_args(q, k, v, cu_seqlens_q, cu_seqlens_kv)
-    if out is not None:
+    if out is not None or lse is not None:
         _given(out, _BF16, "out", total_q * h_q * d_v, dev)
-    if lse is not None:
         _given(lse, _F32, "lse", total_q * h_q, dev)
+        _separate(((out, 2 * total_q * h_q * d_v, "out"), (lse, 4 * total_q * h_q, "lse")),
+                  ((q, "q"), (k, "k"), (v, "v"), (cu_seqlens_q, "cu_seqlens_q"), (cu_seqlens_kv, "cu_seqlens_kv")))
     fill = (_MHA_FILL_OUT if out is None else 0) | (_MHA_FILL_LSE if lse is None else 0)
 
     return _run(_mha_fwd, dev, stream, "dense_mha_fwd", q, k, v, steps, cu_seqlens_q, cu_seqlens_kv, batch, sm_scale, out,
@@ -991,6 +1015,11 @@ def dense_mha_bwd(q, k, v, sm_scale, out, lse, dout, cu_seqlens_q=None, cu_seqle
         _given(dk, _BF16, "dk", total_kv * h_kv * d_qk, dev)
         _given(dv, _BF16, "dv", total_kv * h_kv * d_v, dev)
         _workspace(workspace, dev)
+        _separate(((dq, 2 * total_q * h_q * d_qk, "dq"), (dk, 2 * total_kv * h_kv * d_qk, "dk"),
+                   (dv, 2 * total_kv * h_kv * d_v, "dv"),
+                   (workspace, 0 if workspace is None else workspace.numel() * workspace.element_size(), "workspace")),
+                  ((q, "q"), (k, "k"), (v, "v"), (out, "out"), (lse, "lse"), (dout, "dout"),
+                   (cu_seqlens_q, "cu_seqlens_q"), (cu_seqlens_kv, "cu_seqlens_kv")))
     return _run(_mha_bwd, dev, stream, "dense_mha_bwd", q, k, v, steps, cu_seqlens_q, cu_seqlens_kv, batch, sm_scale, out,
                 lse, dout, dq, dk, dv, workspace, total_q, total_kv, h_q, h_kv, d_qk, d_v)
 

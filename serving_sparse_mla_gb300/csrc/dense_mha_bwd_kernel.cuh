@@ -27,9 +27,15 @@
 // A signal from the tensor core to the threads that wait for it and back takes about 1000
 // cycles, as long as two products of a block.  So P and dS have columns of their own in
 // TMEM, and the next block's S and T are formed as soon as this one's have been read: with
-// P and dS in the columns of S and T a block of 64 rows took 2250 cycles, of which its
-// products are 1024.  That is what sets the blocks: at 192 columns 96 keys (dq; 2 x 96 + 48
-// + 192 + 64 columns of TMEM) and 64 query rows.
+// P and dS in the columns of S and T a block of 64 rows took 2250 cycles where 1280 are
+// products.  That is what sets the blocks: at 192 columns 96 keys (dq; 2 x 96 + 48 + 192 + 64 columns of TMEM) and
+// 64 query rows (dk, dv; 128 + 192 + 2 x 64 + 2 x 32).
+//
+// What bounds dk and dv at 192 columns: a block's products are 1280 cycles, but 1600 as both
+// operands of S^T and T^T come from shared memory and N = 64 (48 cycles for each 16 columns
+// where the product itself takes 32).  8192 tokens of 32 heads: 945 us, 2080 cycles a block
+// with all that a tile costs once (8000 cycles to the first scores, 5500 for the sums' way
+// out); dq 617 us.  At 128 columns K stays in TMEM as A of S^T and a block is 1152 cycles.
 //
 // All waits are bounded, as in the forward.
 #pragma once
@@ -381,18 +387,16 @@ __global__ void __launch_bounds__(MhaDqShape<DQK>::kThreads, 1) dense_mha_dq_ker
       mbar_wait(smem_u32(drain), 0, global_timer_ns() + 100000000ull, &never);
     } else if (blocks > 0) {
       if (lane_id() == 0) {
-        {
-          int kf = 0, vf = 0;
-          if (!mha_dq_load<DQK>(p, m, sb, w, t0, blocks, pack0, kf, vf)) mha_bwd_raise(m, kErrMhaDqLoadWait);
-          // every copy issued has landed before the CTA exits
-          const uint64_t dl = global_timer_ns() + 100000000ull;
-          mbar_wait(smem_u32(&m.q_full), 0, dl, &never);
-          mbar_wait(smem_u32(&m.o_full), 0, dl, &never);
-          for (int i = max(0, kf - C::kKStages); i < kf; ++i)
-            mbar_wait(smem_u32(&m.k_full[i % C::kKStages]), i / C::kKStages & 1, dl, &never);
-          for (int i = max(0, vf - C::kVStages); i < vf; ++i)
-            mbar_wait(smem_u32(&m.v_full[i % C::kVStages]), i / C::kVStages & 1, dl, &never);
-        }
+        int kf = 0, vf = 0;
+        if (!mha_dq_load<DQK>(p, m, sb, w, t0, blocks, pack0, kf, vf)) mha_bwd_raise(m, kErrMhaDqLoadWait);
+        // every copy issued has landed before the CTA exits
+        const uint64_t dl = global_timer_ns() + 100000000ull;
+        mbar_wait(smem_u32(&m.q_full), 0, dl, &never);
+        mbar_wait(smem_u32(&m.o_full), 0, dl, &never);
+        for (int i = max(0, kf - C::kKStages); i < kf; ++i)
+          mbar_wait(smem_u32(&m.k_full[i % C::kKStages]), i / C::kKStages & 1, dl, &never);
+        for (int i = max(0, vf - C::kVStages); i < vf; ++i)
+          mbar_wait(smem_u32(&m.v_full[i % C::kVStages]), i / C::kVStages & 1, dl, &never);
       }
       __syncwarp();
     }
@@ -808,16 +812,14 @@ __global__ void __launch_bounds__(MhaDkvShape<DQK>::kThreads, 1) dense_mha_dkv_k
         commit_to(elect_one(), drain);   // every MMA issued completes before TMEM is freed
         mbar_wait(smem_u32(drain), 0, global_timer_ns() + 100000000ull, &never);
       } else if (lane_id() == 0) {
-        {
-          int fills = 0;
-          if (!mha_dkv_load<DQK>(p, m, sb, w, s, kvh, fills)) mha_bwd_raise(m, kErrMhaDkvLoadWait);
-          // every copy issued has landed before the CTA exits
-          const uint64_t dl = global_timer_ns() + 100000000ull;
-          mbar_wait(smem_u32(&m.k_full), 0, dl, &never);
-          for (int i = max(0, fills - C::kStages); i < fills; ++i) {
-            mbar_wait(smem_u32(&m.q_full[i % C::kStages]), i / C::kStages & 1, dl, &never);
-            mbar_wait(smem_u32(&m.do_full[i % C::kStages]), i / C::kStages & 1, dl, &never);
-          }
+        int fills = 0;
+        if (!mha_dkv_load<DQK>(p, m, sb, w, s, kvh, fills)) mha_bwd_raise(m, kErrMhaDkvLoadWait);
+        // every copy issued has landed before the CTA exits
+        const uint64_t dl = global_timer_ns() + 100000000ull;
+        mbar_wait(smem_u32(&m.k_full), 0, dl, &never);
+        for (int i = max(0, fills - C::kStages); i < fills; ++i) {
+          mbar_wait(smem_u32(&m.q_full[i % C::kStages]), i / C::kStages & 1, dl, &never);
+          mbar_wait(smem_u32(&m.do_full[i % C::kStages]), i / C::kStages & 1, dl, &never);
         }
       }
       __syncwarp();

@@ -12,7 +12,7 @@
 //
 //   warps 0 .. 4 NT - 1  softmax, a thread per row: S from TMEM, running maximum and
 //                        sum, P (bf16) back into the same TMEM columns; the epilogue
-//   warp 4 NT            one thread issues the MMAs:
+//   warp 4 NT            issues the MMAs (one thread, chosen by the whole warp):
 //                          S_t = Q_t K_j^T   (both operands in shared memory)
 //                          O_t += P_t V_j    (P_t in TMEM)
 //   warp 4 NT + 1        one thread issues the TMA loads: Q once, then K and V through
@@ -22,11 +22,20 @@
 // With two tiles the tensor core works on one while the softmax works on the other.  Where
 // there are few tiles a CTA takes one, and a cluster of CTAs shares its keys out: each
 // leaves its O, maximum and sum in its shared memory, and every CTA of the cluster joins a
-// share of the rows from there.  O
-// is rescaled only when a row's maximum has grown by more than 2^8: until then the
-// weights are relative to the older maximum, which the sum and the LSE take into
-// account exactly.  P is rounded to bf16 for the product (2^-8 of each weight at most);
-// scores, sums and O are fp32.
+// share of the rows from there.  O is
+// rescaled only when a row's maximum has grown by more than 2^8: until then the weights
+// are relative to the older maximum, which the sum and the LSE take into account exactly.
+// P is rounded to bf16 for the product (2^-8 of each weight at most); scores, sums and O
+// are fp32.
+//
+// What bounds it: the products (768 + 512 cycles a tile and block at 192 columns), as long
+// as a softmax of one tile ends within the products of the other.  8192 tokens of 64 heads
+// take 913 us, 1505 TFLOP/s or 80% of a large library product's rate; the rest is the
+// pipeline's filling per tile and the diagonal's half-empty blocks.  Packed prompts of 3 to
+// 2000 tokens take 152 us for 134 GFLOP: each CTA has some 5 to 15 blocks, and about 10000
+// cycles go into starting (finding the tile, Q and K from memory) and the way out.  One
+// token against 5001 keys is 14 us, of which the launch, the first loads and the join are
+// all but 4.
 //
 // All waits are bounded; a CTA that times out records an error, waits (bounded) for its
 // copies and MMAs in flight, frees TMEM and returns.
@@ -514,8 +523,7 @@ struct MhaFwdShape {
   static constexpr uint32_t kMiscOff = kQBytes + kUnits * kMhaUnit;
   static constexpr int kBytes = static_cast<int>(kMiscOff) + static_cast<int>(sizeof(MhaMisc)) + 1024;
   static constexpr int kAhead = NT == 1 ? 2 : 1;               // key blocks whose scores are ahead of the weights
-  static constexpr int kThreads = NT * 128 + 64;               // two tiles: 200 registers each, no more than their rows take
-  static constexpr int kTmemCols = 512;
+  static constexpr int kThreads = NT * 128 + 64;               // two tiles: ptxas leaves 168 registers each, which spills 84 bytes
   static constexpr uint32_t kO = 256;                          // columns of TMEM: two S of 128 each, then O
   static_assert(kUnits >= kSub + 4, "a K block and two V blocks");
   static_assert(kBytes <= kMaxSmem, "shared memory");
@@ -986,7 +994,7 @@ __global__ void __launch_bounds__(MhaFwdShape<DQK, NT>::kThreads, 1) dense_mha_f
     prefetch_tmap(&p.map_v);
   }
   if (warp == 4 * NT) {
-    tmem_alloc(smem_u32(&m.tmem_base), C::kTmemCols);
+    tmem_alloc(smem_u32(&m.tmem_base), 512);
     tmem_relinquish();
   }
   if (warp == 4 * NT + 1) {
@@ -1015,16 +1023,14 @@ __global__ void __launch_bounds__(MhaFwdShape<DQK, NT>::kThreads, 1) dense_mha_f
         commit_to(elect_one(), &m.drain);
         mbar_wait(smem_u32(&m.drain), 0, global_timer_ns() + 100000000ull, &never);
       } else if (s.most > 0 && lane_id() == 0) {
-        {
-          uint32_t fills = 0;
-          if (!mha_load<DQK, NT>(p, m, sb, w, s, pack0, pack0 / p.group, fills)) mha_raise(m, kErrMhaLoadWait);
-          // every copy issued has landed before the CTA exits (only a unit's last fill can be in flight)
-          const uint64_t dl = global_timer_ns() + 100000000ull;
-          for (int t = 0; t < NT; ++t)
-            if (s.blocks[t] > 0) mbar_wait(smem_u32(&m.q_full[t]), 0, dl, &never);
-          for (uint32_t i = fills > C::kUnits ? fills - C::kUnits : 0; i < fills; ++i)
-            mbar_wait(smem_u32(&m.full[i % C::kUnits]), (i / C::kUnits) & 1u, dl, &never);
-        }
+        uint32_t fills = 0;
+        if (!mha_load<DQK, NT>(p, m, sb, w, s, pack0, pack0 / p.group, fills)) mha_raise(m, kErrMhaLoadWait);
+        // every copy issued has landed before the CTA exits (only a unit's last fill can be in flight)
+        const uint64_t dl = global_timer_ns() + 100000000ull;
+        for (int t = 0; t < NT; ++t)
+          if (s.blocks[t] > 0) mbar_wait(smem_u32(&m.q_full[t]), 0, dl, &never);
+        for (uint32_t i = fills > C::kUnits ? fills - C::kUnits : 0; i < fills; ++i)
+          mbar_wait(smem_u32(&m.full[i % C::kUnits]), (i / C::kUnits) & 1u, dl, &never);
       }
       __syncwarp();
     }
@@ -1032,7 +1038,7 @@ __global__ void __launch_bounds__(MhaFwdShape<DQK, NT>::kThreads, 1) dense_mha_f
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 4 * NT) tmem_dealloc(tmem, C::kTmemCols);
+  if (warp == 4 * NT) tmem_dealloc(tmem, 512);
   if constexpr (NT == 1) {
     if (p.cluster > 1) {
       cluster_sync();   // every CTA's part is there

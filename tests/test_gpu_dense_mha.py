@@ -375,7 +375,7 @@ def test_few_rows_and_values_that_are_not_finite(smla, what):
     (192, 64, 64, [1100], [1100]), (128, 64, 8, [1300], [1300]), (192, 64, 8, [900, 1300, 600], [1000, 1300, 700]),
     (128, 160, 32, [513], [900]), (192, 96, 96, [700, 1025], [640, 1025]), (128, 128, 1, [700], [700])])
 def test_many_tiles(smla, d, h, hk, lq, lk):
-    """Pairs of CTAs that share their products; rows that end in either CTA's tiles, and before them."""
+    """Two tiles to a CTA; rows that end in either, and before them."""
     _run(smla, h + lq[0], lq, lk, h, hk, d, tail=3)
 
 
@@ -395,3 +395,35 @@ def test_many_tiles_and_hidden_values_that_are_not_finite(smla, at, what):
     assert torch.equal(out[..., ~cols], want[0][..., ~cols]) and not out[at:][..., cols].isfinite().any()
     out, lse = smla.dense_mha_fwd(q, k2, v2, 0.1)
     assert torch.equal(lse[:at], want[1][:at]) and torch.equal(out[:at], want[0][:at])
+
+
+@pytest.mark.parametrize("d,h,hk", [(192, 2, 2), (128, 10, 2)])
+@pytest.mark.parametrize("lq,lk", [([5, 700, 1], [9000, 700, 4500]), ([4400, 3, 70], [4400, 3, 4300]),
+                                   ([30, 1, 2500] + [9] * 40, [30, 6000, 2500] + [11] * 40)])
+def test_sequences_of_very_different_lengths(smla, lq, lk, d, h, hk):
+    """Tiles of more blocks than a warp has lanes, and more sequences than that."""
+    _run(smla, sum(lk), lq, lk, h, hk, d, tail=2)
+
+
+def test_more_heads_than_run_side_by_side(smla):
+    _run(smla, 24, [5200], [5200], 24, 24, 192, dense=True)
+
+
+def test_two_calls_at_once(smla):
+    sets = [_inputs(20 + i, lq, lk, 8, 2, 192) for i, (lq, lk) in
+            enumerate((([700, 1, 333], [900, 1, 333]), ([64, 1000], [640, 1000])))]
+
+    def both(q, k, v, do, cq, ck):
+        a = smla.dense_mha_fwd(q, k, v, 0.1, cq, ck)
+        return a + smla.dense_mha_bwd(q, k, v, 0.1, *a, do, cq, ck)
+
+    want = [both(*s) for s in sets]
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream(), torch.cuda.Stream()], []
+    for _ in range(4):
+        for st, s in zip(streams, sets):
+            with torch.cuda.stream(st):
+                got.append(both(*s))
+    torch.cuda.synchronize()
+    for i, g in enumerate(got):
+        assert all(torch.equal(x, y) for x, y in zip(g, want[i % 2]))

@@ -5,6 +5,8 @@ import glob
 import os
 import re
 
+import math
+
 import pytest
 import torch
 
@@ -217,3 +219,25 @@ def test_dense_mha_bwd_hands_over(b):  # noqa: F811
         _ok(b, "dense_mha_bwd", b.dense_mha_bwd, **_bwd_args(**kw))
     dq, dk, dv = b.dense_mha_bwd(**_bwd_args(), stream=STREAM)
     assert dq.shape == (5, 8, 192) and dk.shape == (9, 4, 192) and dv.shape == (9, 4, 128)
+
+
+def test_dense_mha_refuses_memory_that_it_reads(b):  # noqa: F811
+    def part(pool, start, *shape):
+        n = math.prod(shape)
+        return pool[start:start + n].view(*shape)
+
+    pool = torch.zeros(1 << 16, dtype=BF)
+    q, out = part(pool, 0, 5, 8, 192), part(pool, 7680, 5, 8, 128)
+    _ok(b, "dense_mha_fwd", b.dense_mha_fwd, **dict(_mha_args(), q=q, out=out))
+    for kw in (dict(out=part(pool, 7672, 5, 8, 128)), dict(out=part(pool, 0, 5, 8, 128)),
+               dict(lse=part(pool, 7600, 80).view(F32)), dict(out=out, lse=part(pool, 12720, 80).view(F32))):
+        _refused(b, b.dense_mha_fwd, **dict(_mha_args(), q=q, **kw))
+    latent = part(pool, 0, 9, 4, 384)   # an output between the rows' parts that are read
+    _refused(b, b.dense_mha_fwd, **dict(_mha_args(), k=latent[..., :192], out=part(pool, 192, 5, 8, 128)))
+    a = _bwd_args(q=q, out=out)
+    dk, dv = part(pool, 16384, 9, 4, 192), part(pool, 24576, 9, 4, 128)
+    _ok(b, "dense_mha_bwd", b.dense_mha_bwd, **dict(a, dk=dk, dv=dv, dq=part(pool, 32768, 5, 8, 192)))
+    for kw in (dict(dq=q), dict(dk=part(pool, 12792, 9, 4, 192)), dict(dk=dk, dv=part(pool, 16384, 9, 4, 128)),
+               dict(dv=part(pool, 0, 9, 4, 128)),
+               dict(dv=dv, workspace=dv.view(torch.uint8).view(-1))):
+        _refused(b, b.dense_mha_bwd, **dict(a, **kw))
