@@ -478,8 +478,10 @@ size_t mla_add_norm_bwd_workspace_size(int n, int d);
  *   fill DENSE_MHA_FILL_OUT | DENSE_MHA_FILL_LSE
  *
  * d_qk is 192 or 128 and d_v 128 (SPARSE_MLA_ERR_UNSUPPORTED_SHAPE otherwise);
- * h_kv divides h_q.  Sums are taken in a fixed order: the same call gives the
- * same bits.
+ * h_kv divides h_q.  Keys and values that a query does not see have no part in
+ * its row, not even where they are NaN or infinite.  Outputs share no memory
+ * with each other or the inputs.  Sums are taken in a fixed order: the same call
+ * gives the same bits.
  */
 sparse_mla_status_t dense_mha_fwd(const void* q, long long q_tok_stride, long long q_head_stride, const void* k,
                                   long long k_tok_stride, long long k_head_stride, const void* v,
@@ -504,8 +506,9 @@ sparse_mla_status_t dense_mha_fwd(const void* q, long long q_tok_stride, long lo
  *                  aligned; contents ignored.  Two calls that may run
  *                  concurrently need separate workspaces
  *
- * Rows of no sequence take no part: their gradients are zero.  Sums are taken
- * in a fixed order: the same call gives the same bits.
+ * Rows of no sequence take no part: their gradients are zero.  Outputs and
+ * workspace share no memory with each other or the inputs.  Sums are taken in a
+ * fixed order: the same call gives the same bits.
  */
 sparse_mla_status_t dense_mha_bwd(const void* q, long long q_tok_stride, long long q_head_stride, const void* k,
                                   long long k_tok_stride, long long k_head_stride, const void* v,

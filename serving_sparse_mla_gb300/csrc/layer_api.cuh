@@ -42,8 +42,14 @@ smla::AddNormParams add_norm_params(const void* x, long long x_stride, const voi
   return p;
 }
 
-// Vectors of 8 values per thread, and threads: whole warps that hold a row.
-int add_norm_vectors(int d, bool backward) { return d <= (backward ? 8192 : 2048) ? 1 : 2; }
+// Vectors of 8 values per thread, and threads: whole warps that hold a row.  The forward
+// takes two: one takes 0.6 us less for a single row of 1536 but longer for many (16384 x 1536
+// in 16 bits, groups: 40 and 47 us against 34 and 40; 8192 x 7168: 87 and 106 against 73 and
+// 93), four with 80 registers 38, 45, 76 and 91.  The backward, with twice the values in a
+// thread's registers, takes one up to the 1024 threads of a CTA (8192 x 7168: 74 us, with
+// two 108).
+constexpr int kAddNormVectors = 2;
+int add_norm_bwd_vectors(int d) { return d <= 8192 ? 1 : 2; }
 int add_norm_threads(int d, int v) { return ((d / 8 + v - 1) / v + 31) / 32 * 32; }
 
 // CTAs: as many as are resident at once.
@@ -53,11 +59,10 @@ int add_norm_ctas(int n, int threads, int sms, int regs) {
 }
 constexpr int kAddNormBwdRegs = 64;
 
-template <int V>
 void add_norm_launch(const smla::AddNormParams& p, int form, int ctas, int threads, cudaStream_t cs) {
-  if (form == smla::kAddNormBf16) smla::add_norm_kernel<V, smla::kAddNormBf16><<<ctas, threads, 0, cs>>>(p);
-  else if (form == smla::kAddNormGroups) smla::add_norm_kernel<V, smla::kAddNormGroups><<<ctas, threads, 0, cs>>>(p);
-  else smla::add_norm_kernel<V, smla::kAddNormRow><<<ctas, threads, 0, cs>>>(p);
+  if (form == smla::kAddNormBf16) smla::add_norm_kernel<kAddNormVectors, smla::kAddNormBf16><<<ctas, threads, 0, cs>>>(p);
+  else if (form == smla::kAddNormGroups) smla::add_norm_kernel<kAddNormVectors, smla::kAddNormGroups><<<ctas, threads, 0, cs>>>(p);
+  else smla::add_norm_kernel<kAddNormVectors, smla::kAddNormRow><<<ctas, threads, 0, cs>>>(p);
 }
 
 }  // namespace
@@ -84,11 +89,9 @@ sparse_mla_status_t mla_add_norm(const void* x, long long x_stride, const void* 
   p.z = static_cast<__nv_bfloat16*>(residual_out);
   p.out = out;
   p.scales = scales;
-  const int v = add_norm_vectors(d, false), threads = add_norm_threads(d, v);
-  const int ctas = add_norm_ctas(n, threads, sms, smla::kAddNormRegs);
-  cudaStream_t cs = static_cast<cudaStream_t>(stream);
-  if (v == 1) add_norm_launch<1>(p, out_format, ctas, threads, cs);
-  else add_norm_launch<2>(p, out_format, ctas, threads, cs);
+  const int threads = add_norm_threads(d, kAddNormVectors);
+  add_norm_launch(p, out_format, add_norm_ctas(n, threads, sms, smla::kAddNormRegs), threads,
+                  static_cast<cudaStream_t>(stream));
   return cudaGetLastError() == cudaSuccess ? SPARSE_MLA_OK : SPARSE_MLA_ERR_CUDA;
 }
 
@@ -96,7 +99,7 @@ size_t mla_add_norm_bwd_workspace_size(int n, int d) {
   if (n < 1 || d < 8 || d % 8 != 0 || d > smla::kAddNormMaxWidth) return 0;
   int sms = 0;
   if (device_setup(&sms) != SPARSE_MLA_OK) return 0;
-  const int ctas = add_norm_ctas(n, add_norm_threads(d, add_norm_vectors(d, true)), sms, kAddNormBwdRegs);
+  const int ctas = add_norm_ctas(n, add_norm_threads(d, add_norm_bwd_vectors(d)), sms, kAddNormBwdRegs);
   return static_cast<size_t>(ctas) * static_cast<size_t>(d) * sizeof(float);   // one share of the sums per CTA
 }
 
@@ -125,7 +128,7 @@ sparse_mla_status_t mla_add_norm_bwd(const void* z, long long z_stride, const vo
   p.dresidual_step = dresidual_stride;
   p.dx = static_cast<__nv_bfloat16*>(dx);
   p.part = static_cast<float*>(workspace);
-  const int v = add_norm_vectors(d, true), threads = add_norm_threads(d, v);
+  const int v = add_norm_bwd_vectors(d), threads = add_norm_threads(d, v);
   const int ctas = add_norm_ctas(n, threads, sms, kAddNormBwdRegs);
   if (v == 1) smla::add_norm_bwd_kernel<1><<<ctas, threads, 0, cs>>>(p);
   else smla::add_norm_bwd_kernel<2><<<ctas, threads, 0, cs>>>(p);
