@@ -65,7 +65,6 @@ struct MhaBwdParams {
   int pack, tok_tile;                      // rows of a query tile: tok_tile tokens x pack heads
   MhaDiv per;                              // tok_tile
   int slots;                               // tiles per head (pack) that the grid has room for
-  int heads;                               // head packs (of keys: heads)
   MhaHeads order;
   float scale, scale_log2;
   const __nv_bfloat16* k;                  // row (t, h) at k + t k_tok + h k_head
@@ -325,7 +324,7 @@ __global__ void __launch_bounds__(MhaDqShape<DQK>::kThreads, 1) dense_mha_dq_ker
   const uint32_t sb = smem_u32(sbase);
   asm volatile("griddepcontrol.launch_dependents;");   // dk's and dv's kernel may be set up (it waits for this grid's end)
   int slot, head;
-  mha_unit(blockIdx.x, p.slots, p.heads, p.order, slot, head);
+  mha_unit(static_cast<int>(blockIdx.x), p.slots, p.order, slot, head);
   const int pack0 = head * p.pack;
 
   if (threadIdx.x == 0) {
@@ -448,7 +447,7 @@ struct MhaQueries {
   __device__ __forceinline__ MhaQueries(const MhaBwdParams& p, const MhaWork& w) {
     const int lq = w.q1 - w.q0, lk = w.k1 - w.k0;
     first = max(0, w.tile * kMhaTile - (lk - lq));
-    blocks = first < lq ? (lq - first + p.tok_tile - 1) / p.tok_tile : 0;
+    blocks = first < lq ? p.per.of(lq - first + p.tok_tile - 1) : 0;
     total = blocks * (p.group / p.pack);
   }
 };
@@ -742,7 +741,7 @@ __global__ void __launch_bounds__(MhaDkvShape<DQK>::kThreads, 1) dense_mha_dkv_k
   const int warp = static_cast<int>(threadIdx.x >> 5);
   const uint32_t sb = smem_u32(sbase);
   int slot, kvh;
-  mha_unit(blockIdx.x, p.slots, p.heads, p.order, slot, kvh);
+  mha_unit(static_cast<int>(blockIdx.x), p.slots, p.order, slot, kvh);
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 4; ++i) {

@@ -63,19 +63,22 @@ enum MhaErrCode : int {
   kErrMhaSoftmaxWait = 0x703,
 };
 
-// n / d for n < 2^31 as n m >> s: with s = 31 + log2 d (rounded up) and m = 2^s / d + 1
-// (rounded down), m d is above 2^s by d <= 2^(s - 31) at most.
+// n / d for n < 2^31 as 2n m >> 32 + log: with log = log2 d (rounded up) and m = 2^(31 + log)
+// / d + 1 (rounded down, below 2^32), m d is above 2^(31 + log) by d <= 2^log at most.
 struct MhaDiv {
-  unsigned long long m;
-  int d, s;
-  __device__ __forceinline__ int of(int n) const { return static_cast<int>(static_cast<unsigned>(n) * m >> s); }
+  unsigned m;
+  int d, log;
+  __device__ __forceinline__ int of(int n) const {
+    return static_cast<int>(__umulhi(static_cast<unsigned>(n) << 1, m) >> log);
+  }
 };
 
 // Heads (packs of them) whose tiles run side by side, the longest first: `near` at a time, so
 // that what they read stays close, and behind the first `lead` all of the rest, so that the
 // SMs end together.
 struct MhaHeads {
-  int near, lead;
+  MhaDiv near, tiles, rest;   // tiles: of `near` heads; rest: heads behind the first `lead`
+  int lead;
 };
 
 struct MhaFwdParams {
@@ -85,7 +88,6 @@ struct MhaFwdParams {
   int pack, tok_tile;                      // a tile is tok_tile tokens x pack heads
   MhaDiv per;                              // tokens of a CTA (NT tiles)
   int slots;                               // tiles (of NT) per head pack that the grid has room for
-  int packs;                               // head packs
   MhaHeads order;
   int cluster;                             // CTAs that share a tile's keys out (one tile a CTA; else 1)
   float scale_log2;
@@ -171,6 +173,7 @@ __device__ __forceinline__ MhaWork mha_find(const int32_t* cu_q, const int32_t* 
       for (int base = 0; base < batch; base += 32) {
         const int4 x = base == 0 ? mine : seq(base + lane);
         const int lq = x.y - x.x, lk = x.w - x.z;
+#pragma unroll 1   // run once by each CTA: its instructions take longer to come than to run
         for (int i = 0; i < min(32, batch - base); ++i)
           n += mha_tiles_above<KEYS>(__shfl_sync(0xffffffffu, lq, i), __shfl_sync(0xffffffffu, lk, i), per, guess);
       }
@@ -220,17 +223,11 @@ __device__ __forceinline__ void mha_fill_rows(void* out, long long words, int fi
 }
 
 // Unit -> tile and head (pack).
-__device__ __forceinline__ void mha_unit(unsigned unit, int slots, int heads, const MhaHeads& h, int& slot, int& head) {
-  const unsigned lead = static_cast<unsigned>(h.lead) * static_cast<unsigned>(slots);
-  unsigned first = static_cast<unsigned>(h.lead), wide = static_cast<unsigned>(heads - h.lead), at = unit - lead;
-  if (unit < lead) {
-    wide = static_cast<unsigned>(h.near);
-    const unsigned per = static_cast<unsigned>(slots) * wide;
-    first = unit / per * wide;
-    at = unit % per;
-  }
-  slot = static_cast<int>(at / wide);
-  head = static_cast<int>(first + at % wide);
+__device__ __forceinline__ void mha_unit(int unit, int slots, const MhaHeads& h, int& slot, int& head) {
+  const int lead = h.lead * slots, turn = unit < lead ? h.tiles.of(unit) : 0;
+  const int at = unit < lead ? unit - turn * h.tiles.d : unit - lead;
+  slot = unit < lead ? h.near.of(at) : h.rest.of(at);
+  head = unit < lead ? turn * h.near.d + at - slot * h.near.d : h.lead + at - slot * h.rest.d;
 }
 
 // ------------------------------------------------------------------ PTX
@@ -968,7 +965,7 @@ __global__ void __launch_bounds__(MhaFwdShape<DQK, NT>::kThreads, 1) dense_mha_f
   const unsigned ctas = NT == 1 ? static_cast<unsigned>(p.cluster) : 1u, unit = blockIdx.x / ctas;
   const int rank = static_cast<int>(blockIdx.x % ctas);
   int slot, head;
-  mha_unit(unit, p.slots, p.packs, p.order, slot, head);
+  mha_unit(unit, p.slots, p.order, slot, head);
   const int pack0 = head * p.pack;
 
   if (threadIdx.x == 0) {

@@ -180,8 +180,8 @@ int mha_pack(int group, int rows) {
 
 smla::MhaDiv mha_div(int d) {
   int log = 0;
-  while (1 << log < d) ++log;
-  return {(1ull << (31 + log)) / static_cast<unsigned>(d) + 1, d, 31 + log};
+  while (1ll << log < d) ++log;
+  return {static_cast<unsigned>((1ull << (31 + log)) / static_cast<unsigned>(d) + 1), d, log};
 }
 
 // Tiles of `per` rows that any `batch` sequences of `total` rows (> 0) in all have at most
@@ -326,8 +326,8 @@ constexpr double kMhaNearKeys = 2.4e7, kMhaNearRows = 1.1e7;
 smla::MhaHeads mha_order(int heads, double bytes, double most, long long slots, int sms) {
   const double near = std::max(1.0, std::min<double>(heads, std::floor(most / (bytes + 1))));
   const double last = std::max(near, std::ceil(2.0 * sms / std::max<double>(slots, 1)));
-  const int n = static_cast<int>(near);
-  return {n, last < heads ? (heads - static_cast<int>(last)) / n * n : 0};
+  const int n = static_cast<int>(near), lead = last < heads ? (heads - static_cast<int>(last)) / n * n : 0;
+  return {mha_div(n), mha_div(lead > 0 ? static_cast<int>(slots) * n : 1), mha_div(heads - lead), lead};
 }
 
 // dq (and D into the workspace), then dk and dv.
@@ -383,8 +383,7 @@ sparse_mla_status_t mha_bwd_launch(const MhaRows& q, const MhaRows& k, const Mha
     const long long slots = mha_slots(total_q, p.tok_tile, seqs), ctas = slots * (h_q / p.pack);
     if (ctas > INT_MAX) return SPARSE_MLA_ERR_INVALID_ARG;
     p.slots = static_cast<int>(slots);
-    p.heads = h_q / p.pack;
-    p.order = mha_order(p.heads, static_cast<double>(total_kv) * (DQK + smla::kMhaDv) * 2 * p.pack / p.group,
+    p.order = mha_order(h_q / p.pack, static_cast<double>(total_kv) * (DQK + smla::kMhaDv) * 2 * p.pack / p.group,
                         kMhaNearKeys, slots, sms);
     smla::dense_mha_dq_kernel<DQK><<<static_cast<unsigned>(ctas), C::kThreads, C::kBytes, cs>>>(p);
     if (cudaGetLastError() != cudaSuccess) return SPARSE_MLA_ERR_CUDA;
@@ -395,7 +394,6 @@ sparse_mla_status_t mha_bwd_launch(const MhaRows& q, const MhaRows& k, const Mha
     const long long slots = mha_slots(total_kv, smla::kMhaTile, seqs), ctas = slots * h_kv;
     if (ctas > INT_MAX) return SPARSE_MLA_ERR_INVALID_ARG;
     p.slots = static_cast<int>(slots);
-    p.heads = h_kv;
     p.order = mha_order(h_kv, static_cast<double>(total_q) * (DQK + smla::kMhaDv) * 2 * p.group,
                         kMhaNearRows, slots, sms);
     // its CTAs may take the SMs that the last tiles of dq leave (and themselves wait for D)
@@ -469,11 +467,10 @@ sparse_mla_status_t dense_mha_fwd(const void* q, long long q_tok_stride, long lo
     return st;
   p.cluster = plan.cluster;
   p.per = mha_div(p.tok_tile * plan.tiles);
-  p.packs = h_q / p.pack;
-  p.order = mha_order(p.packs, static_cast<double>(total_kv) * (d_qk + d_v) * 2 * p.pack / group, kMhaNearKeys,
-                      plan.slots, sms);
   const long long ctas = plan.slots * (h_q / p.pack) * plan.cluster;
   if (ctas > INT_MAX) return SPARSE_MLA_ERR_INVALID_ARG;
+  p.order = mha_order(h_q / p.pack, static_cast<double>(total_kv) * (d_qk + d_v) * 2 * p.pack / group, kMhaNearKeys,
+                      plan.slots, sms);
   p.slots = static_cast<int>(plan.slots);
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   const unsigned n = static_cast<unsigned>(ctas);
