@@ -32,7 +32,7 @@
 // as a softmax of one tile ends within the products of the other.  8192 tokens of 64 heads
 // take 913 us, 1505 TFLOP/s or 80% of a large library product's rate; the rest is the
 // pipeline's filling per tile and the diagonal's half-empty blocks.  Packed prompts of 3 to
-// 2000 tokens take 152 us for 134 GFLOP: each CTA has some 5 to 15 blocks, and about 10000
+// 2000 tokens take 148 us for 134 GFLOP: each CTA has some 5 to 15 blocks, and about 9000
 // cycles go into starting (finding the tile, Q and K from memory) and the way out.  One
 // token against 5001 keys is 14 us, of which the launch, the first loads and the join are
 // all but 4.
@@ -114,103 +114,71 @@ struct MhaWork {
   int end;              // of the sequences' rows: the ones behind belong to none
 };
 
-// The tiles of one sequence that have more than `blocks` blocks of work (-1: all).
-//   queries: tiles of `per` rows; a block is 128 of the keys that the last row sees
-//   keys:    tiles of 128 rows; a block is `per` of the queries that see the first row
-template <bool KEYS>
-__device__ __forceinline__ int mha_tiles_above(int lq, int lk, const MhaDiv& per, int blocks) {
-  if constexpr (KEYS) {
-    const int tiles = (lk + kMhaTile - 1) >> 7;
-    const int seen = lq - blocks * per.d;   // the first row's queries start before this one
-    return blocks < 0 ? tiles : (seen <= 0 ? 0 : min(tiles, max(0, (seen + lk - lq + kMhaTile - 1) >> 7)));
-  } else {
-    const int tiles = per.of(lq + per.d - 1);
-    const int past = blocks * kMhaTile + lq - lk;   // the last row is behind this one
-    return blocks < 0 || past <= 0 ? tiles : (past >= lq ? 0 : tiles - per.of(past));
-  }
-}
-
-constexpr int kMhaSortBatch = 128;   // sequences up to which tiles are handed out by their work
-
-// Tile `slot` of all sequences' tiles, the ones with most work first (of many sequences: in
-// their order); q1 = k1 = 0 where there are not so many.  One warp, all lanes.
+// Tile `slot` of all sequences' tiles; q1 = k1 = 0 where there are not so many.  Up to 32
+// sequences are taken from the longest to the shortest (of keys, whose tiles' work is the
+// queries: by their queries), so that the SMs end together; more in their order.  A
+// sequence's tiles come with the most work first: its last of queries, its first of keys.
+// One warp, all lanes.  Every CTA goes through this before it can load anything, so it is
+// kept short: with all tiles in the order of their work, by a search, 100 texts of 3 to 600
+// tokens took 436 us where they take 256, and 15 of up to 2000 249 where they take 222; with
+// every batch in its order the gradients of 9 texts of 122 to 2119 take 624 in the place of 584.
 template <bool KEYS>
 __device__ __forceinline__ MhaWork mha_find(const int32_t* cu_q, const int32_t* cu_kv, int batch, int total_q,
                                             int total_kv, int slot, const MhaDiv& per) {
   MhaWork w = {0, 0, 0, 0, 0, KEYS ? total_kv : total_q};
+  auto tiles = [&](int lq, int lk) { return KEYS ? (lk + kMhaTile - 1) >> 7 : per.of(lq + per.d - 1); };
   if (cu_q == nullptr) {
-    const int tiles = mha_tiles_above<KEYS>(total_q, total_kv, per, -1);
-    if (slot < tiles) {
+    const int n = tiles(total_q, total_kv);
+    if (slot < n) {
       w.q1 = total_q;
       w.k1 = total_kv;
-      w.tile = KEYS ? slot : tiles - 1 - slot;
+      w.tile = KEYS ? slot : n - 1 - slot;
     }
     return w;
   }
   const int lane = static_cast<int>(lane_id());
-  auto seq = [&](int b) -> int4 {
-    if (b >= batch) return make_int4(0, 0, 0, 0);
-    const int q0 = mha_offset(cu_q, b, total_q), k0 = mha_offset(cu_kv, b, total_kv);
-    return make_int4(q0, max(q0, mha_offset(cu_q, b + 1, total_q)), k0, max(k0, mha_offset(cu_kv, b + 1, total_kv)));
-  };
-  const int4 mine = seq(lane);   // of the first 32, which are often all
-  auto above = [&](const int4& x, int blocks) { return mha_tiles_above<KEYS>(x.y - x.x, x.w - x.z, per, blocks); };
-  int longest = 0;   // most blocks of a tile, or more
-  w.end = 0;
-  for (int base = 0; base < batch; base += 32) {
-    const int4 x = base == 0 ? mine : seq(base + lane);
-    longest = max(longest, __reduce_max_sync(0xffffffffu, KEYS ? per.of(x.y - x.x + per.d - 1) : (x.w - x.z + 127) >> 7));
-    w.end = max(w.end, __reduce_max_sync(0xffffffffu, KEYS ? x.w : x.y));
-  }
-  // the tiles before this one have more than `blocks` blocks, or as many and lie in earlier sequences
-  int blocks = -1, before = 0;
-  if (batch > 1 && batch <= kMhaSortBatch) {
-    // the fewest blocks that at most `slot` tiles exceed, by 32 guesses at a time
-    int lo = 0, hi = longest;
-    while (lo < hi) {
-      const int step = (hi - lo + 31) >> 5, guess = min(hi, lo + lane * step);
-      int n = 0;
-      for (int base = 0; base < batch; base += 32) {
-        const int4 x = base == 0 ? mine : seq(base + lane);
-        const int lq = x.y - x.x, lk = x.w - x.z;
-#pragma unroll 1   // run once by each CTA: its instructions take longer to come than to run
-        for (int i = 0; i < min(32, batch - base); ++i)
-          n += mha_tiles_above<KEYS>(__shfl_sync(0xffffffffu, lq, i), __shfl_sync(0xffffffffu, lk, i), per, guess);
-      }
-      const uint32_t few = __ballot_sync(0xffffffffu, n <= slot);
-      const int at = few != 0u ? __ffs(few) - 1 : 32;
-      const int next = at > 0 ? __shfl_sync(0xffffffffu, guess, at - 1) + 1 : lo;
-      if (at < 32) {
-        hi = __shfl_sync(0xffffffffu, guess, at);
-        before = __shfl_sync(0xffffffffu, n, at);
-      }
-      lo = min(next, hi);
+  int end = 0;
+#pragma unroll 4
+  for (int b = lane; b < batch; b += 32) end = max(end, KEYS ? mha_offset(cu_kv, b + 1, total_kv) : mha_offset(cu_q, b + 1, total_q));
+  w.end = __reduce_max_sync(0xffffffffu, end);
+  int4 x;          // a lane's sequence, its tiles, and the tiles before them
+  int n, before;
+  uint32_t past = 0u;
+  for (int base = 0, all = 0; base < batch && past == 0u; base += 32) {
+    x = make_int4(0, 0, 0, 0);
+    if (const int b = base + lane; b < batch) {
+      const int q0 = mha_offset(cu_q, b, total_q), k0 = mha_offset(cu_kv, b, total_kv);
+      x = make_int4(q0, max(q0, mha_offset(cu_q, b + 1, total_q)), k0, max(k0, mha_offset(cu_kv, b + 1, total_kv)));
     }
-    blocks = hi;
-  }
-  for (int base = 0; base < batch; base += 32) {
-    const int4 x = base == 0 ? mine : seq(base + lane);
-    const int more = blocks < 0 ? 0 : above(x, blocks);
-    const int n = above(x, blocks - 1) - more;   // of so many blocks (or, unsorted, all)
-    int incl = n;
+    n = tiles(x.y - x.x, x.w - x.z);
+    if (batch <= 32) {
+      const int key = KEYS ? x.y - x.x : x.w - x.z;
+      before = 0;
+#pragma unroll 4
+      for (int i = 0; i < batch; ++i) {
+        const int other = __shfl_sync(0xffffffffu, key, i), m = __shfl_sync(0xffffffffu, n, i);
+        before += other > key || (other == key && i < lane) ? m : 0;
+      }
+    } else {
+      before = all + n;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += y;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, before, o);
+        if (lane >= o) before += y - all;
+      }
+      before -= n;
     }
-    const uint32_t past = __ballot_sync(0xffffffffu, before + incl > slot);
-    if (past != 0u) {
-      const int at = __ffs(past) - 1;
-      w.q0 = __shfl_sync(0xffffffffu, x.x, at);
-      w.q1 = __shfl_sync(0xffffffffu, x.y, at);
-      w.k0 = __shfl_sync(0xffffffffu, x.z, at);
-      w.k1 = __shfl_sync(0xffffffffu, x.w, at);
-      const int nth = slot - before - __shfl_sync(0xffffffffu, incl - n, at) + __shfl_sync(0xffffffffu, more, at);
-      // the most work is in a sequence's last tile of queries, in its first of keys
-      w.tile = KEYS ? nth : mha_tiles_above<KEYS>(w.q1 - w.q0, w.k1 - w.k0, per, -1) - 1 - nth;
-      return w;
-    }
-    before += __shfl_sync(0xffffffffu, incl, 31);
+    past = __ballot_sync(0xffffffffu, before <= slot && slot - before < n);
+    all += __reduce_add_sync(0xffffffffu, n);
+  }
+  if (past != 0u) {
+    const int at = __ffs(past) - 1;
+    w.q0 = __shfl_sync(0xffffffffu, x.x, at);
+    w.q1 = __shfl_sync(0xffffffffu, x.y, at);
+    w.k0 = __shfl_sync(0xffffffffu, x.z, at);
+    w.k1 = __shfl_sync(0xffffffffu, x.w, at);
+    const int nth = slot - __shfl_sync(0xffffffffu, before, at);
+    w.tile = KEYS ? nth : __shfl_sync(0xffffffffu, n, at) - 1 - nth;
   }
   return w;
 }

@@ -171,7 +171,8 @@ sparse_mla_status_t check_mha(const MhaRows& q, const MhaRows& k, const MhaRows&
 }
 
 // Query heads of one group that a tile of `rows` takes side by side: the most that leave
-// at most one row in 16 unused.
+// at most one row in 16 unused.  Without (us): 15 texts of up to 2000 tokens, 32 heads on 8, 276
+// in the place of 249, their gradients 762 and 722; 16 tokens' gradients on 9000 keys 122 and 97.
 int mha_pack(int group, int rows) {
   for (int n = group < rows ? group : rows; n > 1; --n)
     if (group % n == 0 && rows % n <= rows / 16) return n;
@@ -286,6 +287,10 @@ struct MhaPlan {
 // The layout whose slowest CTA has the least to do, by the sequences' mean lengths: key
 // blocks one after the other, of a longest tile and of the card's mean.  A CTA of two
 // tiles takes about as long for a block of both as one of a single tile for its own.
+// Measured (us; two tiles a CTA / one / one and the keys shared out):
+//   1 token on 5001 keys, 8 heads    64.7 /  59.9 / 14.5
+//   16 tokens on 9000, 32 heads on 8 102 / 76 / 27      1024 tokens, 8 heads  22.3 / 18.4 / 18.0
+//   15 texts to 2000, 32 heads on 8  222 / 355 (the latter with another order of the tiles)
 MhaPlan mha_plan(int total_q, int total_kv, int batch, bool packed, int packs, int tok_tile, int sms,
                  const int* clusters) {
   const double lq = static_cast<double>(total_q) / batch, lk = static_cast<double>(total_kv) / batch;
