@@ -647,7 +647,9 @@ __device__ __forceinline__ bool mha_dkv_rows(const MhaBwdParams& p, MhaDkvMisc& 
     // the columns that see this thread's key
     const int lo = edge ? p.pack * (key - (lk - lq) - t0) - kHalf * half : 0;
     const int hi = edge ? p.pack * (lq - t0) - kHalf * half : kHalf;
-    if (!warp_wait(smem_u32(&m.s_full), j & 1, deadline, ab)) return false;
+    // the rows' numbers are another warp's plain stores: what tells that they are there is its arrival beside the copy
+    // of Q, not the tensor core's on s_full
+    if (!warp_wait_both(smem_u32(&m.q_full[st]), turn, smem_u32(&m.s_full), j & 1, deadline, ab)) return false;
     tc_fence_after();
     float x[kHalf], y[kHalf];
     tmem_load<kHalf>(ts, x);
@@ -658,12 +660,10 @@ __device__ __forceinline__ bool mha_dkv_rows(const MhaBwdParams& p, MhaDkvMisc& 
       // the products with P and dS must not meet what is not finite in a row that does not
       // see a key; the product that gives T has read dout by then
       if (!warp_wait(smem_u32(&m.t_full), j & 1, deadline, ab)) return false;
-      if (!warp_wait(smem_u32(&m.q_full[st]), turn, deadline, ab) || !warp_wait(smem_u32(&m.do_full[st]), turn, deadline, ab))
-        return false;
+      if (!warp_wait(smem_u32(&m.do_full[st]), turn, deadline, ab)) return false;
       mha_clear<256>(sb + C::kQOff + st * C::kQBytes, C::kQBytes);
       mha_clear<256>(sb + C::kDoOff + st * C::kDoBytes, C::kDoBytes);
     }
-    // they came with Q, which S has read
     const float4* l4 = reinterpret_cast<const float4*>(&m.shift[st][kHalf * half]);
 #pragma unroll
     for (int i = 0; i < kHalf; i += 4) {

@@ -230,6 +230,16 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint64_
   return true;
 }
 
+// warp_wait for two barriers, of which the first has most likely been passed: their tries are under way together.
+__device__ __forceinline__ bool warp_wait_both(uint32_t bar, uint32_t parity, uint32_t bar2, uint32_t parity2,
+                                               uint64_t deadline_ns, const volatile int* abort_flag) {
+  for (;;) {
+    const bool one = mbar_try_wait(bar, parity), two = mbar_try_wait(bar2, parity2);
+    if (__all_sync(0xffffffffu, one && two)) return true;
+    if (__any_sync(0xffffffffu, *abort_flag != 0 || global_timer_ns() > deadline_ns)) return false;
+  }
+}
+
 // D[tmem] (+)= A * B[smem] by the chosen thread, A in shared memory or (a row per lane, two
 // bf16 values per column) in TMEM.
 __device__ __forceinline__ void mma_ss(uint32_t chosen, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
