@@ -713,9 +713,10 @@ __device__ __forceinline__ bool mha_mma(const MhaFwdParams& p, MhaMisc& m, uint3
 // A hidden key's weight is 0, but 0 times an infinity or a NaN is a NaN: before a product
 // with a block that some rows do not see all of, values that are not finite are taken
 // out of it.  Each of N threads (the CTA's first, or the N behind them) looks over its share
-// of `bytes`, a multiple of 2 KB; true where it found some.
+// of `bytes`, a multiple of 2 KB, and sets `found` where there are some, before it takes them
+// out: whoever meets zeros in their place finds it set.
 template <int N>
-__device__ __forceinline__ bool mha_clear(uint32_t tile, uint32_t bytes) {
+__device__ __forceinline__ void mha_clear(uint32_t tile, uint32_t bytes, int* found = nullptr) {
   uint32_t seen = 0;
   for (uint32_t at = threadIdx.x % N * 16; at < bytes; at += N * 16) {
     uint32_t x[4];
@@ -725,7 +726,11 @@ __device__ __forceinline__ bool mha_clear(uint32_t tile, uint32_t bytes) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) seen |= (x[i] & 0x7fff7fffu) + 0x00800080u;
   }
-  if ((seen & 0x80008000u) == 0u) return false;
+  if ((seen & 0x80008000u) == 0u) return;
+  if (found != nullptr) {
+    *reinterpret_cast<volatile int*>(found) = 1;
+    __threadfence_block();
+  }
   for (uint32_t at = threadIdx.x % N * 16; at < bytes; at += N * 16) {
     uint32_t x[4];
     asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
@@ -738,7 +743,6 @@ __device__ __forceinline__ bool mha_clear(uint32_t tile, uint32_t bytes) {
     st_shared_v4(tile + at, x[0], x[1], x[2], x[3]);
   }
   fence_proxy_async_smem();
-  return true;
 }
 
 // One thread per row of tile t.
@@ -765,7 +769,7 @@ __device__ __forceinline__ bool mha_softmax(const MhaFwdParams& p, MhaMisc& m, u
       for (int i = 0; i < 2; ++i) {   // the block's V: units behind those of the K before it and of the V before it
         const uint32_t n = static_cast<uint32_t>(min(j + C::kAhead, s.most) * C::kSub + 2 * j + i);
         if (!warp_wait(smem_u32(&m.full[n % C::kUnits]), n / C::kUnits & 1u, deadline, ab)) return false;
-        if (mha_clear<128>(sb + C::kQBytes + n % C::kUnits * kMhaUnit, kMhaUnit)) m.cleared = 1;
+        mha_clear<128>(sb + C::kQBytes + n % C::kUnits * kMhaUnit, kMhaUnit, &m.cleared);
       }
     }
     if (!warp_wait(smem_u32(&m.s_full[buf]), par, deadline, ab)) return false;
@@ -860,6 +864,10 @@ __device__ __forceinline__ bool mha_softmax(const MhaFwdParams& p, MhaMisc& m, u
       mha_store_sums<kCols / 32>(o + kCols * i, stage, to + kCols * i, inv, blocks > 0, live);
       bulk_wait();
     }
+  }
+  if (blocks > 0) {   // long past: the other warps' arrivals with their weights of the last block, and what they have found by then
+    const int last = blocks - 1;
+    if (!warp_wait(smem_u32(&m.p_full[NT == 1 ? last & 1 : t]), NT == 1 ? last >> 1 & 1 : last & 1, deadline, ab)) return false;
   }
   if (blocks > 0 && live && *reinterpret_cast<volatile int*>(&m.cleared)) {
     // columns where a key that the row sees is not finite, among the blocks that were looked over

@@ -25,3 +25,21 @@ def test_gradients_repeat_bit_for_bit(smla, d, h, hk):  # noqa: F811
         got = smla.dense_mha_bwd(q, k, v, 0.1, out, lse, do, cq, ck)
         assert all(torch.equal(a, b) for a, b in zip(got, want)), i
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("what", [float("nan"), float("inf")])
+def test_two_tiles_that_end_in_one_block(smla, what):  # noqa: F811
+    """All heads of a token side by side, two tokens to a CTA: both tiles look over the same last block of values,
+    and what either takes out is put back in the rows of both that see it."""
+    n, h = 900, 128
+    q, k, v, *_ = _inputs(31, [n], [n], h, 1, 128)
+    want = smla.dense_mha_fwd(q, k, v, 0.1)
+    cols = torch.zeros(128, dtype=torch.bool, device=v.device)
+    cols[3::50] = True
+    for at in (0, 127, 128, 300, 301, 640, 898, 899):
+        v2 = v.clone()
+        v2[at, :, cols] = what
+        for _ in range(5):
+            out, lse = smla.dense_mha_fwd(q, k, v2, 0.1)
+            assert torch.equal(lse, want[1]) and torch.equal(out[:at], want[0][:at])
+            assert torch.equal(out[..., ~cols], want[0][..., ~cols]) and not out[at:][..., cols].isfinite().any()
