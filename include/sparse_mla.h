@@ -479,7 +479,10 @@ size_t mla_add_norm_bwd_workspace_size(int n, int d);
  *
  * d_qk is 192 or 128 and d_v 128 (SPARSE_MLA_ERR_UNSUPPORTED_SHAPE otherwise);
  * h_kv divides h_q.  Keys and values that a query does not see have no part in
- * its row, not even where they are NaN or infinite.  Outputs share no memory
+ * its row, not even where they are NaN or infinite.  Where the keys that it sees
+ * have values that are not finite, that column of its row is the sum of those
+ * alone (an infinity, or NaN), however small their weights; where a score of it
+ * is NaN or +infinite, its row and LSE are NaN.  Outputs share no memory
  * with each other or the inputs.  Sums are taken in a fixed order: the same call
  * gives the same bits.
  */

@@ -37,6 +37,9 @@
 // token against 5001 keys is 14 us, of which the launch, the first loads and the join are
 // all but 4.
 //
+// A weight of a key that is seen counts as above 0 where its value is not finite, even where it
+// underflows: see mha_restore.
+//
 // All waits are bounded; a CTA that times out records an error, waits (bounded) for its
 // copies and MMAs in flight, frees TMEM and returns.
 #pragma once
@@ -404,20 +407,71 @@ __device__ __forceinline__ void bulk_wait() {
   asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group 0;" ::: "memory");
 }
 
+// Turns `odd` into NaN where one of 32 values is not finite (0 times it is a NaN).
+__device__ __forceinline__ void mha_odd32(const float* x, float (&odd)[2]) {
+#pragma unroll
+  for (int k = 0; k < 32; k += 2)
+    asm("{\n\t.reg .b64 px, pz, po;\n\t"
+        "mov.b64 px, {%2, %3};\n\t"
+        "mov.b64 pz, {%4, %4};\n\t"
+        "mov.b64 po, {%0, %1};\n\t"
+        "fma.rn.f32x2 po, px, pz, po;\n\t"
+        "mov.b64 {%0, %1}, po;\n\t}"
+        : "+f"(odd[0]), "+f"(odd[1])
+        : "f"(x[k]), "f"(x[k + 1]), "f"(0.f));
+}
+__device__ __forceinline__ bool mha_finite(float x) { return fabsf(x) <= 3.402823466e38f; }
+// Not 0 where one of eight bf16 values is not finite: the sign bit's place is carried into
+// where the exponent is all ones.
+__device__ __forceinline__ uint32_t odd_halves(const uint4& x) {
+  return (((x.x & 0x7fff7fffu) + 0x00800080u) | ((x.y & 0x7fff7fffu) + 0x00800080u) | ((x.z & 0x7fff7fffu) + 0x00800080u) |
+          ((x.w & 0x7fff7fffu) + 0x00800080u)) & 0x80008000u;
+}
+
+// Adds to acc, for this lane's 8 of 8 LANES columns (lane % LANES), what is not finite in rows
+// from .. end - 1 at `rows`, `step` elements apart; the rows are dealt out over the warp's
+// groups of LANES lanes.
+template <int LANES>
+__device__ __forceinline__ void mha_take_odd(const __nv_bfloat16* rows, long long step, int from, int end, float (&acc)[8]) {
+  const int lane = static_cast<int>(lane_id());
+#pragma unroll 4
+  for (int r = from + lane / LANES; r < end; r += 32 / LANES) {
+    const uint4 x = __ldg(reinterpret_cast<const uint4*>(rows + r * step) + lane % LANES);
+    if (odd_halves(x) == 0u) continue;
+    float y[8];
+    unpack8(x, y);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) acc[k] += mha_finite(y[k]) ? 0.f : y[k];
+  }
+}
+// The groups' shares of acc together.
+template <int LANES>
+__device__ __forceinline__ void mha_sum_odd(const float (&acc)[8], float (&sum)[8]) {
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    sum[k] = acc[k];
+#pragma unroll
+    for (int o = LANES; o < 32; o <<= 1) sum[k] += __shfl_xor_sync(0xffffffffu, sum[k], o);
+  }
+}
+
 // 32 N columns of this thread's TMEM lane times `f` as a bf16 row (zeros where there are no
 // sums), put together in its own part of shared memory (`stage`) and copied from there:
 // stored by the threads themselves, 32 rows' pieces of 16 bytes at a time, a tile's rows
 // take about 2 us of the CTA's time.  Rows of the stage are 64 N + 16 bytes apart:
-// neighbours are in other banks.  `sums` is the same for a whole warp.
-template <int N>
-__device__ __forceinline__ void mha_store_sums(__nv_bfloat16* row, uint32_t stage, uint32_t taddr, float f, bool sums,
+// neighbours are in other banks.  `sums` is the same for a whole warp.  Whether a value is not
+// finite, where ODD asks for it.
+template <int N, bool ODD = false>
+__device__ __forceinline__ bool mha_store_sums(__nv_bfloat16* row, uint32_t stage, uint32_t taddr, float f, bool sums,
                                                bool live) {
+  float odd[2] = {0.f, 0.f};
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     float x[32];
     if (sums) tmem_load32(taddr + 32 * i, x);
 #pragma unroll
     for (int k = 0; k < 32; ++k) x[k] = sums ? x[k] * f : 0.f;
+    if (ODD) mha_odd32(x, odd);
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const uint4 v = pack8(x + 8 * k);
@@ -426,6 +480,7 @@ __device__ __forceinline__ void mha_store_sums(__nv_bfloat16* row, uint32_t stag
   }
   fence_proxy_async_smem();
   if (live) bulk_store(row, stage, 64 * N);
+  return odd[0] + odd[1] != 0.f;
 }
 template <int N>
 __device__ constexpr uint32_t mha_stage_row() {
@@ -745,6 +800,37 @@ __device__ __forceinline__ void mha_clear(uint32_t tile, uint32_t bytes, int* fo
   fence_proxy_async_smem();
 }
 
+// A weight is above 0, however small: a value that is not finite makes its column of each row
+// that sees its key infinite, and two of them that do not agree, or a NaN, make it NaN.  The
+// products have this otherwise where the weight underflows (0 times an infinity), where a sum
+// of weights relative to an older maximum does, and where the value was taken out.  So the
+// columns of the rows of `asked` become the sums of what is not finite among keys first .. end - 1
+// (a lane's end is its row's; it does not fall from lane to lane).  One warp, a row per lane;
+// `part`, where it is given, takes the sums in place of `out`.
+__device__ __forceinline__ void mha_restore(uint32_t asked, const __nv_bfloat16* values, long long step, int first, int end,
+                                         __nv_bfloat16* out, float* part) {
+  const int col = static_cast<int>(lane_id()) % 16 * 8;
+  float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  __syncwarp();   // the rows' own threads have written them
+  for (; asked != 0u; asked &= asked - 1) {
+    const int row = __ffs(asked) - 1, upto = __shfl_sync(0xffffffffu, end, row);
+    __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(out), row));
+    float* q = reinterpret_cast<float*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(part), row));
+    mha_take_odd<16>(values, step, first, upto, acc);
+    first = max(first, upto);
+    float sum[8];
+    mha_sum_odd<16>(acc, sum);
+    if (lane_id() < 16) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        if (sum[k] == 0.f) continue;
+        if (q != nullptr) q[col + k] = sum[k];
+        else o[col + k] = __float2bfloat16_rn(sum[k]);
+      }
+    }
+  }
+}
+
 // One thread per row of tile t.
 template <int DQK, int NT>
 __device__ __forceinline__ bool mha_softmax(const MhaFwdParams& p, MhaMisc& m, uint8_t* sbase, uint32_t sb, uint32_t tmem,
@@ -843,17 +929,23 @@ __device__ __forceinline__ bool mha_softmax(const MhaFwdParams& p, MhaMisc& m, u
   if (live && !join) p.lse[at] = sum == 0.f ? -INFINITY : (top * c + log2f(sum)) * 0.6931471805599453f;
   // the products and loads are done: the ring's memory holds the rows that are joined
   float* part = reinterpret_cast<float*>(sbase + C::kQBytes) + row * kMhaPartRow;
+  bool odd = false;   // a sum is not finite
   if (join) {
     m.part[row] = make_float2(sum == 0.f ? -INFINITY : top * c, sum);
+    float odds[2] = {0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < kMhaDv / 32; ++i) {
       float x[32];
-      if (blocks > 0) tmem_load32(to + 32 * i, x);
+      if (blocks > 0) {
+        tmem_load32(to + 32 * i, x);
+        mha_odd32(x, odds);
+      }
 #pragma unroll
       for (int k = 0; k < 32; k += 4)
         *reinterpret_cast<float4*>(part + 32 * i + k) =
             sum == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(x[k], x[k + 1], x[k + 2], x[k + 3]);
     }
+    odd = odds[0] + odds[1] != 0.f;
   } else {
     // the tile's Q is not needed any more: its memory is the stage, at 128 columns for half a row at a time
     constexpr int kPieces = C::kSub * kMhaUnit >= kMhaTile * mha_stage_row<4>() ? 1 : 2, kCols = kMhaDv / kPieces;
@@ -861,32 +953,18 @@ __device__ __forceinline__ bool mha_softmax(const MhaFwdParams& p, MhaMisc& m, u
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
-      mha_store_sums<kCols / 32>(o + kCols * i, stage, to + kCols * i, inv, blocks > 0, live);
+      odd |= mha_store_sums<kCols / 32, true>(o + kCols * i, stage, to + kCols * i, inv, blocks > 0, live);
       bulk_wait();
     }
   }
   if (blocks > 0) {   // long past: the other warps' arrivals with their weights of the last block, and what they have found by then
     const int last = blocks - 1;
     if (!warp_wait(smem_u32(&m.p_full[NT == 1 ? last & 1 : t]), NT == 1 ? last >> 1 & 1 : last & 1, deadline, ab)) return false;
-  }
-  if (blocks > 0 && live && *reinterpret_cast<volatile int*>(&m.cleared)) {
-    // columns where a key that the row sees is not finite, among the blocks that were looked over
-    const int first = max(max(0, s.t0[0] + lk - lq + 1) / kMhaTile, s.from) * kMhaTile;
-    const int end = min(tok + lk - lq + 1, (s.from + blocks) * kMhaTile);
-    const __nv_bfloat16* values = p.v + w.k0 * p.v_tok + pack0 / p.group * p.v_head;
-#pragma unroll 1
-    for (int d = 0; d < kMhaDv; ++d) {
-      float acc = 0.f;
-#pragma unroll 1
-      for (int key = first; key < end; ++key) {
-        const float y = __bfloat162float(values[key * p.v_tok + d]);
-        if (!(fabsf(y) <= 3.402823466e38f)) acc += y;
-      }
-      if (acc != 0.f) {
-        if (join) part[d] = acc;
-        else o[d] = __float2bfloat16_rn(acc);
-      }
-    }
+    const bool ask = live && sum > 0.f && mha_finite(sum) && (odd || *reinterpret_cast<volatile int*>(&m.cleared));
+    const uint32_t rows = __ballot_sync(0xffffffffu, ask);
+    if (rows != 0u)
+      mha_restore(rows, p.v + w.k0 * p.v_tok + pack0 / p.group * p.v_head, p.v_tok, s.from * kMhaTile,
+                  min(tok + lk - lq + 1, (s.from + blocks) * kMhaTile), o, join ? part : nullptr);
   }
   return true;
 }
@@ -917,13 +995,16 @@ __device__ __forceinline__ void mha_join(const MhaFwdParams& p, MhaMisc& m, uint
       for (int k = 0; k < W / 4; ++k) x[k] = ld_cluster_f4(from + 16 * k);
       const float f = own_sum == 0.f ? 0.f : fast_exp2(own - top);   // a sum that is NaN passes it on
       sum += f * own_sum;
-      if (f == 0.f) continue;
+      // a part whose weight is 0: what is not finite counts even so
+      const bool none = f == 0.f;
+      const float g = none ? 1.f : f;
+      auto add = [&](float& to, float y) { to += g * (none && mha_finite(y) ? 0.f : y); };
 #pragma unroll
       for (int k = 0; k < W / 4; ++k) {
-        acc[4 * k] += f * x[k].x;
-        acc[4 * k + 1] += f * x[k].y;
-        acc[4 * k + 2] += f * x[k].z;
-        acc[4 * k + 3] += f * x[k].w;
+        add(acc[4 * k], x[k].x);
+        add(acc[4 * k + 1], x[k].y);
+        add(acc[4 * k + 2], x[k].z);
+        add(acc[4 * k + 3], x[k].w);
       }
     }
     const float inv = sum == 0.f ? 0.f : 1.f / sum;

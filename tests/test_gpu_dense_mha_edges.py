@@ -43,3 +43,51 @@ def test_two_tiles_that_end_in_one_block(smla, what):  # noqa: F811
             out, lse = smla.dense_mha_fwd(q, k, v2, 0.1)
             assert torch.equal(lse, want[1]) and torch.equal(out[:at], want[0][:at])
             assert torch.equal(out[..., ~cols], want[0][..., ~cols]) and not out[at:][..., cols].isfinite().any()
+
+
+NAN, INF = float("nan"), float("inf")
+
+
+def _odd_sums(x):
+    """The sums of what is not finite in rows 0 .. i of x (0: there is none), for each i."""
+    some = lambda mask: mask.cumsum(0) > 0  # noqa: E731
+    up, down, bad = some(x == INF), some(x == -INF), some(x.isnan())
+    s = torch.zeros(x.shape, device=x.device)
+    s[up], s[down] = INF, -INF
+    s[bad | (up & down)] = NAN
+    return s
+
+
+@pytest.mark.parametrize("scores", ["far apart", "rising"])
+@pytest.mark.parametrize("lq,lk,h,hk,d", [(300, 300, 2, 2, 192), (1, 5000, 8, 8, 192), (130, 4500, 2, 1, 128),
+                                          (1050, 1100, 64, 64, 128), (900, 900, 128, 1, 192), (70, 40, 3, 1, 128)])
+def test_a_seen_value_that_is_not_finite_counts_however_small_its_weight(smla, lq, lk, h, hk, d, scores):  # noqa: F811
+    """Weights that underflow, in whole blocks, in blocks that some rows do not see all of, in parts of a cluster,
+    and behind a maximum that has grown: a column is the sum of what is not finite in it."""
+    q, k, v, *_ = _inputs(32, [lq], [lk], h, hk, d)
+    q[..., 0], k[..., 0] = 8.0, 0.0
+    a, b = 3, lk - 2
+    if scores == "rising":
+        k[..., 0] = (torch.arange(lk, device=k.device) * 0.5).bfloat16()[:, None]
+    else:
+        k[a, :, 0] = k[b, :, 0] = -400.0
+    want = smla.dense_mha_fwd(q, k, v, 0.5)
+    v2 = v.clone()
+    v2[a, :, 7], v2[a, :, 9], v2[a, :, 11], v2[b, :, 11], v2[b, :, 13], v2[lk // 2, 0, 40:50] = INF, -INF, INF, -INF, NAN, INF
+    out, lse = smla.dense_mha_fwd(q, k, v2, 0.5)
+    assert torch.equal(lse, want[1])
+    first = max(0, lq - lk)   # rows before it see nothing
+    assert torch.equal(out[:first], want[0][:first])
+    odd = _odd_sums(v2)[lk - lq + first:].repeat_interleave(h // hk, 1).float()
+    ref = torch.where(odd == 0, want[0][first:].float(), odd)
+    assert torch.equal(torch.nan_to_num(out[first:].float(), nan=12345.0), torch.nan_to_num(ref, nan=12345.0))
+
+
+def test_a_row_whose_scores_are_not_finite_is_nan(smla):  # noqa: F811
+    """Its weights are NaN: an infinity among its values changes nothing."""
+    q, k, v, *_ = _inputs(33, [300], [300], 2, 2, 128)
+    k[150, 0, 5] = NAN
+    v[140, 0, 3], v[160, 0, 4] = INF, INF
+    out, lse = smla.dense_mha_fwd(q, k, v, 0.1)
+    assert out[150:, 0].isnan().all() and lse[150:, 0].isnan().all() and lse[:150].isfinite().all()
+    assert (out[140:150, 0, 3] == INF).all() and out[:140].isfinite().all() and out[:, 1].isfinite().all()
