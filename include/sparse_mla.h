@@ -728,7 +728,8 @@ sparse_mla_status_t sparse_mla_clear_device_error(void);
  * the call (process-wide; default 1 s; 0 restores the default).  Each CTA
  * restarts the clock at every unit of work it takes up (one token's head
  * group, or a CTA's share of one), so the bound applies per unit, not to the
- * whole launch.
+ * whole launch; those of dense_mha_fwd and dense_mha_bwd, whose units are as long
+ * as their sequences, at every block of a unit.
  */
 void sparse_mla_set_wait_timeout_ns(unsigned long long ns);
 

@@ -37,7 +37,8 @@
 // with all that a tile costs once (8000 cycles to the first scores, 5500 for the sums' way
 // out); dq 617 us.  At 128 columns K stays in TMEM as A of S^T and a block is 1152 cycles.
 //
-// All waits are bounded, as in the forward.
+// Every wait is bounded, as in the forward.  dk's and dv's kernel waits for dq's grid, which has
+// a bound of its own, outside of these waits: no warp has one for D under way before.
 #pragma once
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -125,7 +126,7 @@ __device__ __forceinline__ bool mha_dq_load(const MhaBwdParams& p, MhaDqMisc& m,
                                             int blocks, int pack0, int& k_fills, int& v_fills) {
   using C = MhaDqShape<DQK>;
   const volatile int* ab = &m.abort_flag;
-  const uint64_t deadline = global_timer_ns() + p.timeout_ns;
+  uint64_t deadline = global_timer_ns() + p.timeout_ns;
   const int kvh = pack0 / p.group;
   uint32_t bar = smem_u32(&m.q_full);
   mbar_arrive_expect_tx(bar, C::kSub * static_cast<uint32_t>(p.pack * p.tok_tile) * 128u);
@@ -139,6 +140,7 @@ __device__ __forceinline__ bool mha_dq_load(const MhaBwdParams& p, MhaDqMisc& m,
     tma_load_3d(sb + C::kOOff + c * kMhaUnit, &p.map_o, 64 * c, pack0, w.q0 + t0, bar);
   }
   for (int j = 0; j < blocks; ++j) {
+    deadline = global_timer_ns() + p.timeout_ns;
     if (j == 1 && !mbar_wait(smem_u32(&m.do_ready), 0, deadline, ab)) return false;
     const int ks = j % C::kKStages, vs = j % C::kVStages, row = w.k0 + j * C::kN;
     if (!mbar_wait(smem_u32(&m.k_empty[ks]), (j / C::kKStages & 1) ^ 1, deadline, ab)) return false;
@@ -166,9 +168,10 @@ __device__ __forceinline__ bool mha_dq_scores(const MhaBwdParams& p, MhaDqMisc& 
                  v_desc = smem_desc(sb + C::kVOff, 16, 1024, SWZ_128B);
   const uint32_t chosen = elect_one();
   const volatile int* ab = &m.abort_flag;
-  const uint64_t deadline = global_timer_ns() + p.timeout_ns;
+  uint64_t deadline = global_timer_ns() + p.timeout_ns;
   if (!warp_wait(smem_u32(&m.q_full), 0, deadline, ab)) return false;
   for (int j = 0; j < blocks; ++j) {
+    deadline = global_timer_ns() + p.timeout_ns;
     const int ks = j % C::kKStages, vs = j % C::kVStages;
     if (!warp_wait(smem_u32(&m.k_full[ks]), j / C::kKStages & 1, deadline, ab)) return false;
     if (j > 0 && !warp_wait(smem_u32(&m.s_free), (j - 1) & 1, deadline, ab)) return false;
@@ -199,8 +202,9 @@ __device__ __forceinline__ bool mha_dq_sums(const MhaBwdParams& p, MhaDqMisc& m,
   const uint64_t k_desc = smem_desc(sb + C::kKOff, C::kKUnit, 1024, SWZ_128B);   // its rows as columns
   const uint32_t chosen = elect_one();
   const volatile int* ab = &m.abort_flag;
-  const uint64_t deadline = global_timer_ns() + p.timeout_ns;
+  uint64_t deadline = global_timer_ns() + p.timeout_ns;
   for (int j = 0; j < blocks; ++j) {
+    deadline = global_timer_ns() + p.timeout_ns;
     const int ks = j % C::kKStages;
     const uint64_t k = desc_plus(k_desc, ks * C::kKBytes);
     if (!warp_wait(smem_u32(&m.ds_full), j & 1, deadline, ab)) return false;
@@ -220,7 +224,7 @@ __device__ __forceinline__ bool mha_dq_rows(const MhaBwdParams& p, MhaDqMisc& m,
                                             const MhaWork& w, int t0, int blocks, int pack0) {
   using C = MhaDqShape<DQK>;
   const volatile int* ab = &m.abort_flag;
-  const uint64_t deadline = global_timer_ns() + p.timeout_ns;
+  uint64_t deadline = global_timer_ns() + p.timeout_ns;
   const int row = static_cast<int>(threadIdx.x) & 127, half = static_cast<int>(threadIdx.x) >> 7;
   const int lq = w.q1 - w.q0, lk = w.k1 - w.k0;
   const int tok = t0 + row / p.pack, head = pack0 + row % p.pack;
@@ -262,6 +266,7 @@ __device__ __forceinline__ bool mha_dq_rows(const MhaBwdParams& p, MhaDqMisc& m,
   const uint32_t ts = lane0 + C::kS + kHalf * half, tt = lane0 + C::kT + kHalf * half,
                  td = lane0 + C::kDs + kHalf / 2 * half;
   for (int j = 0; j < blocks; ++j) {
+    deadline = global_timer_ns() + p.timeout_ns;
     if (!warp_wait(smem_u32(&m.s_full), j & 1, deadline, ab)) return false;
     tc_fence_after();
     float s[kHalf], x[kHalf];
@@ -408,6 +413,9 @@ __global__ void __launch_bounds__(MhaDqShape<DQK>::kThreads, 1) dense_mha_dq_ker
 
 // ------------------------------------------------------------------ dk, dv
 
+// Until the grid before (dq's) has ended, and all that it has written is there.
+__device__ __forceinline__ void mha_other_grid() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 struct __align__(16) MhaDkvMisc {
   uint64_t k_full, k_ready, q_full[4], do_full[4], empty[4];
   uint64_t s_full, s_free, p_full, p_free, t_full, t_free, ds_full, out_full, drain[2];
@@ -457,7 +465,7 @@ __device__ __forceinline__ bool mha_dkv_load(const MhaBwdParams& p, MhaDkvMisc& 
                                              const MhaQueries& s, int kvh, int& fills) {
   using C = MhaDkvShape<DQK>;
   const volatile int* ab = &m.abort_flag;
-  const uint64_t deadline = global_timer_ns() + p.timeout_ns;
+  uint64_t deadline = global_timer_ns() + p.timeout_ns;
   const uint32_t kb = smem_u32(&m.k_full);
   mbar_arrive_expect_tx(kb, (C::kKTmem ? 2 : C::kSub + 2) * kMhaUnit);
   for (int c = 0; c < C::kSub && !C::kKTmem; ++c)
@@ -466,6 +474,11 @@ __device__ __forceinline__ bool mha_dkv_load(const MhaBwdParams& p, MhaDkvMisc& 
   const uint32_t bytes = static_cast<uint32_t>(p.pack * p.tok_tile) * 128u;
   int head = kvh * p.group, b = 0, st = 0, turn = 0;
   for (int j = 0; j < s.total; ++j) {
+    deadline = global_timer_ns() + p.timeout_ns;
+    if (j == C::kStages) {   // the first stages' copies wait for nothing
+      mha_other_grid();
+      deadline = global_timer_ns() + p.timeout_ns;
+    }
     const int tok = w.q0 + s.first + b * p.tok_tile;
     if (!mbar_wait(smem_u32(&m.empty[st]), turn ^ 1, deadline, ab)) return false;
     uint32_t bar = smem_u32(&m.q_full[st]);
@@ -498,11 +511,13 @@ __device__ __forceinline__ bool mha_dkv_scores(const MhaBwdParams& p, MhaDkvMisc
                  q_desc = smem_desc(sb + C::kQOff, 16, 1024, SWZ_128B), g_desc = smem_desc(sb + C::kDoOff, 16, 1024, SWZ_128B);
   const uint32_t chosen = elect_one();
   const volatile int* ab = &m.abort_flag;
-  const uint64_t deadline = global_timer_ns() + p.timeout_ns;
+  uint64_t deadline = global_timer_ns() + p.timeout_ns;
   if (!warp_wait(smem_u32(&m.k_full), 0, deadline, ab)) return false;
   if (C::kKTmem && !warp_wait(smem_u32(&m.k_ready), 0, deadline, ab)) return false;
+  mha_other_grid();
   int st = 0, turn = 0;
   for (int j = 0; j < total; ++j) {
+    deadline = global_timer_ns() + p.timeout_ns;
     const uint64_t q = desc_plus(q_desc, st * C::kQBytes), g = desc_plus(g_desc, st * C::kDoBytes);
     if (!warp_wait(smem_u32(&m.q_full[st]), turn, deadline, ab)) return false;
     if (j > 0 && !warp_wait(smem_u32(&m.s_free), (j - 1) & 1, deadline, ab)) return false;
@@ -539,11 +554,13 @@ __device__ __forceinline__ bool mha_dkv_sums(const MhaBwdParams& p, MhaDkvMisc& 
   constexpr uint32_t kIdescK = idesc_bf16_f32(kMhaTile, DQK, false, true);
   const uint64_t q_desc = smem_desc(sb + C::kQOff, C::kQUnit, 1024, SWZ_128B),    // their rows as columns
                  g_desc = smem_desc(sb + C::kDoOff, C::kQUnit, 1024, SWZ_128B);
+  mha_other_grid();
   const uint32_t chosen = elect_one();
   const volatile int* ab = &m.abort_flag;
-  const uint64_t deadline = global_timer_ns() + p.timeout_ns;
+  uint64_t deadline = global_timer_ns() + p.timeout_ns;
   int st = 0, turn = 0;
   for (int j = 0; j < total; ++j) {
+    deadline = global_timer_ns() + p.timeout_ns;
     const uint64_t q = desc_plus(q_desc, st * C::kQBytes), g = desc_plus(g_desc, st * C::kDoBytes);
     if (!warp_wait(smem_u32(&m.p_full), j & 1, deadline, ab)) return false;
     if (!warp_wait(smem_u32(&m.do_full[st]), turn, deadline, ab)) return false;
@@ -576,10 +593,11 @@ __device__ __forceinline__ bool mha_dkv_stats(const MhaBwdParams& p, MhaDkvMisc&
                                               int kvh) {
   using C = MhaDkvShape<DQK>;
   const volatile int* ab = &m.abort_flag;
-  const uint64_t deadline = global_timer_ns() + p.timeout_ns;
+  uint64_t deadline = global_timer_ns() + p.timeout_ns;
   const int lane = static_cast<int>(lane_id()), lq = w.q1 - w.q0;
   int head = kvh * p.group, b = 0, st = 0, turn = 0;
   for (int j = 0; j < s.total; ++j) {
+    deadline = global_timer_ns() + p.timeout_ns;
     float l[C::kN / 32], d[C::kN / 32];
 #pragma unroll
     for (int i = 0; i < C::kN / 32; ++i) {
@@ -619,7 +637,7 @@ __device__ __forceinline__ bool mha_dkv_rows(const MhaBwdParams& p, MhaDkvMisc& 
   using C = MhaDkvShape<DQK>;
   constexpr int kHalf = C::kN / 2;
   const volatile int* ab = &m.abort_flag;
-  const uint64_t deadline = global_timer_ns() + p.timeout_ns;
+  uint64_t deadline = global_timer_ns() + p.timeout_ns;
   const int row = static_cast<int>(threadIdx.x) & 127, half = static_cast<int>(threadIdx.x) >> 7;
   const int lq = w.q1 - w.q0, lk = w.k1 - w.k0;
   const int key = w.tile * kMhaTile + row;
@@ -636,11 +654,13 @@ __device__ __forceinline__ bool mha_dkv_rows(const MhaBwdParams& p, MhaDkvMisc& 
     __syncwarp();
     if (lane_id() == 0) mbar_arrive(smem_u32(&m.k_ready));
   }
+  if (s.total > 0) mha_other_grid();
   const int last_key = min((w.tile + 1) * kMhaTile, lk) - 1;
   const uint32_t ts = lane0 + C::kS + kHalf * half, tt = lane0 + C::kT + kHalf * half,
                  tp = lane0 + C::kP + kHalf / 2 * half, td = lane0 + C::kDs + kHalf / 2 * half;
   int b = 0, st = 0, turn = 0, before = 0, turn_before = 0;   // where the block is, and the one before
   for (int j = 0; j < s.total; ++j) {
+    deadline = global_timer_ns() + p.timeout_ns;
     const int t0 = s.first + b * p.tok_tile;
     if (++b == s.blocks) b = 0;
     const bool edge = t0 + lk - lq < last_key || t0 + p.tok_tile > lq;   // some rows do not see all of the keys
@@ -795,7 +815,7 @@ __global__ void __launch_bounds__(MhaDkvShape<DQK>::kThreads, 1) dense_mha_dkv_k
     mha_fill_rows(p.dv, static_cast<long long>(p.h_kv) * (kMhaDv / 2), w.end, p.total_kv, 0u);
   }
   // D is there, and dq too when this grid ends
-  if (warp == 10) asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (warp == 10) mha_other_grid();
   if (m.prior_error == 0 && w.k1 > w.k0) {
     const MhaQueries s(p, w);
     const int never = 0;
@@ -813,6 +833,7 @@ __global__ void __launch_bounds__(MhaDkvShape<DQK>::kThreads, 1) dense_mha_dkv_k
       } else if (lane_id() == 0) {
         int fills = 0;
         if (!mha_dkv_load<DQK>(p, m, sb, w, s, kvh, fills)) mha_bwd_raise(m, kErrMhaDkvLoadWait);
+        mha_other_grid();   // q_full takes the statistics' arrivals too
         // every copy issued has landed before the CTA exits
         const uint64_t dl = global_timer_ns() + 100000000ull;
         mbar_wait(smem_u32(&m.k_full), 0, dl, &never);

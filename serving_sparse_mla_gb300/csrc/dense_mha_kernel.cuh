@@ -40,7 +40,7 @@
 // A weight of a key that is seen counts as above 0 where its value is not finite, even where it
 // underflows: see mha_restore.
 //
-// All waits are bounded; a CTA that times out records an error, waits (bounded) for its
+// Every wait is bounded; a CTA in which one runs out records an error, waits (bounded) for its
 // copies and MMAs in flight, frees TMEM and returns.
 #pragma once
 #include <cuda.h>
@@ -224,6 +224,10 @@ __device__ __forceinline__ uint32_t elect_one() {
   return chosen;
 }
 
+// A role's waits end at a deadline.  How long a tile takes has no bound, so the deadline is set
+// anew with every block: what is bounded is a stay without progress, not the tile.  (Set by each
+// wait in its own loop it took 4 % of packed prompts' time; so 0.3 %.)
+//
 // mbar_wait by all threads of a warp, with the same result for all.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint64_t deadline_ns,
                                           const volatile int* abort_flag) {
@@ -232,8 +236,7 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint64_
   }
   return true;
 }
-
-// warp_wait for two barriers, of which the first has most likely been passed: their tries are under way together.
+// For two barriers, of which the first has most likely been passed: their tries are under way together.
 __device__ __forceinline__ bool warp_wait_both(uint32_t bar, uint32_t parity, uint32_t bar2, uint32_t parity2,
                                                uint64_t deadline_ns, const volatile int* abort_flag) {
   for (;;) {
@@ -627,7 +630,7 @@ __device__ __forceinline__ bool mha_load(const MhaFwdParams& p, MhaMisc& m, uint
                                          const MhaSpan<NT>& s, int pack0, int kvh, uint32_t& fills) {
   using C = MhaFwdShape<DQK, NT>;
   const volatile int* ab = &m.abort_flag;
-  const uint64_t deadline = global_timer_ns() + p.timeout_ns;
+  uint64_t deadline = global_timer_ns() + p.timeout_ns;
   auto load_q = [&](int t) {
     const uint32_t bar = smem_u32(&m.q_full[t]);
     const uint32_t bytes = static_cast<uint32_t>(p.pack * p.tok_tile) * 128u;
@@ -640,6 +643,7 @@ __device__ __forceinline__ bool mha_load(const MhaFwdParams& p, MhaMisc& m, uint
   MhaOrder now, old;       // the block that is loaded, the one whose units come free next
   int old_left = 0;        // units of `old` that are free and not yet filled
   for (int n = 0; n < 2 * s.most; ++n) {
+    deadline = global_timer_ns() + p.timeout_ns;
     for (int c = 0; c < (now.value ? 2 : C::kSub); ++c) {
       if (fills >= static_cast<uint32_t>(C::kUnits)) {
         if (old_left == 0) {
@@ -675,7 +679,7 @@ __device__ __forceinline__ bool mha_mma(const MhaFwdParams& p, MhaMisc& m, uint3
   constexpr uint32_t kIdescS = idesc_bf16_f32(kMhaTile, kMhaTile, false, false);
   constexpr uint32_t kIdescO = idesc_bf16_f32(kMhaTile, kMhaDv, false, true);
   const volatile int* ab = &m.abort_flag;
-  const uint64_t deadline = global_timer_ns() + p.timeout_ns;
+  uint64_t deadline = global_timer_ns() + p.timeout_ns;
   const uint32_t chosen = elect_one();
   auto commit = [&](uint64_t* bar) { commit_to(chosen, bar); };
   const uint64_t q_desc = smem_desc(sb, 16, 1024, SWZ_128B), k_desc = smem_desc(sb + C::kQBytes, 16, 1024, SWZ_128B),
@@ -725,6 +729,7 @@ __device__ __forceinline__ bool mha_mma(const MhaFwdParams& p, MhaMisc& m, uint3
       r.skip(C::kSub);
     }
     for (int j = 0; j < s.most; ++j) {
+      deadline = global_timer_ns() + p.timeout_ns;
       const int buf = j & 1;
       if (!warp_wait(smem_u32(&m.p_full[buf]), j >> 1 & 1, deadline, ab)) return false;
       tc_fence_after();
@@ -746,6 +751,7 @@ __device__ __forceinline__ bool mha_mma(const MhaFwdParams& p, MhaMisc& m, uint3
     }
     r.skip(C::kSub);
     for (int j = 0; j < s.most; ++j) {
+      deadline = global_timer_ns() + p.timeout_ns;
       MhaRing<C::kUnits> rk = r;                 // block j's V, then block j + 1's K
       rk.skip(2);
 #pragma unroll
@@ -837,7 +843,7 @@ __device__ __forceinline__ bool mha_softmax(const MhaFwdParams& p, MhaMisc& m, u
                                             const MhaWork& w, const MhaSpan<NT>& s, int pack0, int t) {
   using C = MhaFwdShape<DQK, NT>;
   const volatile int* ab = &m.abort_flag;
-  const uint64_t deadline = global_timer_ns() + p.timeout_ns;
+  uint64_t deadline = global_timer_ns() + p.timeout_ns;
   const int row = static_cast<int>(threadIdx.x) & 127;
   const int lq = w.q1 - w.q0, lk = w.k1 - w.k0;
   const int tok = s.t0[t] + row / p.pack;
@@ -849,6 +855,7 @@ __device__ __forceinline__ bool mha_softmax(const MhaFwdParams& p, MhaMisc& m, u
   const float c = p.scale_log2;
   float top = -INFINITY, sum = 0.f;   // the maximum that the weights are relative to, their sum
   for (int j = 0; j < blocks; ++j) {
+    deadline = global_timer_ns() + p.timeout_ns;
     const int buf = NT == 1 ? j & 1 : t, par = NT == 1 ? j >> 1 & 1 : j & 1;   // the S that the block's scores are in
     const uint32_t ts = tmem + quarter + buf * kMhaTile;
     if (j >= whole) {

@@ -91,3 +91,49 @@ def test_a_row_whose_scores_are_not_finite_is_nan(smla):  # noqa: F811
     out, lse = smla.dense_mha_fwd(q, k, v, 0.1)
     assert out[150:, 0].isnan().all() and lse[150:, 0].isnan().all() and lse[:150].isfinite().all()
     assert (out[140:150, 0, 3] == INF).all() and out[:140].isfinite().all() and out[:, 1].isfinite().all()
+
+
+def test_waits_that_run_out_are_reported_and_the_next_call_is_right(smla):  # noqa: F811
+    """A 1 ns bound on a wait: the loading threads, whose waits for the stages before them are the longest, give up at
+    once, and the other warps by the CTA's flag; the kernels record a code, wait for their copies and products, free
+    TMEM and return."""
+    for lq, lk, h, hk, d in (([1100, 2], [1100, 900], 64, 64, 128), ([4100], [4100], 16, 4, 192)):
+        q, k, v, do, cq, ck = _inputs(34, lq, lk, h, hk, d)
+        want = smla.dense_mha_fwd(q, k, v, 0.1, cq, ck)
+        grads = smla.dense_mha_bwd(q, k, v, 0.1, *want, do, cq, ck)
+        torch.cuda.synchronize()
+        codes = []
+        for call in (lambda: smla.dense_mha_fwd(q, k, v, 0.1, cq, ck),
+                     lambda: smla.dense_mha_bwd(q, k, v, 0.1, *want, do, cq, ck)):
+            try:
+                smla.set_wait_timeout_ns(1)
+                call()
+                torch.cuda.synchronize()
+                codes.append(smla.get_device_error())
+            finally:
+                smla.set_wait_timeout_ns(0)
+                smla.clear_device_error()
+        assert 0x701 <= codes[0] <= 0x703 and 0x711 <= codes[1] <= 0x724, codes
+        assert smla.get_device_error() == 0
+        assert all(torch.equal(a, b) for a, b in zip(smla.dense_mha_fwd(q, k, v, 0.1, cq, ck), want))
+        assert all(torch.equal(a, b) for a, b in zip(smla.dense_mha_bwd(q, k, v, 0.1, *want, do, cq, ck), grads))
+
+
+@pytest.mark.parametrize("d", [192, 128])
+def test_the_bound_is_a_waits_not_a_tiles(smla, d):  # noqa: F811
+    """Tiles of 1 to 2 ms under a bound of 0.5: each has hundreds of waits of some microseconds."""
+    n = 131072
+    q, k, v, do, *_ = _inputs(35, [n], [n], 1, 1, d)
+    want = smla.dense_mha_fwd(q, k, v, 0.1)
+    grads = smla.dense_mha_bwd(q, k, v, 0.1, *want, do)
+    torch.cuda.synchronize()
+    try:
+        smla.set_wait_timeout_ns(500000)
+        got = smla.dense_mha_fwd(q, k, v, 0.1)
+        got += smla.dense_mha_bwd(q, k, v, 0.1, *want, do)
+        torch.cuda.synchronize()
+        code = smla.get_device_error()
+    finally:
+        smla.set_wait_timeout_ns(0)
+        smla.clear_device_error()
+    assert code == 0 and all(torch.equal(a, b) for a, b in zip(got, want + grads))
