@@ -3,6 +3,9 @@
 //   P = exp(scale q k^T - lse),  D = rowsum(dout out),  dS = P (dout V^T - D),
 //   dq = scale dS K,   dk = scale dS^T q,   dv = P^T dout
 //
+// A row that sees one key has P = 1 and out = v, so its dS is 0: T is taken for D there, where
+// two sums of the same products, added up in different orders, would leave their rounding.
+//
 // dk and dv are sums over the queries, dq over the keys: two kernels, each with its own
 // accumulators in TMEM and in a fixed order, at the price of forming S and dout V^T
 // twice (512 + 640 products a pair at 192 columns where one pass would have 832, but
@@ -262,6 +265,7 @@ __device__ __forceinline__ bool mha_dq_rows(const MhaBwdParams& p, MhaDqMisc& m,
     if (live && half == 0) p.delta[at] = delta;
   }
   constexpr int kHalf = C::kN / 2;
+  const bool one = tok + lk == lq;   // the row sees one key: out is its value, and T is D
   const int whole = max(0, t0 + lk - lq + 1) / C::kN;
   const uint32_t ts = lane0 + C::kS + kHalf * half, tt = lane0 + C::kT + kHalf * half,
                  td = lane0 + C::kDs + kHalf / 2 * half;
@@ -293,6 +297,7 @@ __device__ __forceinline__ bool mha_dq_rows(const MhaBwdParams& p, MhaDqMisc& m,
     tc_fence_before();
     __syncwarp();
     if (lane_id() == 0) mbar_arrive(smem_u32(&m.t_free));
+    x[0] = one ? delta : x[0];
 #pragma unroll
     for (int i = 0; i < kHalf; i += 2) weigh2(s[i], s[i + 1], x[i], x[i + 1], -delta, -delta);
     if (edge) {
@@ -711,6 +716,11 @@ __device__ __forceinline__ bool mha_dkv_rows(const MhaBwdParams& p, MhaDkvMisc& 
     __syncwarp();
     if (lane_id() == 0) mbar_arrive(smem_u32(&m.t_free));
     const float4* d4 = reinterpret_cast<const float4*>(&m.minus_d[st][kHalf * half]);
+    if (t0 == lq - lk && row < 32) {   // the block's first token sees the first key alone, and T is D
+      const int ones = key == 0 ? p.pack - kHalf * half : 0;
+#pragma unroll
+      for (int i = 0; i < kHalf; ++i) y[i] = i < ones ? -m.minus_d[st][kHalf * half + i] : y[i];
+    }
 #pragma unroll
     for (int i = 0; i < kHalf; i += 4) {
       const float4 d = d4[i >> 2];

@@ -137,3 +137,28 @@ def test_the_bound_is_a_waits_not_a_tiles(smla, d):  # noqa: F811
         smla.set_wait_timeout_ns(0)
         smla.clear_device_error()
     assert code == 0 and all(torch.equal(a, b) for a, b in zip(got, want + grads))
+
+
+@pytest.mark.parametrize("d", [192, 128])
+@pytest.mark.parametrize("h,hk", [(2, 2), (64, 1), (128, 1), (48, 1), (5, 1), (6, 2)])
+def test_rows_that_see_one_key_have_no_gradient_of_scores(smla, h, hk, d):  # noqa: F811
+    """P is 1 and out is v there, so dS = dout v - dout out is 0, and with it dq and the row's part of dk."""
+    # sequences of one token, of one key, of one query
+    q, k, v, do, cq, ck = _inputs(36, [1, 1, 300, 1, 1, 0], [1, 1, 1, 1, 0, 3], h, hk, d)
+    out, lse = smla.dense_mha_fwd(q, k, v, 0.1, cq, ck)
+    dq, dk, dv = smla.dense_mha_bwd(q, k, v, 0.1, out, lse, do, cq, ck)
+    assert (dq == 0).all() and (dk == 0).all()
+    # dv is the one row's dout, summed over the heads: dout is bf16, P within 2^-16 of 1 and rounded, 2^-8
+    rows = [0, 1, 301, 302]
+    want = do[rows].double().view(4, hk, h // hk, 128)
+    assert ((dv[:4].double() - want.sum(2)).abs() <= 2.0 ** -7 * want.abs().sum(2)).all() and (dv[4:] == 0).all()
+    # the first row of longer sequences, of all keys' tiles: other rows get no upstream gradient
+    for lq, lk in (([300, 129, 40], [300, 129, 40]), ([300, 200], [150, 3])):
+        q, k, v, do, cq, ck = _inputs(37, lq, lk, h, hk, d)
+        first = [sum(lq[:i]) + lq[i] - lk[i] for i in range(len(lq))]
+        only = torch.zeros_like(do)
+        only[first] = do[first]
+        out, lse = smla.dense_mha_fwd(q, k, v, 0.1, cq, ck)
+        dq, dk, dv = smla.dense_mha_bwd(q, k, v, 0.1, out, lse, only, cq, ck)
+        assert (dq == 0).all() and (dk == 0).all() and (dv[[sum(lk[:i]) for i in range(len(lk))]] != 0).any()
+        assert (smla.dense_mha_bwd(q, k, v, 0.1, out, lse, do, cq, ck)[0][first] == 0).all()
