@@ -71,8 +71,8 @@ struct MhaBwdParams {
   int slots;                               // tiles per head (pack) that the grid has room for
   MhaHeads order;
   float scale, scale_log2;
-  const __nv_bfloat16* k;                  // row (t, h) at k + t k_tok + h k_head
-  long long k_tok, k_head;
+  const __nv_bfloat16 *k, *dout;           // row (t, h) at k + t k_tok + h k_head
+  long long k_tok, k_head, do_tok, do_head;
   const float* lse;                        // [total_q, h_q]
   float* delta;                            // [total_q, h_q]: D
   __nv_bfloat16 *dq, *dk, *dv;             // [total, h, d]
@@ -262,6 +262,7 @@ __device__ __forceinline__ bool mha_dq_rows(const MhaBwdParams& p, MhaDqMisc& m,
     named_bar_sync(1, 256);
     if (!there) return false;
     delta = m.part[0][row] + m.part[1][row];
+    if (!mha_finite(delta)) delta = __uint_as_float(0x7fc00000u);   // all of the row's dS is then NaN
     if (live && half == 0) p.delta[at] = delta;
   }
   constexpr int kHalf = C::kN / 2;
@@ -427,6 +428,7 @@ struct __align__(16) MhaDkvMisc {
   uint32_t tmem_base;
   int abort_flag;
   int prior_error;
+  int cleared;   // values of dout that are not finite were taken out of a block of which some rows do not see all keys
   MhaWork work;
   alignas(16) float shift[4][64];     // -lse in powers of two and -D of a block's rows, read four at a time
   alignas(16) float minus_d[4][64];
@@ -590,9 +592,8 @@ __device__ __forceinline__ bool mha_dkv_sums(const MhaBwdParams& p, MhaDkvMisc& 
   return true;
 }
 
-// The rows' lse (in powers of two) and D, there with the block's copy of Q; where D is not
-// finite the row's gradient was not, and its weights become NaN.  Rows of no token weigh
-// nothing.
+// The rows' lse (in powers of two) and D, there with the block's copy of Q.  Rows of no token
+// weigh nothing.
 template <int DQK>
 __device__ __forceinline__ bool mha_dkv_stats(const MhaBwdParams& p, MhaDkvMisc& m, const MhaWork& w, const MhaQueries& s,
                                               int kvh) {
@@ -613,7 +614,6 @@ __device__ __forceinline__ bool mha_dkv_stats(const MhaBwdParams& p, MhaDkvMisc&
         const size_t at = static_cast<size_t>(w.q0 + tok) * p.h_q + head + r % p.pack;
         l[i] = __ldg(p.lse + at) * -1.4426950408889634f;
         d[i] = -__ldcg(p.delta + at);
-        if (!(fabsf(d[i]) <= 3.402823466e38f)) l[i] = __uint_as_float(0x7fc00000u);
       }
     }
     if (!warp_wait(smem_u32(&m.empty[st]), turn ^ 1, deadline, ab)) return false;
@@ -634,6 +634,37 @@ __device__ __forceinline__ bool mha_dkv_stats(const MhaBwdParams& p, MhaDkvMisc&
     }
   }
   return true;
+}
+
+// As mha_restore, for dv and what is not finite in dout: the columns (64 from `col0` on) of the
+// keys of `asked` become the sums of what is not finite in the rows that see the key, of all heads
+// of the group; NaN where such a row's lse is not finite, since its weights are NaN.  One warp, a
+// key per lane.
+__device__ __forceinline__ void mha_restore_dv(const MhaBwdParams& p, uint32_t asked, const MhaWork& w, int key, int kvh,
+                                               __nv_bfloat16* out, int col0) {
+  const int lane = static_cast<int>(lane_id()), lq = w.q1 - w.q0, lk = w.k1 - w.k0, heads = kvh * p.group;
+  int end = lq;
+  bool odd = false;   // an lse is not finite
+  float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  __syncwarp();   // the keys' own threads have written them
+  while (asked != 0u) {   // from the last key, which the fewest rows see
+    const int of = 31 - __clz(asked), first = max(0, __shfl_sync(0xffffffffu, key, of) - (lk - lq));
+    __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(out), of));
+    asked &= ~(1u << of);
+    for (int h = heads; h < heads + p.group; ++h) {
+      mha_take_odd<8>(p.dout + w.q0 * p.do_tok + h * p.do_head + col0, p.do_tok, first, end, acc);
+      for (int r = first + lane; r < end; r += 32) odd |= !mha_finite(__ldg(p.lse + static_cast<size_t>(w.q0 + r) * p.h_q + h));
+    }
+    end = first;
+    if (__any_sync(0xffffffffu, odd)) acc[0] = acc[1] = acc[2] = acc[3] = acc[4] = acc[5] = acc[6] = acc[7] = __uint_as_float(0x7fc00000u);
+    float sum[8];
+    mha_sum_odd<8>(acc, sum);
+    if (lane < 8) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (sum[k] != 0.f) o[8 * lane + k] = __float2bfloat16_rn(sum[k]);
+    }
+  }
 }
 
 template <int DQK>
@@ -687,7 +718,7 @@ __device__ __forceinline__ bool mha_dkv_rows(const MhaBwdParams& p, MhaDkvMisc& 
       if (!warp_wait(smem_u32(&m.t_full), j & 1, deadline, ab)) return false;
       if (!warp_wait(smem_u32(&m.do_full[st]), turn, deadline, ab)) return false;
       mha_clear<256>(sb + C::kQOff + st * C::kQBytes, C::kQBytes);
-      mha_clear<256>(sb + C::kDoOff + st * C::kDoBytes, C::kDoBytes);
+      mha_clear<256>(sb + C::kDoOff + st * C::kDoBytes, C::kDoBytes, &m.cleared);
     }
     const float4* l4 = reinterpret_cast<const float4*>(&m.shift[st][kHalf * half]);
 #pragma unroll
@@ -752,12 +783,17 @@ __device__ __forceinline__ bool mha_dkv_rows(const MhaBwdParams& p, MhaDkvMisc& 
   }
   const size_t at = live ? static_cast<size_t>(w.k0 + key) * p.h_kv + kvh : 0;
   // the copies are not needed any more: their memory is the stage
-  mha_store_sums<2>(p.dv + at * kMhaDv + 64 * half, sb + threadIdx.x * mha_stage_row<2>(), lane0 + C::kDv + 64 * half, 1.f,
-                    s.total > 0, live);
+  const bool odd = mha_store_sums<2, true>(p.dv + at * kMhaDv + 64 * half, sb + threadIdx.x * mha_stage_row<2>(),
+                                           lane0 + C::kDv + 64 * half, 1.f, s.total > 0, live);
   mha_store_sums<DQK / 64>(p.dk + at * DQK + half * (DQK / 2),
                            sb + 256 * mha_stage_row<2>() + threadIdx.x * mha_stage_row<DQK / 64>(),
                            lane0 + C::kDk + half * (DQK / 2), p.scale, s.total > 0, live);
   bulk_wait();
+  if (s.total > 0) {   // long past: the other warps' arrivals with their weights of the last block, and what they have found by then
+    if (!warp_wait(smem_u32(&m.p_full), (s.total - 1) & 1, deadline, ab)) return false;
+    const uint32_t keys = __ballot_sync(0xffffffffu, live && (odd || *reinterpret_cast<volatile int*>(&m.cleared)));
+    if (keys != 0u) mha_restore_dv(p, keys, w, key, kvh, p.dv + at * kMhaDv + 64 * half, 64 * half);
+  }
   return true;
 }
 
@@ -792,6 +828,7 @@ __global__ void __launch_bounds__(MhaDkvShape<DQK>::kThreads, 1) dense_mha_dkv_k
     mbar_init(smem_u32(&m.drain[0]), 1);
     mbar_init(smem_u32(&m.drain[1]), 1);
     m.abort_flag = 0;
+    m.cleared = 0;
     m.prior_error = *reinterpret_cast<volatile int*>(&g_device_error);
     fence_mbar_init();
     prefetch_tmap(&p.map_q);

@@ -356,6 +356,9 @@ sparse_mla_status_t mha_bwd_launch(const MhaRows& q, const MhaRows& k, const Mha
   p.k = static_cast<const __nv_bfloat16*>(k.p);
   p.k_tok = k.tok;
   p.k_head = k.head;
+  p.dout = static_cast<const __nv_bfloat16*>(g.p);
+  p.do_tok = g.tok;
+  p.do_head = g.head;
   p.lse = lse;
   p.delta = static_cast<float*>(workspace);
   p.dq = static_cast<__nv_bfloat16*>(dq);

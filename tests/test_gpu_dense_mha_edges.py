@@ -162,3 +162,80 @@ def test_rows_that_see_one_key_have_no_gradient_of_scores(smla, h, hk, d):  # no
         dq, dk, dv = smla.dense_mha_bwd(q, k, v, 0.1, out, lse, only, cq, ck)
         assert (dq == 0).all() and (dk == 0).all() and (dv[[sum(lk[:i]) for i in range(len(lk))]] != 0).any()
         assert (smla.dense_mha_bwd(q, k, v, 0.1, out, lse, do, cq, ck)[0][first] == 0).all()
+
+
+BACK = [([300], [300], 2, 2, 192), ([1100, 70], [1300, 70], 4, 4, 128), ([200, 90], [200, 40], 64, 1, 192),
+        ([400], [450], 5, 1, 128), ([260], [260], 6, 2, 192)]
+
+
+@pytest.mark.parametrize("lq,lk,h,hk,d", BACK)
+def test_dv_does_not_depend_on_values(smla, lq, lk, h, hk, d):  # noqa: F811
+    """An infinite value makes out and D of the rows that see it infinite: their dq and what they give dk is NaN;
+    dv = P^T dout stays."""
+    q, k, v, do, cq, ck = _inputs(38, lq, lk, h, hk, d)
+    want = smla.dense_mha_bwd(q, k, v, 0.1, *smla.dense_mha_fwd(q, k, v, 0.1, cq, ck), do, cq, ck)
+    for at in (0, 37, 127, 128, lk[0] - 1):
+        if at >= lk[0]:
+            continue
+        v2 = v.clone()
+        v2[at, :, 9] = INF
+        dq, dk, dv = smla.dense_mha_bwd(q, k, v2, 0.1, *smla.dense_mha_fwd(q, k, v2, 0.1, cq, ck), do, cq, ck)
+        assert torch.equal(dv, want[2])
+        sees = max(0, at + lq[0] - lk[0])   # the first row that sees the key
+        assert torch.equal(dq[:sees], want[0][:sees]) and torch.equal(dq[lq[0]:], want[0][lq[0]:])
+        assert dq[sees:lq[0]].isnan().all() and dk[:lk[0]].isnan().all()
+        assert torch.equal(dk[lk[0]:], want[1][lk[0]:])
+
+
+@pytest.mark.parametrize("scores", ["near", "far apart"])
+@pytest.mark.parametrize("lq,lk,h,hk,d", BACK)
+def test_upstream_gradients_that_are_not_finite(smla, lq, lk, h, hk, d, scores):  # noqa: F811
+    """A column of dv is the sum of what is not finite in the rows that see the key, also where weights underflow;
+    the other columns, and the keys that those rows do not see, have what they had."""
+    q, k, v, do, cq, ck = _inputs(39, lq, lk, h, hk, d)
+    if scores == "far apart":
+        q[..., 0], k[..., 0] = 8.0, 0.0
+        k[1::3, :, 0] = -2000.0
+    out, lse = smla.dense_mha_fwd(q, k, v, 0.1, cq, ck)
+    want = smla.dense_mha_bwd(q, k, v, 0.1, out, lse, do, cq, ck)
+    n, g = lq[0], h // hk
+    first = max(0, n - lk[0])   # rows before it see nothing
+    do2 = do.clone()
+    rows = sorted({first, first + 5, n // 2, n - 1})
+    for i, r in enumerate(rows):
+        do2[r, i % h, 3], do2[r, -1, 70], do2[r, 0, 90] = INF, (INF, -INF)[i % 2], (NAN, 1.0)[i % 2]
+    dq, dk, dv = smla.dense_mha_bwd(q, k, v, 0.1, out, lse, do2, cq, ck)
+    # suffix sums over the rows of the first sequence, then over the heads of a group
+    odd = torch.where(do2[first:n].isfinite(), 0.0, do2[first:n].float()).flip(0)
+    odd = _odd_sums(odd).flip(0).view(n - first, hk, g, 128).sum(2)
+    at = (torch.arange(lk[0], device=q.device) - (lk[0] - n)).clamp(min=first) - first   # first row that sees a key
+    odd = torch.cat([odd[at], torch.zeros_like(dv[lk[0]:], dtype=torch.float32)])
+    ref = torch.where(odd == 0, want[2].float(), odd)
+    # columns with a changed but finite entry (1.0) are not compared
+    cols = torch.ones(128, dtype=torch.bool, device=q.device)
+    cols[90] = False
+    same = lambda a, b: torch.equal(torch.nan_to_num(a, nan=12345.0), torch.nan_to_num(b, nan=12345.0))  # noqa: E731
+    assert same(dv[..., cols].float(), ref[..., cols])
+    assert (dv[..., 90].isfinite() == odd[..., 90].isfinite()).all()
+    # dq: the heads' rows with such an entry; dk: the keys that one of them sees
+    bad = ~do2.isfinite().all(-1)
+    assert dq[bad].isnan().all()
+    keep = ~bad
+    keep[rows] = False   # their finite heads may have the changed entry
+    assert torch.equal(dq[keep], want[0][keep])
+    bad_key = torch.zeros(dk.shape[:2], dtype=torch.bool, device=q.device)
+    for r, j in bad.nonzero().tolist():
+        bad_key[:min(lk[0], r + lk[0] - n + 1), j // g] = True
+    assert dk[bad_key].isnan().all() and dk[~bad_key].isfinite().all()
+
+
+def test_dv_of_rows_whose_scores_are_not_finite(smla):  # noqa: F811
+    """A NaN key: the rows that see it have NaN weights, whatever their upstream gradient is."""
+    q, k, v, do, *_ = _inputs(40, [300], [300], 4, 2, 128)
+    k[150, 0, 5] = NAN
+    do[[20, 100, 200, 290], :, 7] = INF
+    out, lse = smla.dense_mha_fwd(q, k, v, 0.1)
+    dq, dk, dv = smla.dense_mha_bwd(q, k, v, 0.1, out, lse, do)
+    assert dv[:, 0].isnan().all() and dq[150:, :2].isnan().all() and dk[:, 0].isnan().all()
+    assert (dv[:291, 1, 7] == INF).all() and dv[291:, 1].isfinite().all()
+    assert dv[:, 1, :7].isfinite().all() and dv[:, 1, 8:].isfinite().all()
