@@ -511,7 +511,8 @@ sparse_mla_status_t dense_mha_fwd(const void* q, long long q_tok_stride, long lo
  *
  * Rows of no sequence take no part: their gradients are zero.  Nor do pairs of a
  * query and a key that it does not see.  Where a row's rowsum(dout * out) is not
- * finite, its dq and the dk of the keys that it sees are NaN.  A column of dv
+ * finite, its dq and the dk of the keys that it sees are NaN; so are columns of
+ * its dq in which a key that it sees is not finite.  A column of dv
  * where rows of dout that see the key are not finite is the sum of those values
  * alone, however small their weights; NaN where such a row's lse is not finite.
  * A value of v that is not finite has no part in dv.  Outputs and

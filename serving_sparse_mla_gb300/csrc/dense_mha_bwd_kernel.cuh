@@ -93,6 +93,7 @@ struct __align__(16) MhaDqMisc {
   uint32_t tmem_base;
   int abort_flag;
   int prior_error;
+  int cleared;   // values of K that are not finite were taken out of a block that some rows do not see all of
   MhaWork work;
   float part[2][kMhaTile];
 };
@@ -222,6 +223,34 @@ __device__ __forceinline__ bool mha_dq_sums(const MhaBwdParams& p, MhaDqMisc& m,
   return true;
 }
 
+// A key that is not finite and that a row with a finite lse sees has the score -infinite: its dS
+// is 0, and 0 times an infinity or a NaN is NaN.  So it is where the product meets the key; for
+// keys of the blocks from which such values were taken out, first .. end - 1, the 32 N columns of
+// the rows of `asked` are made so here.  One warp, a row per lane; a lane's end is its row's, and
+// does not fall from lane to lane.
+template <int N>
+__device__ __forceinline__ void mha_restore_dq(uint32_t asked, const __nv_bfloat16* keys, long long step, int first, int end,
+                                               __nv_bfloat16* out) {
+  __syncwarp();   // the rows' own threads have written them
+  for (int c = 0; c < N; ++c) {
+    float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    int from = first;
+    for (uint32_t left = asked; left != 0u; left &= left - 1) {
+      const int row = __ffs(left) - 1, upto = __shfl_sync(0xffffffffu, end, row);
+      __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(out), row));
+      mha_take_odd<4>(keys + 32 * c, step, from, upto, acc);
+      from = max(from, upto);
+      float sum[8];
+      mha_sum_odd<4>(acc, sum);
+      if (lane_id() < 4) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (sum[k] != 0.f) o[32 * c + 8 * lane_id() + k] = __ushort_as_bfloat16(0x7fff);
+      }
+    }
+  }
+}
+
 template <int DQK>
 __device__ __forceinline__ bool mha_dq_rows(const MhaBwdParams& p, MhaDqMisc& m, uint32_t sb, uint32_t tmem,
                                             const MhaWork& w, int t0, int blocks, int pack0) {
@@ -283,7 +312,7 @@ __device__ __forceinline__ bool mha_dq_rows(const MhaBwdParams& p, MhaDqMisc& m,
     if (edge) {   // the product with dS must not meet what is not finite in a hidden key
       const int st = j % C::kKStages;
       if (!warp_wait(smem_u32(&m.k_full[st]), j / C::kKStages & 1, deadline, ab)) return false;
-      mha_clear<256>(sb + C::kKOff + st * C::kKBytes, C::kKBytes);
+      mha_clear<256>(sb + C::kKOff + st * C::kKBytes, C::kKBytes, &m.cleared);
     }
     const int sees = edge ? tok + lk - lq + 1 - j * C::kN - kHalf * half : kHalf;
 #pragma unroll
@@ -322,6 +351,13 @@ __device__ __forceinline__ bool mha_dq_rows(const MhaBwdParams& p, MhaDqMisc& m,
   mha_store_sums<DQK / 64>(p.dq + at * DQK + half * (DQK / 2), sb + threadIdx.x * mha_stage_row<DQK / 64>(),
                            lane0 + C::kDq + half * (DQK / 2), p.scale, blocks > 0, live);
   bulk_wait();
+  if (blocks > whole) {   // long past: the other warps' arrivals with their dS of the last block, and what they have found by then
+    if (!warp_wait(smem_u32(&m.ds_full), (blocks - 1) & 1, deadline, ab)) return false;
+    const uint32_t rows = __ballot_sync(0xffffffffu, live && *reinterpret_cast<volatile int*>(&m.cleared));
+    if (rows != 0u)
+      mha_restore_dq<DQK / 64>(rows, p.k + w.k0 * p.k_tok + pack0 / p.group * p.k_head + half * (DQK / 2), p.k_tok,
+                               whole * C::kN, tok + lk - lq + 1, p.dq + at * DQK + half * (DQK / 2));
+  }
   return true;
 }
 
@@ -357,6 +393,7 @@ __global__ void __launch_bounds__(MhaDqShape<DQK>::kThreads, 1) dense_mha_dq_ker
     mbar_init(smem_u32(&m.drain[0]), 1);
     mbar_init(smem_u32(&m.drain[1]), 1);
     m.abort_flag = 0;
+    m.cleared = 0;
     m.prior_error = *reinterpret_cast<volatile int*>(&g_device_error);
     fence_mbar_init();
     prefetch_tmap(&p.map_q);

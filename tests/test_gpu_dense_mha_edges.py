@@ -239,3 +239,24 @@ def test_dv_of_rows_whose_scores_are_not_finite(smla):  # noqa: F811
     assert dv[:, 0].isnan().all() and dq[150:, :2].isnan().all() and dk[:, 0].isnan().all()
     assert (dv[:291, 1, 7] == INF).all() and dv[291:, 1].isfinite().all()
     assert dv[:, 1, :7].isfinite().all() and dv[:, 1, 8:].isfinite().all()
+
+
+@pytest.mark.parametrize("lq,lk,h,hk,d", [x for x in BACK if x[2] != 5 and x[2] != 6])
+def test_seen_keys_whose_scores_are_minus_infinite(smla, lq, lk, h, hk, d):  # noqa: F811
+    """Weight 0 and dS 0: NaN in dq where the key is not finite (0 times an infinity), whether all rows of a block see
+    it or not; all else as with a key that is only far away.  (No row sees such a key alone.)"""
+    q, k, v, do, cq, ck = _inputs(41, lq, lk, h, hk, d)
+    q[..., 5] = 1.0
+    for at in (1, 90, 95, 96, 130, 199, 200, 255, lk[0] - 1):
+        if at >= lk[0]:
+            continue
+        k2, far = k.clone(), k.clone()
+        k2[at, :, 5], far[at, :, 5] = -INF, -1e30
+        a, b = smla.dense_mha_fwd(q, k2, v, 0.1, cq, ck), smla.dense_mha_fwd(q, far, v, 0.1, cq, ck)
+        sees = max(0, at + lq[0] - lk[0])
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+        got, want = (smla.dense_mha_bwd(q, x, v, 0.1, *y, do, cq, ck) for x, y in ((k2, a), (far, b)))
+        assert torch.equal(got[1], want[1]) and torch.equal(got[2], want[2])
+        assert got[0][sees:lq[0], :, 5].isnan().all()
+        got[0][sees:lq[0], :, 5] = want[0][sees:lq[0], :, 5]
+        assert torch.equal(got[0], want[0])
