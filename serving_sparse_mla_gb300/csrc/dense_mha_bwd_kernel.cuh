@@ -731,6 +731,10 @@ __device__ __forceinline__ bool mha_dkv_rows(const MhaBwdParams& p, MhaDkvMisc& 
   const int last_key = min((w.tile + 1) * kMhaTile, lk) - 1;
   const uint32_t ts = lane0 + C::kS + kHalf * half, tt = lane0 + C::kT + kHalf * half,
                  tp = lane0 + C::kP + kHalf / 2 * half, td = lane0 + C::kDs + kHalf / 2 * half;
+  // the bits of the last columns that are rows; in the others, zeros, a key that is not finite has a score of NaN
+  const int used = p.pack * p.tok_tile - kHalf * half;
+  auto bits = [&](int col) { return (col < used ? 0xffffu : 0u) | (col + 1 < used ? 0xffff0000u : 0u); };
+  const uint32_t rows[2] = {bits(kHalf - 4), bits(kHalf - 2)};
   int b = 0, st = 0, turn = 0, before = 0, turn_before = 0;   // where the block is, and the one before
   for (int j = 0; j < s.total; ++j) {
     deadline = global_timer_ns() + p.timeout_ns;
@@ -772,7 +776,7 @@ __device__ __forceinline__ bool mha_dkv_rows(const MhaBwdParams& p, MhaDkvMisc& 
     }
     if (j > 0 && !warp_wait(smem_u32(&m.p_free), (j - 1) & 1, deadline, ab)) return false;
     tc_fence_after();
-    tmem_store_bf16<kHalf>(tp, x);
+    tmem_store_bf16<kHalf>(tp, x, rows);
     tmem_wait_st();
     tc_fence_before();
     __syncwarp();
@@ -802,7 +806,7 @@ __device__ __forceinline__ bool mha_dkv_rows(const MhaBwdParams& p, MhaDkvMisc& 
     // the product with the dS before has ended when that block is free
     if (j > 0 && !warp_wait(smem_u32(&m.empty[before]), turn_before, deadline, ab)) return false;
     tc_fence_after();
-    tmem_store_bf16<kHalf>(td, y);
+    tmem_store_bf16<kHalf>(td, y, rows);
     tmem_wait_st();
     tc_fence_before();
     __syncwarp();

@@ -58,6 +58,7 @@ constexpr int kMhaTile = 128;              // query rows of a tile, keys of a bl
 constexpr int kMhaDv = 128;
 constexpr int kMhaMaxCluster = 16;
 constexpr uint32_t kMhaUnit = 16384;       // bytes of a ring unit, and of 64 columns of a Q tile
+constexpr int kMhaSpare = 4;               // rows of 64 that heads side by side leave unused at most (dk and dv mask as many)
 constexpr float kMhaLazy = 8.f;            // log2 of the growth of a maximum that O is rescaled for
 
 enum MhaErrCode : int {
@@ -383,12 +384,15 @@ __device__ __forceinline__ void tmem_load(uint32_t taddr, float* v) {
   else if constexpr (N == 48) tmem_load48(taddr, v);
   else tmem_load32(taddr, v);
 }
-// N values rounded to bf16 into N / 2 columns.
+// N values rounded to bf16 into N / 2 columns, of the last two of which `keep` says what stays.
 template <int N>
-__device__ __forceinline__ void tmem_store_bf16(uint32_t taddr, const float* x) {
+__device__ __forceinline__ void tmem_store_bf16(uint32_t taddr, const float* x, const uint32_t* keep = nullptr) {
   float pk[N / 2];
 #pragma unroll
-  for (int i = 0; i < N / 2; ++i) pk[i] = __uint_as_float(pack_bf16x2(x[2 * i], x[2 * i + 1]));
+  for (int i = 0; i < N / 2; ++i) {
+    const uint32_t v = pack_bf16x2(x[2 * i], x[2 * i + 1]);
+    pk[i] = __uint_as_float(keep != nullptr && i >= N / 2 - 2 ? v & keep[i - (N / 2 - 2)] : v);
+  }
 #pragma unroll
   for (int i = 0; i < N / 32; ++i) tmem_st16(taddr + 16 * i, pk + 16 * i);
   if constexpr (N % 32 != 0) tmem_st8(taddr + N / 2 - 8, pk + N / 2 - 8);

@@ -175,7 +175,7 @@ sparse_mla_status_t check_mha(const MhaRows& q, const MhaRows& k, const MhaRows&
 // in the place of 249, their gradients 762 and 722; 16 tokens' gradients on 9000 keys 122 and 97.
 int mha_pack(int group, int rows) {
   for (int n = group < rows ? group : rows; n > 1; --n)
-    if (group % n == 0 && rows % n <= rows / 16) return n;
+    if (group % n == 0 && rows % n <= rows / (64 / smla::kMhaSpare)) return n;
   return 1;
 }
 

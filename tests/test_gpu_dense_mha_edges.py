@@ -241,10 +241,11 @@ def test_dv_of_rows_whose_scores_are_not_finite(smla):  # noqa: F811
     assert dv[:, 1, :7].isfinite().all() and dv[:, 1, 8:].isfinite().all()
 
 
-@pytest.mark.parametrize("lq,lk,h,hk,d", [x for x in BACK if x[2] != 5 and x[2] != 6])
+@pytest.mark.parametrize("lq,lk,h,hk,d", BACK)
 def test_seen_keys_whose_scores_are_minus_infinite(smla, lq, lk, h, hk, d):  # noqa: F811
     """Weight 0 and dS 0: NaN in dq where the key is not finite (0 times an infinity), whether all rows of a block see
-    it or not; all else as with a key that is only far away.  (No row sees such a key alone.)"""
+    it or not; all else as with a key that is only far away.  (No row sees such a key alone.)  A block whose heads
+    side by side leave rows unused gives them no weight."""
     q, k, v, do, cq, ck = _inputs(41, lq, lk, h, hk, d)
     q[..., 5] = 1.0
     for at in (1, 90, 95, 96, 130, 199, 200, 255, lk[0] - 1):
