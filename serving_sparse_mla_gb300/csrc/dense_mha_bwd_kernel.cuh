@@ -741,9 +741,9 @@ __device__ __forceinline__ bool mha_dkv_rows(const MhaBwdParams& p, MhaDkvMisc& 
     const int t0 = s.first + b * p.tok_tile;
     if (++b == s.blocks) b = 0;
     const bool edge = t0 + lk - lq < last_key || t0 + p.tok_tile > lq;   // some rows do not see all of the keys
-    // the columns that see this thread's key
-    const int lo = edge ? p.pack * (key - (lk - lq) - t0) - kHalf * half : 0;
-    const int hi = edge ? p.pack * (lq - t0) - kHalf * half : kHalf;
+    // the columns that see this thread's key, from a token of the block to another (0 to kN: `pack` of them could pass 32 bits)
+    const int lo = edge ? p.pack * max(0, key - (lk - lq) - t0) - kHalf * half : 0;
+    const int hi = edge ? p.pack * min(C::kN, lq - t0) - kHalf * half : kHalf;
     // the rows' numbers are another warp's plain stores: what tells that they are there is its arrival beside the copy
     // of Q, not the tensor core's on s_full
     if (!warp_wait_both(smem_u32(&m.q_full[st]), turn, smem_u32(&m.s_full), j & 1, deadline, ab)) return false;

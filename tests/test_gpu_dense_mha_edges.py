@@ -261,3 +261,19 @@ def test_seen_keys_whose_scores_are_minus_infinite(smla, lq, lk, h, hk, d):  # n
         assert got[0][sees:lq[0], :, 5].isnan().all()
         got[0][sees:lq[0], :, 5] = want[0][sees:lq[0], :, 5]
         assert torch.equal(got[0], want[0])
+
+
+def test_keys_times_heads_past_32_bits(smla):  # noqa: F811
+    """One token of 32 heads over 2^26 keys and more: every key has the same weight and the same dv."""
+    n, h, d = (1 << 26) + 1000, 32, 128
+    q, _, _, do, *_ = _inputs(42, [1], [1], h, 1, d)
+    k, v = (torch.zeros(n, 1, d, dtype=torch.bfloat16, device=q.device) for _ in range(2))
+    out, lse = smla.dense_mha_fwd(q, k, v, 0.1)
+    # ln n is 18.02: fp32's half step there and the sum's roundings (2^-20 of n)
+    assert (out == 0).all() and ((lse.double() - torch.tensor(float(n)).log()).abs() <= 2.0 ** -19).all()
+    dq, dk, dv = smla.dense_mha_bwd(q, k, v, 0.1, out, lse, do)
+    assert (dq == 0).all() and not dk.count_nonzero()
+    row = dv[-1].double()
+    # P is rounded to bf16 and off by lse's error, dv rounded once more
+    assert ((row - do.double().sum(1) / n).abs() <= 2.0 ** -7 * do.double().abs().sum(1) / n).all() and (row != 0).any()
+    assert all(torch.equal(x, dv[-1:].expand_as(x)) for x in dv.split(1 << 22))
