@@ -713,6 +713,17 @@ def mla_norm_rope_bwd(q, kv, positions, cos_sin, dq, dkv, q_weight=None, kv_weig
 
 # ---------------------------------------------------------------- residual norm
 
+_INT_MAX = 2 ** 31 - 1
+
+
+def _countable(**sizes) -> None:
+    """Sizes go to the library as 32-bit counts, and ctypes cuts what has more bits: it
+    would take 2^32 + 5 rows for 5."""
+    for name, n in sizes.items():
+        if n > _INT_MAX:
+            raise ValueError(f"{name} is {n}; the library counts to 2^31 - 1")
+
+
 def _wide_rows(t: torch.Tensor, n: int, d: int, name: str, dev) -> int:
     """Row stride in elements of bf16 rows [n, d], contiguous in themselves, each on 16 bytes."""
     _on_cuda(t, name)
@@ -733,6 +744,8 @@ def _norm_rows(x, weight, others, names):
     if len(shape) != 2:
         raise ValueError(f"{names[0]} must be [n, d], got {tuple(shape)}")
     n, d = shape
+    if n > _INT_MAX or d > _INT_MAX:
+        _countable(n=n, d=d)
     step, one = x.stride()
     bits = step & 7 | x.data_ptr() & 15
     good = (x.is_cuda and x.dtype is _BF16 and one == 1 and weight.dtype is _BF16 and weight.device == dev
@@ -835,6 +848,7 @@ def _add_norm(cs, x, x_step, residual, res_step, weight, eps, out, scales, form,
 
 def add_norm_bwd_workspace_size(n: int, d: int) -> int:
     """Bytes mla_add_norm_bwd needs on the current device."""
+    _countable(n=n, d=d)
     return int(load().mla_add_norm_bwd_workspace_size(n, d))
 
 
@@ -906,6 +920,8 @@ def _mha_args(q, k, v, cu_seqlens_q, cu_seqlens_kv):
     if q.dim() == 3 and k.dim() == 3 and v.dim() == 3:
         (nq, hq, dq), (nk, hk, dk), (nv, hv, dv) = q.shape, k.shape, v.shape
         (qt, qh, q1), (kt, kh, k1), (vt, vh, v1) = q.stride(), k.stride(), v.stride()
+        if nq > _INT_MAX or nk > _INT_MAX or hq > _INT_MAX or dq > _INT_MAX or dv > _INT_MAX:
+            _countable(total_q=nq, total_kv=nk, h_q=hq, d_qk=dq, d_v=dv)
         if (q.is_cuda and q.dtype is _BF16 and k.dtype is _BF16 and v.dtype is _BF16 and k.device == dev
                 and v.device == dev and dq == dk and nk == nv and hk == hv and hk > 0 and hq % hk == 0
                 and q1 == 1 and k1 == 1 and v1 == 1 and not (qt | qh | kt | kh | vt | vh) & 7
@@ -915,7 +931,7 @@ def _mha_args(q, k, v, cu_seqlens_q, cu_seqlens_kv):
                 return nq, nk, hq, hk, dq, dv, 1, dev, (qt, qh, kt, kh, vt, vh)
             if cu_seqlens_q is not None and cu_seqlens_kv is not None:
                 n = cu_seqlens_q.numel()
-                if (n > 0 and cu_seqlens_kv.numel() == n and _dense(cu_seqlens_q, _I32, n, dev)
+                if (0 < n <= _INT_MAX and cu_seqlens_kv.numel() == n and _dense(cu_seqlens_q, _I32, n, dev)
                         and _dense(cu_seqlens_kv, _I32, n, dev)):
                     return nq, nk, hq, hk, dq, dv, n - 1, dev, (qt, qh, kt, kh, vt, vh)
     steps = _heads(q, "q", dev) + _heads(k, "k", dev) + _heads(v, "v", dev)
@@ -928,6 +944,7 @@ def _mha_args(q, k, v, cu_seqlens_q, cu_seqlens_kv):
     if h_kv == 0 or h_q % h_kv:
         raise ValueError(f"{h_q} query heads do not share {h_kv} key heads evenly")
     batch = _seq_args(cu_seqlens_q, cu_seqlens_kv, dev)
+    _countable(batch=batch)
     if cu_seqlens_q is not None and cu_seqlens_kv.numel() != batch + 1:
         raise ValueError(f"cu_seqlens_kv holds {cu_seqlens_kv.numel()} offsets; cu_seqlens_q {batch + 1}")
     return total_q, total_kv, h_q, h_kv, d_qk, v.shape[2], batch, dev, steps
@@ -995,6 +1012,7 @@ def _mha_fwd(cs, q, k, v, steps, cu_q, cu_kv, batch, sm_scale, out, lse, fill, t
 def dense_mha_bwd_workspace_size(total_q: int, total_kv: int, batch: int, h_q: int, h_kv: int, d_qk: int,
                                  d_v: int = 128) -> int:
     """Bytes dense_mha_bwd needs."""
+    _countable(total_q=total_q, total_kv=total_kv, batch=batch, h_q=h_q, h_kv=h_kv, d_qk=d_qk, d_v=d_v)
     return int(load().dense_mha_bwd_workspace_size(total_q, total_kv, batch, h_q, h_kv, d_qk, d_v))
 
 
