@@ -774,21 +774,16 @@ def _norm_rows(x, weight, others, names):
 
 def _apart(out: Optional[torch.Tensor], name: str, size: int, inputs, same=()) -> None:
     """A given output's first `size` bytes may not meet memory that the call still
-    reads: `inputs` are (tensor, its row stride in elements or 0, name).  An output of
-    whole rows may be one of `same`, dense and at the same address (each row is read
-    before it is written)."""
+    reads: `inputs` are (tensor, name).  An output of whole rows may be one of `same`,
+    dense and at the same address (each row is read before it is written)."""
     if out is None:
         return
     at = out.data_ptr()
-    for t, step, what in inputs:
+    for t, what in inputs:
         if t is None:
             continue
-        lo = t.data_ptr()
-        if step and t.shape[0] > 0:
-            first, last = min(0, (t.shape[0] - 1) * step), max(0, (t.shape[0] - 1) * step) + t.shape[1]
-        else:
-            first, last = 0, t.numel()
-        if at < lo + last * t.element_size() and lo + first * t.element_size() < at + size:
+        lo, hi = _span(t)
+        if at < hi and lo < at + size:
             if not (what in same and lo == at and t.is_contiguous()):
                 raise ValueError(f"{name} shares memory with {what}"
                                  + (" other than as the same dense tensor" if what in same else ""))
@@ -819,11 +814,11 @@ def mla_add_norm(x, weight, residual=None, eps: float = 1e-6, group: Optional[in
         if residual is None and residual_out is not None:
             raise ValueError("residual_out is given without residual")
         _given(residual_out, _BF16, "residual_out", n * d, dev)
-        reads = (x, x_step, "x"), (residual, res_step, "residual"), (weight, 0, "weight")
+        reads = (x, "x"), (residual, "residual"), (weight, "weight")
         _apart(residual_out, "residual_out", 2 * n * d, reads, ("x", "residual"))
-        reads += ((residual_out, 0, "residual_out"),)
+        reads += ((residual_out, "residual_out"),)
         _apart(out, "out", width * n * d, reads)
-        _apart(scales, "scales", 4 * n * n_scales, reads + ((out, 0, "out"),))
+        _apart(scales, "scales", 4 * n * n_scales, reads + ((out, "out"),))
 
     return _run(_add_norm, dev, stream, "mla_add_norm", x, x_step, residual, res_step, weight, eps, out, scales, form,
                 n_scales, kind, residual_out, n, d)
@@ -864,12 +859,12 @@ def mla_add_norm_bwd(z, weight, dout, dresidual=None, eps: float = 1e-6, workspa
         _given(dx, _BF16, "dx", n * d, dev)
         _given(dweight, _F32, "dweight", d, dev)
         _workspace(workspace, dev)
-        reads = (z, z_step, "z"), (weight, 0, "weight"), (dout, g_step, "dout"), (dresidual, r_step, "dresidual")
+        reads = (z, "z"), (weight, "weight"), (dout, "dout"), (dresidual, "dresidual")
         _apart(dx, "dx", 2 * n * d, reads, ("dout", "dresidual"))
-        reads += ((dx, 0, "dx"),)
+        reads += ((dx, "dx"),)
         _apart(dweight, "dweight", 4 * d, reads)
         if workspace is not None:
-            _apart(workspace, "workspace", workspace.numel() * workspace.element_size(), reads + ((dweight, 0, "dweight"),))
+            _apart(workspace, "workspace", workspace.numel() * workspace.element_size(), reads + ((dweight, "dweight"),))
 
     return _run(_add_norm_bwd, dev, stream, "mla_add_norm_bwd", z, z_step, weight, eps, dout, g_step, dresidual, r_step, dx,
                 dweight, workspace, n, d)

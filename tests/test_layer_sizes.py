@@ -37,3 +37,18 @@ def test_attention_refuses_counts_past_32_bits(b, nq, nk, h, hk, d, dv):  # noqa
 def test_attention_refuses_more_offsets_than_32_bits_count(b):  # noqa: F811
     q, k, v, cu = _meta(8, 1, 128), _meta(8, 1, 128), _meta(8, 1, 128), _meta(2 ** 32 + 2, dtype=I32)
     _refused(b, b.dense_mha_fwd, q, k, v, 0.1, cu, cu, match="2\\^31")
+
+
+def test_an_output_behind_a_broadcast_row_is_apart_from_it(b):  # noqa: F811
+    """A row that stands for all of them takes up one row of memory."""
+    pool, w = torch.zeros(11, 64, dtype=BF), torch.zeros(64, dtype=BF)
+    row, x, out = pool[:1].expand(5, 64), pool[6:], pool[1:6]
+    for kw in (dict(x=row, out=out), dict(x=x, residual=row, residual_out=out),
+               dict(x=x, residual=row, group=0, scales=out.view(-1)[:10].view(F32))):
+        _ok(b, "mla_add_norm", b.mla_add_norm, weight=w, **kw)
+    _ok(b, "mla_add_norm_bwd", b.mla_add_norm_bwd, z=row, weight=w, dout=x, dx=out)
+    _ok(b, "mla_add_norm_bwd", b.mla_add_norm_bwd, z=x, weight=w, dout=row, dresidual=row, dx=out)
+    # the row itself, and rows that meet it
+    _refused(b, b.mla_add_norm, row, w, out=pool[:5])
+    _refused(b, b.mla_add_norm, x, w, row, residual_out=pool[:5])
+    _refused(b, b.mla_add_norm_bwd, x, w, row, dx=pool[:5])
