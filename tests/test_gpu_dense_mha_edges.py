@@ -5,7 +5,8 @@ tolerances are test_gpu_dense_mha's."""
 import pytest
 import torch
 
-from tests.test_gpu_dense_mha import _inputs, smla  # noqa: F401  (the module's fixture)
+from oracle import dense_mha_oracle as dmo
+from tests.test_gpu_dense_mha import _check_bwd, _check_fwd, _inputs, smla  # noqa: F401  (the module's fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -277,3 +278,61 @@ def test_keys_times_heads_past_32_bits(smla):  # noqa: F811
     # P is rounded to bf16 and off by lse's error, dv rounded once more
     assert ((row - do.double().sum(1) / n).abs() <= 2.0 ** -7 * do.double().abs().sum(1) / n).all() and (row != 0).any()
     assert all(torch.equal(x, dv[-1:].expand_as(x)) for x in dv.split(1 << 22))
+
+
+def test_gradients_under_offsets_outside_of_the_tensors(smla):  # noqa: F811
+    """Offsets are cut to the tensors in the backward as in the forward."""
+    q, k, v, do, *_ = _inputs(7, [90], [90], 2, 1, 128)
+    offsets = lambda *x: torch.tensor(x, dtype=torch.int32, device=q.device)  # noqa: E731
+    cut = offsets(0, 60, 500, 10), offsets(-4, 60, 1000, 2000)
+    good = (offsets(0, 60, 90),) * 2
+    a, b = smla.dense_mha_fwd(q, k, v, 0.1, *cut), smla.dense_mha_fwd(q, k, v, 0.1, *good)
+    a += smla.dense_mha_bwd(q, k, v, 0.1, *a, do, *cut)
+    b += smla.dense_mha_bwd(q, k, v, 0.1, *b, do, *good)
+    assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+@pytest.mark.parametrize("lq,lk,h,hk,d", [([900, 130], [900, 300], 4, 2, 192), ([1500], [1500], 8, 1, 128)])
+def test_gradients_2_norm(smla, lq, lk, h, hk, d):  # noqa: F811
+    """P and dS are rounded to bf16 once, a value once more on its way out: each is spread over half a step, 2^-8 /
+    sqrt(3) in the mean square at most.  The inputs' keys, queries and upstream rows have independent signs, so a sum's
+    terms add up in the mean square as their errors do: sqrt(2 / 3) 2^-8 in all.  fp32's 2^-16 of the terms of
+    T - D, some 10 times its size, is 2^-12.  Together less than 2^-8."""
+    q, k, v, do, cq, ck = _inputs(43, lq, lk, h, hk, d)
+    out, lse = smla.dense_mha_fwd(q, k, v, d ** -0.5, cq, ck)
+    grads = smla.dense_mha_bwd(q, k, v, d ** -0.5, out, lse, do, cq, ck)
+    ref, _ = dmo.bwd(q, k, v, d ** -0.5, out, lse, do, cq, ck)
+    for g, r, name in zip(grads, ref, ("dq", "dk", "dv")):
+        assert (g.double() - r).norm() <= 2.0 ** -8 * r.norm(), name
+
+
+@pytest.mark.parametrize("n", [300, 2000])
+def test_many_short_sequences(smla, n):  # noqa: F811
+    """Far more sequences than a warp has lanes, some without rows, against the same in a few calls."""
+    g = torch.Generator().manual_seed(44)
+    lq = torch.randint(0, 7, (n,), generator=g).tolist()
+    lk = [x + int(y) for x, y in zip(lq, torch.randint(0, 40, (n,), generator=g))]
+    q, k, v, do, cq, ck = _inputs(45, lq, lk, 4, 2, 128, tail=3)
+    out, lse = smla.dense_mha_fwd(q, k, v, 0.1, cq, ck)
+    dq, dk, dv = smla.dense_mha_bwd(q, k, v, 0.1, out, lse, do, cq, ck)
+    assert (out[-3:] == 0).all() and all((t[-3:] == 0).all() for t in (dq, dk, dv))
+    a, b = cq.tolist(), ck.tolist()
+    for i in range(0, n, 25):
+        j = min(n, i + 25)
+        rows, keys = slice(a[i], a[j]), slice(b[i], b[j])
+        c, e = (t[i:j + 1] - t[i] for t in (cq, ck))
+        if a[i] == a[j] or b[i] == b[j]:
+            continue
+        want = smla.dense_mha_fwd(q[rows], k[keys], v[keys], 0.1, c, e)
+        assert torch.equal(want[0], out[rows]) and torch.equal(want[1], lse[rows])
+        back = smla.dense_mha_bwd(q[rows], k[keys], v[keys], 0.1, *want, do[rows], c, e)
+        assert all(torch.equal(x, y) for x, y in zip(back, (dq[rows], dk[keys], dv[keys])))
+
+
+def test_a_long_request_beside_short_ones(smla):  # noqa: F811
+    """16 tokens behind 30000 keys beside 31 short texts: the layout goes by mean lengths, the rows do not."""
+    lq, lk = [16] + [20 + i for i in range(31)], [30000] + [20 + 2 * i for i in range(31)]
+    q, k, v, do, cq, ck = _inputs(46, lq, lk, 8, 8, 192)
+    out, lse = smla.dense_mha_fwd(q, k, v, 0.1, cq, ck)
+    _check_fwd(out, lse, q, k, v, 0.1, cq, ck)
+    _check_bwd(smla.dense_mha_bwd(q, k, v, 0.1, out, lse, do, cq, ck), q, k, v, 0.1, out, lse, do, cq, ck)
