@@ -63,7 +63,7 @@ enum MhaBwdErrCode : int {
 
 struct MhaBwdParams {
   CUtensorMap map_q, map_do, map_o;        // [token, head, d]: boxes 64 x pack x tok_tile
-  CUtensorMap map_k, map_v;                // boxes 64 x 1 x 128
+  CUtensorMap map_k, map_v;                // boxes 64 x 1 x the keys of a block (dq: 128, at 192 columns 96; dk, dv: 128)
   const int32_t *cu_q, *cu_kv;             // [batch + 1], null for one dense sequence
   int batch, total_q, total_kv, h_q, h_kv, group;
   int pack, tok_tile;                      // rows of a query tile: tok_tile tokens x pack heads
@@ -88,8 +88,10 @@ __device__ __forceinline__ void mha_row_to_tmem(uint32_t taddr, const uint4 (&x)
 
 // ------------------------------------------------------------------ dq
 
+constexpr int kMhaDqK = 3, kMhaDqV = 2;   // stages of K and of V
+
 struct __align__(16) MhaDqMisc {
-  uint64_t q_full, o_full, k_full[3], k_empty[3], v_full[3], v_empty[3], do_ready, s_full, s_free, t_full, t_free, ds_full, dq_full, drain[2];
+  uint64_t q_full, o_full, k_full[kMhaDqK], k_empty[kMhaDqK], v_full[kMhaDqV], v_empty[kMhaDqV], do_ready, s_full, s_free, t_full, t_free, ds_full, dq_full, drain[2];
   uint32_t tmem_base;
   int abort_flag;
   int prior_error;
@@ -102,7 +104,7 @@ template <int DQK>
 struct MhaDqShape {
   static constexpr int kN = DQK == 192 ? 96 : 128;             // keys of a block
   static constexpr int kSub = DQK / 64;
-  static constexpr int kKStages = 3, kVStages = 2;
+  static constexpr int kKStages = kMhaDqK, kVStages = kMhaDqV;
   static constexpr uint32_t kKUnit = kN * 128;                 // 64 columns of a block
   static constexpr uint32_t kKBytes = kSub * kKUnit, kVBytes = 2 * kKUnit;
   static constexpr uint32_t kKOff = kSub * kMhaUnit, kVOff = kKOff + kKStages * kKBytes;
@@ -375,9 +377,11 @@ __global__ void __launch_bounds__(MhaDqShape<DQK>::kThreads, 1) dense_mha_dq_ker
   const int pack0 = head * p.pack;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 3; ++i) {
+    for (int i = 0; i < C::kKStages; ++i) {
       mbar_init(smem_u32(&m.k_full[i]), 1);
       mbar_init(smem_u32(&m.k_empty[i]), 1);
+    }
+    for (int i = 0; i < C::kVStages; ++i) {
       mbar_init(smem_u32(&m.v_full[i]), 1);
       mbar_init(smem_u32(&m.v_empty[i]), 1);
     }

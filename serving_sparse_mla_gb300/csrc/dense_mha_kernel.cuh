@@ -536,7 +536,7 @@ __device__ __forceinline__ void add2(float& a0, float& a1, float b0, float b1) {
 // ------------------------------------------------------------------ forward
 
 constexpr int kMhaMaxUnits = 12;
-constexpr int kMhaFree = 4;   // a block's release is told on one of so many barriers in turn: more than the ring has blocks
+constexpr int kMhaFree = 4;   // a block's release is told on one of so many barriers in turn
 
 struct __align__(16) MhaMisc {
   uint64_t q_full[2], full[kMhaMaxUnits], k_free[kMhaFree], v_free[kMhaFree], s_full[2], p_full[2], o_full[2], o_step, drain;
@@ -563,6 +563,11 @@ struct MhaFwdShape {
   static constexpr int kThreads = NT * 128 + 64;               // two tiles: ptxas leaves 168 registers each, which spills 84 bytes
   static constexpr uint32_t kO = 256;                          // columns of TMEM: two S of 128 each, then O
   static_assert(kUnits >= kSub + 4, "a K block and two V blocks");
+  // The barrier that told of block j's release tells of block j + kMhaFree's next, and must not before the first has been
+  // waited for.  The loads wait for releases in order, so it is enough that the last unit of K (V) j + kMhaFree has no
+  // place in the ring while K (V) j is there: between the two are kMhaFree - 1 blocks of the other kind at least.
+  static_assert((kMhaFree + 1) * kSub + (kMhaFree - 1) * 2 > kUnits && (kMhaFree + 1) * 2 + (kMhaFree - 1) * kSub > kUnits,
+                "releases told apart");
   static_assert(kBytes <= kMaxSmem, "shared memory");
   static_assert(kUnits * kMhaUnit >= kMhaTile * kMhaPartRow * 4, "rows that are joined");
 };
