@@ -976,7 +976,7 @@ __device__ __forceinline__ bool mha_softmax(const MhaFwdParams& p, MhaMisc& m, u
   if (blocks > 0) {   // long past: the other warps' arrivals with their weights of the last block, and what they have found by then
     const int last = blocks - 1;
     if (!warp_wait(smem_u32(&m.p_full[NT == 1 ? last & 1 : t]), NT == 1 ? last >> 1 & 1 : last & 1, deadline, ab)) return false;
-    const bool ask = live && sum > 0.f && mha_finite(sum) && (odd || *reinterpret_cast<volatile int*>(&m.cleared));
+    const bool ask = live && mha_finite(sum) && (odd || *reinterpret_cast<volatile int*>(&m.cleared));
     const uint32_t rows = __ballot_sync(0xffffffffu, ask);
     if (rows != 0u)
       mha_restore(rows, p.v + w.k0 * p.v_tok + pack0 / p.group * p.v_head, p.v_tok, s.from * kMhaTile,
@@ -1023,7 +1023,7 @@ __device__ __forceinline__ void mha_join(const MhaFwdParams& p, MhaMisc& m, uint
         add(acc[4 * k + 3], x[k].w);
       }
     }
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const float inv = sum == 0.f ? 1.f : 1.f / sum;   // without weights acc has zeros, and what is not finite
     const size_t out = static_cast<size_t>(w.q0 + t0 + row / p.pack) * p.h_q + pack0 + row % p.pack;
     uint2* o = reinterpret_cast<uint2*>(p.out + out * kMhaDv + col);
 #pragma unroll

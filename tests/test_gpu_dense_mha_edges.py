@@ -336,3 +336,23 @@ def test_a_long_request_beside_short_ones(smla):  # noqa: F811
     out, lse = smla.dense_mha_fwd(q, k, v, 0.1, cq, ck)
     _check_fwd(out, lse, q, k, v, 0.1, cq, ck)
     _check_bwd(smla.dense_mha_bwd(q, k, v, 0.1, out, lse, do, cq, ck), q, k, v, 0.1, out, lse, do, cq, ck)
+
+
+@pytest.mark.parametrize("lq,lk,h,hk,d", [(1, 5000, 8, 8, 192), (130, 4500, 2, 1, 128), (300, 1200, 2, 2, 192),
+                                          (1050, 1100, 64, 64, 128), (900, 1700, 128, 1, 192)])
+def test_seen_values_of_keys_of_weight_zero(smla, lq, lk, h, hk, d):  # noqa: F811
+    """Keys whose scores are -infinite, whole parts of a cluster among them, have no weight; their values that are not
+    finite count as all others do."""
+    q, k, v, *_ = _inputs(47, [lq], [lk], h, hk, d)
+    q[..., 0] = 1.0
+    n = min(700, lk - lq)   # all rows see more than these
+    k[:n, :, 0] = -INF
+    want = smla.dense_mha_fwd(q, k, v, 0.1)
+    assert want[0].isfinite().all() and want[1].isfinite().all()
+    v2 = v.clone()
+    v2[5, :, 7], v2[n // 2, :, 9], v2[n - 1, :, 9], v2[n - 1, :, 100] = INF, INF, -INF, NAN
+    out, lse = smla.dense_mha_fwd(q, k, v2, 0.1)
+    assert torch.equal(lse, want[1])
+    ref = want[0].clone()
+    ref[..., 7], ref[..., 9], ref[..., 100] = INF, NAN, NAN
+    assert torch.equal(torch.nan_to_num(out, nan=12345.0), torch.nan_to_num(ref, nan=12345.0))
