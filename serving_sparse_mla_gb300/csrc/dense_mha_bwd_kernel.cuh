@@ -36,9 +36,9 @@
 //
 // What bounds dk and dv at 192 columns: a block's products are 1280 cycles, but 1600 as both
 // operands of S^T and T^T come from shared memory and N = 64 (48 cycles for each 16 columns
-// where the product itself takes 32).  8192 tokens of 32 heads: 945 us, 2080 cycles a block
+// where the product itself takes 32).  8192 tokens of 32 heads: 960 us, 2110 cycles a block
 // with all that a tile costs once (8000 cycles to the first scores, 5500 for the sums' way
-// out); dq 617 us.  At 128 columns K stays in TMEM as A of S^T and a block is 1152 cycles.
+// out); dq 630 us.  At 128 columns K stays in TMEM as A of S^T and a block is 1152 cycles.
 //
 // Every wait is bounded, as in the forward.  dk's and dv's kernel waits for dq's grid, which has
 // a bound of its own, outside of these waits: no warp has one for D under way before.
@@ -735,6 +735,7 @@ __device__ __forceinline__ bool mha_dkv_rows(const MhaBwdParams& p, MhaDkvMisc& 
   const int last_key = min((w.tile + 1) * kMhaTile, lk) - 1;
   const uint32_t ts = lane0 + C::kS + kHalf * half, tt = lane0 + C::kT + kHalf * half,
                  tp = lane0 + C::kP + kHalf / 2 * half, td = lane0 + C::kDs + kHalf / 2 * half;
+  static_assert(kMhaSpare <= 4, "columns that are masked");
   // the bits of the last columns that are rows; in the others, zeros, a key that is not finite has a score of NaN
   const int used = p.pack * p.tok_tile - kHalf * half;
   auto bits = [&](int col) { return (col < used ? 0xffffu : 0u) | (col + 1 < used ? 0xffff0000u : 0u); };

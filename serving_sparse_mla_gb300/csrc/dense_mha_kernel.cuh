@@ -19,7 +19,8 @@
 //                        a ring of 16 KB units (K: 128 keys x 64 columns, V: 64 keys x
 //                        128 columns)
 //
-// With two tiles the tensor core works on one while the softmax works on the other.  Where
+// With two tiles the tensor core works on one while the softmax works on the other (a published
+// way for this generation of tensor cores, as is the late rescaling below).  Where
 // there are few tiles a CTA takes one, and a cluster of CTAs shares its keys out: each
 // leaves its O, maximum and sum in its shared memory, and every CTA of the cluster joins a
 // share of the rows from there.  O is
@@ -30,9 +31,9 @@
 //
 // What bounds it: the products (768 + 512 cycles a tile and block at 192 columns), as long
 // as a softmax of one tile ends within the products of the other.  8192 tokens of 64 heads
-// take 913 us, 1505 TFLOP/s or 80% of a large library product's rate; the rest is the
+// take 922 us, 1490 TFLOP/s or 79% of a large library product's rate; the rest is the
 // pipeline's filling per tile and the diagonal's half-empty blocks.  Packed prompts of 3 to
-// 2000 tokens take 148 us for 134 GFLOP: each CTA has some 5 to 15 blocks, and about 9000
+// 2000 tokens take 150 us for 134 GFLOP: each CTA has some 5 to 15 blocks, and about 9000
 // cycles go into starting (finding the tile, Q and K from memory) and the way out.  One
 // token against 5001 keys is 14 us, of which the launch, the first loads and the join are
 // all but 4.
@@ -124,8 +125,9 @@ struct MhaWork {
 // sequence's tiles come with the most work first: its last of queries, its first of keys.
 // One warp, all lanes.  Every CTA goes through this before it can load anything, so it is
 // kept short: with all tiles in the order of their work, by a search, 100 texts of 3 to 600
-// tokens took 436 us where they take 256, and 15 of up to 2000 249 where they take 222; with
-// every batch in its order the gradients of 9 texts of 122 to 2119 take 624 in the place of 584.
+// tokens took 1.7 times as long and 15 of up to 2000 1.12 times; with every batch in its order
+// the gradients of 9 texts of 122 to 2119 took 1.07 times as long.  It is CTAs times sequences
+// all the same: 2000 texts of 1 to 30 tokens, 8 heads, take 2350 us, nearly all of it here.
 template <bool KEYS>
 __device__ __forceinline__ MhaWork mha_find(const int32_t* cu_q, const int32_t* cu_kv, int batch, int total_q,
                                             int total_kv, int slot, const MhaDiv& per) {
@@ -823,7 +825,7 @@ __device__ __forceinline__ void mha_clear(uint32_t tile, uint32_t bytes, int* fo
 // (a lane's end is its row's; it does not fall from lane to lane).  One warp, a row per lane;
 // `part`, where it is given, takes the sums in place of `out`.
 __device__ __forceinline__ void mha_restore(uint32_t asked, const __nv_bfloat16* values, long long step, int first, int end,
-                                         __nv_bfloat16* out, float* part) {
+                                            __nv_bfloat16* out, float* part) {
   const int col = static_cast<int>(lane_id()) % 16 * 8;
   float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   __syncwarp();   // the rows' own threads have written them

@@ -47,7 +47,9 @@ smla::AddNormParams add_norm_params(const void* x, long long x_stride, const voi
 // in 16 bits, groups: 40 and 47 us against 34 and 40; 8192 x 7168: 87 and 106 against 73 and
 // 93), four with 80 registers 38, 45, 76 and 91.  The backward, with twice the values in a
 // thread's registers, takes one up to the 1024 threads of a CTA (8192 x 7168: 74 us, with
-// two 108).
+// two 108); above 8192 values it has to take two, which spill 280 bytes of its 64 registers:
+// 7152 x 8200 take 142 us where 7168 x 8192 take 80.  Rows of less than 512 values leave most
+// of a warp idle: 65536 x 128 take 38 to 45 us, four times their bytes.
 constexpr int kAddNormVectors = 2;
 int add_norm_bwd_vectors(int d) { return d <= 8192 ? 1 : 2; }
 int add_norm_threads(int d, int v) { return ((d / 8 + v - 1) / v + 31) / 32 * 32; }
@@ -171,8 +173,9 @@ sparse_mla_status_t check_mha(const MhaRows& q, const MhaRows& k, const MhaRows&
 }
 
 // Query heads of one group that a tile of `rows` takes side by side: the most that leave
-// at most one row in 16 unused.  Without (us): 15 texts of up to 2000 tokens, 32 heads on 8, 276
-// in the place of 249, their gradients 762 and 722; 16 tokens' gradients on 9000 keys 122 and 97.
+// at most one row in 16 unused.  One head a tile and side by side (us): 15 texts of up to 2000
+// tokens, 32 heads on 8, 188 and 149, their gradients 554 and 488; 16 tokens' gradients on 9000
+// keys 122 and 97.
 int mha_pack(int group, int rows) {
   for (int n = group < rows ? group : rows; n > 1; --n)
     if (group % n == 0 && rows % n <= rows / (64 / smla::kMhaSpare)) return n;
@@ -288,9 +291,11 @@ struct MhaPlan {
 // blocks one after the other, of a longest tile and of the card's mean.  A CTA of two
 // tiles takes about as long for a block of both as one of a single tile for its own.
 // Measured (us; two tiles a CTA / one / one and the keys shared out):
-//   1 token on 5001 keys, 8 heads    64.7 /  59.9 / 14.5
-//   16 tokens on 9000, 32 heads on 8 102 / 76 / 27      1024 tokens, 8 heads  22.3 / 18.4 / 18.0
-//   15 texts to 2000, 32 heads on 8  222 / 355 (the latter with another order of the tiles)
+//   1 token on 5001 keys, 8 heads    65.3 / 60.4 / 14.7
+//   16 tokens on 9000, 32 heads on 8 103 / 77.5 / 25.6   1024 tokens, 8 heads  21.7 / 17.8 / 17.5
+//   15 texts to 2000, 32 heads on 8  149 / 198 (too many tiles for clusters)
+// What mean lengths do not show: 16 tokens behind 30000 keys beside 31 short texts, 8 heads, are
+// not shared out and take 352.
 MhaPlan mha_plan(int total_q, int total_kv, int batch, bool packed, int packs, int tok_tile, int sms,
                  const int* clusters) {
   const double lq = static_cast<double>(total_q) / batch, lk = static_cast<double>(total_kv) / batch;
@@ -323,10 +328,10 @@ cudaError_t mha_fwd_launch(const smla::MhaFwdParams& p, unsigned ctas, cudaStrea
 // to `most` (one at least), so that the tiles find each other's reads in the near half of L2;
 // the last ones, two tiles an SM, all together, so that the SMs end together.
 // Measured (us, 192 columns, 8192 tokens; all heads that 100 MB hold / 24 MB / 11 MB):
-//   dk and dv, 32 heads   1393 / 1015 / 966     64 heads   2712 / 2020 / 1950
-//   dq, 32 heads           675 /  632 / 635     out, 64 heads   884 / 866 / 867
-// The tail (1, 2, 4 tiles an SM): nine texts up to 2119, 40 heads on 8, dk and dv 355, 316,
-// 351; 32 heads on 8 of 8192 tokens 812, 900, 890.
+//   dk and dv, 32 heads   1363 / 1026 / 961     64 heads   2700 / 2072 / 1959
+//   dq, 32 heads           661 /  630 / 636     out, 64 heads   890 / 884 / 876
+// The tail (1, 2, 4 tiles an SM): nine texts up to 2119, 40 heads on 8, dk and dv 362, 344,
+// 325; 32 heads on 8 of 8192 tokens 826, 917, 912.  No one of them is the best for both.
 constexpr double kMhaNearKeys = 2.4e7, kMhaNearRows = 1.1e7;
 smla::MhaHeads mha_order(int heads, double bytes, double most, long long slots, int sms) {
   const double near = std::max(1.0, std::min<double>(heads, std::floor(most / (bytes + 1))));
